@@ -598,6 +598,126 @@ typedef struct tl_ag_attn_args {
 int tl_ag_attn_num_flags(int R, int S_shard);
 tl_status tl_ag_attn(const tl_ag_attn_args* args, void* stream);
 
+/* ---------------------------------------------------------------- paged key/value cache in 8 bits
+ * Keys and values that live between calls: a pool of pages of page_size tokens,
+ * each page with a [page_size, head_dim] tile of e4m3 codes for every kv head,
+ * keys and values in buffers (or planes of one buffer) of the same strides.
+ * One E8M0 scale byte b for each (page, kv head), keys and values apart: a code c
+ * stands for c * 2^(b - 127).  The scale is a power of two, so a code's value is
+ * exact in fp32, and a block whose scale grows while it fills is re-coded by a
+ * shift of exponents (only codes that become subnormal are rounded again, by at
+ * most 2^-10 of the new scale).  e4m3 has no infinity: an infinite element is
+ * stored as the largest code of its sign (448) and takes no part in the scale; a
+ * NaN is stored as NaN.  Scale byte 255 stands for NaN.
+ *
+ * A batch is ragged: new tokens of all sequences lie behind one another,
+ * sequence s's at rows cu_seqlens[s] .. cu_seqlens[s+1]-1 (none is allowed), and
+ * seq_lens[s] is its length WITH them, so its new token i has position
+ * seq_lens[s] - n_s + i.  Token position p of sequence s lies in slot
+ * p % page_size of page page_table[s * max_pages + p / page_size].  These arrays
+ * are read on the device.  What is wrong in them (decreasing or out-of-range
+ * cu_seqlens, a length below the new tokens or above max_pages * page_size, a
+ * page outside the pool) records TL_ERR_INVALID with the sequence number in the
+ * signals' status word; the tokens or keys concerned are left out, and nothing
+ * outside the caller's buffers is touched.
+ */
+typedef struct tl_kv_cache {
+  void* k;                     /* device e4m3 codes; element (page, head, slot, d) at byte
+                                  page*page_stride + head*head_stride + slot*token_stride + d */
+  void* v;                     /* the same for values */
+  uint8_t* k_scale;            /* device E8M0 [num_pages, H_kv] */
+  uint8_t* v_scale;
+  int64_t page_stride;         /* bytes, multiples of 16, >= head_dim (strides of a dimension of size 1 too) */
+  int64_t head_stride;
+  int64_t token_stride;
+  int32_t num_pages;           /* >= 1 */
+  int32_t page_size;           /* tokens per page: a multiple of 16, 16..256 */
+  int32_t H_kv;                /* kv heads, >= 1 */
+  int32_t head_dim;            /* 64 or 128 */
+} tl_kv_cache;
+
+/* ---------------------------------------------------------------- append to the cache, rotating on the way
+ * For every new token at position p: k and (if given) q have their first rot_dim
+ * dims rotated by the table rows cos[p], sin[p],
+ *   (y_a, y_b) = (x_a cos_j - x_b sin_j, x_b cos_j + x_a sin_j),  j < rot_dim/2,
+ *   (a, b) = (j, j + rot_dim/2), or (2j, 2j + 1) with interleaved = 1;
+ * k and v are quantised into the cache, and q is written to q_out in bf16.
+ * For each page that receives tokens and each kv head, with amax the largest
+ * finite magnitude of the new rows: need = the least byte with
+ * amax <= 448 * 2^(need-127) (0 for an all-zero block); the block's byte becomes
+ * max(need, its byte before) when the page holds earlier tokens of the sequence,
+ * and need when the new tokens begin the page.  Each code is the exact rotated
+ * value rounded ONCE to nearest even, whatever fp32 would have rounded before.
+ * One launch.  Calling it again with the same arguments gives the same cache.
+ * A page must not receive tokens of two sequences in one call.
+ */
+typedef struct tl_kv_append_args {
+  int32_t n_tokens;            /* new tokens of all sequences, >= 0 (0: nothing to do) */
+  int32_t B;                   /* sequences, >= 1 */
+  int32_t H;                   /* query heads; 0 = no queries (q and q_out NULL) */
+  int32_t rot_dim;             /* rotated dims: a multiple of 16, 0..head_dim */
+  int32_t interleaved;         /* 0: pairs (j, j + rot_dim/2), 1: pairs (2j, 2j+1) */
+  int32_t max_pos;             /* rows of cos and sin; a token at a later position is an error like a bad page */
+  int32_t max_pages;           /* columns of page_table */
+  int32_t max_q_len;           /* hint: most new tokens of one sequence (0 = unknown); the result does not depend on it */
+  tl_kv_cache cache;
+  const void* k;               /* device bf16, element (token, head, d) at token*stride + head*stride + d */
+  const void* v;
+  const void* q;
+  int64_t k_token_stride, k_head_stride;  /* elements, multiples of 8 */
+  int64_t v_token_stride, v_head_stride;
+  int64_t q_token_stride, q_head_stride;
+  void* q_out;                 /* device bf16 [n_tokens, H, head_dim], written */
+  const float* cos;            /* device float [max_pos, rot_dim/2]; NULL when rot_dim = 0 */
+  const float* sin;
+  const int32_t* cu_seqlens;   /* device int32 [B + 1] */
+  const int32_t* seq_lens;     /* device int32 [B] */
+  const int32_t* page_table;   /* device int32 [B, max_pages] */
+  tl_signals* signals;         /* receives device-side errors in its status word (any size >= 1) */
+} tl_kv_append_args;
+
+tl_status tl_kv_append(const tl_kv_append_args* args, void* stream);
+
+/* ---------------------------------------------------------------- attention over the cache
+ * For new token i (0-based) of sequence s and query head h, with kv head
+ * hk = h / (H / H_kv) and k_j, v_j the cache's values:
+ *   s_j = scale * <q, k_j>   for j < seq_lens[s], and with causal = 1
+ *                            j <= seq_lens[s] - n_s + i
+ *   O = bf16( sum_j exp(s_j - lse) v_j ),   lse = log sum_j exp(s_j)
+ * A row that sees no key has O = 0 and lse = -infinity.  What lies in the cache
+ * where a row sees nothing (NaN included) does not reach its result.  Fp32
+ * softmax statistics and sums; the codes enter the products exactly.
+ * Takes queries that tl_kv_append rotated and a cache that holds the new tokens.
+ * May be captured into a graph after a first call outside any capture.
+ */
+typedef struct tl_kv_attn_args {
+  int32_t n_tokens;            /* rows of q, >= 0 (0: nothing to do) */
+  int32_t B;                   /* sequences, >= 1 */
+  int32_t H;                   /* query heads, a multiple of H_kv */
+  int32_t causal;              /* 0 or 1 */
+  int32_t max_pages;           /* columns of page_table */
+  int32_t max_q_len;           /* hint: most new tokens of one sequence (0 = unknown) */
+  float scale;                 /* softmax scale; 0 = 1/sqrt(head_dim) */
+  int32_t reserved0;
+  tl_kv_cache cache;
+  const void* q;               /* device bf16, element (token, head, d) at token*stride + head*stride + d */
+  int64_t q_token_stride, q_head_stride;  /* elements, multiples of 8 */
+  void* out;                   /* device bf16 [n_tokens, H, head_dim], written */
+  float* lse;                  /* optional device float [H, n_tokens] (natural log), written; NULL = none */
+  const int32_t* cu_seqlens;   /* device int32 [B + 1] */
+  const int32_t* seq_lens;     /* device int32 [B] */
+  const int32_t* page_table;   /* device int32 [B, max_pages] */
+  void* workspace;             /* device scratch, 16-byte aligned, zeroed before its first use; left ready for
+                                  the next call by every call.  Calls sharing it must not run concurrently. */
+  size_t workspace_bytes;      /* >= tl_kv_attn_workspace_size(n_tokens, B, H, H_kv, head_dim, 0) */
+  tl_signals* signals;         /* receives device-side errors in its status word (any size >= 1) */
+} tl_kv_attn_args;
+
+/* Workspace bytes for the sizes; 0 for invalid ones.  Never falls as n_tokens or B
+ * grow.  sm_count 0 = the current device's. */
+size_t tl_kv_attn_workspace_size(int n_tokens, int B, int H, int H_kv, int head_dim, int sm_count);
+tl_status tl_kv_attn(const tl_kv_attn_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -37,6 +37,7 @@ EXPORTED = [
     "tl_moe_down_workspace_size", "tl_moe_down_num_flags", "tl_moe_down",
     "tl_ag_attn_num_flags", "tl_ag_attn", "tl_allgather_ll_link_bytes", "tl_allgather_ll",
     "tl_test_hold_chunks",
+    "tl_kv_append", "tl_kv_attn_workspace_size", "tl_kv_attn",
 ]
 
 
@@ -138,6 +139,39 @@ class tl_reduce_scatter_args(ctypes.Structure):
     ]
 
 
+class tl_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp),
+        ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+    ]
+
+
+class tl_kv_append_args(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32), ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("max_pos", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("max_q_len", ctypes.c_int32), ("cache", tl_kv_cache), ("k", _vp), ("v", _vp), ("q", _vp),
+        ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("q_out", _vp), ("cos", _vp), ("sin", _vp), ("cu_seqlens", _vp), ("seq_lens", _vp), ("page_table", _vp),
+        ("signals", _vp),
+    ]
+
+
+class tl_kv_attn_args(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32), ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("causal", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32), ("max_q_len", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("reserved0", ctypes.c_int32), ("cache", tl_kv_cache), ("q", _vp),
+        ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("out", _vp), ("lse", _vp),
+        ("cu_seqlens", _vp), ("seq_lens", _vp), ("page_table", _vp), ("workspace", _vp),
+        ("workspace_bytes", ctypes.c_size_t), ("signals", _vp),
+    ]
+
+
 def _decl(name, restype, *argtypes):
     f = getattr(lib, name)
     f.restype = restype
@@ -178,6 +212,9 @@ _decl("tl_allgather_ll", _i, ctypes.POINTER(tl_allgather_ll_args), _vp)
 _decl("tl_test_hold_chunks", _i, _i, _i, _u64)
 _decl("tl_ag_attn_num_flags", _i, _i, _i)
 _decl("tl_ag_attn", _i, ctypes.POINTER(tl_ag_attn_args), _vp)
+_decl("tl_kv_append", _i, ctypes.POINTER(tl_kv_append_args), _vp)
+_decl("tl_kv_attn_workspace_size", _sz, _i, _i, _i, _i, _i, _i)
+_decl("tl_kv_attn", _i, ctypes.POINTER(tl_kv_attn_args), _vp)
 
 
 def _check(code):
@@ -496,3 +533,114 @@ def tl_ag_attn(Q, K_shards, V_shards, K_gathered, V_gathered, O, signals: Signal
                         signals=signals.handle, epoch=int(epoch) & 0xFFFFFFFF, reserved0=0,
                         timeout_ns=int(timeout_ns))
     _check(lib.tl_ag_attn(ctypes.byref(a), _stream(stream)))
+
+
+def _inner(t, what):
+    """Strides of a [tokens, heads, dim] tensor whose dims must lie next to one another."""
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{what}: a [tokens, heads, dim] tensor with its dims next to one another")
+    return t.stride(0), t.stride(1)
+
+
+def _typed(t, what, dtype, shape=None):
+    """t is a CUDA tensor of this type (and shape, contiguous, where one is given)."""
+    if t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA tensor of {dtype}, not {t.dtype} on {t.device}")
+    if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{what}: a contiguous tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+class KvCache:
+    """The paged 8-bit cache (see tilelink.h): k and v are uint8 or float8_e4m3fn tensors of codes
+    [num_pages, H_kv, page_size, head_dim] (any strides that are multiples of 16 and the same for both,
+    dims next to one another: views of one buffer will do), k_scale and v_scale the E8M0 bytes
+    [num_pages, H_kv].  Holds the tensors."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        for t in (k, v):
+            if t.dim() != 4 or t.element_size() != 1 or not t.is_cuda:
+                raise ValueError("KvCache: codes are 4-D CUDA tensors of 8-bit elements")
+            if t.stride(3) != 1:
+                raise ValueError("KvCache: the dims of a code tensor must lie next to one another")
+        if k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("KvCache: k and v must have the same shape and strides")
+        for t in (k_scale, v_scale):
+            if tuple(t.shape) != tuple(k.shape[:2]) or t.element_size() != 1 or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError("KvCache: scales are contiguous [num_pages, H_kv] CUDA tensors of bytes")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.H_kv, self.page_size, self.head_dim = k.shape
+        self.struct = tl_kv_cache(k=_ptr(k), v=_ptr(v), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale),
+                                  page_stride=k.stride(0), head_stride=k.stride(1), token_stride=k.stride(2),
+                                  num_pages=self.num_pages, page_size=self.page_size, H_kv=self.H_kv,
+                                  head_dim=self.head_dim)
+
+
+def _batch(cu_seqlens, seq_lens, page_table):
+    """(B, columns of the page table) of a ragged batch, its arrays' types checked."""
+    import torch
+    B = seq_lens.shape[0]
+    _typed(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    _typed(seq_lens, "seq_lens", torch.int32, (B,))
+    max_pages = page_table.shape[1]
+    _typed(page_table, "page_table", torch.int32, (B, max_pages))
+    return B, max_pages
+
+
+def tl_kv_append(cache: KvCache, k, v, cu_seqlens, seq_lens, page_table, signals: Signals, *, q=None, q_out=None,
+                 cos=None, sin=None, interleaved=False, max_q_len=0, stream=None):
+    """Append k, v [n, H_kv, D] (bf16; views of a fused projection will do) to the cache, k rotated by the
+    tables cos, sin [positions, rot_dim/2] at each token's position; q [n, H, D] rotated into q_out
+    (see tilelink.h).  No tables: no rotation."""
+    import torch
+    n, D = k.shape[0], cache.head_dim
+    B, max_pages = _batch(cu_seqlens, seq_lens, page_table)
+    ks, vs, qs = _inner(k, "k"), _inner(v, "v"), (0, 0)
+    for t, what in ((k, "k"), (v, "v")):
+        _typed(t, what, torch.bfloat16)
+        if tuple(t.shape) != (n, cache.H_kv, D):
+            raise ValueError(f"{what}: shape {(n, cache.H_kv, D)}, not {tuple(t.shape)}")
+    H = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        H, qs = q.shape[1], _inner(q, "q")
+        _typed(q, "q", torch.bfloat16)
+        if tuple(q.shape) != (n, H, D):
+            raise ValueError(f"q: shape {(n, H, D)}, not {tuple(q.shape)}")
+        _typed(q_out, "q_out", torch.bfloat16, (n, H, D))
+    rot = max_pos = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        _typed(cos, "cos", torch.float32, (max_pos, rot // 2))
+        _typed(sin, "sin", torch.float32, (max_pos, rot // 2))
+    a = tl_kv_append_args(n, B, H, rot, int(bool(interleaved)), max_pos, max_pages, int(max_q_len), cache.struct,
+                          _ptr(k), _ptr(v), _ptr(q), ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], _ptr(q_out), _ptr(cos),
+                          _ptr(sin), _ptr(cu_seqlens), _ptr(seq_lens), _ptr(page_table), signals.handle)
+    _check(lib.tl_kv_append(ctypes.byref(a), _stream(stream)))
+
+
+def tl_kv_attn_workspace_size(n_tokens, B, H, H_kv, head_dim, sm_count=0):
+    return int(lib.tl_kv_attn_workspace_size(n_tokens, B, H, H_kv, head_dim, sm_count))
+
+
+def tl_kv_attn(q, cache: KvCache, out, cu_seqlens, seq_lens, page_table, workspace, signals: Signals, *, causal=True,
+               scale=0.0, max_q_len=0, lse=None, stream=None):
+    """out [n, H, D] = attention of q [n, H, D] over each sequence's keys and values in the cache, the new
+    tokens' included; lse optional float [H, n] (see tilelink.h)."""
+    import torch
+    n, H, D = q.shape
+    B, max_pages = _batch(cu_seqlens, seq_lens, page_table)
+    _typed(q, "q", torch.bfloat16)
+    if D != cache.head_dim:
+        raise ValueError(f"q: head dim {D}, the cache's is {cache.head_dim}")
+    qs = _inner(q, "q")
+    _typed(out, "out", torch.bfloat16, (n, H, D))
+    if lse is not None:
+        _typed(lse, "lse", torch.float32, (H, n))
+    a = tl_kv_attn_args(n, B, H, int(bool(causal)), max_pages, int(max_q_len), float(scale), 0, cache.struct, _ptr(q),
+                        qs[0], qs[1], _ptr(out), _ptr(lse), _ptr(cu_seqlens), _ptr(seq_lens), _ptr(page_table),
+                        _ptr(workspace), _nbytes(workspace), signals.handle)
+    _check(lib.tl_kv_attn(ctypes.byref(a), _stream(stream)))

@@ -298,6 +298,24 @@ tl_status launch_coop(const void* kernel, int grid, int block, size_t smem, cuda
   return cuda_ok(cudaLaunchKernelExC(&cfg, kernel, args), "cooperative launch");
 }
 
+tl_status launch(const void* kernel, int grid, int block, size_t smem, cudaStream_t st, void** args, bool early_start) {
+  int dev = 0;
+  if (tl_status s = cuda_ok(cudaGetDevice(&dev), "cudaGetDevice")) return s;
+  if (smem > 48 * 1024)
+    if (tl_status s = ensure_smem_limit(dev, kernel, smem)) return s;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early_start ? 1 : 0;
+  return cuda_ok(cudaLaunchKernelExC(&cfg, kernel, args), "kernel launch");
+}
+
 }  // namespace tl
 
 // ---------------------------------------------------------------- kernels of the signal API

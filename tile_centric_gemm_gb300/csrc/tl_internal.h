@@ -59,6 +59,13 @@ tl_status make_map_bf16_3d(CUtensorMap* map, const void* base, uint64_t planes, 
 tl_status launch_coop(const void* kernel, int grid, int block, size_t smem, cudaStream_t st, void** args,
                       int cluster = 1, bool early_start = false);
 
+// Launch a grid whose CTAs do not wait for one another.  early_start: programmatic
+// dependent launch, as above.
+tl_status launch(const void* kernel, int grid, int block, size_t smem, cudaStream_t st, void** args, bool early_start);
+
+// The checks of a tl_kv_cache that the calls on it share.
+tl_status check_kv_cache(const char* who, const tl_kv_cache& c);
+
 // Where each of R shard pointers lives: device memory of `device` (bulk TMA
 // copies), or pinned host / managed memory (plain loads; bit r of *host_mask).
 // dev[r] receives the address the device uses.  Pageable host memory and other
