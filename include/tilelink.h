@@ -718,6 +718,47 @@ typedef struct tl_kv_attn_args {
 size_t tl_kv_attn_workspace_size(int n_tokens, int B, int H, int H_kv, int head_dim, int sm_count);
 tl_status tl_kv_attn(const tl_kv_attn_args* args, void* stream);
 
+/* ---------------------------------------------------------------- MoE layer for a few tokens
+ * A whole mixture-of-experts layer for the tokens of a decode step: router
+ * selection, gated experts, combine.  For token t:
+ *   ids[t]    = the topk experts of the largest logits[t], largest first; equal
+ *               logits go to the lower index, NaN ranks below every number
+ *   gates[t]  = softmax of the logits over the chosen experts (normalize = 1) or
+ *               over all E experts (normalize = 0); 0 where every logit of that
+ *               softmax is -infinity
+ *   h_s       = silu(x W1_e[:, :I]) * (x W1_e[:, I:])       e = ids[t, s]
+ *   out[t]    = bf16( sum_s gates[t, s] * (h_s W2_e) )       slots in order
+ * Every product is summed in fp32; h is kept to 16 bits of mantissa (two bf16
+ * terms).  The weights of an expert that no token chose are not read.
+ * Two stream-ordered launches, the second set up while the first runs
+ * (programmatic dependent launch).  Deterministic.  Beyond 64 tokens
+ * tl_moe_ag_gemm and tl_moe_down are the calls.
+ */
+typedef struct tl_moe_decode_args {
+  int32_t T;                   /* tokens, 0..64 (0: nothing to do) */
+  int32_t H;                   /* hidden size (rows of W1), multiple of 8, >= 8 */
+  int32_t I;                   /* intermediate columns, multiple of 8, >= 8 */
+  int32_t Hd;                  /* output columns, multiple of 8, >= 8 */
+  int32_t E;                   /* experts, 1..TL_MAX_EXPERTS */
+  int32_t topk;                /* experts per token, 1..min(E, 16) */
+  int32_t normalize;           /* 1: gates sum to 1 over the chosen experts; 0: softmax over all experts */
+  int32_t reserved0;
+  const void* x;               /* device bf16 [T, H] */
+  const float* logits;         /* device float [T, E] */
+  const void* const* W1;       /* host array of E device pointers, bf16 [H, 2*I]: gate columns, then up columns */
+  const void* const* W2;       /* host array of E device pointers, bf16 [I, Hd] */
+  void* out;                   /* device bf16 [T, Hd], written */
+  int32_t* ids;                /* device int32 [T, topk], written */
+  float* gates;                /* device float [T, topk], written */
+  void* workspace;             /* device scratch, 16-byte aligned, zeroed before its first use; left ready for
+                                  the next call by every call.  Calls sharing it must not run concurrently. */
+  size_t workspace_bytes;      /* >= tl_moe_decode_workspace_size(T, topk, E, H, I, Hd) */
+} tl_moe_decode_args;
+
+/* Workspace bytes for the sizes; 0 for invalid ones. */
+size_t tl_moe_decode_workspace_size(int T, int topk, int E, int H, int I, int Hd);
+tl_status tl_moe_decode(const tl_moe_decode_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

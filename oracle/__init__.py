@@ -21,4 +21,4 @@ closed forms, invariants, hand-worked fixtures under ``tests/golden/`` and,
 for bf16 rounding, the float32 -> bfloat16 conversion of an independent
 library.
 """
-from . import bf16, ag_gemm, gemm_rs, moe, attention, kv_cache  # noqa: F401
+from . import bf16, ag_gemm, gemm_rs, moe, attention, kv_cache, moe_decode  # noqa: F401

@@ -1,4 +1,4 @@
-"""Argument checks of the serving calls (8-bit paged cache, attention over it) that need no device, and the
+"""Argument checks of the serving calls (8-bit paged cache, attention over it, experts for a few tokens) that need no device, and the
 cache's oracle against torch's own e4m3 and against attention over plain values."""
 import ctypes
 
@@ -105,6 +105,50 @@ def test_binding_refuses_wrong_tensors(B):
         B.KvCache(k, k, torch.zeros(2, 1, dtype=torch.uint8), torch.zeros(2, 1, dtype=torch.uint8))  # not on a GPU
 
 
+def moe_args(L, **kw):
+    import ctypes as ct
+    e = kw.get("E", 4)
+    ptrs = ct.cast((ct.c_void_p * max(e, 1))(*[16] * max(e, 1)), ct.POINTER(ct.c_void_p))
+    a = dict(T=3, H=64, I=32, Hd=64, E=4, topk=2, normalize=1, reserved0=0, x=16, logits=4, W1=ptrs, W2=ptrs, out=32,
+             ids=4, gates=8, workspace=256, workspace_bytes=1 << 30)
+    a.update(kw)
+    return L.tl_moe_decode_args(**a)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), 1), (dict(T=65), 4), (dict(H=0), 1), (dict(H=60), 4), (dict(I=12), 4), (dict(Hd=4), 4),
+    (dict(E=0), 1), (dict(E=257), 4), (dict(topk=0), 1), (dict(topk=5), 1), (dict(E=32, topk=17), 4),
+    (dict(normalize=2), 1), (dict(x=None), 1), (dict(logits=None), 1), (dict(W1=None), 1), (dict(W2=None), 1),
+    (dict(out=None), 1), (dict(ids=None), 1), (dict(gates=None), 1), (dict(workspace=None), 1), (dict(x=24), 1),
+    (dict(out=40), 1), (dict(workspace=264), 1), (dict(logits=6), 1), (dict(gates=9), 1), (dict(workspace_bytes=4096), 1)])
+def test_moe_refuses(B, kw, code):
+    a = moe_args(B, **kw)
+    assert B.lib.tl_moe_decode(ctypes.byref(a), None) == code, kw
+    assert "tl_moe_decode" in B.tl_last_error()
+
+
+def test_moe_refuses_bad_weight_pointers(B):
+    for bad in (None, 24):
+        ptrs = ctypes.cast((ctypes.c_void_p * 4)(16, 32, bad, 48), ctypes.POINTER(ctypes.c_void_p))
+        for name in ("W1", "W2"):
+            assert B.lib.tl_moe_decode(ctypes.byref(moe_args(B, **{name: ptrs})), None) == B.TL_ERR_INVALID
+            assert "expert 2" in B.tl_last_error()
+
+
+def test_moe_null_and_nothing_to_do(B):
+    assert B.lib.tl_moe_decode(None, None) == B.TL_ERR_INVALID
+    assert B.lib.tl_moe_decode(ctypes.byref(moe_args(B, T=0, x=None, out=None, workspace=None)), None) == 0
+
+
+def test_moe_workspace_size(B):
+    size = B.tl_moe_decode_workspace_size
+    assert size(1, 2, 32, 4096, 1408, 4096) >= 2 * (1408 * 4 + 4096 * 4)
+    assert size(64, 2, 32, 4096, 1408, 4096) > size(8, 2, 32, 4096, 1408, 4096)
+    for bad in [(-1, 2, 8, 64, 64, 64), (65, 2, 8, 64, 64, 64), (1, 9, 8, 64, 64, 64), (1, 2, 8, 60, 64, 64),
+                (1, 17, 32, 64, 64, 64), (1, 1, 257, 64, 64, 64)]:
+        assert size(*bad) == 0
+
+
 # ------------------------------------------------------------------ the oracle
 def test_oracle_codes_are_torchs():
     import torch
@@ -154,3 +198,24 @@ def test_oracle_rotation_is_complex_multiplication():
         y = ora.rotate(x, 2, cos, sin, inter)
         assert np.allclose(y[:, first], z.real) and np.allclose(y[:, second], z.imag)
         assert np.array_equal(y[:, 6:], x[:, 6:])
+
+
+def test_oracle_selection():
+    from oracle import moe_decode
+    l = np.array([[0.0, 2.0, 2.0, -1.0], [np.nan, -np.inf, 1.0, 1.0], [-np.inf] * 4])
+    ids, gates = moe_decode.select(l, 3, True)
+    assert ids.tolist() == [[1, 2, 0], [2, 3, 1], [0, 1, 2]]
+    assert np.allclose(gates[0], np.exp([0, 0, -2]) / np.exp([0, 0, -2]).sum())
+    assert np.allclose(gates[1], [0.5, 0.5, 0.0]) and (gates[2] == 0).all()
+    assert np.allclose(moe_decode.select(l[:1], 2, False)[1][0], np.exp([0, 0]) / np.exp([-2, 0, 0, -3]).sum())
+
+
+def test_oracle_layer_by_hand():
+    from oracle import moe_decode
+    x = np.array([[1.0, 2.0]])
+    W1 = [np.array([[1.0, 3.0], [0.5, -1.0]]), np.zeros((2, 2))]
+    W2 = [np.array([[2.0, -1.0]]), np.zeros((1, 2))]
+    g, u = 2.0, 1.0
+    h = g / (1 + np.exp(-g)) * u
+    out = moe_decode.layer(x, np.array([[np.log(3.0), 0.0]]), W1, W2, 2, True)[0]
+    assert np.allclose(out, 0.75 * h * np.array([[2.0, -1.0]]))

@@ -38,6 +38,7 @@ EXPORTED = [
     "tl_ag_attn_num_flags", "tl_ag_attn", "tl_allgather_ll_link_bytes", "tl_allgather_ll",
     "tl_test_hold_chunks",
     "tl_kv_append", "tl_kv_attn_workspace_size", "tl_kv_attn",
+    "tl_moe_decode_workspace_size", "tl_moe_decode",
 ]
 
 
@@ -172,6 +173,15 @@ class tl_kv_attn_args(ctypes.Structure):
     ]
 
 
+class tl_moe_decode_args(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("Hd", ctypes.c_int32),
+        ("E", ctypes.c_int32), ("topk", ctypes.c_int32), ("normalize", ctypes.c_int32), ("reserved0", ctypes.c_int32),
+        ("x", _vp), ("logits", _vp), ("W1", ctypes.POINTER(_vp)), ("W2", ctypes.POINTER(_vp)), ("out", _vp),
+        ("ids", _vp), ("gates", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 def _decl(name, restype, *argtypes):
     f = getattr(lib, name)
     f.restype = restype
@@ -215,6 +225,8 @@ _decl("tl_ag_attn", _i, ctypes.POINTER(tl_ag_attn_args), _vp)
 _decl("tl_kv_append", _i, ctypes.POINTER(tl_kv_append_args), _vp)
 _decl("tl_kv_attn_workspace_size", _sz, _i, _i, _i, _i, _i, _i)
 _decl("tl_kv_attn", _i, ctypes.POINTER(tl_kv_attn_args), _vp)
+_decl("tl_moe_decode_workspace_size", _sz, _i, _i, _i, _i, _i, _i)
+_decl("tl_moe_decode", _i, ctypes.POINTER(tl_moe_decode_args), _vp)
 
 
 def _check(code):
@@ -644,3 +656,42 @@ def tl_kv_attn(q, cache: KvCache, out, cu_seqlens, seq_lens, page_table, workspa
                         qs[0], qs[1], _ptr(out), _ptr(lse), _ptr(cu_seqlens), _ptr(seq_lens), _ptr(page_table),
                         _ptr(workspace), _nbytes(workspace), signals.handle)
     _check(lib.tl_kv_attn(ctypes.byref(a), _stream(stream)))
+
+
+class MoeWeights:
+    """The experts of tl_moe_decode: E contiguous bf16 matrices W1[e] [H, 2*I] (gate columns, then up columns) and
+    W2[e] [I, Hd].  Holds the tensors and their pointers."""
+
+    def __init__(self, W1, W2):
+        import torch
+        if len(W1) != len(W2) or not W1:
+            raise ValueError("MoeWeights: as many W1 as W2, one at least")
+        self.E, (self.H, two_I), (self.I, self.Hd) = len(W1), W1[0].shape, W2[0].shape
+        if two_I != 2 * self.I:
+            raise ValueError(f"MoeWeights: W1 has {two_I} columns, W2 has {self.I} rows: twice as many are wanted")
+        for w1, w2 in zip(W1, W2):
+            _typed(w1, "W1", torch.bfloat16, (self.H, two_I))
+            _typed(w2, "W2", torch.bfloat16, (self.I, self.Hd))
+        self.W1, self.W2 = W1, W2
+        self.p1 = ctypes.cast(_ptr_array(W1), ctypes.POINTER(_vp))
+        self.p2 = ctypes.cast(_ptr_array(W2), ctypes.POINTER(_vp))
+
+
+def tl_moe_decode_workspace_size(T, topk, E, H, I, Hd):
+    return int(lib.tl_moe_decode_workspace_size(T, topk, E, H, I, Hd))
+
+
+def tl_moe_decode(x, logits, weights: MoeWeights, out, ids, gates, workspace, *, normalize=True, stream=None):
+    """out [T, Hd] = the mixture-of-experts layer of x [T, H] under the router's logits [T, E]; the chosen experts
+    and their gates into ids and gates [T, topk] (see tilelink.h)."""
+    import torch
+    w = weights
+    T, topk = ids.shape
+    _typed(x, "x", torch.bfloat16, (T, w.H))
+    _typed(logits, "logits", torch.float32, (T, w.E))
+    _typed(out, "out", torch.bfloat16, (T, w.Hd))
+    _typed(ids, "ids", torch.int32, (T, topk))
+    _typed(gates, "gates", torch.float32, (T, topk))
+    a = tl_moe_decode_args(T, w.H, w.I, w.Hd, w.E, topk, int(bool(normalize)), 0, _ptr(x), _ptr(logits), w.p1, w.p2,
+                           _ptr(out), _ptr(ids), _ptr(gates), _ptr(workspace), _nbytes(workspace))
+    _check(lib.tl_moe_decode(ctypes.byref(a), _stream(stream)))
