@@ -12,17 +12,20 @@
 // sum) in the workspace; the CTA that arrives last joins them in CTA order, so
 // the result does not depend on timing.
 //
-// Inside a CTA the eight warps take a run's chunks in turn, each on its own:
+// Inside a CTA the eight warps take a run's chunks of 32 tokens in turn, each on its
+// own.  Keys and values are the products' first operand (S^T = K Q^T, O^T = V^T P^T):
+// 16 tokens or dims by 8 query rows, so a tile of 8 rows wastes little of a product,
+// and a tile of 16 takes two.
 //  * The contraction index of a product may be permuted at will if both operands
-//    are.  Lane (g, t) of an m16n8k16 product holds, for key g, the dims that it
-//    gets from two 16-byte loads of that key's codes, and for values four tokens'
-//    16 dims each; so every lane copies (cp.async) just the bytes that it will
-//    multiply, into a ring of its own in shared memory: no transposition, no
-//    barrier between copy and use, six chunks (4 KB) in flight per warp.
+//    are.  Lane (g, t) holds, for key g, the dims that it gets from two 16-byte
+//    loads of that key's codes, and for values four tokens' 16 dims each; so every
+//    lane copies (cp.async) just the bytes that it will multiply, into a ring of its
+//    own in shared memory: no barrier between copy and use, and P^T comes from S^T by
+//    two 8 x 8 transpositions in registers (movmatrix).
 //  * e4m3 to fp16 is exact (one conversion for two codes).  Queries are brought
 //    to fp16 by a power of two for each row, exact but below 2^-25 of the row's
 //    largest element.  The K scale multiplies the scores, the V scale of the
-//    chunk relative to the largest seen multiplies P, both powers of two.
+//    half chunk relative to the largest seen multiplies P, both powers of two.
 //  * P is kept as exp2(s - m + 7) with m raised only when a score passes it by 8:
 //    at most 2^15, in fp16 with full precision down to 2^-21 of the largest and a
 //    grain of 2^-31 of it, so even a tail of millions of small weights counts.
@@ -38,9 +41,9 @@ namespace {
 
 constexpr int WARPS = 8;
 constexpr int THREADS = WARPS * 32;
-constexpr int STAGES = 6;
-constexpr int TILE = 16;   // query rows of one tile
-constexpr int CHUNK = 16;  // tokens of one chunk (a page holds whole chunks)
+constexpr int STAGES = 3;
+constexpr int MAX_TILE = 16;  // query rows of one tile: 8 or 16
+constexpr int CHUNK = 32;     // tokens of one chunk; its halves of 16 lie in one page each
 constexpr float kShift = 7.0f;
 constexpr float kSlack = 8.0f;
 
@@ -57,14 +60,15 @@ struct DecodeParams {
   float scale_log2;
 };
 
-template <int D>
+template <int D, int NR>
 struct DecodeSmem {
-  static constexpr int STAGE = CHUNK * D * 2;          // bytes of one chunk, keys and values
-  static constexpr int PITCH = D / 4 + 1;              // 16-byte units of one row of the merge buffers
+  static constexpr int TILE = 8 * NR;
+  static constexpr int STAGE = CHUNK * D * 2;  // bytes of one chunk, keys and values
+  static constexpr int PITCH = D / 4 + 1;      // 16-byte units of one row of the merge buffers
   uint8_t ring[WARPS][STAGES][STAGE];
   float4 merge[WARPS / 2][TILE * PITCH];
   float m[WARPS][TILE], l[WARPS][TILE];
-  uint32_t meta[WARPS][STAGES];  // bit 16: the page is good; scale bytes of keys (0-7) and values (8-15)
+  uint2 meta[WARPS][STAGES];  // scale bytes (k, v of the first half, k, v of the second); which halves' pages are good
   int32_t e[WARPS];
   int64_t warp_sum[WARPS];
   int64_t begin_off;
@@ -74,29 +78,38 @@ struct DecodeSmem {
 // One run's piece of one tile: chunks cb .. ce-1 of the tile's nch.
 struct Segment {
   KvSeq seq;
-  int s, nch, tiles, sub, cb, ce;  // sub = kv head * tiles + row tile
-  int64_t left;                    // chunks of the run from cb on
+  int s, nch, tiles, hk, rt, cb, ce;  // kv head and row tile
+  int64_t left;                       // chunks of the run from cb on
 };
 
+template <int TILE>
 __device__ __forceinline__ int seq_tiles(const DecodeParams& p, const KvSeq& q) {
   return int((int64_t(q.q) * p.group + TILE - 1) / TILE);
 }
 __device__ __forceinline__ int seq_chunks(const KvSeq& q) { return max(1, (q.len + CHUNK - 1) / CHUNK); }
 
+template <int TILE>
 __device__ __forceinline__ void seg_open(const DecodeParams& p, Segment& g, int s, int64_t off, int64_t left) {
   g.seq = kv_seq(p.b, p.c.ps, s);
   g.s = s;
   g.nch = seq_chunks(g.seq);
-  g.tiles = seq_tiles(p, g.seq);
-  g.sub = int(off / g.nch);
-  g.cb = int(off - int64_t(g.sub) * g.nch);
+  g.tiles = seq_tiles<TILE>(p, g.seq);
+  const int sub = int(off / g.nch);
+  g.hk = sub / max(g.tiles, 1);
+  g.rt = sub - g.hk * g.tiles;
+  g.cb = int(off - int64_t(sub) * g.nch);
   g.left = left;
   g.ce = int(min(int64_t(g.nch), g.cb + left));
 }
+template <int TILE>
 __device__ __forceinline__ bool seg_next(const DecodeParams& p, Segment& g) {
   g.left -= g.ce - g.cb;
   if (g.left <= 0) return false;
-  if (++g.sub < g.tiles * p.c.Hkv) {
+  if (++g.rt == g.tiles) {
+    g.rt = 0;
+    ++g.hk;
+  }
+  if (g.hk < p.c.Hkv) {
     g.cb = 0;
     g.ce = int(min(int64_t(g.nch), g.left));
     return true;
@@ -104,15 +117,16 @@ __device__ __forceinline__ bool seg_next(const DecodeParams& p, Segment& g) {
   int s = g.s + 1;
   while (s < p.b.B && kv_seq(p.b, p.c.ps, s).q == 0) ++s;
   if (s >= p.b.B) return false;
-  seg_open(p, g, s, 0, g.left);
+  seg_open<TILE>(p, g, s, 0, g.left);
   return true;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 or 8 bytes, zeros when not ok
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -139,25 +153,40 @@ __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+// over the eight lanes that share t
+__device__ __forceinline__ float column_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float column_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements, two to a lane
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 // Which bytes are e4m3 NaN (0x7f, 0xff): 0x80 there.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-// 16-byte unit c of row r in a merge buffer (the exclusive-or spreads a quad's blocks over the banks).
-template <int D>
+// 16-byte unit c of row r in a merge buffer (the exclusive-or spreads a column's lanes over the banks)
+template <int D, int NR>
 __device__ __forceinline__ int merge_at(int r, int c) {
-  return r * DecodeSmem<D>::PITCH + (c ^ (((c >> 3) & 3) << 1));
+  return r * DecodeSmem<D, NR>::PITCH + (c ^ ((c >> 3) & 3));
 }
 
-template <int D>
+// NR: products of 8 query rows to a tile
+template <int D, int NR>
 __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_constant__ DecodeParams p) {
-  using Smem = DecodeSmem<D>;
+  using Smem = DecodeSmem<D, NR>;
+  constexpr int TILE = 8 * NR;
   constexpr int KL = D / 64;   // 16-byte key loads of one lane and key
-  constexpr int NT = D / 8;    // n tiles of the output: dim = lane group * NT + n tile
-  constexpr int VB = NT;       // value bytes of one lane and token
+  constexpr int MTS = D / 16;  // m tiles of the output
+  constexpr int VB = D / 8;    // value bytes of one lane and token: dims g * VB + (0 .. VB-1)
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -169,7 +198,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
   int64_t mine = 0;
   for (int s = first; s < end; ++s) {
     const KvSeq q = kv_seq(b, p.c.ps, s);
-    mine += int64_t(seq_tiles(p, q)) * p.c.Hkv * seq_chunks(q);
+    mine += int64_t(seq_tiles<TILE>(p, q)) * p.c.Hkv * seq_chunks(q);
   }
   int64_t before = mine;
 #pragma unroll
@@ -196,7 +225,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
     int64_t at = before;
     for (int s = first; s < end; ++s) {
       const KvSeq q = kv_seq(b, p.c.ps, s);
-      const int64_t size = int64_t(seq_tiles(p, q)) * p.c.Hkv * seq_chunks(q);
+      const int64_t size = int64_t(seq_tiles<TILE>(p, q)) * p.c.Hkv * seq_chunks(q);
       if (run0 < at + size) {
         sm.begin_seq = s;
         sm.begin_off = run0 - at;
@@ -207,18 +236,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
   }
   __syncthreads();
   Segment f, c;  // where copies are, and where products are
-  seg_open(p, c, sm.begin_seq, sm.begin_off, run1 - run0);
+  seg_open<TILE>(p, c, sm.begin_seq, sm.begin_off, run1 - run0);
   f = c;
 
   // ---------------------------------------------------------------- the copies of one warp
   const uint32_t ring = smem_u32(sm.ring[warp]);
-  const int page_chunks = p.c.ps / CHUNK;
-  bool f_ok = true;
-  int fc = f.cb + warp, f_base = 0, pages = 0, scales = 0;
-  bool f_new = true;
+  const int page_halves = p.c.ps / 16;
+  const int64_t k_lane = int64_t(g) * p.c.token_stride + t * 16, v_lane = int64_t(2 * t) * p.c.token_stride + g * VB;
+  const int64_t eight = 8 * p.c.token_stride;
+  bool f_ok = true, f_new = true;
+  int fc = f.cb + warp, f_at = 0;
+  int64_t offs[2] = {-1, -1};  // of the lane's chunk: where its halves begin in the pool, below 0: nowhere
+  uint32_t scales = 0;
   auto settle = [&]() {  // on to a segment that has a chunk for this warp
     while (f_ok && fc >= f.ce) {
-      f_ok = seg_next(p, f);
+      f_ok = seg_next<TILE>(p, f);
       fc = f.cb + warp;
       f_new = true;
     }
@@ -226,46 +258,57 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
   settle();
   auto fetch = [&](int stage) {
     if (f_ok) {
-      int at = (fc - f_base) / WARPS;
-      if (f_new || at == 32) {  // the pages of the next 32 chunks, one to a lane
-        f_base = fc;
+      if (f_new || f_at == 32) {  // the next 32 chunks' pages and scales, a chunk to a lane
         f_new = false;
-        at = 0;
+        f_at = 0;
         const int ch = fc + lane * WARPS;
-        pages = -1;
         scales = 0;
-        if (ch < f.ce && ch * CHUNK < f.seq.len) {
-          pages = __ldg(b.table + int64_t(f.s) * b.max_pages + ch / page_chunks);
-          if (pages < 0 || pages >= p.c.num_pages) {
-            record_error(b.status, kKvInvalid, uint32_t(f.s), uint32_t(pages), uint32_t(ch / page_chunks));
-            pages = -1;
-          } else {
-            const int64_t i = int64_t(pages) * p.c.Hkv + f.sub / f.tiles;
-            scales = 0x10000 | int(p.c.ks[i]) | (int(p.c.vs[i]) << 8);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int half = ch * 2 + h;
+          offs[h] = -1;
+          if (ch < f.ce && half * 16 < f.seq.len) {
+            const int no = half / page_halves;
+            const int page = __ldg(b.table + int64_t(f.s) * b.max_pages + no);
+            if (page < 0 || page >= p.c.num_pages) {
+              record_error(b.status, kKvInvalid, uint32_t(f.s), uint32_t(page), uint32_t(no));
+            } else {
+              offs[h] = int64_t(page) * p.c.page_stride + int64_t(f.hk) * p.c.head_stride +
+                        int64_t((half - no * page_halves) * 16) * p.c.token_stride;
+              const int64_t i = int64_t(page) * p.c.Hkv + f.hk;
+              scales |= (uint32_t(p.c.ks[i]) | (uint32_t(p.c.vs[i]) << 8)) << (16 * h);
+            }
           }
         }
         __syncwarp();
       }
-      const int page = __shfl_sync(0xffffffffu, pages, at);
-      if (page >= 0) {
-        const int64_t off = int64_t(page) * p.c.page_stride + int64_t(f.sub / f.tiles) * p.c.head_stride +
-                            int64_t(fc % page_chunks * CHUNK) * p.c.token_stride;
-        const uint32_t dst = ring + uint32_t(stage * Smem::STAGE) + uint32_t(lane * 16);
+      const uint32_t dst = ring + uint32_t(stage * Smem::STAGE) + uint32_t(lane * 16);
+      const uint32_t vdst = ring + uint32_t(stage * Smem::STAGE + CHUNK * D) + uint32_t(lane * VB);
+      uint32_t good = 0;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+      for (int h = 0; h < 2; ++h) {
+        const int64_t off = __shfl_sync(0xffffffffu, offs[h], f_at);
+        const bool ok = off >= 0;
+        good |= ok ? 1u << h : 0u;
+        const uint8_t* ksrc = p.c.k + (ok ? off + k_lane : 0);
+        const uint8_t* vsrc = p.c.v + (ok ? off + v_lane : 0);
+        const int64_t step8 = ok ? eight : 0, step1 = ok ? p.c.token_stride : 0;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int j = 0; j < KL; ++j)
-            cp_async16(dst + uint32_t((nt * KL + j) * 512), p.c.k + off + (nt * 8 + g) * p.c.token_stride + j * 64 + t * 16);
-        const uint32_t vdst = ring + uint32_t(stage * Smem::STAGE + CHUNK * D) + uint32_t(lane * VB);
+            cp_async16(dst + uint32_t(((h * 2 + r) * KL + j) * 512), ksrc + r * step8 + (ok ? j * 64 : 0), ok);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint8_t* src = p.c.v + off + (2 * t + (j & 1) + (j >> 1) * 8) * p.c.token_stride + g * VB;
-          if (VB == 16) cp_async16(vdst + uint32_t(j * 32 * VB), src);
-          else cp_async8(vdst + uint32_t(j * 32 * VB), src);
+          const uint8_t* src = vsrc + (j >> 1) * step8 + (j & 1) * step1;
+          const uint32_t to = vdst + uint32_t((h * 4 + j) * 32 * VB);
+          if (VB == 16) cp_async16(to, src, ok);
+          else cp_async8(to, src, ok);
         }
       }
-      const int sc = __shfl_sync(0xffffffffu, scales, at);
-      if (lane == 0) sm.meta[warp][stage] = uint32_t(sc);
+      const uint32_t sc = __shfl_sync(0xffffffffu, scales, f_at);
+      if (lane == 0) sm.meta[warp][stage] = make_uint2(sc, good);
+      ++f_at;
       fc += WARPS;
       settle();
     }
@@ -277,19 +320,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
   int stage = 0;
   int64_t at = run0;  // position of c.cb in the list
   while (true) {
-    const int hk = c.sub / c.tiles, r0 = (c.sub % c.tiles) * TILE;
+    const int r0 = c.rt * TILE;
     const int rows = min(TILE, int(int64_t(c.seq.q) * p.group - r0));
-    // this lane's two rows: key limits and queries
-    int lim[2];
-    float f_row[2];
-    uint32_t qa[KL * 4][4];
     const int start = c.seq.len - c.seq.q;
+    auto limit = [&](int row) {  // keys that a row of the tile sees
+      return p.causal ? max(0, min(c.seq.len, start + (r0 + min(row, rows - 1)) / p.group + 1)) : c.seq.len;
+    };
+    // queries: row g of each product; scales and limits of rows 2t and 2t + 1
+    uint32_t qb[NR][KL * 4][2];
+    float f_row[NR][2];
+    int lim[NR][2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int r = r0 + min(g + 8 * x, rows - 1);
+    for (int x = 0; x < NR; ++x) {
+      const int r = r0 + min(8 * x + g, rows - 1);
       const int i = r / p.group;
-      lim[x] = p.causal ? max(0, min(c.seq.len, start + i + 1)) : c.seq.len;
-      const uint16_t* src = p.q + int64_t(c.seq.row0 + i) * p.q_ts + int64_t(hk * p.group + r % p.group) * p.q_hs;
+      const uint16_t* src = p.q + int64_t(c.seq.row0 + i) * p.q_ts + int64_t(c.hk * p.group + r - i * p.group) * p.q_hs;
       uint4 w[KL * 2];
       float amax = 0.0f;
 #pragma unroll
@@ -306,8 +351,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
       }
       amax = quad_max(amax);
       const int e = max(int(__float_as_uint(amax) >> 23) - 127, -126);
-      const float down = pow2f(-e);
-      f_row[x] = pow2f(e) * p.scale_log2;
+      const float down = pow2f(-e), fr = pow2f(e) * p.scale_log2;
 #pragma unroll
       for (int j = 0; j < KL * 2; ++j) {
         const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
@@ -316,99 +360,131 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
         for (int k = 0; k < 4; ++k)
           h[k] = pack_f16x2(__uint_as_float(u[k] << 16) * down, __uint_as_float(u[k] & 0xFFFF0000u) * down);
         // dims 4v .. 4v+3 of the lane's 16 are the k slots (2t, 2t+1, 2t+8, 2t+9) of step v
-        qa[2 * j][x] = h[0];
-        qa[2 * j][2 + x] = h[1];
-        qa[2 * j + 1][x] = h[2];
-        qa[2 * j + 1][2 + x] = h[3];
+        qb[x][2 * j][0] = h[0];
+        qb[x][2 * j][1] = h[1];
+        qb[x][2 * j + 1][0] = h[2];
+        qb[x][2 * j + 1][1] = h[3];
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        f_row[x][y] = __shfl_sync(0xffffffffu, fr, (2 * t + y) * 4);
+        lim[x][y] = limit(8 * x + 2 * t + y);
       }
     }
-    const int min_lim = p.causal ? max(0, min(c.seq.len, start + r0 / p.group + 1)) : c.seq.len;
+    const int min_lim = limit(0);
 
-    float o[NT][4];
+    float o[NR][MTS][4];  // dims g * VB + i and g * VB + VB/2 + i of rows 2t, 2t + 1
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int x = 0; x < NR; ++x)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+      for (int i = 0; i < MTS; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[x][i][j] = 0.0f;
+    float m[NR][2], l[NR][2];
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      m[x][0] = m[x][1] = -INFINITY;
+      l[x][0] = l[x][1] = 0.0f;
+    }
     int ve = -127;
 
     for (int ch = c.cb + warp; ch < c.ce; ch += WARPS) {
       cp_async_wait<STAGES - 2>();
       __syncwarp();
-      const uint32_t meta = sm.meta[warp][stage];
+      const uint2 meta = sm.meta[warp][stage];
       const uint32_t src = ring + uint32_t(stage * Smem::STAGE);
-      if (meta & 0x10000u) {
-        const int tok = ch * CHUNK;
-        float s[2][4];
+      const int tok = ch * CHUNK;
+      const bool edge = tok + CHUNK > min_lim || meta.y != 3u;
+      float s[2][NR][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
+      for (int h = 0; h < 2; ++h) {
+        // two chains of products, one for each half of the dims
+        float part[KL][NR][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[nt][j] = 0.0f;
+        for (int j = 0; j < KL; ++j) {
 #pragma unroll
-          for (int j = 0; j < KL; ++j) {
-            const uint4 w = lds128(src + uint32_t((nt * KL + j) * 512 + lane * 16));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          for (int x = 0; x < NR; ++x)
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              mma_f16(s[nt], qa[j * 4 + v][0], qa[j * 4 + v][1], qa[j * 4 + v][2], qa[j * 4 + v][3],
-                      e4m3x2_to_f16x2(u[v]), e4m3x2_to_f16x2_hi(u[v]));
+            for (int k = 0; k < 4; ++k) part[j][x][k] = 0.0f;
+          const uint4 a = lds128(src + uint32_t(((h * 2) * KL + j) * 512 + lane * 16));
+          const uint4 d = lds128(src + uint32_t(((h * 2 + 1) * KL + j) * 512 + lane * 16));
+          const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a0 = e4m3x2_to_f16x2(u[k]), a2 = e4m3x2_to_f16x2_hi(u[k]);
+            const uint32_t a1 = e4m3x2_to_f16x2(v[k]), a3 = e4m3x2_to_f16x2_hi(v[k]);
+#pragma unroll
+            for (int x = 0; x < NR; ++x) mma_f16(part[j][x], a0, a1, a2, a3, qb[x][j * 4 + k][0], qb[x][j * 4 + k][1]);
           }
         }
-        const float kf = pow2f(int(meta & 0xFFu) - 127);
-        const float fx[2] = {f_row[0] * kf, f_row[1] * kf};
-        const bool edge = tok + CHUNK > min_lim;
-        float mx[2] = {-INFINITY, -INFINITY};
+        const float kf = pow2f(int((meta.x >> (16 * h)) & 0xFFu) - 127);
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int x = 0; x < NR; ++x)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[nt][j] *= fx[j >> 1];
-            if (edge && tok + nt * 8 + 2 * t + (j & 1) >= lim[j >> 1]) s[nt][j] = -INFINITY;
-            mx[j >> 1] = fmaxf(mx[j >> 1], s[nt][j]);
-          }
-        mx[0] = quad_max(mx[0]);
-        mx[1] = quad_max(mx[1]);
-        const int vb = int((meta >> 8) & 0xFFu);
-        const bool up = vb != 255 && vb - 127 > ve;
-        if (__any_sync(0xffffffffu, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack) || up) {
+          for (int k = 0; k < 4; ++k)
+            s[h][x][k] = (KL == 2 ? part[0][x][k] + part[KL - 1][x][k] : part[0][x][k]) * (f_row[x][k & 1] * kf);
+      }
+      if (edge) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int x = 0; x < NR; ++x)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (!(meta.y >> h & 1u) || tok + h * 16 + g + (k >> 1) * 8 >= lim[x][k & 1]) s[h][x][k] = -INFINITY;
+      }
+      float mx[NR][2];
+      bool raise = false;
+#pragma unroll
+      for (int x = 0; x < NR; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          mx[x][y] = column_max(fmaxf(fmaxf(s[0][x][y], s[0][x][2 + y]), fmaxf(s[1][x][y], s[1][x][2 + y])));
+          raise |= mx[x][y] > m[x][y] + kSlack;
+        }
+      const int vb[2] = {int((meta.x >> 8) & 0xFFu), int(meta.x >> 24)};
+      const int vtop = max(vb[0] == 255 ? -127 : vb[0] - 127, vb[1] == 255 ? -127 : vb[1] - 127);
+      if (__any_sync(0xffffffffu, raise) || vtop > ve) {
+        const float down = pow2f(max(min(ve - vtop, 0), -127));
+        ve = max(ve, vtop);
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
           float a[2];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float mn = mx[x] > m[x] + kSlack ? mx[x] : m[x];
-            a[x] = mn == m[x] ? 1.0f : ex2_approx(m[x] - mn);
-            m[x] = mn;
-            l[x] *= a[x];
-          }
-          if (up) {
-            const float down = pow2f(max(ve - (vb - 127), -127));
-            ve = vb - 127;
-            a[0] *= down;
-            a[1] *= down;
+          for (int y = 0; y < 2; ++y) {
+            const float mn = mx[x][y] > m[x][y] + kSlack ? mx[x][y] : m[x][y];
+            a[y] = mn == m[x][y] ? 1.0f : ex2_approx(m[x][y] - mn);
+            m[x][y] = mn;
+            l[x][y] *= a[y];
+            a[y] *= down;
           }
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            o[i][0] *= a[0];
-            o[i][1] *= a[0];
-            o[i][2] *= a[1];
-            o[i][3] *= a[1];
-          }
+          for (int i = 0; i < MTS; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[x][i][k] *= a[k & 1];
         }
-        const float vf = vb == 255 ? pow2f(128) : pow2f(max(vb - 127 - ve, -127));
-        const float nm[2] = {m[0] == -INFINITY ? kShift : kShift - m[0], m[1] == -INFINITY ? kShift : kShift - m[1]};
+      }
+      uint32_t pb[2][NR][2];  // P^T: tokens (2t, 2t+1) and (2t+8, 2t+9) of the half, row g
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+      for (int h = 0; h < 2; ++h) {
+        const float vf = vb[h] == 255 ? pow2f(128) : pow2f(max(vb[h] - 127 - ve, -127));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[nt][j] = ex2_approx(s[nt][j] + nm[j >> 1]);
-        l[0] += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
-        l[1] += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
-        uint32_t pa[4];
-        pa[0] = pack_f16x2(s[0][0] * vf, s[0][1] * vf);
-        pa[1] = pack_f16x2(s[0][2] * vf, s[0][3] * vf);
-        pa[2] = pack_f16x2(s[1][0] * vf, s[1][1] * vf);
-        pa[3] = pack_f16x2(s[1][2] * vf, s[1][3] * vf);
-
+        for (int x = 0; x < NR; ++x) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float mm = m[x][k & 1];
+            s[h][x][k] = ex2_approx(s[h][x][k] + (mm == -INFINITY ? kShift : kShift - mm));
+          }
+          l[x][0] += s[h][x][0] + s[h][x][2];
+          l[x][1] += s[h][x][1] + s[h][x][3];
+          pb[h][x][0] = transposed(pack_f16x2(s[h][x][0] * vf, s[h][x][1] * vf));
+          pb[h][x][1] = transposed(pack_f16x2(s[h][x][2] * vf, s[h][x][3] * vf));
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         uint32_t vw[4][VB / 4];
-        const uint32_t vsrc = src + uint32_t(CHUNK * D + lane * VB);
+        const uint32_t vsrc = src + uint32_t(CHUNK * D + h * 4 * 32 * VB + lane * VB);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (VB == 16) {
@@ -425,12 +501,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
         }
         if (edge) {
           // slots past the sequence's end hold anything: zero.  A NaN value that some rows see and
-          // others do not would reach the others as 0 * NaN: it is taken out here and counted for
+          // others do not would reach the others as NaN * 0: it is taken out here and counted for
           // the rows that see it by a product of 0/1 matrices.
           uint32_t nans = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const bool past = tok + 2 * t + (j & 1) + (j >> 1) * 8 >= c.seq.len;
+            const bool past = tok + h * 16 + 2 * t + (j & 1) + (j >> 1) * 8 >= c.seq.len;
 #pragma unroll
             for (int k = 0; k < VB / 4; ++k) {
               if (past) vw[j][k] = 0;
@@ -438,22 +514,28 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
             }
           }
           if (__any_sync(0xffffffffu, nans != 0)) {
-            uint32_t sees[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int tk = tok + 2 * t + (j >> 1) * 8, li = lim[j & 1];
-              sees[j] = (tk < li ? 0x3C00u : 0u) | (tk + 1 < li ? 0x3C000000u : 0u);
-            }
+            for (int x = 0; x < NR; ++x) {
+              const int li = limit(8 * x + g), tk = tok + h * 16 + 2 * t;
+              const uint32_t b0 = (tk < li ? 0x3C00u : 0u) | (tk + 1 < li ? 0x3C000000u : 0u);
+              const uint32_t b1 = (tk + 8 < li ? 0x3C00u : 0u) | (tk + 9 < li ? 0x3C000000u : 0u);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              uint32_t bit[4];
+              for (int i = 0; i < MTS; ++i) {
+                uint32_t a[2][2];  // [dims i or VB/2 + i][tokens 2t.. or 2t+8..]
 #pragma unroll
-              for (int j = 0; j < 4; ++j) bit[j] = (nan_bytes(vw[j][i / 4]) >> (8 * (i % 4))) & 0x80u ? 0x3C00u : 0u;
-              float cnt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              mma_f16(cnt, sees[0], sees[1], sees[2], sees[3], bit[0] | (bit[1] << 16), bit[2] | (bit[3] << 16));
+                for (int q = 0; q < 2; ++q)
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (cnt[j] > 0.0f) o[i][j] = __uint_as_float(0x7FFFFFFFu);
+                  for (int y = 0; y < 2; ++y) {
+                    const int by = q * (VB / 2) + i;
+                    a[q][y] = ((nan_bytes(vw[2 * y][by / 4]) >> (8 * (by % 4))) & 0x80u ? 0x3C00u : 0u) |
+                              ((nan_bytes(vw[2 * y + 1][by / 4]) >> (8 * (by % 4))) & 0x80u ? 0x3C000000u : 0u);
+                  }
+                float cnt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma_f16(cnt, a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (cnt[k] > 0.0f) o[x][i][k] = __uint_as_float(0x7FFFFFFFu);
+              }
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -462,112 +544,120 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
           }
         }
 #pragma unroll
-        for (int i = 0; i < NT; i += 2) {
+        for (int i = 0; i < MTS; i += 2) {
           const uint32_t sel = (i & 2) ? 0x7362u : 0x5140u;
-          const uint32_t x = __byte_perm(vw[0][i / 4], vw[1][i / 4], sel), y = __byte_perm(vw[2][i / 4], vw[3][i / 4], sel);
-          mma_f16(o[i], pa[0], pa[1], pa[2], pa[3], e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
-          mma_f16(o[i + 1], pa[0], pa[1], pa[2], pa[3], e4m3x2_to_f16x2_hi(x), e4m3x2_to_f16x2_hi(y));
+          const int lo = i / 4, hi = VB / 8 + i / 4;
+          const uint32_t a0 = __byte_perm(vw[0][lo], vw[1][lo], sel), a1 = __byte_perm(vw[0][hi], vw[1][hi], sel);
+          const uint32_t a2 = __byte_perm(vw[2][lo], vw[3][lo], sel), a3 = __byte_perm(vw[2][hi], vw[3][hi], sel);
+          const uint32_t e0 = e4m3x2_to_f16x2(a0), e1 = e4m3x2_to_f16x2(a1), e2 = e4m3x2_to_f16x2(a2),
+                         e3 = e4m3x2_to_f16x2(a3);
+          const uint32_t h0 = e4m3x2_to_f16x2_hi(a0), h1 = e4m3x2_to_f16x2_hi(a1), h2 = e4m3x2_to_f16x2_hi(a2),
+                         h3 = e4m3x2_to_f16x2_hi(a3);
+#pragma unroll
+          for (int x = 0; x < NR; ++x) {
+            mma_f16(o[x][i], e0, e1, e2, e3, pb[h][x][0], pb[h][x][1]);
+            mma_f16(o[x][i + 1], h0, h1, h2, h3, pb[h][x][0], pb[h][x][1]);
+          }
         }
       }
       __syncwarp();
-      fetch((stage + STAGES - 1) % STAGES);
+      fetch(stage == 0 ? STAGES - 1 : stage - 1);
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
 
     // ---------------------------------------------------------------- the eight warps' results become one
-    l[0] = quad_sum(l[0]);
-    l[1] = quad_sum(l[1]);
-    if (t == 0) {
-      sm.m[warp][g] = m[0];
-      sm.m[warp][g + 8] = m[1];
-      sm.l[warp][g] = l[0];
-      sm.l[warp][g + 8] = l[1];
-    }
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        l[x][y] = column_sum(l[x][y]);
+        if (g == 0) {
+          sm.m[warp][8 * x + 2 * t + y] = m[x][y];
+          sm.l[warp][8 * x + 2 * t + y] = l[x][y];
+        }
+      }
     if (lane == 0) sm.e[warp] = ve;
     __syncthreads();
     int em = -127;
-    float M[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      em = max(em, sm.e[w]);
-      M[0] = fmaxf(M[0], sm.m[w][g]);
-      M[1] = fmaxf(M[1], sm.m[w][g + 8]);
-    }
-    {
-      const float vd = pow2f(max(ve - em, -127));
-      const float a0 = m[0] == -INFINITY ? vd * (l[0] == 0.0f ? 1.0f : l[0]) : vd * ex2_approx(m[0] - M[0]);
-      const float a1 = m[1] == -INFINITY ? vd * (l[1] == 0.0f ? 1.0f : l[1]) : vd * ex2_approx(m[1] - M[1]);
+    for (int w = 0; w < WARPS; ++w) em = max(em, sm.e[w]);
+    const float vd = pow2f(max(ve - em, -127));
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        o[i][0] *= a0;
-        o[i][1] *= a0;
-        o[i][2] *= a1;
-        o[i][3] *= a1;
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, sm.m[w][8 * x + 2 * t + y]);
+        // a warp that saw no key has m = -inf, l = 0 and o = 0 (l is NaN when its scores were)
+        const float a = m[x][y] == -INFINITY ? vd * (l[x][y] == 0.0f ? 1.0f : l[x][y]) : vd * ex2_approx(m[x][y] - top);
+#pragma unroll
+        for (int i = 0; i < MTS; ++i) {
+          o[x][i][y] *= a;
+          o[x][i][2 + y] *= a;
+        }
       }
-    }
-    // o[i][0..1]: row g, dims 2t * NT + i and (2t+1) * NT + i; o[i][2..3]: row g + 8
+    // a row's dims g * VB .. g * VB + VB - 1 as 16-byte units
     auto each_unit = [&](auto&& fn) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < NR; ++x)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int i4 = 0; i4 < NT / 4; ++i4) fn(x, h, i4, merge_at<D>(g + 8 * x, (2 * t + h) * (NT / 4) + i4));
+          for (int u = 0; u < VB / 4; ++u) {
+            constexpr int HALF = VB / 8;  // units of dims i, then of dims VB/2 + i
+            const int q = u / HALF * 2 + y, i = (u % HALF) * 4;
+            fn(merge_at<D, NR>(8 * x + 2 * t + y, g * (VB / 4) + u), o[x][i][q], o[x][i + 1][q], o[x][i + 2][q],
+               o[x][i + 3][q]);
+          }
     };
-    if (warp >= WARPS / 2) {
-      float4* buf = sm.merge[warp - WARPS / 2];
-      each_unit([&](int x, int h, int i4, int a) {
-        buf[a] = make_float4(o[4 * i4][2 * x + h], o[4 * i4 + 1][2 * x + h], o[4 * i4 + 2][2 * x + h], o[4 * i4 + 3][2 * x + h]);
-      });
-    }
+    float4* buf = sm.merge[warp % (WARPS / 2)];
+    if (warp >= WARPS / 2) each_unit([&](int i, float v0, float v1, float v2, float v3) { buf[i] = make_float4(v0, v1, v2, v3); });
     __syncthreads();
-    if (warp < WARPS / 2) {
-      float4* buf = sm.merge[warp];
-      each_unit([&](int x, int h, int i4, int a) {
-        const float4 w = buf[a];
-        buf[a] = make_float4(w.x + o[4 * i4][2 * x + h], w.y + o[4 * i4 + 1][2 * x + h], w.z + o[4 * i4 + 2][2 * x + h],
-                             w.w + o[4 * i4 + 3][2 * x + h]);
+    if (warp < WARPS / 2)
+      each_unit([&](int i, float v0, float v1, float v2, float v3) {
+        const float4 w = buf[i];
+        buf[i] = make_float4(w.x + v0, w.y + v1, w.z + v2, w.w + v3);
       });
-    }
     __syncthreads();
-    // sixteen threads to a row now
-    constexpr int EPT = D / 16;
-    const int row = tid >> 4, d0 = (tid & 15) * EPT;
+    constexpr int EPT = TILE * D / THREADS < 4 ? 4 : TILE * D / THREADS;  // elements of one thread
+    const int row = tid / (D / EPT), d0 = tid % (D / EPT) * EPT;
+    const bool mine_row = row < rows;
     float M1 = -INFINITY, L = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) M1 = fmaxf(M1, sm.m[w][row]);
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float mw = sm.m[w][row];
-      L += mw == -INFINITY ? sm.l[w][row] : sm.l[w][row] * ex2_approx(mw - M1);
-    }
     float acc[EPT];
+    if (mine_row) {
 #pragma unroll
-    for (int u = 0; u < EPT / 4; ++u) {
-      const int a = merge_at<D>(row, d0 / 4 + u);
-      const float4 w0 = sm.merge[0][a], w1 = sm.merge[1][a], w2 = sm.merge[2][a], w3 = sm.merge[3][a];
-      acc[4 * u] = (w0.x + w1.x) + (w2.x + w3.x);
-      acc[4 * u + 1] = (w0.y + w1.y) + (w2.y + w3.y);
-      acc[4 * u + 2] = (w0.z + w1.z) + (w2.z + w3.z);
-      acc[4 * u + 3] = (w0.w + w1.w) + (w2.w + w3.w);
+      for (int w = 0; w < WARPS; ++w) M1 = fmaxf(M1, sm.m[w][row]);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float mw = sm.m[w][row];
+        L += mw == -INFINITY ? sm.l[w][row] : sm.l[w][row] * ex2_approx(mw - M1);
+      }
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L, pe = pow2f(em);
+#pragma unroll
+      for (int u = 0; u < EPT / 4; ++u) {
+        const int a = merge_at<D, NR>(row, d0 / 4 + u);
+        const float4 w0 = sm.merge[0][a], w1 = sm.merge[1][a], w2 = sm.merge[2][a], w3 = sm.merge[3][a];
+        acc[4 * u] = ((w0.x + w1.x) + (w2.x + w3.x)) * inv * pe;
+        acc[4 * u + 1] = ((w0.y + w1.y) + (w2.y + w3.y)) * inv * pe;
+        acc[4 * u + 2] = ((w0.z + w1.z) + (w2.z + w3.z)) * inv * pe;
+        acc[4 * u + 3] = ((w0.w + w1.w) + (w2.w + w3.w)) * inv * pe;
+      }
     }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L, pe = pow2f(em);
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) acc[i] = acc[i] * inv * pe;
 
     bool done = true;
     if (c.cb != 0 || c.ce != c.nch) {
       const int64_t t0 = at - c.cb;  // the tile's first chunk in the list
       const int64_t c0 = ((t0 + 1) * n - 1) / total, c1 = ((t0 + c.nch) * n - 1) / total;
       constexpr int SLOT = TILE * D + 2 * TILE;
-      float* mineat = p.partial + (2 * cta + (c.cb == 0 ? 1 : 0)) * SLOT;
-      if (row < rows) {
+      float* slot = p.partial + (2 * cta + (c.cb == 0 ? 1 : 0)) * SLOT;
+      if (mine_row) {
 #pragma unroll
         for (int u = 0; u < EPT / 4; ++u)
-          st_global_cg_v4f(mineat + row * D + d0 + 4 * u, acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
-        if ((tid & 15) == 0) {
-          __stcg(mineat + TILE * D + row, M1);
-          __stcg(mineat + TILE * D + TILE + row, L);
+          st_global_cg_v4f(slot + row * D + d0 + 4 * u, acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
+        if (d0 == 0) {
+          __stcg(slot + TILE * D + row, M1);
+          __stcg(slot + TILE * D + TILE + row, L);
         }
       }
       __threadfence();
@@ -579,23 +669,24 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
       }
       __syncthreads();
       done = sm.last;
-      if (done && row < rows) {
+      if (done && mine_row) {
         __threadfence();
-        const float* tile = p.partial;
         M1 = -INFINITY;
-        for (int64_t x = c0; x <= c1; ++x) M1 = fmaxf(M1, __ldcg(tile + (2 * x + (x == c0)) * SLOT + TILE * D + row));
+#pragma unroll 4
+        for (int64_t x = c0; x <= c1; ++x)
+          M1 = fmaxf(M1, __ldcg(p.partial + (2 * x + (x == c0)) * SLOT + TILE * D + row));
         L = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPT; ++i) acc[i] = 0.0f;
 #pragma unroll 4
         for (int64_t x = c0; x <= c1; ++x) {
-          const float* slot = tile + (2 * x + (x == c0)) * SLOT;
-          const float mw = __ldcg(slot + TILE * D + row), lw = __ldcg(slot + TILE * D + TILE + row);
+          const float* from = p.partial + (2 * x + (x == c0)) * SLOT;
+          const float mw = __ldcg(from + TILE * D + row), lw = __ldcg(from + TILE * D + TILE + row);
           const float wgt = mw == -INFINITY ? lw : lw * ex2_approx(mw - M1);
           L += wgt;
 #pragma unroll
           for (int u = 0; u < EPT / 4; ++u) {
-            const float4 w = ld_global_cg_v4f(slot + row * D + d0 + 4 * u);
+            const float4 w = ld_global_cg_v4f(from + row * D + d0 + 4 * u);
             acc[4 * u] = fmaf(wgt, w.x, acc[4 * u]);
             acc[4 * u + 1] = fmaf(wgt, w.y, acc[4 * u + 1]);
             acc[4 * u + 2] = fmaf(wgt, w.z, acc[4 * u + 2]);
@@ -607,20 +698,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
         for (int i = 0; i < EPT; ++i) acc[i] *= i2;
       }
     }
-    if (done && row < rows) {
-      const int r = r0 + row, tok = c.seq.row0 + r / p.group, h = hk * p.group + r % p.group;
-      uint32_t w[EPT / 2];
-#pragma unroll
-      for (int i = 0; i < EPT / 2; ++i) w[i] = pack_bf16x2(acc[2 * i], acc[2 * i + 1]);
+    if (done && mine_row) {
+      const int r = r0 + row, i = r / p.group, tok = c.seq.row0 + i, h = c.hk * p.group + r - i * p.group;
       uint16_t* dst = p.out + (int64_t(tok) * p.H + h) * D + d0;
-      if (EPT == 8) st_global_v4(dst, w[0], w[1], w[EPT / 2 - 2], w[EPT / 2 - 1]);
-      else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-      if ((tid & 15) == 0 && p.lse)
-        p.lse[int64_t(h) * b.n_tokens + tok] =
-            L == 0.0f ? -INFINITY : (M1 - kShift + log2f(L)) * 0.69314718055994531f;
+#pragma unroll
+      for (int u = 0; u < EPT / 4; ++u)
+        reinterpret_cast<uint2*>(dst)[u] =
+            make_uint2(pack_bf16x2(acc[4 * u], acc[4 * u + 1]), pack_bf16x2(acc[4 * u + 2], acc[4 * u + 3]));
+      if (d0 == 0 && p.lse)
+        p.lse[int64_t(h) * b.n_tokens + tok] = L == 0.0f ? -INFINITY : (M1 - kShift + log2f(L)) * 0.69314718055994531f;
     }
     at += c.ce - c.cb;
-    if (!seg_next(p, c)) break;
+    if (!seg_next<TILE>(p, c)) break;
     __syncthreads();  // the merge buffers are free again
   }
   cp_async_wait<0>();
@@ -628,7 +717,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
 
 // ---------------------------------------------------------------- workspace: counters, then partial tiles
 size_t counters_bytes(int ctas) { return (size_t(ctas) * 4 + 255) / 256 * 256; }
-size_t decode_partial_bytes(int ctas, int D) { return size_t(ctas) * 2 * (TILE * D + 2 * TILE) * sizeof(float); }
+size_t decode_partial_bytes(int ctas, int D) { return size_t(ctas) * 2 * (MAX_TILE * D + 2 * MAX_TILE) * sizeof(float); }
 
 }  // namespace
 }  // namespace tl
@@ -690,9 +779,20 @@ extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
   p.group = a->H / c.H_kv;
   p.causal = a->causal;
   p.scale_log2 = (a->scale > 0.0f ? a->scale : 1.0f / std::sqrt(float(c.head_dim))) * 1.4426950408889634f;
-  const void* kernel = c.head_dim == 128 ? reinterpret_cast<const void*>(&kv_decode_kernel<128>)
-                                         : reinterpret_cast<const void*>(&kv_decode_kernel<64>);
-  const size_t smem = c.head_dim == 128 ? sizeof(DecodeSmem<128>) : sizeof(DecodeSmem<64>);
+  // Tiles of 8 query rows where a sequence's rows of one kv head fit in one, of 16 otherwise
+  const int per_seq = a->max_q_len ? std::min(a->max_q_len, a->n_tokens) : cdiv(a->n_tokens, a->B);
+  const bool small = int64_t(per_seq) * p.group <= 8;
+  const void* kernel;
+  size_t smem;
+  if (c.head_dim == 128) {
+    kernel = small ? reinterpret_cast<const void*>(&kv_decode_kernel<128, 1>)
+                   : reinterpret_cast<const void*>(&kv_decode_kernel<128, 2>);
+    smem = small ? sizeof(DecodeSmem<128, 1>) : sizeof(DecodeSmem<128, 2>);
+  } else {
+    kernel = small ? reinterpret_cast<const void*>(&kv_decode_kernel<64, 1>)
+                   : reinterpret_cast<const void*>(&kv_decode_kernel<64, 2>);
+    smem = small ? sizeof(DecodeSmem<64, 1>) : sizeof(DecodeSmem<64, 2>);
+  }
   void* args[] = {&p};
   return launch(kernel, di.sm_count, THREADS, smem, static_cast<cudaStream_t>(stream), args, false);
 }
