@@ -17,11 +17,11 @@
 // 16 tokens or dims by 8 query rows, so a tile of 8 rows wastes little of a product,
 // and a tile of 16 takes two.
 //  * The contraction index of a product may be permuted at will if both operands
-//    are.  Lane (g, t) holds, for key g, the dims that it gets from two 16-byte
-//    loads of that key's codes, and for values four tokens' 16 dims each; so every
-//    lane copies (cp.async) just the bytes that it will multiply, into a ring of its
-//    own in shared memory: no barrier between copy and use, and P^T comes from S^T by
-//    two 8 x 8 transpositions in registers (movmatrix).
+//    are.  So lane (g, t) multiplies, for key g, the dims of two 16-byte units of that
+//    key's codes, and for values four tokens' 16 dims: wide loads from the chunk as it
+//    lies in the cache, nothing transposed.  Each warp copies (cp.async) whole tokens
+//    into a ring of its own, so no barrier stands between copy and use; P^T comes from
+//    S^T by 8 x 8 transpositions in registers (movmatrix).
 //  * e4m3 to fp16 is exact (one conversion for two codes).  Queries are brought
 //    to fp16 by a power of two for each row, exact but below 2^-25 of the row's
 //    largest element.  The K scale multiplies the scores, the V scale of the
@@ -39,9 +39,6 @@
 namespace tl {
 namespace {
 
-constexpr int WARPS = 8;
-constexpr int THREADS = WARPS * 32;
-constexpr int STAGES = 3;
 constexpr int MAX_TILE = 16;  // query rows of one tile: 8 or 16
 constexpr int CHUNK = 32;     // tokens of one chunk; its halves of 16 lie in one page each
 constexpr float kShift = 7.0f;
@@ -60,9 +57,10 @@ struct DecodeParams {
   float scale_log2;
 };
 
-template <int D, int NR>
+template <int D, int NR, int WARPS>
 struct DecodeSmem {
   static constexpr int TILE = 8 * NR;
+  static constexpr int STAGES = 24 / WARPS;    // 192 KB for head_dim 128
   static constexpr int STAGE = CHUNK * D * 2;  // bytes of one chunk, keys and values
   static constexpr int PITCH = D / 4 + 1;      // 16-byte units of one row of the merge buffers
   uint8_t ring[WARPS][STAGES][STAGE];
@@ -121,28 +119,17 @@ __device__ __forceinline__ bool seg_next(const DecodeParams& p, Segment& g) {
   return true;
 }
 
-// 16 or 8 bytes, zeros when not ok
+// 16 bytes, zeros when not ok
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 r;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
-  return r;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 r;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
-  return r;
-}
+__device__ __forceinline__ uint4 lds128(const uint8_t* a) { return *reinterpret_cast<const uint4*>(a); }
+__device__ __forceinline__ uint2 lds64(const uint8_t* a) { return *reinterpret_cast<const uint2*>(a); }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -170,19 +157,32 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+// Where 16-byte unit `unit` of a chunk's token `row` lies, so that neither the copies (whole tokens by
+// neighbouring lanes) nor a product's loads (keys: unit t or 4 + t of tokens g; values: unit g, or half of
+// unit g / 2, of tokens 2t) meet in a bank.
+template <int D>
+__device__ __forceinline__ int k_at(int row, int unit) {
+  return D == 128 ? row * 128 + ((unit ^ ((row & 1) << 2)) << 4) : row * 64 + (unit << 4);
+}
+template <int D>
+__device__ __forceinline__ int v_at(int row, int unit) {
+  return D == 128 ? row * 128 + ((unit ^ (row & 7)) << 4)
+                  : (row >> 1) * 128 + (((((row & 1) << 2) | unit) ^ (((row >> 1) & 3) << 1)) << 4);
+}
 // Which bytes are e4m3 NaN (0x7f, 0xff): 0x80 there.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
 // 16-byte unit c of row r in a merge buffer (the exclusive-or spreads a column's lanes over the banks)
-template <int D, int NR>
+template <int D>
 __device__ __forceinline__ int merge_at(int r, int c) {
-  return r * DecodeSmem<D, NR>::PITCH + (c ^ ((c >> 3) & 3));
+  return r * (D / 4 + 1) + (c ^ ((c >> 3) & 3));
 }
 
 // NR: products of 8 query rows to a tile
-template <int D, int NR>
-__global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_constant__ DecodeParams p) {
-  using Smem = DecodeSmem<D, NR>;
+template <int D, int NR, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_constant__ DecodeParams p) {
+  using Smem = DecodeSmem<D, NR, WARPS>;
+  constexpr int THREADS = WARPS * 32, STAGES = Smem::STAGES;
   constexpr int TILE = 8 * NR;
   constexpr int KL = D / 64;   // 16-byte key loads of one lane and key
   constexpr int MTS = D / 16;  // m tiles of the output
@@ -242,8 +242,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
   // ---------------------------------------------------------------- the copies of one warp
   const uint32_t ring = smem_u32(sm.ring[warp]);
   const int page_halves = p.c.ps / 16;
-  const int64_t k_lane = int64_t(g) * p.c.token_stride + t * 16, v_lane = int64_t(2 * t) * p.c.token_stride + g * VB;
-  const int64_t eight = 8 * p.c.token_stride;
+  constexpr int UNITS = D / 16, RPC = 32 / UNITS;  // 16-byte units of a token, tokens of one copy instruction
+  const int64_t lane_off = int64_t(lane / UNITS) * p.c.token_stride + lane % UNITS * 16;
+  const int64_t rows_off = RPC * p.c.token_stride;
   bool f_ok = true, f_new = true;
   int fc = f.cb + warp, f_at = 0;
   int64_t offs[2] = {-1, -1};  // of the lane's chunk: where its halves begin in the pool, below 0: nowhere
@@ -282,28 +283,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
         }
         __syncwarp();
       }
-      const uint32_t dst = ring + uint32_t(stage * Smem::STAGE) + uint32_t(lane * 16);
-      const uint32_t vdst = ring + uint32_t(stage * Smem::STAGE + CHUNK * D) + uint32_t(lane * VB);
+      const uint32_t dst = ring + uint32_t(stage * Smem::STAGE);
       uint32_t good = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int64_t off = __shfl_sync(0xffffffffu, offs[h], f_at);
         const bool ok = off >= 0;
         good |= ok ? 1u << h : 0u;
-        const uint8_t* ksrc = p.c.k + (ok ? off + k_lane : 0);
-        const uint8_t* vsrc = p.c.v + (ok ? off + v_lane : 0);
-        const int64_t step8 = ok ? eight : 0, step1 = ok ? p.c.token_stride : 0;
+        const uint8_t* ksrc = p.c.k + (ok ? off + lane_off : 0);
+        const uint8_t* vsrc = p.c.v + (ok ? off + lane_off : 0);
+        const int64_t step = ok ? rows_off : 0;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int j = 0; j < KL; ++j)
-            cp_async16(dst + uint32_t(((h * 2 + r) * KL + j) * 512), ksrc + r * step8 + (ok ? j * 64 : 0), ok);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint8_t* src = vsrc + (j >> 1) * step8 + (j & 1) * step1;
-          const uint32_t to = vdst + uint32_t((h * 4 + j) * 32 * VB);
-          if (VB == 16) cp_async16(to, src, ok);
-          else cp_async8(to, src, ok);
+        for (int i = 0; i < 16 / RPC; ++i) {
+          const int row = h * 16 + i * RPC + lane / UNITS;
+          cp_async16(dst + k_at<D>(row, lane % UNITS), ksrc + i * step, ok);
+          cp_async16(dst + CHUNK * D + v_at<D>(row, lane % UNITS), vsrc + i * step, ok);
         }
       }
       const uint32_t sc = __shfl_sync(0xffffffffu, scales, f_at);
@@ -391,8 +385,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
     for (int ch = c.cb + warp; ch < c.ce; ch += WARPS) {
       cp_async_wait<STAGES - 2>();
       __syncwarp();
+      fetch(stage == 0 ? STAGES - 1 : stage - 1);  // over the chunk before this one
       const uint2 meta = sm.meta[warp][stage];
-      const uint32_t src = ring + uint32_t(stage * Smem::STAGE);
+      const uint8_t* src = sm.ring[warp][stage];
       const int tok = ch * CHUNK;
       const bool edge = tok + CHUNK > min_lim || meta.y != 3u;
       float s[2][NR][4];
@@ -406,8 +401,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
           for (int x = 0; x < NR; ++x)
 #pragma unroll
             for (int k = 0; k < 4; ++k) part[j][x][k] = 0.0f;
-          const uint4 a = lds128(src + uint32_t(((h * 2) * KL + j) * 512 + lane * 16));
-          const uint4 d = lds128(src + uint32_t(((h * 2 + 1) * KL + j) * 512 + lane * 16));
+          const uint4 a = lds128(src + k_at<D>(h * 16 + g, j * 4 + t));
+          const uint4 d = lds128(src + k_at<D>(h * 16 + 8 + g, j * 4 + t));
           const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -484,17 +479,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t vw[4][VB / 4];
-        const uint32_t vsrc = src + uint32_t(CHUNK * D + h * 4 * 32 * VB + lane * VB);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (VB == 16) {
-            const uint4 w = lds128(vsrc + uint32_t(j * 32 * VB));
+            const uint4 w = lds128(src + CHUNK * D + v_at<D>(h * 16 + 2 * t + (j & 1) + (j >> 1) * 8, g));
             vw[j][0] = w.x;
             vw[j][1] = w.y;
             vw[j][VB / 4 - 2] = w.z;
             vw[j][VB / 4 - 1] = w.w;
           } else {
-            const uint2 w = lds64(vsrc + uint32_t(j * 32 * VB));
+            const uint2 w = lds64(src + CHUNK * D + v_at<D>(h * 16 + 2 * t + (j & 1) + (j >> 1) * 8, g >> 1) + (g & 1) * 8);
             vw[j][0] = w.x;
             vw[j][1] = w.y;
           }
@@ -560,8 +554,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
           }
         }
       }
-      __syncwarp();
-      fetch(stage == 0 ? STAGES - 1 : stage - 1);
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
 
@@ -607,7 +599,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
           for (int u = 0; u < VB / 4; ++u) {
             constexpr int HALF = VB / 8;  // units of dims i, then of dims VB/2 + i
             const int q = u / HALF * 2 + y, i = (u % HALF) * 4;
-            fn(merge_at<D, NR>(8 * x + 2 * t + y, g * (VB / 4) + u), o[x][i][q], o[x][i + 1][q], o[x][i + 2][q],
+            fn(merge_at<D>(8 * x + 2 * t + y, g * (VB / 4) + u), o[x][i][q], o[x][i + 1][q], o[x][i + 2][q],
                o[x][i + 3][q]);
           }
     };
@@ -636,12 +628,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
       const float inv = L == 0.0f ? 0.0f : 1.0f / L, pe = pow2f(em);
 #pragma unroll
       for (int u = 0; u < EPT / 4; ++u) {
-        const int a = merge_at<D, NR>(row, d0 / 4 + u);
-        const float4 w0 = sm.merge[0][a], w1 = sm.merge[1][a], w2 = sm.merge[2][a], w3 = sm.merge[3][a];
-        acc[4 * u] = ((w0.x + w1.x) + (w2.x + w3.x)) * inv * pe;
-        acc[4 * u + 1] = ((w0.y + w1.y) + (w2.y + w3.y)) * inv * pe;
-        acc[4 * u + 2] = ((w0.z + w1.z) + (w2.z + w3.z)) * inv * pe;
-        acc[4 * u + 3] = ((w0.w + w1.w) + (w2.w + w3.w)) * inv * pe;
+        const int a = merge_at<D>(row, d0 / 4 + u);
+        float4 w0 = sm.merge[0][a];
+#pragma unroll
+        for (int k = 1; k < WARPS / 2; ++k) {
+          const float4 wk = sm.merge[k][a];
+          w0.x += wk.x;
+          w0.y += wk.y;
+          w0.z += wk.z;
+          w0.w += wk.w;
+        }
+        acc[4 * u] = w0.x * inv * pe;
+        acc[4 * u + 1] = w0.y * inv * pe;
+        acc[4 * u + 2] = w0.z * inv * pe;
+        acc[4 * u + 3] = w0.w * inv * pe;
       }
     }
 
@@ -715,6 +715,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_decode_kernel(const __grid_cons
   cp_async_wait<0>();
 }
 
+template <int D, int NR, int WARPS>
+tl_status launch_decode(void** args, int ctas, cudaStream_t st) {
+  using Smem = DecodeSmem<D, NR, WARPS>;
+  static_assert(sizeof(Smem) <= 232448, "shared memory above the per-CTA limit");
+  return launch(reinterpret_cast<const void*>(&kv_decode_kernel<D, NR, WARPS>), ctas, WARPS * 32, sizeof(Smem), st, args,
+                false);
+}
+
 // ---------------------------------------------------------------- workspace: counters, then partial tiles
 size_t counters_bytes(int ctas) { return (size_t(ctas) * 4 + 255) / 256 * 256; }
 size_t decode_partial_bytes(int ctas, int D) { return size_t(ctas) * 2 * (MAX_TILE * D + 2 * MAX_TILE) * sizeof(float); }
@@ -782,17 +790,8 @@ extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
   // Tiles of 8 query rows where a sequence's rows of one kv head fit in one, of 16 otherwise
   const int per_seq = a->max_q_len ? std::min(a->max_q_len, a->n_tokens) : cdiv(a->n_tokens, a->B);
   const bool small = int64_t(per_seq) * p.group <= 8;
-  const void* kernel;
-  size_t smem;
-  if (c.head_dim == 128) {
-    kernel = small ? reinterpret_cast<const void*>(&kv_decode_kernel<128, 1>)
-                   : reinterpret_cast<const void*>(&kv_decode_kernel<128, 2>);
-    smem = small ? sizeof(DecodeSmem<128, 1>) : sizeof(DecodeSmem<128, 2>);
-  } else {
-    kernel = small ? reinterpret_cast<const void*>(&kv_decode_kernel<64, 1>)
-                   : reinterpret_cast<const void*>(&kv_decode_kernel<64, 2>);
-    smem = small ? sizeof(DecodeSmem<64, 1>) : sizeof(DecodeSmem<64, 2>);
-  }
   void* args[] = {&p};
-  return launch(kernel, di.sm_count, THREADS, smem, static_cast<cudaStream_t>(stream), args, false);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (c.head_dim == 128) return small ? launch_decode<128, 1, 12>(args, di.sm_count, st) : launch_decode<128, 2, 8>(args, di.sm_count, st);
+  return small ? launch_decode<64, 1, 12>(args, di.sm_count, st) : launch_decode<64, 2, 8>(args, di.sm_count, st);
 }
