@@ -62,12 +62,10 @@ struct DecodeSmem {
   static constexpr int TILE = 8 * NR;
   static constexpr int STAGES = 24 / WARPS;    // 192 KB for head_dim 128
   static constexpr int STAGE = CHUNK * D * 2;  // bytes of one chunk, keys and values
-  static constexpr int PITCH = D / 4 + 1;      // 16-byte units of one row of the merge buffers
-  uint8_t ring[WARPS][STAGES][STAGE];
-  float4 merge[WARPS / 2][TILE * PITCH];
-  float m[WARPS][TILE], l[WARPS][TILE];
+  uint8_t ring[WARPS][STAGES][STAGE];          // a tile's merge takes the stage that each warp used last
+  float2 ml[TILE][WARPS];                      // maximum and sum of each row and warp
   uint2 meta[WARPS][STAGES];  // scale bytes (k, v of the first half, k, v of the second); which halves' pages are good
-  int32_t e[WARPS];
+  int32_t e[WARPS], spare[WARPS];
   int64_t warp_sum[WARPS];
   int64_t begin_off;
   int32_t begin_seq, last;
@@ -80,9 +78,13 @@ struct Segment {
   int64_t left;                       // chunks of the run from cb on
 };
 
+// a / b, in 32 bits where that is enough (a 64-bit division takes about 500 cycles)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) ? a / b : int64_t(uint32_t(a) / uint32_t(b));
+}
 template <int TILE>
 __device__ __forceinline__ int seq_tiles(const DecodeParams& p, const KvSeq& q) {
-  return int((int64_t(q.q) * p.group + TILE - 1) / TILE);
+  return int((uint32_t(q.q) * uint32_t(p.group) + TILE - 1) / TILE);  // rows fit in 31 bits (checked by the host)
 }
 __device__ __forceinline__ int seq_chunks(const KvSeq& q) { return max(1, (q.len + CHUNK - 1) / CHUNK); }
 
@@ -92,7 +94,7 @@ __device__ __forceinline__ void seg_open(const DecodeParams& p, Segment& g, int 
   g.s = s;
   g.nch = seq_chunks(g.seq);
   g.tiles = seq_tiles<TILE>(p, g.seq);
-  const int sub = int(off / g.nch);
+  const int sub = int(quotient(off, g.nch));
   g.hk = sub / max(g.tiles, 1);
   g.rt = sub - g.hk * g.tiles;
   g.cb = int(off - int64_t(sub) * g.nch);
@@ -175,7 +177,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7
 // 16-byte unit c of row r in a merge buffer (the exclusive-or spreads a column's lanes over the banks)
 template <int D>
 __device__ __forceinline__ int merge_at(int r, int c) {
-  return r * (D / 4 + 1) + (c ^ ((c >> 3) & 3));
+  return r * (D / 4) + (c ^ ((c >> 3) & 3) ^ ((r >> 1) & 3));
 }
 
 // NR: products of 8 query rows to a tile
@@ -216,10 +218,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
   }
   before -= mine;
   // a CTA gets a chunk for each warp at least
-  const int64_t n = min(int64_t(gridDim.x), max(int64_t(1), total / WARPS));
+  const int64_t n = min(int64_t(gridDim.x), max(int64_t(1), quotient(total, WARPS)));
   const int64_t cta = blockIdx.x;
   if (cta >= n || total == 0) return;
-  const int64_t run0 = cta * total / n, run1 = (cta + 1) * total / n;
+  const int64_t run0 = quotient(cta * total, n), run1 = quotient((cta + 1) * total, n);
   if (run0 >= run1) return;
   if (mine > 0 && before <= run0 && run0 < before + mine) {
     int64_t at = before;
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
   bool f_ok = true, f_new = true;
   int fc = f.cb + warp, f_at = 0;
   int64_t offs[2] = {-1, -1};  // of the lane's chunk: where its halves begin in the pool, below 0: nowhere
-  uint32_t scales = 0;
+  uint32_t scale_bytes[2][2] = {{0, 0}, {0, 0}};
   auto settle = [&]() {  // on to a segment that has a chunk for this warp
     while (f_ok && fc >= f.ce) {
       f_ok = seg_next<TILE>(p, f);
@@ -263,7 +265,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
         f_new = false;
         f_at = 0;
         const int ch = fc + lane * WARPS;
-        scales = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int half = ch * 2 + h;
@@ -277,7 +278,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
               offs[h] = int64_t(page) * p.c.page_stride + int64_t(f.hk) * p.c.head_stride +
                         int64_t((half - no * page_halves) * 16) * p.c.token_stride;
               const int64_t i = int64_t(page) * p.c.Hkv + f.hk;
-              scales |= (uint32_t(p.c.ks[i]) | (uint32_t(p.c.vs[i]) << 8)) << (16 * h);
+              scale_bytes[h][0] = p.c.ks[i];  // looked at after the copies are on their way
+              scale_bytes[h][1] = p.c.vs[i];
             }
           }
         }
@@ -300,7 +302,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
           cp_async16(dst + CHUNK * D + v_at<D>(row, lane % UNITS), vsrc + i * step, ok);
         }
       }
-      const uint32_t sc = __shfl_sync(0xffffffffu, scales, f_at);
+      const uint32_t sc = __shfl_sync(0xffffffffu, scale_bytes[0][0] | scale_bytes[0][1] << 8 | scale_bytes[1][0] << 16 |
+                                                       scale_bytes[1][1] << 24, f_at);
       if (lane == 0) sm.meta[warp][stage] = make_uint2(sc, good);
       ++f_at;
       fc += WARPS;
@@ -308,6 +311,22 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     }
     cp_async_commit();
   };
+  uint4 qraw[NR][KL * 2];  // row g of each product's queries, on their way while pages are looked up
+  auto load_q = [&]() {
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      const int last = int(int64_t(c.seq.q) * p.group) - 1;
+      const int r = min(c.rt * TILE + 8 * x + g, last);
+      const int i = r / p.group;
+      const uint16_t* src = p.q + int64_t(c.seq.row0 + i) * p.q_ts + int64_t(c.hk * p.group + r - i * p.group) * p.q_hs;
+#pragma unroll
+      for (int j = 0; j < KL; ++j) {
+        qraw[x][2 * j] = *reinterpret_cast<const uint4*>(src + j * 64 + t * 16);
+        qraw[x][2 * j + 1] = *reinterpret_cast<const uint4*>(src + j * 64 + t * 16 + 8);
+      }
+    }
+  };
+  load_q();
   for (int i = 0; i < STAGES - 1; ++i) fetch(i);
 
   // ---------------------------------------------------------------- segment by segment
@@ -326,16 +345,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     int lim[NR][2];
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
-      const int r = r0 + min(8 * x + g, rows - 1);
-      const int i = r / p.group;
-      const uint16_t* src = p.q + int64_t(c.seq.row0 + i) * p.q_ts + int64_t(c.hk * p.group + r - i * p.group) * p.q_hs;
-      uint4 w[KL * 2];
+      const uint4(&w)[KL * 2] = qraw[x];
       float amax = 0.0f;
-#pragma unroll
-      for (int j = 0; j < KL; ++j) {
-        w[2 * j] = *reinterpret_cast<const uint4*>(src + j * 64 + t * 16);
-        w[2 * j + 1] = *reinterpret_cast<const uint4*>(src + j * 64 + t * 16 + 8);
-      }
 #pragma unroll
       for (int j = 0; j < KL * 2; ++j) {
         const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
@@ -557,40 +568,19 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
 
-    // ---------------------------------------------------------------- the eight warps' results become one
+    // ---------------------------------------------------------------- the warps' results become one
 #pragma unroll
     for (int x = 0; x < NR; ++x)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         l[x][y] = column_sum(l[x][y]);
-        if (g == 0) {
-          sm.m[warp][8 * x + 2 * t + y] = m[x][y];
-          sm.l[warp][8 * x + 2 * t + y] = l[x][y];
-        }
+        if (g == 0) sm.ml[8 * x + 2 * t + y][warp] = make_float2(m[x][y], l[x][y]);
       }
     if (lane == 0) sm.e[warp] = ve;
-    __syncthreads();
-    int em = -127;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) em = max(em, sm.e[w]);
-    const float vd = pow2f(max(ve - em, -127));
-#pragma unroll
-    for (int x = 0; x < NR; ++x)
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, sm.m[w][8 * x + 2 * t + y]);
-        // a warp that saw no key has m = -inf, l = 0 and o = 0 (l is NaN when its scores were)
-        const float a = m[x][y] == -INFINITY ? vd * (l[x][y] == 0.0f ? 1.0f : l[x][y]) : vd * ex2_approx(m[x][y] - top);
-#pragma unroll
-        for (int i = 0; i < MTS; ++i) {
-          o[x][i][y] *= a;
-          o[x][i][2 + y] *= a;
-        }
-      }
-    // a row's dims g * VB .. g * VB + VB - 1 as 16-byte units
-    auto each_unit = [&](auto&& fn) {
+    const int spare = stage == 0 ? STAGES - 1 : stage - 1;  // the stage that this warp's next copy will fill
+    {
+      float4* buf = reinterpret_cast<float4*>(sm.ring[warp][spare]);
+      // a row's dims g * VB .. g * VB + VB - 1 as 16-byte units
 #pragma unroll
       for (int x = 0; x < NR; ++x)
 #pragma unroll
@@ -599,18 +589,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
           for (int u = 0; u < VB / 4; ++u) {
             constexpr int HALF = VB / 8;  // units of dims i, then of dims VB/2 + i
             const int q = u / HALF * 2 + y, i = (u % HALF) * 4;
-            fn(merge_at<D>(8 * x + 2 * t + y, g * (VB / 4) + u), o[x][i][q], o[x][i + 1][q], o[x][i + 2][q],
-               o[x][i + 3][q]);
+            buf[merge_at<D>(8 * x + 2 * t + y, g * (VB / 4) + u)] =
+                make_float4(o[x][i][q], o[x][i + 1][q], o[x][i + 2][q], o[x][i + 3][q]);
           }
-    };
-    float4* buf = sm.merge[warp % (WARPS / 2)];
-    if (warp >= WARPS / 2) each_unit([&](int i, float v0, float v1, float v2, float v3) { buf[i] = make_float4(v0, v1, v2, v3); });
-    __syncthreads();
-    if (warp < WARPS / 2)
-      each_unit([&](int i, float v0, float v1, float v2, float v3) {
-        const float4 w = buf[i];
-        buf[i] = make_float4(w.x + v0, w.y + v1, w.z + v2, w.w + v3);
-      });
+    }
+    if (lane == 0) sm.spare[warp] = spare;
     __syncthreads();
     constexpr int EPT = TILE * D / THREADS < 4 ? 4 : TILE * D / THREADS;  // elements of one thread
     const int row = tid / (D / EPT), d0 = tid % (D / EPT) * EPT;
@@ -618,37 +601,40 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     float M1 = -INFINITY, L = 0.0f;
     float acc[EPT];
     if (mine_row) {
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) M1 = fmaxf(M1, sm.m[w][row]);
+      int em = -127;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
-        const float mw = sm.m[w][row];
-        L += mw == -INFINITY ? sm.l[w][row] : sm.l[w][row] * ex2_approx(mw - M1);
+        em = max(em, sm.e[w]);
+        M1 = fmaxf(M1, sm.ml[row][w].x);
+      }
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) acc[i] = 0.0f;
+#pragma unroll 4
+      for (int w = 0; w < WARPS; ++w) {
+        // a warp that saw no key has m = -inf, l = 0 and o = 0 (l is NaN when its scores were)
+        const float2 ml = sm.ml[row][w];
+        const float a = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : ml.y) : ex2_approx(ml.x - M1);
+        L = fmaf(a, ml.x == -INFINITY ? 1.0f : ml.y, L);
+        const float av = a * pow2f(max(sm.e[w] - em, -127));
+        const float4* buf = reinterpret_cast<const float4*>(sm.ring[w][sm.spare[w]]);
+#pragma unroll
+        for (int u = 0; u < EPT / 4; ++u) {
+          const float4 v = buf[merge_at<D>(row, d0 / 4 + u)];
+          acc[4 * u] = fmaf(av, v.x, acc[4 * u]);
+          acc[4 * u + 1] = fmaf(av, v.y, acc[4 * u + 1]);
+          acc[4 * u + 2] = fmaf(av, v.z, acc[4 * u + 2]);
+          acc[4 * u + 3] = fmaf(av, v.w, acc[4 * u + 3]);
+        }
       }
       const float inv = L == 0.0f ? 0.0f : 1.0f / L, pe = pow2f(em);
 #pragma unroll
-      for (int u = 0; u < EPT / 4; ++u) {
-        const int a = merge_at<D>(row, d0 / 4 + u);
-        float4 w0 = sm.merge[0][a];
-#pragma unroll
-        for (int k = 1; k < WARPS / 2; ++k) {
-          const float4 wk = sm.merge[k][a];
-          w0.x += wk.x;
-          w0.y += wk.y;
-          w0.z += wk.z;
-          w0.w += wk.w;
-        }
-        acc[4 * u] = w0.x * inv * pe;
-        acc[4 * u + 1] = w0.y * inv * pe;
-        acc[4 * u + 2] = w0.z * inv * pe;
-        acc[4 * u + 3] = w0.w * inv * pe;
-      }
+      for (int i = 0; i < EPT; ++i) acc[i] = acc[i] * inv * pe;
     }
 
     bool done = true;
     if (c.cb != 0 || c.ce != c.nch) {
       const int64_t t0 = at - c.cb;  // the tile's first chunk in the list
-      const int64_t c0 = ((t0 + 1) * n - 1) / total, c1 = ((t0 + c.nch) * n - 1) / total;
+      const int64_t c0 = quotient((t0 + 1) * n - 1, total), c1 = quotient((t0 + c.nch) * n - 1, total);
       constexpr int SLOT = TILE * D + 2 * TILE;
       float* slot = p.partial + (2 * cta + (c.cb == 0 ? 1 : 0)) * SLOT;
       if (mine_row) {
@@ -672,25 +658,42 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
       if (done && mine_row) {
         __threadfence();
         M1 = -INFINITY;
-#pragma unroll 4
-        for (int64_t x = c0; x <= c1; ++x)
-          M1 = fmaxf(M1, __ldcg(p.partial + (2 * x + (x == c0)) * SLOT + TILE * D + row));
         L = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPT; ++i) acc[i] = 0.0f;
-#pragma unroll 4
-        for (int64_t x = c0; x <= c1; ++x) {
-          const float* from = p.partial + (2 * x + (x == c0)) * SLOT;
-          const float mw = __ldcg(from + TILE * D + row), lw = __ldcg(from + TILE * D + TILE + row);
-          const float wgt = mw == -INFINITY ? lw : lw * ex2_approx(mw - M1);
-          L += wgt;
+        constexpr int BATCH = 8;  // slots on their way at once
+        for (int64_t x0 = c0; x0 <= c1; x0 += BATCH) {
+          float mw[BATCH], lw[BATCH];
+          float4 v[BATCH][EPT / 4];
 #pragma unroll
-          for (int u = 0; u < EPT / 4; ++u) {
-            const float4 w = ld_global_cg_v4f(from + row * D + d0 + 4 * u);
-            acc[4 * u] = fmaf(wgt, w.x, acc[4 * u]);
-            acc[4 * u + 1] = fmaf(wgt, w.y, acc[4 * u + 1]);
-            acc[4 * u + 2] = fmaf(wgt, w.z, acc[4 * u + 2]);
-            acc[4 * u + 3] = fmaf(wgt, w.w, acc[4 * u + 3]);
+          for (int k = 0; k < BATCH; ++k) {
+            const int64_t x = min(x0 + k, c1);
+            const float* from = p.partial + (2 * x + (x == c0)) * SLOT;
+            mw[k] = __ldcg(from + TILE * D + row);
+            lw[k] = __ldcg(from + TILE * D + TILE + row);
+#pragma unroll
+            for (int u = 0; u < EPT / 4; ++u) v[k][u] = ld_global_cg_v4f(from + row * D + d0 + 4 * u);
+          }
+          float top = M1;
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) top = fmaxf(top, mw[k]);
+          const float down = M1 == -INFINITY ? 1.0f : ex2_approx(M1 - top);
+          M1 = top;
+          L *= down;
+#pragma unroll
+          for (int i = 0; i < EPT; ++i) acc[i] *= down;
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            if (x0 + k > c1) break;
+            const float wgt = mw[k] == -INFINITY ? lw[k] : lw[k] * ex2_approx(mw[k] - M1);
+            L += wgt;
+#pragma unroll
+            for (int u = 0; u < EPT / 4; ++u) {
+              acc[4 * u] = fmaf(wgt, v[k][u].x, acc[4 * u]);
+              acc[4 * u + 1] = fmaf(wgt, v[k][u].y, acc[4 * u + 1]);
+              acc[4 * u + 2] = fmaf(wgt, v[k][u].z, acc[4 * u + 2]);
+              acc[4 * u + 3] = fmaf(wgt, v[k][u].w, acc[4 * u + 3]);
+            }
           }
         }
         const float i2 = L == 0.0f ? 0.0f : 1.0f / L;
@@ -710,6 +713,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     }
     at += c.ce - c.cb;
     if (!seg_next<TILE>(p, c)) break;
+    load_q();
     __syncthreads();  // the merge buffers are free again
   }
   cp_async_wait<0>();
