@@ -618,8 +618,8 @@ tl_status tl_ag_attn(const tl_ag_attn_args* args, void* stream);
  * are read on the device.  What is wrong in them (decreasing or out-of-range
  * cu_seqlens, a length below the new tokens or above max_pages * page_size, a
  * page outside the pool) records TL_ERR_INVALID with the sequence number in the
- * signals' status word; the tokens or keys concerned are left out, and nothing
- * outside the caller's buffers is touched.
+ * signals' status word; what that sequence gets is then undefined, the other
+ * sequences come out right, and nothing outside the caller's buffers is touched.
  */
 typedef struct tl_kv_cache {
   void* k;                     /* device e4m3 codes; element (page, head, slot, d) at byte

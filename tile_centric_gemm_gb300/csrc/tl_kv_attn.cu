@@ -35,12 +35,14 @@
 
 #include "tl_internal.h"
 #include "tl_kv.cuh"
+#include "tl_kv_prefill.h"
 
 namespace tl {
 namespace {
 
 constexpr int MAX_TILE = 16;  // query rows of one tile: 8 or 16
 constexpr int CHUNK = 32;     // tokens of one chunk; its halves of 16 lie in one page each
+constexpr int FEW_ROWS = 64;  // query rows per kv head up to which this kernel serves a sequence
 constexpr float kShift = 7.0f;
 constexpr float kSlack = 8.0f;
 
@@ -54,6 +56,7 @@ struct DecodeParams {
   uint32_t* counters;  // [CTAs], zero between calls
   float* partial;      // [CTAs][2][TILE * D + 2 * TILE]
   int32_t H, group, causal;
+  int32_t max_rows;    // sequences of more query rows per kv head are left to the kernel for many
   float scale_log2;
 };
 
@@ -84,7 +87,8 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 }
 template <int TILE>
 __device__ __forceinline__ int seq_tiles(const DecodeParams& p, const KvSeq& q) {
-  return int((uint32_t(q.q) * uint32_t(p.group) + TILE - 1) / TILE);  // rows fit in 31 bits (checked by the host)
+  const uint32_t rows = uint32_t(q.q) * uint32_t(p.group);  // in 31 bits (checked by the host)
+  return rows > uint32_t(p.max_rows) ? 0 : int((rows + TILE - 1) / TILE);
 }
 __device__ __forceinline__ int seq_chunks(const KvSeq& q) { return max(1, (q.len + CHUNK - 1) / CHUNK); }
 
@@ -115,7 +119,7 @@ __device__ __forceinline__ bool seg_next(const DecodeParams& p, Segment& g) {
     return true;
   }
   int s = g.s + 1;
-  while (s < p.b.B && kv_seq(p.b, p.c.ps, s).q == 0) ++s;
+  while (s < p.b.B && seq_tiles<TILE>(p, kv_seq(p.b, p.c.ps, s)) == 0) ++s;
   if (s >= p.b.B) return false;
   seg_open<TILE>(p, g, s, 0, g.left);
   return true;
@@ -220,9 +224,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
   // a CTA gets a chunk for each warp at least
   const int64_t n = min(int64_t(gridDim.x), max(int64_t(1), quotient(total, WARPS)));
   const int64_t cta = blockIdx.x;
-  if (cta >= n || total == 0) return;
+  if (cta >= n || total == 0) {
+    pdl_wait_previous();
+    return;
+  }
   const int64_t run0 = quotient(cta * total, n), run1 = quotient((cta + 1) * total, n);
-  if (run0 >= run1) return;
+  if (run0 >= run1) {
+    pdl_wait_previous();
+    return;
+  }
   if (mine > 0 && before <= run0 && run0 < before + mine) {
     int64_t at = before;
     for (int s = first; s < end; ++s) {
@@ -473,7 +483,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
       uint32_t pb[2][NR][2];  // P^T: tokens (2t, 2t+1) and (2t+8, 2t+9) of the half, row g
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float vf = vb[h] == 255 ? pow2f(128) : pow2f(max(vb[h] - 127 - ve, -127));
+        const float vf = vb[h] == 255 ? 1.0f : pow2f(max(vb[h] - 127 - ve, -127));  // 255: its codes count as NaN
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
 #pragma unroll
@@ -503,6 +513,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
             vw[j][0] = w.x;
             vw[j][1] = w.y;
           }
+        }
+        if (vb[h] == 255) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < VB / 4; ++k) vw[j][k] = 0x7F7F7F7Fu;
         }
         if (edge) {
           // slots past the sequence's end hold anything: zero.  A NaN value that some rows see and
@@ -717,14 +733,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     __syncthreads();  // the merge buffers are free again
   }
   cp_async_wait<0>();
+  pdl_wait_previous();  // the call ends when the kernel for many rows has ended too
 }
 
 template <int D, int NR, int WARPS>
-tl_status launch_decode(void** args, int ctas, cudaStream_t st) {
+tl_status launch_decode(void** args, int ctas, cudaStream_t st, bool early) {
   using Smem = DecodeSmem<D, NR, WARPS>;
   static_assert(sizeof(Smem) <= 232448, "shared memory above the per-CTA limit");
   return launch(reinterpret_cast<const void*>(&kv_decode_kernel<D, NR, WARPS>), ctas, WARPS * 32, sizeof(Smem), st, args,
-                false);
+                early);
 }
 
 // ---------------------------------------------------------------- workspace: counters, then partial tiles
@@ -743,7 +760,9 @@ extern "C" size_t tl_kv_attn_workspace_size(int n_tokens, int B, int H, int H_kv
     if (device_info(&di) != TL_OK) return 0;
     sm_count = di.sm_count;
   }
-  return counters_bytes(sm_count) + decode_partial_bytes(sm_count, head_dim);
+  size_t bytes = counters_bytes(sm_count) + decode_partial_bytes(sm_count, head_dim);
+  if (int64_t(n_tokens) * (H / H_kv) > FEW_ROWS) bytes += prefill_counter_bytes(sm_count) + prefill_partial_bytes(sm_count, head_dim);
+  return bytes;
 }
 
 extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
@@ -791,11 +810,38 @@ extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
   p.group = a->H / c.H_kv;
   p.causal = a->causal;
   p.scale_log2 = (a->scale > 0.0f ? a->scale : 1.0f / std::sqrt(float(c.head_dim))) * 1.4426950408889634f;
-  // Tiles of 8 query rows where a sequence's rows of one kv head fit in one, of 16 otherwise
-  const int per_seq = a->max_q_len ? std::min(a->max_q_len, a->n_tokens) : cdiv(a->n_tokens, a->B);
-  const bool small = int64_t(per_seq) * p.group <= 8;
-  void* args[] = {&p};
+  // Most new tokens that a sequence can have, as far as the host knows
+  const int most = a->max_q_len ? std::min(a->max_q_len, a->n_tokens) : std::max(1, a->n_tokens - a->B + 1);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (c.head_dim == 128) return small ? launch_decode<128, 1, 12>(args, di.sm_count, st) : launch_decode<128, 2, 8>(args, di.sm_count, st);
-  return small ? launch_decode<64, 1, 12>(args, di.sm_count, st) : launch_decode<64, 2, 8>(args, di.sm_count, st);
+  const bool many = int64_t(most) * p.group > FEW_ROWS;
+  p.max_rows = 0x7FFFFFFF;
+  if (many) {
+    // A sequence of many rows goes to the tensor-core kernel, one of few to this file's; where there is one
+    // sequence only, the first takes it whatever it is.
+    PrefillParams f{};
+    f.c = p.c;
+    f.b = p.b;
+    f.q = p.q;
+    f.q_ts = p.q_ts;
+    f.q_hs = p.q_hs;
+    f.out = p.out;
+    f.lse = p.lse;
+    uint8_t* at = static_cast<uint8_t*>(a->workspace) + counters_bytes(di.sm_count) + decode_partial_bytes(di.sm_count, c.head_dim);
+    f.counters = reinterpret_cast<uint32_t*>(at);
+    f.partial = reinterpret_cast<float*>(at + prefill_counter_bytes(di.sm_count));
+    f.timeout_ns = 3 * kDefaultTimeoutNs;
+    f.H = a->H;
+    f.group = p.group;
+    f.causal = a->causal;
+    f.min_rows = a->B == 1 ? 0 : FEW_ROWS;
+    f.scale_log2 = p.scale_log2;
+    if (tl_status s = launch_kv_prefill(f, c.head_dim, di.sm_count, st)) return s;
+    if (a->B == 1) return TL_OK;
+    p.max_rows = FEW_ROWS;
+  }
+  // Tiles of 8 query rows where a sequence's rows of one kv head fit in one, of 16 otherwise
+  const bool small = int64_t(most) * p.group <= 8;
+  void* args[] = {&p};
+  if (c.head_dim == 128) return small ? launch_decode<128, 1, 12>(args, di.sm_count, st, many) : launch_decode<128, 2, 8>(args, di.sm_count, st, many);
+  return small ? launch_decode<64, 1, 12>(args, di.sm_count, st, many) : launch_decode<64, 2, 8>(args, di.sm_count, st, many);
 }

@@ -1,0 +1,796 @@
+// tl_kv_prefill.cu -- attention of many new tokens of a sequence (a prompt's chunk)
+// over the 8-bit paged cache, on tcgen05.
+//
+//   s_j = scale <q, k_j>,  O = sum_j exp(s_j - lse) v_j,  causal within the chunk
+//
+// Bound by the tensor cores and the exponentials that feed them.  A unit is one kv
+// head and 256 of a sequence's query rows, rows being (token, head of the group), so
+// that all heads of a group share every key/value tile; two 128-row tiles A and B
+// take turns, one in the softmax while the tensor cores work for the other.
+//   warps 0-3    convert: queries bf16 -> fp16 (each row by a power of two), then
+//                each 128-token tile of codes -> fp16, K and V, into shared memory in
+//                the 128-byte-swizzled layout that the products read.  A tile's loads
+//                are in registers a tile ahead.
+//   warp 4       issues the products: S_X = Q_X K^T and O_X += P_X V (M = 128), P from
+//                tensor memory, in the order QK_A(0) QK_B(0) | PV_A(j) QK_A(j+1)
+//                PV_B(j) QK_B(j+1) | ...
+//   warps 8-11   softmax of tile A, warps 12-15 of tile B, a row to a thread.
+// Everything is fp16 with powers of two taken out: codes are exact in fp16, and the
+// block scales enter relative to the largest of the unit's keys (values), a factor of
+// at most 1 that costs nothing above 2^-25 of it; P runs up to 2^15, with a grain of
+// 2^-31 of the largest (P <= 2^8 times 2^7 between rescales of O).
+//
+// The work is the list of (unit, key/value tile), cut into equal runs, one to a CTA,
+// as in the kernel for few rows: short lists fill the SMs by splitting units, long
+// ones have no last wave.  Partial results are joined in CTA order by the CTA that
+// arrives last.
+//
+// A NaN value that only some rows of a unit see is taken out of V, and the least such
+// token of each dim is kept: rows see prefixes, so a row's result in that dim is NaN
+// exactly if the row sees that token.
+//
+// TMEM (lane = query row of the tile): S_A columns 0-127 (P_A in 0-63), S_B 128-255,
+// O_A from 256, O_B from 384.
+#include <algorithm>
+#include <cmath>
+
+#include "tl_common.cuh"
+#include "tl_internal.h"
+#include "tl_kv.cuh"
+#include "tl_kv_prefill.h"
+
+namespace tl {
+namespace {
+
+constexpr int THREADS = 512;
+constexpr int KV = 128;          // tokens of a tile
+constexpr int ROWS = 128;        // query rows of a tile
+constexpr int UNIT = 2 * ROWS;
+constexpr int KST = 2, VST = 3;  // ring stages
+constexpr int MIN_TILES = 4;     // of a CTA's run
+constexpr float kShift = 7.0f, kSlack = 8.0f;
+constexpr uint32_t BOX = 128 * 64 * 2;  // 128 rows of 64 fp16, one swizzle span wide
+
+struct __align__(8) Bars {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint32_t tmem_base, abort;
+};
+
+template <int D>
+struct Layout {
+  static constexpr uint32_t TILE = BOX * (D / 64);  // a tile of queries, keys or values
+  static constexpr uint32_t Q = 0, K = Q + 2 * TILE, V = K + KST * TILE, BARS = V + VST * TILE;
+};
+
+struct Side {
+  Bars bars;
+  int8_t q_exp[2][UNIT];   // rows' exponents, by segment parity
+  int32_t kv_exp[4][2];    // exponents of the segment's keys and values
+  int32_t nan_at[4][128];  // least token whose value is NaN in the dim, among those not all rows see
+  int32_t warp_max[4][2];
+  int64_t warp_sum[16];
+  int64_t begin_left;
+  int32_t begin[4];        // sequence, kv head, row block, tile
+  int32_t last[2];
+};
+
+template <int D>
+constexpr uint32_t smem_bytes() {
+  return Layout<D>::BARS + uint32_t(sizeof(Side));
+}
+static_assert(smem_bytes<128>() <= 232448, "shared memory above the per-CTA limit");
+
+constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// ---------------------------------------------------------------- the list of work
+struct Seg {
+  KvSeq seq;
+  int s, hk, qb, nkv, t0, t1;  // tiles t0 .. t1-1 of the unit's nkv
+  int64_t left;
+};
+__device__ __forceinline__ int seq_rows(const PrefillParams& p, const KvSeq& q) {
+  const int rows = q.q * p.group;
+  return rows > p.min_rows ? rows : 0;
+}
+__device__ __forceinline__ int row_limit(const PrefillParams& p, const KvSeq& q, int row) {
+  return p.causal ? max(0, min(q.len, q.len - q.q + row / p.group + 1)) : q.len;
+}
+__device__ __forceinline__ int unit_tiles(const PrefillParams& p, const KvSeq& q, int rows, int qb) {
+  const int lim = row_limit(p, q, min(rows, (qb + 1) * UNIT) - 1);
+  return max(1, (lim + KV - 1) / KV);
+}
+__device__ __forceinline__ int64_t seq_tiles(const PrefillParams& p, const KvSeq& q) {  // of one kv head
+  const int rows = seq_rows(p, q), blocks = (rows + UNIT - 1) / UNIT;
+  if (!p.causal) return rows ? int64_t(blocks) * unit_tiles(p, q, rows, 0) : 0;
+  int64_t n = 0;
+  for (int b = 0; b < blocks; ++b) n += unit_tiles(p, q, rows, b);
+  return n;
+}
+__device__ __forceinline__ bool seg_next(const PrefillParams& p, Seg& g) {
+  g.left -= g.t1 - g.t0;
+  if (g.left <= 0) return false;
+  const int rows = seq_rows(p, g.seq);
+  if (++g.qb * UNIT >= rows) {
+    g.qb = 0;
+    if (++g.hk == p.c.Hkv) {
+      g.hk = 0;
+      do {
+        if (++g.s >= p.b.B) return false;
+        g.seq = kv_seq(p.b, p.c.ps, g.s);
+      } while (seq_rows(p, g.seq) == 0);
+    }
+  }
+  g.nkv = unit_tiles(p, g.seq, seq_rows(p, g.seq), g.qb);
+  g.t0 = 0;
+  g.t1 = int(min(int64_t(g.nkv), g.left));
+  return true;
+}
+
+// ---------------------------------------------------------------- products
+__device__ __forceinline__ void mma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t smem, int X, int ks, uint32_t d_tmem) {
+  using L = Layout<D>;
+  const uint32_t q0 = smem + L::Q + X * L::TILE, k0 = smem + L::K + ks * L::TILE;
+#pragma unroll
+  for (int kk = 0; kk < D / UMMA_K; ++kk) {
+    const uint64_t ad = sdesc_sw128(q0 + (kk >> 2) * BOX + (kk & 3) * 32, 16, 1024);
+    const uint64_t bd = sdesc_sw128(k0 + (kk >> 2) * BOX + (kk & 3) * 32, 16, 1024);
+    tc_mma_bf16(d_tmem, ad, bd, idesc_f16_f32(ROWS, KV, false), kk > 0 ? 1u : 0u);
+  }
+}
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t smem, uint32_t p_tmem, int vs, uint32_t d_tmem, bool accumulate) {
+  const uint32_t v0 = smem + Layout<D>::V + vs * Layout<D>::TILE;
+#pragma unroll
+  for (int kk = 0; kk < KV / UMMA_K; ++kk)
+    mma_tmem_a(d_tmem, p_tmem + uint32_t(kk * 8), sdesc_sw128(v0 + kk * 2048, BOX, 1024), idesc_f16_f32(ROWS, D, true),
+               (accumulate || kk > 0) ? 1u : 0u);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// Factor of a block with this scale byte relative to 2^top, as two halves.
+__device__ __forceinline__ uint32_t block_factor(int byte, int top) {
+  const float f = byte == 255 ? pow2f(128) : pow2f(max(byte - 127 - top, -127));
+  return pack_f16x2(f, f);
+}
+
+// Sixteen codes (dims 16u .. 16u+15 of row r) times f into a swizzled tile.
+__device__ __forceinline__ void put16(uint32_t tile, int r, int u, uint4 w, uint32_t f) {
+  const uint32_t c[4] = {w.x, w.y, w.z, w.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[2 * i] = mul_f16x2(e4m3x2_to_f16x2(c[i]), f);
+    h[2 * i + 1] = mul_f16x2(e4m3x2_to_f16x2_hi(c[i]), f);
+  }
+  const uint32_t row = tile + uint32_t((u >> 2) * BOX + r * 128), at = uint32_t((u & 3) * 2);
+  st_shared_v4(row + ((at ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+  st_shared_v4(row + (((at + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+}
+
+template <int NREG>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(NREG));
+}
+template <int NREG>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(NREG));
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_constant__ PrefillParams p) {
+  using L = Layout<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t smem = smem_u32(smem_raw);
+  Side& sd = *reinterpret_cast<Side*>(smem_raw + L::BARS);
+  Bars* bars = &sd.bars;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile uint32_t* abort = &bars->abort;
+  const KvBatch& b = p.b;
+  const uint64_t tmo = p.timeout_ns;
+  pdl_launch_dependents();
+  if (smem & 1023u) {  // the swizzle counts on it
+    if (tid == 0) record_error(b.status, 5u, 0xFFFF0001u, smem, 0u);
+    return;
+  }
+
+  // ---------------------------------------------------------------- this CTA's run of tiles
+  const int per = (b.B + THREADS - 1) / THREADS;
+  const int first = min(b.B, tid * per), end = min(b.B, first + per);
+  int64_t mine = 0;
+  for (int s = first; s < end; ++s) mine += p.c.Hkv * seq_tiles(p, kv_seq(b, p.c.ps, s));
+  int64_t before = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane >= d) before += x;
+  }
+  if (lane == 31) sd.warp_sum[warp] = before;
+  if (tid == 0) {
+    mbar_init(&bars->q_full, 4);
+    mbar_init(&bars->q_empty, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars->s_full[x], 1);
+      mbar_init(&bars->p_full[x], 4);
+      mbar_init(&bars->o_full[x], 1);
+      mbar_init(&bars->o_empty[x], 4);
+    }
+    for (int i = 0; i < KST; ++i) {
+      mbar_init(&bars->k_full[i], 4);
+      mbar_init(&bars->k_empty[i], 1);
+    }
+    for (int i = 0; i < VST; ++i) {
+      mbar_init(&bars->v_full[i], 4);
+      mbar_init(&bars->v_empty[i], 1);
+    }
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w == warp) before += total;
+    total += sd.warp_sum[w];
+  }
+  before -= mine;
+  const int64_t n = min(int64_t(gridDim.x), max(int64_t(1), total / MIN_TILES));
+  const int64_t cta = blockIdx.x;
+  const int64_t run0 = cta < n ? cta * total / n : 0, run1 = cta < n ? (cta + 1) * total / n : 0;
+  if (run0 >= run1) return;
+  if (mine > 0 && before <= run0 && run0 < before + mine) {
+    int64_t at = before;
+    for (int s = first; s < end; ++s) {
+      const KvSeq q = kv_seq(b, p.c.ps, s);
+      const int64_t one = seq_tiles(p, q), size = one * p.c.Hkv;
+      if (run0 < at + size) {
+        int64_t off = run0 - at;
+        const int hk = int(off / one);
+        off -= hk * one;
+        int qb = 0;
+        const int rows = seq_rows(p, q);
+        for (int t; (t = unit_tiles(p, q, rows, qb)) <= off; ++qb) off -= t;
+        sd.begin[0] = s;
+        sd.begin[1] = hk;
+        sd.begin[2] = qb;
+        sd.begin[3] = int(off);
+        break;
+      }
+      at += size;
+    }
+  }
+  if (warp == 4) {
+    tmem_alloc(&bars->tmem_base, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = bars->tmem_base;
+  Seg g;
+  g.s = sd.begin[0];
+  g.hk = sd.begin[1];
+  g.qb = sd.begin[2];
+  g.t0 = sd.begin[3];
+  g.left = run1 - run0;
+  g.seq = kv_seq(b, p.c.ps, g.s);
+  g.nkv = unit_tiles(p, g.seq, seq_rows(p, g.seq), g.qb);
+  g.t1 = int(min(int64_t(g.nkv), g.t0 + g.left));
+
+  if (warp < 4) {
+    // ---------------------------------------------------------------- conversion
+    reg_dec<112>();
+    constexpr int UN = D / 16;       // 16-code units of a token
+    constexpr int PASS = D / 64;     // units of one thread and row
+    constexpr int GR = 4;            // rows of one thread and tile
+    const int r8 = lane >> 2, u4 = lane & 3;
+    int ks = 0, vs = 0;
+    uint32_t kph = 0, vph = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const int rows = seq_rows(p, g.seq);
+      const int len = g.seq.len;
+      const int min_lim = row_limit(p, g.seq, g.qb * UNIT);
+      // the largest scales of the segment's pages
+      const int tok_end = min(len, g.t1 * KV);
+      int km = -127, vm = -127;
+      for (int pg = g.t0 * KV / p.c.ps + tid; pg * int64_t(p.c.ps) < tok_end; pg += 128) {
+        const int page = __ldg(b.table + int64_t(g.s) * b.max_pages + pg);
+        if (page < 0 || page >= p.c.num_pages) {
+          record_error(b.status, kKvInvalid, uint32_t(g.s), uint32_t(page), uint32_t(pg));
+          continue;
+        }
+        const int kb = p.c.ks[int64_t(page) * p.c.Hkv + g.hk], vb = p.c.vs[int64_t(page) * p.c.Hkv + g.hk];
+        if (kb != 255) km = max(km, kb - 127);
+        if (vb != 255) vm = max(vm, vb - 127);
+      }
+      km = __reduce_max_sync(0xffffffffu, km);
+      vm = __reduce_max_sync(0xffffffffu, vm);
+      if (lane == 0) {
+        sd.warp_max[warp][0] = km;
+        sd.warp_max[warp][1] = vm;
+      }
+      named_bar_sync(1, 128);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        km = max(km, sd.warp_max[w][0]);
+        vm = max(vm, sd.warp_max[w][1]);
+      }
+      if (tid == 0) {
+        sd.kv_exp[i & 3][0] = km;
+        sd.kv_exp[i & 3][1] = vm;
+      }
+      if (tid < D) sd.nan_at[i & 3][tid] = 0x7FFFFFFF;
+      named_bar_sync(1, 128);
+
+      // a tile's codes, on their way in registers
+      uint4 kw[GR * PASS], vw[GR * PASS];
+      int sk[2] = {0, 0}, sv[2] = {0, 0};  // scale bytes of the warp's two groups of 16 tokens
+      int pages[2] = {-1, -1};
+      auto look_up = [&](int j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int tok = j * KV + warp * 32 + h * 16;
+          pages[h] = -1;
+          if (j < g.t1 && tok < len) {
+            const int page = __ldg(b.table + int64_t(g.s) * b.max_pages + tok / p.c.ps);
+            if (page >= 0 && page < p.c.num_pages) pages[h] = page;
+          }
+        }
+      };
+      auto scales_of = [&]() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t at = int64_t(max(pages[h], 0)) * p.c.Hkv + g.hk;
+          sk[h] = pages[h] < 0 ? 0 : p.c.ks[at];
+          sv[h] = pages[h] < 0 ? 0 : p.c.vs[at];
+        }
+      };
+      auto load = [&](const uint8_t* pool, int j, uint4(&w)[GR * PASS]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int tok = j * KV + warp * 32 + h * 16;
+          const uint8_t* at = pool + int64_t(max(pages[h], 0)) * p.c.page_stride + int64_t(g.hk) * p.c.head_stride +
+                              int64_t(tok % p.c.ps + r8) * p.c.token_stride + u4 * 16;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const bool in = pages[h] >= 0 && tok + 8 * y + r8 < len;
+#pragma unroll
+            for (int u = 0; u < PASS; ++u) {
+              uint4& x = w[(h * 2 + y) * PASS + u];
+              x = make_uint4(0, 0, 0, 0);
+              if (in) x = *reinterpret_cast<const uint4*>(at + int64_t(8 * y) * p.c.token_stride + u * 64);
+            }
+          }
+        }
+      };
+      look_up(g.t0);
+      scales_of();
+      load(p.c.k, g.t0, kw);
+      load(p.c.v, g.t0, vw);
+
+      // queries: a row to D/8 lanes
+      ok = mbar_wait(&bars->q_empty, uint32_t(i & 1) ^ 1u, abort, b.status, tmo, 11);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      {
+        constexpr int LPR = D / 8, RPP = 128 / LPR;  // lanes of a row, rows of a pass of the warpgroup
+        const int c8 = tid % LPR;
+#pragma unroll 4
+        for (int r = tid / LPR; r < UNIT; r += RPP) {
+          const int row = g.qb * UNIT + r;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (row < rows) {
+            const int tk = row / p.group;
+            w = *reinterpret_cast<const uint4*>(p.q + int64_t(g.seq.row0 + tk) * p.q_ts +
+                                                int64_t(g.hk * p.group + row - tk * p.group) * p.q_hs + c8 * 8);
+          }
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          float amax = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
+#pragma unroll
+          for (int d = LPR / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+          const int e = min(max(int(__float_as_uint(amax) >> 23) - 127, -126), 127);
+          const float down = pow2f(-e);
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            h[k] = pack_f16x2(__uint_as_float(u[k] << 16) * down, __uint_as_float(u[k] & 0xFFFF0000u) * down);
+          const uint32_t at = smem + L::Q + uint32_t((r >> 7) * L::TILE + (c8 >> 3) * BOX + (r & 127) * 128);
+          st_shared_v4(at + (((c8 & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+          if (c8 == 0) sd.q_exp[i & 1][r] = int8_t(e);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full);
+      }
+
+      for (int j = g.t0; j < g.t1; ++j) {
+        uint32_t fk[2], fv[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          fk[h] = block_factor(sk[h], km);
+          fv[h] = block_factor(sv[h], vm);
+          if (sv[h] == 255) {  // values of NaN: as codes, so that rows that do not see them can be spared
+            fv[h] = 0x3C003C00u;
+#pragma unroll
+            for (int x = 2 * h; x < 2 * h + 2; ++x)
+              if (j * KV + warp * 32 + x * 8 + r8 < len) {
+#pragma unroll
+                for (int u = 0; u < PASS; ++u) vw[x * PASS + u] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+              }
+          }
+        }
+        if (j + 1 < g.t1) look_up(j + 1);
+        ok = mbar_wait(&bars->k_empty[ks], kph ^ 1u, abort, b.status, tmo, 12);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int x = 0; x < GR; ++x)
+#pragma unroll
+          for (int u = 0; u < PASS; ++u)
+            put16(smem + L::K + ks * L::TILE, warp * 32 + x * 8 + r8, u * 4 + u4, kw[x * PASS + u], fk[x >> 1]);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->k_full[ks]);
+        if (++ks == KST) {
+          ks = 0;
+          kph ^= 1u;
+        }
+        if (j + 1 < g.t1) {
+          load(p.c.k, j + 1, kw);
+          scales_of();
+        }
+        if ((j + 1) * KV > min_lim) {
+#pragma unroll
+          for (int x = 0; x < GR; ++x)
+#pragma unroll
+            for (int u = 0; u < PASS; ++u) {
+              uint4& w = vw[x * PASS + u];
+              if (nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w)) {
+                const int tok = j * KV + warp * 32 + x * 8 + r8;
+                uint32_t c[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t bad = nan_bytes(c[k]);
+#pragma unroll
+                  for (int y = 0; y < 4; ++y)
+                    if (bad >> (8 * y) & 0x80u) atomicMin(&sd.nan_at[i & 3][(u * 4 + u4) * 16 + k * 4 + y], tok);
+                  c[k] &= ~((bad >> 7) * 0xFFu);
+                }
+                w = make_uint4(c[0], c[1], c[2], c[3]);
+              }
+            }
+        }
+        ok = mbar_wait(&bars->v_empty[vs], vph ^ 1u, abort, b.status, tmo, 13);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int x = 0; x < GR; ++x)
+#pragma unroll
+          for (int u = 0; u < PASS; ++u)
+            put16(smem + L::V + vs * L::TILE, warp * 32 + x * 8 + r8, u * 4 + u4, vw[x * PASS + u], fv[x >> 1]);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->v_full[vs]);
+        if (++vs == VST) {
+          vs = 0;
+          vph ^= 1u;
+        }
+        if (j + 1 < g.t1) load(p.c.v, j + 1, vw);
+      }
+      if (!ok || !seg_next(p, g)) break;
+    }
+  } else if (warp < 8) {
+    reg_dec<64>();
+    if (warp == 4 && lane == 0) {
+      // ---------------------------------------------------------------- the issuing thread
+      int ks = 0, vs = 0;
+      uint32_t kph = 0, vph = 0;
+      uint32_t pcount[2] = {0, 0};
+      const uint32_t s_tmem[2] = {tmem_base, tmem_base + 128};
+      const uint32_t o_tmem[2] = {tmem_base + 256, tmem_base + 384};
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int tiles = g.t1 - g.t0;
+        const uint32_t uph = uint32_t(i & 1);
+        ok = mbar_wait(&bars->q_full, uph, abort, b.status, tmo, 21) &&
+             mbar_wait(&bars->k_full[ks], kph, abort, b.status, tmo, 22);
+        if (!ok) break;
+        tc_fence_after();
+        for (int X = 0; X < 2; ++X) {
+          issue_qk<D>(smem, X, ks, s_tmem[X]);
+          tc_commit(&bars->s_full[X]);
+        }
+        if (tiles == 1) tc_commit(&bars->q_empty);
+        tc_commit(&bars->k_empty[ks]);
+        if (++ks == KST) {
+          ks = 0;
+          kph ^= 1u;
+        }
+        for (int j = 0; j < tiles && ok; ++j) {
+          if (!(ok = mbar_wait(&bars->v_full[vs], vph, abort, b.status, tmo, 23))) break;
+          for (int X = 0; X < 2; ++X) {
+            ok = mbar_wait(&bars->p_full[X], pcount[X] & 1u, abort, b.status, tmo, 24);
+            ++pcount[X];
+            if (ok && j == 0) ok = mbar_wait(&bars->o_empty[X], uph ^ 1u, abort, b.status, tmo, 25);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv<D>(smem, s_tmem[X], vs, o_tmem[X], j > 0);
+            if (X == 1) {
+              tc_commit(&bars->v_empty[vs]);
+              if (++vs == VST) {
+                vs = 0;
+                vph ^= 1u;
+              }
+            }
+            if (j + 1 < tiles) {
+              if (X == 0) {
+                if (!(ok = mbar_wait(&bars->k_full[ks], kph, abort, b.status, tmo, 26))) break;
+                tc_fence_after();
+              }
+              issue_qk<D>(smem, X, ks, s_tmem[X]);
+              tc_commit(&bars->s_full[X]);
+              if (X == 1) {
+                if (j + 2 == tiles) tc_commit(&bars->q_empty);
+                tc_commit(&bars->k_empty[ks]);
+                if (++ks == KST) {
+                  ks = 0;
+                  kph ^= 1u;
+                }
+              }
+            } else {
+              tc_commit(&bars->o_full[X]);
+            }
+          }
+        }
+        if (!ok || !seg_next(p, g)) break;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax, a row to a thread
+    reg_inc<168>();
+    const int X = (warp - 8) >> 2;
+    const int row = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem_base + lane_base + uint32_t(X * 128);
+    const uint32_t o_addr = tmem_base + lane_base + uint32_t(256 + X * 128);
+    uint32_t sc = 0;
+    bool ok = true;
+    int64_t at = run0;
+    for (int i = 0;; ++i) {
+      const int r = g.qb * UNIT + X * ROWS + row;
+      const int rows = seq_rows(p, g.seq);
+      const int lim = row_limit(p, g.seq, min(r, rows - 1));
+      float m = -INFINITY, l = 0.0f, f = 0.0f;
+      for (int j = g.t0; j < g.t1; ++j) {
+        ok = mbar_wait(&bars->s_full[X], sc & 1u, abort, b.status, tmo, 31);
+        ++sc;
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (j == g.t0) {
+          const int e = int(sd.q_exp[i & 1][X * ROWS + row]) + sd.kv_exp[i & 3][0];
+          // above 0, so that a masked score stays -inf
+          f = fmaxf(p.scale_log2 * pow2f(max(min(e / 2, 127), -126)) * pow2f(max(min(e - e / 2, 127), -126)), 1e-38f);
+        }
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32cols(s_addr + uint32_t(c * 32), v[c]);
+        tmem_ld_wait();
+        const int vis = lim - j * KV;
+        if (vis < KV) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c * 32 + k >= vis) v[c][k] = __float_as_uint(-INFINITY);
+        }
+        // row max in eight chains
+        float mq[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t* x = &v[q >> 1][(q & 1) * 16];
+          float a = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+#pragma unroll
+          for (int k = 3; k < 15; k += 2) a = max3(a, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+          mq[q] = fmaxf(a, __uint_as_float(x[15]));
+        }
+        const float mx = fmaxf(max3(mq[0], mq[1], mq[2]), max3(max3(mq[3], mq[4], mq[5]), mq[6], mq[7]));
+        const float mnew = fmaxf(m, mx * f);
+        const bool resc = mnew > m + kSlack;
+        float alpha = 1.0f;
+        if (resc) {
+          alpha = ex2_approx(m - mnew);
+          m = mnew;
+          l *= alpha;
+        }
+        const float add = m == -INFINITY ? kShift : kShift - m;
+        float sq[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sq[q] = 0.0f;
+        // P as fp16 pairs over the first 64 columns of S (all of S is in registers by now)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const int key = c * 64 + 2 * k;
+            const float p0 = ex2_approx(fmaf(__uint_as_float(v[key >> 5][key & 31]), f, add));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(v[(key + 1) >> 5][(key + 1) & 31]), f, add));
+            sq[k & 7] += p0 + p1;
+            w[k] = pack_f16x2(p0, p1);
+          }
+          tmem_st_32cols(s_addr + uint32_t(c * 32), w);
+          if (c == 0 && j > g.t0 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld_32cols(o_addr + uint32_t(q * 32), o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st_32cols(o_addr + uint32_t(q * 32), o);
+            }
+          }
+        }
+        l += ((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7]));
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[X]);
+      }
+      if (!ok) break;
+      ok = mbar_wait(&bars->o_full[X], uint32_t(i & 1), abort, b.status, tmo, 32);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l, pe = pow2f(sd.kv_exp[i & 3][1]);
+      const bool row_ok = r < rows;
+      const bool whole = g.t0 == 0 && g.t1 == g.nkv;
+      const int tk = r / p.group, head = g.hk * p.group + r - tk * p.group;
+      uint16_t* orow = p.out + (int64_t(g.seq.row0 + tk) * p.H + head) * D;
+      constexpr int64_t SLOT = 2 * ROWS * (D + 2);  // one segment's rows: D means, maximum, sum
+      float* mine_row = p.partial + (2 * cta + (g.t0 == 0 ? 1 : 0)) * SLOT + int64_t(X * ROWS + row) * (D + 2);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld_32cols(o_addr + uint32_t(c * 32), o);
+        tmem_ld_wait();
+        float x[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          x[k] = __uint_as_float(o[k]) * inv * pe;
+          if (sd.nan_at[i & 3][c * 32 + k] < lim) x[k] = __uint_as_float(0x7FFFFFFFu);
+        }
+        if (!row_ok) continue;
+        if (whole) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            st_global_v4(orow + c * 32 + q * 8, pack_bf16x2(x[q * 8], x[q * 8 + 1]), pack_bf16x2(x[q * 8 + 2], x[q * 8 + 3]),
+                         pack_bf16x2(x[q * 8 + 4], x[q * 8 + 5]), pack_bf16x2(x[q * 8 + 6], x[q * 8 + 7]));
+        } else {
+#pragma unroll
+          for (int q = 0; q < 16; ++q) __stcg(reinterpret_cast<float2*>(mine_row + c * 32) + q, make_float2(x[2 * q], x[2 * q + 1]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->o_empty[X]);
+      if (whole) {
+        if (row_ok && p.lse)
+          p.lse[int64_t(head) * b.n_tokens + g.seq.row0 + tk] =
+              l == 0.0f ? -INFINITY : (m - kShift + log2f(l)) * 0.69314718055994531f;
+      } else {
+        if (row_ok) __stcg(reinterpret_cast<float2*>(mine_row + D), make_float2(m, l));
+        const int64_t t0 = at - g.t0;
+        const int64_t c0 = ((t0 + 1) * n - 1) / total, c1 = ((t0 + g.nkv) * n - 1) / total;
+        __threadfence();
+        named_bar_sync(2 + X, 128);
+        if ((tid & 127) == 0) {
+          uint32_t* counter = p.counters + 2 * c0 + X;
+          sd.last[X] = atomicAdd(counter, 1u) == uint32_t(c1 - c0);
+          if (sd.last[X]) *counter = 0;
+        }
+        named_bar_sync(2 + X, 128);
+        if (sd.last[X] && row_ok) {
+          __threadfence();
+          const float* rows_at = p.partial + int64_t(X * ROWS + row) * (D + 2);
+          auto slot = [&](int64_t c) { return rows_at + (2 * c + (c == c0)) * SLOT; };
+          float top = -INFINITY, sum = 0.0f;
+          for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(slot(c) + D));
+          for (int64_t c = c0; c <= c1; ++c) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot(c) + D));
+            sum += ml.x == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - top);
+          }
+          const float is = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll 1
+          for (int q = 0; q < D / 8; ++q) {
+            float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+            for (int64_t c = c0; c <= c1; ++c) {
+              const float* from = slot(c);
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + D));
+              const float wgt = (ml.x == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - top)) * is;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 v2 = __ldcg(reinterpret_cast<const float2*>(from + q * 8) + k);
+                x[2 * k] = fmaf(wgt, v2.x, x[2 * k]);
+                x[2 * k + 1] = fmaf(wgt, v2.y, x[2 * k + 1]);
+              }
+            }
+            st_global_v4(orow + q * 8, pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                         pack_bf16x2(x[6], x[7]));
+          }
+          if (p.lse)
+            p.lse[int64_t(head) * b.n_tokens + g.seq.row0 + tk] =
+                sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * 0.69314718055994531f;
+        }
+      }
+      at += g.t1 - g.t0;
+      if (!seg_next(p, g)) break;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (bars->abort) {  // products that nobody waits for end before their memory is given back
+    const uint64_t t0 = now_ns();
+    while (now_ns() - t0 < 50000) {
+    }
+  }
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+}  // namespace
+
+size_t prefill_counter_bytes(int ctas) { return (size_t(ctas) * 2 * 4 + 255) / 256 * 256; }
+size_t prefill_partial_bytes(int ctas, int D) { return size_t(ctas) * 2 * UNIT * (D + 2) * sizeof(float); }
+
+tl_status launch_kv_prefill(PrefillParams& p, int D, int ctas, cudaStream_t st) {
+  void* args[] = {&p};
+  return D == 128 ? launch(reinterpret_cast<const void*>(&kv_prefill_kernel<128>), ctas, THREADS, smem_bytes<128>(), st,
+                           args, false)
+                  : launch(reinterpret_cast<const void*>(&kv_prefill_kernel<64>), ctas, THREADS, smem_bytes<64>(), st,
+                           args, false);
+}
+
+}  // namespace tl
