@@ -71,8 +71,9 @@ struct Side {
   int32_t nan_at[4][128];  // least token whose value is NaN in the dim, among those not all rows see
   int32_t warp_max[4][2];
   int64_t warp_sum[16];
-  int64_t begin_left;
-  int32_t begin[4];        // sequence, kv head, row block, tile
+  int64_t total, ctas, run0;  // tiles of all runs, runs, this run's first tile
+  int32_t begin[4];           // sequence, kv head, row block, tile
+  int32_t tiles[4];           // of the segments in work
   int32_t last[2];
 };
 
@@ -90,7 +91,7 @@ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, bool b_mn_major) {
 struct Seg {
   KvSeq seq;
   int s, hk, qb, nkv, t0, t1;  // tiles t0 .. t1-1 of the unit's nkv
-  int64_t left;
+  int left;                    // tiles of the run from t0 on
 };
 __device__ __forceinline__ int seq_rows(const PrefillParams& p, const KvSeq& q) {
   const int rows = q.q * p.group;
@@ -126,7 +127,7 @@ __device__ __forceinline__ bool seg_next(const PrefillParams& p, Seg& g) {
   }
   g.nkv = unit_tiles(p, g.seq, seq_rows(p, g.seq), g.qb);
   g.t0 = 0;
-  g.t1 = int(min(int64_t(g.nkv), g.left));
+  g.t1 = min(g.nkv, g.left);
   return true;
 }
 
@@ -140,23 +141,20 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uin
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Descriptors count in 16 bytes and lie in one 18-bit address space, so a step is an addition to the first.
 template <int D>
-__device__ __forceinline__ void issue_qk(uint32_t smem, int X, int ks, uint32_t d_tmem) {
-  using L = Layout<D>;
-  const uint32_t q0 = smem + L::Q + X * L::TILE, k0 = smem + L::K + ks * L::TILE;
+__device__ __forceinline__ void issue_qk(uint64_t q0, uint64_t k0, uint32_t d_tmem) {
 #pragma unroll
   for (int kk = 0; kk < D / UMMA_K; ++kk) {
-    const uint64_t ad = sdesc_sw128(q0 + (kk >> 2) * BOX + (kk & 3) * 32, 16, 1024);
-    const uint64_t bd = sdesc_sw128(k0 + (kk >> 2) * BOX + (kk & 3) * 32, 16, 1024);
-    tc_mma_bf16(d_tmem, ad, bd, idesc_f16_f32(ROWS, KV, false), kk > 0 ? 1u : 0u);
+    const uint64_t step = uint64_t((kk >> 2) * (BOX >> 4) + (kk & 3) * 2);
+    tc_mma_bf16(d_tmem, q0 + step, k0 + step, idesc_f16_f32(ROWS, KV, false), kk > 0 ? 1u : 0u);
   }
 }
 template <int D>
-__device__ __forceinline__ void issue_pv(uint32_t smem, uint32_t p_tmem, int vs, uint32_t d_tmem, bool accumulate) {
-  const uint32_t v0 = smem + Layout<D>::V + vs * Layout<D>::TILE;
+__device__ __forceinline__ void issue_pv(uint32_t p_tmem, uint64_t v0, uint32_t d_tmem, bool accumulate) {
 #pragma unroll
   for (int kk = 0; kk < KV / UMMA_K; ++kk)
-    mma_tmem_a(d_tmem, p_tmem + uint32_t(kk * 8), sdesc_sw128(v0 + kk * 2048, BOX, 1024), idesc_f16_f32(ROWS, D, true),
+    mma_tmem_a(d_tmem, p_tmem + uint32_t(kk * 8), v0 + uint64_t(kk * (2048 >> 4)), idesc_f16_f32(ROWS, D, true),
                (accumulate || kk > 0) ? 1u : 0u);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -170,6 +168,15 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// Codes are read once here: no place in L1, which is small beside the tiles
+__device__ __forceinline__ uint4 ld_codes(const uint8_t* a) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(a));
+  return r;
+}
 
 // Factor of a block with this scale byte relative to 2^top, as two halves.
 __device__ __forceinline__ uint32_t block_factor(int byte, int top) {
@@ -191,13 +198,24 @@ __device__ __forceinline__ void put16(uint32_t tile, int r, int u, uint4 w, uint
   st_shared_v4(row + (((at + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
 }
 
-template <int NREG>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(NREG));
+// Scores from the row's limit on become -infinity.
+__device__ __forceinline__ void mask(uint32_t (&v)[32], int vis) {
+  if (vis < 32) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (k >= vis) v[k] = __float_as_uint(-INFINITY);
+  }
 }
-template <int NREG>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(NREG));
+__device__ __forceinline__ float max32(const uint32_t (&v)[32]) {  // in four chains
+  float q[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    q[c] = max3(__uint_as_float(v[8 * c]), __uint_as_float(v[8 * c + 1]), __uint_as_float(v[8 * c + 2]));
+    q[c] = max3(q[c], __uint_as_float(v[8 * c + 3]), __uint_as_float(v[8 * c + 4]));
+    q[c] = max3(q[c], __uint_as_float(v[8 * c + 5]), __uint_as_float(v[8 * c + 6]));
+    q[c] = fmaxf(q[c], __uint_as_float(v[8 * c + 7]));
+  }
+  return max3(q[0], q[1], fmaxf(q[2], q[3]));
 }
 
 template <int D>
@@ -282,6 +300,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       at += size;
     }
   }
+  if (tid == 0) {
+    sd.total = total;
+    sd.ctas = n;
+    sd.run0 = run0;
+  }
   if (warp == 4) {
     tmem_alloc(&bars->tmem_base, TMEM_COLS);
     tmem_relinquish();
@@ -295,14 +318,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   g.hk = sd.begin[1];
   g.qb = sd.begin[2];
   g.t0 = sd.begin[3];
-  g.left = run1 - run0;
+  g.left = int(run1 - run0);
   g.seq = kv_seq(b, p.c.ps, g.s);
   g.nkv = unit_tiles(p, g.seq, seq_rows(p, g.seq), g.qb);
-  g.t1 = int(min(int64_t(g.nkv), g.t0 + g.left));
+  g.t1 = min(g.nkv, g.t0 + g.left);
 
   if (warp < 4) {
     // ---------------------------------------------------------------- conversion
-    reg_dec<112>();
     constexpr int UN = D / 16;       // 16-code units of a token
     constexpr int PASS = D / 64;     // units of one thread and row
     constexpr int GR = 4;            // rows of one thread and tile
@@ -340,6 +362,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         vm = max(vm, sd.warp_max[w][1]);
       }
       if (tid == 0) {
+        sd.tiles[i & 3] = g.left > g.t1 - g.t0 ? g.t1 - g.t0 : g.t0 - g.t1;  // the run's last one: negative
         sd.kv_exp[i & 3][0] = km;
         sd.kv_exp[i & 3][1] = vm;
       }
@@ -382,7 +405,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
             for (int u = 0; u < PASS; ++u) {
               uint4& x = w[(h * 2 + y) * PASS + u];
               x = make_uint4(0, 0, 0, 0);
-              if (in) x = *reinterpret_cast<const uint4*>(at + int64_t(8 * y) * p.c.token_stride + u * 64);
+              if (in) x = ld_codes(at + int64_t(8 * y) * p.c.token_stride + u * 64);
             }
           }
         }
@@ -513,24 +536,24 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       if (!ok || !seg_next(p, g)) break;
     }
   } else if (warp < 8) {
-    reg_dec<64>();
     if (warp == 4 && lane == 0) {
       // ---------------------------------------------------------------- the issuing thread
       int ks = 0, vs = 0;
       uint32_t kph = 0, vph = 0;
       uint32_t pcount[2] = {0, 0};
-      const uint32_t s_tmem[2] = {tmem_base, tmem_base + 128};
-      const uint32_t o_tmem[2] = {tmem_base + 256, tmem_base + 384};
+      const uint64_t q0 = sdesc_sw128(smem + L::Q, 16, 1024), k0 = sdesc_sw128(smem + L::K, 16, 1024);
+      const uint64_t v0 = sdesc_sw128(smem + L::V, BOX, 1024);
+      constexpr uint64_t TSTEP = L::TILE >> 4;
       bool ok = true;
       for (int i = 0; ok; ++i) {
-        const int tiles = g.t1 - g.t0;
         const uint32_t uph = uint32_t(i & 1);
         ok = mbar_wait(&bars->q_full, uph, abort, b.status, tmo, 21) &&
              mbar_wait(&bars->k_full[ks], kph, abort, b.status, tmo, 22);
         if (!ok) break;
         tc_fence_after();
+        const int said = *reinterpret_cast<volatile int32_t*>(&sd.tiles[i & 3]), tiles = said < 0 ? -said : said;
         for (int X = 0; X < 2; ++X) {
-          issue_qk<D>(smem, X, ks, s_tmem[X]);
+          issue_qk<D>(q0 + X * TSTEP, k0 + ks * TSTEP, tmem_base + X * 128);
           tc_commit(&bars->s_full[X]);
         }
         if (tiles == 1) tc_commit(&bars->q_empty);
@@ -547,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
             if (ok && j == 0) ok = mbar_wait(&bars->o_empty[X], uph ^ 1u, abort, b.status, tmo, 25);
             if (!ok) break;
             tc_fence_after();
-            issue_pv<D>(smem, s_tmem[X], vs, o_tmem[X], j > 0);
+            issue_pv<D>(tmem_base + X * 128, v0 + vs * TSTEP, tmem_base + 256 + X * 128, j > 0);
             if (X == 1) {
               tc_commit(&bars->v_empty[vs]);
               if (++vs == VST) {
@@ -560,7 +583,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
                 if (!(ok = mbar_wait(&bars->k_full[ks], kph, abort, b.status, tmo, 26))) break;
                 tc_fence_after();
               }
-              issue_qk<D>(smem, X, ks, s_tmem[X]);
+              issue_qk<D>(q0 + X * TSTEP, k0 + ks * TSTEP, tmem_base + X * 128);
               tc_commit(&bars->s_full[X]);
               if (X == 1) {
                 if (j + 2 == tiles) tc_commit(&bars->q_empty);
@@ -575,13 +598,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
             }
           }
         }
-        if (!ok || !seg_next(p, g)) break;
+        if (!ok || said < 0) break;
       }
     }
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax, a row to a thread
-    reg_inc<168>();
     const int X = (warp - 8) >> 2;
     const int row = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
@@ -589,7 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     const uint32_t o_addr = tmem_base + lane_base + uint32_t(256 + X * 128);
     uint32_t sc = 0;
     bool ok = true;
-    int64_t at = run0;
+    int done = 0;  // tiles of the run before this segment
     for (int i = 0;; ++i) {
       const int r = g.qb * UNIT + X * ROWS + row;
       const int rows = seq_rows(p, g.seq);
@@ -608,29 +630,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           // above 0, so that a masked score stays -inf
           f = fmaxf(p.scale_log2 * pow2f(max(min(e / 2, 127), -126)) * pow2f(max(min(e - e / 2, 127), -126)), 1e-38f);
         }
-        uint32_t v[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32cols(s_addr + uint32_t(c * 32), v[c]);
-        tmem_ld_wait();
+        // S is read in halves, the first one last, so that it is still in registers when P takes its place;
+        // a whole row would leave no registers for anything else
         const int vis = lim - j * KV;
-        if (vis < KV) {
+        uint32_t va[32], vb[32];
+        float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c * 32 + k >= vis) v[c][k] = __float_as_uint(-INFINITY);
+        for (int half = 1; half >= 0; --half) {
+          tmem_ld_32cols(s_addr + uint32_t(half * 64), va);
+          tmem_ld_32cols(s_addr + uint32_t(half * 64 + 32), vb);
+          tmem_ld_wait();
+          mask(va, vis - half * 64);
+          mask(vb, vis - half * 64 - 32);
+          mx = max3(mx, max32(va), max32(vb));
         }
-        // row max in eight chains
-        float mq[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t* x = &v[q >> 1][(q & 1) * 16];
-          float a = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
-#pragma unroll
-          for (int k = 3; k < 15; k += 2) a = max3(a, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-          mq[q] = fmaxf(a, __uint_as_float(x[15]));
-        }
-        const float mx = fmaxf(max3(mq[0], mq[1], mq[2]), max3(max3(mq[3], mq[4], mq[5]), mq[6], mq[7]));
         const float mnew = fmaxf(m, mx * f);
         const bool resc = mnew > m + kSlack;
         float alpha = 1.0f;
@@ -640,35 +653,45 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           l *= alpha;
         }
         const float add = m == -INFINITY ? kShift : kShift - m;
-        float sq[8];
+        float sq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        // P as fp16 pairs over the first 64 columns of S
 #pragma unroll
-        for (int q = 0; q < 8; ++q) sq[q] = 0.0f;
-        // P as fp16 pairs over the first 64 columns of S (all of S is in registers by now)
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1) {
+            if (j > g.t0 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                tmem_ld_32cols(o_addr + uint32_t(q * 32), va);
+                tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+                for (int k = 0; k < 32; ++k) va[k] = __float_as_uint(__uint_as_float(va[k]) * alpha);
+                tmem_st_32cols(o_addr + uint32_t(q * 32), va);
+              }
+            }
+            tmem_ld_32cols(s_addr + 64u, va);
+            tmem_ld_32cols(s_addr + 96u, vb);
+            tmem_ld_wait();
+            mask(va, vis - 64);
+            mask(vb, vis - 96);
+          }
           uint32_t w[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int key = c * 64 + 2 * k;
-            const float p0 = ex2_approx(fmaf(__uint_as_float(v[key >> 5][key & 31]), f, add));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(v[(key + 1) >> 5][(key + 1) & 31]), f, add));
-            sq[k & 7] += p0 + p1;
+          for (int k = 0; k < 16; ++k) {
+            const float p0 = ex2_approx(fmaf(__uint_as_float(va[2 * k]), f, add));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(va[2 * k + 1]), f, add));
+            sq[k & 3] += p0 + p1;
             w[k] = pack_f16x2(p0, p1);
           }
-          tmem_st_32cols(s_addr + uint32_t(c * 32), w);
-          if (c == 0 && j > g.t0 && __any_sync(0xffffffffu, resc)) {
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld_32cols(o_addr + uint32_t(q * 32), o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-              tmem_st_32cols(o_addr + uint32_t(q * 32), o);
-            }
+          for (int k = 0; k < 16; ++k) {
+            const float p0 = ex2_approx(fmaf(__uint_as_float(vb[2 * k]), f, add));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(vb[2 * k + 1]), f, add));
+            sq[k & 3] += p0 + p1;
+            w[16 + k] = pack_f16x2(p0, p1);
           }
+          tmem_st_32cols(s_addr + uint32_t(half * 32), w);
         }
-        l += ((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7]));
+        l += (sq[0] + sq[1]) + (sq[2] + sq[3]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -687,7 +710,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const int tk = r / p.group, head = g.hk * p.group + r - tk * p.group;
       uint16_t* orow = p.out + (int64_t(g.seq.row0 + tk) * p.H + head) * D;
       constexpr int64_t SLOT = 2 * ROWS * (D + 2);  // one segment's rows: D means, maximum, sum
-      float* mine_row = p.partial + (2 * cta + (g.t0 == 0 ? 1 : 0)) * SLOT + int64_t(X * ROWS + row) * (D + 2);
+      float* mine_row = p.partial + (2 * int64_t(blockIdx.x) + (g.t0 == 0 ? 1 : 0)) * SLOT + int64_t(X * ROWS + row) * (D + 2);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -719,8 +742,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
               l == 0.0f ? -INFINITY : (m - kShift + log2f(l)) * 0.69314718055994531f;
       } else {
         if (row_ok) __stcg(reinterpret_cast<float2*>(mine_row + D), make_float2(m, l));
-        const int64_t t0 = at - g.t0;
-        const int64_t c0 = ((t0 + 1) * n - 1) / total, c1 = ((t0 + g.nkv) * n - 1) / total;
+        const int64_t t0 = sd.run0 + done - g.t0;
+        const int64_t c0 = ((t0 + 1) * sd.ctas - 1) / sd.total, c1 = ((t0 + g.nkv) * sd.ctas - 1) / sd.total;
         __threadfence();
         named_bar_sync(2 + X, 128);
         if ((tid & 127) == 0) {
@@ -762,7 +785,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
                 sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * 0.69314718055994531f;
         }
       }
-      at += g.t1 - g.t0;
+      done += g.t1 - g.t0;
       if (!seg_next(p, g)) break;
     }
   }
