@@ -7,11 +7,11 @@
 // head and 256 of a sequence's query rows, rows being (token, head of the group), so
 // that all heads of a group share every key/value tile; two 128-row tiles A and B
 // take turns, one in the softmax while the tensor cores work for the other.
-//   warps 0-3    convert: queries bf16 -> fp16 (each row by a power of two), then
-//                each 128-token tile of codes -> fp16, K and V, into shared memory in
-//                the 128-byte-swizzled layout that the products read.  A tile's loads
-//                are in registers a tile ahead.
-//   warp 4       issues the products: S_X = Q_X K^T and O_X += P_X V (M = 128), P from
+//   warps 0-7    convert: queries bf16 -> fp16 (each row by a power of two), then
+//                each 128-token tile of codes -> fp16, warps 0-3 keys and 4-7 values,
+//                into shared memory in the 128-byte-swizzled layout that the products
+//                read.  A tile's loads are in registers a tile ahead.
+//   warp 16      issues the products: S_X = Q_X K^T and O_X += P_X V (M = 128), P from
 //                tensor memory, in the order QK_A(0) QK_B(0) | PV_A(j) QK_A(j+1)
 //                PV_B(j) QK_B(j+1) | ...
 //   warps 8-11   softmax of tile A, warps 12-15 of tile B, a row to a thread.
@@ -42,7 +42,8 @@
 namespace tl {
 namespace {
 
-constexpr int THREADS = 512;
+constexpr int THREADS = 17 * 32;
+constexpr int WARP_SOFTMAX = 8, WARP_MMA = 16;
 constexpr int KV = 128;          // tokens of a tile
 constexpr int ROWS = 128;        // query rows of a tile
 constexpr int UNIT = 2 * ROWS;
@@ -69,8 +70,8 @@ struct Side {
   int8_t q_exp[2][UNIT];   // rows' exponents, by segment parity
   int32_t kv_exp[4][2];    // exponents of the segment's keys and values
   int32_t nan_at[4][128];  // least token whose value is NaN in the dim, among those not all rows see
-  int32_t warp_max[4][2];
-  int64_t warp_sum[16];
+  int32_t warp_max[8][2];
+  int64_t warp_sum[17];
   int64_t total, ctas, run0;  // tiles of all runs, runs, this run's first tile
   int32_t begin[4];           // sequence, kv head, row block, tile
   int32_t tiles[4];           // of the segments in work
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   }
   if (lane == 31) sd.warp_sum[warp] = before;
   if (tid == 0) {
-    mbar_init(&bars->q_full, 4);
+    mbar_init(&bars->q_full, 8);
     mbar_init(&bars->q_empty, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     sd.ctas = n;
     sd.run0 = run0;
   }
-  if (warp == 4) {
+  if (warp == WARP_MMA) {
     tmem_alloc(&bars->tmem_base, TMEM_COLS);
     tmem_relinquish();
   }
@@ -323,24 +324,31 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   g.nkv = unit_tiles(p, g.seq, seq_rows(p, g.seq), g.qb);
   g.t1 = min(g.nkv, g.t0 + g.left);
 
-  if (warp < 4) {
-    // ---------------------------------------------------------------- conversion
-    constexpr int UN = D / 16;       // 16-code units of a token
-    constexpr int PASS = D / 64;     // units of one thread and row
+  if (warp < WARP_SOFTMAX) {
+    // ---------------------------------------------------------------- conversion: warps 0-3 keys, 4-7 values
+    constexpr int PASS = D / 64;     // 16-code units of one thread and row
     constexpr int GR = 4;            // rows of one thread and tile
-    const int r8 = lane >> 2, u4 = lane & 3;
-    int ks = 0, vs = 0;
-    uint32_t kph = 0, vph = 0;
+    const bool val = warp >= 4;
+    const int r8 = lane >> 2, u4 = lane & 3, w32 = (warp & 3) * 32;
+    const uint8_t* pool = val ? p.c.v : p.c.k;
+    const uint8_t* scale_at = val ? p.c.vs : p.c.ks;
+    uint64_t* full = val ? bars->v_full : bars->k_full;
+    uint64_t* empty = val ? bars->v_empty : bars->k_empty;
+    const uint32_t ring = smem + (val ? L::V : L::K);
+    const int stages = val ? VST : KST;
+    int st = 0;
+    uint32_t ph = 0;
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const int rows = seq_rows(p, g.seq);
       const int len = g.seq.len;
       const int min_lim = row_limit(p, g.seq, g.qb * UNIT);
+      const int32_t* table = b.table + int64_t(g.s) * b.max_pages;
       // the largest scales of the segment's pages
       const int tok_end = min(len, g.t1 * KV);
       int km = -127, vm = -127;
-      for (int pg = g.t0 * KV / p.c.ps + tid; pg * int64_t(p.c.ps) < tok_end; pg += 128) {
-        const int page = __ldg(b.table + int64_t(g.s) * b.max_pages + pg);
+      for (int pg = g.t0 * KV / p.c.ps + tid; pg * int64_t(p.c.ps) < tok_end; pg += 256) {
+        const int page = __ldg(table + pg);
         if (page < 0 || page >= p.c.num_pages) {
           record_error(b.status, kKvInvalid, uint32_t(g.s), uint32_t(page), uint32_t(pg));
           continue;
@@ -355,9 +363,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         sd.warp_max[warp][0] = km;
         sd.warp_max[warp][1] = vm;
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(1, 256);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < 8; ++w) {
         km = max(km, sd.warp_max[w][0]);
         vm = max(vm, sd.warp_max[w][1]);
       }
@@ -367,35 +375,28 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         sd.kv_exp[i & 3][1] = vm;
       }
       if (tid < D) sd.nan_at[i & 3][tid] = 0x7FFFFFFF;
-      named_bar_sync(1, 128);
+      named_bar_sync(1, 256);
+      const int top = val ? vm : km;
 
       // a tile's codes, on their way in registers
-      uint4 kw[GR * PASS], vw[GR * PASS];
-      int sk[2] = {0, 0}, sv[2] = {0, 0};  // scale bytes of the warp's two groups of 16 tokens
+      uint4 cw[GR * PASS];
+      int sb[2] = {0, 0};  // scale bytes of the warp's two groups of 16 tokens
       int pages[2] = {-1, -1};
       auto look_up = [&](int j) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int tok = j * KV + warp * 32 + h * 16;
+          const int tok = j * KV + w32 + h * 16;
           pages[h] = -1;
           if (j < g.t1 && tok < len) {
-            const int page = __ldg(b.table + int64_t(g.s) * b.max_pages + tok / p.c.ps);
+            const int page = __ldg(table + tok / p.c.ps);
             if (page >= 0 && page < p.c.num_pages) pages[h] = page;
           }
         }
       };
-      auto scales_of = [&]() {
+      auto load = [&](int j) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int64_t at = int64_t(max(pages[h], 0)) * p.c.Hkv + g.hk;
-          sk[h] = pages[h] < 0 ? 0 : p.c.ks[at];
-          sv[h] = pages[h] < 0 ? 0 : p.c.vs[at];
-        }
-      };
-      auto load = [&](const uint8_t* pool, int j, uint4(&w)[GR * PASS]) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int tok = j * KV + warp * 32 + h * 16;
+          const int tok = j * KV + w32 + h * 16;
           const uint8_t* at = pool + int64_t(max(pages[h], 0)) * p.c.page_stride + int64_t(g.hk) * p.c.head_stride +
                               int64_t(tok % p.c.ps + r8) * p.c.token_stride + u4 * 16;
 #pragma unroll
@@ -403,17 +404,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
             const bool in = pages[h] >= 0 && tok + 8 * y + r8 < len;
 #pragma unroll
             for (int u = 0; u < PASS; ++u) {
-              uint4& x = w[(h * 2 + y) * PASS + u];
+              uint4& x = cw[(h * 2 + y) * PASS + u];
               x = make_uint4(0, 0, 0, 0);
               if (in) x = ld_codes(at + int64_t(8 * y) * p.c.token_stride + u * 64);
             }
           }
+          sb[h] = pages[h] < 0 ? 0 : scale_at[int64_t(pages[h]) * p.c.Hkv + g.hk];
         }
       };
       look_up(g.t0);
-      scales_of();
-      load(p.c.k, g.t0, kw);
-      load(p.c.v, g.t0, vw);
+      load(g.t0);
+      look_up(g.t0 + 1);
 
       // queries: a row to D/8 lanes
       ok = mbar_wait(&bars->q_empty, uint32_t(i & 1) ^ 1u, abort, b.status, tmo, 11);
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         break;
       }
       {
-        constexpr int LPR = D / 8, RPP = 128 / LPR;  // lanes of a row, rows of a pass of the warpgroup
+        constexpr int LPR = D / 8, RPP = 256 / LPR;  // lanes of a row, rows of a pass of the converting warps
         const int c8 = tid % LPR;
 #pragma unroll 4
         for (int r = tid / LPR; r < UNIT; r += RPP) {
@@ -456,87 +457,67 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       }
 
       for (int j = g.t0; j < g.t1; ++j) {
-        uint32_t fk[2], fv[2];
+        uint32_t f[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          fk[h] = block_factor(sk[h], km);
-          fv[h] = block_factor(sv[h], vm);
-          if (sv[h] == 255) {  // values of NaN: as codes, so that rows that do not see them can be spared
-            fv[h] = 0x3C003C00u;
+          f[h] = block_factor(sb[h], top);
+          if (val && sb[h] == 255) {  // values of NaN: as codes, so that rows that do not see them can be spared
+            f[h] = 0x3C003C00u;
 #pragma unroll
             for (int x = 2 * h; x < 2 * h + 2; ++x)
-              if (j * KV + warp * 32 + x * 8 + r8 < len) {
+              if (j * KV + w32 + x * 8 + r8 < len) {
 #pragma unroll
-                for (int u = 0; u < PASS; ++u) vw[x * PASS + u] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                for (int u = 0; u < PASS; ++u) cw[x * PASS + u] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
               }
           }
         }
-        if (j + 1 < g.t1) look_up(j + 1);
-        ok = mbar_wait(&bars->k_empty[ks], kph ^ 1u, abort, b.status, tmo, 12);
+        if (val && (j + 1) * KV > min_lim) {
+          uint32_t any = 0;
+#pragma unroll
+          for (int x = 0; x < GR * PASS; ++x)
+            any |= nan_bytes(cw[x].x) | nan_bytes(cw[x].y) | nan_bytes(cw[x].z) | nan_bytes(cw[x].w);
+          if (any) {
+#pragma unroll
+            for (int x = 0; x < GR * PASS; ++x) {
+              const int tok = j * KV + w32 + x / PASS * 8 + r8, d0 = (x % PASS * 4 + u4) * 16;
+              uint32_t c[4] = {cw[x].x, cw[x].y, cw[x].z, cw[x].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t bad = nan_bytes(c[k]);
+                for (uint32_t left = bad; left; left &= left - 1)
+                  atomicMin(&sd.nan_at[i & 3][d0 + k * 4 + ((__ffs(left) - 1) >> 3)], tok);
+                c[k] &= ~((bad >> 7) * 0xFFu);
+              }
+              cw[x] = make_uint4(c[0], c[1], c[2], c[3]);
+            }
+          }
+        }
+        ok = mbar_wait(empty + st, ph ^ 1u, abort, b.status, tmo, 12);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
+        const uint32_t tile = ring + uint32_t(st) * L::TILE;
 #pragma unroll
         for (int x = 0; x < GR; ++x)
 #pragma unroll
-          for (int u = 0; u < PASS; ++u)
-            put16(smem + L::K + ks * L::TILE, warp * 32 + x * 8 + r8, u * 4 + u4, kw[x * PASS + u], fk[x >> 1]);
+          for (int u = 0; u < PASS; ++u) put16(tile, w32 + x * 8 + r8, u * 4 + u4, cw[x * PASS + u], f[x >> 1]);
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->k_full[ks]);
-        if (++ks == KST) {
-          ks = 0;
-          kph ^= 1u;
+        if (lane == 0) mbar_arrive(full + st);
+        if (++st == stages) {
+          st = 0;
+          ph ^= 1u;
         }
         if (j + 1 < g.t1) {
-          load(p.c.k, j + 1, kw);
-          scales_of();
+          load(j + 1);
+          look_up(j + 2);
         }
-        if ((j + 1) * KV > min_lim) {
-#pragma unroll
-          for (int x = 0; x < GR; ++x)
-#pragma unroll
-            for (int u = 0; u < PASS; ++u) {
-              uint4& w = vw[x * PASS + u];
-              if (nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w)) {
-                const int tok = j * KV + warp * 32 + x * 8 + r8;
-                uint32_t c[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t bad = nan_bytes(c[k]);
-#pragma unroll
-                  for (int y = 0; y < 4; ++y)
-                    if (bad >> (8 * y) & 0x80u) atomicMin(&sd.nan_at[i & 3][(u * 4 + u4) * 16 + k * 4 + y], tok);
-                  c[k] &= ~((bad >> 7) * 0xFFu);
-                }
-                w = make_uint4(c[0], c[1], c[2], c[3]);
-              }
-            }
-        }
-        ok = mbar_wait(&bars->v_empty[vs], vph ^ 1u, abort, b.status, tmo, 13);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int x = 0; x < GR; ++x)
-#pragma unroll
-          for (int u = 0; u < PASS; ++u)
-            put16(smem + L::V + vs * L::TILE, warp * 32 + x * 8 + r8, u * 4 + u4, vw[x * PASS + u], fv[x >> 1]);
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->v_full[vs]);
-        if (++vs == VST) {
-          vs = 0;
-          vph ^= 1u;
-        }
-        if (j + 1 < g.t1) load(p.c.v, j + 1, vw);
       }
       if (!ok || !seg_next(p, g)) break;
     }
-  } else if (warp < 8) {
-    if (warp == 4 && lane == 0) {
+  } else if (warp == WARP_MMA) {
+    if (lane == 0) {
       // ---------------------------------------------------------------- the issuing thread
       int ks = 0, vs = 0;
       uint32_t kph = 0, vph = 0;
@@ -604,7 +585,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax, a row to a thread
-    const int X = (warp - 8) >> 2;
+    const int X = (warp - WARP_SOFTMAX) >> 2;
     const int row = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem_base + lane_base + uint32_t(X * 128);
@@ -797,7 +778,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     while (now_ns() - t0 < 50000) {
     }
   }
-  if (warp == 4) {
+  if (warp == WARP_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
