@@ -7,11 +7,11 @@
 // head and 256 of a sequence's query rows, rows being (token, head of the group), so
 // that all heads of a group share every key/value tile; two 128-row tiles A and B
 // take turns, one in the softmax while the tensor cores work for the other.
-//   warps 0-7    convert: queries bf16 -> fp16 (each row by a power of two), then
-//                each 128-token tile of codes -> fp16, warps 0-3 keys and 4-7 values,
-//                into shared memory in the 128-byte-swizzled layout that the products
-//                read.  A tile's loads are in registers a tile ahead.
-//   warp 16      issues the products: S_X = Q_X K^T and O_X += P_X V (M = 128), P from
+//   warps 0-6    convert: queries bf16 -> fp16 (each row by a power of two), then
+//                each 128-token tile of codes -> fp16, keys and values, 16 tokens an
+//                item, into shared memory in the 128-byte-swizzled layout that the
+//                products read.  A warp's next two items are on their way in registers.
+//   warp 7       issues the products: S_X = Q_X K^T and O_X += P_X V (M = 128), P from
 //                tensor memory, in the order QK_A(0) QK_B(0) | PV_A(j) QK_A(j+1)
 //                PV_B(j) QK_B(j+1) | ...
 //   warps 8-11   softmax of tile A, warps 12-15 of tile B, a row to a thread.
@@ -42,8 +42,9 @@
 namespace tl {
 namespace {
 
-constexpr int THREADS = 17 * 32;
-constexpr int WARP_SOFTMAX = 8, WARP_MMA = 16;
+constexpr int THREADS = 512;
+constexpr int CONV = 7;           // converting warps
+constexpr int WARP_MMA = 7, WARP_SOFTMAX = 8;
 constexpr int KV = 128;          // tokens of a tile
 constexpr int ROWS = 128;        // query rows of a tile
 constexpr int UNIT = 2 * ROWS;
@@ -70,8 +71,8 @@ struct Side {
   int8_t q_exp[2][UNIT];   // rows' exponents, by segment parity
   int32_t kv_exp[4][2];    // exponents of the segment's keys and values
   int32_t nan_at[4][128];  // least token whose value is NaN in the dim, among those not all rows see
-  int32_t warp_max[8][2];
-  int64_t warp_sum[17];
+  int32_t warp_max[CONV][2];
+  int64_t warp_sum[16];
   int64_t total, ctas, run0;  // tiles of all runs, runs, this run's first tile
   int32_t begin[4];           // sequence, kv head, row block, tile
   int32_t tiles[4];           // of the segments in work
@@ -133,30 +134,51 @@ __device__ __forceinline__ bool seg_next(const PrefillParams& p, Seg& g) {
 }
 
 // ---------------------------------------------------------------- products
-__device__ __forceinline__ void mma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// The issuing warp runs as one: control flow and operands are the same in all lanes, so that descriptors
+// stay in uniform registers, and the lane that issues is chosen by the predicate of the instruction alone.
+__device__ __forceinline__ void mma_smem(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
       : "memory");
 }
 // Descriptors count in 16 bytes and lie in one 18-bit address space, so a step is an addition to the first.
 template <int D>
-__device__ __forceinline__ void issue_qk(uint64_t q0, uint64_t k0, uint32_t d_tmem) {
+__device__ __forceinline__ void issue_qk(uint64_t q0, uint64_t k0, uint32_t d_tmem, uint32_t leader) {
 #pragma unroll
   for (int kk = 0; kk < D / UMMA_K; ++kk) {
     const uint64_t step = uint64_t((kk >> 2) * (BOX >> 4) + (kk & 3) * 2);
-    tc_mma_bf16(d_tmem, q0 + step, k0 + step, idesc_f16_f32(ROWS, KV, false), kk > 0 ? 1u : 0u);
+    mma_smem(d_tmem, q0 + step, k0 + step, idesc_f16_f32(ROWS, KV, false), kk > 0 ? 1u : 0u, leader);
   }
 }
 template <int D>
-__device__ __forceinline__ void issue_pv(uint32_t p_tmem, uint64_t v0, uint32_t d_tmem, bool accumulate) {
+__device__ __forceinline__ void issue_pv(uint32_t p_tmem, uint64_t v0, uint32_t d_tmem, bool accumulate, uint32_t leader) {
 #pragma unroll
   for (int kk = 0; kk < KV / UMMA_K; ++kk)
     mma_tmem_a(d_tmem, p_tmem + uint32_t(kk * 8), v0 + uint64_t(kk * (2048 >> 4)), idesc_f16_f32(ROWS, D, true),
-               (accumulate || kk > 0) ? 1u : 0u);
+               (accumulate || kk > 0) ? 1u : 0u, leader);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -168,7 +190,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
 // Codes are read once here: no place in L1, which is small beside the tiles
 __device__ __forceinline__ uint4 ld_codes(const uint8_t* a) {
@@ -199,6 +220,27 @@ __device__ __forceinline__ void put16(uint32_t tile, int r, int u, uint4 w, uint
   st_shared_v4(row + (((at + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
 }
 
+// In 16 tokens of a value tile that not all rows see: NaN out of the tile, and the least token with one kept
+// for each dim.  (Slots past the sequence's end are zero, or NaN under a NaN scale: no row's limit is beyond them.)
+template <int D>
+__device__ __noinline__ void spare_nan(uint32_t tile, int row0, int tok0, int32_t* nan_at) {
+  __syncwarp();
+  for (int x = int(lane_id()); x < 16 * D / 2; x += 32) {
+    const int r = row0 + x / (D / 2), d = x % (D / 2) * 2, c = d >> 3 & 7;
+    const uint32_t at = tile + uint32_t((d >> 6) * BOX + r * 128 + ((c ^ (r & 7)) << 4) + (d & 7) * 2);
+    uint32_t w;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+    const bool lo = (w & 0x7FFFu) > 0x7C00u, hi = (w & 0x7FFF0000u) > 0x7C000000u;
+    if (lo) atomicMin(nan_at + d, tok0 + r - row0);
+    if (hi) atomicMin(nan_at + d + 1, tok0 + r - row0);
+    if (lo | hi) {
+      w &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0xFFFFu : 0xFFFFFFFFu);
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
+    }
+  }
+  __syncwarp();
+}
+
 // Scores from the row's limit on become -infinity.
 __device__ __forceinline__ void mask(uint32_t (&v)[32], int vis) {
   if (vis < 32) {
@@ -226,7 +268,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   const uint32_t smem = smem_u32(smem_raw);
   Side& sd = *reinterpret_cast<Side*>(smem_raw + L::BARS);
   Bars* bars = &sd.bars;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // a reduction over the warp: the result is known to be the same in all lanes
+  const int tid = threadIdx.x, lane = tid & 31, warp = int(__reduce_max_sync(0xffffffffu, uint32_t(tid) >> 5));
   volatile uint32_t* abort = &bars->abort;
   const KvBatch& b = p.b;
   const uint64_t tmo = p.timeout_ns;
@@ -249,7 +292,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   }
   if (lane == 31) sd.warp_sum[warp] = before;
   if (tid == 0) {
-    mbar_init(&bars->q_full, 8);
+    mbar_init(&bars->q_full, CONV);
     mbar_init(&bars->q_empty, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
@@ -258,11 +301,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       mbar_init(&bars->o_empty[x], 4);
     }
     for (int i = 0; i < KST; ++i) {
-      mbar_init(&bars->k_full[i], 4);
+      mbar_init(&bars->k_full[i], 8);  // groups of 16 tokens
       mbar_init(&bars->k_empty[i], 1);
     }
     for (int i = 0; i < VST; ++i) {
-      mbar_init(&bars->v_full[i], 4);
+      mbar_init(&bars->v_full[i], 8);
       mbar_init(&bars->v_empty[i], 1);
     }
     bars->abort = 0;
@@ -324,20 +367,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   g.nkv = unit_tiles(p, g.seq, seq_rows(p, g.seq), g.qb);
   g.t1 = min(g.nkv, g.t0 + g.left);
 
-  if (warp < WARP_SOFTMAX) {
-    // ---------------------------------------------------------------- conversion: warps 0-3 keys, 4-7 values
-    constexpr int PASS = D / 64;     // 16-code units of one thread and row
-    constexpr int GR = 4;            // rows of one thread and tile
-    const bool val = warp >= 4;
-    const int r8 = lane >> 2, u4 = lane & 3, w32 = (warp & 3) * 32;
-    const uint8_t* pool = val ? p.c.v : p.c.k;
-    const uint8_t* scale_at = val ? p.c.vs : p.c.ks;
-    uint64_t* full = val ? bars->v_full : bars->k_full;
-    uint64_t* empty = val ? bars->v_empty : bars->k_empty;
-    const uint32_t ring = smem + (val ? L::V : L::K);
-    const int stages = val ? VST : KST;
-    int st = 0;
-    uint32_t ph = 0;
+  if (warp < CONV) {
+    // ---------------------------------------------------------------- conversion, item by item
+    // Item n of a segment: keys and values of 16 tokens, group n % 8 of its tile n / 8.  Warp w takes items w,
+    // w + 7, ...; the next one's codes are on their way in registers.  (The loop is kept short: with the softmax and
+    // the issuing loop it has to live in the instruction cache; two or three items ahead measured slower.)
+    constexpr int PASS = D / 64;     // 16-code units of one thread and token
+    const int r8 = lane >> 2, u4 = lane & 3;
+    int before_seg = 0;              // tiles of earlier segments
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const int rows = seq_rows(p, g.seq);
@@ -347,7 +384,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       // the largest scales of the segment's pages
       const int tok_end = min(len, g.t1 * KV);
       int km = -127, vm = -127;
-      for (int pg = g.t0 * KV / p.c.ps + tid; pg * int64_t(p.c.ps) < tok_end; pg += 256) {
+      for (int pg = g.t0 * KV / p.c.ps + tid; pg * int64_t(p.c.ps) < tok_end; pg += CONV * 32) {
         const int page = __ldg(table + pg);
         if (page < 0 || page >= p.c.num_pages) {
           record_error(b.status, kKvInvalid, uint32_t(g.s), uint32_t(page), uint32_t(pg));
@@ -363,9 +400,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         sd.warp_max[warp][0] = km;
         sd.warp_max[warp][1] = vm;
       }
-      named_bar_sync(1, 256);
+      named_bar_sync(1, CONV * 32);
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
+      for (int w = 0; w < CONV; ++w) {
         km = max(km, sd.warp_max[w][0]);
         vm = max(vm, sd.warp_max[w][1]);
       }
@@ -375,46 +412,46 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         sd.kv_exp[i & 3][1] = vm;
       }
       if (tid < D) sd.nan_at[i & 3][tid] = 0x7FFFFFFF;
-      named_bar_sync(1, 256);
-      const int top = val ? vm : km;
+      named_bar_sync(1, CONV * 32);
 
-      // a tile's codes, on their way in registers
-      uint4 cw[GR * PASS];
-      int sb[2] = {0, 0};  // scale bytes of the warp's two groups of 16 tokens
-      int pages[2] = {-1, -1};
-      auto look_up = [&](int j) {
+      const int items = (g.t1 - g.t0) * 8;
+      const int64_t lane_off = int64_t(g.hk) * p.c.head_stride + int64_t(r8) * p.c.token_stride + u4 * 16;
+      const int64_t eight = 8 * p.c.token_stride;
+      uint4 ck[2 * PASS], cv[2 * PASS];  // tokens r8 and r8 + 8 of the item
+      int sk = 0, sv = 0, page = -1;     // its scale bytes; the page of the item to be loaded next
+      auto group = [&](int n) { return g.t0 * 8 + n; };                               // of 16 tokens, in the sequence
+      // gr / (page_size / 16)
+      auto page_of = [&](int gr) { return p.page_magic ? int(__umulhi(uint32_t(gr), p.page_magic)) : gr; };
+      auto look_up = [&](int n) {
+        const int gr = group(n);
+        int pg = -1;
+        if (n < items && gr * 16 < len) pg = __ldg(table + page_of(gr));
+        return pg < p.c.num_pages ? pg : -1;
+      };
+      auto load = [&](const uint8_t* pool, uint4(&c)[2 * PASS], int n) {
+        const int gr = group(n), slot = gr - page_of(gr) * (p.c.ps >> 4);
+        const uint8_t* at = pool + int64_t(page) * p.c.page_stride + int64_t(slot) * 2 * eight + lane_off;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int tok = j * KV + w32 + h * 16;
-          pages[h] = -1;
-          if (j < g.t1 && tok < len) {
-            const int page = __ldg(table + tok / p.c.ps);
-            if (page >= 0 && page < p.c.num_pages) pages[h] = page;
+        for (int y = 0; y < 2; ++y) {
+          const bool in = page >= 0 && gr * 16 + 8 * y + r8 < len;
+#pragma unroll
+          for (int u = 0; u < PASS; ++u) {
+            c[y * PASS + u] = make_uint4(0, 0, 0, 0);
+            if (in) c[y * PASS + u] = ld_codes(at + y * eight + u * 64);
           }
         }
       };
-      auto load = [&](int j) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int tok = j * KV + w32 + h * 16;
-          const uint8_t* at = pool + int64_t(max(pages[h], 0)) * p.c.page_stride + int64_t(g.hk) * p.c.head_stride +
-                              int64_t(tok % p.c.ps + r8) * p.c.token_stride + u4 * 16;
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const bool in = pages[h] >= 0 && tok + 8 * y + r8 < len;
-#pragma unroll
-            for (int u = 0; u < PASS; ++u) {
-              uint4& x = cw[(h * 2 + y) * PASS + u];
-              x = make_uint4(0, 0, 0, 0);
-              if (in) x = ld_codes(at + int64_t(8 * y) * p.c.token_stride + u * 64);
-            }
-          }
-          sb[h] = pages[h] < 0 ? 0 : scale_at[int64_t(pages[h]) * p.c.Hkv + g.hk];
-        }
+      auto load_scales = [&]() {
+        const int64_t at = int64_t(max(page, 0)) * p.c.Hkv + g.hk;
+        sk = p.c.ks[at];
+        sv = p.c.vs[at];
+        if (page < 0) sk = sv = 0;
       };
-      look_up(g.t0);
-      load(g.t0);
-      look_up(g.t0 + 1);
+      page = look_up(warp);
+      load(p.c.k, ck, warp);
+      load(p.c.v, cv, warp);
+      load_scales();
+      page = look_up(warp + CONV);
 
       // queries: a row to D/8 lanes
       ok = mbar_wait(&bars->q_empty, uint32_t(i & 1) ^ 1u, abort, b.status, tmo, 11);
@@ -423,11 +460,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         break;
       }
       {
-        constexpr int LPR = D / 8, RPP = 256 / LPR;  // lanes of a row, rows of a pass of the converting warps
-        const int c8 = tid % LPR;
-#pragma unroll 4
-        for (int r = tid / LPR; r < UNIT; r += RPP) {
-          const int row = g.qb * UNIT + r;
+        constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp
+        const int c8 = lane % LPR;
+#pragma unroll 10
+        for (int r0 = warp * RPW; r0 < UNIT; r0 += CONV * RPW) {
+          const int r = r0 + lane / LPR, row = g.qb * UNIT + r;
           uint4 w = make_uint4(0, 0, 0, 0);
           if (row < rows) {
             const int tk = row / p.group;
@@ -456,69 +493,44 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&bars->q_full);
       }
 
-      for (int j = g.t0; j < g.t1; ++j) {
-        uint32_t f[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          f[h] = block_factor(sb[h], top);
-          if (val && sb[h] == 255) {  // values of NaN: as codes, so that rows that do not see them can be spared
-            f[h] = 0x3C003C00u;
-#pragma unroll
-            for (int x = 2 * h; x < 2 * h + 2; ++x)
-              if (j * KV + w32 + x * 8 + r8 < len) {
-#pragma unroll
-                for (int u = 0; u < PASS; ++u) cw[x * PASS + u] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-              }
-          }
-        }
-        if (val && (j + 1) * KV > min_lim) {
-          uint32_t any = 0;
-#pragma unroll
-          for (int x = 0; x < GR * PASS; ++x)
-            any |= nan_bytes(cw[x].x) | nan_bytes(cw[x].y) | nan_bytes(cw[x].z) | nan_bytes(cw[x].w);
-          if (any) {
-#pragma unroll
-            for (int x = 0; x < GR * PASS; ++x) {
-              const int tok = j * KV + w32 + x / PASS * 8 + r8, d0 = (x % PASS * 4 + u4) * 16;
-              uint32_t c[4] = {cw[x].x, cw[x].y, cw[x].z, cw[x].w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t bad = nan_bytes(c[k]);
-                for (uint32_t left = bad; left; left &= left - 1)
-                  atomicMin(&sd.nan_at[i & 3][d0 + k * 4 + ((__ffs(left) - 1) >> 3)], tok);
-                c[k] &= ~((bad >> 7) * 0xFFu);
-              }
-              cw[x] = make_uint4(c[0], c[1], c[2], c[3]);
-            }
-          }
-        }
-        ok = mbar_wait(empty + st, ph ^ 1u, abort, b.status, tmo, 12);
+      for (int n = warp; n < items; n += CONV) {
+        const int count = before_seg + (n >> 3), kst = count % KST, vst = count % VST;
+        const uint32_t fk = block_factor(sk, km), fv = block_factor(sv, vm);
+        // the values' slot is free by then: P V of three tiles ago is issued before Q K of two tiles ago
+        ok = mbar_wait(bars->k_empty + kst, uint32_t(count / KST & 1) ^ 1u, abort, b.status, tmo, 12) &&
+             mbar_wait(bars->v_empty + vst, uint32_t(count / VST & 1) ^ 1u, abort, b.status, tmo, 13);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
-        const uint32_t tile = ring + uint32_t(st) * L::TILE;
+        const uint32_t ktile = smem + L::K + uint32_t(kst) * L::TILE, vtile = smem + L::V + uint32_t(vst) * L::TILE;
+        const int row0 = (n & 7) * 16;
 #pragma unroll
-        for (int x = 0; x < GR; ++x)
+        for (int x = 0; x < 2 * PASS; ++x) put16(ktile, row0 + x / PASS * 8 + r8, x % PASS * 4 + u4, ck[x], fk);
+        load(p.c.k, ck, n + CONV);
 #pragma unroll
-          for (int u = 0; u < PASS; ++u) put16(tile, w32 + x * 8 + r8, u * 4 + u4, cw[x * PASS + u], f[x >> 1]);
+        for (int x = 0; x < 2 * PASS; ++x) put16(vtile, row0 + x / PASS * 8 + r8, x % PASS * 4 + u4, cv[x], fv);
+        load(p.c.v, cv, n + CONV);
+        load_scales();
+        page = look_up(n + 2 * CONV);
+        if (group(n) * 16 + 16 > min_lim) spare_nan<D>(vtile, row0, group(n) * 16, sd.nan_at[i & 3]);
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full + st);
-        if (++st == stages) {
-          st = 0;
-          ph ^= 1u;
-        }
-        if (j + 1 < g.t1) {
-          load(j + 1);
-          look_up(j + 2);
+        if (lane == 0) {
+          mbar_arrive(bars->k_full + kst);
+          mbar_arrive(bars->v_full + vst);
         }
       }
+      before_seg += g.t1 - g.t0;
       if (!ok || !seg_next(p, g)) break;
     }
   } else if (warp == WARP_MMA) {
-    if (lane == 0) {
-      // ---------------------------------------------------------------- the issuing thread
+    // ---------------------------------------------------------------- the issuing warp
+    {
+      const uint32_t leader = lane == 0, tmem = __reduce_max_sync(0xffffffffu, tmem_base);
+      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t tag) {
+        return __reduce_min_sync(0xffffffffu, uint32_t(mbar_wait(bar, parity, abort, b.status, tmo, tag))) != 0;
+      };
       int ks = 0, vs = 0;
       uint32_t kph = 0, vph = 0;
       uint32_t pcount[2] = {0, 0};
@@ -528,32 +540,33 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       bool ok = true;
       for (int i = 0; ok; ++i) {
         const uint32_t uph = uint32_t(i & 1);
-        ok = mbar_wait(&bars->q_full, uph, abort, b.status, tmo, 21) &&
-             mbar_wait(&bars->k_full[ks], kph, abort, b.status, tmo, 22);
+        ok = wait(&bars->q_full, uph, 21) &&
+             wait(&bars->k_full[ks], kph, 22);
         if (!ok) break;
         tc_fence_after();
-        const int said = *reinterpret_cast<volatile int32_t*>(&sd.tiles[i & 3]), tiles = said < 0 ? -said : said;
+        const int said = int(__reduce_max_sync(0xffffffffu, uint32_t(*reinterpret_cast<volatile int32_t*>(&sd.tiles[i & 3]))));
+        const int tiles = said < 0 ? -said : said;
         for (int X = 0; X < 2; ++X) {
-          issue_qk<D>(q0 + X * TSTEP, k0 + ks * TSTEP, tmem_base + X * 128);
-          tc_commit(&bars->s_full[X]);
+          issue_qk<D>(q0 + X * TSTEP, k0 + ks * TSTEP, tmem + X * 128, leader);
+          commit(&bars->s_full[X], leader);
         }
-        if (tiles == 1) tc_commit(&bars->q_empty);
-        tc_commit(&bars->k_empty[ks]);
+        if (tiles == 1) commit(&bars->q_empty, leader);
+        commit(&bars->k_empty[ks], leader);
         if (++ks == KST) {
           ks = 0;
           kph ^= 1u;
         }
         for (int j = 0; j < tiles && ok; ++j) {
-          if (!(ok = mbar_wait(&bars->v_full[vs], vph, abort, b.status, tmo, 23))) break;
+          if (!(ok = wait(&bars->v_full[vs], vph, 23))) break;
           for (int X = 0; X < 2; ++X) {
-            ok = mbar_wait(&bars->p_full[X], pcount[X] & 1u, abort, b.status, tmo, 24);
+            ok = wait(&bars->p_full[X], pcount[X] & 1u, 24);
             ++pcount[X];
-            if (ok && j == 0) ok = mbar_wait(&bars->o_empty[X], uph ^ 1u, abort, b.status, tmo, 25);
+            if (ok && j == 0) ok = wait(&bars->o_empty[X], uph ^ 1u, 25);
             if (!ok) break;
             tc_fence_after();
-            issue_pv<D>(tmem_base + X * 128, v0 + vs * TSTEP, tmem_base + 256 + X * 128, j > 0);
+            issue_pv<D>(tmem + X * 128, v0 + vs * TSTEP, tmem + 256 + X * 128, j > 0, leader);
             if (X == 1) {
-              tc_commit(&bars->v_empty[vs]);
+              commit(&bars->v_empty[vs], leader);
               if (++vs == VST) {
                 vs = 0;
                 vph ^= 1u;
@@ -561,21 +574,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
             }
             if (j + 1 < tiles) {
               if (X == 0) {
-                if (!(ok = mbar_wait(&bars->k_full[ks], kph, abort, b.status, tmo, 26))) break;
+                if (!(ok = wait(&bars->k_full[ks], kph, 26))) break;
                 tc_fence_after();
               }
-              issue_qk<D>(q0 + X * TSTEP, k0 + ks * TSTEP, tmem_base + X * 128);
-              tc_commit(&bars->s_full[X]);
+              issue_qk<D>(q0 + X * TSTEP, k0 + ks * TSTEP, tmem + X * 128, leader);
+              commit(&bars->s_full[X], leader);
               if (X == 1) {
-                if (j + 2 == tiles) tc_commit(&bars->q_empty);
-                tc_commit(&bars->k_empty[ks]);
+                if (j + 2 == tiles) commit(&bars->q_empty, leader);
+                commit(&bars->k_empty[ks], leader);
                 if (++ks == KST) {
                   ks = 0;
                   kph ^= 1u;
                 }
               }
             } else {
-              tc_commit(&bars->o_full[X]);
+              commit(&bars->o_full[X], leader);
             }
           }
         }
@@ -616,7 +629,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         const int vis = lim - j * KV;
         uint32_t va[32], vb[32];
         float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
         for (int half = 1; half >= 0; --half) {
           tmem_ld_32cols(s_addr + uint32_t(half * 64), va);
           tmem_ld_32cols(s_addr + uint32_t(half * 64 + 32), vb);
@@ -636,7 +649,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         const float add = m == -INFINITY ? kShift : kShift - m;
         float sq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         // P as fp16 pairs over the first 64 columns of S
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           if (half == 1) {
             if (j > g.t0 && __any_sync(0xffffffffu, resc)) {
@@ -690,8 +703,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const bool whole = g.t0 == 0 && g.t1 == g.nkv;
       const int tk = r / p.group, head = g.hk * p.group + r - tk * p.group;
       uint16_t* orow = p.out + (int64_t(g.seq.row0 + tk) * p.H + head) * D;
-      constexpr int64_t SLOT = 2 * ROWS * (D + 2);  // one segment's rows: D means, maximum, sum
-      float* mine_row = p.partial + (2 * int64_t(blockIdx.x) + (g.t0 == 0 ? 1 : 0)) * SLOT + int64_t(X * ROWS + row) * (D + 2);
+      // a segment's partial result: for each tile D means, maximum and sum, row next to row
+      constexpr int64_t SLOT = 2 * ROWS * (D + 2);
+      float* mine_row = p.partial + (2 * int64_t(blockIdx.x) + (g.t0 == 0 ? 1 : 0)) * SLOT + X * (D + 2) * ROWS + row;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -711,7 +725,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
                          pack_bf16x2(x[q * 8 + 4], x[q * 8 + 5]), pack_bf16x2(x[q * 8 + 6], x[q * 8 + 7]));
         } else {
 #pragma unroll
-          for (int q = 0; q < 16; ++q) __stcg(reinterpret_cast<float2*>(mine_row + c * 32) + q, make_float2(x[2 * q], x[2 * q + 1]));
+          for (int k = 0; k < 32; ++k) __stcg(mine_row + (c * 32 + k) * ROWS, x[k]);
         }
       }
       tc_fence_before();
@@ -722,7 +736,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           p.lse[int64_t(head) * b.n_tokens + g.seq.row0 + tk] =
               l == 0.0f ? -INFINITY : (m - kShift + log2f(l)) * 0.69314718055994531f;
       } else {
-        if (row_ok) __stcg(reinterpret_cast<float2*>(mine_row + D), make_float2(m, l));
+        if (row_ok) {
+          __stcg(mine_row + D * ROWS, m);
+          __stcg(mine_row + (D + 1) * ROWS, l);
+        }
         const int64_t t0 = sd.run0 + done - g.t0;
         const int64_t c0 = ((t0 + 1) * sd.ctas - 1) / sd.total, c1 = ((t0 + g.nkv) * sd.ctas - 1) / sd.total;
         __threadfence();
@@ -735,31 +752,31 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         named_bar_sync(2 + X, 128);
         if (sd.last[X] && row_ok) {
           __threadfence();
-          const float* rows_at = p.partial + int64_t(X * ROWS + row) * (D + 2);
+          const float* rows_at = p.partial + X * (D + 2) * ROWS + row;
           auto slot = [&](int64_t c) { return rows_at + (2 * c + (c == c0)) * SLOT; };
           float top = -INFINITY, sum = 0.0f;
-          for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(slot(c) + D));
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot(c) + D));
-            sum += ml.x == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - top);
-          }
+          for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(slot(c) + D * ROWS));
+          auto weight = [&](int64_t c) {
+            const float mc = __ldcg(slot(c) + D * ROWS), lc = __ldcg(slot(c) + (D + 1) * ROWS);
+            return mc == -INFINITY ? lc : lc * ex2_approx(mc - top);
+          };
+          for (int64_t c = c0; c <= c1; ++c) sum += weight(c);
           const float is = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll 1
-          for (int q = 0; q < D / 8; ++q) {
-            float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-            for (int64_t c = c0; c <= c1; ++c) {
-              const float* from = slot(c);
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + D));
-              const float wgt = (ml.x == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - top)) * is;
+          for (int q = 0; q < D / 32; ++q) {
+            float x[32];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 v2 = __ldcg(reinterpret_cast<const float2*>(from + q * 8) + k);
-                x[2 * k] = fmaf(wgt, v2.x, x[2 * k]);
-                x[2 * k + 1] = fmaf(wgt, v2.y, x[2 * k + 1]);
-              }
+            for (int k = 0; k < 32; ++k) x[k] = 0.0f;
+            for (int64_t c = c0; c <= c1; ++c) {
+              const float wgt = weight(c) * is;
+              const float* from = slot(c) + q * 32 * ROWS;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[k] = fmaf(wgt, __ldcg(from + k * ROWS), x[k]);
             }
-            st_global_v4(orow + q * 8, pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                         pack_bf16x2(x[6], x[7]));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              st_global_v4(orow + q * 32 + k * 8, pack_bf16x2(x[k * 8], x[k * 8 + 1]), pack_bf16x2(x[k * 8 + 2], x[k * 8 + 3]),
+                           pack_bf16x2(x[k * 8 + 4], x[k * 8 + 5]), pack_bf16x2(x[k * 8 + 6], x[k * 8 + 7]));
           }
           if (p.lse)
             p.lse[int64_t(head) * b.n_tokens + g.seq.row0 + tk] =
@@ -790,6 +807,9 @@ size_t prefill_counter_bytes(int ctas) { return (size_t(ctas) * 2 * 4 + 255) / 2
 size_t prefill_partial_bytes(int ctas, int D) { return size_t(ctas) * 2 * UNIT * (D + 2) * sizeof(float); }
 
 tl_status launch_kv_prefill(PrefillParams& p, int D, int ctas, cudaStream_t st) {
+  // floor(g / h) = floor(g m / 2^32), m = floor(2^32 / h) + 1, as long as g < 2^32 / h: g < 2^27, h <= 16
+  const uint32_t halves = uint32_t(p.c.ps) / 16;
+  p.page_magic = halves == 1 ? 0u : uint32_t((uint64_t(1) << 32) / halves) + 1;
   void* args[] = {&p};
   return D == 128 ? launch(reinterpret_cast<const void*>(&kv_prefill_kernel<128>), ctas, THREADS, smem_bytes<128>(), st,
                            args, false)

@@ -14,11 +14,12 @@ struct PrefillParams {
   uint16_t* out;
   float* lse;
   uint32_t* counters;  // [CTAs][2], zero between calls
-  float* partial;      // [CTAs][2][256][D + 2]
+  float* partial;      // [CTAs][2][2][D + 2][128]
   uint64_t timeout_ns;
   int32_t H, group, causal;
   int32_t min_rows;    // sequences of more query rows per kv head than this are this kernel's
   float scale_log2;
+  uint32_t page_magic; // groups of 16 tokens to pages: the upper half of a product with it (set by launch_kv_prefill)
 };
 
 size_t prefill_counter_bytes(int ctas);
