@@ -185,6 +185,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// Pairs of fp32 in one instruction: (x, y) = (a, b) * f + c, and (x, y) += (a, b).
+__device__ __forceinline__ void fma2(float a, float b, float f, float c, float& x, float& y) {
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmov.b64 r, {%5, %5};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(f), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -670,18 +683,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           }
           uint32_t w[32];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(va[2 * k]), f, add));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(va[2 * k + 1]), f, add));
-            sq[k & 3] += p0 + p1;
+          for (int k = 0; k < 32; ++k) {
+            const uint32_t* s = k < 16 ? &va[2 * k] : &vb[2 * k - 32];
+            float p0, p1;
+            fma2(__uint_as_float(s[0]), __uint_as_float(s[1]), f, add, p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            add2(sq[2 * (k & 1)], sq[2 * (k & 1) + 1], p0, p1);
             w[k] = pack_f16x2(p0, p1);
-          }
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(vb[2 * k]), f, add));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(vb[2 * k + 1]), f, add));
-            sq[k & 3] += p0 + p1;
-            w[16 + k] = pack_f16x2(p0, p1);
           }
           tmem_st_32cols(s_addr + uint32_t(half * 32), w);
         }

@@ -20,12 +20,14 @@
 //
 // Inside a CTA warp (group, kq) takes 64 columns (group 0: gate columns, group 1:
 // up columns; in the down launch the tile's two halves) and every fourth 32 rows of
-// the contraction.  Weights are row-major [K, N], the product wants pairs along K:
-// a lane copies (cp.async, 16 bytes) eight rows' eight columns into a ring of its
-// own and interleaves two rows' words with a byte permutation; since the order of
-// the contraction is free, those eight rows are also the eight consecutive elements
-// of a token that one 16-byte load brings for the other operand.  No barrier and no
-// transposition between memory and the tensor cores.
+// the contraction.  Weights are row-major [K, N], the product wants pairs along K: the
+// warp copies (cp.async) whole lines of 32 rows and 64 columns into a ring of its own,
+// a lane takes eight rows' eight columns from it and interleaves two rows' words with a
+// byte permutation; since the order of the contraction is free, those eight rows are
+// also the eight consecutive elements of a token that one 16-byte load brings for the
+// other operand.  No barrier and no transposition between memory and the tensor cores.
+// (Copies of single sectors, each lane fetching what it multiplies, ran at half the
+// rate.)
 //
 // h goes from launch to launch as two bf16 terms (16 bits of mantissa): the down
 // product takes one multiplication more for each, which the stream of weights
@@ -100,6 +102,8 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Where the 16 bytes `unit` of a step's weight row lie: a product's loads (unit g of rows 8t + const) meet in no bank.
+__device__ __forceinline__ uint32_t w_at(int row, int unit) { return uint32_t(row * 128 + ((unit ^ ((row >> 3) << 1)) << 4)); }
 __device__ __forceinline__ int merge_at(int r, int c) { return r * PITCH + (c ^ (((c >> 3) & 1) << 1)); }
 
 // ---------------------------------------------------------------- routing, by every CTA for itself
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
 
   auto open = [&]() {
     const int rt = f.unit % sm.tiles, ct = f.unit / sm.tiles;
-    const int col = DOWN ? ct * 128 + group * 64 + g * 8 : ct * 64 + g * 8;
+    const int col = DOWN ? ct * 128 + group * 64 + (lane & 7) * 8 : ct * 64 + (lane & 7) * 8;
     f_col = col < cols;
     f_w = static_cast<const uint16_t*>(p.w[sm.tile_expert[rt]]) + (f_col ? col + (DOWN ? 0 : group * p.I) : 0);
 #pragma unroll
@@ -273,12 +277,15 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
     f_open = true;
   };
   auto copy_w = [&](int stage) {
-    const int k0 = f.k * STEP + kq * 32 + t * 8;
-    const uint32_t dst = ring + uint32_t(stage * Smem::STAGE) + uint32_t(lane * 16);
-    const bool ok = f_col && k0 < K;
-    const uint16_t* src = f_w + (ok ? int64_t(k0) * ld : 0);
+    // whole 128-byte lines by eight neighbouring lanes, four rows an instruction
+    const int k0 = f.k * STEP + kq * 32 + (lane >> 3);
+    const uint32_t dst = ring + uint32_t(stage * Smem::STAGE);
+    const uint16_t* src = f_w + (f_col && k0 < K ? int64_t(k0) * ld : 0);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cp_async16z(dst + uint32_t(j * 512), src + (ok ? int64_t(j) * ld : 0), ok);
+    for (int j = 0; j < 8; ++j) {
+      const bool ok = f_col && k0 + j * 4 < K;
+      cp_async16z(dst + w_at((lane >> 3) + j * 4, lane & 7), src + (ok ? int64_t(j * 4) * ld : 0), ok);
+    }
   };
   auto copy_a = [&](int stage) {
     const int k0 = f.k * STEP + kq * 32 + t * 8;
@@ -353,7 +360,8 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
 
     for (int k = k_begin; k < k_end; ++k) {
       cp_wait<STAGES - 2>();
-      const uint32_t src = ring + uint32_t(stage * Smem::STAGE) + uint32_t(lane * 16);
+      __syncwarp();
+      const uint32_t src = ring + uint32_t(stage * Smem::STAGE);
       uint32_t a[MT][2][PLANES][4];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -361,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int q = 0; q < PLANES; ++q) {
-            const uint4 w = lds128(src + uint32_t(W_BYTES + ((m * 2 + h) * PLANES + q) * 512));
+            const uint4 w = lds128(src + uint32_t(W_BYTES + ((m * 2 + h) * PLANES + q) * 512 + lane * 16));
             a[m][h][q][0] = w.x;
             a[m][h][q][1] = w.y;
             a[m][h][q][2] = w.z;
@@ -372,7 +380,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
         uint32_t w[4][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint4 v = lds128(src + uint32_t((u * 4 + j) * 512));
+          const uint4 v = lds128(src + w_at(t * 8 + u * 4 + j, g));
           w[j][0] = v.x;
           w[j][1] = v.y;
           w[j][2] = v.z;
