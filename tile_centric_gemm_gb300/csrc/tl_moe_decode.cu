@@ -48,7 +48,6 @@ constexpr int STEP = 128;            // contraction of one step: 32 for each of 
 constexpr int MAX_T = 64, MAX_K = 16, MAX_ROWS = MAX_T * MAX_K;
 constexpr int MAX_CTAS = 256;
 constexpr int W_BYTES = 32 * 128;    // one warp's weights of one step: 32 rows of 64 columns
-constexpr int PITCH = 17;            // 16-byte units of one row of the merge buffers
 
 struct MoeParams {
   const void* w[TL_MAX_EXPERTS];
@@ -69,8 +68,7 @@ struct MoeSmem {
   static constexpr int PLANES = DOWN ? 2 : 1;
   static constexpr int STAGE = W_BYTES + PLANES * MT * 1024;
   static constexpr int STAGES = (24 * 1024) / STAGE;
-  uint8_t ring[WARPS][STAGES][STAGE];
-  float4 merge[4][TILE * PITCH];
+  uint8_t ring[WARPS][STAGES][STAGE];  // a tile's merge takes the stage that each warp used last
   unsigned long long mask[TL_MAX_EXPERTS];  // the tokens that chose the expert
   float gates[MAX_T][MAX_K];
   uint16_t row_of[MAX_T][MAX_K];            // sorted row of (token, slot)
@@ -104,7 +102,8 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 }
 // Where the 16 bytes `unit` of a step's weight row lie: a product's loads (unit g of rows 8t + const) meet in no bank.
 __device__ __forceinline__ uint32_t w_at(int row, int unit) { return uint32_t(row * 128 + ((unit ^ ((row >> 3) << 1)) << 4)); }
-__device__ __forceinline__ int merge_at(int r, int c) { return r * PITCH + (c ^ (((c >> 3) & 1) << 1)); }
+// 16-byte unit c of row r of a warp's 16 x 64 sums
+__device__ __forceinline__ int merge_at(int r, int c) { return r * 16 + (c ^ (r & 1) ^ ((c >> 3) << 1)); }
 
 // ---------------------------------------------------------------- routing, by every CTA for itself
 // Order of the logits as unsigned keys: larger first, NaN (1) below -infinity, 0 = taken.
@@ -114,39 +113,41 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-template <class Smem>
-__device__ void route(const MoeParams& p, Smem& sm, int rows_per_tile, bool write) {
-  constexpr int J = TL_MAX_EXPERTS / 32;
-  const int warp = int(warp_id()), lane = int(lane_id());
-  for (int e = threadIdx.x; e < p.E; e += THREADS) sm.mask[e] = 0;
-  __syncthreads();
-  const int mine = (p.E + 31) / 32;
-  for (int t = warp; t < p.T; t += WARPS) {
-    float v[J];
-    uint32_t key[J];
-    float top = -INFINITY;
+// One warp selects for N tokens at once (their chains of reductions overlap); J: experts of a lane.
+template <int J, int N, class Smem>
+__device__ __forceinline__ void select(const MoeParams& p, Smem& sm, int t0, int step, bool write) {
+  const int lane = int(lane_id());
+  float v[N][J], top[N], chosen[N];
+  uint32_t key[N][J];
+  int chosen_e[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int t = min(t0 + i * step, p.T - 1);
+    top[i] = chosen[i] = -INFINITY;
+    chosen_e[i] = 0;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int e = j * 32 + lane;
-      v[j] = -INFINITY;
-      key[j] = 0;
-      if (j < mine && e < p.E) {
-        v[j] = p.logits[int64_t(t) * p.E + e];
-        key[j] = logit_key(v[j]);
+      v[i][j] = -INFINITY;
+      key[i][j] = 0;
+      if (e < p.E) {
+        v[i][j] = p.logits[int64_t(t) * p.E + e];
+        key[i][j] = logit_key(v[i][j]);
       }
     }
-    float chosen = -INFINITY;  // lane s: the logit in slot s
-    int chosen_e = 0;
-    for (int s = 0; s < p.topk; ++s) {
+  }
+  for (int s = 0; s < p.topk; ++s) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
       uint32_t best = 0;
       int at = 0x7FFFFFFF;
       float val = 0.0f;
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (j < mine && key[j] > best) {
-          best = key[j];
+        if (key[i][j] > best) {
+          best = key[i][j];
           at = j * 32 + lane;
-          val = v[j];
+          val = v[i][j];
         }
       const uint32_t most = __reduce_max_sync(0xffffffffu, best);
       const int e = __reduce_min_sync(0xffffffffu, best == most ? at : 0x7FFFFFFF);
@@ -154,34 +155,50 @@ __device__ void route(const MoeParams& p, Smem& sm, int rows_per_tile, bool writ
       if (lane == (e & 31)) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
-          if (j == e >> 5) key[j] = 0;
+          if (j == e >> 5) key[i][j] = 0;
       }
       if (lane == s) {
-        chosen = val;
-        chosen_e = e;
+        chosen[i] = val;
+        chosen_e[i] = e;
       }
-      if (s == 0) top = val;
+      if (s == 0) top[i] = val;
     }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int t = t0 + i * step;
     float sum = 0.0f;
     if (p.normalize) {
-      if (lane < p.topk) sum = expf(chosen - top);
+      if (lane < p.topk) sum = expf(chosen[i] - top[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (j < mine && j * 32 + lane < p.E) sum += expf(v[j] - top);
+        if (j * 32 + lane < p.E) sum += expf(v[i][j] - top[i]);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane < p.topk) {
-      const float gate = top == -INFINITY && !(sum > 0.0f) ? 0.0f : expf(chosen - top) / sum;
-      sm.ids[t][lane] = uint8_t(chosen_e);
+    if (lane < p.topk && t < p.T) {
+      const float gate = top[i] == -INFINITY && !(sum > 0.0f) ? 0.0f : expf(chosen[i] - top[i]) / sum;
+      sm.ids[t][lane] = uint8_t(chosen_e[i]);
       sm.gates[t][lane] = gate;
-      atomicOr(&sm.mask[chosen_e], 1ull << t);
+      atomicOr(&sm.mask[chosen_e[i]], 1ull << t);
       if (write) {
-        p.ids[t * p.topk + lane] = chosen_e;
+        p.ids[t * p.topk + lane] = chosen_e[i];
         p.gates[t * p.topk + lane] = gate;
       }
     }
+  }
+}
+
+template <class Smem>
+__device__ void route(const MoeParams& p, Smem& sm, int rows_per_tile, bool write) {
+  const int warp = int(warp_id()), lane = int(lane_id());
+  for (int e = threadIdx.x; e < p.E; e += THREADS) sm.mask[e] = 0;
+  __syncthreads();
+  if (p.E <= 64) {
+    for (int t = warp; t < p.T; t += 4 * WARPS) select<2, 4>(p, sm, t, WARPS, write);
+  } else {
+    for (int t = warp; t < p.T; t += WARPS) select<TL_MAX_EXPERTS / 32, 1>(p, sm, t, WARPS, write);
   }
   __syncthreads();
   if (warp == 0) {
@@ -234,7 +251,9 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
   if (!DOWN) pdl_launch_dependents();
   route(p, sm, MT * TILE, !DOWN && blockIdx.x == 0);
 
-  // the list of steps: (column tile, row tile, step); this CTA's run
+  // the list of steps; this CTA's run.  Up: (row tile, column tile, step), so that neighbouring column tiles are read
+  // at about the same time and a line that two of them share (rows that are no multiple of 128 bytes) is read from
+  // memory once.  Down: (column tile, row tile, step), so that column tiles are combined as the launch goes on.
   const int K = DOWN ? p.I : p.H;                      // contraction
   const int cols = DOWN ? p.Hd : p.I;                  // columns of one group's matrix
   const int ld = DOWN ? p.Hd : 2 * p.I;                // weights' row length
@@ -249,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
   // ---------------------------------------------------------------- copies of one warp: a cursor over the run
   const uint32_t ring = smem_u32(sm.ring[warp]);
   struct Cursor {
-    int unit, k;  // unit = column tile * row tiles + row tile
+    int unit, k;
   };
   Cursor f{int(run0 / ks), int(run0 % ks)};
   int64_t f_left = run1 - run0;
@@ -261,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
   const int64_t plane = int64_t(p.T) * p.topk * p.I;
 
   auto open = [&]() {
-    const int rt = f.unit % sm.tiles, ct = f.unit / sm.tiles;
+    const int rt = DOWN ? f.unit % sm.tiles : f.unit / col_tiles, ct = DOWN ? f.unit / sm.tiles : f.unit % col_tiles;
     const int col = DOWN ? ct * 128 + group * 64 + (lane & 7) * 8 : ct * 64 + (lane & 7) * 8;
     f_col = col < cols;
     f_w = static_cast<const uint16_t*>(p.w[sm.tile_expert[rt]]) + (f_col ? col + (DOWN ? 0 : group * p.I) : 0);
@@ -348,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
   while (at < run1) {
     const int unit = int(at / ks), k_begin = int(at % ks);
     const int k_end = int(min(int64_t(ks), k_begin + (run1 - at)));
-    const int rt = unit % sm.tiles, ct = unit / sm.tiles;
+    const int rt = DOWN ? unit % sm.tiles : unit / col_tiles, ct = DOWN ? unit / sm.tiles : unit % col_tiles;
     const int rows = sm.tile_rows[rt], row0 = sm.tile_first[rt];
     float acc[MT][8][4];
 #pragma unroll
@@ -451,37 +470,38 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
         if (col + 64 < p.Hd) st_global_cg_v4f(dst + 64, v[4], v[5], v[6], v[7]);
       }
     };
+    const int spare = stage == 0 ? STAGES - 1 : stage - 1;  // the stage that the warp's next copy will fill: all warps' alike
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       if (m > 0 && rows <= m * TILE) break;
-      __syncthreads();  // the merge buffers are free
-      auto each_unit = [&](auto&& fn) {
+      if (m > 0) __syncthreads();
+      float4* buf = reinterpret_cast<float4*>(sm.ring[warp][spare]);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i4 = 0; i4 < 2; ++i4)
-              fn(merge_at(g + 8 * x, 4 * t + 2 * h + i4), acc[m][4 * i4][2 * x + h], acc[m][4 * i4 + 1][2 * x + h],
-                 acc[m][4 * i4 + 2][2 * x + h], acc[m][4 * i4 + 3][2 * x + h]);
-      };
-      float4* buf = sm.merge[group * 2 + (kq & 1)];
-      if (kq >= 2) each_unit([&](int i, float a, float b, float c, float d) { buf[i] = make_float4(a, b, c, d); });
-      __syncthreads();
-      if (kq < 2)
-        each_unit([&](int i, float a, float b, float c, float d) {
-          const float4 w = buf[i];
-          buf[i] = make_float4(w.x + a, w.y + b, w.z + c, w.w + d);
-        });
+          for (int i4 = 0; i4 < 2; ++i4)
+            buf[merge_at(g + 8 * x, 4 * t + 2 * h + i4)] =
+                make_float4(acc[m][4 * i4][2 * x + h], acc[m][4 * i4 + 1][2 * x + h], acc[m][4 * i4 + 2][2 * x + h],
+                            acc[m][4 * i4 + 3][2 * x + h]);
       __syncthreads();
       float v[8];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const float4 a = sm.merge[2 * q][merge_at(row, c4)], b = sm.merge[2 * q + 1][merge_at(row, c4)];
-        v[4 * q] = a.x + b.x;
-        v[4 * q + 1] = a.y + b.y;
-        v[4 * q + 2] = a.z + b.z;
-        v[4 * q + 3] = a.w + b.w;
+        float4 a = reinterpret_cast<const float4*>(sm.ring[4 * q][spare])[merge_at(row, c4)];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+          const float4 b = reinterpret_cast<const float4*>(sm.ring[4 * q + w][spare])[merge_at(row, c4)];
+          a.x += b.x;
+          a.y += b.y;
+          a.z += b.z;
+          a.w += b.w;
+        }
+        v[4 * q] = a.x;
+        v[4 * q + 1] = a.y;
+        v[4 * q + 2] = a.z;
+        v[4 * q + 3] = a.w;
       }
       if (whole) {
         finish(m, v);
@@ -542,14 +562,20 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
           const int tok = i >> 5, col = ct * 128 + (i & 31) * 4;
           if (col >= p.Hd) continue;
           float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-          for (int s = 0; s < p.topk; ++s) {
-            const float gate = sm.gates[tok][s];
-            const float4 w = ld_global_cg_v4f(p.y + int64_t(sm.row_of[tok][s]) * p.Hd + col);
-            o[0] = fmaf(gate, w.x, o[0]);
-            o[1] = fmaf(gate, w.y, o[1]);
-            o[2] = fmaf(gate, w.z, o[2]);
-            o[3] = fmaf(gate, w.w, o[3]);
+          for (int s0 = 0; s0 < p.topk; s0 += 8) {
+            float4 w[8];
+#pragma unroll
+            for (int s = 0; s < 8; ++s)  // all on their way at once
+              w[s] = ld_global_cg_v4f(p.y + int64_t(sm.row_of[tok][min(s0 + s, p.topk - 1)]) * p.Hd + col);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+              if (s0 + s >= p.topk) break;
+              const float gate = sm.gates[tok][s0 + s];
+              o[0] = fmaf(gate, w[s].x, o[0]);
+              o[1] = fmaf(gate, w[s].y, o[1]);
+              o[2] = fmaf(gate, w[s].z, o[2]);
+              o[3] = fmaf(gate, w[s].w, o[3]);
+            }
           }
           *reinterpret_cast<uint2*>(p.out + int64_t(tok) * p.Hd + col) =
               make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
@@ -557,6 +583,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
       }
     }
     at += k_end - k_begin;
+    __syncthreads();  // the spare stages are free again
   }
   cp_wait<0>();
 }
