@@ -708,7 +708,8 @@ typedef struct tl_kv_attn_args {
   const int32_t* seq_lens;     /* device int32 [B] */
   const int32_t* page_table;   /* device int32 [B, max_pages] */
   void* workspace;             /* device scratch, 16-byte aligned, zeroed before its first use; left ready for
-                                  the next call by every call.  Calls sharing it must not run concurrently. */
+                                  the next call, of any sizes, by every call.  Calls sharing it must not run
+                                  concurrently. */
   size_t workspace_bytes;      /* >= tl_kv_attn_workspace_size(n_tokens, B, H, H_kv, head_dim, 0) */
   tl_signals* signals;         /* receives device-side errors in its status word (any size >= 1) */
 } tl_kv_attn_args;
@@ -731,7 +732,7 @@ tl_status tl_kv_attn(const tl_kv_attn_args* args, void* stream);
  * Every product is summed in fp32; h is kept to 16 bits of mantissa (two bf16
  * terms).  The weights of an expert that no token chose are not read.
  * Two stream-ordered launches, the second set up while the first runs
- * (programmatic dependent launch).  Deterministic.  Beyond 64 tokens
+ * (programmatic dependent launch).  Deterministic.  Hd up to 65536.  Beyond 64 tokens
  * tl_moe_ag_gemm and tl_moe_down are the calls.
  */
 typedef struct tl_moe_decode_args {
@@ -751,7 +752,8 @@ typedef struct tl_moe_decode_args {
   int32_t* ids;                /* device int32 [T, topk], written */
   float* gates;                /* device float [T, topk], written */
   void* workspace;             /* device scratch, 16-byte aligned, zeroed before its first use; left ready for
-                                  the next call by every call.  Calls sharing it must not run concurrently. */
+                                  the next call, of any sizes, by every call.  Calls sharing it must not run
+                                  concurrently. */
   size_t workspace_bytes;      /* >= tl_moe_decode_workspace_size(T, topk, E, H, I, Hd) */
 } tl_moe_decode_args;
 

@@ -256,6 +256,15 @@ def test_same_bits_again_on_a_stream_and_in_a_graph(B, q):
         assert torch.equal(c.out, first)
 
 
+def test_one_workspace_for_many_calls(B):
+    calls = [Call(B, Batch(q, n, seed=21, **LAYOUTS[i])) for i, q, n in
+             ((0, [1, 1], [900, 30]), (1, [200, 3], [500, 400]), (0, [300], [1500]), (4, [2] * 9, [77] * 9), (1, [1], [3000]))]
+    ws = max((c.ws for c in calls), key=lambda w: w.numel()).clone()
+    for c in calls + calls[::-1]:
+        c.ws = ws
+        c.run().check()
+
+
 def test_offsets_past_32_bits(B):
     """A pool of more than 4 GiB, the sequence's pages at its far end."""
     D, ps = 128, 256

@@ -745,7 +745,9 @@ tl_status launch_decode(void** args, int ctas, cudaStream_t st, bool early) {
 }
 
 // ---------------------------------------------------------------- workspace: counters, then partial tiles
-size_t counters_bytes(int ctas) { return (size_t(ctas) * 4 + 255) / 256 * 256; }
+// The counters of both kernels come first, in a place that does not depend on the sizes: one workspace may serve
+// calls of many.
+size_t counters_bytes(int ctas) { return (size_t(ctas) * 3 * 4 + 255) / 256 * 256; }
 size_t decode_partial_bytes(int ctas, int D) { return size_t(ctas) * 2 * (MAX_TILE * D + 2 * MAX_TILE) * sizeof(float); }
 
 }  // namespace
@@ -761,7 +763,7 @@ extern "C" size_t tl_kv_attn_workspace_size(int n_tokens, int B, int H, int H_kv
     sm_count = di.sm_count;
   }
   size_t bytes = counters_bytes(sm_count) + decode_partial_bytes(sm_count, head_dim);
-  if (int64_t(n_tokens) * (H / H_kv) > FEW_ROWS) bytes += prefill_counter_bytes(sm_count) + prefill_partial_bytes(sm_count, head_dim);
+  if (int64_t(n_tokens) * (H / H_kv) > FEW_ROWS) bytes += prefill_partial_bytes(sm_count, head_dim);
   return bytes;
 }
 
@@ -826,9 +828,8 @@ extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
     f.q_hs = p.q_hs;
     f.out = p.out;
     f.lse = p.lse;
-    uint8_t* at = static_cast<uint8_t*>(a->workspace) + counters_bytes(di.sm_count) + decode_partial_bytes(di.sm_count, c.head_dim);
-    f.counters = reinterpret_cast<uint32_t*>(at);
-    f.partial = reinterpret_cast<float*>(at + prefill_counter_bytes(di.sm_count));
+    f.counters = p.counters + di.sm_count;
+    f.partial = p.partial + decode_partial_bytes(di.sm_count, c.head_dim) / sizeof(float);
     f.timeout_ns = 3 * kDefaultTimeoutNs;
     f.H = a->H;
     f.group = p.group;

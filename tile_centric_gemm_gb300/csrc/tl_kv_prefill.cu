@@ -812,7 +812,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
 
 }  // namespace
 
-size_t prefill_counter_bytes(int ctas) { return (size_t(ctas) * 2 * 4 + 255) / 256 * 256; }
 size_t prefill_partial_bytes(int ctas, int D) { return size_t(ctas) * 2 * UNIT * (D + 2) * sizeof(float); }
 
 tl_status launch_kv_prefill(PrefillParams& p, int D, int ctas, cudaStream_t st) {

@@ -22,7 +22,6 @@ struct PrefillParams {
   uint32_t page_magic; // groups of 16 tokens to pages: the upper half of a product with it (set by launch_kv_prefill)
 };
 
-size_t prefill_counter_bytes(int ctas);
 size_t prefill_partial_bytes(int ctas, int D);
 tl_status launch_kv_prefill(PrefillParams& p, int D, int ctas, cudaStream_t st);
 

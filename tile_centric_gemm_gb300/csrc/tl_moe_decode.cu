@@ -18,9 +18,10 @@
 // its CTAs take the SMs that become free, work out the routing and fill their
 // rings with W2 before they wait for the first launch's results.
 //
-// Inside a CTA warp (group, kq) takes 64 columns (group 0: gate columns, group 1:
-// up columns; in the down launch the tile's two halves) and every fourth 32 rows of
-// the contraction.  Weights are row-major [K, N], the product wants pairs along K: the
+// Inside a CTA warp (group, sub, kq) takes 64 columns (group 0: gate columns, group 1:
+// up columns; in the down launch the tile's two halves) and, where the tile is narrow,
+// its share of the rows: every row's strips lie next to one another, so that lines are
+// read whole whatever the row length.  Weights are row-major [K, N], the product wants pairs along K: the
 // warp copies (cp.async) whole lines of 32 rows and 64 columns into a ring of its own,
 // a lane takes eight rows' eight columns from it and interleaves two rows' words with a
 // byte permutation; since the order of the contraction is free, those eight rows are
@@ -44,9 +45,9 @@ namespace {
 constexpr int WARPS = 8;
 constexpr int THREADS = WARPS * 32;
 constexpr int TILE = 16;             // rows of one product
-constexpr int STEP = 128;            // contraction of one step: 32 for each of four warps
 constexpr int MAX_T = 64, MAX_K = 16, MAX_ROWS = MAX_T * MAX_K;
 constexpr int MAX_CTAS = 256;
+constexpr int MAX_HD = 65536;
 constexpr int W_BYTES = 32 * 128;    // one warp's weights of one step: 32 rows of 64 columns
 
 struct MoeParams {
@@ -58,9 +59,10 @@ struct MoeParams {
   float* gates;
   uint16_t* act;        // [2][P][I]: the two terms of h, expert-sorted rows
   float* y;             // [P][Hd]
-  float* partial;       // [CTAs][2][MT * TILE][128]
-  uint32_t* counters;   // [MAX_CTAS] runs of launch 1, [MAX_CTAS] of launch 2, then one for each column tile
+  float* partial;       // [CTAs][2][slot_rows][128 * SUB]
+  uint32_t* counters;   // [MAX_CTAS] runs of launch 1, [MAX_CTAS] of launch 2, then one for each column tile and token
   int32_t T, H, I, Hd, E, topk, normalize;
+  int32_t slot_rows;    // rows that a tile can have
 };
 
 template <bool DOWN, int MT>
@@ -78,6 +80,7 @@ struct MoeSmem {
   uint8_t tile_rows[TL_MAX_EXPERTS + MAX_ROWS / TILE];
   uint8_t ids[MAX_T][MAX_K];
   uint8_t row_token[MAX_ROWS];
+  int16_t ready[2 * TILE];                  // the tile's tokens that are complete, or -1
   int32_t tiles, last;
 };
 
@@ -240,14 +243,17 @@ __device__ void route(const MoeParams& p, Smem& sm, int rows_per_tile, bool writ
 }
 
 // ---------------------------------------------------------------- one launch: up (DOWN = false) or down
-template <bool DOWN, int MT>
+// SUB: 64-column strips of a group that lie next to one another; 4 / SUB warps share a strip's contraction
+template <bool DOWN, int MT, int SUB>
 __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_constant__ MoeParams p) {
   using Smem = MoeSmem<DOWN, MT>;
   constexpr int STAGES = Smem::STAGES, PLANES = Smem::PLANES;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int group = warp >> 2, kq = warp & 3;
+  constexpr int KQ = 4 / SUB, STEP = 32 * KQ;    // rows of the contraction in one step
+  constexpr int WIDE = (DOWN ? 128 : 64) * SUB;  // columns of a tile
+  const int group = warp >> 2, sub = (warp & 3) / KQ, kq = warp % KQ;
   if (!DOWN) pdl_launch_dependents();
   route(p, sm, MT * TILE, !DOWN && blockIdx.x == 0);
 
@@ -257,7 +263,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
   const int K = DOWN ? p.I : p.H;                      // contraction
   const int cols = DOWN ? p.Hd : p.I;                  // columns of one group's matrix
   const int ld = DOWN ? p.Hd : 2 * p.I;                // weights' row length
-  const int col_tiles = DOWN ? (cols + 127) / 128 : (cols + 63) / 64;
+  const int col_tiles = (cols + WIDE - 1) / WIDE;
   const int ks = (K + STEP - 1) / STEP;
   const int64_t total = int64_t(col_tiles) * sm.tiles * ks;
   const int64_t n = min(int64_t(gridDim.x), max(int64_t(1), total / 2));
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
 
   auto open = [&]() {
     const int rt = DOWN ? f.unit % sm.tiles : f.unit / col_tiles, ct = DOWN ? f.unit / sm.tiles : f.unit % col_tiles;
-    const int col = DOWN ? ct * 128 + group * 64 + (lane & 7) * 8 : ct * 64 + (lane & 7) * 8;
+    const int col = ct * WIDE + ((DOWN ? group * SUB : 0) + sub) * 64 + (lane & 7) * 8;
     f_col = col < cols;
     f_w = static_cast<const uint16_t*>(p.w[sm.tile_expert[rt]]) + (f_col ? col + (DOWN ? 0 : group * p.I) : 0);
 #pragma unroll
@@ -437,13 +443,14 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
     const bool whole = k_begin == 0 && k_end == ks;
     const int64_t t0 = at - k_begin;
     const int row = tid >> 4, c4 = tid & 15;
-    float* slot = p.partial + (2 * cta + (k_begin == 0 ? 1 : 0)) * int64_t(MT * TILE * 128);
-    // four columns of each group: [0..3] group 0, [4..7] group 1, at column 4 c4 of the group
-    auto finish = [&](int m, const float(&v)[8]) {
+    const int64_t slot_size = int64_t(p.slot_rows) * (128 * SUB);
+    float* slot = p.partial + (2 * cta + (k_begin == 0 ? 1 : 0)) * slot_size;
+    // four columns of each group: [0..3] group 0, [4..7] group 1, at column 4 c4 of strip s
+    auto finish = [&](int m, int s, const float(&v)[8]) {
       const int r = m * TILE + row;
       if (r >= rows) return;
       if (!DOWN) {
-        const int col = ct * 64 + 4 * c4;
+        const int col = ct * WIDE + s * 64 + 4 * c4;
         if (col >= p.I) return;
         uint32_t hi[2], lo[2];
 #pragma unroll
@@ -464,10 +471,10 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
         *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
         *reinterpret_cast<uint2*>(dst + plane) = make_uint2(lo[0], lo[1]);
       } else {
-        const int col = ct * 128 + 4 * c4;
+        const int col = ct * WIDE + s * 64 + 4 * c4;
         float* dst = p.y + int64_t(row0 + r) * p.Hd + col;
         if (col < p.Hd) st_global_cg_v4f(dst, v[0], v[1], v[2], v[3]);
-        if (col + 64 < p.Hd) st_global_cg_v4f(dst + 64, v[4], v[5], v[6], v[7]);
+        if (col + SUB * 64 < p.Hd) st_global_cg_v4f(dst + SUB * 64, v[4], v[5], v[6], v[7]);
       }
     };
     const int spare = stage == 0 ? STAGES - 1 : stage - 1;  // the stage that the warp's next copy will fill: all warps' alike
@@ -486,29 +493,32 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
                 make_float4(acc[m][4 * i4][2 * x + h], acc[m][4 * i4 + 1][2 * x + h], acc[m][4 * i4 + 2][2 * x + h],
                             acc[m][4 * i4 + 3][2 * x + h]);
       __syncthreads();
-      float v[8];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float4 a = reinterpret_cast<const float4*>(sm.ring[4 * q][spare])[merge_at(row, c4)];
+      for (int s = 0; s < SUB; ++s) {
+        float v[8];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) {
-          const float4 b = reinterpret_cast<const float4*>(sm.ring[4 * q + w][spare])[merge_at(row, c4)];
-          a.x += b.x;
-          a.y += b.y;
-          a.z += b.z;
-          a.w += b.w;
+        for (int q = 0; q < 2; ++q) {
+          float4 a = reinterpret_cast<const float4*>(sm.ring[4 * q + s * KQ][spare])[merge_at(row, c4)];
+#pragma unroll
+          for (int w = 1; w < KQ; ++w) {
+            const float4 b = reinterpret_cast<const float4*>(sm.ring[4 * q + s * KQ + w][spare])[merge_at(row, c4)];
+            a.x += b.x;
+            a.y += b.y;
+            a.z += b.z;
+            a.w += b.w;
+          }
+          v[4 * q] = a.x;
+          v[4 * q + 1] = a.y;
+          v[4 * q + 2] = a.z;
+          v[4 * q + 3] = a.w;
         }
-        v[4 * q] = a.x;
-        v[4 * q + 1] = a.y;
-        v[4 * q + 2] = a.z;
-        v[4 * q + 3] = a.w;
-      }
-      if (whole) {
-        finish(m, v);
-      } else if (m * TILE + row < rows) {
-        float* dst = slot + (m * TILE + row) * 128 + 4 * c4;
-        st_global_cg_v4f(dst, v[0], v[1], v[2], v[3]);
-        st_global_cg_v4f(dst + 64, v[4], v[5], v[6], v[7]);
+        if (whole) {
+          finish(m, s, v);
+        } else if (m * TILE + row < rows) {
+          float* dst = slot + (m * TILE + row) * (128 * SUB) + s * 64 + 4 * c4;
+          st_global_cg_v4f(dst, v[0], v[1], v[2], v[3]);
+          st_global_cg_v4f(dst + SUB * 64, v[4], v[5], v[6], v[7]);
+        }
       }
     }
     bool done = whole;
@@ -525,13 +535,14 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
       done = sm.last;
       if (done) {
         __threadfence();
-        for (int m = 0; m * TILE < rows; ++m) {
+        for (int ms = 0; ms / SUB * TILE < rows; ++ms) {
+          const int m = ms / SUB, s = ms % SUB;
           float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
           if (m * TILE + row < rows) {
-#pragma unroll 2
+#pragma unroll 4
             for (int64_t c = c0; c <= c1; ++c) {
-              const float* src = p.partial + (2 * c + (c == c0)) * int64_t(MT * TILE * 128) + (m * TILE + row) * 128 + 4 * c4;
-              const float4 a = ld_global_cg_v4f(src), b = ld_global_cg_v4f(src + 64);
+              const float* src = p.partial + (2 * c + (c == c0)) * slot_size + (m * TILE + row) * (128 * SUB) + s * 64 + 4 * c4;
+              const float4 a = ld_global_cg_v4f(src), b = ld_global_cg_v4f(src + SUB * 64);
               v[0] += a.x;
               v[1] += a.y;
               v[2] += a.z;
@@ -542,44 +553,45 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
               v[7] += b.w;
             }
           }
-          finish(m, v);
+          finish(m, s, v);
         }
       }
     }
     if (DOWN && done) {
-      // the column tile's last row tile: combine its 128 columns for every token
+      // combine the column tile for every token whose last slot this tile was
       __threadfence();
       __syncthreads();
-      if (tid == 0) {
-        uint32_t* counter = p.counters + 2 * MAX_CTAS + ct;
-        sm.last = atomicAdd(counter, 1u) == uint32_t(sm.tiles - 1);
-        if (sm.last) *counter = 0;
+      if (tid < rows) {
+        const int tok = sm.row_token[row0 + tid];
+        uint32_t* counter = p.counters + 2 * MAX_CTAS + ct * MAX_T + tok;
+        const bool last = atomicAdd(counter, 1u) == uint32_t(p.topk - 1);
+        if (last) *counter = 0;
+        sm.ready[tid] = last ? tok : -1;
       }
       __syncthreads();
-      if (sm.last) {
-        __threadfence();
-        for (int i = tid; i < p.T * 32; i += THREADS) {
-          const int tok = i >> 5, col = ct * 128 + (i & 31) * 4;
-          if (col >= p.Hd) continue;
-          float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          for (int s0 = 0; s0 < p.topk; s0 += 8) {
-            float4 w[8];
+      __threadfence();
+      constexpr int TPT = WIDE / 4;  // threads to a token
+      for (int r = tid / TPT; r < rows; r += THREADS / TPT) {
+        const int tok = sm.ready[r], col = ct * WIDE + tid % TPT * 4;
+        if (tok < 0 || col >= p.Hd) continue;
+        float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s0 = 0; s0 < p.topk; s0 += 8) {
+          float4 w[8];
 #pragma unroll
-            for (int s = 0; s < 8; ++s)  // all on their way at once
-              w[s] = ld_global_cg_v4f(p.y + int64_t(sm.row_of[tok][min(s0 + s, p.topk - 1)]) * p.Hd + col);
+          for (int s = 0; s < 8; ++s)  // all on their way at once
+            w[s] = ld_global_cg_v4f(p.y + int64_t(sm.row_of[tok][min(s0 + s, p.topk - 1)]) * p.Hd + col);
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-              if (s0 + s >= p.topk) break;
-              const float gate = sm.gates[tok][s0 + s];
-              o[0] = fmaf(gate, w[s].x, o[0]);
-              o[1] = fmaf(gate, w[s].y, o[1]);
-              o[2] = fmaf(gate, w[s].z, o[2]);
-              o[3] = fmaf(gate, w[s].w, o[3]);
-            }
+          for (int s = 0; s < 8; ++s) {
+            if (s0 + s >= p.topk) break;
+            const float gate = sm.gates[tok][s0 + s];
+            o[0] = fmaf(gate, w[s].x, o[0]);
+            o[1] = fmaf(gate, w[s].y, o[1]);
+            o[2] = fmaf(gate, w[s].z, o[2]);
+            o[3] = fmaf(gate, w[s].w, o[3]);
           }
-          *reinterpret_cast<uint2*>(p.out + int64_t(tok) * p.Hd + col) =
-              make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
         }
+        *reinterpret_cast<uint2*>(p.out + int64_t(tok) * p.Hd + col) =
+            make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
       }
     }
     at += k_end - k_begin;
@@ -595,8 +607,9 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 MoeLayout moe_layout(int T, int topk, int I, int Hd) {
   const size_t P = size_t(T) * topk;
   MoeLayout l{};
-  l.partial = up256((2 * MAX_CTAS + size_t(cdiv(Hd, 128))) * 4);
-  l.act = l.partial + size_t(MAX_CTAS) * 2 * (2 * TILE * 128) * 4;
+  // the counters' place does not depend on the sizes: one workspace may serve calls of many
+  l.partial = up256((2 * MAX_CTAS + size_t(MAX_HD / 128) * MAX_T) * 4);
+  l.act = l.partial + size_t(MAX_CTAS) * 2 * std::min(T, 2 * TILE) * 512 * 4;
   l.y = l.act + up256(P * I * 2 * 2);
   l.bytes = l.y + P * Hd * 4;
   return l;
@@ -604,19 +617,37 @@ MoeLayout moe_layout(int T, int topk, int I, int Hd) {
 bool moe_sizes_ok(int T, int topk, int E, int H, int I, int Hd) {
   return T >= 0 && T <= MAX_T && E >= 1 && E <= TL_MAX_EXPERTS && topk >= 1 && topk <= MAX_K && topk <= E && H >= 8 &&
          H % 8 == 0 && I >= 8 && I % 8 == 0 && Hd >= 8 && Hd % 8 == 0 && H <= (1 << 20) && I <= (1 << 20) &&
-         Hd <= (1 << 20);
+         Hd <= MAX_HD;
 }
 
-template <bool DOWN>
-tl_status launch_moe(const MoeParams& p, bool two, int ctas, cudaStream_t st) {
-  const void* kernel = two ? reinterpret_cast<const void*>(&moe_decode_kernel<DOWN, 2>)
-                           : reinterpret_cast<const void*>(&moe_decode_kernel<DOWN, 1>);
+template <bool DOWN, int MT>
+tl_status launch_moe(const MoeParams& p, int sub, int ctas, cudaStream_t st) {
+  static_assert(sizeof(MoeSmem<DOWN, MT>) <= 232448, "shared memory above the per-CTA limit");
+  const void* kernel = sub == 4   ? reinterpret_cast<const void*>(&moe_decode_kernel<DOWN, MT, 4>)
+                       : sub == 2 ? reinterpret_cast<const void*>(&moe_decode_kernel<DOWN, MT, 2>)
+                                  : reinterpret_cast<const void*>(&moe_decode_kernel<DOWN, MT, 1>);
   void* args[] = {const_cast<MoeParams*>(&p)};
-  return launch(kernel, ctas, THREADS, two ? sizeof(MoeSmem<DOWN, 2>) : sizeof(MoeSmem<DOWN, 1>), st, args, DOWN);
+  return launch(kernel, ctas, THREADS, sizeof(MoeSmem<DOWN, MT>), st, args, DOWN);
 }
-static_assert(sizeof(MoeSmem<true, 2>) <= 232448 && sizeof(MoeSmem<false, 2>) <= 232448 &&
-                  sizeof(MoeSmem<true, 1>) <= 232448 && sizeof(MoeSmem<false, 1>) <= 232448,
-              "shared memory above the per-CTA limit");
+
+// Strips of 64 columns next to one another in a tile of `one * sub` columns: the width that reads least.  Columns that a
+// last tile lacks cost the time of their strips; where the rows are no multiples of 128 bytes, a tile's two edges cost
+// about a line in each row (reads 1.84 times the weights with strips alone, 64 x 2048 x 2000: 161 us, 124 us with four).
+// Of equals the widest, which has the fewest tiles to finish.  With fewer tiles than CTAs, strips alone: a tile is then
+// shared by fewer CTAs (one token, two experts of 4096 x 1408: 31 us, 38 us with the widest).
+int strips(int cols, int one, bool aligned, int row_tiles, int ctas) {
+  int best = 1;
+  double least = 1e30;
+  for (int sub : {1, 2, 4}) {
+    const int tiles = cdiv(cols, one * sub);
+    const double cost = double(tiles) * sub * (aligned ? 1.0 : 1.0 + 0.84 / sub);
+    if (cost <= least && (sub == 1 || tiles * row_tiles >= ctas)) {
+      least = cost;
+      best = sub;
+    }
+  }
+  return best;
+}
 
 }  // namespace
 }  // namespace tl
@@ -678,7 +709,10 @@ extern "C" tl_status tl_moe_decode(const tl_moe_decode_args* a, void* stream) {
   // Row tiles of 32 where an expert expects more than a tile of 16: its weights are then read once for both
   const bool two = a->T > TILE && a->T * a->topk > 12 * a->E;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (tl_status s = launch_moe<false>(p, two, ctas, st)) return s;
+  p.slot_rows = std::min(a->T, two ? 2 * TILE : TILE);
+  const int row_tiles = std::min(a->E, a->T * a->topk);  // about as many experts are chosen
+  const int up = strips(a->I, 64, a->I % 32 == 0, row_tiles, ctas), down = strips(a->Hd, 128, a->Hd % 64 == 0, row_tiles, ctas);
+  if (tl_status s = two ? launch_moe<false, 2>(p, up, ctas, st) : launch_moe<false, 1>(p, up, ctas, st)) return s;
   for (int e = 0; e < a->E; ++e) p.w[e] = a->W2[e];
-  return launch_moe<true>(p, two, ctas, st);
+  return two ? launch_moe<true, 2>(p, down, ctas, st) : launch_moe<true, 1>(p, down, ctas, st);
 }
