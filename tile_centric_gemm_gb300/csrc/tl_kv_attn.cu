@@ -611,7 +611,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     }
     if (lane == 0) sm.spare[warp] = spare;
     __syncthreads();
-    constexpr int EPT = TILE * D / THREADS < 4 ? 4 : TILE * D / THREADS;  // elements of one thread
+    constexpr int EPT = TILE * D <= 4 * THREADS ? 4 : 8;  // elements of one thread, whole 16-byte units
+    static_assert(D % EPT == 0 && TILE * D <= EPT * THREADS, "a tile is more than the threads' share");
     const int row = tid / (D / EPT), d0 = tid % (D / EPT) * EPT;
     const bool mine_row = row < rows;
     float M1 = -INFINITY, L = 0.0f;

@@ -49,7 +49,7 @@ constexpr int KV = 128;          // tokens of a tile
 constexpr int ROWS = 128;        // query rows of a tile
 constexpr int UNIT = 2 * ROWS;
 constexpr int KST = 2, VST = 3;  // ring stages
-constexpr int MIN_TILES = 4;     // of a CTA's run
+constexpr int MIN_TILES = 4;     // of a CTA's run, where units are split
 constexpr float kShift = 7.0f, kSlack = 8.0f;
 constexpr uint32_t BOX = 128 * 64 * 2;  // 128 rows of 64 fp16, one swizzle span wide
 
@@ -73,6 +73,7 @@ struct Side {
   int32_t nan_at[4][128];  // least token whose value is NaN in the dim, among those not all rows see
   int32_t warp_max[CONV][2];
   int64_t warp_sum[16];
+  uint32_t warp_units[16];
   int64_t total, ctas, run0;  // tiles of all runs, runs, this run's first tile
   int32_t begin[4];           // sequence, kv head, row block, tile
   int32_t tiles[4];           // of the segments in work
@@ -296,7 +297,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   const int per = (b.B + THREADS - 1) / THREADS;
   const int first = min(b.B, tid * per), end = min(b.B, first + per);
   int64_t mine = 0;
-  for (int s = first; s < end; ++s) mine += p.c.Hkv * seq_tiles(p, kv_seq(b, p.c.ps, s));
+  uint32_t units = 0;
+  for (int s = first; s < end; ++s) {
+    const KvSeq q = kv_seq(b, p.c.ps, s);
+    mine += p.c.Hkv * seq_tiles(p, q);
+    units += uint32_t(p.c.Hkv) * uint32_t((seq_rows(p, q) + UNIT - 1) / UNIT);
+  }
+  units = __reduce_add_sync(0xffffffffu, units);
+  if (lane == 0) sd.warp_units[warp] = units;
   int64_t before = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -325,14 +333,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     fence_mbar_init();
   }
   __syncthreads();
-  int64_t total = 0;
+  int64_t total = 0, all_units = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w == warp) before += total;
     total += sd.warp_sum[w];
+    all_units += sd.warp_units[w];
   }
   before -= mine;
-  const int64_t n = min(int64_t(gridDim.x), max(int64_t(1), total / MIN_TILES));
+  // a CTA for each unit as far as they go, and where units are split four tiles to a CTA at least
+  const int64_t n = min(int64_t(gridDim.x), max(all_units, total / MIN_TILES));
   const int64_t cta = blockIdx.x;
   const int64_t run0 = cta < n ? cta * total / n : 0, run1 = cta < n ? (cta + 1) * total / n : 0;
   if (run0 >= run1) return;
