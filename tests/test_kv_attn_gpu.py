@@ -265,6 +265,31 @@ def test_one_workspace_for_many_calls(B):
         c.run().check()
 
 
+def test_binding_refuses_wrong_tensors(B):
+    b = Batch([2, 1], [30, 5], seed=22, **LAYOUTS[0])
+    c = Call(B, b)
+    cu, lens, table = c.args
+    out, lse = torch.empty_like(c.dq), torch.empty(b.H, b.n, device="cuda")
+    good = dict(q=c.dq, cache=c.cache, out=out, cu_seqlens=cu, seq_lens=lens, page_table=table, workspace=c.ws,
+                signals=c.sig, lse=lse)
+    B.tl_kv_attn(**good)
+    for bad in (dict(q=c.dq.float()), dict(q=c.dq[..., :64]), dict(q=c.dq.cpu()), dict(out=out[:1]), dict(cu_seqlens=cu.long()),
+                dict(cu_seqlens=cu[:2]), dict(seq_lens=lens.cpu()), dict(page_table=table.long()), dict(lse=lse.t()),
+                dict(page_table=table.repeat(1, 2)[:, ::2])):
+        with pytest.raises(ValueError):
+            B.tl_kv_attn(**{**good, **bad})
+    with pytest.raises(B.TLError):
+        B.tl_kv_attn(**{**good, "workspace": c.ws[:256]})
+    rows = torch.zeros(b.n, b.Hkv, b.D, dtype=torch.bfloat16, device="cuda")
+    cos = torch.zeros(64, 64, device="cuda")
+    good = dict(cache=c.cache, k=rows, v=rows, cu_seqlens=cu, seq_lens=lens, page_table=table, signals=c.sig)
+    for bad in (dict(k=rows.half()), dict(v=rows[:, :1]), dict(q=rows), dict(cos=cos), dict(cos=cos, sin=cos.double()),
+                dict(q=rows, q_out=rows.float()), dict(k=rows.transpose(1, 2).contiguous().transpose(1, 2))):
+        with pytest.raises(ValueError):
+            B.tl_kv_append(**{**good, **bad})
+    assert B.tl_query_status(c.sig)[0] == 0
+
+
 def test_offsets_past_32_bits(B):
     """A pool of more than 4 GiB, the sequence's pages at its far end."""
     D, ps = 128, 256

@@ -149,6 +149,23 @@ def test_moe_workspace_size(B):
         assert size(*bad) == 0
 
 
+@pytest.mark.parametrize("name", ["APPEND", "ATTN", "MOE"])
+def test_packed_arguments_are_the_structures(B, name):
+    fmt = getattr(B, "_" + name)
+    cls = {"APPEND": B.tl_kv_append_args, "ATTN": B.tl_kv_attn_args, "MOE": B.tl_moe_decode_args}[name]
+
+    def flat(s):
+        for f, _ in s._fields_:
+            v = getattr(s, f)
+            if isinstance(v, ctypes.Structure):
+                yield from flat(v)
+            else:
+                yield ctypes.cast(v, ctypes.c_void_p).value if isinstance(v, ctypes._Pointer) else v
+    n = len(list(flat(cls())))
+    want = [float(i + 1) if i == 6 and name == "ATTN" else i + 1 for i in range(n)]
+    assert list(flat(cls.from_buffer_copy(fmt.pack(*want)))) == want
+
+
 # ------------------------------------------------------------------ the oracle
 def test_oracle_codes_are_torchs():
     import torch

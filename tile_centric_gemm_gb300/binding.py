@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libtilelink.so")
 
@@ -547,19 +548,64 @@ def tl_ag_attn(Q, K_shards, V_shards, K_gathered, V_gathered, O, signals: Signal
     _check(lib.tl_ag_attn(ctypes.byref(a), _stream(stream)))
 
 
-def _inner(t, what):
-    """Strides of a [tokens, heads, dim] tensor whose dims must lie next to one another."""
-    if t.dim() != 3 or t.stride(2) != 1:
-        raise ValueError(f"{what}: a [tokens, heads, dim] tensor with its dims next to one another")
-    return t.stride(0), t.stride(1)
+# ---------------------------------------------------------------- serving: the 8-bit paged cache, experts for a few tokens
+# A decode step's calls take a few microseconds on the GPU, so their marshalling is kept short: the arguments are packed
+# in one go, laid out as the C structures above.
+
+_APPEND = struct.Struct("@8i4P3q4i3P6q7P")
+_ATTN = struct.Struct("@6ifi4P3q4iP2q6PNP")
+_MOE = struct.Struct("@8i8PN")
+assert _APPEND.size == ctypes.sizeof(tl_kv_append_args) and _ATTN.size == ctypes.sizeof(tl_kv_attn_args) and \
+    _MOE.size == ctypes.sizeof(tl_moe_decode_args)
+
+
+def _packed(name):
+    """The library's function, taking its argument structure as packed bytes."""
+    f = lib[name]
+    f.restype, f.argtypes = _i, [ctypes.c_char_p, _vp]
+    return f
+
+
+_kv_append, _kv_attn, _moe_decode = _packed("tl_kv_append"), _packed("tl_kv_attn"), _packed("tl_moe_decode")
+_torch = None
+
+
+def _raw_stream(stream):
+    global _torch
+    if _torch is None:
+        import torch
+        torch.cuda.init()
+        _torch = torch
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+    return _stream(stream)
+
+
+def _address(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _mistyped(t, what, dtype, shape):
+    raise ValueError(f"{what}: a {'' if shape is None else 'contiguous '}CUDA tensor of {dtype}"
+                     f"{'' if shape is None else f' and shape {tuple(shape)}'}, not {t.dtype} {tuple(t.shape)} on {t.device}"
+                     f"{'' if t.is_contiguous() else ', not contiguous'}")
 
 
 def _typed(t, what, dtype, shape=None):
-    """t is a CUDA tensor of this type (and shape, contiguous, where one is given)."""
-    if t.dtype != dtype or not t.is_cuda:
-        raise ValueError(f"{what}: a CUDA tensor of {dtype}, not {t.dtype} on {t.device}")
-    if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
-        raise ValueError(f"{what}: a contiguous tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
+    """t is a CUDA tensor of this type (and shape, contiguous, where one is given); its address."""
+    if t.dtype is not dtype or not t.is_cuda or (shape is not None and (t.shape != shape or not t.is_contiguous())):
+        _mistyped(t, what, dtype, shape)
+    return t.data_ptr()
+
+
+def _rows(t, what, dtype, shape):
+    """A CUDA tensor [tokens, heads, dim] whose dims lie next to one another: its address and outer strides."""
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape:
+        _mistyped(t, what, dtype, shape)
+    a, b, c = t.stride()
+    if c != 1:
+        raise ValueError(f"{what}: the dims of a head must lie next to one another")
+    return t.data_ptr(), a, b
 
 
 class KvCache:
@@ -582,21 +628,15 @@ class KvCache:
                 raise ValueError("KvCache: scales are contiguous [num_pages, H_kv] CUDA tensors of bytes")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.H_kv, self.page_size, self.head_dim = k.shape
-        self.struct = tl_kv_cache(k=_ptr(k), v=_ptr(v), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale),
-                                  page_stride=k.stride(0), head_stride=k.stride(1), token_stride=k.stride(2),
-                                  num_pages=self.num_pages, page_size=self.page_size, H_kv=self.H_kv,
-                                  head_dim=self.head_dim)
+        self.fields = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.stride(0), k.stride(1),
+                       k.stride(2), self.num_pages, self.page_size, self.H_kv, self.head_dim)
 
 
-def _batch(cu_seqlens, seq_lens, page_table):
-    """(B, columns of the page table) of a ragged batch, its arrays' types checked."""
-    import torch
-    B = seq_lens.shape[0]
-    _typed(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
-    _typed(seq_lens, "seq_lens", torch.int32, (B,))
-    max_pages = page_table.shape[1]
-    _typed(page_table, "page_table", torch.int32, (B, max_pages))
-    return B, max_pages
+def _batch(cu_seqlens, seq_lens, page_table, int32):
+    """(B, columns of the page table, the three addresses) of a ragged batch, its arrays' types checked."""
+    B, max_pages = page_table.shape
+    return (B, max_pages, _typed(cu_seqlens, "cu_seqlens", int32, (B + 1,)), _typed(seq_lens, "seq_lens", int32, (B,)),
+            _typed(page_table, "page_table", int32, (B, max_pages)))
 
 
 def tl_kv_append(cache: KvCache, k, v, cu_seqlens, seq_lens, page_table, signals: Signals, *, q=None, q_out=None,
@@ -604,34 +644,29 @@ def tl_kv_append(cache: KvCache, k, v, cu_seqlens, seq_lens, page_table, signals
     """Append k, v [n, H_kv, D] (bf16; views of a fused projection will do) to the cache, k rotated by the
     tables cos, sin [positions, rot_dim/2] at each token's position; q [n, H, D] rotated into q_out
     (see tilelink.h).  No tables: no rotation."""
-    import torch
+    st = _raw_stream(stream)
+    bf16, f32 = _torch.bfloat16, _torch.float32
     n, D = k.shape[0], cache.head_dim
-    B, max_pages = _batch(cu_seqlens, seq_lens, page_table)
-    ks, vs, qs = _inner(k, "k"), _inner(v, "v"), (0, 0)
-    for t, what in ((k, "k"), (v, "v")):
-        _typed(t, what, torch.bfloat16)
-        if tuple(t.shape) != (n, cache.H_kv, D):
-            raise ValueError(f"{what}: shape {(n, cache.H_kv, D)}, not {tuple(t.shape)}")
-    H = 0
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    if q is not None:
-        H, qs = q.shape[1], _inner(q, "q")
-        _typed(q, "q", torch.bfloat16)
-        if tuple(q.shape) != (n, H, D):
-            raise ValueError(f"q: shape {(n, H, D)}, not {tuple(q.shape)}")
-        _typed(q_out, "q_out", torch.bfloat16, (n, H, D))
-    rot = max_pos = 0
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin go together")
-    if cos is not None:
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
-        _typed(cos, "cos", torch.float32, (max_pos, rot // 2))
-        _typed(sin, "sin", torch.float32, (max_pos, rot // 2))
-    a = tl_kv_append_args(n, B, H, rot, int(bool(interleaved)), max_pos, max_pages, int(max_q_len), cache.struct,
-                          _ptr(k), _ptr(v), _ptr(q), ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], _ptr(q_out), _ptr(cos),
-                          _ptr(sin), _ptr(cu_seqlens), _ptr(seq_lens), _ptr(page_table), signals.handle)
-    _check(lib.tl_kv_append(ctypes.byref(a), _stream(stream)))
+    B, max_pages, cu, lens, table = _batch(cu_seqlens, seq_lens, page_table, _torch.int32)
+    kp, ka, kb = _rows(k, "k", bf16, (n, cache.H_kv, D))
+    vp, va, vb = _rows(v, "v", bf16, (n, cache.H_kv, D))
+    H = qp = qa = qb = out = rot = max_pos = cp = sp = 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out go together")
+        H = q.shape[1]
+        qp, qa, qb = _rows(q, "q", bf16, (n, H, D))
+        out = _typed(q_out, "q_out", bf16, (n, H, D))
+    if cos is not None or sin is not None:
+        if cos is None or sin is None:
+            raise ValueError("cos and sin go together")
+        max_pos, rot = cos.shape
+        cp, sp = _typed(cos, "cos", f32, (max_pos, rot)), _typed(sin, "sin", f32, (max_pos, rot))
+        rot *= 2
+    code = _kv_append(_APPEND.pack(n, B, H, rot, bool(interleaved), max_pos, max_pages, max_q_len, *cache.fields, kp, vp, qp,
+                                   ka, kb, va, vb, qa, qb, out, cp, sp, cu, lens, table, signals.handle.value), st)
+    if code:
+        _check(code)
 
 
 def tl_kv_attn_workspace_size(n_tokens, B, H, H_kv, head_dim, sm_count=0):
@@ -642,20 +677,19 @@ def tl_kv_attn(q, cache: KvCache, out, cu_seqlens, seq_lens, page_table, workspa
                scale=0.0, max_q_len=0, lse=None, stream=None):
     """out [n, H, D] = attention of q [n, H, D] over each sequence's keys and values in the cache, the new
     tokens' included; lse optional float [H, n] (see tilelink.h)."""
-    import torch
+    st = _raw_stream(stream)
+    bf16 = _torch.bfloat16
     n, H, D = q.shape
-    B, max_pages = _batch(cu_seqlens, seq_lens, page_table)
-    _typed(q, "q", torch.bfloat16)
     if D != cache.head_dim:
         raise ValueError(f"q: head dim {D}, the cache's is {cache.head_dim}")
-    qs = _inner(q, "q")
-    _typed(out, "out", torch.bfloat16, (n, H, D))
-    if lse is not None:
-        _typed(lse, "lse", torch.float32, (H, n))
-    a = tl_kv_attn_args(n, B, H, int(bool(causal)), max_pages, int(max_q_len), float(scale), 0, cache.struct, _ptr(q),
-                        qs[0], qs[1], _ptr(out), _ptr(lse), _ptr(cu_seqlens), _ptr(seq_lens), _ptr(page_table),
-                        _ptr(workspace), _nbytes(workspace), signals.handle)
-    _check(lib.tl_kv_attn(ctypes.byref(a), _stream(stream)))
+    B, max_pages, cu, lens, table = _batch(cu_seqlens, seq_lens, page_table, _torch.int32)
+    qp, qa, qb = _rows(q, "q", bf16, (n, H, D))
+    code = _kv_attn(_ATTN.pack(n, B, H, bool(causal), max_pages, max_q_len, scale, 0, *cache.fields, qp, qa, qb,
+                               _typed(out, "out", bf16, (n, H, D)),
+                               0 if lse is None else _typed(lse, "lse", _torch.float32, (H, n)), cu, lens, table,
+                               _address(workspace), _nbytes(workspace), signals.handle.value), st)
+    if code:
+        _check(code)
 
 
 class MoeWeights:
@@ -673,8 +707,8 @@ class MoeWeights:
             _typed(w1, "W1", torch.bfloat16, (self.H, two_I))
             _typed(w2, "W2", torch.bfloat16, (self.I, self.Hd))
         self.W1, self.W2 = W1, W2
-        self.p1 = ctypes.cast(_ptr_array(W1), ctypes.POINTER(_vp))
-        self.p2 = ctypes.cast(_ptr_array(W2), ctypes.POINTER(_vp))
+        self.pointers = _ptr_array(W1), _ptr_array(W2)
+        self.addresses = tuple(ctypes.addressof(p) for p in self.pointers)
 
 
 def tl_moe_decode_workspace_size(T, topk, E, H, I, Hd):
@@ -684,14 +718,12 @@ def tl_moe_decode_workspace_size(T, topk, E, H, I, Hd):
 def tl_moe_decode(x, logits, weights: MoeWeights, out, ids, gates, workspace, *, normalize=True, stream=None):
     """out [T, Hd] = the mixture-of-experts layer of x [T, H] under the router's logits [T, E]; the chosen experts
     and their gates into ids and gates [T, topk] (see tilelink.h)."""
-    import torch
-    w = weights
+    st = _raw_stream(stream)
+    bf16, f32, w = _torch.bfloat16, _torch.float32, weights
     T, topk = ids.shape
-    _typed(x, "x", torch.bfloat16, (T, w.H))
-    _typed(logits, "logits", torch.float32, (T, w.E))
-    _typed(out, "out", torch.bfloat16, (T, w.Hd))
-    _typed(ids, "ids", torch.int32, (T, topk))
-    _typed(gates, "gates", torch.float32, (T, topk))
-    a = tl_moe_decode_args(T, w.H, w.I, w.Hd, w.E, topk, int(bool(normalize)), 0, _ptr(x), _ptr(logits), w.p1, w.p2,
-                           _ptr(out), _ptr(ids), _ptr(gates), _ptr(workspace), _nbytes(workspace))
-    _check(lib.tl_moe_decode(ctypes.byref(a), _stream(stream)))
+    code = _moe_decode(_MOE.pack(T, w.H, w.I, w.Hd, w.E, topk, bool(normalize), 0, _typed(x, "x", bf16, (T, w.H)),
+                                 _typed(logits, "logits", f32, (T, w.E)), *w.addresses, _typed(out, "out", bf16, (T, w.Hd)),
+                                 _typed(ids, "ids", _torch.int32, (T, topk)), _typed(gates, "gates", f32, (T, topk)),
+                                 _address(workspace), _nbytes(workspace)), st)
+    if code:
+        _check(code)
