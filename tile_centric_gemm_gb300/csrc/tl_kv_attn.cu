@@ -43,6 +43,7 @@ namespace {
 constexpr int MAX_TILE = 16;  // query rows of one tile: 8 or 16
 constexpr int CHUNK = 32;     // tokens of one chunk; its halves of 16 lie in one page each
 constexpr int FEW_ROWS = 64;  // query rows per kv head up to which this kernel serves a sequence
+constexpr int SEGMENT_COST = 24;  // what a second tile costs a CTA, in chunks (about 9000 cycles)
 constexpr float kShift = 7.0f;
 constexpr float kSlack = 8.0f;
 
@@ -70,8 +71,10 @@ struct DecodeSmem {
   uint2 meta[WARPS][STAGES];  // scale bytes (k, v of the first half, k, v of the second); which halves' pages are good
   int32_t e[WARPS], spare[WARPS];
   int64_t warp_sum[WARPS];
+  int32_t warp_items[WARPS];
   int64_t begin_off;
   int32_t begin_seq, last;
+  int32_t pieces[WARPS];
 };
 
 // One run's piece of one tile: chunks cb .. ce-1 of the tile's nch.
@@ -202,9 +205,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
   const int per = (b.B + THREADS - 1) / THREADS;
   const int first = min(b.B, tid * per), end = min(b.B, first + per);
   int64_t mine = 0;
+  uint32_t items = 0;
   for (int s = first; s < end; ++s) {
     const KvSeq q = kv_seq(b, p.c.ps, s);
-    mine += int64_t(seq_tiles<TILE>(p, q)) * p.c.Hkv * seq_chunks(q);
+    const int tiles = seq_tiles<TILE>(p, q) * p.c.Hkv;
+    items += uint32_t(tiles);
+    mine += int64_t(tiles) * seq_chunks(q);
   }
   int64_t before = mine;
 #pragma unroll
@@ -212,43 +218,109 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     const int64_t x = __shfl_up_sync(0xffffffffu, before, d);
     if (lane >= d) before += x;
   }
-  if (lane == 31) sm.warp_sum[warp] = before;
+  items = __reduce_add_sync(0xffffffffu, items);
+  if (lane == 31) {
+    sm.warp_sum[warp] = before;
+    sm.warp_items[warp] = int(items);
+  }
   __syncthreads();
-  int64_t total = 0;
+  int64_t total = 0, all_items = 0;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     if (w == warp) before += total;
     total += sm.warp_sum[w];
+    all_items += sm.warp_items[w];
   }
   before -= mine;
-  // a CTA gets a chunk for each warp at least
-  const int64_t n = min(int64_t(gridDim.x), max(int64_t(1), quotient(total, WARPS)));
+  Segment f, c;  // where copies are, and where products are
+  // A run's first chunk in the list and its length; a tile's CTAs where runs end with tiles (below 0: they do not).
   const int64_t cta = blockIdx.x;
-  if (cta >= n || total == 0) {
+  int64_t run0 = 0, n = 0;
+  int tile_c0 = -1, tile_c1 = -1;
+  if (total == 0) {
     pdl_wait_previous();
     return;
   }
-  const int64_t run0 = quotient(cta * total, n), run1 = quotient((cta + 1) * total, n);
-  if (run0 >= run1) {
-    pdl_wait_previous();
-    return;
-  }
-  if (mine > 0 && before <= run0 && run0 < before + mine) {
-    int64_t at = before;
-    for (int s = first; s < end; ++s) {
+  if (all_items <= int64_t(gridDim.x)) {
+    // Few tiles: a CTA that works on two of them pays for two merges one after the other, so each tile is cut for
+    // itself, into pieces of at most L chunks, with the least L that the CTAs suffice for.  Each warp tries one L.
+    constexpr int TRY = (SEGMENT_COST + WARPS - 2) / (WARPS - 1);
+    const int least = max(WARPS, int(quotient(total + gridDim.x - 1, gridDim.x)));
+    uint32_t pieces = 0;
+    for (int s = lane; s < b.B; s += 32) {
       const KvSeq q = kv_seq(b, p.c.ps, s);
-      const int64_t size = int64_t(seq_tiles<TILE>(p, q)) * p.c.Hkv * seq_chunks(q);
-      if (run0 < at + size) {
-        sm.begin_seq = s;
-        sm.begin_off = run0 - at;
-        break;
+      const int L = least + warp * TRY;
+      pieces += uint32_t(seq_tiles<TILE>(p, q) * p.c.Hkv) * uint32_t((seq_chunks(q) + L - 1) / L);
+    }
+    pieces = __reduce_add_sync(0xffffffffu, pieces);
+    if (lane == 0) sm.pieces[warp] = int(pieces);
+    __syncthreads();
+    int w = 0;
+    while (w < WARPS && sm.pieces[w] > int(gridDim.x)) ++w;
+    if (w < WARPS) {
+      if (cta >= sm.pieces[w]) {
+        pdl_wait_previous();
+        return;
       }
-      at += size;
+      const int L = least + w * TRY;
+      int at = int(cta);
+      for (int s0 = 0;; s0 += 32) {  // the sequence that this CTA's piece is of
+        const int s = s0 + lane;
+        int cnt = 0;
+        if (s < b.B) {
+          const KvSeq q = kv_seq(b, p.c.ps, s);
+          cnt = seq_tiles<TILE>(p, q) * p.c.Hkv * ((seq_chunks(q) + L - 1) / L);
+        }
+        int sum = cnt;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, sum, d);
+          if (lane >= d) sum += x;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, at < sum);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          at -= __shfl_sync(0xffffffffu, sum - cnt, src);
+          seg_open<TILE>(p, c, s0 + src, 0, 1);
+          break;
+        }
+        at -= __shfl_sync(0xffffffffu, sum, 31);
+      }
+      const int parts = (c.nch + L - 1) / L, sub = at / parts, part = at - sub * parts;
+      c.hk = sub / c.tiles;
+      c.rt = sub - c.hk * c.tiles;
+      c.cb = int(quotient(int64_t(c.nch) * part, parts));
+      c.ce = int(quotient(int64_t(c.nch) * (part + 1), parts));
+      c.left = c.ce - c.cb;
+      tile_c0 = int(cta) - part;
+      tile_c1 = tile_c0 + parts - 1;
     }
   }
-  __syncthreads();
-  Segment f, c;  // where copies are, and where products are
-  seg_open<TILE>(p, c, sm.begin_seq, sm.begin_off, run1 - run0);
+  if (tile_c0 < 0) {
+    // a CTA gets a chunk for each warp at least
+    n = min(int64_t(gridDim.x), max(int64_t(1), quotient(total, WARPS)));
+    run0 = cta < n ? quotient(cta * total, n) : 0;
+    const int64_t run1 = cta < n ? quotient((cta + 1) * total, n) : 0;
+    if (run0 >= run1) {
+      pdl_wait_previous();
+      return;
+    }
+    if (mine > 0 && before <= run0 && run0 < before + mine) {
+      int64_t at = before;
+      for (int s = first; s < end; ++s) {
+        const KvSeq q = kv_seq(b, p.c.ps, s);
+        const int64_t size = int64_t(seq_tiles<TILE>(p, q)) * p.c.Hkv * seq_chunks(q);
+        if (run0 < at + size) {
+          sm.begin_seq = s;
+          sm.begin_off = run0 - at;
+          break;
+        }
+        at += size;
+      }
+    }
+    __syncthreads();
+    seg_open<TILE>(p, c, sm.begin_seq, sm.begin_off, run1 - run0);
+  }
   f = c;
 
   // ---------------------------------------------------------------- the copies of one warp
@@ -651,7 +723,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     bool done = true;
     if (c.cb != 0 || c.ce != c.nch) {
       const int64_t t0 = at - c.cb;  // the tile's first chunk in the list
-      const int64_t c0 = quotient((t0 + 1) * n - 1, total), c1 = quotient((t0 + c.nch) * n - 1, total);
+      const int64_t c0 = tile_c0 >= 0 ? tile_c0 : quotient((t0 + 1) * n - 1, total);
+      const int64_t c1 = tile_c0 >= 0 ? tile_c1 : quotient((t0 + c.nch) * n - 1, total);
       constexpr int SLOT = TILE * D + 2 * TILE;
       float* slot = p.partial + (2 * cta + (c.cb == 0 ? 1 : 0)) * SLOT;
       if (mine_row) {
