@@ -50,8 +50,7 @@ struct AppendParams {
   int32_t kv_blocks, groups;  // blocks for keys and values; blocks of one item
 };
 
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -59,6 +58,8 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
     x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
 }
+
+__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) { unpack8(*reinterpret_cast<const uint4*>(p), x); }
 
 // x c + t s rounded to odd (see above); not finite: the plain fp32 value.
 __device__ __forceinline__ float dot2_odd(float x, float c, float t, float s) {
@@ -70,14 +71,11 @@ __device__ __forceinline__ float dot2_odd(float x, float c, float t, float s) {
   const float lo = __fadd_rn(err, __fadd_rn(pe, re));
   const float hi = __fadd_rn(sum, lo);
   const float rest = __fsub_rn(lo, __fsub_rn(hi, sum));
-  uint32_t u = __float_as_uint(hi);
-  if ((__float_as_uint(sum) & 0x7F800000u) == 0x7F800000u) return sum;
-  if ((u & 0x7F800000u) == 0x7F800000u) return hi;
-  if (rest != 0.0f) {
-    if ((rest < 0.0f) != (hi < 0.0f)) --u;
-    u |= 1u;
-  }
-  return __uint_as_float(u);
+  // what is left below hi decides: one step towards zero where it points there, and the last bit set
+  const uint32_t u = __float_as_uint(hi);
+  const uint32_t odd = (u + uint32_t(int32_t(__float_as_uint(rest) ^ u) >> 31)) | 1u;
+  const bool finite = (__float_as_uint(sum) & 0x7FFFFFFFu) < 0x7F800000u;
+  return finite ? __uint_as_float(rest != 0.0f ? odd : u) : sum;
 }
 
 template <bool EXACT>
@@ -85,38 +83,67 @@ __device__ __forceinline__ float dot2(float x, float c, float t, float s) {
   return EXACT ? dot2_odd(x, c, t, s) : fmaf(x, c, t * s);
 }
 
-// Dims 8u .. 8u+7 of one row, rotated by the table row at `pos`.
-template <bool EXACT>
-__device__ __forceinline__ void rotated8(const AppendParams& p, const uint16_t* row, int u, int pos, float (&y)[8]) {
-  load8(row + 8 * u, y);
+// What a thread needs of the tables for dims 8u .. 8u+7 at one position: eight pairs' (halves) or four pairs'
+// (interleaved) cos and sin, and where in a row the other element of each pair is.
+struct Turn {
+  float c[8], s[8];
+  int partner;  // first dim of the partner unit (halves); below 0: not rotated
+  bool first;
+};
+__device__ __forceinline__ void load4(const float* p, float* x) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x;
+  x[1] = v.y;
+  x[2] = v.z;
+  x[3] = v.w;
+}
+__device__ __forceinline__ void turn_at(const AppendParams& p, int u, int pos, Turn& w) {
+  w.partner = -1;
+  w.first = true;
   if (8 * u >= p.rot) return;
   const int half = p.rot >> 1;
   const float* cr = p.cos + int64_t(pos) * half;
   const float* sr = p.sin + int64_t(pos) * half;
   if (p.interleaved) {
-    const float4 c = *reinterpret_cast<const float4*>(cr + 4 * u), s = *reinterpret_cast<const float4*>(sr + 4 * u);
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = y[2 * i], b = y[2 * i + 1];
-      y[2 * i] = dot2<EXACT>(a, cc[i], -b, ss[i]);
-      y[2 * i + 1] = dot2<EXACT>(b, cc[i], a, ss[i]);
-    }
+    w.partner = 8 * u;
+    load4(cr + 4 * u, w.c);
+    load4(sr + 4 * u, w.s);
     return;
   }
-  const bool first = 8 * u < half;
-  const int j = first ? 8 * u : 8 * u - half;
-  float t[8];
-  load8(row + (first ? 8 * u + half : j), t);
+  w.first = 8 * u < half;
+  const int j = w.first ? 8 * u : 8 * u - half;
+  w.partner = w.first ? 8 * u + half : j;
+  load4(cr + j, w.c);
+  load4(cr + j + 4, w.c + 4);
+  load4(sr + j, w.s);
+  load4(sr + j + 4, w.s + 4);
+}
+// x: the unit's dims, t: its partner's (halves)
+template <bool EXACT>
+__device__ __forceinline__ void turn(const AppendParams& p, const Turn& w, const float (&x)[8], const float (&t)[8], float (&y)[8]) {
+  if (w.partner < 0) {
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const float4 c = *reinterpret_cast<const float4*>(cr + j + 4 * q);
-    const float4 s = *reinterpret_cast<const float4*>(sr + j + 4 * q);
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    for (int i = 0; i < 8; ++i) y[i] = x[i];
+  } else if (p.interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      y[4 * q + i] = dot2<EXACT>(y[4 * q + i], cc[i], first ? -t[4 * q + i] : t[4 * q + i], ss[i]);
+    for (int i = 0; i < 4; ++i) {
+      y[2 * i] = dot2<EXACT>(x[2 * i], w.c[i], -x[2 * i + 1], w.s[i]);
+      y[2 * i + 1] = dot2<EXACT>(x[2 * i + 1], w.c[i], x[2 * i], w.s[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = dot2<EXACT>(x[i], w.c[i], w.first ? -t[i] : t[i], w.s[i]);
   }
+}
+// Dims 8u .. 8u+7 of one row, rotated by the table row at `pos`.
+template <bool EXACT>
+__device__ __forceinline__ void rotated8(const AppendParams& p, const uint16_t* row, int u, int pos, float (&y)[8]) {
+  Turn w;
+  turn_at(p, u, pos, w);
+  float x[8], t[8];
+  load8(row + 8 * u, x);
+  load8(row + max(w.partner, 0), t);
+  turn<EXACT>(p, w, x, t, y);
 }
 
 // Sum of one count per thread over the block.
@@ -145,7 +172,7 @@ __device__ __forceinline__ uint4 recode16(uint4 w, float f) {
 
 // TEAM threads to one (page, head, keys or values); KEEP passes' rows stay in registers.
 template <int D, int TEAM, int KEEP>
-__global__ void __launch_bounds__(APP_THREADS) kv_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int UNITS = D / 8;             // threads to a row
   constexpr int STEP = TEAM / UNITS;       // rows of one pass
   __shared__ int counts[4];
@@ -170,12 +197,30 @@ __global__ void __launch_bounds__(APP_THREADS) kv_append_kernel(const __grid_con
     }
     const uint16_t* row = p.q + int64_t(t) * p.q_ts;
     uint16_t* dst = p.q_out + int64_t(t) * p.H * D;
-    for (int i = tid; i < p.H * UNITS; i += APP_THREADS) {
-      const int h = i / UNITS, u = i % UNITS;
-      float y[8];
-      rotated8<false>(p, row + h * p.q_hs, u, pos, y);
-      st_global_v4(dst + h * D + 8 * u, pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                   pack_bf16x2(y[6], y[7]));
+    // a thread has the same dims of every fourth (eighth) head or so: the tables once, four heads' loads at a time
+    const int u = tid % UNITS;
+    constexpr int STRIDE = APP_THREADS / UNITS, BATCH = 4;
+    Turn w;
+    turn_at(p, u, pos, w);
+    for (int h0 = tid / UNITS; h0 < p.H; h0 += STRIDE * BATCH) {
+      uint4 x[BATCH], t4[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const uint16_t* head = row + min(h0 + k * STRIDE, p.H - 1) * p.q_hs;
+        x[k] = *reinterpret_cast<const uint4*>(head + 8 * u);
+        t4[k] = *reinterpret_cast<const uint4*>(head + max(w.partner, 0));
+      }
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int h = h0 + k * STRIDE;
+        if (h >= p.H) break;
+        float a[8], b8[8], y[8];
+        unpack8(x[k], a);
+        unpack8(t4[k], b8);
+        turn<false>(p, w, a, b8, y);
+        st_global_v4(dst + h * D + 8 * u, pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                     pack_bf16x2(y[6], y[7]));
+      }
     }
     return;
   }
@@ -351,7 +396,7 @@ extern "C" tl_status tl_kv_append(const tl_kv_append_args* a, void* stream) {
   p.interleaved = a->interleaved;
   p.max_pos = a->max_pos;
   const int per_seq = a->max_q_len ? std::min(a->max_q_len, a->n_tokens) : cdiv(a->n_tokens, a->B);
-  const bool wide = per_seq >= 8;  // a page gets several rows: a whole block to its keys or values of one head
+  const bool wide = std::min(per_seq, c.page_size) >= 32;  // rows of a page: a whole block to its keys or values of one head
   const int64_t items = int64_t(a->n_tokens) / c.page_size + 2 * int64_t(a->B);
   p.groups = wide ? 2 * c.H_kv : cdiv(2 * c.H_kv, APP_THREADS / 32);
   const int64_t blocks = items * p.groups + (a->H > 0 ? a->n_tokens : 0);
@@ -359,10 +404,10 @@ extern "C" tl_status tl_kv_append(const tl_kv_append_args* a, void* stream) {
   p.kv_blocks = int(items * p.groups);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (c.head_dim == 128) {
-    if (wide) kv_append_kernel<128, 128, 8><<<unsigned(blocks), APP_THREADS, 0, st>>>(p);
+    if (wide) kv_append_kernel<128, 128, 1><<<unsigned(blocks), APP_THREADS, 0, st>>>(p);
     else kv_append_kernel<128, 32, 2><<<unsigned(blocks), APP_THREADS, 0, st>>>(p);
   } else {
-    if (wide) kv_append_kernel<64, 128, 4><<<unsigned(blocks), APP_THREADS, 0, st>>>(p);
+    if (wide) kv_append_kernel<64, 128, 1><<<unsigned(blocks), APP_THREADS, 0, st>>>(p);
     else kv_append_kernel<64, 32, 2><<<unsigned(blocks), APP_THREADS, 0, st>>>(p);
   }
   return cuda_ok(cudaGetLastError(), "tl_kv_append launch");
