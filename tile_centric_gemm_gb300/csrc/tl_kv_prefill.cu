@@ -220,8 +220,8 @@ __device__ __forceinline__ uint32_t block_factor(int byte, int top) {
   return pack_f16x2(f, f);
 }
 
-// Sixteen codes (dims 16u .. 16u+15 of row r) times f into a swizzled tile.
-__device__ __forceinline__ void put16(uint32_t tile, int r, int u, uint4 w, uint32_t f) {
+// Sixteen codes times f into a swizzled tile: eight fp16 each at two places.
+__device__ __forceinline__ void put16(uint32_t lo, uint32_t hi, uint4 w, uint32_t f) {
   const uint32_t c[4] = {w.x, w.y, w.z, w.w};
   uint32_t h[8];
 #pragma unroll
@@ -229,9 +229,8 @@ __device__ __forceinline__ void put16(uint32_t tile, int r, int u, uint4 w, uint
     h[2 * i] = mul_f16x2(e4m3x2_to_f16x2(c[i]), f);
     h[2 * i + 1] = mul_f16x2(e4m3x2_to_f16x2_hi(c[i]), f);
   }
-  const uint32_t row = tile + uint32_t((u >> 2) * BOX + r * 128), at = uint32_t((u & 3) * 2);
-  st_shared_v4(row + ((at ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-  st_shared_v4(row + (((at + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+  st_shared_v4(lo, h[0], h[1], h[2], h[3]);
+  st_shared_v4(hi, h[4], h[5], h[6], h[7]);
 }
 
 // In 16 tokens of a value tile that not all rows see: NaN out of the tile, and the least token with one kept
@@ -397,6 +396,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     // the issuing loop it has to live in the instruction cache; two or three items ahead measured slower.)
     constexpr int PASS = D / 64;     // 16-code units of one thread and token
     const int r8 = lane >> 2, u4 = lane & 3;
+    // where a lane's 16 dims of token r8 go: 16-byte units 2 u4 and 2 u4 + 1 of the row, swizzled by the row
+    const uint32_t lane_lo = uint32_t(r8 * 128 + (((2 * u4) ^ r8) << 4)), lane_hi = uint32_t(r8 * 128 + (((2 * u4 + 1) ^ r8) << 4));
     int before_seg = 0;              // tiles of earlier segments
     bool ok = true;
     for (int i = 0; ok; ++i) {
@@ -528,11 +529,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         const uint32_t ktile = smem + L::K + uint32_t(kst) * L::TILE, vtile = smem + L::V + uint32_t(vst) * L::TILE;
         const int row0 = (n & 7) * 16;
+        const uint32_t klo = ktile + uint32_t(row0 * 128) + lane_lo, khi = ktile + uint32_t(row0 * 128) + lane_hi;
+        const uint32_t vlo = vtile + uint32_t(row0 * 128) + lane_lo, vhi = vtile + uint32_t(row0 * 128) + lane_hi;
 #pragma unroll
-        for (int x = 0; x < 2 * PASS; ++x) put16(ktile, row0 + x / PASS * 8 + r8, x % PASS * 4 + u4, ck[x], fk);
+        for (int x = 0; x < 2 * PASS; ++x) put16(klo + x / PASS * 1024 + x % PASS * BOX, khi + x / PASS * 1024 + x % PASS * BOX, ck[x], fk);
         load(p.c.k, ck, n + CONV);
 #pragma unroll
-        for (int x = 0; x < 2 * PASS; ++x) put16(vtile, row0 + x / PASS * 8 + r8, x % PASS * 4 + u4, cv[x], fv);
+        for (int x = 0; x < 2 * PASS; ++x) put16(vlo + x / PASS * 1024 + x % PASS * BOX, vhi + x / PASS * 1024 + x % PASS * BOX, cv[x], fv);
         load(p.c.v, cv, n + CONV);
         load_scales();
         page = look_up(n + 2 * CONV);
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     {
       const uint32_t leader = lane == 0, tmem = __reduce_max_sync(0xffffffffu, tmem_base);
       auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t tag) {
-        return __reduce_min_sync(0xffffffffu, uint32_t(mbar_wait(bar, parity, abort, b.status, tmo, tag))) != 0;
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, b.status, tmo, tag)) != 0;
       };
       int ks = 0, vs = 0;
       uint32_t kph = 0, vph = 0;
