@@ -689,6 +689,9 @@ tl_status tl_kv_append(const tl_kv_append_args* args, void* stream);
  * softmax statistics and sums; the codes enter the products exactly.
  * Takes queries that tl_kv_append rotated and a cache that holds the new tokens.
  * May be captured into a graph after a first call outside any capture.
+ * Every wait inside the kernels is bounded (3 s); one that runs out records
+ * TL_ERR_INTERNAL, the outputs are then undefined and the workspace has to be
+ * zeroed before it is used again.
  */
 typedef struct tl_kv_attn_args {
   int32_t n_tokens;            /* rows of q, >= 0 (0: nothing to do) */

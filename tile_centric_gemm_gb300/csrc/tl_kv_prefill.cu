@@ -7,13 +7,16 @@
 // head and 256 of a sequence's query rows, rows being (token, head of the group), so
 // that all heads of a group share every key/value tile; two 128-row tiles A and B
 // take turns, one in the softmax while the tensor cores work for the other.
-//   warps 0-6    convert: queries bf16 -> fp16 (each row by a power of two), then
-//                each 128-token tile of codes -> fp16, keys and values, 16 tokens an
+//   warps 0-5    convert: queries bf16 -> fp16 (each row by a power of two), then
+//                each 64-token tile of codes -> fp16, keys and values, 16 tokens an
 //                item, into shared memory in the 128-byte-swizzled layout that the
 //                products read.  A warp's next two items are on their way in registers.
-//   warp 7       issues the products: S_X = Q_X K^T and O_X += P_X V (M = 128), P from
-//                tensor memory, in the order QK_A(0) QK_B(0) | PV_A(j) QK_A(j+1)
-//                PV_B(j) QK_B(j+1) | ...
+//   warps 6, 7   issue the products, one warp to a query tile X: S_X = Q_X K^T and O_X += P_X V (M = 128), P from
+//                tensor memory.  S has two buffers for each query tile and its scores
+//                are issued two tiles ahead, PV_X(j) QK_X(j+2), so
+//                that a softmax finds its next scores ready: with one buffer of 128
+//                keys each round trip from scores to P and back was waited for
+//                (590 us for two chunks of 2048 over 12289).
 //   warps 8-11   softmax of tile A, warps 12-15 of tile B, a row to a thread.
 // Everything is fp16 with powers of two taken out: codes are exact in fp16, and the
 // block scales enter relative to the largest of the unit's keys (values), a factor of
@@ -29,8 +32,8 @@
 // token of each dim is kept: rows see prefixes, so a row's result in that dim is NaN
 // exactly if the row sees that token.
 //
-// TMEM (lane = query row of the tile): S_A columns 0-127 (P_A in 0-63), S_B 128-255,
-// O_A from 256, O_B from 384.
+// TMEM (lane = query row of the tile): S_A columns 0-63 and 64-127, S_B 128-191 and
+// 192-255 (P in the first half of each), O_A from 256, O_B from 384.
 #include <algorithm>
 #include <cmath>
 
@@ -43,37 +46,45 @@ namespace tl {
 namespace {
 
 constexpr int THREADS = 512;
-constexpr int CONV = 7;           // converting warps
-constexpr int WARP_MMA = 7, WARP_SOFTMAX = 8;
-constexpr int KV = 128;          // tokens of a tile
+constexpr int CONV = 6;           // converting warps
+constexpr int WARP_MMA = 6, WARP_SOFTMAX = 8;
+constexpr int KV = 64;           // tokens of a tile
+constexpr int GROUPS = KV / 16;  // of 16 tokens in a tile
 constexpr int ROWS = 128;        // query rows of a tile
 constexpr int UNIT = 2 * ROWS;
-constexpr int KST = 2, VST = 3;  // ring stages
-constexpr int MIN_TILES = 4;     // of a CTA's run, where units are split
+// Ring stages: keys of tile j + 2 are needed with values of tile j, so that many fewer of them.
+constexpr int KST = 4, VST = 6;
+constexpr int MIN_TILES = 8;     // of a CTA's run, where units are split
 constexpr float kShift = 7.0f, kSlack = 8.0f;
-constexpr uint32_t BOX = 128 * 64 * 2;  // 128 rows of 64 fp16, one swizzle span wide
+constexpr uint32_t BOX = ROWS * 64 * 2;    // a query tile's rows of 64 fp16, one swizzle span wide
+constexpr uint32_t KV_BOX = KV * 64 * 2;   // a key or value tile's
 
 struct __align__(8) Bars {
   uint64_t q_full, q_empty;
   uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t s_full[2][2], p_full[2][2], o_done[2][2], o_empty[2];  // by query tile, and by the tile number's parity
+  uint64_t conv[2], soft[2];                                   // among the converting warps; among a tile's softmax warps
   uint32_t tmem_base, abort;
 };
 
 template <int D>
 struct Layout {
-  static constexpr uint32_t TILE = BOX * (D / 64);  // a tile of queries, keys or values
-  static constexpr uint32_t Q = 0, K = Q + 2 * TILE, V = K + KST * TILE, BARS = V + VST * TILE;
+  static constexpr uint32_t Q_TILE = BOX * (D / 64), TILE = KV_BOX * (D / 64);  // queries; keys or values
+  static constexpr uint32_t Q = 0, K = Q + 2 * Q_TILE, V = K + KST * TILE, BARS = V + VST * TILE;
 };
 
 struct Side {
   Bars bars;
   int8_t q_exp[2][UNIT];   // rows' exponents, by segment parity
   int32_t kv_exp[4][2];    // exponents of the segment's keys and values
-  int32_t nan_at[4][128];  // least token whose value is NaN in the dim, among those not all rows see
+  union {
+    int32_t nan_at[4][128];  // least token whose value is NaN in the dim, among those not all rows see
+    struct {                 // before the segments: sums of the work list
+      int64_t warp_sum[16];
+      uint32_t warp_units[16];
+    };
+  };
   int32_t warp_max[CONV][2];
-  int64_t warp_sum[16];
-  uint32_t warp_units[16];
   int64_t total, ctas, run0;  // tiles of all runs, runs, this run's first tile
   int32_t begin[4];           // sequence, kv head, row block, tile
   int32_t tiles[4];           // of the segments in work
@@ -165,13 +176,22 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
       "r"(leader)
       : "memory");
 }
+// Some warps wait for one another, like a named barrier but for a bounded time: a warp that has given up does not leave
+// the others waiting.
+__device__ __forceinline__ bool meet(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* status,
+                                     uint64_t timeout_ns, uint32_t tag) {
+  __syncwarp();
+  if (lane_id() == 0) mbar_arrive(bar);
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, timeout_ns, tag)) != 0;
+}
 // Descriptors count in 16 bytes and lie in one 18-bit address space, so a step is an addition to the first.
 template <int D>
 __device__ __forceinline__ void issue_qk(uint64_t q0, uint64_t k0, uint32_t d_tmem, uint32_t leader) {
 #pragma unroll
   for (int kk = 0; kk < D / UMMA_K; ++kk) {
-    const uint64_t step = uint64_t((kk >> 2) * (BOX >> 4) + (kk & 3) * 2);
-    mma_smem(d_tmem, q0 + step, k0 + step, idesc_f16_f32(ROWS, KV, false), kk > 0 ? 1u : 0u, leader);
+    const uint64_t at = uint64_t((kk & 3) * 2);
+    mma_smem(d_tmem, q0 + at + (kk >> 2) * (BOX >> 4), k0 + at + (kk >> 2) * (KV_BOX >> 4), idesc_f16_f32(ROWS, KV, false),
+             kk > 0 ? 1u : 0u, leader);
   }
 }
 template <int D>
@@ -240,7 +260,7 @@ __device__ __noinline__ void spare_nan(uint32_t tile, int row0, int tok0, int32_
   __syncwarp();
   for (int x = int(lane_id()); x < 16 * D / 2; x += 32) {
     const int r = row0 + x / (D / 2), d = x % (D / 2) * 2, c = d >> 3 & 7;
-    const uint32_t at = tile + uint32_t((d >> 6) * BOX + r * 128 + ((c ^ (r & 7)) << 4) + (d & 7) * 2);
+    const uint32_t at = tile + uint32_t((d >> 6) * KV_BOX + r * 128 + ((c ^ (r & 7)) << 4) + (d & 7) * 2);
     uint32_t w;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
     const bool lo = (w & 0x7FFFu) > 0x7C00u, hi = (w & 0x7FFF0000u) > 0x7C000000u;
@@ -313,20 +333,25 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   if (lane == 31) sd.warp_sum[warp] = before;
   if (tid == 0) {
     mbar_init(&bars->q_full, CONV);
-    mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->q_empty, 2);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_full[x], 4);
-      mbar_init(&bars->o_full[x], 1);
+      mbar_init(&bars->s_full[x][0], 1);
+      mbar_init(&bars->s_full[x][1], 1);
+      mbar_init(&bars->p_full[x][0], 4);
+      mbar_init(&bars->p_full[x][1], 4);
+      mbar_init(&bars->conv[x], CONV);
+      mbar_init(&bars->soft[x], 4);
+      mbar_init(&bars->o_done[x][0], 1);
+      mbar_init(&bars->o_done[x][1], 1);
       mbar_init(&bars->o_empty[x], 4);
     }
     for (int i = 0; i < KST; ++i) {
-      mbar_init(&bars->k_full[i], 8);  // groups of 16 tokens
-      mbar_init(&bars->k_empty[i], 1);
+      mbar_init(&bars->k_full[i], GROUPS);
+      mbar_init(&bars->k_empty[i], 2);
     }
     for (int i = 0; i < VST; ++i) {
-      mbar_init(&bars->v_full[i], 8);
-      mbar_init(&bars->v_empty[i], 1);
+      mbar_init(&bars->v_full[i], GROUPS);
+      mbar_init(&bars->v_empty[i], 2);
     }
     bars->abort = 0;
     fence_mbar_init();
@@ -391,8 +416,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
 
   if (warp < CONV) {
     // ---------------------------------------------------------------- conversion, item by item
-    // Item n of a segment: keys and values of 16 tokens, group n % 8 of its tile n / 8.  Warp w takes items w,
-    // w + 7, ...; the next one's codes are on their way in registers.  (The loop is kept short: with the softmax and
+    // Item n of a segment: keys and values of 16 tokens, group n % 4 of its tile n / 4.  Warp w takes items w,
+    // w + 6, ...; the next one's codes are on their way in registers.  (The loop is kept short: with the softmax and
     // the issuing loop it has to live in the instruction cache; two or three items ahead measured slower.)
     constexpr int PASS = D / 64;     // 16-code units of one thread and token
     const int r8 = lane >> 2, u4 = lane & 3;
@@ -424,7 +449,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         sd.warp_max[warp][0] = km;
         sd.warp_max[warp][1] = vm;
       }
-      named_bar_sync(1, CONV * 32);
+      ok = meet(&bars->conv[0], i & 1, abort, b.status, tmo, 14);
+      if (!ok) break;
 #pragma unroll
       for (int w = 0; w < CONV; ++w) {
         km = max(km, sd.warp_max[w][0]);
@@ -436,14 +462,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         sd.kv_exp[i & 3][1] = vm;
       }
       if (tid < D) sd.nan_at[i & 3][tid] = 0x7FFFFFFF;
-      named_bar_sync(1, CONV * 32);
+      ok = meet(&bars->conv[1], i & 1, abort, b.status, tmo, 15);
+      if (!ok) break;
 
-      const int items = (g.t1 - g.t0) * 8;
+      const int items = (g.t1 - g.t0) * GROUPS;
       const int64_t lane_off = int64_t(g.hk) * p.c.head_stride + int64_t(r8) * p.c.token_stride + u4 * 16;
       const int64_t eight = 8 * p.c.token_stride;
       uint4 ck[2 * PASS], cv[2 * PASS];  // tokens r8 and r8 + 8 of the item
       int sk = 0, sv = 0, page = -1;     // its scale bytes; the page of the item to be loaded next
-      auto group = [&](int n) { return g.t0 * 8 + n; };                               // of 16 tokens, in the sequence
+      auto group = [&](int n) { return g.t0 * GROUPS + n; };                               // of 16 tokens, in the sequence
       // gr / (page_size / 16)
       auto page_of = [&](int gr) { return p.page_magic ? int(__umulhi(uint32_t(gr), p.page_magic)) : gr; };
       auto look_up = [&](int n) {
@@ -508,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             h[k] = pack_f16x2(__uint_as_float(u[k] << 16) * down, __uint_as_float(u[k] & 0xFFFF0000u) * down);
-          const uint32_t at = smem + L::Q + uint32_t((r >> 7) * L::TILE + (c8 >> 3) * BOX + (r & 127) * 128);
+          const uint32_t at = smem + L::Q + uint32_t((r >> 7) * L::Q_TILE + (c8 >> 3) * BOX + (r & 127) * 128);
           st_shared_v4(at + (((c8 & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
           if (c8 == 0) sd.q_exp[i & 1][r] = int8_t(e);
         }
@@ -518,9 +545,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       }
 
       for (int n = warp; n < items; n += CONV) {
-        const int count = before_seg + (n >> 3), kst = count % KST, vst = count % VST;
+        const int count = before_seg + n / GROUPS, kst = count % KST, vst = count % VST;
         const uint32_t fk = block_factor(sk, km), fv = block_factor(sv, vm);
-        // the values' slot is free by then: P V of three tiles ago is issued before Q K of two tiles ago
         ok = mbar_wait(bars->k_empty + kst, uint32_t(count / KST & 1) ^ 1u, abort, b.status, tmo, 12) &&
              mbar_wait(bars->v_empty + vst, uint32_t(count / VST & 1) ^ 1u, abort, b.status, tmo, 13);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -528,14 +554,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           break;
         }
         const uint32_t ktile = smem + L::K + uint32_t(kst) * L::TILE, vtile = smem + L::V + uint32_t(vst) * L::TILE;
-        const int row0 = (n & 7) * 16;
+        const int row0 = n % GROUPS * 16;
         const uint32_t klo = ktile + uint32_t(row0 * 128) + lane_lo, khi = ktile + uint32_t(row0 * 128) + lane_hi;
         const uint32_t vlo = vtile + uint32_t(row0 * 128) + lane_lo, vhi = vtile + uint32_t(row0 * 128) + lane_hi;
 #pragma unroll
-        for (int x = 0; x < 2 * PASS; ++x) put16(klo + x / PASS * 1024 + x % PASS * BOX, khi + x / PASS * 1024 + x % PASS * BOX, ck[x], fk);
+        for (int x = 0; x < 2 * PASS; ++x) put16(klo + x / PASS * 1024 + x % PASS * KV_BOX, khi + x / PASS * 1024 + x % PASS * KV_BOX, ck[x], fk);
         load(p.c.k, ck, n + CONV);
 #pragma unroll
-        for (int x = 0; x < 2 * PASS; ++x) put16(vlo + x / PASS * 1024 + x % PASS * BOX, vhi + x / PASS * 1024 + x % PASS * BOX, cv[x], fv);
+        for (int x = 0; x < 2 * PASS; ++x) put16(vlo + x / PASS * 1024 + x % PASS * KV_BOX, vhi + x / PASS * 1024 + x % PASS * KV_BOX, cv[x], fv);
         load(p.c.v, cv, n + CONV);
         load_scales();
         page = look_up(n + 2 * CONV);
@@ -550,72 +576,60 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       before_seg += g.t1 - g.t0;
       if (!ok || !seg_next(p, g)) break;
     }
-  } else if (warp == WARP_MMA) {
-    // ---------------------------------------------------------------- the issuing warp
+  } else if (warp < WARP_SOFTMAX) {
+    // ---------------------------------------------------------------- the issuing warps, one to a query tile
     {
+      const int X = warp - WARP_MMA;
       const uint32_t leader = lane == 0, tmem = __reduce_max_sync(0xffffffffu, tmem_base);
       auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t tag) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, b.status, tmo, tag)) != 0;
       };
+      const uint64_t q0 = sdesc_sw128(smem + L::Q + X * L::Q_TILE, 16, 1024), k0 = sdesc_sw128(smem + L::K, 16, 1024);
+      const uint64_t v0 = sdesc_sw128(smem + L::V, KV_BOX, 1024);
+      constexpr uint64_t TSTEP = L::TILE >> 4;
+      const uint32_t s_tmem = tmem + X * 128, o_tmem = tmem + 256 + X * 128;
       int ks = 0, vs = 0;
       uint32_t kph = 0, vph = 0;
-      uint32_t pcount[2] = {0, 0};
-      const uint64_t q0 = sdesc_sw128(smem + L::Q, 16, 1024), k0 = sdesc_sw128(smem + L::K, 16, 1024);
-      const uint64_t v0 = sdesc_sw128(smem + L::V, BOX, 1024);
-      constexpr uint64_t TSTEP = L::TILE >> 4;
+      uint32_t scount = 0, pcount = 0;  // tiles whose S, whose O += P V has been issued
       bool ok = true;
-      for (int i = 0; ok; ++i) {
-        const uint32_t uph = uint32_t(i & 1);
-        ok = wait(&bars->q_full, uph, 21) &&
-             wait(&bars->k_full[ks], kph, 22);
-        if (!ok) break;
-        tc_fence_after();
-        const int said = int(__reduce_max_sync(0xffffffffu, uint32_t(*reinterpret_cast<volatile int32_t*>(&sd.tiles[i & 3]))));
-        const int tiles = said < 0 ? -said : said;
-        for (int X = 0; X < 2; ++X) {
-          issue_qk<D>(q0 + X * TSTEP, k0 + ks * TSTEP, tmem + X * 128, leader);
-          commit(&bars->s_full[X], leader);
-        }
-        if (tiles == 1) commit(&bars->q_empty, leader);
+      auto scores = [&](bool last) {
+        issue_qk<D>(q0, k0 + ks * TSTEP, s_tmem + (scount & 1) * 64, leader);
+        commit(&bars->s_full[X][scount & 1], leader);
         commit(&bars->k_empty[ks], leader);
+        if (last) commit(&bars->q_empty, leader);
+        ++scount;
         if (++ks == KST) {
           ks = 0;
           kph ^= 1u;
         }
+      };
+      for (int i = 0; ok; ++i) {
+        ok = wait(&bars->q_full, uint32_t(i & 1), 21);
+        if (!ok) break;
+        const int said = int(__reduce_max_sync(0xffffffffu, uint32_t(*reinterpret_cast<volatile int32_t*>(&sd.tiles[i & 3]))));
+        const int tiles = said < 0 ? -said : said;
+        for (int j = 0; j < min(tiles, 2) && ok; ++j) {  // two tiles' scores ahead
+          if (!(ok = wait(&bars->k_full[ks], kph, 22))) break;
+          tc_fence_after();
+          scores(j + 1 == tiles);
+        }
         for (int j = 0; j < tiles && ok; ++j) {
-          if (!(ok = wait(&bars->v_full[vs], vph, 23))) break;
-          for (int X = 0; X < 2; ++X) {
-            ok = wait(&bars->p_full[X], pcount[X] & 1u, 24);
-            ++pcount[X];
-            if (ok && j == 0) ok = wait(&bars->o_empty[X], uph ^ 1u, 25);
-            if (!ok) break;
+          ok = wait(&bars->v_full[vs], vph, 23) && wait(&bars->p_full[X][pcount & 1], (pcount >> 1) & 1u, 24);
+          if (ok && j == 0) ok = wait(&bars->o_empty[X], uint32_t(i & 1) ^ 1u, 25);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv<D>(s_tmem + (pcount & 1) * 64, v0 + vs * TSTEP, o_tmem, j > 0, leader);
+          commit(&bars->o_done[X][pcount & 1], leader);
+          commit(&bars->v_empty[vs], leader);
+          ++pcount;
+          if (++vs == VST) {
+            vs = 0;
+            vph ^= 1u;
+          }
+          if (j + 2 < tiles) {
+            if (!(ok = wait(&bars->k_full[ks], kph, 26))) break;
             tc_fence_after();
-            issue_pv<D>(tmem + X * 128, v0 + vs * TSTEP, tmem + 256 + X * 128, j > 0, leader);
-            if (X == 1) {
-              commit(&bars->v_empty[vs], leader);
-              if (++vs == VST) {
-                vs = 0;
-                vph ^= 1u;
-              }
-            }
-            if (j + 1 < tiles) {
-              if (X == 0) {
-                if (!(ok = wait(&bars->k_full[ks], kph, 26))) break;
-                tc_fence_after();
-              }
-              issue_qk<D>(q0 + X * TSTEP, k0 + ks * TSTEP, tmem + X * 128, leader);
-              commit(&bars->s_full[X], leader);
-              if (X == 1) {
-                if (j + 2 == tiles) commit(&bars->q_empty, leader);
-                commit(&bars->k_empty[ks], leader);
-                if (++ks == KST) {
-                  ks = 0;
-                  kph ^= 1u;
-                }
-              }
-            } else {
-              commit(&bars->o_full[X], leader);
-            }
+            scores(j + 3 == tiles);  // where P of this tile was: products run in the order they are issued in
           }
         }
         if (!ok || said < 0) break;
@@ -627,9 +641,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     const int X = (warp - WARP_SOFTMAX) >> 2;
     const int row = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem_base + lane_base + uint32_t(X * 128);
+    const uint32_t s_base = tmem_base + lane_base + uint32_t(X * 128);
     const uint32_t o_addr = tmem_base + lane_base + uint32_t(256 + X * 128);
-    uint32_t sc = 0;
+    uint32_t sc = 0, meets = 0;  // tiles so far; times that the tile's four warps have met
     bool ok = true;
     int done = 0;  // tiles of the run before this segment
     for (int i = 0;; ++i) {
@@ -637,9 +651,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const int rows = seq_rows(p, g.seq);
       const int lim = row_limit(p, g.seq, min(r, rows - 1));
       float m = -INFINITY, l = 0.0f, f = 0.0f;
-      for (int j = g.t0; j < g.t1; ++j) {
-        ok = mbar_wait(&bars->s_full[X], sc & 1u, abort, b.status, tmo, 31);
-        ++sc;
+      for (int j = g.t0; j < g.t1; ++j, ++sc) {
+        ok = mbar_wait(&bars->s_full[X][sc & 1], (sc >> 1) & 1u, abort, b.status, tmo, 31);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -650,21 +663,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           // above 0, so that a masked score stays -inf
           f = fmaxf(p.scale_log2 * pow2f(max(min(e / 2, 127), -126)) * pow2f(max(min(e - e / 2, 127), -126)), 1e-38f);
         }
-        // S is read in halves, the first one last, so that it is still in registers when P takes its place;
-        // a whole row would leave no registers for anything else
+        const uint32_t s_addr = s_base + (sc & 1) * 64;
         const int vis = lim - j * KV;
         uint32_t va[32], vb[32];
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int half = 1; half >= 0; --half) {
-          tmem_ld_32cols(s_addr + uint32_t(half * 64), va);
-          tmem_ld_32cols(s_addr + uint32_t(half * 64 + 32), vb);
-          tmem_ld_wait();
-          mask(va, vis - half * 64);
-          mask(vb, vis - half * 64 - 32);
-          mx = max3(mx, max32(va), max32(vb));
-        }
-        const float mnew = fmaxf(m, mx * f);
+        tmem_ld_32cols(s_addr, va);
+        tmem_ld_32cols(s_addr + 32u, vb);
+        tmem_ld_wait();
+        mask(va, vis);
+        mask(vb, vis - 32);
+        const float mnew = fmaxf(m, fmaxf(max32(va), max32(vb)) * f);
         const bool resc = mnew > m + kSlack;
         float alpha = 1.0f;
         if (resc) {
@@ -674,47 +681,44 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         const float add = m == -INFINITY ? kShift : kShift - m;
         float sq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        // P as fp16 pairs over the first 64 columns of S
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (half == 1) {
-            if (j > g.t0 && __any_sync(0xffffffffu, resc)) {
-#pragma unroll 1
-              for (int q = 0; q < D / 32; ++q) {
-                tmem_ld_32cols(o_addr + uint32_t(q * 32), va);
-                tmem_ld_wait();
+        // P as fp16 pairs over the first 32 columns of S
+        uint32_t w[32];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) va[k] = __float_as_uint(__uint_as_float(va[k]) * alpha);
-                tmem_st_32cols(o_addr + uint32_t(q * 32), va);
-              }
-            }
-            tmem_ld_32cols(s_addr + 64u, va);
-            tmem_ld_32cols(s_addr + 96u, vb);
+        for (int k = 0; k < 32; ++k) {
+          const uint32_t* s = k < 16 ? &va[2 * k] : &vb[2 * k - 32];
+          float p0, p1;
+          fma2(__uint_as_float(s[0]), __uint_as_float(s[1]), f, add, p0, p1);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          add2(sq[2 * (k & 1)], sq[2 * (k & 1) + 1], p0, p1);
+          w[k] = pack_f16x2(p0, p1);
+        }
+        tmem_st_32cols(s_addr, w);
+        if (j > g.t0 && __any_sync(0xffffffffu, resc)) {
+          // O holds everything up to the tile before this one once that tile's product is done
+          ok = mbar_wait(&bars->o_done[X][(sc - 1) & 1], ((sc - 1) >> 1) & 1u, abort, b.status, tmo, 33);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            tmem_ld_32cols(o_addr + uint32_t(q * 32), va);
             tmem_ld_wait();
-            mask(va, vis - 64);
-            mask(vb, vis - 96);
-          }
-          uint32_t w[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const uint32_t* s = k < 16 ? &va[2 * k] : &vb[2 * k - 32];
-            float p0, p1;
-            fma2(__uint_as_float(s[0]), __uint_as_float(s[1]), f, add, p0, p1);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            add2(sq[2 * (k & 1)], sq[2 * (k & 1) + 1], p0, p1);
-            w[k] = pack_f16x2(p0, p1);
+            for (int k = 0; k < 32; ++k) va[k] = __float_as_uint(__uint_as_float(va[k]) * alpha);
+            tmem_st_32cols(o_addr + uint32_t(q * 32), va);
           }
-          tmem_st_32cols(s_addr + uint32_t(half * 32), w);
         }
         l += (sq[0] + sq[1]) + (sq[2] + sq[3]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[X]);
+        if (lane == 0) mbar_arrive(&bars->p_full[X][sc & 1]);
       }
       if (!ok) break;
-      ok = mbar_wait(&bars->o_full[X], uint32_t(i & 1), abort, b.status, tmo, 32);
+      ok = mbar_wait(&bars->o_done[X][(sc - 1) & 1], ((sc - 1) >> 1) & 1u, abort, b.status, tmo, 32);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
@@ -765,13 +769,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         const int64_t t0 = sd.run0 + done - g.t0;
         const int64_t c0 = ((t0 + 1) * sd.ctas - 1) / sd.total, c1 = ((t0 + g.nkv) * sd.ctas - 1) / sd.total;
         __threadfence();
-        named_bar_sync(2 + X, 128);
+        ok = meet(&bars->soft[X], meets++ & 1, abort, b.status, tmo, 34);
+        if (!ok) break;
         if ((tid & 127) == 0) {
           uint32_t* counter = p.counters + 2 * c0 + X;
           sd.last[X] = atomicAdd(counter, 1u) == uint32_t(c1 - c0);
           if (sd.last[X]) *counter = 0;
         }
-        named_bar_sync(2 + X, 128);
+        ok = meet(&bars->soft[X], meets++ & 1, abort, b.status, tmo, 35);
+        if (!ok) break;
         if (sd.last[X] && row_ok) {
           __threadfence();
           const float* rows_at = p.partial + X * (D + 2) * ROWS + row;
