@@ -42,7 +42,10 @@ namespace {
 
 constexpr int MAX_TILE = 16;  // query rows of one tile: 8 or 16
 constexpr int CHUNK = 32;     // tokens of one chunk; its halves of 16 lie in one page each
-constexpr int FEW_ROWS = 64;  // query rows per kv head up to which this kernel serves a sequence
+// Query rows per kv head up to which this kernel serves a sequence.  It reads the cache once for each 16 of them (16
+// sequences of 6000: 85 us for 32 rows, 152 us for 64); the kernel for many rows takes as long for a few as for 128
+// (103 us), but has more to set up (one sequence of 16000: 36 us here for 64 rows, 67 us there).
+int few_rows(int B) { return B >= 8 ? 32 : 64; }
 constexpr int SEGMENT_COST = 24;  // what a second tile costs a CTA, in chunks (about 9000 cycles)
 constexpr float kShift = 7.0f;
 constexpr float kSlack = 8.0f;
@@ -837,7 +840,7 @@ extern "C" size_t tl_kv_attn_workspace_size(int n_tokens, int B, int H, int H_kv
     sm_count = di.sm_count;
   }
   size_t bytes = counters_bytes(sm_count) + decode_partial_bytes(sm_count, head_dim);
-  if (int64_t(n_tokens) * (H / H_kv) > FEW_ROWS) bytes += prefill_partial_bytes(sm_count, head_dim);
+  if (int64_t(n_tokens) * (H / H_kv) > few_rows(B)) bytes += prefill_partial_bytes(sm_count, head_dim);
   return bytes;
 }
 
@@ -889,7 +892,7 @@ extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
   // Most new tokens that a sequence can have, as far as the host knows
   const int most = a->max_q_len ? std::min(a->max_q_len, a->n_tokens) : std::max(1, a->n_tokens - a->B + 1);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool many = int64_t(most) * p.group > FEW_ROWS;
+  const bool many = int64_t(most) * p.group > few_rows(a->B);
   p.max_rows = 0x7FFFFFFF;
   if (many) {
     // A sequence of many rows goes to the tensor-core kernel, one of few to this file's; where there is one
@@ -908,11 +911,11 @@ extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
     f.H = a->H;
     f.group = p.group;
     f.causal = a->causal;
-    f.min_rows = a->B == 1 ? 0 : FEW_ROWS;
+    f.min_rows = a->B == 1 ? 0 : few_rows(a->B);
     f.scale_log2 = p.scale_log2;
     if (tl_status s = launch_kv_prefill(f, c.head_dim, di.sm_count, st)) return s;
     if (a->B == 1) return TL_OK;
-    p.max_rows = FEW_ROWS;
+    p.max_rows = few_rows(a->B);
   }
   // Tiles of 8 query rows where a sequence's rows of one kv head fit in one, of 16 otherwise
   const bool small = int64_t(most) * p.group <= 8;
