@@ -198,7 +198,9 @@ __device__ void route(const MoeParams& p, Smem& sm, int rows_per_tile, bool writ
   const int warp = int(warp_id()), lane = int(lane_id());
   for (int e = threadIdx.x; e < p.E; e += THREADS) sm.mask[e] = 0;
   __syncthreads();
-  if (p.E <= 64) {
+  if (p.T <= WARPS && p.E <= 64) {  // a token to a warp: the short form, for what little there is to wait for
+    if (warp < p.T) select<2, 1>(p, sm, warp, 0, write);
+  } else if (p.E <= 64) {
     for (int t = warp; t < p.T; t += 4 * WARPS) select<2, 4>(p, sm, t, WARPS, write);
   } else {
     for (int t = warp; t < p.T; t += WARPS) select<TL_MAX_EXPERTS / 32, 1>(p, sm, t, WARPS, write);
