@@ -23,9 +23,14 @@
 // single one would.  Thus keys next to a rounding border do not depend on how
 // fp32 rounds on the way.
 //
-// Bound by memory for prompts and by latency for single tokens: each row is read
-// once from memory (its partner half comes from L1) and kept in registers between
-// the maximum and the write.
+// Bound by latency for single tokens (one sequence, 32 + 8 heads: 3.2 us of GPU time
+// in a graph, 15.7 us a call with the host's share) and for prompts by the issue of
+// the exact rounding together with the pages' chain from maximum to write.  A team
+// keeps the first pass of its rows in registers between the two; the rest are read
+// and rotated again (from L2: 106 MB come from memory for the 102 MB of the rows), as
+// more rows in registers cost more in occupancy than they saved.  8192 tokens of
+// 32 + 8 heads of 128 into pages of 64: 52 us, 3.65 TB/s over the bytes read and
+// written, issue slots 65 % busy.
 #include <algorithm>
 
 #include "tl_internal.h"

@@ -3,7 +3,11 @@
 //
 //   s_j = scale <q, k_j>,  O = sum_j exp(s_j - lse) v_j,  causal within the chunk
 //
-// Bound by the tensor cores and the exponentials that feed them.  A unit is one kv
+// Bound by the round trip between tensor cores and softmax: two chunks of 2048 over
+// 12289 (32 heads, 8 kv heads of 128) take 500 us, 1100 TFLOP/s, with the tensor cores
+// 51 % busy; the products and their hand-over alone, with no exponentials, took 488 us.
+// What moved it: short loops (the instruction cache), no register spills, scores ahead.
+// A unit is one kv
 // head and 256 of a sequence's query rows, rows being (token, head of the group), so
 // that all heads of a group share every key/value tile; two 128-row tiles A and B
 // take turns, one in the softmax while the tensor cores work for the other.
@@ -423,6 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     const int r8 = lane >> 2, u4 = lane & 3;
     // where a lane's 16 dims of token r8 go: 16-byte units 2 u4 and 2 u4 + 1 of the row, swizzled by the row
     const uint32_t lane_lo = uint32_t(r8 * 128 + (((2 * u4) ^ r8) << 4)), lane_hi = uint32_t(r8 * 128 + (((2 * u4 + 1) ^ r8) << 4));
+    const int step_tk = CONV * 256 / D / p.group, step_hd = CONV * 256 / D - step_tk * p.group;  // from a lane's query row to its next
     int before_seg = 0;              // tiles of earlier segments
     bool ok = true;
     for (int i = 0; ok; ++i) {
@@ -499,50 +504,78 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         if (page < 0) sk = sv = 0;
       };
       page = look_up(warp);
-      load(p.c.k, ck, warp);
-      load(p.c.v, cv, warp);
-      load_scales();
-      page = look_up(warp + CONV);
 
-      // queries: a row to D/8 lanes
+      // Queries: a row to D/8 lanes.  Eight rows of a lane are loaded before the first is used, the first eight before the
+      // wait; row after row they took 25000 cycles a segment, as long as the products of 14 tiles (552 us -> 500 us for
+      // two chunks of 2048 over 12289; eleven rows: 515 us, spilled registers).
+      constexpr int LPR = D / 8, RPW = 32 / LPR, STRIDE = CONV * RPW;  // lanes of a row; rows of a warp, of all
+      constexpr int BATCH = 8;
+      const int c8 = lane % LPR;
+      int qr = warp * RPW + lane / LPR, tk = (g.qb * UNIT + qr) / p.group, hd = g.qb * UNIT + qr - tk * p.group;
+      uint4 qw[BATCH];
+      auto load_queries = [&]() {
+        int r = qr;
+#pragma unroll
+        for (int a = 0; a < BATCH; ++a, r += STRIDE) {
+          qw[a] = make_uint4(0, 0, 0, 0);
+          if (r < UNIT && g.qb * UNIT + r < rows)
+            qw[a] = *reinterpret_cast<const uint4*>(p.q + int64_t(g.seq.row0 + tk) * p.q_ts +
+                                                    int64_t(g.hk * p.group + hd) * p.q_hs + c8 * 8);
+          tk += step_tk;
+          hd += step_hd;
+          if (hd >= p.group) {
+            hd -= p.group;
+            ++tk;
+          }
+        }
+      };
+      load_queries();
       ok = mbar_wait(&bars->q_empty, uint32_t(i & 1) ^ 1u, abort, b.status, tmo, 11);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
-      {
-        constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp
-        const int c8 = lane % LPR;
-#pragma unroll 10
-        for (int r0 = warp * RPW; r0 < UNIT; r0 += CONV * RPW) {
-          const int r = r0 + lane / LPR, row = g.qb * UNIT + r;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (row < rows) {
-            const int tk = row / p.group;
-            w = *reinterpret_cast<const uint4*>(p.q + int64_t(g.seq.row0 + tk) * p.q_ts +
-                                                int64_t(g.hk * p.group + row - tk * p.group) * p.q_hs + c8 * 8);
-          }
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-          float amax = 0.0f;
+#pragma unroll 1
+      for (;;) {
+        float amax[BATCH];
+#pragma unroll
+        for (int a = 0; a < BATCH; ++a) {
+          const uint32_t u[4] = {qw[a].x, qw[a].y, qw[a].z, qw[a].w};
+          amax[a] = 0.0f;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
+            amax[a] = fmaxf(amax[a], fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
+        }
 #pragma unroll
-          for (int d = LPR / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-          const int e = min(max(int(__float_as_uint(amax) >> 23) - 127, -126), 127);
+        for (int d = LPR / 2; d > 0; d >>= 1) {
+#pragma unroll
+          for (int a = 0; a < BATCH; ++a) amax[a] = fmaxf(amax[a], __shfl_xor_sync(0xffffffffu, amax[a], d));
+        }
+#pragma unroll
+        for (int a = 0; a < BATCH; ++a, qr += STRIDE) {
+          const uint32_t u[4] = {qw[a].x, qw[a].y, qw[a].z, qw[a].w};
+          const int e = min(max(int(__float_as_uint(amax[a]) >> 23) - 127, -126), 127);
           const float down = pow2f(-e);
           uint32_t h[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             h[k] = pack_f16x2(__uint_as_float(u[k] << 16) * down, __uint_as_float(u[k] & 0xFFFF0000u) * down);
-          const uint32_t at = smem + L::Q + uint32_t((r >> 7) * L::Q_TILE + (c8 >> 3) * BOX + (r & 127) * 128);
-          st_shared_v4(at + (((c8 & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-          if (c8 == 0) sd.q_exp[i & 1][r] = int8_t(e);
+          if (qr < UNIT) {
+            const uint32_t at = smem + L::Q + uint32_t((qr >> 7) * L::Q_TILE + (c8 >> 3) * BOX + (qr & 127) * 128);
+            st_shared_v4(at + (((c8 & 7) ^ (qr & 7)) << 4), h[0], h[1], h[2], h[3]);
+            if (c8 == 0) sd.q_exp[i & 1][qr] = int8_t(e);
+          }
         }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->q_full);
+        if (__all_sync(0xffffffffu, qr >= UNIT)) break;
+        load_queries();
       }
+      load(p.c.k, ck, warp);
+      load(p.c.v, cv, warp);
+      load_scales();
+      page = look_up(warp + CONV);
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_full);
 
       for (int n = warp; n < items; n += CONV) {
         const int count = before_seg + n / GROUPS, kst = count % KST, vst = count % VST;
@@ -725,6 +758,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       }
       tc_fence_after();
       const float inv = l == 0.0f ? 0.0f : 1.0f / l, pe = pow2f(sd.kv_exp[i & 3][1]);
+      int least_nan = sd.nan_at[i & 3][lane];
+#pragma unroll
+      for (int k = 1; k < D / 32; ++k) least_nan = min(least_nan, sd.nan_at[i & 3][lane + 32 * k]);
+      least_nan = __reduce_min_sync(0xffffffffu, least_nan);
       const bool row_ok = r < rows;
       const bool whole = g.t0 == 0 && g.t1 == g.nkv;
       const int tk = r / p.group, head = g.hk * p.group + r - tk * p.group;
@@ -739,9 +776,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         tmem_ld_wait();
         float x[32];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          x[k] = __uint_as_float(o[k]) * inv * pe;
-          if (sd.nan_at[i & 3][c * 32 + k] < lim) x[k] = __uint_as_float(0x7FFFFFFFu);
+        for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(o[k]) * inv * pe;
+        if (least_nan < lim) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (sd.nan_at[i & 3][c * 32 + k] < lim) x[k] = __uint_as_float(0x7FFFFFFFu);
         }
         if (!row_ok) continue;
         if (whole) {

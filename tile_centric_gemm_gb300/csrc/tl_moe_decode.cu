@@ -33,6 +33,12 @@
 // h goes from launch to launch as two bf16 terms (16 bits of mantissa): the down
 // product takes one multiplication more for each, which the stream of weights
 // hides, and the result keeps the accuracy of fp32 activations.
+//
+// Bound by memory where every expert is met (27 tokens, top 2 of 27 experts of 4096 x
+// 1408: 157 us for 914 MB, 87 % of a copy's rate).  One token (29 us for 69 MB; two
+// thirds are the launches' latency: routing and join cost about 2 us in each) and rows
+// that are no whole number of lines (64 tokens over 64 experts of 2048 x 1000: 191 us,
+// 62 %: lines at the rows' ends are fetched for two strips) stay below that.
 #include <algorithm>
 #include <cmath>
 
