@@ -229,6 +229,14 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// 16 bytes to shared memory, zeros if !in.
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ld_shared_v4(uint32_t a, uint32_t& x, uint32_t& y, uint32_t& z, uint32_t& w) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w) : "r"(a) : "memory");
+}
+
 // Codes are read once here: no place in L1, which is small beside the tiles
 __device__ __forceinline__ uint4 ld_codes(const uint8_t* a) {
   uint4 r;
@@ -296,6 +304,34 @@ __device__ __forceinline__ float max32(const uint32_t (&v)[32]) {  // in four ch
     q[c] = fmaxf(q[c], __uint_as_float(v[8 * c + 7]));
   }
   return max3(q[0], q[1], fmaxf(q[2], q[3]));
+}
+
+// 32 dims of a row of each lane to memory.  Four lanes exchange theirs first, so that a store covers 64 bytes of eight
+// rows, not 16 of 32: the rows' lines are what a store costs.
+__device__ __forceinline__ void put_rows(const float (&x)[32], uint16_t* row, bool row_ok, int dim) {
+  const int lane = int(lane_id());
+  uint32_t u[4][4];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) u[k >> 2][k & 3] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      if (a & d) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & d ? u[a][k] : u[a + d][k], d);
+        if (lane & d) u[a][k] = got;
+        else u[a + d][k] = got;
+      }
+    }
+  }
+  const unsigned long long mine = row_ok ? reinterpret_cast<unsigned long long>(row + dim) : 0ull;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const unsigned long long at = __shfl_sync(0xffffffffu, mine, (lane & 28) + a);
+    if (at) st_global_v4(reinterpret_cast<uint16_t*>(at) + (lane & 3) * 8, u[a][0], u[a][1], u[a][2], u[a][3]);
+  }
 }
 
 template <int D>
@@ -427,7 +463,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     const int r8 = lane >> 2, u4 = lane & 3;
     // where a lane's 16 dims of token r8 go: 16-byte units 2 u4 and 2 u4 + 1 of the row, swizzled by the row
     const uint32_t lane_lo = uint32_t(r8 * 128 + (((2 * u4) ^ r8) << 4)), lane_hi = uint32_t(r8 * 128 + (((2 * u4 + 1) ^ r8) << 4));
-    const int step_tk = CONV * 256 / D / p.group, step_hd = CONV * 256 / D - step_tk * p.group;  // from a lane's query row to its next
+    // from a lane's query row to its next
+    const int step_tk = CONV * 256 / D / p.group, step_hd = CONV * 256 / D - step_tk * p.group;
+    const int64_t q_step = step_tk * p.q_ts + step_hd * p.q_hs, q_wrap = p.q_ts - p.group * p.q_hs;
     int before_seg = 0;              // tiles of earlier segments
     bool ok = true;
     for (int i = 0; ok; ++i) {
@@ -505,74 +543,68 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       };
       page = look_up(warp);
 
-      // Queries: a row to D/8 lanes.  Eight rows of a lane are loaded before the first is used, the first eight before the
-      // wait; row after row they took 25000 cycles a segment, as long as the products of 14 tiles (552 us -> 500 us for
-      // two chunks of 2048 over 12289; eleven rows: 515 us, spilled registers).
+      load(p.c.k, ck, warp);
+      load(p.c.v, cv, warp);
+      load_scales();
+      page = look_up(warp + CONV);
+      // Queries: a row to D/8 lanes, copied to its place in bf16, all rows at once, and brought to fp16 there by the lanes
+      // that copied it.  (Through registers, row after row, this took 25000 cycles a segment.)
       constexpr int LPR = D / 8, RPW = 32 / LPR, STRIDE = CONV * RPW;  // lanes of a row; rows of a warp, of all
-      constexpr int BATCH = 8;
-      const int c8 = lane % LPR;
-      int qr = warp * RPW + lane / LPR, tk = (g.qb * UNIT + qr) / p.group, hd = g.qb * UNIT + qr - tk * p.group;
-      uint4 qw[BATCH];
-      auto load_queries = [&]() {
-        int r = qr;
-#pragma unroll
-        for (int a = 0; a < BATCH; ++a, r += STRIDE) {
-          qw[a] = make_uint4(0, 0, 0, 0);
-          if (r < UNIT && g.qb * UNIT + r < rows)
-            qw[a] = *reinterpret_cast<const uint4*>(p.q + int64_t(g.seq.row0 + tk) * p.q_ts +
-                                                    int64_t(g.hk * p.group + hd) * p.q_hs + c8 * 8);
-          tk += step_tk;
-          hd += step_hd;
-          if (hd >= p.group) {
-            hd -= p.group;
-            ++tk;
-          }
-        }
+      const int c8 = lane % LPR, r0 = warp * RPW + lane / LPR;
+      auto place = [&](int r) {
+        return smem + L::Q + uint32_t((r >> 7) * L::Q_TILE + (c8 >> 3) * BOX + (r & 127) * 128 + (((c8 & 7) ^ (r & 7)) << 4));
       };
-      load_queries();
+      const int tk0 = (g.qb * UNIT + r0) / p.group;
+      int hd = g.qb * UNIT + r0 - tk0 * p.group;
+      const uint16_t* from = p.q + int64_t(g.seq.row0 + tk0) * p.q_ts + int64_t(g.hk * p.group + hd) * p.q_hs + c8 * 8;
       ok = mbar_wait(&bars->q_empty, uint32_t(i & 1) ^ 1u, abort, b.status, tmo, 11);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
+#pragma unroll 2
+      for (int r = r0; r < UNIT; r += STRIDE) {
+        const bool in = g.qb * UNIT + r < rows;
+        cp_async16z(place(r), in ? from : p.q, in);
+        hd += step_hd;
+        from += q_step;
+        if (hd >= p.group) {
+          hd -= p.group;
+          from += q_wrap;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
-      for (;;) {
-        float amax[BATCH];
+      for (int r1 = r0; r1 < UNIT; r1 += 4 * STRIDE) {  // four rows side by side: each is a chain of shuffles
+        uint32_t u[4][4];
+        float amax[4];
 #pragma unroll
-        for (int a = 0; a < BATCH; ++a) {
-          const uint32_t u[4] = {qw[a].x, qw[a].y, qw[a].z, qw[a].w};
+        for (int a = 0; a < 4; ++a) {
+          ld_shared_v4(place(min(r1 + a * STRIDE, UNIT - 1)), u[a][0], u[a][1], u[a][2], u[a][3]);
           amax[a] = 0.0f;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            amax[a] = fmaxf(amax[a], fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
+            amax[a] = fmaxf(amax[a], fmaxf(fabsf(__uint_as_float(u[a][k] << 16)), fabsf(__uint_as_float(u[a][k] & 0xFFFF0000u))));
         }
 #pragma unroll
         for (int d = LPR / 2; d > 0; d >>= 1) {
 #pragma unroll
-          for (int a = 0; a < BATCH; ++a) amax[a] = fmaxf(amax[a], __shfl_xor_sync(0xffffffffu, amax[a], d));
+          for (int a = 0; a < 4; ++a) amax[a] = fmaxf(amax[a], __shfl_xor_sync(0xffffffffu, amax[a], d));
         }
 #pragma unroll
-        for (int a = 0; a < BATCH; ++a, qr += STRIDE) {
-          const uint32_t u[4] = {qw[a].x, qw[a].y, qw[a].z, qw[a].w};
+        for (int a = 0; a < 4; ++a) {
+          const int r = r1 + a * STRIDE;
           const int e = min(max(int(__float_as_uint(amax[a]) >> 23) - 127, -126), 127);
           const float down = pow2f(-e);
-          uint32_t h[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            h[k] = pack_f16x2(__uint_as_float(u[k] << 16) * down, __uint_as_float(u[k] & 0xFFFF0000u) * down);
-          if (qr < UNIT) {
-            const uint32_t at = smem + L::Q + uint32_t((qr >> 7) * L::Q_TILE + (c8 >> 3) * BOX + (qr & 127) * 128);
-            st_shared_v4(at + (((c8 & 7) ^ (qr & 7)) << 4), h[0], h[1], h[2], h[3]);
-            if (c8 == 0) sd.q_exp[i & 1][qr] = int8_t(e);
+            u[a][k] = pack_f16x2(__uint_as_float(u[a][k] << 16) * down, __uint_as_float(u[a][k] & 0xFFFF0000u) * down);
+          if (r < UNIT) {
+            st_shared_v4(place(r), u[a][0], u[a][1], u[a][2], u[a][3]);
+            if (c8 == 0) sd.q_exp[i & 1][r] = int8_t(e);
           }
         }
-        if (__all_sync(0xffffffffu, qr >= UNIT)) break;
-        load_queries();
       }
-      load(p.c.k, ck, warp);
-      load(p.c.v, cv, warp);
-      load_scales();
-      page = look_up(warp + CONV);
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->q_full);
@@ -782,13 +814,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           for (int k = 0; k < 32; ++k)
             if (sd.nan_at[i & 3][c * 32 + k] < lim) x[k] = __uint_as_float(0x7FFFFFFFu);
         }
-        if (!row_ok) continue;
         if (whole) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            st_global_v4(orow + c * 32 + q * 8, pack_bf16x2(x[q * 8], x[q * 8 + 1]), pack_bf16x2(x[q * 8 + 2], x[q * 8 + 3]),
-                         pack_bf16x2(x[q * 8 + 4], x[q * 8 + 5]), pack_bf16x2(x[q * 8 + 6], x[q * 8 + 7]));
-        } else {
+          put_rows(x, orow, row_ok, c * 32);
+        } else if (row_ok) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) __stcg(mine_row + (c * 32 + k) * ROWS, x[k]);
         }
@@ -817,7 +845,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         ok = meet(&bars->soft[X], meets++ & 1, abort, b.status, tmo, 35);
         if (!ok) break;
-        if (sd.last[X] && row_ok) {
+        if (sd.last[X]) {
           __threadfence();
           const float* rows_at = p.partial + X * (D + 2) * ROWS + row;
           auto slot = [&](int64_t c) { return rows_at + (2 * c + (c == c0)) * SLOT; };
@@ -840,12 +868,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
 #pragma unroll
               for (int k = 0; k < 32; ++k) x[k] = fmaf(wgt, __ldcg(from + k * ROWS), x[k]);
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              st_global_v4(orow + q * 32 + k * 8, pack_bf16x2(x[k * 8], x[k * 8 + 1]), pack_bf16x2(x[k * 8 + 2], x[k * 8 + 3]),
-                           pack_bf16x2(x[k * 8 + 4], x[k * 8 + 5]), pack_bf16x2(x[k * 8 + 6], x[k * 8 + 7]));
+            put_rows(x, orow, row_ok, q * 32);
           }
-          if (p.lse)
+          if (p.lse && row_ok)
             p.lse[int64_t(head) * b.n_tokens + g.seq.row0 + tk] =
                 sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * 0.69314718055994531f;
         }
