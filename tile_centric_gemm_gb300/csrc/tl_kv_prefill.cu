@@ -3,10 +3,13 @@
 //
 //   s_j = scale <q, k_j>,  O = sum_j exp(s_j - lse) v_j,  causal within the chunk
 //
-// Bound by the round trip between tensor cores and softmax: two chunks of 2048 over
-// 12289 (32 heads, 8 kv heads of 128) take 500 us, 1100 TFLOP/s, with the tensor cores
-// 51 % busy; the products and their hand-over alone, with no exponentials, took 488 us.
-// What moved it: short loops (the instruction cache), no register spills, scores ahead.
+// Bound by shared memory: a tile of 64 tokens takes 1800 cycles, of which its products
+// read operands for 1024 (at 128 bytes a cycle) and the conversion writes for 256; the
+// issuing warps stand at the tensor cores' queue for 1250, the softmax is busy for 1400.
+// Two chunks of 2048 over 12289 (32 heads, 8 kv heads of 128) take 472 us, 1160 TFLOP/s.
+// What moved it: short loops (the instruction cache), no register spills, scores ahead,
+// queries and outputs of a unit in whole lines.  Scores of 128 keys at a time would read
+// a quarter less, but leave no second buffer in tensor memory.
 // A unit is one kv
 // head and 256 of a sequence's query rows, rows being (token, head of the group), so
 // that all heads of a group share every key/value tile; two 128-row tiles A and B
@@ -25,7 +28,9 @@
 // Everything is fp16 with powers of two taken out: codes are exact in fp16, and the
 // block scales enter relative to the largest of the unit's keys (values), a factor of
 // at most 1 that costs nothing above 2^-25 of it; P runs up to 2^15, with a grain of
-// 2^-31 of the largest (P <= 2^8 times 2^7 between rescales of O).
+// 2^-31 of that.  A row's reference m is its first tile's maximum and is raised, and O
+// rescaled, only when a tile's weights exp2(s - m + 7) add up to more than 2^15, so that
+// most tiles are done without looking for their maximum (482 us -> 472 us).
 //
 // The work is the list of (unit, key/value tile), cut into equal runs, one to a CTA,
 // as in the kernel for few rows: short lists fill the SMs by splitting units, long
@@ -59,7 +64,7 @@ constexpr int UNIT = 2 * ROWS;
 // Ring stages: keys of tile j + 2 are needed with values of tile j, so that many fewer of them.
 constexpr int KST = 4, VST = 6;
 constexpr int MIN_TILES = 8;     // of a CTA's run, where units are split
-constexpr float kShift = 7.0f, kSlack = 8.0f;
+constexpr float kShift = 7.0f, kMost = 32768.0f;
 constexpr uint32_t BOX = ROWS * 64 * 2;    // a query tile's rows of 64 fp16, one swizzle span wide
 constexpr uint32_t KV_BOX = KV * 64 * 2;   // a key or value tile's
 
@@ -730,33 +735,47 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         const uint32_t s_addr = s_base + (sc & 1) * 64;
         const int vis = lim - j * KV;
-        uint32_t va[32], vb[32];
-        tmem_ld_32cols(s_addr, va);
-        tmem_ld_32cols(s_addr + 32u, vb);
-        tmem_ld_wait();
-        mask(va, vis);
-        mask(vb, vis - 32);
-        const float mnew = fmaxf(m, fmaxf(max32(va), max32(vb)) * f);
-        const bool resc = mnew > m + kSlack;
-        float alpha = 1.0f;
-        if (resc) {
-          alpha = ex2_approx(m - mnew);
-          m = mnew;
-          l *= alpha;
-        }
-        const float add = m == -INFINITY ? kShift : kShift - m;
-        float sq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        // P as fp16 pairs over the first 32 columns of S
-        uint32_t w[32];
+        // P first with the maximum as it is; the sum tells whether that was enough (each weight is at most the sum, and up to
+        // 2^15 is fine).  Only if it was not is the tile's maximum taken, for the rows concerned, and P once more: on a
+        // segment's first tile, and seldom after it.
+        uint32_t va[32], w[32];
+        float sum, alpha = 1.0f;
+        bool bad = false, again = false, resc = false;
+#pragma unroll 1
+        for (;;) {
+          uint32_t vb[32];
+          tmem_ld_32cols(s_addr, va);
+          tmem_ld_32cols(s_addr + 32u, vb);
+          tmem_ld_wait();
+          mask(va, vis);
+          mask(vb, vis - 32);
+          if (again) {
+            const float mnew = fmaxf(max32(va), max32(vb)) * f;
+            resc = bad && mnew > m;
+            if (resc) {
+              alpha = ex2_approx(m - mnew);
+              m = mnew;
+              l *= alpha;
+            }
+          }
+          const float add = m == -INFINITY ? kShift : kShift - m;
+          float sq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          // P as fp16 pairs over the first 32 columns of S
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const uint32_t* s = k < 16 ? &va[2 * k] : &vb[2 * k - 32];
-          float p0, p1;
-          fma2(__uint_as_float(s[0]), __uint_as_float(s[1]), f, add, p0, p1);
-          p0 = ex2_approx(p0);
-          p1 = ex2_approx(p1);
-          add2(sq[2 * (k & 1)], sq[2 * (k & 1) + 1], p0, p1);
-          w[k] = pack_f16x2(p0, p1);
+          for (int k = 0; k < 32; ++k) {
+            const uint32_t* s = k < 16 ? &va[2 * k] : &vb[2 * k - 32];
+            float p0, p1;
+            fma2(__uint_as_float(s[0]), __uint_as_float(s[1]), f, add, p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            add2(sq[2 * (k & 1)], sq[2 * (k & 1) + 1], p0, p1);
+            w[k] = pack_f16x2(p0, p1);
+          }
+          sum = (sq[0] + sq[1]) + (sq[2] + sq[3]);
+          if (again) break;
+          bad = !(sum <= kMost) || m == -INFINITY;
+          again = __any_sync(0xffffffffu, bad) != 0;
+          if (!again) break;
         }
         tmem_st_32cols(s_addr, w);
         if (j > g.t0 && __any_sync(0xffffffffu, resc)) {
@@ -776,7 +795,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
             tmem_st_32cols(o_addr + uint32_t(q * 32), va);
           }
         }
-        l += (sq[0] + sq[1]) + (sq[2] + sq[3]);
+        l += sum;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
