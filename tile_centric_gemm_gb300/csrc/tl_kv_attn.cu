@@ -54,7 +54,10 @@ constexpr int CHUNK = 32;     // tokens of one chunk; its halves of 16 lie in on
 // sequences of 6000: 85 us for 32 rows, 152 us for 64); the kernel for many rows takes as long for a few as for 128
 // (103 us), but has more to set up (one sequence of 16000: 36 us here for 64 rows, 67 us there).
 int few_rows(int B) { return B >= 8 ? 32 : 64; }
-constexpr int SEGMENT_COST = 24;  // what a second tile costs a CTA, in chunks (about 9000 cycles)
+// What a tile costs a CTA beside its chunks, in chunks (about 9000 cycles): the list of work has that many places before a
+// tile's chunks, so that runs of equal length take equally long (16 sequences of 4 drafts over 6000: 45 -> 41 us; 200
+// single tokens over 300 each: 72 -> 57 us).
+constexpr int LEAD = 24;
 constexpr float kShift = 7.0f;
 constexpr float kSlack = 8.0f;
 
@@ -92,7 +95,8 @@ struct DecodeSmem {
 struct Segment {
   KvSeq seq;
   int s, nch, tiles, hk, rt, cb, ce;  // kv head and row tile
-  int64_t left;                       // chunks of the run from cb on
+  int o, used;                        // places of the list: of the piece's first in its tile, and how many it takes
+  int64_t left;                       // of the run from there on
 };
 
 // a / b, in 32 bits where that is enough (a 64-bit division takes about 500 cycles)
@@ -106,30 +110,34 @@ __device__ __forceinline__ int seq_tiles(const DecodeParams& p, const KvSeq& q) 
 }
 __device__ __forceinline__ int seq_chunks(const KvSeq& q) { return max(1, (q.len + CHUNK - 1) / CHUNK); }
 
+__device__ __forceinline__ void seg_cut(Segment& g, int o) {
+  g.o = o;
+  g.used = int(min(int64_t(g.nch + LEAD - o), g.left));
+  g.cb = max(0, o - LEAD);
+  g.ce = o + g.used - LEAD;  // not above cb: nothing but places that stand for a tile's cost
+}
 template <int TILE>
 __device__ __forceinline__ void seg_open(const DecodeParams& p, Segment& g, int s, int64_t off, int64_t left) {
   g.seq = kv_seq(p.b, p.c.ps, s);
   g.s = s;
   g.nch = seq_chunks(g.seq);
   g.tiles = seq_tiles<TILE>(p, g.seq);
-  const int sub = int(quotient(off, g.nch));
+  const int sub = int(quotient(off, g.nch + LEAD));
   g.hk = sub / max(g.tiles, 1);
   g.rt = sub - g.hk * g.tiles;
-  g.cb = int(off - int64_t(sub) * g.nch);
   g.left = left;
-  g.ce = int(min(int64_t(g.nch), g.cb + left));
+  seg_cut(g, int(off - int64_t(sub) * (g.nch + LEAD)));
 }
 template <int TILE>
 __device__ __forceinline__ bool seg_next(const DecodeParams& p, Segment& g) {
-  g.left -= g.ce - g.cb;
-  if (g.left <= 0) return false;
+  g.left -= g.used;
+  if (g.left <= LEAD) return false;
   if (++g.rt == g.tiles) {
     g.rt = 0;
     ++g.hk;
   }
   if (g.hk < p.c.Hkv) {
-    g.cb = 0;
-    g.ce = int(min(int64_t(g.nch), g.left));
+    seg_cut(g, 0);
     return true;
   }
   int s = g.s + 1;
@@ -221,7 +229,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     const KvSeq q = kv_seq(b, p.c.ps, s);
     const int tiles = seq_tiles<TILE>(p, q) * p.c.Hkv;
     items += uint32_t(tiles);
-    mine += int64_t(tiles) * seq_chunks(q);
+    mine += int64_t(tiles) * (seq_chunks(q) + LEAD);
   }
   int64_t before = mine;
 #pragma unroll
@@ -243,8 +251,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     all_items += sm.warp_items[w];
   }
   before -= mine;
+  const int64_t chunks = total - all_items * LEAD;
   Segment f, c;  // where copies are, and where products are
-  // A run's first chunk in the list and its length; a tile's CTAs where runs end with tiles (below 0: they do not).
+  // A run's first place in the list and the number of runs; a tile's CTAs where runs end with tiles (below 0: they do not).
   const int64_t cta = blockIdx.x;
   int64_t run0 = 0, n = 0;
   int tile_c0 = -1, tile_c1 = -1;
@@ -255,8 +264,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
   if (all_items <= int64_t(gridDim.x)) {
     // Few tiles: a CTA that works on two of them pays for two merges one after the other, so each tile is cut for
     // itself, into pieces of at most L chunks, with the least L that the CTAs suffice for.  Each warp tries one L.
-    constexpr int TRY = (SEGMENT_COST + WARPS - 2) / (WARPS - 1);
-    const int least = max(WARPS, int(quotient(total + gridDim.x - 1, gridDim.x)));
+    constexpr int TRY = (LEAD + WARPS - 2) / (WARPS - 1);
+    const int least = max(WARPS, int(quotient(chunks + gridDim.x - 1, gridDim.x)));
     uint32_t pieces = 0;
     for (int s = lane; s < b.B; s += 32) {
       const KvSeq q = kv_seq(b, p.c.ps, s);
@@ -302,14 +311,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
       c.rt = sub - c.hk * c.tiles;
       c.cb = int(quotient(int64_t(c.nch) * part, parts));
       c.ce = int(quotient(int64_t(c.nch) * (part + 1), parts));
-      c.left = c.ce - c.cb;
+      c.left = c.used = c.ce - c.cb;
       tile_c0 = int(cta) - part;
       tile_c1 = tile_c0 + parts - 1;
     }
   }
   if (tile_c0 < 0) {
     // a CTA gets a chunk for each warp at least
-    n = min(int64_t(gridDim.x), max(int64_t(1), quotient(total, WARPS)));
+    n = min(int64_t(gridDim.x), max(int64_t(1), quotient(chunks, WARPS)));
     run0 = cta < n ? quotient(cta * total, n) : 0;
     const int64_t run1 = cta < n ? quotient((cta + 1) * total, n) : 0;
     if (run0 >= run1) {
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
       int64_t at = before;
       for (int s = first; s < end; ++s) {
         const KvSeq q = kv_seq(b, p.c.ps, s);
-        const int64_t size = int64_t(seq_tiles<TILE>(p, q)) * p.c.Hkv * seq_chunks(q);
+        const int64_t size = int64_t(seq_tiles<TILE>(p, q)) * p.c.Hkv * (seq_chunks(q) + LEAD);
         if (run0 < at + size) {
           sm.begin_seq = s;
           sm.begin_off = run0 - at;
@@ -331,6 +340,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     }
     __syncthreads();
     seg_open<TILE>(p, c, sm.begin_seq, sm.begin_off, run1 - run0);
+    if (c.ce <= c.cb) {
+      pdl_wait_previous();
+      return;
+    }
   }
   f = c;
 
@@ -405,7 +418,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     cp_async_commit();
   };
   uint4 qraw[NR][KL * 2];  // row g of each product's queries, on their way while pages are looked up
-  auto load_q = [&]() {
+  auto load_q = [&](const Segment& c) {
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
       const int last = int(int64_t(c.seq.q) * p.group) - 1;
@@ -419,12 +432,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
       }
     }
   };
-  load_q();
+  load_q(c);
   for (int i = 0; i < STAGES - 1; ++i) fetch(i);
 
   // ---------------------------------------------------------------- segment by segment
   int stage = 0;
-  int64_t at = run0;  // position of c.cb in the list
+  int64_t at = run0;  // the piece's first place in the list
   while (true) {
     const int r0 = c.rt * TILE;
     const int rows = min(TILE, int(int64_t(c.seq.q) * p.group - r0));
@@ -733,7 +746,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
 
     bool done = true;
     if (c.cb != 0 || c.ce != c.nch) {
-      const int64_t t0 = at - c.cb;  // the tile's first chunk in the list
+      const int64_t t0 = at - c.o + LEAD;  // the tile's first chunk in the list
       const int64_t c0 = tile_c0 >= 0 ? tile_c0 : quotient((t0 + 1) * n - 1, total);
       const int64_t c1 = tile_c0 >= 0 ? tile_c1 : quotient((t0 + c.nch) * n - 1, total);
       constexpr int SLOT = TILE * D + 2 * TILE;
@@ -812,9 +825,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
       if (d0 == 0 && p.lse)
         p.lse[int64_t(h) * b.n_tokens + tok] = L == 0.0f ? -INFINITY : (M1 - kShift + log2f(L)) * 0.69314718055994531f;
     }
-    at += c.ce - c.cb;
+    at += c.used;
     if (!seg_next<TILE>(p, c)) break;
-    load_q();
+    load_q(c);
     __syncthreads();  // the merge buffers are free again
   }
   cp_async_wait<0>();
