@@ -98,6 +98,23 @@ def test_many_short_sequences(B):
     Call(B, Batch(q, lens, H=2, Hkv=2, D=64, ps=16, seed=7)).run().check()
 
 
+# Enough tiles for two and for four blocks to an SM, single tokens and tiles of 16 rows, some of them cut.
+@pytest.mark.parametrize("seqs", [30, 70])
+@pytest.mark.parametrize("q_len", [1, 4])
+@pytest.mark.parametrize("D,longest", [(128, 700), (64, 40), (128, 1100)])
+def test_several_blocks_of_an_sm(B, seqs, q_len, D, longest):
+    rng = np.random.default_rng(seqs + longest)
+    q = [q_len] * (seqs - 2) + [0, 1]
+    lens = [int(x) for x in rng.integers(1, longest, seqs - 3)] + [longest, 0, 1]
+    lens = [max(a, c) for a, c in zip(lens, q)]
+    b = Batch(q, lens, H=32, Hkv=8, D=D, ps=32, seed=seqs)
+    call = Call(B, b, max_q_len=q_len).run().check()
+    first = call.out.clone(), call.lse.clone()
+    call.run()
+    torch.cuda.synchronize()
+    assert torch.equal(first[0], call.out) and torch.equal(first[1], call.lse)
+
+
 @pytest.mark.parametrize("q_len", [1, 40])
 def test_rows_that_see_nothing(B, q_len):
     # sequence 0 has a new token and no length with it: an error by the batch's own count, rows empty all the same

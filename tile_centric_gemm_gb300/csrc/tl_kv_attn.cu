@@ -4,7 +4,7 @@
 //   s_j = scale <q, k_j>,  O = sum_j exp(s_j - lse) v_j
 //
 // The cache is read once; everything else is small, so the kernel is a stream of
-// pages through one CTA per SM.  The work is the list of (sequence, kv head,
+// pages through the SMs, by one CTA each where there are few tiles.  The work is the list of (sequence, kv head,
 // 16-row tile, 16-token chunk), cut into equal runs, one to a CTA: a long context
 // is spread over many CTAs and short ones share a CTA, whatever the mix.  Runs are
 // found on the device from the lengths, so the host needs no lengths.  A tile
@@ -12,7 +12,7 @@
 // sum) in the workspace; the CTA that arrives last joins them in CTA order, so
 // the result does not depend on timing.
 //
-// Inside a CTA the warps (12 for tiles of 8 rows, 8 for 16, which need the registers)
+// Inside a CTA the warps (of an SM 12 for tiles of 8 rows, 8 for 16, which need the registers)
 // take a run's chunks of 32 tokens in turn, each on its own.  Keys and values are the products' first operand (S^T = K Q^T, O^T = V^T P^T):
 // 16 tokens or dims by 8 query rows, so a tile of 8 rows wastes little of a product,
 // and a tile of 16 takes two.
@@ -40,6 +40,7 @@
 // 255 registers leave no room for more.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "tl_internal.h"
 #include "tl_kv.cuh"
@@ -58,6 +59,13 @@ int few_rows(int B) { return B >= 8 ? 32 : 64; }
 // tile's chunks, so that runs of equal length take equally long (16 sequences of 4 drafts over 6000: 45 -> 41 us; 200
 // single tokens over 300 each: 72 -> 57 us).
 constexpr int LEAD = 24;
+// CTAs of an SM, by the tiles of 8 (16) query rows that a batch has at least.  While one opens or joins a tile, which takes
+// latency and no bandwidth, the others read; but a tile cut among more CTAs takes longer to join.  For tiles of 8, with 1, 2
+// and 4 of 12, 6 and 3 warps, 8 kv heads: 200 tokens over 300 57, 39, 29 us; 76 over 1500 47, 41, 38 us; 38 over 500 23,
+// 12, 15 us; 24 over 2000 25, 21, 25 us; 19 over 500 12, 13, 14 us; one over 4099 15, 18, 29 us; 64 over 8192 132, 133, 134 us.
+// For tiles of 16, with 1 and 2 of 8 and 4 warps: 32 sequences of 4 tokens over 3000 37, 35 us; 16 over 750 14, 16 us.
+constexpr int MAX_PER_SM = 4;
+int per_sm(int64_t tiles, bool small, int sms) { return tiles <= sms ? 1 : small && tiles > 3 * sms ? 4 : 2; }
 constexpr float kShift = 7.0f;
 constexpr float kSlack = 8.0f;
 
@@ -68,17 +76,17 @@ struct DecodeParams {
   int64_t q_ts, q_hs;
   uint16_t* out;
   float* lse;
-  uint32_t* counters;  // [CTAs], zero between calls
+  uint32_t* counters;  // [CTAs], zero between calls; CTAs up to MAX_PER_SM times the SMs
   float* partial;      // [CTAs][2][TILE * D + 2 * TILE]
   int32_t H, group, causal;
   int32_t max_rows;    // sequences of more query rows per kv head are left to the kernel for many
   float scale_log2;
 };
 
-template <int D, int NR, int WARPS>
+template <int D, int NR, int WARPS, int PER_SM>
 struct DecodeSmem {
   static constexpr int TILE = 8 * NR;
-  static constexpr int STAGES = 24 / WARPS;    // 192 KB for head_dim 128
+  static constexpr int STAGES = 24 / WARPS / PER_SM;  // 192 KB of an SM for head_dim 128
   static constexpr int STAGE = CHUNK * D * 2;  // bytes of one chunk, keys and values
   uint8_t ring[WARPS][STAGES][STAGE];          // a tile's merge takes the stage that each warp used last
   float2 ml[TILE][WARPS];                      // maximum and sum of each row and warp
@@ -207,9 +215,10 @@ __device__ __forceinline__ int merge_at(int r, int c) {
 }
 
 // NR: products of 8 query rows to a tile
-template <int D, int NR, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_constant__ DecodeParams p) {
-  using Smem = DecodeSmem<D, NR, WARPS>;
+// PER_SM: CTAs of an SM
+template <int D, int NR, int WARPS, int PER_SM>
+__global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __grid_constant__ DecodeParams p) {
+  using Smem = DecodeSmem<D, NR, WARPS, PER_SM>;
   constexpr int THREADS = WARPS * 32, STAGES = Smem::STAGES;
   constexpr int TILE = 8 * NR;
   constexpr int KL = D / 64;   // 16-byte key loads of one lane and key
@@ -707,7 +716,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
     }
     if (lane == 0) sm.spare[warp] = spare;
     __syncthreads();
-    constexpr int EPT = TILE * D <= 4 * THREADS ? 4 : 8;  // elements of one thread, whole 16-byte units
+    constexpr int EPT = TILE * D <= 4 * THREADS ? 4 : TILE * D <= 8 * THREADS ? 8 : 16;  // elements of one thread, whole 16-byte units
     static_assert(D % EPT == 0 && TILE * D <= EPT * THREADS, "a tile is more than the threads' share");
     const int row = tid / (D / EPT), d0 = tid % (D / EPT) * EPT;
     const bool mine_row = row < rows;
@@ -775,7 +784,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
         L = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPT; ++i) acc[i] = 0.0f;
-        constexpr int BATCH = 8;  // slots on their way at once
+        constexpr int BATCH = EPT < 16 ? 8 : 4;  // slots on their way at once
         for (int64_t x0 = c0; x0 <= c1; x0 += BATCH) {
           float mw[BATCH], lw[BATCH];
           float4 v[BATCH][EPT / 4];
@@ -834,19 +843,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_decode_kernel(const __grid_c
   pdl_wait_previous();  // the call ends when the kernel for many rows has ended too
 }
 
-template <int D, int NR, int WARPS>
+template <int D, int NR, int WARPS, int PER_SM>
 tl_status launch_decode(void** args, int ctas, cudaStream_t st, bool early) {
-  using Smem = DecodeSmem<D, NR, WARPS>;
-  static_assert(sizeof(Smem) <= 232448, "shared memory above the per-CTA limit");
-  return launch(reinterpret_cast<const void*>(&kv_decode_kernel<D, NR, WARPS>), ctas, WARPS * 32, sizeof(Smem), st, args,
+  using Smem = DecodeSmem<D, NR, WARPS, PER_SM>;
+  static_assert(sizeof(Smem) <= 232448 / PER_SM - (PER_SM - 1) * 1024, "shared memory above the limit");
+  return launch(reinterpret_cast<const void*>(&kv_decode_kernel<D, NR, WARPS, PER_SM>), ctas * PER_SM, WARPS * 32, sizeof(Smem), st, args,
                 early);
 }
 
 // ---------------------------------------------------------------- workspace: counters, then partial tiles
 // The counters of both kernels come first, in a place that does not depend on the sizes: one workspace may serve
 // calls of many.
-size_t counters_bytes(int ctas) { return (size_t(ctas) * 3 * 4 + 255) / 256 * 256; }
-size_t decode_partial_bytes(int ctas, int D) { return size_t(ctas) * 2 * (MAX_TILE * D + 2 * MAX_TILE) * sizeof(float); }
+size_t counters_bytes(int ctas) { return (size_t(ctas) * (MAX_PER_SM + 2) * 4 + 255) / 256 * 256; }
+// (Four CTAs of an SM only with tiles of half MAX_TILE.)
+size_t decode_partial_bytes(int ctas, int D) { return size_t(ctas) * (MAX_PER_SM / 2) * 2 * (MAX_TILE * D + 2 * MAX_TILE) * sizeof(float); }
 
 }  // namespace
 }  // namespace tl
@@ -926,7 +936,7 @@ extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
     f.q_hs = p.q_hs;
     f.out = p.out;
     f.lse = p.lse;
-    f.counters = p.counters + di.sm_count;
+    f.counters = p.counters + MAX_PER_SM * di.sm_count;
     f.partial = p.partial + decode_partial_bytes(di.sm_count, c.head_dim) / sizeof(float);
     f.timeout_ns = 3 * kDefaultTimeoutNs;
     f.H = a->H;
@@ -941,6 +951,12 @@ extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
   // Tiles of 8 query rows where a sequence's rows of one kv head fit in one, of 16 otherwise
   const bool small = int64_t(most) * p.group <= 8;
   void* args[] = {&p};
-  if (c.head_dim == 128) return small ? launch_decode<128, 1, 12>(args, di.sm_count, st, many) : launch_decode<128, 2, 8>(args, di.sm_count, st, many);
-  return small ? launch_decode<64, 1, 12>(args, di.sm_count, st, many) : launch_decode<64, 2, 8>(args, di.sm_count, st, many);
+  const int per = per_sm(int64_t(a->B) * c.H_kv, small, di.sm_count);
+  auto go = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    if (!small) return per == 1 ? launch_decode<D, 2, 8, 1>(args, di.sm_count, st, many) : launch_decode<D, 2, 4, 2>(args, di.sm_count, st, many);
+    if (per == 1) return launch_decode<D, 1, 12, 1>(args, di.sm_count, st, many);
+    return per == 2 ? launch_decode<D, 1, 6, 2>(args, di.sm_count, st, many) : launch_decode<D, 1, 3, 4>(args, di.sm_count, st, many);
+  };
+  return c.head_dim == 128 ? go(std::integral_constant<int, 128>()) : go(std::integral_constant<int, 64>());
 }
