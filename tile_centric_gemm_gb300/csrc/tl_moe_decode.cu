@@ -34,11 +34,12 @@
 // product takes one multiplication more for each, which the stream of weights
 // hides, and the result keeps the accuracy of fp32 activations.
 //
-// Bound by memory where every expert is met (27 tokens, top 2 of 27 experts of 4096 x
-// 1408: 157 us for 914 MB, 87 % of a copy's rate).  One token (29 us for 69 MB; two
-// thirds are the launches' latency: routing and join cost about 2 us in each) and rows
-// that are no whole number of lines (64 tokens over 64 experts of 2048 x 1000: 191 us,
-// 62 %: lines at the rows' ends are fetched for two strips) stay below that.
+// Bound by memory where every expert is met (27 tokens, top 2 of 32 experts of 4096 x
+// 1408: 154 us for 914 MB, 89 % of a copy's rate).  One token (27 us for 69 MB) waits for
+// the launches' latency: routing, opening and join cost about 2 us each in both.  Rows
+// that are no whole number of lines (64 tokens over 64 experts of 2048 x 1000: 183 us,
+// 64 %; 162 us for 1024) are read partly twice, for two strips; the selection of 64
+// tokens takes 10 us of it.
 #include <algorithm>
 #include <cmath>
 
@@ -149,46 +150,59 @@ __device__ __forceinline__ void select(const MoeParams& p, Smem& sm, int t0, int
     }
   }
   for (int s = 0; s < p.topk; ++s) {
+    // step by step for all tokens (reductions keep their order: token by token each would wait for the last one's)
+    uint32_t best[N], most[N];
+    int at[N], e[N];
+    float val[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      uint32_t best = 0;
-      int at = 0x7FFFFFFF;
-      float val = 0.0f;
+      best[i] = 0;
+      at[i] = 0x7FFFFFFF;
+      val[i] = 0.0f;
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (key[i][j] > best) {
-          best = key[i][j];
-          at = j * 32 + lane;
-          val = v[i][j];
+        if (key[i][j] > best[i]) {
+          best[i] = key[i][j];
+          at[i] = j * 32 + lane;
+          val[i] = v[i][j];
         }
-      const uint32_t most = __reduce_max_sync(0xffffffffu, best);
-      const int e = __reduce_min_sync(0xffffffffu, best == most ? at : 0x7FFFFFFF);
-      val = __shfl_sync(0xffffffffu, val, e & 31);
-      if (lane == (e & 31)) {
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-          if (j == e >> 5) key[i][j] = 0;
-      }
-      if (lane == s) {
-        chosen[i] = val;
-        chosen_e[i] = e;
-      }
-      if (s == 0) top[i] = val;
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) most[i] = __reduce_max_sync(0xffffffffu, best[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = __reduce_min_sync(0xffffffffu, best[i] == most[i] ? at[i] : 0x7FFFFFFF);
+#pragma unroll
+    for (int i = 0; i < N; ++i) val[i] = __shfl_sync(0xffffffffu, val[i], e[i] & 31);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) key[i][j] = j * 32 + lane == e[i] ? 0u : key[i][j];
+      chosen[i] = lane == s ? val[i] : chosen[i];
+      chosen_e[i] = lane == s ? e[i] : chosen_e[i];
+      top[i] = s == 0 ? val[i] : top[i];
+    }
+  }
+  float sums[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    sums[i] = 0.0f;
+    if (p.normalize) {
+      if (lane < p.topk) sums[i] = expf(chosen[i] - top[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (j * 32 + lane < p.E) sums[i] += expf(v[i][j] - top[i]);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], d);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int t = t0 + i * step;
-    float sum = 0.0f;
-    if (p.normalize) {
-      if (lane < p.topk) sum = expf(chosen[i] - top[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (j * 32 + lane < p.E) sum += expf(v[i][j] - top[i]);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const float sum = sums[i];
     if (lane < p.topk && t < p.T) {
       const float gate = top[i] == -INFINITY && !(sum > 0.0f) ? 0.0f : expf(chosen[i] - top[i]) / sum;
       sm.ids[t][lane] = uint8_t(chosen_e[i]);
@@ -212,7 +226,7 @@ __device__ void route(const MoeParams& p, Smem& sm, int rows_per_tile, bool writ
   } else if (p.E <= 64) {
     for (int t = warp; t < p.T; t += 4 * WARPS) select<2, 4>(p, sm, t, WARPS, write);
   } else {
-    for (int t = warp; t < p.T; t += WARPS) select<TL_MAX_EXPERTS / 32, 1>(p, sm, t, WARPS, write);
+    for (int t = warp; t < p.T; t += 2 * WARPS) select<TL_MAX_EXPERTS / 32, 2>(p, sm, t, WARPS, write);
   }
   __syncthreads();
   if (warp == 0) {
