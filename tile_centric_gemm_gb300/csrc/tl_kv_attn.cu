@@ -31,13 +31,14 @@
 //    grain of 2^-31 of it, so even a tail of millions of small weights counts.
 //    Sums of P are taken in fp32 before P is rounded.
 //
-// Bound by memory when there are many tokens to read: 64 single tokens over 6000 each
-// (8 kv heads of 128): 134 us for 826 MB, 92 % of a copy's rate; one over 300000, 101 us, 91 %.
-// Copies of 64-byte half lines, which fit the products' lanes without a swizzle, ran at 75 %.
-// A single short context (14 us for 8 MB, 12 us in a graph) is a chain of loads that wait
-// for one another (lengths, page, scale and codes, merge, the join); 16-row tiles (16 drafts
-// of 8 tokens over 2000 each: 46 us, 46 % of a copy's rate) by eight warps' latency: their
-// 255 registers leave no room for more.
+// Bound by memory when there are many tokens to read: 64 single tokens over 8192 at most
+// (8 kv heads of 128): 133 us for 826 MB, 93 % of a copy's rate; three over 131072 at most,
+// 99 us for 615 MB, 93 %.  Copies of 64-byte half lines, which fit the products' lanes
+// without a swizzle, ran at 75 %.  A single short context (14 us for 8 MB, 12 us in a
+// graph) is a chain of loads that wait for one another (lengths, page, scale and codes,
+// merge, the join); 16-row tiles (16 sequences of 4 drafts over 6000 at most: 42 us for
+// 141 MB, 50 %) lose to opening and joining tiles, 8000 cycles each, and to eight warps'
+// latency: their 255 registers leave no room for more.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -53,7 +54,7 @@ constexpr int MAX_TILE = 16;  // query rows of one tile: 8 or 16
 constexpr int CHUNK = 32;     // tokens of one chunk; its halves of 16 lie in one page each
 // Query rows per kv head up to which this kernel serves a sequence.  It reads the cache once for each 16 of them (16
 // sequences of 6000: 85 us for 32 rows, 152 us for 64); the kernel for many rows takes as long for a few as for 128
-// (103 us), but has more to set up (one sequence of 16000: 36 us here for 64 rows, 67 us there).
+// (100 us), but has more to set up (one sequence of 16000: 37 us here for 64 rows, 72 us there).
 int few_rows(int B) { return B >= 8 ? 32 : 64; }
 // What a tile costs a CTA beside its chunks, in chunks (about 9000 cycles): the list of work has that many places before a
 // tile's chunks, so that runs of equal length take equally long (16 sequences of 4 drafts over 6000: 45 -> 41 us; 200
