@@ -401,7 +401,9 @@ extern "C" tl_status tl_kv_append(const tl_kv_append_args* a, void* stream) {
   p.interleaved = a->interleaved;
   p.max_pos = a->max_pos;
   const int per_seq = a->max_q_len ? std::min(a->max_q_len, a->n_tokens) : cdiv(a->n_tokens, a->B);
-  const bool wide = std::min(per_seq, c.page_size) >= 32;  // rows of a page: a whole block to its keys or values of one head
+  // A whole block to a page's keys or values of one head where a page gets 32 rows, else a warp: 8192 tokens of 8 kv heads
+  // of 128 into pages of 16, 32, 64 and 256 take 58, 54, 52 and 82 us with blocks, 54, 54, 75 and 211 us with warps.
+  const bool wide = std::min(per_seq, c.page_size) >= 32;
   const int64_t items = int64_t(a->n_tokens) / c.page_size + 2 * int64_t(a->B);
   p.groups = wide ? 2 * c.H_kv : cdiv(2 * c.H_kv, APP_THREADS / 32);
   const int64_t blocks = items * p.groups + (a->H > 0 ? a->n_tokens : 0);
