@@ -217,6 +217,27 @@ def test_a_long_tail_of_small_weights_counts(B, q_len):
     assert abs(float(c.lse[0, 0]) - (15.0 + np.log1p(tail))) < 1e-5
 
 
+# Maxima that come late: scores that rise (fall) with the token, slowly and by far more than fp16 holds, and a last key
+# above all others.
+@pytest.mark.parametrize("q_len", [1, 3, 60])
+@pytest.mark.parametrize("ramp", [1.0, 8.0, -1.0, -8.0, "last"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_scores_that_rise_along_the_sequence(B, q_len, ramp, causal):
+    n = 1500
+
+    def edit(c):
+        c.kc[:] = 0
+        c.ks[:], c.vs[:] = 127, 121
+        c.q[:] = 0
+        c.q[..., 0] = 1.0 if ramp == "last" else float(ramp)
+        for j in range(n):
+            page, slot = c.b.table[0, j // 64], j % 64
+            x = (14.0 if j == n - 1 else 0.0) if ramp == "last" else 16.0 * j / n - 8.0
+            c.kc[page, :, slot, 0] = ora.encode(x)
+    b = Batch([q_len], [n], H=4, Hkv=1, D=128, ps=64, seed=19)
+    Call(B, b, edit=edit, scale=1.0, causal=causal, max_q_len=q_len).run().check()
+
+
 def test_scale_byte_255_is_nan(B):
     def edit(c):
         c.ks[c.b.table[0, 0]] = 255
