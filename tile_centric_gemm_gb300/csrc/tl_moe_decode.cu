@@ -564,25 +564,28 @@ __global__ void __launch_bounds__(THREADS, 1) moe_decode_kernel(const __grid_con
       done = sm.last;
       if (done) {
         __threadfence();
-        for (int ms = 0; ms / SUB * TILE < rows; ++ms) {
-          const int m = ms / SUB, s = ms % SUB;
-          float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        for (int m = 0; m * TILE < rows; ++m) {
+          float v[SUB][8] = {};  // the strips' parts of a CTA on their way together
           if (m * TILE + row < rows) {
-#pragma unroll 4
+#pragma unroll 2
             for (int64_t c = c0; c <= c1; ++c) {
-              const float* src = p.partial + (2 * c + (c == c0)) * slot_size + (m * TILE + row) * (128 * SUB) + s * 64 + 4 * c4;
-              const float4 a = ld_global_cg_v4f(src), b = ld_global_cg_v4f(src + SUB * 64);
-              v[0] += a.x;
-              v[1] += a.y;
-              v[2] += a.z;
-              v[3] += a.w;
-              v[4] += b.x;
-              v[5] += b.y;
-              v[6] += b.z;
-              v[7] += b.w;
+              const float* src = p.partial + (2 * c + (c == c0)) * slot_size + (m * TILE + row) * (128 * SUB) + 4 * c4;
+#pragma unroll
+              for (int s = 0; s < SUB; ++s) {
+                const float4 a = ld_global_cg_v4f(src + s * 64), b = ld_global_cg_v4f(src + s * 64 + SUB * 64);
+                v[s][0] += a.x;
+                v[s][1] += a.y;
+                v[s][2] += a.z;
+                v[s][3] += a.w;
+                v[s][4] += b.x;
+                v[s][5] += b.y;
+                v[s][6] += b.z;
+                v[s][7] += b.w;
+              }
             }
           }
-          finish(m, s, v);
+#pragma unroll
+          for (int s = 0; s < SUB; ++s) finish(m, s, v[s]);
         }
       }
     }
