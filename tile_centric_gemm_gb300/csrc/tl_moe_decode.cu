@@ -35,10 +35,10 @@
 // hides, and the result keeps the accuracy of fp32 activations.
 //
 // Bound by memory where every expert is met (27 tokens, top 2 of 32 experts of 4096 x
-// 1408: 154 us for 914 MB, 89 % of a copy's rate).  One token (27 us for 69 MB) waits for
+// 1408: 150 us for 914 MB, 91 % of a copy's rate).  One token (27 us for 69 MB) waits for
 // the launches' latency: routing, opening and join cost about 2 us each in both.  Rows
-// that are no whole number of lines (64 tokens over 64 experts of 2048 x 1000: 183 us,
-// 64 %; 162 us for 1024) are read partly twice, for two strips; the selection of 64
+// that are no whole number of lines (64 tokens over 64 experts of 2048 x 1000: 175 us,
+// 67 %; 157 us for 1024) are read partly twice, for two strips; the selection of 64
 // tokens takes 10 us of it.
 #include <algorithm>
 #include <cmath>
