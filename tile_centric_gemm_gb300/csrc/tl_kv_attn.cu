@@ -385,6 +385,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
         for (int h = 0; h < 2; ++h) {
           const int half = ch * 2 + h;
           offs[h] = -1;
+          scale_bytes[h][0] = scale_bytes[h][1] = 0;  // the least scale there is: nothing of another tile's stays
           if (ch < f.ce && half * 16 < f.seq.len) {
             const int no = half / page_halves;
             const int page = __ldg(b.table + int64_t(f.s) * b.max_pages + no);
