@@ -615,11 +615,13 @@ tl_status tl_ag_attn(const tl_ag_attn_args* args, void* stream);
  * seq_lens[s] is its length WITH them, so its new token i has position
  * seq_lens[s] - n_s + i.  Token position p of sequence s lies in slot
  * p % page_size of page page_table[s * max_pages + p / page_size].  These arrays
- * are read on the device.  What is wrong in them (decreasing or out-of-range
- * cu_seqlens, a length below the new tokens or above max_pages * page_size, a
+ * are read on the device.  What is wrong in them (cu_seqlens that fall or leave
+ * 0..n_tokens, a length below the new tokens or above max_pages * page_size, a
  * page outside the pool) records TL_ERR_INVALID with the sequence number in the
  * signals' status word; what that sequence gets is then undefined, the other
  * sequences come out right, and nothing outside the caller's buffers is touched.
+ * A wrong entry of cu_seqlens is wrong for the two sequences that it bounds, and
+ * for those whose rows it gives to a second one.
  */
 typedef struct tl_kv_cache {
   void* k;                     /* device e4m3 codes; element (page, head, slot, d) at byte

@@ -13,8 +13,9 @@
 // Which page is which: sequence s owns the items f(s) .. f(s+1)-1 of the grid with
 // f(s) = cu[s] / page_size + 2 s.  n new tokens touch at most n / page_size + 2
 // pages, wherever they begin, and f(s+1) - f(s) is at least that, so a block
-// finds its sequence by counting the f(s) <= item: one load for each sequence,
-// all at once, and no prefix sum.
+// finds its sequence by counting the f(s) <= item: two loads for each sequence,
+// all at once, and no prefix sum.  Where the count meets entries out of order,
+// sums over the sequences that are right take its place.
 //
 // A code is ONE rounding of the exact rotated value.  x_a c is exact as p + e with
 // e = fma(x_a, c, -p); the two products' sum is exact as a pair by the two-sum
@@ -151,12 +152,83 @@ __device__ __forceinline__ void rotated8(const AppendParams& p, const uint16_t* 
   turn<EXACT>(p, w, x, t, y);
 }
 
-// Sum of one count per thread over the block.
-__device__ __forceinline__ int block_sum(int n, int* smem) {
-  n = __reduce_add_sync(0xffffffffu, n);
+// How many of the f(s) given by the functor are at or below x, over the block; and in the upper bits whether any
+// sequence's rows are out of order or out of range.
+constexpr uint32_t kOutOfOrder = 1u << 24;  // B is at most 2^20
+template <class F>
+__device__ __forceinline__ uint32_t count_below(const KvBatch& b, int x, uint32_t* smem, F f) {
+  uint32_t n = 0;
+  bool odd = false;
+  for (int s = threadIdx.x; s < b.B; s += APP_THREADS) {
+    const int c0 = b.cu[s], c1 = b.cu[s + 1];
+    n += f(s, c0) <= x;
+    odd |= c0 < 0 || c1 < c0 || c1 > b.n_tokens;
+  }
+  n = __reduce_add_sync(0xffffffffu, n + (odd ? kOutOfOrder : 0u));
   if (lane_id() == 0) smem[warp_id()] = n;
   __syncthreads();
   return smem[0] + smem[1] + smem[2] + smem[3];
+}
+
+// The same search where cu_seqlens is wrong somewhere, so that counting would go astray for sequences that are right.
+// A sequence counts if its rows are in order, in range and begin no earlier than those of the ones before it end;
+// such sequences share no row, so the grid has an item for each of their pages.  The one with token t (PAGES: with
+// item t) or -1, and its first item.  All threads of the block call it.
+template <bool PAGES>
+__device__ __noinline__ int2 find_among_wrong(const KvBatch& b, int ps, int t) {
+  __shared__ int ends[4], sums[4], found[2];
+  const int lane = int(lane_id()), warp = int(warp_id());
+  if (threadIdx.x == 0) found[0] = -1;
+  int end_before = 0, items_before = 0;
+  for (int s0 = 0; s0 < b.B; s0 += APP_THREADS) {
+    const int s = s0 + int(threadIdx.x);
+    int c0 = 0, c1 = 0;
+    if (s < b.B) {
+      c0 = b.cu[s];
+      c1 = b.cu[s + 1];
+    }
+    const bool ordered = c0 >= 0 && c1 >= c0 && c1 <= b.n_tokens;
+    int end = ordered ? c1 : 0;  // the largest end so far
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, end, d);
+      if (lane >= d) end = max(end, x);
+    }
+    if (lane == 31) ends[warp] = end;
+    __syncthreads();
+    int before = __shfl_up_sync(0xffffffffu, end, 1);
+    if (lane == 0) before = 0;
+    before = max(before, end_before);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < warp) before = max(before, ends[w]);
+      end_before = max(end_before, ends[w]);
+    }
+    const bool own = ordered && c0 >= before;
+    if (s < b.B && !own) record_error(b.status, kKvInvalid, uint32_t(s), uint32_t(c0), uint32_t(c1));
+    const int need = own && c1 > c0 ? (c1 - c0) / ps + 2 : 0;
+    int sum = need;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += x;
+    }
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+    sum += items_before;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < warp) sum += sums[w];
+      items_before += sums[w];
+    }
+    if (PAGES ? t >= sum - need && t < sum : own && t >= c0 && t < c1) {  // one thread at most
+      found[0] = s;
+      found[1] = sum - need;
+    }
+    __syncthreads();
+    if (found[0] >= 0) break;
+  }
+  return make_int2(found[0], found[1]);
 }
 
 // The least scale byte whose 448 * 2^(byte-127) holds the magnitude with these bits.
@@ -180,7 +252,7 @@ template <int D, int TEAM, int KEEP>
 __global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int UNITS = D / 8;             // threads to a row
   constexpr int STEP = TEAM / UNITS;       // rows of one pass
-  __shared__ int counts[4];
+  __shared__ uint32_t counts[4];
   __shared__ uint32_t team_max[4];
   const int tid = threadIdx.x;
   const KvBatch& b = p.b;
@@ -189,9 +261,8 @@ __global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_
   if (int(blockIdx.x) >= p.kv_blocks) {
     // ---------------------------------------------------------------- one token's queries
     const int t = int(blockIdx.x) - p.kv_blocks;
-    int n = 0;
-    for (int s = tid; s < b.B; s += APP_THREADS) n += b.cu[s] <= t;
-    const int s = block_sum(n, counts) - 1;
+    const uint32_t n = count_below(b, t, counts, [](int, int c0) { return c0; });
+    const int s = n < kOutOfOrder ? int(n) - 1 : find_among_wrong<false>(b, ps, t).x;
     if (s < 0) return;
     const KvSeq seq = kv_seq(b, ps, s);
     if (t < seq.row0 || t >= seq.row0 + seq.q) return;
@@ -232,16 +303,17 @@ __global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_
 
   // ---------------------------------------------------------------- one page's keys and values
   const int item = int(blockIdx.x) / p.groups;
-  int n = 0;
-  for (int s = tid; s < b.B; s += APP_THREADS) n += min(max(b.cu[s], 0), b.n_tokens) / ps + 2 * s <= item;
-  const int s = block_sum(n, counts) - 1;
+  const uint32_t n = count_below(b, item, counts, [ps](int s, int c0) { return c0 / ps + 2 * s; });
+  int2 at = make_int2(int(n) - 1, -1);
+  if (n >= kOutOfOrder) at = find_among_wrong<true>(b, ps, item);
+  const int s = at.x;
   const int team = (int(blockIdx.x) % p.groups) * (APP_THREADS / TEAM) + tid / TEAM;
   if (s < 0) return;
   const KvSeq seq = kv_seq(b, ps, s);
   const int start = seq.len - seq.q;
   if (seq.q == 0) return;
   const int begin = max(start, 0);
-  const int64_t page_no = begin / ps + (item - (seq.row0 / ps + 2 * s));
+  const int64_t page_no = begin / ps + (item - (at.y >= 0 ? at.y : seq.row0 / ps + 2 * s));
   const int64_t page_begin = page_no * ps;
   if (page_begin >= seq.len || page_no < begin / ps) return;
   const int lo = max(int(page_begin), begin);                    // new positions in the page
