@@ -647,8 +647,8 @@ typedef struct tl_kv_cache {
  * For each page that receives tokens and each kv head, with amax the largest
  * finite magnitude of the new rows: need = the least byte with
  * amax <= 448 * 2^(need-127) (0 for an all-zero block); the block's byte becomes
- * max(need, its byte before) when the page holds earlier tokens of the sequence,
- * and need when the new tokens begin the page.  Each code is the exact rotated
+ * max(need, its byte before) when the page holds earlier tokens of the sequence
+ * (so a block of byte 255 stays NaN), and need when the new tokens begin the page.  Each code is the exact rotated
  * value rounded ONCE to nearest even, whatever fp32 would have rounded before.
  * One launch.  Calling it again with the same arguments gives the same cache.
  * A page must not receive tokens of two sequences in one call.

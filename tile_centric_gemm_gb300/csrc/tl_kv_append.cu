@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_
   const int slot0 = lo - int(page_begin), rows = hi - lo;
   const int src0 = seq.row0 + (lo - start);
   const int member = tid % TEAM, u = member % UNITS, r0 = member / UNITS;
-  const int old = slot0 > 0 ? min(int(*scale_at), 254) : 0;
+  const int old = slot0 > 0 ? int(*scale_at) : 0;
 
   float y[KEEP][8];
   uint32_t amax = 0;
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_
     __syncwarp();  // the scale is read by the whole team before one of it writes it
   }
   const int byte = max(old, scale_need(amax));
-  const float inv = pow2f(127 - byte);
+  const float inv = byte == 255 ? __uint_as_float(0x00200000u) : pow2f(127 - byte);  // 255: NaN it was and stays
   if (slot0 > 0 && byte > old) {
     const float f = pow2f(max(old - byte, -127));
     for (int i = member; i < slot0 * (D / 16); i += TEAM) {
