@@ -69,6 +69,10 @@ constexpr int MAX_PER_SM = 4;
 int per_sm(int64_t tiles, bool small, int sms) { return tiles <= sms ? 1 : small && tiles > 3 * sms ? 4 : 2; }
 constexpr float kShift = 7.0f;
 constexpr float kSlack = 8.0f;
+// Value blocks whose scale is within 2^kNear of the largest so far share a reference with it; above 2^kFar, what was
+// summed before would leave fp32.
+constexpr int kNear = 6, kFar = 60;
+constexpr int kOwn = 1000;  // above all scales: once a row has its own reference it keeps it
 
 struct DecodeParams {
   KvCacheDev c;
@@ -91,8 +95,9 @@ struct DecodeSmem {
   static constexpr int STAGE = CHUNK * D * 2;  // bytes of one chunk, keys and values
   uint8_t ring[WARPS][STAGES][STAGE];          // a tile's merge takes the stage that each warp used last
   float2 ml[TILE][WARPS];                      // maximum and sum of each row and warp
+  int32_t e[TILE][WARPS];                      // what the row's sums are in units of: 2^e
   uint2 meta[WARPS][STAGES];  // scale bytes (k, v of the first half, k, v of the second); which halves' pages are good
-  int32_t e[WARPS], spare[WARPS];
+  int32_t spare[WARPS];
   int64_t warp_sum[WARPS];
   int32_t warp_items[WARPS];
   int64_t begin_off;
@@ -385,7 +390,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
         for (int h = 0; h < 2; ++h) {
           const int half = ch * 2 + h;
           offs[h] = -1;
-          scale_bytes[h][0] = scale_bytes[h][1] = 0;  // the least scale there is: nothing of another tile's stays
+          scale_bytes[h][0] = scale_bytes[h][1] = h ? scale_bytes[0][1] : 0u;  // nothing of another tile's stays
           if (ch < f.ce && half * 16 < f.seq.len) {
             const int no = half / page_halves;
             const int page = __ldg(b.table + int64_t(f.s) * b.max_pages + no);
@@ -508,7 +513,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
       m[x][0] = m[x][1] = -INFINITY;
       l[x][0] = l[x][1] = 0.0f;
     }
-    int ve = -127;
+    int ve = -128;  // O is in units of 2^ve, the largest value scale of the tile's chunks so far; kOwn: of a row's own, sm.e
 
     for (int ch = c.cb + warp; ch < c.ce; ch += WARPS) {
       cp_async_wait<STAGES - 2>();
@@ -566,9 +571,50 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
           raise |= mx[x][y] > m[x][y] + kSlack;
         }
       const int vb[2] = {int((meta.x >> 8) & 0xFFu), int(meta.x >> 24)};
-      const int vtop = max(vb[0] == 255 ? -127 : vb[0] - 127, vb[1] == 255 ? -127 : vb[1] - 127);
-      if (__any_sync(0xffffffffu, raise) || vtop > ve) {
-        const float down = pow2f(max(min(ve - vtop, 0), -127));
+      // of both halves (one that does not exist has the other's); far below what O is in units of, far above it, or NaN
+      const int vtop = max(vb[0], vb[1]) - 127, vlow = min(vb[0], vb[1]) - 127;
+      const bool far = max(ve, vtop) - vlow > kNear || vtop > 127 || (vtop - ve > kFar && ve > -128);
+      if (far) {
+        // a reference for each row: see the head of the file
+        if (ve != kOwn) {
+          if (g == 0) {
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) sm.e[8 * x + 2 * t + y][warp] = ve;
+          }
+          __syncwarp();
+          ve = kOwn;
+        }
+        const bool has[2] = {(meta.y & 1u) && vb[0] != 255, (meta.y & 2u) && vb[1] != 255};
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float mo = m[x][y], mn = fmaxf(mo, mx[x][y]);
+            int32_t* at = &sm.e[8 * x + 2 * t + y][warp];
+            const int eo = *at;
+            int e = mo == -INFINITY ? -1000 : eo + int(ceilf(fmaxf(mo - mn, -1000.0f)));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float mh = column_max(fmaxf(s[h][x][y], s[h][x][2 + y]));
+              if (has[h] && mh > -INFINITY) e = max(e, vb[h] - 127 + int(ceilf(fmaxf(mh - mn, -1000.0f))));
+            }
+            e = max(e, -127);
+            if (mo != mn) l[x][y] *= ex2_approx(mo - mn);
+            const float a = mo == -INFINITY ? 1.0f : ex2_approx(mo - mn + float(eo - e));
+            m[x][y] = mn;
+#pragma unroll
+            for (int i = 0; i < MTS; ++i) {
+              o[x][i][y] *= a;
+              o[x][i][2 + y] *= a;
+            }
+            __syncwarp();
+            if (g == 0) *at = e;
+          }
+        __syncwarp();
+      } else if (__any_sync(0xffffffffu, raise) || vtop > ve) {
+        const float down = pow2f(min(ve - vtop, 0));
         ve = max(ve, vtop);
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
@@ -589,8 +635,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
       }
       uint32_t pb[2][NR][2];  // P^T: tokens (2t, 2t+1) and (2t+8, 2t+9) of the half, row g
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float vf = vb[h] == 255 ? 1.0f : pow2f(max(vb[h] - 127 - ve, -127));  // 255: its codes count as NaN
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
 #pragma unroll
@@ -600,10 +645,38 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
           }
           l[x][0] += s[h][x][0] + s[h][x][2];
           l[x][1] += s[h][x][1] + s[h][x][3];
-          pb[h][x][0] = transposed(pack_f16x2(s[h][x][0] * vf, s[h][x][1] * vf));
-          pb[h][x][1] = transposed(pack_f16x2(s[h][x][2] * vf, s[h][x][3] * vf));
+        }
+      if (far) {
+        const bool has[2] = {(meta.y & 1u) && vb[0] != 255, (meta.y & 2u) && vb[1] != 255};
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int e = sm.e[8 * x + 2 * t + y][warp];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float f = has[h] ? pow2f(min(max(vb[h] - 127 - e, -127), 127)) : 1.0f;  // 255: its codes count as NaN
+              s[h][x][y] *= f;
+              s[h][x][2 + y] *= f;
+            }
+          }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float vf = pow2f(vb[h] - 127 - ve);
+#pragma unroll
+          for (int x = 0; x < NR; ++x)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[h][x][k] *= vf;
         }
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+          pb[h][x][0] = transposed(pack_f16x2(s[h][x][0], s[h][x][1]));
+          pb[h][x][1] = transposed(pack_f16x2(s[h][x][2], s[h][x][3]));
+        }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t vw[4][VB / 4];
@@ -697,9 +770,13 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         l[x][y] = column_sum(l[x][y]);
-        if (g == 0) sm.ml[8 * x + 2 * t + y][warp] = make_float2(m[x][y], l[x][y]);
+        if (g == 0) {
+          const int r = 8 * x + 2 * t + y;
+          sm.ml[r][warp] = make_float2(m[x][y], l[x][y]);
+          if (m[x][y] == -INFINITY) sm.e[r][warp] = -127;  // it saw nothing
+          else if (ve != kOwn) sm.e[r][warp] = ve;
+        }
       }
-    if (lane == 0) sm.e[warp] = ve;
     const int spare = stage == 0 ? STAGES - 1 : stage - 1;  // the stage that this warp's next copy will fill
     {
       float4* buf = reinterpret_cast<float4*>(sm.ring[warp][spare]);
@@ -727,10 +804,9 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
     if (mine_row) {
       int em = -127;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        em = max(em, sm.e[w]);
-        M1 = fmaxf(M1, sm.ml[row][w].x);
-      }
+      for (int w = 0; w < WARPS; ++w) M1 = fmaxf(M1, sm.ml[row][w].x);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) em = max(em, sm.e[row][w] + int(ceilf(fmaxf(sm.ml[row][w].x - M1, -1000.0f))));
 #pragma unroll
       for (int i = 0; i < EPT; ++i) acc[i] = 0.0f;
 #pragma unroll 4
@@ -739,7 +815,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
         const float2 ml = sm.ml[row][w];
         const float a = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : ml.y) : ex2_approx(ml.x - M1);
         L = fmaf(a, ml.x == -INFINITY ? 1.0f : ml.y, L);
-        const float av = a * pow2f(max(sm.e[w] - em, -127));
+        const float av = ml.x == -INFINITY ? a : ex2_approx(ml.x - M1 + float(sm.e[row][w] - em));
         const float4* buf = reinterpret_cast<const float4*>(sm.ring[w][sm.spare[w]]);
 #pragma unroll
         for (int u = 0; u < EPT / 4; ++u) {
