@@ -65,6 +65,7 @@ constexpr int UNIT = 2 * ROWS;
 constexpr int KST = 4, VST = 6;
 constexpr int MIN_TILES = 8;     // of a CTA's run, where units are split
 constexpr float kShift = 7.0f, kMost = 32768.0f;
+constexpr float kGreat = 16777216.0f;  // from here on the rounding of a score is as much as the span of a softmax
 constexpr uint32_t BOX = ROWS * 64 * 2;    // a query tile's rows of 64 fp16, one swizzle span wide
 constexpr uint32_t KV_BOX = KV * 64 * 2;   // a key or value tile's
 
@@ -234,6 +235,14 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 // 16 bytes to shared memory, zeros if !in.
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
@@ -337,6 +346,28 @@ __device__ __forceinline__ void put_rows(const float (&x)[32], uint16_t* row, bo
     const unsigned long long at = __shfl_sync(0xffffffffu, mine, (lane & 28) + a);
     if (at) st_global_v4(reinterpret_cast<uint16_t*>(at) + (lane & 3) * 8, u[a][0], u[a][1], u[a][2], u[a][3]);
   }
+}
+
+// P of a tile with great scores, and its sum.  Elsewhere s f - m is one fused operation, whose product is not rounded as the
+// maximum m was: of scores above 2^27 the largest would come out beyond what P holds, or vanish.
+__device__ __noinline__ float great_tile(uint32_t s_addr, int vis, float f, float add) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // P of 32 tokens takes 16 columns: over scores that have been read
+    uint32_t v[32], w[16];
+    tmem_ld_32cols(s_addr + uint32_t(h * 32), v);
+    tmem_ld_wait();
+    mask(v, vis - 32 * h);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float p0 = ex2_approx(__fadd_rn(__fmul_rn(__uint_as_float(v[2 * k]), f), add));
+      const float p1 = ex2_approx(__fadd_rn(__fmul_rn(__uint_as_float(v[2 * k + 1]), f), add));
+      sum += p0 + p1;
+      w[k] = pack_f16x2(p0, p1);
+    }
+    tmem_st_16cols(s_addr + uint32_t(h * 16), w);
+  }
+  return sum;
 }
 
 template <int D>
@@ -750,7 +781,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           mask(va, vis);
           mask(vb, vis - 32);
           if (again) {
-            const float mnew = fmaxf(max32(va), max32(vb)) * f;
+            const float mnew = __fmul_rn(fmaxf(max32(va), max32(vb)), f);
             resc = bad && mnew > m;
             if (resc) {
               alpha = ex2_approx(m - mnew);
@@ -773,11 +804,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           }
           sum = (sq[0] + sq[1]) + (sq[2] + sq[3]);
           if (again) break;
-          bad = !(sum <= kMost) || m == -INFINITY;
+          bad = !(sum <= kMost) || !(fabsf(m) < kGreat);  // (m = -infinity: none yet)
           again = __any_sync(0xffffffffu, bad) != 0;
           if (!again) break;
         }
-        tmem_st_32cols(s_addr, w);
+        if (again && __any_sync(0xffffffffu, fabsf(m) >= kGreat && m != -INFINITY))
+          sum = great_tile(s_addr, vis, f, m == -INFINITY ? kShift : kShift - m);
+        else
+          tmem_st_32cols(s_addr, w);
         if (j > g.t0 && __any_sync(0xffffffffu, resc)) {
           // O holds everything up to the tile before this one once that tile's product is done
           ok = mbar_wait(&bars->o_done[X][(sc - 1) & 1], ((sc - 1) >> 1) & 1u, abort, b.status, tmo, 33);
