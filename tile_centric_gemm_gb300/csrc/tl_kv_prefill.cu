@@ -25,10 +25,10 @@
 //                keys each round trip from scores to P and back was waited for
 //                (590 us for two chunks of 2048 over 12289).
 //   warps 8-11   softmax of tile A, warps 12-15 of tile B, a row to a thread.
-// Everything is fp16 with powers of two taken out: codes are exact in fp16, and the
-// block scales enter relative to the largest of the unit's keys (values), a factor of
-// at most 1 that costs nothing above 2^-25 of it; P runs up to 2^15, with a grain of
-// 2^-31 of that.  A row's reference m is its first tile's maximum and is raised, and O
+// Everything is fp16 with powers of two taken out: codes are exact in fp16, also times
+// the block scales relative to the largest of the segment's keys (values), as long as
+// these lie within 2^15 of each other.  Where they do not, codes stay as they are and the
+// scales enter in the softmax (far_tile).  P runs up to 2^15, with a grain of 2^-24.  A row's reference m is its first tile's maximum and is raised, and O
 // rescaled, only when a tile's weights exp2(s - m + 7) add up to more than 2^15, so that
 // most tiles are done without looking for their maximum (482 us -> 472 us).
 //
@@ -65,6 +65,8 @@ constexpr int UNIT = 2 * ROWS;
 constexpr int KST = 4, VST = 6;
 constexpr int MIN_TILES = 8;     // of a CTA's run, where units are split
 constexpr float kShift = 7.0f, kMost = 32768.0f;
+constexpr int kNear = 15;  // codes (the least is 2^-9) are exact in fp16 (2^-24) relative to a scale up to 2^this larger
+constexpr int kFar = 1000;
 constexpr float kGreat = 16777216.0f;  // from here on the rounding of a score is as much as the span of a softmax
 constexpr uint32_t BOX = ROWS * 64 * 2;    // a query tile's rows of 64 fp16, one swizzle span wide
 constexpr uint32_t KV_BOX = KV * 64 * 2;   // a key or value tile's
@@ -86,7 +88,8 @@ struct Layout {
 struct Side {
   Bars bars;
   int8_t q_exp[2][UNIT];   // rows' exponents, by segment parity
-  int32_t kv_exp[4][2];    // exponents of the segment's keys and values
+  int16_t kv_exp[4][2];    // exponents of the segment's keys and values; kFar in place of the keys': of each 16 tokens' own
+  uint16_t far[8][GROUPS]; // these tokens' scale bytes (keys' and values'), by tile
   union {
     int32_t nan_at[4][128];  // least token whose value is NaN in the dim, among those not all rows see
     struct {                 // before the segments: sums of the work list
@@ -94,7 +97,7 @@ struct Side {
       uint32_t warp_units[16];
     };
   };
-  int32_t warp_max[CONV][2];
+  int8_t warp_range[CONV][4];
   int64_t total, ctas, run0;  // tiles of all runs, runs, this run's first tile
   int32_t begin[4];           // sequence, kv head, row block, tile
   int32_t tiles[4];           // of the segments in work
@@ -348,26 +351,73 @@ __device__ __forceinline__ void put_rows(const float (&x)[32], uint16_t* row, bo
   }
 }
 
-// P of a tile with great scores, and its sum.  Elsewhere s f - m is one fused operation, whose product is not rounded as the
-// maximum m was: of scores above 2^27 the largest would come out beyond what P holds, or vanish.
-__device__ __noinline__ float great_tile(uint32_t s_addr, int vis, float f, float add) {
-  float sum = 0.0f;
+// scale * 2^e, finite and above 0, so that a masked score stays -infinity
+__device__ __forceinline__ float score_factor(float scale, int e) {
+  return fmaxf(scale * pow2f(max(min(e / 2, 127), -126)) * pow2f(max(min(e - e / 2, 127), -126)), 1e-38f);
+}
+
+// A tile's softmax where the scales of the segment's blocks are far apart: S holds products with the codes as they are.
+// The scales of 16 tokens' keys enter their scores in fp32; those of their values multiply P relative to 2^e, e a
+// row's own: at least what the largest product of weight and scale asks for among the keys that the row sees, so that
+// P is at most 2^7 and neither a block that the row does not see nor one of little weight costs the others bits.
+// Returns the row's reference, its sum, e, and what O so far has to be multiplied by.
+// Without scale bytes (nullptr): f is the factor of all scores, e stays 0.  This is for great scores.  Elsewhere s f - m
+// is one fused operation, whose product is not rounded as the maximum m was: of scores above 2^27 the largest would come
+// out beyond what P holds, or vanish.
+__device__ __noinline__ float4 far_tile(uint32_t s_addr, int vis, const volatile uint16_t* bytes, float scale, int qe, float m,
+                                        float l, int e) {
+  float most[GROUPS], f[GROUPS];
+  int vb[GROUPS];
+  float mn = m;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {  // P of 32 tokens takes 16 columns: over scores that have been read
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[32];
+    tmem_ld_32cols(s_addr + uint32_t(h * 32), v);
+    tmem_ld_wait();
+    mask(v, vis - 32 * h);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t b = bytes ? bytes[2 * h + q] : 127u | 127u << 8;
+      const int kb = int(b & 0xFFu);
+      f[2 * h + q] = score_factor(scale, qe + (kb == 255 ? 0 : kb - 127));  // 255: the codes are NaN
+      vb[2 * h + q] = int(b >> 8);
+      float x = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[16 * q + k]));
+      most[2 * h + q] = __fmul_rn(x, f[2 * h + q]);
+      mn = fmaxf(mn, most[2 * h + q]);
+    }
+  }
+  int en = m == -INFINITY ? -1000 : e + int(ceilf(fmaxf(m - mn, -1000.0f)));
+#pragma unroll
+  for (int q = 0; q < GROUPS; ++q)
+    if (vb[q] != 255 && most[q] > -INFINITY) en = max(en, vb[q] - 127 + int(ceilf(fmaxf(most[q] - mn, -1000.0f))));
+  en = max(en, -127);
+  const float alpha = m == -INFINITY ? 1.0f : ex2_approx(m - mn + float(e - en));
+  if (m != mn) l *= ex2_approx(m - mn);
+  const float add = mn == -INFINITY ? kShift : kShift - mn;
+  float sum = 0.0f;
+  // P of 32 tokens takes 16 columns: over scores that have been read
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
     uint32_t v[32], w[16];
     tmem_ld_32cols(s_addr + uint32_t(h * 32), v);
     tmem_ld_wait();
     mask(v, vis - 32 * h);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float p0 = ex2_approx(__fadd_rn(__fmul_rn(__uint_as_float(v[2 * k]), f), add));
-      const float p1 = ex2_approx(__fadd_rn(__fmul_rn(__uint_as_float(v[2 * k + 1]), f), add));
-      sum += p0 + p1;
-      w[k] = pack_f16x2(p0, p1);
+    for (int q = 0; q < 2; ++q) {
+      const float c = vb[2 * h + q] == 255 ? 1.0f : pow2f(min(max(vb[2 * h + q] - 127 - en, -127), 127));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float p0 = ex2_approx(__fadd_rn(__fmul_rn(__uint_as_float(v[16 * q + 2 * k]), f[2 * h + q]), add));
+        const float p1 = ex2_approx(__fadd_rn(__fmul_rn(__uint_as_float(v[16 * q + 2 * k + 1]), f[2 * h + q]), add));
+        sum += p0 + p1;
+        w[8 * q + k] = pack_f16x2(p0 * c, p1 * c);
+      }
     }
     tmem_st_16cols(s_addr + uint32_t(h * 16), w);
   }
-  return sum;
+  return make_float4(mn, l + sum, float(en), alpha);
 }
 
 template <int D>
@@ -511,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const int32_t* table = b.table + int64_t(g.s) * b.max_pages;
       // the largest scales of the segment's pages
       const int tok_end = min(len, g.t1 * KV);
-      int km = -127, vm = -127;
+      int km = -127, vm = -127, kl = 127, vl = 127;
       for (int pg = g.t0 * KV / p.c.ps + tid; pg * int64_t(p.c.ps) < tok_end; pg += CONV * 32) {
         const int page = __ldg(table + pg);
         if (page < 0 || page >= p.c.num_pages) {
@@ -519,26 +569,39 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           continue;
         }
         const int kb = p.c.ks[int64_t(page) * p.c.Hkv + g.hk], vb = p.c.vs[int64_t(page) * p.c.Hkv + g.hk];
-        if (kb != 255) km = max(km, kb - 127);
-        if (vb != 255) vm = max(vm, vb - 127);
+        if (kb != 255) {
+          km = max(km, kb - 127);
+          kl = min(kl, kb - 127);
+        }
+        if (vb != 255) {
+          vm = max(vm, vb - 127);
+          vl = min(vl, vb - 127);
+        }
       }
       km = __reduce_max_sync(0xffffffffu, km);
       vm = __reduce_max_sync(0xffffffffu, vm);
+      kl = __reduce_min_sync(0xffffffffu, kl);
+      vl = __reduce_min_sync(0xffffffffu, vl);
       if (lane == 0) {
-        sd.warp_max[warp][0] = km;
-        sd.warp_max[warp][1] = vm;
+        sd.warp_range[warp][0] = int8_t(km);
+        sd.warp_range[warp][1] = int8_t(vm);
+        sd.warp_range[warp][2] = int8_t(kl);
+        sd.warp_range[warp][3] = int8_t(vl);
       }
       ok = meet(&bars->conv[0], i & 1, abort, b.status, tmo, 14);
       if (!ok) break;
 #pragma unroll
       for (int w = 0; w < CONV; ++w) {
-        km = max(km, sd.warp_max[w][0]);
-        vm = max(vm, sd.warp_max[w][1]);
+        km = max(km, int(sd.warp_range[w][0]));
+        vm = max(vm, int(sd.warp_range[w][1]));
+        kl = min(kl, int(sd.warp_range[w][2]));
+        vl = min(vl, int(sd.warp_range[w][3]));
       }
+      if (km - kl > kNear || vm - vl > kNear) km = kFar;
       if (tid == 0) {
         sd.tiles[i & 3] = g.left > g.t1 - g.t0 ? g.t1 - g.t0 : g.t0 - g.t1;  // the run's last one: negative
-        sd.kv_exp[i & 3][0] = km;
-        sd.kv_exp[i & 3][1] = vm;
+        sd.kv_exp[i & 3][0] = int16_t(km);
+        sd.kv_exp[i & 3][1] = int16_t(vm);
       }
       if (tid < D) sd.nan_at[i & 3][tid] = 0x7FFFFFFF;
       ok = meet(&bars->conv[1], i & 1, abort, b.status, tmo, 15);
@@ -647,7 +710,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
 
       for (int n = warp; n < items; n += CONV) {
         const int count = before_seg + n / GROUPS, kst = count % KST, vst = count % VST;
-        const uint32_t fk = block_factor(sk, km), fv = block_factor(sv, vm);
+        const uint32_t fk = block_factor(sk, km == kFar ? sk - 127 : km), fv = block_factor(sv, km == kFar ? sv - 127 : vm);
+        const uint16_t bytes = uint16_t(sk | sv << 8);
         ok = mbar_wait(bars->k_empty + kst, uint32_t(count / KST & 1) ^ 1u, abort, b.status, tmo, 12) &&
              mbar_wait(bars->v_empty + vst, uint32_t(count / VST & 1) ^ 1u, abort, b.status, tmo, 13);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -670,6 +734,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
+          // (a softmax has read these when the scores two tiles on are issued, and the ring of keys is four tiles long)
+          if (km == kFar) sd.far[count & 7][n % GROUPS] = bytes;
           mbar_arrive(bars->k_full + kst);
           mbar_arrive(bars->v_full + vst);
         }
@@ -752,6 +818,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const int rows = seq_rows(p, g.seq);
       const int lim = row_limit(p, g.seq, min(r, rows - 1));
       float m = -INFINITY, l = 0.0f, f = 0.0f;
+      int e = kFar;  // O is in units of 2^e where scales are far apart
       for (int j = g.t0; j < g.t1; ++j, ++sc) {
         ok = mbar_wait(&bars->s_full[X][sc & 1], (sc >> 1) & 1u, abort, b.status, tmo, 31);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -760,9 +827,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         tc_fence_after();
         if (j == g.t0) {
-          const int e = int(sd.q_exp[i & 1][X * ROWS + row]) + sd.kv_exp[i & 3][0];
-          // above 0, so that a masked score stays -inf
-          f = fmaxf(p.scale_log2 * pow2f(max(min(e / 2, 127), -126)) * pow2f(max(min(e - e / 2, 127), -126)), 1e-38f);
+          const int qe = int(sd.q_exp[i & 1][X * ROWS + row]), ke = sd.kv_exp[i & 3][0];
+          if (ke == kFar) e = -127;
+          else f = score_factor(p.scale_log2, qe + ke);
         }
         const uint32_t s_addr = s_base + (sc & 1) * 64;
         const int vis = lim - j * KV;
@@ -770,10 +837,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         // 2^15 is fine).  Only if it was not is the tile's maximum taken, for the rows concerned, and P once more: on a
         // segment's first tile, and seldom after it.
         uint32_t va[32], w[32];
-        float sum, alpha = 1.0f;
+        float sum = 0.0f, alpha = 1.0f;
         bool bad = false, again = false, resc = false;
 #pragma unroll 1
-        for (;;) {
+        while (e == kFar) {
           uint32_t vb[32];
           tmem_ld_32cols(s_addr, va);
           tmem_ld_32cols(s_addr + 32u, vb);
@@ -808,10 +875,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           again = __any_sync(0xffffffffu, bad) != 0;
           if (!again) break;
         }
-        if (again && __any_sync(0xffffffffu, fabsf(m) >= kGreat && m != -INFINITY))
-          sum = great_tile(s_addr, vis, f, m == -INFINITY ? kShift : kShift - m);
-        else
+        const bool far = e != kFar;
+        if (far || (again && __any_sync(0xffffffffu, fabsf(m) >= kGreat && m != -INFINITY))) {
+          const float4 r = far ? far_tile(s_addr, vis, sd.far[sc & 7], p.scale_log2, sd.q_exp[i & 1][X * ROWS + row], m, l, e)
+                               : far_tile(s_addr, vis, nullptr, f, 0, m, l, 0);
+          m = r.x;
+          l = r.y;
+          sum = 0.0f;
+          if (far) e = int(r.z);
+          alpha *= r.w;
+          resc = alpha != 1.0f;
+        } else {
           tmem_st_32cols(s_addr, w);
+        }
         if (j > g.t0 && __any_sync(0xffffffffu, resc)) {
           // O holds everything up to the tile before this one once that tile's product is done
           ok = mbar_wait(&bars->o_done[X][(sc - 1) & 1], ((sc - 1) >> 1) & 1u, abort, b.status, tmo, 33);
@@ -842,7 +918,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         break;
       }
       tc_fence_after();
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l, pe = pow2f(sd.kv_exp[i & 3][1]);
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l, pe = pow2f(e == kFar ? sd.kv_exp[i & 3][1] : e);
       int least_nan = sd.nan_at[i & 3][lane];
 #pragma unroll
       for (int k = 1; k < D / 32; ++k) least_nan = min(least_nan, sd.nan_at[i & 3][lane + 32 * k]);
