@@ -669,7 +669,7 @@ typedef struct tl_kv_append_args {
   int64_t k_token_stride, k_head_stride;  /* elements, multiples of 8 */
   int64_t v_token_stride, v_head_stride;
   int64_t q_token_stride, q_head_stride;
-  void* q_out;                 /* device bf16 [n_tokens, H, head_dim], written */
+  void* q_out;                 /* device bf16 [n_tokens, H, head_dim], written; must not overlap q */
   const float* cos;            /* device float [max_pos, rot_dim/2]; NULL when rot_dim = 0 */
   const float* sin;
   const int32_t* cu_seqlens;   /* device int32 [B + 1] */

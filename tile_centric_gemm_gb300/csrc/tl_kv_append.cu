@@ -400,6 +400,14 @@ __global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_
   }
 }
 
+// Whether any of n rows of `span` bytes, `stride` apart from `rows` on, meets the `bytes` at `block`.
+bool rows_meet(const void* rows, int64_t stride, int64_t span, int64_t n, const void* block, int64_t bytes) {
+  const int64_t at = int64_t(reinterpret_cast<uintptr_t>(block)) - int64_t(reinterpret_cast<uintptr_t>(rows));
+  // row t is [t stride, t stride + span): the first that ends behind the block's begin
+  const int64_t t = at < span || stride == 0 ? 0 : (at - span) / stride + 1;
+  return t < n && t * stride + span > at && t * stride < at + bytes;
+}
+
 }  // namespace
 
 // Checks shared by the cache's calls (tl_kv_attn too).
@@ -446,6 +454,10 @@ extern "C" tl_status tl_kv_append(const tl_kv_append_args* a, void* stream) {
   for (int64_t s : {a->k_token_stride, a->k_head_stride, a->v_token_stride, a->v_head_stride, a->q_token_stride,
                     a->q_head_stride})
     if (s < 0 || s % 8) return fail(TL_ERR_INVALID, "tl_kv_append: strides must be multiples of 8 elements");
+  // A row's dims are read by the threads of both of a pair's units, with no order between them and the writes.
+  if (a->H > 0 && rows_meet(a->q, a->q_token_stride * 2, (int64_t(a->H - 1) * a->q_head_stride + D) * 2, a->n_tokens,
+                            a->q_out, int64_t(a->n_tokens) * a->H * D * 2))
+    return fail(TL_ERR_INVALID, "tl_kv_append: q_out overlaps q");
   DeviceInfo di{};
   if (tl_status s = device_info(&di)) return s;
   if (a->signals->device != di.device)
