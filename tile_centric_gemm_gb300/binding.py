@@ -570,42 +570,53 @@ _kv_append, _kv_attn, _moe_decode = _packed("tl_kv_append"), _packed("tl_kv_attn
 _torch = None
 
 
-def _raw_stream(stream):
+def _place(stream):
+    """(The stream's handle, the number of the current device): where a call's kernels run, and its tensors have to be."""
     global _torch
     if _torch is None:
         import torch
         torch.cuda.init()
         _torch = torch
-    if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
-    return _stream(stream)
+    dev = _torch._C._cuda_getDevice()
+    return (_torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)), dev
 
 
-def _address(t):
-    return 0 if t is None else t.data_ptr()
+def _mistyped(t, what, dtype, shape, dev):
+    raise ValueError(f"{what}: a tensor on device cuda:{dev} of {dtype} and shape {tuple(shape)}, not {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _mistyped(t, what, dtype, shape):
-    raise ValueError(f"{what}: a {'' if shape is None else 'contiguous '}CUDA tensor of {dtype}"
-                     f"{'' if shape is None else f' and shape {tuple(shape)}'}, not {t.dtype} {tuple(t.shape)} on {t.device}"
-                     f"{'' if t.is_contiguous() else ', not contiguous'}")
-
-
-def _typed(t, what, dtype, shape=None):
-    """t is a CUDA tensor of this type (and shape, contiguous, where one is given); its address."""
-    if t.dtype is not dtype or not t.is_cuda or (shape is not None and (t.shape != shape or not t.is_contiguous())):
-        _mistyped(t, what, dtype, shape)
+def _typed(t, what, dtype, shape, dev):
+    """t is a contiguous tensor of this type and shape on CUDA device `dev`; its address."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _mistyped(t, what, dtype, shape, dev)
     return t.data_ptr()
 
 
-def _rows(t, what, dtype, shape):
-    """A CUDA tensor [tokens, heads, dim] whose dims lie next to one another: its address and outer strides."""
-    if t.dtype is not dtype or not t.is_cuda or t.shape != shape:
-        _mistyped(t, what, dtype, shape)
+def _rows(t, what, dtype, shape, dev):
+    """A tensor [tokens, heads, dim] on CUDA device `dev` whose dims lie next to one another: its address and outer strides."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _mistyped(t, what, dtype, shape, dev)
     a, b, c = t.stride()
     if c != 1:
         raise ValueError(f"{what}: the dims of a head must lie next to one another")
     return t.data_ptr(), a, b
+
+
+def _scratch(t, dev):
+    """Address and size of a call's workspace."""
+    if t is None:
+        return 0, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on device cuda:{dev}, not on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _held(x, dev):
+    """A cache or weights whose tensors are on CUDA device `dev`."""
+    if x.device != dev:
+        raise ValueError(f"{type(x).__name__}: its tensors are on cuda:{x.device}, the current device is cuda:{dev}")
 
 
 class KvCache:
@@ -626,17 +637,19 @@ class KvCache:
         for t in (k_scale, v_scale):
             if tuple(t.shape) != tuple(k.shape[:2]) or t.element_size() != 1 or not t.is_contiguous() or not t.is_cuda:
                 raise ValueError("KvCache: scales are contiguous [num_pages, H_kv] CUDA tensors of bytes")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.get_device()
+        if any(t.get_device() != self.device for t in (v, k_scale, v_scale)):
+            raise ValueError("KvCache: codes and scales must be on one device")
         self.num_pages, self.H_kv, self.page_size, self.head_dim = k.shape
         self.fields = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.stride(0), k.stride(1),
                        k.stride(2), self.num_pages, self.page_size, self.H_kv, self.head_dim)
 
 
-def _batch(cu_seqlens, seq_lens, page_table, int32):
+def _batch(cu_seqlens, seq_lens, page_table, int32, dev):
     """(B, columns of the page table, the three addresses) of a ragged batch, its arrays' types checked."""
     B, max_pages = page_table.shape
-    return (B, max_pages, _typed(cu_seqlens, "cu_seqlens", int32, (B + 1,)), _typed(seq_lens, "seq_lens", int32, (B,)),
-            _typed(page_table, "page_table", int32, (B, max_pages)))
+    return (B, max_pages, _typed(cu_seqlens, "cu_seqlens", int32, (B + 1,), dev), _typed(seq_lens, "seq_lens", int32, (B,), dev),
+            _typed(page_table, "page_table", int32, (B, max_pages), dev))
 
 
 def tl_kv_append(cache: KvCache, k, v, cu_seqlens, seq_lens, page_table, signals: Signals, *, q=None, q_out=None,
@@ -644,24 +657,25 @@ def tl_kv_append(cache: KvCache, k, v, cu_seqlens, seq_lens, page_table, signals
     """Append k, v [n, H_kv, D] (bf16; views of a fused projection will do) to the cache, k rotated by the
     tables cos, sin [positions, rot_dim/2] at each token's position; q [n, H, D] rotated into q_out
     (see tilelink.h).  No tables: no rotation."""
-    st = _raw_stream(stream)
+    st, dev = _place(stream)
     bf16, f32 = _torch.bfloat16, _torch.float32
     n, D = k.shape[0], cache.head_dim
-    B, max_pages, cu, lens, table = _batch(cu_seqlens, seq_lens, page_table, _torch.int32)
-    kp, ka, kb = _rows(k, "k", bf16, (n, cache.H_kv, D))
-    vp, va, vb = _rows(v, "v", bf16, (n, cache.H_kv, D))
+    _held(cache, dev)
+    B, max_pages, cu, lens, table = _batch(cu_seqlens, seq_lens, page_table, _torch.int32, dev)
+    kp, ka, kb = _rows(k, "k", bf16, (n, cache.H_kv, D), dev)
+    vp, va, vb = _rows(v, "v", bf16, (n, cache.H_kv, D), dev)
     H = qp = qa = qb = out = rot = max_pos = cp = sp = 0
     if q is not None or q_out is not None:
         if q is None or q_out is None:
             raise ValueError("q and q_out go together")
         H = q.shape[1]
-        qp, qa, qb = _rows(q, "q", bf16, (n, H, D))
-        out = _typed(q_out, "q_out", bf16, (n, H, D))
+        qp, qa, qb = _rows(q, "q", bf16, (n, H, D), dev)
+        out = _typed(q_out, "q_out", bf16, (n, H, D), dev)
     if cos is not None or sin is not None:
         if cos is None or sin is None:
             raise ValueError("cos and sin go together")
         max_pos, rot = cos.shape
-        cp, sp = _typed(cos, "cos", f32, (max_pos, rot)), _typed(sin, "sin", f32, (max_pos, rot))
+        cp, sp = _typed(cos, "cos", f32, (max_pos, rot), dev), _typed(sin, "sin", f32, (max_pos, rot), dev)
         rot *= 2
     code = _kv_append(_APPEND.pack(n, B, H, rot, bool(interleaved), max_pos, max_pages, max_q_len, *cache.fields, kp, vp, qp,
                                    ka, kb, va, vb, qa, qb, out, cp, sp, cu, lens, table, signals.handle.value), st)
@@ -677,17 +691,18 @@ def tl_kv_attn(q, cache: KvCache, out, cu_seqlens, seq_lens, page_table, workspa
                scale=0.0, max_q_len=0, lse=None, stream=None):
     """out [n, H, D] = attention of q [n, H, D] over each sequence's keys and values in the cache, the new
     tokens' included; lse optional float [H, n] (see tilelink.h)."""
-    st = _raw_stream(stream)
+    st, dev = _place(stream)
     bf16 = _torch.bfloat16
     n, H, D = q.shape
     if D != cache.head_dim:
         raise ValueError(f"q: head dim {D}, the cache's is {cache.head_dim}")
-    B, max_pages, cu, lens, table = _batch(cu_seqlens, seq_lens, page_table, _torch.int32)
-    qp, qa, qb = _rows(q, "q", bf16, (n, H, D))
+    _held(cache, dev)
+    B, max_pages, cu, lens, table = _batch(cu_seqlens, seq_lens, page_table, _torch.int32, dev)
+    qp, qa, qb = _rows(q, "q", bf16, (n, H, D), dev)
     code = _kv_attn(_ATTN.pack(n, B, H, bool(causal), max_pages, max_q_len, scale, 0, *cache.fields, qp, qa, qb,
-                               _typed(out, "out", bf16, (n, H, D)),
-                               0 if lse is None else _typed(lse, "lse", _torch.float32, (H, n)), cu, lens, table,
-                               _address(workspace), _nbytes(workspace), signals.handle.value), st)
+                               _typed(out, "out", bf16, (n, H, D), dev),
+                               0 if lse is None else _typed(lse, "lse", _torch.float32, (H, n), dev), cu, lens, table,
+                               *_scratch(workspace, dev), signals.handle.value), st)
     if code:
         _check(code)
 
@@ -703,9 +718,12 @@ class MoeWeights:
         self.E, (self.H, two_I), (self.I, self.Hd) = len(W1), W1[0].shape, W2[0].shape
         if two_I != 2 * self.I:
             raise ValueError(f"MoeWeights: W1 has {two_I} columns, W2 has {self.I} rows: twice as many are wanted")
+        self.device = W1[0].get_device()
+        if self.device < 0:
+            raise ValueError("MoeWeights: the matrices are on a CUDA device")
         for w1, w2 in zip(W1, W2):
-            _typed(w1, "W1", torch.bfloat16, (self.H, two_I))
-            _typed(w2, "W2", torch.bfloat16, (self.I, self.Hd))
+            _typed(w1, "W1", torch.bfloat16, (self.H, two_I), self.device)
+            _typed(w2, "W2", torch.bfloat16, (self.I, self.Hd), self.device)
         self.W1, self.W2 = W1, W2
         self.pointers = _ptr_array(W1), _ptr_array(W2)
         self.addresses = tuple(ctypes.addressof(p) for p in self.pointers)
@@ -718,12 +736,13 @@ def tl_moe_decode_workspace_size(T, topk, E, H, I, Hd):
 def tl_moe_decode(x, logits, weights: MoeWeights, out, ids, gates, workspace, *, normalize=True, stream=None):
     """out [T, Hd] = the mixture-of-experts layer of x [T, H] under the router's logits [T, E]; the chosen experts
     and their gates into ids and gates [T, topk] (see tilelink.h)."""
-    st = _raw_stream(stream)
+    st, dev = _place(stream)
     bf16, f32, w = _torch.bfloat16, _torch.float32, weights
     T, topk = ids.shape
-    code = _moe_decode(_MOE.pack(T, w.H, w.I, w.Hd, w.E, topk, bool(normalize), 0, _typed(x, "x", bf16, (T, w.H)),
-                                 _typed(logits, "logits", f32, (T, w.E)), *w.addresses, _typed(out, "out", bf16, (T, w.Hd)),
-                                 _typed(ids, "ids", _torch.int32, (T, topk)), _typed(gates, "gates", f32, (T, topk)),
-                                 _address(workspace), _nbytes(workspace)), st)
+    _held(w, dev)
+    code = _moe_decode(_MOE.pack(T, w.H, w.I, w.Hd, w.E, topk, bool(normalize), 0, _typed(x, "x", bf16, (T, w.H), dev),
+                                 _typed(logits, "logits", f32, (T, w.E), dev), *w.addresses,
+                                 _typed(out, "out", bf16, (T, w.Hd), dev), _typed(ids, "ids", _torch.int32, (T, topk), dev),
+                                 _typed(gates, "gates", f32, (T, topk), dev), *_scratch(workspace, dev)), st)
     if code:
         _check(code)
