@@ -220,6 +220,21 @@ __device__ __forceinline__ int merge_at(int r, int c) {
   return r * (D / 4) + (c ^ ((c >> 3) & 3) ^ ((r >> 1) & 3));
 }
 
+// A row's own reference (at `at`, 2^e) and maximum (mo, now mn) move on: h0 and h1 are the lane's largest scores of a chunk's
+// halves, b0 and b1 their value scales' bytes.  Returns what the row's sum and its O have to be multiplied by.
+__device__ __noinline__ float2 own_reference(int32_t* at, float mo, float mn, float h0, float h1, int b0, int b1) {
+  const int eo = *at;
+  h0 = column_max(h0);
+  h1 = column_max(h1);
+  int e = mo == -INFINITY ? -127 : max(eo + int(ceilf(fmaxf(mo - mn, -1000.0f))), -127);
+  if (b0 != 255 && h0 > -INFINITY) e = max(e, b0 - 127 + int(ceilf(fmaxf(h0 - mn, -1000.0f))));
+  if (b1 != 255 && h1 > -INFINITY) e = max(e, b1 - 127 + int(ceilf(fmaxf(h1 - mn, -1000.0f))));
+  __syncwarp();
+  if (lane_id() < 4) *at = e;
+  __syncwarp();
+  return make_float2(mo != mn ? ex2_approx(mo - mn) : 1.0f, mo == -INFINITY ? 1.0f : ex2_approx(mo - mn + float(eo - e)));
+}
+
 // NR: products of 8 query rows to a tile
 // PER_SM: CTAs of an SM
 template <int D, int NR, int WARPS, int PER_SM>
@@ -593,26 +608,17 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
           for (int y = 0; y < 2; ++y) {
             const float mo = m[x][y], mn = fmaxf(mo, mx[x][y]);
             int32_t* at = &sm.e[8 * x + 2 * t + y][warp];
-            const int eo = *at;
-            int e = mo == -INFINITY ? -1000 : eo + int(ceilf(fmaxf(mo - mn, -1000.0f)));
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float mh = column_max(fmaxf(s[h][x][y], s[h][x][2 + y]));
-              if (has[h] && mh > -INFINITY) e = max(e, vb[h] - 127 + int(ceilf(fmaxf(mh - mn, -1000.0f))));
-            }
-            e = max(e, -127);
-            if (mo != mn) l[x][y] *= ex2_approx(mo - mn);
-            const float a = mo == -INFINITY ? 1.0f : ex2_approx(mo - mn + float(eo - e));
+            const float2 r = own_reference(at, mo, mn, fmaxf(s[0][x][y], s[0][x][2 + y]), fmaxf(s[1][x][y], s[1][x][2 + y]),
+                                           has[0] ? vb[0] : 255, has[1] ? vb[1] : 255);
+            l[x][y] *= r.x;
+            const float a = r.y;
             m[x][y] = mn;
 #pragma unroll
             for (int i = 0; i < MTS; ++i) {
               o[x][i][y] *= a;
               o[x][i][2 + y] *= a;
             }
-            __syncwarp();
-            if (g == 0) *at = e;
           }
-        __syncwarp();
       } else if (__any_sync(0xffffffffu, raise) || vtop > ve) {
         const float down = pow2f(min(ve - vtop, 0));
         ve = max(ve, vtop);
@@ -635,7 +641,8 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
       }
       uint32_t pb[2][NR][2];  // P^T: tokens (2t, 2t+1) and (2t+8, 2t+9) of the half, row g
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        const float vf = pow2f(min(vb[h] - 127 - ve, 0));
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
 #pragma unroll
@@ -645,38 +652,18 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
           }
           l[x][0] += s[h][x][0] + s[h][x][2];
           l[x][1] += s[h][x][1] + s[h][x][3];
-        }
-      if (far) {
-        const bool has[2] = {(meta.y & 1u) && vb[0] != 255, (meta.y & 2u) && vb[1] != 255};
+          float c[2] = {vf, vf};
+          if (far) {
 #pragma unroll
-        for (int x = 0; x < NR; ++x)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int e = sm.e[8 * x + 2 * t + y][warp];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float f = has[h] ? pow2f(min(max(vb[h] - 127 - e, -127), 127)) : 1.0f;  // 255: its codes count as NaN
-              s[h][x][y] *= f;
-              s[h][x][2 + y] *= f;
+            for (int y = 0; y < 2; ++y) {
+              const int d = vb[h] - 127 - sm.e[8 * x + 2 * t + y][warp];
+              c[y] = vb[h] != 255 ? pow2f(min(max(d, -127), 127)) : 1.0f;  // 255: its codes count as NaN
             }
           }
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float vf = pow2f(vb[h] - 127 - ve);
-#pragma unroll
-          for (int x = 0; x < NR; ++x)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[h][x][k] *= vf;
+          pb[h][x][0] = transposed(pack_f16x2(s[h][x][0] * c[0], s[h][x][1] * c[1]));
+          pb[h][x][1] = transposed(pack_f16x2(s[h][x][2] * c[0], s[h][x][3] * c[1]));
         }
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int x = 0; x < NR; ++x) {
-          pb[h][x][0] = transposed(pack_f16x2(s[h][x][0], s[h][x][1]));
-          pb[h][x][1] = transposed(pack_f16x2(s[h][x][2], s[h][x][3]));
-        }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t vw[4][VB / 4];
