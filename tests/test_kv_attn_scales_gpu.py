@@ -119,3 +119,46 @@ def test_nan_blocks_beside_large_ones(B, q_len):
     want = expected_rows(b, f64(c.q), c.kc, c.ks, c.vc, c.vs, True, b.D ** -0.5)
     keep = np.r_[0:q_len - 1, q_len:q_len + 2]
     check_rows(out[keep], lse[:, keep], want[0][keep], want[1][:, keep], want[2][keep], want[3][:, keep])
+
+
+def falling_weights(c, step):
+    """Every page's values are 2^step larger than the page's before and its weights about as much smaller (step 0: the second
+    half of the pages 2^28 larger): all pages count alike."""
+    c.q[..., 5] = 1.0
+    c.rng = np.random.default_rng(48)
+    for s in range(len(c.b.q)):
+        pages = -(-c.b.lens[s] // c.b.ps)
+        for j in range(pages):
+            up = step * j if step else 28 * (2 * j >= pages)
+            page = c.b.table[s, j]
+            c.vs[page] = 115 + up
+            c.ks[page] = 127
+            c.kc[page] = 0
+            c.kc[page, :, :, 5] = ora_code(-up * 0.6931 * c.b.D ** 0.5)
+            c.kc[page, :, :, 6] = c.kc[page, :, :, 7] = ora_code(c.rng.standard_normal(c.kc[page, :, :, 6].shape) * 4)
+
+
+# Enough tiles that a warp goes through many chunks of one tile.
+@pytest.mark.parametrize("layout,q_len", [(dict(H=8, Hkv=8, D=128, ps=64), 1), (dict(H=16, Hkv=4, D=64, ps=64), 4),
+                                          (dict(H=16, Hkv=4, D=128, ps=32), 4)])
+@pytest.mark.parametrize("step", [0, 1, 2, 4])
+def test_scales_that_rise_as_weights_fall(B, layout, q_len, step):
+    seqs = 160
+    rng = np.random.default_rng(47)
+    lens = [int(x) for x in rng.integers(200, 400, seqs)]
+    check(B, Batch([q_len] * seqs, lens, seed=47, **layout), lambda c: falling_weights(c, step))
+
+
+@pytest.mark.parametrize("q_len,n,seqs", [(1, 37, 1), (1, 37, 40), (3, 60, 300), (16, 700, 2), (1, 3000, 3)])
+@pytest.mark.parametrize("score", [20.0, 96.0, 400.0])
+def test_large_values_of_no_weight(B, q_len, n, seqs, score):
+    """One key has all the weight and values of 2^-80; the last page's values are 2^134 larger and have none."""
+    def edit(c):
+        c.q[:] = 0
+        c.q[..., 5] = 1.0
+        c.kc[:, :, :, 5] = 0
+        c.ks[:], c.vs[:] = 127, 120
+        for s in range(seqs):
+            c.vs[c.b.table[s, 0]], c.vs[c.b.table[s, n // 16]] = 47, 181
+            c.kc[c.b.table[s, 0], :, 3, 5] = ora_code(score)
+    check(B, Batch([q_len] * seqs, [n] * seqs, H=2, Hkv=1, D=64, ps=16, seed=51), edit, causal=False, scale=1.0)

@@ -5,7 +5,7 @@
 //
 // The cache is read once; everything else is small, so the kernel is a stream of
 // pages through the SMs, by one CTA each where there are few tiles.  The work is the list of (sequence, kv head,
-// 16-row tile, 16-token chunk), cut into equal runs, one to a CTA: a long context
+// tile of 8 or 16 rows, 32-token chunk), cut into equal runs, one to a CTA: a long context
 // is spread over many CTAs and short ones share a CTA, whatever the mix.  Runs are
 // found on the device from the lengths, so the host needs no lengths.  A tile
 // whose chunks fall to several CTAs leaves partial results (mean value, maximum,
@@ -23,21 +23,27 @@
 //    into a ring of its own, so no barrier stands between copy and use; P^T comes from
 //    S^T by 8 x 8 transpositions in registers (movmatrix).
 //  * e4m3 to fp16 is exact (one conversion for two codes).  Queries are brought
-//    to fp16 by a power of two for each row, exact but below 2^-25 of the row's
-//    largest element.  The K scale multiplies the scores, the V scale of the
-//    half chunk relative to the largest seen multiplies P, both powers of two.
+//    to fp16 by a power of two for each row, off by at most 2^-25 of the row's
+//    largest element.  The K scale multiplies the scores in fp32, the V scale of the
+//    half chunk relative to a reference multiplies P, both powers of two.
+//  * That reference is one for the warp's rows while the V scales that it meets lie within
+//    2^3 of the first ones, as they mostly do (64 single tokens over 8192 take 134 us with it
+//    and 137 us without, 16 drafts of 4 over 6000 41 and 49 us).  Otherwise each row has its own,
+//    2^e with e at least what the largest product of weight and scale asks for among the keys
+//    that the row sees: P times the scale relative to 2^e is at most 2^7, and a block that the
+//    row does not see, or hardly, takes no bits from the others.
 //  * P is kept as exp2(s - m + 7) with m raised only when a score passes it by 8:
 //    at most 2^15, in fp16 with full precision down to 2^-21 of the largest and a
 //    grain of 2^-31 of it, so even a tail of millions of small weights counts.
 //    Sums of P are taken in fp32 before P is rounded.
 //
 // Bound by memory when there are many tokens to read: 64 single tokens over 8192 at most
-// (8 kv heads of 128): 133 us for 826 MB, 93 % of a copy's rate; three over 131072 at most,
-// 99 us for 615 MB, 93 %.  Copies of 64-byte half lines, which fit the products' lanes
-// without a swizzle, ran at 75 %.  A single short context (14 us for 8 MB, 12 us in a
+// (8 kv heads of 128): 135 us for 826 MB, 91 % of a copy's rate; three over 131072 at most,
+// 101 us for 615 MB, 91 %.  Copies of 64-byte half lines, which fit the products' lanes
+// without a swizzle, ran at 75 %.  A single short context (14 us for 8 MB, 13 us in a
 // graph) is a chain of loads that wait for one another (lengths, page, scale and codes,
-// merge, the join); 16-row tiles (16 sequences of 4 drafts over 6000 at most: 42 us for
-// 141 MB, 50 %) lose to opening and joining tiles, 8000 cycles each, and to eight warps'
+// merge, the join); 16-row tiles (16 sequences of 4 drafts over 6000 at most: 43 us for
+// 141 MB, 49 %) lose to opening and joining tiles, 8000 cycles each, and to eight warps'
 // latency: their 255 registers leave no room for more.
 #include <algorithm>
 #include <cmath>
@@ -69,9 +75,9 @@ constexpr int MAX_PER_SM = 4;
 int per_sm(int64_t tiles, bool small, int sms) { return tiles <= sms ? 1 : small && tiles > 3 * sms ? 4 : 2; }
 constexpr float kShift = 7.0f;
 constexpr float kSlack = 8.0f;
-// Value blocks whose scale is within 2^kNear of the largest so far share a reference with it; above 2^kFar, what was
-// summed before would leave fp32.
-constexpr int kNear = 6, kFar = 60;
+// A warp's reference for a tile's value blocks is 2^kRoom above the first ones' scale; it serves scales up to it and down
+// to 2^kNear below.
+constexpr int kRoom = 3, kNear = 6;
 constexpr int kOwn = 1000;  // above all scales: once a row has its own reference it keeps it
 
 struct DecodeParams {
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
       m[x][0] = m[x][1] = -INFINITY;
       l[x][0] = l[x][1] = 0.0f;
     }
-    int ve = -128;  // O is in units of 2^ve, the largest value scale of the tile's chunks so far; kOwn: of a row's own, sm.e
+    int ve = -128;  // O is in units of 2^ve (-128: nothing yet); kOwn: of a row's own, sm.e
 
     for (int ch = c.cb + warp; ch < c.ce; ch += WARPS) {
       cp_async_wait<STAGES - 2>();
@@ -586,10 +592,14 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
           raise |= mx[x][y] > m[x][y] + kSlack;
         }
       const int vb[2] = {int((meta.x >> 8) & 0xFFu), int(meta.x >> 24)};
-      // of both halves (one that does not exist has the other's); far below what O is in units of, far above it, or NaN
+      // of both halves (one that does not exist has the other's; 255 is above any reference)
       const int vtop = max(vb[0], vb[1]) - 127, vlow = min(vb[0], vb[1]) - 127;
-      const bool far = max(ve, vtop) - vlow > kNear || vtop > 127 || (vtop - ve > kFar && ve > -128);
-      if (far) {
+      bool far = vtop > ve || vlow < ve - kNear;
+      if (far && ve == -128) {
+        ve = min(vtop + kRoom, 127);
+        far = vtop > ve || vlow < ve - kNear;
+      }
+      if (__builtin_expect(far, 0)) {
         // a reference for each row: see the head of the file
         if (ve != kOwn) {
           if (g == 0) {
@@ -619,9 +629,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
               o[x][i][2 + y] *= a;
             }
           }
-      } else if (__any_sync(0xffffffffu, raise) || vtop > ve) {
-        const float down = pow2f(min(ve - vtop, 0));
-        ve = max(ve, vtop);
+      } else if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
           float a[2];
@@ -631,7 +639,6 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
             a[y] = mn == m[x][y] ? 1.0f : ex2_approx(m[x][y] - mn);
             m[x][y] = mn;
             l[x][y] *= a[y];
-            a[y] *= down;
           }
 #pragma unroll
           for (int i = 0; i < MTS; ++i)
@@ -640,28 +647,41 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
         }
       }
       uint32_t pb[2][NR][2];  // P^T: tokens (2t, 2t+1) and (2t+8, 2t+9) of the half, row g
+      if (__builtin_expect(far, 0)) {
+        // weight times scale from one exponent: of a small weight and a large scale each alone may leave fp32
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float vf = pow2f(min(vb[h] - 127 - ve, 0));
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int x = 0; x < NR; ++x) {
+          for (int x = 0; x < NR; ++x) {
+            float w[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float mm = m[x][k & 1];
-            s[h][x][k] = ex2_approx(s[h][x][k] + (mm == -INFINITY ? kShift : kShift - mm));
-          }
-          l[x][0] += s[h][x][0] + s[h][x][2];
-          l[x][1] += s[h][x][1] + s[h][x][3];
-          float c[2] = {vf, vf};
-          if (far) {
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int d = vb[h] - 127 - sm.e[8 * x + 2 * t + y][warp];
-              c[y] = vb[h] != 255 ? pow2f(min(max(d, -127), 127)) : 1.0f;  // 255: its codes count as NaN
+            for (int k = 0; k < 4; ++k) {
+              const int y = k & 1, d = vb[h] - 127 - sm.e[8 * x + 2 * t + y][warp];
+              const float at = s[h][x][k] + (m[x][y] == -INFINITY ? kShift : kShift - m[x][y]);
+              s[h][x][k] = ex2_approx(at);
+              w[k] = vb[h] != 255 ? ex2_approx(at + float(d)) : s[h][x][k];  // 255: its codes count as NaN
             }
+            l[x][0] += s[h][x][0] + s[h][x][2];
+            l[x][1] += s[h][x][1] + s[h][x][3];
+            pb[h][x][0] = transposed(pack_f16x2(w[0], w[1]));
+            pb[h][x][1] = transposed(pack_f16x2(w[2], w[3]));
           }
-          pb[h][x][0] = transposed(pack_f16x2(s[h][x][0] * c[0], s[h][x][1] * c[1]));
-          pb[h][x][1] = transposed(pack_f16x2(s[h][x][2] * c[0], s[h][x][3] * c[1]));
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float vf = pow2f(vb[h] - 127 - ve);
+#pragma unroll
+          for (int x = 0; x < NR; ++x) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float mm = m[x][k & 1];
+              s[h][x][k] = ex2_approx(s[h][x][k] + (mm == -INFINITY ? kShift : kShift - mm));
+            }
+            l[x][0] += s[h][x][0] + s[h][x][2];
+            l[x][1] += s[h][x][1] + s[h][x][3];
+            pb[h][x][0] = transposed(pack_f16x2(s[h][x][0] * vf, s[h][x][1] * vf));
+            pb[h][x][1] = transposed(pack_f16x2(s[h][x][2] * vf, s[h][x][3] * vf));
+          }
         }
       }
 #pragma unroll
@@ -792,6 +812,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
       int em = -127;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) M1 = fmaxf(M1, sm.ml[row][w].x);
+      // as for a row's own reference: a warp of large values and no weight must not take the others' bits
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) em = max(em, sm.e[row][w] + int(ceilf(fmaxf(sm.ml[row][w].x - M1, -1000.0f))));
 #pragma unroll
@@ -865,22 +886,23 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
           float top = M1;
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) top = fmaxf(top, mw[k]);
-          const float down = M1 == -INFINITY ? 1.0f : ex2_approx(M1 - top);
+          // factors of a part go in two halves: that of a large mean of little weight may leave fp32 alone
+          const float down = M1 == -INFINITY ? 1.0f : ex2_approx(0.5f * (M1 - top));
           M1 = top;
-          L *= down;
+          L *= down * down;
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) acc[i] *= down;
+          for (int i = 0; i < EPT; ++i) acc[i] = acc[i] * down * down;
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) {
             if (x0 + k > c1) break;
-            const float wgt = mw[k] == -INFINITY ? lw[k] : lw[k] * ex2_approx(mw[k] - M1);
-            L += wgt;
+            const float half = mw[k] == -INFINITY ? 1.0f : ex2_approx(0.5f * (mw[k] - M1)), wgt = lw[k] * half;
+            L = fmaf(wgt, half, L);
 #pragma unroll
             for (int u = 0; u < EPT / 4; ++u) {
-              acc[4 * u] = fmaf(wgt, v[k][u].x, acc[4 * u]);
-              acc[4 * u + 1] = fmaf(wgt, v[k][u].y, acc[4 * u + 1]);
-              acc[4 * u + 2] = fmaf(wgt, v[k][u].z, acc[4 * u + 2]);
-              acc[4 * u + 3] = fmaf(wgt, v[k][u].w, acc[4 * u + 3]);
+              acc[4 * u] = fmaf(wgt, half * v[k][u].x, acc[4 * u]);
+              acc[4 * u + 1] = fmaf(wgt, half * v[k][u].y, acc[4 * u + 1]);
+              acc[4 * u + 2] = fmaf(wgt, half * v[k][u].z, acc[4 * u + 2]);
+              acc[4 * u + 3] = fmaf(wgt, half * v[k][u].w, acc[4 * u + 3]);
             }
           }
         }

@@ -6,7 +6,7 @@
 // Bound by shared memory: a tile of 64 tokens takes 1800 cycles, of which its products
 // read operands for 1024 (at 128 bytes a cycle) and the conversion writes for 256; the
 // issuing warps stand at the tensor cores' queue for 1250, the softmax is busy for 1400.
-// Two chunks of 2048 over 12289 (32 heads, 8 kv heads of 128) take 472 us, 1160 TFLOP/s.
+// Two chunks of 2048 over 12289 (32 heads, 8 kv heads of 128) take 477 us, 1150 TFLOP/s.
 // What moved it: short loops (the instruction cache), no register spills, scores ahead,
 // queries and outputs of a unit in whole lines.  Scores of 128 keys at a time would read
 // a quarter less, but leave no second buffer in tensor memory.
@@ -17,7 +17,7 @@
 //   warps 0-5    convert: queries bf16 -> fp16 (each row by a power of two), then
 //                each 64-token tile of codes -> fp16, keys and values, 16 tokens an
 //                item, into shared memory in the 128-byte-swizzled layout that the
-//                products read.  A warp's next two items are on their way in registers.
+//                products read.  A warp's next item is on its way in registers.
 //   warps 6, 7   issue the products, one warp to a query tile X: S_X = Q_X K^T and O_X += P_X V (M = 128), P from
 //                tensor memory.  S has two buffers for each query tile and its scores
 //                are issued two tiles ahead, PV_X(j) QK_X(j+2), so
@@ -27,10 +27,12 @@
 //   warps 8-11   softmax of tile A, warps 12-15 of tile B, a row to a thread.
 // Everything is fp16 with powers of two taken out: codes are exact in fp16, also times
 // the block scales relative to the largest of the segment's keys (values), as long as
-// these lie within 2^15 of each other.  Where they do not, codes stay as they are and the
-// scales enter in the softmax (far_tile).  P runs up to 2^15, with a grain of 2^-24.  A row's reference m is its first tile's maximum and is raised, and O
-// rescaled, only when a tile's weights exp2(s - m + 7) add up to more than 2^15, so that
-// most tiles are done without looking for their maximum (482 us -> 472 us).
+// these lie within 2^15 (2^6) of each other.  Where they do not, codes stay as they are and the
+// scales enter in the softmax (far_tile: two chunks of 2048 over 12289 take 870 us with it,
+// 470 us without, in a graph).  P runs up to 2^15, with a grain of 2^-24.  A row's reference
+// m is its first tile's maximum and is raised, and O rescaled, only when a tile's weights exp2(s - m + 7) add up to more than 2^15, so that
+// most tiles are done without looking for their maximum (482 us -> 472 us).  Great scores
+// are computed apart (far_tile).
 //
 // The work is the list of (unit, key/value tile), cut into equal runs, one to a CTA,
 // as in the kernel for few rows: short lists fill the SMs by splitting units, long
@@ -63,9 +65,13 @@ constexpr int ROWS = 128;        // query rows of a tile
 constexpr int UNIT = 2 * ROWS;
 // Ring stages: keys of tile j + 2 are needed with values of tile j, so that many fewer of them.
 constexpr int KST = 4, VST = 6;
-constexpr int MIN_TILES = 8;     // of a CTA's run, where units are split
+// Tiles of a CTA's run, where units are split: shorter ones open and join more than they compute (8 units: 64 tokens over
+// 500 25, 22, 22 us with 4, 8, 16; over 4000 89, 60, 54 us; chunks that fill the CTAs anyway do not care).
+constexpr int MIN_TILES = 8;
 constexpr float kShift = 7.0f, kMost = 32768.0f;
-constexpr int kNear = 15;  // codes (the least is 2^-9) are exact in fp16 (2^-24) relative to a scale up to 2^this larger
+// Relative to a scale up to 2^kNearK larger codes (the least is 2^-9) are exact in fp16 (2^-24).  Values count no more than
+// P does: their scales lie so close that the grain of P, times the largest, stays below 2^-25 of a row's largest product.
+constexpr int kNearK = 15, kNearV = 6;
 constexpr int kFar = 1000;
 constexpr float kGreat = 16777216.0f;  // from here on the rounding of a score is as much as the span of a softmax
 constexpr uint32_t BOX = ROWS * 64 * 2;    // a query tile's rows of 64 fp16, one swizzle span wide
@@ -406,18 +412,60 @@ __device__ __noinline__ float4 far_tile(uint32_t s_addr, int vis, const volatile
     mask(v, vis - 32 * h);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const float c = vb[2 * h + q] == 255 ? 1.0f : pow2f(min(max(vb[2 * h + q] - 127 - en, -127), 127));
+      // weight times scale from one exponent: of a small weight and a large scale each alone may leave fp32
+      const float c = vb[2 * h + q] == 255 ? 0.0f : float(vb[2 * h + q] - 127 - en);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float p0 = ex2_approx(__fadd_rn(__fmul_rn(__uint_as_float(v[16 * q + 2 * k]), f[2 * h + q]), add));
-        const float p1 = ex2_approx(__fadd_rn(__fmul_rn(__uint_as_float(v[16 * q + 2 * k + 1]), f[2 * h + q]), add));
-        sum += p0 + p1;
-        w[8 * q + k] = pack_f16x2(p0 * c, p1 * c);
+        const float a0 = __fadd_rn(__fmul_rn(__uint_as_float(v[16 * q + 2 * k]), f[2 * h + q]), add);
+        const float a1 = __fadd_rn(__fmul_rn(__uint_as_float(v[16 * q + 2 * k + 1]), f[2 * h + q]), add);
+        sum += ex2_approx(a0) + ex2_approx(a1);
+        w[8 * q + k] = pack_f16x2(ex2_approx(a0 + c), ex2_approx(a1 + c));
       }
     }
     tmem_st_16cols(s_addr + uint32_t(h * 16), w);
   }
   return make_float4(mn, l + sum, float(en), alpha);
+}
+
+// A row's parts, those of CTAs c0 .. c1 in this order, become one: its output, and its reference and sum.
+template <int D>
+__device__ __noinline__ float2 join_parts(const float* rows_at, int c0, int c1, uint16_t* orow, bool row_ok) {
+  constexpr int64_t SLOT = 2 * ROWS * (D + 3);
+  const int n = c1 - c0;
+  const float* first = rows_at + (2 * int64_t(c0) + 1) * SLOT;  // the first CTA's second slot, then the others' first ones
+  auto slot = [&](int i) { return first + (i ? (2 * int64_t(i) - 1) * SLOT : 0); };
+  float top = -INFINITY, sum = 0.0f;
+  for (int i = 0; i <= n; ++i) top = fmaxf(top, __ldcg(slot(i) + D * ROWS));
+  // the joined means' unit: by the largest product of weight and unit, as for a row's own reference
+  float unit = -127.0f;
+  for (int i = 0; i <= n; ++i) {
+    const float* at = slot(i) + D * ROWS;
+    const float m = __ldcg(at), l = __ldcg(at + ROWS), e = __ldcg(at + 2 * ROWS);
+    sum += m == -INFINITY ? l : l * ex2_approx(m - top);
+    unit = fmaxf(unit, e + ceilf(fmaxf(m - top, -1000.0f)));
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum, pe = pow2f(int(unit));
+#pragma unroll 1
+  for (int q = 0; q < D / 32; ++q) {
+    float x[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = 0.0f;
+    const float* from = first;
+#pragma unroll 1
+    for (int i = 0; i <= n; ++i, from = slot(i)) {
+      const float m = __ldcg(from + D * ROWS), l = __ldcg(from + (D + 1) * ROWS), e = __ldcg(from + (D + 2) * ROWS);
+      float v[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = __ldcg(from + (q * 32 + k) * ROWS);
+      const float w = m == -INFINITY ? l : l * ex2_approx(m - top + (e - unit));
+#pragma unroll
+      for (int k = 0; k < 32; ++k) x[k] = fmaf(w, v[k], x[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = x[k] * inv * pe;
+    put_rows(x, orow, row_ok, q * 32);
+  }
+  return make_float2(top, sum);
 }
 
 template <int D>
@@ -491,7 +539,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     all_units += sd.warp_units[w];
   }
   before -= mine;
-  // a CTA for each unit as far as they go, and where units are split four tiles to a CTA at least
+  // a CTA for each unit as far as they go, and where units are split MIN_TILES to a CTA at least
   const int64_t n = min(int64_t(gridDim.x), max(all_units, total / MIN_TILES));
   const int64_t cta = blockIdx.x;
   const int64_t run0 = cta < n ? cta * total / n : 0, run1 = cta < n ? (cta + 1) * total / n : 0;
@@ -597,7 +645,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         kl = min(kl, int(sd.warp_range[w][2]));
         vl = min(vl, int(sd.warp_range[w][3]));
       }
-      if (km - kl > kNear || vm - vl > kNear) km = kFar;
+      if (km - kl > kNearK || vm - vl > kNearV) km = kFar;
       if (tid == 0) {
         sd.tiles[i & 3] = g.left > g.t1 - g.t0 ? g.t1 - g.t0 : g.t0 - g.t1;  // the run's last one: negative
         sd.kv_exp[i & 3][0] = int16_t(km);
@@ -918,18 +966,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         break;
       }
       tc_fence_after();
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l, pe = pow2f(e == kFar ? sd.kv_exp[i & 3][1] : e);
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int unit = e == kFar ? sd.kv_exp[i & 3][1] : e;  // O is in units of 2^unit
       int least_nan = sd.nan_at[i & 3][lane];
 #pragma unroll
       for (int k = 1; k < D / 32; ++k) least_nan = min(least_nan, sd.nan_at[i & 3][lane + 32 * k]);
       least_nan = __reduce_min_sync(0xffffffffu, least_nan);
       const bool row_ok = r < rows;
       const bool whole = g.t0 == 0 && g.t1 == g.nkv;
+      const float pe = whole ? pow2f(unit) : 1.0f;
       const int tk = r / p.group, head = g.hk * p.group + r - tk * p.group;
       uint16_t* orow = p.out + (int64_t(g.seq.row0 + tk) * p.H + head) * D;
-      // a segment's partial result: for each tile D means, maximum and sum, row next to row
-      constexpr int64_t SLOT = 2 * ROWS * (D + 2);
-      float* mine_row = p.partial + (2 * int64_t(blockIdx.x) + (g.t0 == 0 ? 1 : 0)) * SLOT + X * (D + 2) * ROWS + row;
+      // a segment's partial result: for each tile D means, maximum, sum and the means' unit, row next to row
+      constexpr int64_t SLOT = 2 * ROWS * (D + 3);
+      float* mine_row = p.partial + (2 * int64_t(blockIdx.x) + (g.t0 == 0 ? 1 : 0)) * SLOT + X * (D + 3) * ROWS + row;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -961,6 +1011,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         if (row_ok) {
           __stcg(mine_row + D * ROWS, m);
           __stcg(mine_row + (D + 1) * ROWS, l);
+          __stcg(mine_row + (D + 2) * ROWS, float(unit));
         }
         const int64_t t0 = sd.run0 + done - g.t0;
         const int64_t c0 = ((t0 + 1) * sd.ctas - 1) / sd.total, c1 = ((t0 + g.nkv) * sd.ctas - 1) / sd.total;
@@ -976,32 +1027,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         if (!ok) break;
         if (sd.last[X]) {
           __threadfence();
-          const float* rows_at = p.partial + X * (D + 2) * ROWS + row;
-          auto slot = [&](int64_t c) { return rows_at + (2 * c + (c == c0)) * SLOT; };
-          float top = -INFINITY, sum = 0.0f;
-          for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(slot(c) + D * ROWS));
-          auto weight = [&](int64_t c) {
-            const float mc = __ldcg(slot(c) + D * ROWS), lc = __ldcg(slot(c) + (D + 1) * ROWS);
-            return mc == -INFINITY ? lc : lc * ex2_approx(mc - top);
-          };
-          for (int64_t c = c0; c <= c1; ++c) sum += weight(c);
-          const float is = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            float x[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = 0.0f;
-            for (int64_t c = c0; c <= c1; ++c) {
-              const float wgt = weight(c) * is;
-              const float* from = slot(c) + q * 32 * ROWS;
-#pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = fmaf(wgt, __ldcg(from + k * ROWS), x[k]);
-            }
-            put_rows(x, orow, row_ok, q * 32);
-          }
+          const float2 all = join_parts<D>(p.partial + X * (D + 3) * ROWS + row, int(c0), int(c1), orow, row_ok);
           if (p.lse && row_ok)
             p.lse[int64_t(head) * b.n_tokens + g.seq.row0 + tk] =
-                sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * 0.69314718055994531f;
+                all.y == 0.0f ? -INFINITY : (all.x - kShift + log2f(all.y)) * 0.69314718055994531f;
         }
       }
       done += g.t1 - g.t0;
@@ -1024,7 +1053,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
 
 }  // namespace
 
-size_t prefill_partial_bytes(int ctas, int D) { return size_t(ctas) * 2 * UNIT * (D + 2) * sizeof(float); }
+size_t prefill_partial_bytes(int ctas, int D) { return size_t(ctas) * 2 * UNIT * (D + 3) * sizeof(float); }
 
 tl_status launch_kv_prefill(PrefillParams& p, int D, int ctas, cudaStream_t st) {
   // floor(g / h) = floor(g m / 2^32), m = floor(2^32 / h) + 1, as long as g < 2^32 / h: g < 2^27, h <= 16

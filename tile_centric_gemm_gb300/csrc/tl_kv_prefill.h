@@ -14,7 +14,7 @@ struct PrefillParams {
   uint16_t* out;
   float* lse;
   uint32_t* counters;  // [CTAs][2], zero between calls
-  float* partial;      // [CTAs][2][2][D + 2][128]
+  float* partial;      // [CTAs][2][2][D + 3][128]
   uint64_t timeout_ns;
   int32_t H, group, causal;
   int32_t min_rows;    // sequences of more query rows per kv head than this are this kernel's
