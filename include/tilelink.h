@@ -39,8 +39,9 @@
  *    (int32_t)(v - E) >= 0.  Each call that uses a signals object releases its
  *    flags with the caller's epoch, so flags are never reset between calls; a
  *    later call on the same object must use a larger epoch (mod 2^32).
- *  - Every wait inside a kernel is bounded by timeout_ns (0 = 1 s).  When a
- *    bound runs out the kernel records TL_ERR_TIMEOUT, stops waiting for the
+ *  - Every wait inside a kernel is bounded, that for a flag by timeout_ns (0 =
+ *    1 s).  When a bound runs out the kernel records TL_ERR_TIMEOUT for a flag,
+ *    TL_ERR_INTERNAL for a wait among a block's own warps, stops waiting for the
  *    rest of the launch, and finishes; its outputs are then undefined.
  *  - Failure: no call aborts the process; no exception crosses the ABI.
  *    tl_last_error() returns a message for the calling thread's last error.
@@ -687,8 +688,13 @@ tl_status tl_kv_append(const tl_kv_append_args* args, void* stream);
  *                            j <= seq_lens[s] - n_s + i
  *   O = bf16( sum_j exp(s_j - lse) v_j ),   lse = log sum_j exp(s_j)
  * A row that sees no key has O = 0 and lse = -infinity.  What lies in the cache
- * where a row sees nothing (NaN included) does not reach its result.  Fp32
- * softmax statistics and sums; the codes enter the products exactly.
+ * where a row sees nothing (NaN, or blocks of any scale) does not reach its result.
+ * Fp32 scores, softmax statistics and sums; the codes enter the products exactly,
+ * whatever the scales of their blocks.  Rounded to fp16 are: a row's query, off by
+ * at most 2^-25 of its largest element; and the weights before they meet the
+ * values, off by at most 2^-11 of each, or (small ones) so that weight times value
+ * is off by at most 2^-25 of the row's largest product of a weight and its block's
+ * largest value.
  * Takes queries that tl_kv_append rotated and a cache that holds the new tokens.
  * May be captured into a graph after a first call outside any capture.
  * Every wait inside the kernels is bounded (3 s); one that runs out records
@@ -738,7 +744,10 @@ tl_status tl_kv_attn(const tl_kv_attn_args* args, void* stream);
  * terms).  The weights of an expert that no token chose are not read.
  * Two stream-ordered launches, the second set up while the first runs
  * (programmatic dependent launch).  Deterministic.  Hd up to 65536.  Beyond 64 tokens
- * tl_moe_ag_gemm and tl_moe_down are the calls.
+ * there is no such call: tl_moe_ag_gemm and tl_moe_down do the experts' two products
+ * (up to 64 experts) on routing that the caller brings, with no selection and no gated
+ * activation between them.  More tokens can be given 64 at a time; each call reads the
+ * chosen experts' weights anew.
  */
 typedef struct tl_moe_decode_args {
   int32_t T;                   /* tokens, 0..64 (0: nothing to do) */

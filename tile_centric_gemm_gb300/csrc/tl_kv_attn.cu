@@ -27,8 +27,8 @@
 //    largest element.  The K scale multiplies the scores in fp32, the V scale of the
 //    half chunk relative to a reference multiplies P, both powers of two.
 //  * That reference is one for the warp's rows while the V scales that it meets lie within
-//    2^3 of the first ones, as they mostly do (64 single tokens over 8192 take 134 us with it
-//    and 137 us without, 16 drafts of 4 over 6000 41 and 49 us).  Otherwise each row has its own,
+//    2^3 of the first ones, as they mostly do (64 single tokens over 8192 take 132 us with it
+//    and 140 us without, 16 drafts of 4 over 6000 40 and 50 us, in a graph).  Otherwise each row has its own,
 //    2^e with e at least what the largest product of weight and scale asks for among the keys
 //    that the row sees: P times the scale relative to 2^e is at most 2^7, and a block that the
 //    row does not see, or hardly, takes no bits from the others.
@@ -38,8 +38,8 @@
 //    Sums of P are taken in fp32 before P is rounded.
 //
 // Bound by memory when there are many tokens to read: 64 single tokens over 8192 at most
-// (8 kv heads of 128): 135 us for 826 MB, 91 % of a copy's rate; three over 131072 at most,
-// 101 us for 615 MB, 91 %.  Copies of 64-byte half lines, which fit the products' lanes
+// (8 kv heads of 128): 136 us for 826 MB, 91 % of a copy's rate; three over 131072 at most,
+// 102 us for 615 MB, 90 %.  Copies of 64-byte half lines, which fit the products' lanes
 // without a swizzle, ran at 75 %.  A single short context (14 us for 8 MB, 13 us in a
 // graph) is a chain of loads that wait for one another (lengths, page, scale and codes,
 // merge, the join); 16-row tiles (16 sequences of 4 drafts over 6000 at most: 43 us for

@@ -6,7 +6,7 @@
 // Bound by shared memory: a tile of 64 tokens takes 1800 cycles, of which its products
 // read operands for 1024 (at 128 bytes a cycle) and the conversion writes for 256; the
 // issuing warps stand at the tensor cores' queue for 1250, the softmax is busy for 1400.
-// Two chunks of 2048 over 12289 (32 heads, 8 kv heads of 128) take 477 us, 1150 TFLOP/s.
+// Two chunks of 2048 over 12289 (32 heads, 8 kv heads of 128) take 479 us, 1150 TFLOP/s.
 // What moved it: short loops (the instruction cache), no register spills, scores ahead,
 // queries and outputs of a unit in whole lines.  Scores of 128 keys at a time would read
 // a quarter less, but leave no second buffer in tensor memory.
@@ -28,8 +28,8 @@
 // Everything is fp16 with powers of two taken out: codes are exact in fp16, also times
 // the block scales relative to the largest of the segment's keys (values), as long as
 // these lie within 2^15 (2^6) of each other.  Where they do not, codes stay as they are and the
-// scales enter in the softmax (far_tile: two chunks of 2048 over 12289 take 870 us with it,
-// 470 us without, in a graph).  P runs up to 2^15, with a grain of 2^-24.  A row's reference
+// scales enter in the softmax (far_tile: two chunks of 2048 over 12289 take 905 us with it,
+// 469 us without, in a graph).  P runs up to 2^15, with a grain of 2^-24.  A row's reference
 // m is its first tile's maximum and is raised, and O rescaled, only when a tile's weights exp2(s - m + 7) add up to more than 2^15, so that
 // most tiles are done without looking for their maximum (482 us -> 472 us).  Great scores
 // are computed apart (far_tile).
@@ -66,7 +66,7 @@ constexpr int UNIT = 2 * ROWS;
 // Ring stages: keys of tile j + 2 are needed with values of tile j, so that many fewer of them.
 constexpr int KST = 4, VST = 6;
 // Tiles of a CTA's run, where units are split: shorter ones open and join more than they compute (8 units: 64 tokens over
-// 500 25, 22, 22 us with 4, 8, 16; over 4000 89, 60, 54 us; chunks that fill the CTAs anyway do not care).
+// 500 25, 22, 22 us with 4, 8, 16; over 4000 89, 60, 54 us, before the join was made shorter; chunks that fill the CTAs anyway do not care).
 constexpr int MIN_TILES = 8;
 constexpr float kShift = 7.0f, kMost = 32768.0f;
 // Relative to a scale up to 2^kNearK larger codes (the least is 2^-9) are exact in fp16 (2^-24).  Values count no more than

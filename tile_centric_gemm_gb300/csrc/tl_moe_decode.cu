@@ -35,10 +35,10 @@
 // hides, and the result keeps the accuracy of fp32 activations.
 //
 // Bound by memory where every expert is met (27 tokens, top 2 of 32 experts of 4096 x
-// 1408: 150 us for 914 MB, 91 % of a copy's rate).  One token (27 us for 69 MB) waits for
+// 1408: 147-155 us for 914 MB, 88-93 % of a copy's rate).  One token (27 us for 69 MB) waits for
 // the launches' latency: routing, opening and join cost about 2 us each in both.  Rows
-// that are no whole number of lines (64 tokens over 64 experts of 2048 x 1000: 175 us,
-// 67 %; 157 us for 1024) are read partly twice, for two strips; the selection of 64
+// that are no whole number of lines (64 tokens over 64 experts of 2048 x 1000: 173-178 us,
+// 66 %; 157 us for 1024) are read partly twice, for two strips; the selection of 64
 // tokens takes 10 us of it.
 #include <algorithm>
 #include <cmath>
@@ -56,7 +56,7 @@ constexpr int MAX_T = 64, MAX_K = 16, MAX_ROWS = MAX_T * MAX_K;
 constexpr int MAX_CTAS = 256;
 constexpr int MAX_HD = 65536;
 // What a tile costs a CTA beside its steps, in steps: the list of work has that many places before a tile's steps, so that
-// runs of equal length take equally long (one token: 26.7 -> 24.6 us; four: 55 -> 53 us; no difference from 16 on).
+// runs of equal length take equally long (one token: 29.0 us without, 27.0 us with; no difference from 16 tokens on).
 constexpr int LEAD = 4;
 constexpr int W_BYTES = 32 * 128;    // one warp's weights of one step: 32 rows of 64 columns
 
