@@ -119,9 +119,9 @@ __device__ __forceinline__ uint32_t w_at(int row, int unit) { return uint32_t(ro
 __device__ __forceinline__ int merge_at(int r, int c) { return r * 16 + (c ^ (r & 1) ^ ((c >> 3) << 1)); }
 
 // ---------------------------------------------------------------- routing, by every CTA for itself
-// Order of the logits as unsigned keys: larger first, NaN (1) below -infinity, 0 = taken.
+// Order of the logits as unsigned keys: larger first, zeros of both signs equal, NaN (1) below -infinity, 0 = taken.
 __device__ __forceinline__ uint32_t logit_key(float v) {
-  const uint32_t u = __float_as_uint(v);
+  const uint32_t u = __float_as_uint(__fadd_rn(v, 0.0f));  // -0 + 0 = 0
   if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 1u;
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
