@@ -681,6 +681,30 @@ typedef struct tl_kv_append_args {
 
 tl_status tl_kv_append(const tl_kv_append_args* args, void* stream);
 
+/* ---------------------------------------------------------------- append with norms, drafts' positions
+ * tl_kv_append with a norm of each head's queries and keys before the rotation,
+ *   x <- x * w / sqrt(mean_d x_d^2 + eps)
+ * over the head_dim dims of one token and head, w the call's weights (q_weight for
+ * queries, k_weight for keys; NULL: that side is not normed), and with the tables read
+ * at positions[t] for new token t where positions are given: tokens of a drafted tree
+ * rotate by their depth, not by their slot.  All else is as for tl_kv_append: the slots,
+ * the scales, and each key's code, which is the exact normed and rotated value (to
+ * 2^-40 of it) rounded once.  Queries are computed in fp32 and rounded once to bf16.
+ * A row with an infinite element has 0 in its finite ones and NaN in the others; one
+ * with a NaN is NaN.  A position outside 0..max_pos-1 records TL_ERR_INVALID with the
+ * sequence number, and that token is undefined.
+ */
+typedef struct tl_kv_append_norm_args {
+  tl_kv_append_args append;
+  const void* q_weight;        /* device bf16 [head_dim], 16-byte aligned, or NULL */
+  const void* k_weight;        /* device bf16 [head_dim], 16-byte aligned, or NULL */
+  const int32_t* positions;    /* device int32 [n_tokens], or NULL: a token's position in its sequence */
+  float eps;                   /* 1e-12 .. 1e12 where a weight is given */
+  int32_t reserved0;
+} tl_kv_append_norm_args;
+
+tl_status tl_kv_append_norm(const tl_kv_append_norm_args* args, void* stream);
+
 /* ---------------------------------------------------------------- attention over the cache
  * For new token i (0-based) of sequence s and query head h, with kv head
  * hk = h / (H / H_kv) and k_j, v_j the cache's values:

@@ -56,6 +56,13 @@ def rotate(x, pos, cos, sin, interleaved):
     return y
 
 
+def normed(x, weight, eps):
+    """x [..., D], each row over its root mean square, times the weights."""
+    x = np.asarray(x, dtype=np.float64)
+    with np.errstate(invalid="ignore", over="ignore"):
+        return x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * weight
+
+
 def append(codes, scales, rows, cu, lens, table):
     """Put rows [n, H_kv, D] (float64, rotated) into copies of codes [pages, H_kv, ps, D] and scales."""
     codes, scales = codes.copy(), scales.copy()

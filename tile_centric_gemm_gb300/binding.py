@@ -38,7 +38,7 @@ EXPORTED = [
     "tl_moe_down_workspace_size", "tl_moe_down_num_flags", "tl_moe_down",
     "tl_ag_attn_num_flags", "tl_ag_attn", "tl_allgather_ll_link_bytes", "tl_allgather_ll",
     "tl_test_hold_chunks",
-    "tl_kv_append", "tl_kv_attn_workspace_size", "tl_kv_attn",
+    "tl_kv_append", "tl_kv_append_norm", "tl_kv_attn_workspace_size", "tl_kv_attn",
     "tl_moe_decode_workspace_size", "tl_moe_decode",
 ]
 
@@ -160,6 +160,13 @@ class tl_kv_append_args(ctypes.Structure):
         ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
         ("q_out", _vp), ("cos", _vp), ("sin", _vp), ("cu_seqlens", _vp), ("seq_lens", _vp), ("page_table", _vp),
         ("signals", _vp),
+    ]
+
+
+class tl_kv_append_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("append", tl_kv_append_args), ("q_weight", _vp), ("k_weight", _vp), ("positions", _vp), ("eps", ctypes.c_float),
+        ("reserved0", ctypes.c_int32),
     ]
 
 
@@ -553,9 +560,11 @@ def tl_ag_attn(Q, K_shards, V_shards, K_gathered, V_gathered, O, signals: Signal
 # in one go, laid out as the C structures above.
 
 _APPEND = struct.Struct("@8i4P3q4i3P6q7P")
+_APPEND_NORM = struct.Struct(_APPEND.format + "3Pfi")
 _ATTN = struct.Struct("@6ifi4P3q4iP2q6PNP")
 _MOE = struct.Struct("@8i8PN")
-assert _APPEND.size == ctypes.sizeof(tl_kv_append_args) and _ATTN.size == ctypes.sizeof(tl_kv_attn_args) and \
+assert _APPEND.size == ctypes.sizeof(tl_kv_append_args) and \
+    _APPEND_NORM.size == ctypes.sizeof(tl_kv_append_norm_args) and _ATTN.size == ctypes.sizeof(tl_kv_attn_args) and \
     _MOE.size == ctypes.sizeof(tl_moe_decode_args)
 
 
@@ -567,6 +576,7 @@ def _packed(name):
 
 
 _kv_append, _kv_attn, _moe_decode = _packed("tl_kv_append"), _packed("tl_kv_attn"), _packed("tl_moe_decode")
+_kv_append_norm = _packed("tl_kv_append_norm")
 _torch = None
 
 
@@ -652,12 +662,8 @@ def _batch(cu_seqlens, seq_lens, page_table, int32, dev):
             _typed(page_table, "page_table", int32, (B, max_pages), dev))
 
 
-def tl_kv_append(cache: KvCache, k, v, cu_seqlens, seq_lens, page_table, signals: Signals, *, q=None, q_out=None,
-                 cos=None, sin=None, interleaved=False, max_q_len=0, stream=None):
-    """Append k, v [n, H_kv, D] (bf16; views of a fused projection will do) to the cache, k rotated by the
-    tables cos, sin [positions, rot_dim/2] at each token's position; q [n, H, D] rotated into q_out
-    (see tilelink.h).  No tables: no rotation."""
-    st, dev = _place(stream)
+def _append_fields(dev, cache, k, v, cu_seqlens, seq_lens, page_table, signals, q, q_out, cos, sin, interleaved, max_q_len):
+    """tl_kv_append_args, field by field."""
     bf16, f32 = _torch.bfloat16, _torch.float32
     n, D = k.shape[0], cache.head_dim
     _held(cache, dev)
@@ -677,8 +683,35 @@ def tl_kv_append(cache: KvCache, k, v, cu_seqlens, seq_lens, page_table, signals
         max_pos, rot = cos.shape
         cp, sp = _typed(cos, "cos", f32, (max_pos, rot), dev), _typed(sin, "sin", f32, (max_pos, rot), dev)
         rot *= 2
-    code = _kv_append(_APPEND.pack(n, B, H, rot, bool(interleaved), max_pos, max_pages, max_q_len, *cache.fields, kp, vp, qp,
-                                   ka, kb, va, vb, qa, qb, out, cp, sp, cu, lens, table, signals.handle.value), st)
+    return (n, B, H, rot, bool(interleaved), max_pos, max_pages, max_q_len, *cache.fields, kp, vp, qp, ka, kb, va, vb, qa, qb,
+            out, cp, sp, cu, lens, table, signals.handle.value)
+
+
+def tl_kv_append(cache: KvCache, k, v, cu_seqlens, seq_lens, page_table, signals: Signals, *, q=None, q_out=None,
+                 cos=None, sin=None, interleaved=False, max_q_len=0, stream=None):
+    """Append k, v [n, H_kv, D] (bf16; views of a fused projection will do) to the cache, k rotated by the
+    tables cos, sin [positions, rot_dim/2] at each token's position; q [n, H, D] rotated into q_out
+    (see tilelink.h).  No tables: no rotation."""
+    st, dev = _place(stream)
+    code = _kv_append(_APPEND.pack(*_append_fields(dev, cache, k, v, cu_seqlens, seq_lens, page_table, signals, q, q_out, cos,
+                                                   sin, interleaved, max_q_len)), st)
+    if code:
+        _check(code)
+
+
+def tl_kv_append_norm(cache: KvCache, k, v, cu_seqlens, seq_lens, page_table, signals: Signals, *, q=None, q_out=None,
+                      q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=None, positions=None, interleaved=False,
+                      max_q_len=0, stream=None):
+    """tl_kv_append with each head's queries and keys normed by the weights q_weight, k_weight [D] (bf16; None: not
+    normed) before the rotation, and the tables read at positions [n] (int32; None: the tokens' own; see tilelink.h)."""
+    st, dev = _place(stream)
+    bf16, i32, D = _torch.bfloat16, _torch.int32, cache.head_dim
+    fields = _append_fields(dev, cache, k, v, cu_seqlens, seq_lens, page_table, signals, q, q_out, cos, sin, interleaved,
+                            max_q_len)
+    code = _kv_append_norm(_APPEND_NORM.pack(*fields, 0 if q_weight is None else _typed(q_weight, "q_weight", bf16, (D,), dev),
+                                             0 if k_weight is None else _typed(k_weight, "k_weight", bf16, (D,), dev),
+                                             0 if positions is None else _typed(positions, "positions", i32, (k.shape[0],), dev),
+                                             eps, 0), st)
     if code:
         _check(code)
 

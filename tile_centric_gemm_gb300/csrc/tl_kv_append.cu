@@ -33,6 +33,7 @@
 // 32 + 8 heads of 128 into pages of 64: 52 us, 3.65 TB/s over the bytes read and
 // written, issue slots 65 % busy.
 #include <algorithm>
+#include <type_traits>
 
 #include "tl_internal.h"
 #include "tl_kv.cuh"
@@ -54,6 +55,10 @@ struct AppendParams {
   const float* sin;
   int32_t H, rot, interleaved, max_pos;
   int32_t kv_blocks, groups;  // blocks for keys and values; blocks of one item
+  const uint16_t* q_w;        // tl_kv_append_norm: weights of the norms, and where the tables are read
+  const uint16_t* k_w;
+  const int32_t* positions;
+  float eps;
 };
 
 __device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
@@ -67,21 +72,30 @@ __device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
 
 __device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) { unpack8(*reinterpret_cast<const uint4*>(p), x); }
 
-// x c + t s rounded to odd (see above); not finite: the plain fp32 value.
-__device__ __forceinline__ float dot2_odd(float x, float c, float t, float s) {
+// x c + t s as hi + rest, exactly but for what lies below 2^-48 of it; hi is the nearest float.  False: not finite,
+// and hi is the plain fp32 value.
+__device__ __forceinline__ bool dot2_pair(float x, float c, float t, float s, float& hi, float& rest) {
   const float p = __fmul_rn(x, c), r = __fmul_rn(t, s);
   const float pe = __fmaf_rn(x, c, -p), re = __fmaf_rn(t, s, -r);
   const float sum = __fadd_rn(p, r);
   const float back = __fsub_rn(sum, p);
   const float err = __fadd_rn(__fsub_rn(p, __fsub_rn(sum, back)), __fsub_rn(r, back));
   const float lo = __fadd_rn(err, __fadd_rn(pe, re));
-  const float hi = __fadd_rn(sum, lo);
-  const float rest = __fsub_rn(lo, __fsub_rn(hi, sum));
-  // what is left below hi decides: one step towards zero where it points there, and the last bit set
+  const bool finite = (__float_as_uint(sum) & 0x7FFFFFFFu) < 0x7F800000u;
+  hi = finite ? __fadd_rn(sum, lo) : sum;
+  rest = __fsub_rn(lo, __fsub_rn(hi, sum));
+  return finite;
+}
+// hi + rest rounded to odd (see above): one step towards zero where rest points there, and the last bit set
+__device__ __forceinline__ float to_odd(float hi, float rest) {
   const uint32_t u = __float_as_uint(hi);
   const uint32_t odd = (u + uint32_t(int32_t(__float_as_uint(rest) ^ u) >> 31)) | 1u;
-  const bool finite = (__float_as_uint(sum) & 0x7FFFFFFFu) < 0x7F800000u;
-  return finite ? __uint_as_float(rest != 0.0f ? odd : u) : sum;
+  return __uint_as_float(rest != 0.0f ? odd : u);
+}
+__device__ __forceinline__ float dot2_odd(float x, float c, float t, float s) {
+  float hi, rest;
+  const bool finite = dot2_pair(x, c, t, s, hi, rest);
+  return finite ? to_odd(hi, rest) : hi;
 }
 
 template <bool EXACT>
@@ -150,6 +164,120 @@ __device__ __forceinline__ void rotated8(const AppendParams& p, const uint16_t* 
   load8(row + 8 * u, x);
   load8(row + max(w.partner, 0), t);
   turn<EXACT>(p, w, x, t, y);
+}
+
+// ---------------------------------------------------------------- norms
+// A row's factor 1 / sqrt(mean x^2 + eps), as hi + lo, for its elements times `scale` (1, or 2^-80 where the sum of
+// squares would leave fp32).  A row with an infinity has 0 (finite elements become 0 and infinities NaN), one with a
+// NaN has NaN.
+struct Norm {
+  float hi, lo, scale;
+};
+__device__ __forceinline__ void two_sum(float a, float b, float& sum, float& err) {
+  sum = __fadd_rn(a, b);
+  const float back = __fsub_rn(sum, a);
+  err = __fadd_rn(__fsub_rn(a, __fsub_rn(sum, back)), __fsub_rn(b, back));
+}
+// The sum of squares over the D dims of a row that UNITS neighbouring lanes hold: squares of bf16 are exact in fp32, sums
+// are pairs.  Below 2^-63 squares lose bits, which eps (1e-12 at least) makes up for.
+template <int D, bool EXACT>
+__device__ __forceinline__ void square_sum(const float (&x)[8], float scale, uint32_t mask, float& s, float& e) {
+  s = e = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = x[i] * scale;
+    if (EXACT) {
+      float d;
+      two_sum(s, __fmul_rn(v, v), s, d);
+      e += d;
+    } else {
+      s = fmaf(v, v, s);
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < D / 8; d <<= 1) {
+    const float s2 = __shfl_xor_sync(mask, s, d);
+    if (EXACT) {
+      const float e2 = __shfl_xor_sync(mask, e, d);
+      float f;
+      two_sum(s, s2, s, f);
+      e = (e + e2) + f;
+    } else {
+      s += s2;
+    }
+  }
+}
+// EXACT: to about 2^-45 by a step of Newton's iteration from the reciprocal root, its residual taken exactly:
+// r (1 + d / 2 + 3 d^2 / 8), d = 1 - a r^2.
+template <int D, bool EXACT>
+__device__ __forceinline__ Norm row_norm(const float (&x)[8], float eps) {
+  constexpr uint32_t UNITS = D / 8;
+  const uint32_t mask = ((1u << UNITS) - 1u) << (lane_id() & ~(UNITS - 1u));
+  Norm n{0.0f, 0.0f, 1.0f};
+  float s, e;
+  square_sum<D, EXACT>(x, 1.0f, mask, s, e);
+  if (!(s < INFINITY)) {  // the same for all lanes of the row
+    n.scale = 0x1p-80f;
+    square_sum<D, EXACT>(x, n.scale, mask, s, e);
+    if (!(s < INFINITY)) {
+      n.hi = s == INFINITY ? 0.0f : s;
+      return n;
+    }
+    eps = 0.0f;
+  }
+  if (!EXACT) {
+    n.hi = rsqrtf(fmaf(s, 1.0f / D, eps));
+    return n;
+  }
+  float h, l;
+  two_sum(s * (1.0f / D), eps, h, l);
+  l = fmaf(e, 1.0f / D, l);
+  const float a = __fadd_rn(h, l), b = __fsub_rn(l, __fsub_rn(a, h));  // mean + eps = a + b
+  const float r = rsqrtf(a);
+  const float p = __fmul_rn(r, r), pe = __fmaf_rn(r, r, -p);
+  const float u = __fmul_rn(a, p), ue = __fmaf_rn(a, p, -u);
+  const float d = __fsub_rn(__fsub_rn(1.0f, u), __fadd_rn(ue, __fmaf_rn(a, pe, __fmul_rn(b, p))));
+  const float step = __fmul_rn(r, __fmul_rn(d, fmaf(0.375f, d, 0.5f)));
+  n.hi = __fadd_rn(r, step);
+  n.lo = __fsub_rn(step, __fsub_rn(n.hi, r));
+  return n;
+}
+// (x c + t s) times the row's factor; x and t with their weights, exact in fp32.  EXACT: rounded to odd.
+template <bool EXACT>
+__device__ __forceinline__ float normed_dot2(const Norm& n, float x, float c, float t, float s) {
+  if (!EXACT) return fmaf(x, c, t * s) * n.hi;
+  float hi, rest;
+  if (!dot2_pair(x, c, t, s, hi, rest)) return hi * n.hi;
+  const float y = __fmul_rn(hi, n.hi);
+  const float e = __fmaf_rn(hi, n.lo, __fmaf_rn(rest, n.hi, __fmaf_rn(hi, n.hi, -y)));
+  const float z = __fadd_rn(y, e);
+  return to_odd(z, __fsub_rn(e, __fsub_rn(z, y)));
+}
+// Dims 8u .. 8u+7 of a row, normed by n with the weights wx (its partner's: wt) and rotated.
+template <bool EXACT>
+__device__ __forceinline__ void turn_normed(const AppendParams& p, const Turn& w, const Norm& n, const float (&x)[8],
+                                            const float (&t)[8], uint4 wx, uint4 wt, float (&y)[8]) {
+  float a[8], b[8];
+  unpack8(wx, a);
+  unpack8(wt, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] *= x[i] * n.scale;
+    b[i] *= t[i] * n.scale;
+  }
+  if (w.partner < 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = normed_dot2<EXACT>(n, a[i], 1.0f, 0.0f, 0.0f);
+  } else if (p.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[2 * i] = normed_dot2<EXACT>(n, a[2 * i], w.c[i], -a[2 * i + 1], w.s[i]);
+      y[2 * i + 1] = normed_dot2<EXACT>(n, a[2 * i + 1], w.c[i], a[2 * i], w.s[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = normed_dot2<EXACT>(n, a[i], w.c[i], w.first ? -b[i] : b[i], w.s[i]);
+  }
 }
 
 // How many of the f(s) given by the functor are at or below x, over the block; and in the upper bits whether any
@@ -247,9 +375,18 @@ __device__ __forceinline__ uint4 recode16(uint4 w, float f) {
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// Where the tables are read for the token at `pos`, new token `t` of the batch.
+__device__ __forceinline__ int table_row(const AppendParams& p, int t, int pos, int s) {
+  if (!p.positions || p.rot == 0) return pos;
+  const int at = p.positions[t];
+  if (at >= 0 && at < p.max_pos) return at;
+  record_error(p.b.status, kKvInvalid, uint32_t(s), uint32_t(at), uint32_t(p.max_pos));
+  return 0;
+}
+
 // TEAM threads to one (page, head, keys or values); KEEP passes' rows stay in registers.
-template <int D, int TEAM, int KEEP>
-__global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_constant__ AppendParams p) {
+template <int D, int TEAM, int KEEP, bool NORM>
+__global__ void __launch_bounds__(APP_THREADS, NORM ? 5 : 8) kv_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int UNITS = D / 8;             // threads to a row
   constexpr int STEP = TEAM / UNITS;       // rows of one pass
   __shared__ uint32_t counts[4];
@@ -266,7 +403,8 @@ __global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_
     if (s < 0) return;
     const KvSeq seq = kv_seq(b, ps, s);
     if (t < seq.row0 || t >= seq.row0 + seq.q) return;
-    const int pos = seq.len - seq.q + (t - seq.row0);
+    int pos = seq.len - seq.q + (t - seq.row0);
+    if (NORM && pos >= 0) pos = table_row(p, t, pos, s);
     if (p.rot > 0 && (pos < 0 || pos >= p.max_pos)) {
       if (tid == 0) record_error(b.status, kKvInvalid, uint32_t(s), uint32_t(pos), uint32_t(p.max_pos));
       return;
@@ -278,6 +416,12 @@ __global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_
     constexpr int STRIDE = APP_THREADS / UNITS, BATCH = 4;
     Turn w;
     turn_at(p, u, pos, w);
+    const bool norm = NORM && p.q_w;
+    uint4 wx = make_uint4(0, 0, 0, 0), wt = wx;
+    if (norm) {
+      wx = *reinterpret_cast<const uint4*>(p.q_w + 8 * u);
+      wt = *reinterpret_cast<const uint4*>(p.q_w + max(w.partner, 0));
+    }
     for (int h0 = tid / UNITS; h0 < p.H; h0 += STRIDE * BATCH) {
       uint4 x[BATCH], t4[BATCH];
 #pragma unroll
@@ -293,7 +437,8 @@ __global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_
         float a[8], b8[8], y[8];
         unpack8(x[k], a);
         unpack8(t4[k], b8);
-        turn<false>(p, w, a, b8, y);
+        if (norm) turn_normed<false>(p, w, row_norm<D, false>(a, p.eps), a, b8, wx, wt, y);
+        else turn<false>(p, w, a, b8, y);
         st_global_v4(dst + h * D + 8 * u, pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                      pack_bf16x2(y[6], y[7]));
       }
@@ -319,7 +464,7 @@ __global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_
   const int lo = max(int(page_begin), begin);                    // new positions in the page
   const int hi = int(min(page_begin + ps, int64_t(seq.len)));
   const int page = b.table[int64_t(s) * b.max_pages + page_no];  // page_no < max_pages: the length was checked
-  if (page < 0 || page >= p.c.num_pages || (p.rot > 0 && hi > p.max_pos)) {
+  if (page < 0 || page >= p.c.num_pages || (p.rot > 0 && hi > p.max_pos && !(NORM && p.positions))) {
     if (tid == 0) record_error(b.status, kKvInvalid, uint32_t(s), uint32_t(page), uint32_t(page_no));
     return;
   }
@@ -341,8 +486,22 @@ __global__ void __launch_bounds__(APP_THREADS, 8) kv_append_kernel(const __grid_
   uint32_t amax = 0;
   auto row8 = [&](int r, float(&out)[8]) {
     const uint16_t* row = src + int64_t(src0 + r) * src_ts;
-    if (values) load8(row + 8 * u, out);
-    else rotated8<true>(p, row, u, lo + r, out);
+    if (values) {
+      load8(row + 8 * u, out);
+    } else if (NORM) {
+      Turn w;
+      turn_at(p, u, table_row(p, src0 + r, lo + r, s), w);
+      float x[8], t[8];
+      load8(row + 8 * u, x);
+      load8(row + max(w.partner, 0), t);
+      if (p.k_w)
+        turn_normed<true>(p, w, row_norm<D, true>(x, p.eps), x, t, *reinterpret_cast<const uint4*>(p.k_w + 8 * u),
+                          *reinterpret_cast<const uint4*>(p.k_w + max(w.partner, 0)), out);
+      else
+        turn<true>(p, w, x, t, out);
+    } else {
+      rotated8<true>(p, row, u, lo + r, out);
+    }
   };
   auto take_max = [&](const float(&x)[8]) {
 #pragma unroll
@@ -428,40 +587,50 @@ tl_status check_kv_cache(const char* who, const tl_kv_cache& c) {
 
 }  // namespace tl
 
-extern "C" tl_status tl_kv_append(const tl_kv_append_args* a, void* stream) {
-  using namespace tl;
-  if (!a) return fail(TL_ERR_INVALID, "tl_kv_append: NULL args");
+namespace tl {
+namespace {
+
+// Both calls; n: what tl_kv_append_norm has beside the rest, or NULL.
+tl_status append(const char* who, const tl_kv_append_args* a, const tl_kv_append_norm_args* n, void* stream) {
+  if (!a) return fail(TL_ERR_INVALID, "%s: NULL args", who);
   if (a->n_tokens < 0 || a->B < 1 || a->B > (1 << 20) || a->max_pages < 1)
-    return fail(TL_ERR_INVALID, "tl_kv_append: n_tokens %d, B %d, max_pages %d", a->n_tokens, a->B, a->max_pages);
-  if (tl_status s = check_kv_cache("tl_kv_append", a->cache)) return s;
+    return fail(TL_ERR_INVALID, "%s: n_tokens %d, B %d, max_pages %d", who, a->n_tokens, a->B, a->max_pages);
+  if (tl_status s = check_kv_cache(who, a->cache)) return s;
   const int D = a->cache.head_dim;
-  if (a->H < 0 || a->H > 65536) return fail(TL_ERR_INVALID, "tl_kv_append: H %d", a->H);
+  if (a->H < 0 || a->H > 65536) return fail(TL_ERR_INVALID, "%s: H %d", who, a->H);
   if (a->rot_dim < 0 || a->rot_dim > D || a->rot_dim % 16)
-    return fail(TL_ERR_UNSUPPORTED, "tl_kv_append: rot_dim %d (a multiple of 16, 0..head_dim)", a->rot_dim);
+    return fail(TL_ERR_UNSUPPORTED, "%s: rot_dim %d (a multiple of 16, 0..head_dim)", who, a->rot_dim);
   if (a->interleaved != 0 && a->interleaved != 1)
-    return fail(TL_ERR_INVALID, "tl_kv_append: interleaved %d", a->interleaved);
-  if (a->max_q_len < 0) return fail(TL_ERR_INVALID, "tl_kv_append: max_q_len %d", a->max_q_len);
+    return fail(TL_ERR_INVALID, "%s: interleaved %d", who, a->interleaved);
+  if (a->max_q_len < 0) return fail(TL_ERR_INVALID, "%s: max_q_len %d", who, a->max_q_len);
   if (!a->cu_seqlens || !a->seq_lens || !a->page_table || !a->signals)
-    return fail(TL_ERR_INVALID, "tl_kv_append: NULL pointer argument");
+    return fail(TL_ERR_INVALID, "%s: NULL pointer argument", who);
   if (a->n_tokens == 0) return TL_OK;
-  if (!a->k || !a->v) return fail(TL_ERR_INVALID, "tl_kv_append: NULL pointer argument");
+  if (!a->k || !a->v) return fail(TL_ERR_INVALID, "%s: NULL pointer argument", who);
   if ((a->H > 0) != (a->q != nullptr) || (a->H > 0) != (a->q_out != nullptr))
-    return fail(TL_ERR_INVALID, "tl_kv_append: q and q_out go with H > 0");
+    return fail(TL_ERR_INVALID, "%s: q and q_out go with H > 0", who);
   if (a->rot_dim > 0 && (!a->cos || !a->sin || a->max_pos < 1))
-    return fail(TL_ERR_INVALID, "tl_kv_append: rot_dim %d needs cos, sin and max_pos", a->rot_dim);
+    return fail(TL_ERR_INVALID, "%s: rot_dim %d needs cos, sin and max_pos", who, a->rot_dim);
   for (const void* ptr : {a->k, a->v, a->q, (const void*)a->q_out, (const void*)a->cos, (const void*)a->sin})
-    if (!aligned16(ptr)) return fail(TL_ERR_INVALID, "tl_kv_append: pointers must be 16-byte aligned");
+    if (!aligned16(ptr)) return fail(TL_ERR_INVALID, "%s: pointers must be 16-byte aligned", who);
   for (int64_t s : {a->k_token_stride, a->k_head_stride, a->v_token_stride, a->v_head_stride, a->q_token_stride,
                     a->q_head_stride})
-    if (s < 0 || s % 8) return fail(TL_ERR_INVALID, "tl_kv_append: strides must be multiples of 8 elements");
+    if (s < 0 || s % 8) return fail(TL_ERR_INVALID, "%s: strides must be multiples of 8 elements", who);
   // A row's dims are read by the threads of both of a pair's units, with no order between them and the writes.
   if (a->H > 0 && rows_meet(a->q, a->q_token_stride * 2, (int64_t(a->H - 1) * a->q_head_stride + D) * 2, a->n_tokens,
                             a->q_out, int64_t(a->n_tokens) * a->H * D * 2))
-    return fail(TL_ERR_INVALID, "tl_kv_append: q_out overlaps q");
+    return fail(TL_ERR_INVALID, "%s: q_out overlaps q", who);
+  if (n) {
+    if (!aligned16(n->q_weight) || !aligned16(n->k_weight) || (reinterpret_cast<uintptr_t>(n->positions) & 3u))
+      return fail(TL_ERR_INVALID, "%s: weights must be 16-byte aligned, positions 4-byte", who);
+    if (n->q_weight && a->H == 0) return fail(TL_ERR_INVALID, "%s: q_weight without queries", who);
+    if ((n->q_weight || n->k_weight) && !(n->eps >= 1e-12f && n->eps <= 1e12f))
+      return fail(TL_ERR_INVALID, "%s: eps must lie within 1e-12 and 1e12", who);
+  }
   DeviceInfo di{};
   if (tl_status s = device_info(&di)) return s;
   if (a->signals->device != di.device)
-    return fail(TL_ERR_INVALID, "tl_kv_append: signals belong to another device");
+    return fail(TL_ERR_INVALID, "%s: signals belong to another device", who);
 
   AppendParams p{};
   const tl_kv_cache& c = a->cache;
@@ -484,6 +653,12 @@ extern "C" tl_status tl_kv_append(const tl_kv_append_args* a, void* stream) {
   p.rot = a->rot_dim;
   p.interleaved = a->interleaved;
   p.max_pos = a->max_pos;
+  if (n) {
+    p.q_w = static_cast<const uint16_t*>(n->q_weight);
+    p.k_w = static_cast<const uint16_t*>(n->k_weight);
+    p.positions = n->positions;
+    p.eps = n->eps;
+  }
   const int per_seq = a->max_q_len ? std::min(a->max_q_len, a->n_tokens) : cdiv(a->n_tokens, a->B);
   // A whole block to a page's keys or values of one head where a page gets 32 rows, else a warp: 8192 tokens of 8 kv heads
   // of 128 into pages of 16, 32, 64 and 256 take 58, 54, 52 and 82 us with blocks, 54, 54, 75 and 211 us with warps.
@@ -491,15 +666,28 @@ extern "C" tl_status tl_kv_append(const tl_kv_append_args* a, void* stream) {
   const int64_t items = int64_t(a->n_tokens) / c.page_size + 2 * int64_t(a->B);
   p.groups = wide ? 2 * c.H_kv : cdiv(2 * c.H_kv, APP_THREADS / 32);
   const int64_t blocks = items * p.groups + (a->H > 0 ? a->n_tokens : 0);
-  if (blocks > 0x7FFFFFFFll) return fail(TL_ERR_UNSUPPORTED, "tl_kv_append: too many tokens");
+  if (blocks > 0x7FFFFFFFll) return fail(TL_ERR_UNSUPPORTED, "%s: too many tokens", who);
   p.kv_blocks = int(items * p.groups);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (c.head_dim == 128) {
-    if (wide) kv_append_kernel<128, 128, 1><<<unsigned(blocks), APP_THREADS, 0, st>>>(p);
-    else kv_append_kernel<128, 32, 2><<<unsigned(blocks), APP_THREADS, 0, st>>>(p);
-  } else {
-    if (wide) kv_append_kernel<64, 128, 1><<<unsigned(blocks), APP_THREADS, 0, st>>>(p);
-    else kv_append_kernel<64, 32, 2><<<unsigned(blocks), APP_THREADS, 0, st>>>(p);
-  }
-  return cuda_ok(cudaGetLastError(), "tl_kv_append launch");
+  auto go = [&](auto dim, auto norm) {
+    constexpr int D = decltype(dim)::value;
+    constexpr bool NORM = decltype(norm)::value;
+    if (wide) kv_append_kernel<D, 128, 1, NORM><<<unsigned(blocks), APP_THREADS, 0, st>>>(p);
+    else kv_append_kernel<D, 32, 2, NORM><<<unsigned(blocks), APP_THREADS, 0, st>>>(p);
+  };
+  auto pick = [&](auto dim) { n ? go(dim, std::true_type()) : go(dim, std::false_type()); };
+  if (c.head_dim == 128) pick(std::integral_constant<int, 128>());
+  else pick(std::integral_constant<int, 64>());
+  return cuda_ok(cudaGetLastError(), who);
+}
+
+}  // namespace
+}  // namespace tl
+
+extern "C" tl_status tl_kv_append(const tl_kv_append_args* a, void* stream) {
+  return tl::append("tl_kv_append", a, nullptr, stream);
+}
+
+extern "C" tl_status tl_kv_append_norm(const tl_kv_append_norm_args* a, void* stream) {
+  return tl::append("tl_kv_append_norm", a ? &a->append : nullptr, a, stream);
 }
