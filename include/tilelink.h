@@ -754,6 +754,27 @@ typedef struct tl_kv_attn_args {
 size_t tl_kv_attn_workspace_size(int n_tokens, int B, int H, int H_kv, int head_dim, int sm_count);
 tl_status tl_kv_attn(const tl_kv_attn_args* args, void* stream);
 
+/* ---------------------------------------------------------------- attention of a tree of drafts over the cache
+ * tl_kv_attn for new tokens that are several continuations at once (a tree of drafts):
+ * all of a sequence's n_s new tokens lie in the cache at its end, and new token i sees
+ * the keys before them and those new tokens j whose bit is set in its mask,
+ *   s_j = scale * <q, k_j>   for j < seq_lens[s] - n_s, and
+ *                            for j = seq_lens[s] - n_s + b, b < n_s, where bit b % 32
+ *                            of tree[t * tree_words + b / 32] is 1
+ * (t the row of token i).  A token's own bit counts like any other; masks need not be
+ * those of a tree; bits from n_s on are not looked at, and new tokens from
+ * 32 * tree_words on are seen by none.  All else is as for tl_kv_attn, the workspace
+ * and its size too (attn.causal is 0).
+ */
+typedef struct tl_kv_tree_attn_args {
+  tl_kv_attn_args attn;
+  const uint32_t* tree;        /* device uint32 [n_tokens, tree_words] */
+  int32_t tree_words;          /* 1..256 */
+  int32_t reserved0;
+} tl_kv_tree_attn_args;
+
+tl_status tl_kv_tree_attn(const tl_kv_tree_attn_args* args, void* stream);
+
 /* ---------------------------------------------------------------- MoE layer for a few tokens
  * A whole mixture-of-experts layer for the tokens of a decode step: router
  * selection, gated experts, combine.  For token t:

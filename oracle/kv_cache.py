@@ -113,3 +113,22 @@ def attention(q, k, v, causal, scale):
             out[i, h] = (w[:, None] * v[:end, h // group]).sum(0) / w.sum()
             lse[h, i] = m + np.log(w.sum())
     return out, lse
+
+
+def tree_attention(q, k, v, sees, scale):
+    """q [n, H, D] of the last n of len(k) tokens: token i over the keys before them and the new tokens j with sees[i, j]."""
+    n, H, D = q.shape
+    group = H // k.shape[1]
+    out, lse = np.zeros((n, H, D)), np.full((H, n), -np.inf)
+    before = np.arange(len(k) - n)
+    for i in range(n):
+        keys = np.concatenate([before, len(k) - n + np.flatnonzero(sees[i])]).astype(int)
+        if len(keys) == 0:
+            continue
+        for h in range(H):
+            s = scale * (k[keys, h // group] @ q[i, h])
+            m = s.max()
+            w = np.exp(s - m)
+            out[i, h] = (w[:, None] * v[keys, h // group]).sum(0) / w.sum()
+            lse[h, i] = m + np.log(w.sum())
+    return out, lse

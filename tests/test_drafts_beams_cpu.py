@@ -61,3 +61,30 @@ def test_append_norm_null_and_nothing_to_do(B):
 def test_append_norm_packed_arguments_are_the_structure(B):
     n = len(list(flat(B.tl_kv_append_norm_args())))
     check_packed(B._APPEND_NORM, B.tl_kv_append_norm_args, floats=[n - 2])
+
+
+# ------------------------------------------------------------------ attention of a tree
+def tree_args(L, c=None, **kw):
+    from tests.test_serving_cpu import attn_args
+    a = dict(tree=4, tree_words=2, reserved0=0)
+    inner = {"causal": 0, **{k: v for k, v in kw.items() if k not in a}}
+    a.update({k: v for k, v in kw.items() if k in a})
+    return L.tl_kv_tree_attn_args(attn=attn_args(L, c, **inner), **a)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_tokens=-1), 1), (dict(H=3), 1), (dict(causal=1), 1), (dict(scale=-1.0), 1), (dict(q=None), 1), (dict(out=24), 1),
+    (dict(workspace=None), 1), (dict(tree=None), 1), (dict(tree=6), 1), (dict(tree_words=0), 4), (dict(tree_words=-3), 4),
+    (dict(tree_words=257), 4)])
+def test_tree_attention_refuses(B, kw, code):
+    assert B.lib.tl_kv_tree_attn(ctypes.byref(tree_args(B, **kw)), None) == code, kw
+    assert "tl_kv_tree_attn" in B.tl_last_error()
+
+
+def test_tree_attention_null_and_nothing_to_do(B):
+    assert B.lib.tl_kv_tree_attn(None, None) == B.TL_ERR_INVALID
+    assert B.lib.tl_kv_tree_attn(ctypes.byref(tree_args(B, n_tokens=0, q=None, out=None, workspace=None, tree=None)), None) == 0
+
+
+def test_tree_attention_packed_arguments_are_the_structure(B):
+    check_packed(B._TREE, B.tl_kv_tree_attn_args, floats=[6])

@@ -38,7 +38,7 @@ EXPORTED = [
     "tl_moe_down_workspace_size", "tl_moe_down_num_flags", "tl_moe_down",
     "tl_ag_attn_num_flags", "tl_ag_attn", "tl_allgather_ll_link_bytes", "tl_allgather_ll",
     "tl_test_hold_chunks",
-    "tl_kv_append", "tl_kv_append_norm", "tl_kv_attn_workspace_size", "tl_kv_attn",
+    "tl_kv_append", "tl_kv_append_norm", "tl_kv_attn_workspace_size", "tl_kv_attn", "tl_kv_tree_attn",
     "tl_moe_decode_workspace_size", "tl_moe_decode",
 ]
 
@@ -179,6 +179,10 @@ class tl_kv_attn_args(ctypes.Structure):
         ("cu_seqlens", _vp), ("seq_lens", _vp), ("page_table", _vp), ("workspace", _vp),
         ("workspace_bytes", ctypes.c_size_t), ("signals", _vp),
     ]
+
+
+class tl_kv_tree_attn_args(ctypes.Structure):
+    _fields_ = [("attn", tl_kv_attn_args), ("tree", _vp), ("tree_words", ctypes.c_int32), ("reserved0", ctypes.c_int32)]
 
 
 class tl_moe_decode_args(ctypes.Structure):
@@ -562,9 +566,10 @@ def tl_ag_attn(Q, K_shards, V_shards, K_gathered, V_gathered, O, signals: Signal
 _APPEND = struct.Struct("@8i4P3q4i3P6q7P")
 _APPEND_NORM = struct.Struct(_APPEND.format + "3Pfi")
 _ATTN = struct.Struct("@6ifi4P3q4iP2q6PNP")
+_TREE = struct.Struct(_ATTN.format + "P2i")
 _MOE = struct.Struct("@8i8PN")
 assert _APPEND.size == ctypes.sizeof(tl_kv_append_args) and \
-    _APPEND_NORM.size == ctypes.sizeof(tl_kv_append_norm_args) and _ATTN.size == ctypes.sizeof(tl_kv_attn_args) and \
+    _APPEND_NORM.size == ctypes.sizeof(tl_kv_append_norm_args) and _TREE.size == ctypes.sizeof(tl_kv_tree_attn_args) and _ATTN.size == ctypes.sizeof(tl_kv_attn_args) and \
     _MOE.size == ctypes.sizeof(tl_moe_decode_args)
 
 
@@ -576,7 +581,7 @@ def _packed(name):
 
 
 _kv_append, _kv_attn, _moe_decode = _packed("tl_kv_append"), _packed("tl_kv_attn"), _packed("tl_moe_decode")
-_kv_append_norm = _packed("tl_kv_append_norm")
+_kv_append_norm, _kv_tree_attn = _packed("tl_kv_append_norm"), _packed("tl_kv_tree_attn")
 _torch = None
 
 
@@ -720,11 +725,8 @@ def tl_kv_attn_workspace_size(n_tokens, B, H, H_kv, head_dim, sm_count=0):
     return int(lib.tl_kv_attn_workspace_size(n_tokens, B, H, H_kv, head_dim, sm_count))
 
 
-def tl_kv_attn(q, cache: KvCache, out, cu_seqlens, seq_lens, page_table, workspace, signals: Signals, *, causal=True,
-               scale=0.0, max_q_len=0, lse=None, stream=None):
-    """out [n, H, D] = attention of q [n, H, D] over each sequence's keys and values in the cache, the new
-    tokens' included; lse optional float [H, n] (see tilelink.h)."""
-    st, dev = _place(stream)
+def _attn_fields(dev, q, cache, out, cu_seqlens, seq_lens, page_table, workspace, signals, causal, scale, max_q_len, lse):
+    """tl_kv_attn_args, field by field."""
     bf16 = _torch.bfloat16
     n, H, D = q.shape
     if D != cache.head_dim:
@@ -732,10 +734,30 @@ def tl_kv_attn(q, cache: KvCache, out, cu_seqlens, seq_lens, page_table, workspa
     _held(cache, dev)
     B, max_pages, cu, lens, table = _batch(cu_seqlens, seq_lens, page_table, _torch.int32, dev)
     qp, qa, qb = _rows(q, "q", bf16, (n, H, D), dev)
-    code = _kv_attn(_ATTN.pack(n, B, H, bool(causal), max_pages, max_q_len, scale, 0, *cache.fields, qp, qa, qb,
-                               _typed(out, "out", bf16, (n, H, D), dev),
-                               0 if lse is None else _typed(lse, "lse", _torch.float32, (H, n), dev), cu, lens, table,
-                               *_scratch(workspace, dev), signals.handle.value), st)
+    return (n, B, H, causal, max_pages, max_q_len, scale, 0, *cache.fields, qp, qa, qb, _typed(out, "out", bf16, (n, H, D), dev),
+            0 if lse is None else _typed(lse, "lse", _torch.float32, (H, n), dev), cu, lens, table, *_scratch(workspace, dev),
+            signals.handle.value)
+
+
+def tl_kv_attn(q, cache: KvCache, out, cu_seqlens, seq_lens, page_table, workspace, signals: Signals, *, causal=True,
+               scale=0.0, max_q_len=0, lse=None, stream=None):
+    """out [n, H, D] = attention of q [n, H, D] over each sequence's keys and values in the cache, the new
+    tokens' included; lse optional float [H, n] (see tilelink.h)."""
+    st, dev = _place(stream)
+    code = _kv_attn(_ATTN.pack(*_attn_fields(dev, q, cache, out, cu_seqlens, seq_lens, page_table, workspace, signals,
+                                             bool(causal), scale, max_q_len, lse)), st)
+    if code:
+        _check(code)
+
+
+def tl_kv_tree_attn(q, cache: KvCache, out, cu_seqlens, seq_lens, page_table, tree, workspace, signals: Signals, *, scale=0.0,
+                    max_q_len=0, lse=None, stream=None):
+    """tl_kv_attn for a tree of drafts: tree [n, words] (int32 bits) says which of its sequence's new tokens each new
+    token sees beside those before them (see tilelink.h)."""
+    st, dev = _place(stream)
+    words = tree.shape[1]
+    fields = _attn_fields(dev, q, cache, out, cu_seqlens, seq_lens, page_table, workspace, signals, 0, scale, max_q_len, lse)
+    code = _kv_tree_attn(_TREE.pack(*fields, _typed(tree, "tree", _torch.int32, (q.shape[0], words), dev), words, 0), st)
     if code:
         _check(code)
 

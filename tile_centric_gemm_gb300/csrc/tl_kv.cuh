@@ -87,6 +87,23 @@ __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
   return r;
 }
 
+// A tree of new tokens: bit j of a token's mask says whether it sees its sequence's new token j.  Tokens before the new
+// ones are seen by all.
+struct KvTree {
+  const uint32_t* mask;  // [n_tokens, words]
+  int32_t words;
+};
+// Which of the 32 tokens from number rel among the new ones on (below 0: before them) a token with mask m sees.
+__device__ __forceinline__ uint32_t tree_window(const uint32_t* m, int words, int rel) {
+  const int w = rel >> 5;
+  if (w < -1) return 0xFFFFFFFFu;
+  const uint32_t lo = w < 0 ? 0xFFFFFFFFu : w < words ? __ldg(m + w) : 0u;
+  const uint32_t hi = w + 1 < words ? __ldg(m + w + 1) : 0u;
+  return __funnelshift_r(lo, hi, uint32_t(rel) & 31u);
+}
+// The lowest n of 32 bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // 2^e for -127 <= e <= 127 (2^-127 is a subnormal); anything above is NaN (scale byte 255).
 __device__ __forceinline__ float pow2f(int e) {
   if (e > 127) return __uint_as_float(0x7FFFFFFFu);

@@ -92,6 +92,7 @@ struct DecodeParams {
   int32_t H, group, causal;
   int32_t max_rows;    // sequences of more query rows per kv head are left to the kernel for many
   float scale_log2;
+  KvTree tree;         // tl_kv_tree_attn
 };
 
 template <int D, int NR, int WARPS, int PER_SM>
@@ -243,7 +244,9 @@ __device__ __noinline__ float2 own_reference(int32_t* at, float mo, float mn, fl
 
 // NR: products of 8 query rows to a tile
 // PER_SM: CTAs of an SM
-template <int D, int NR, int WARPS, int PER_SM>
+// TREE: which new tokens a row sees goes by its token's mask (p.causal is 0 then); only chunks that hold new tokens,
+// at a sequence's end, look at it.
+template <int D, int NR, int WARPS, int PER_SM, bool TREE>
 __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __grid_constant__ DecodeParams p) {
   using Smem = DecodeSmem<D, NR, WARPS, PER_SM>;
   constexpr int THREADS = WARPS * 32, STAGES = Smem::STAGES;
@@ -482,10 +485,14 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
     auto limit = [&](int row) {  // keys that a row of the tile sees
       return p.causal ? max(0, min(c.seq.len, start + (r0 + min(row, rows - 1)) / p.group + 1)) : c.seq.len;
     };
+    auto token = [&](int row) { return c.seq.row0 + (r0 + min(row, rows - 1)) / p.group; };
+    auto window = [&](int t, int tok) {  // of 32 tokens from tok on, those that new token t sees
+      return tree_window(p.tree.mask + int64_t(t) * p.tree.words, p.tree.words, tok - start) & low_bits(c.seq.len - tok);
+    };
     // queries: row g of each product; scales and limits of rows 2t and 2t + 1
     uint32_t qb[NR][KL * 4][2];
     float f_row[NR][2];
-    int lim[NR][2];
+    int lim[NR][2];  // with TREE: the rows' tokens
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
       const uint4(&w)[KL * 2] = qraw[x];
@@ -516,10 +523,10 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         f_row[x][y] = __shfl_sync(0xffffffffu, fr, (2 * t + y) * 4);
-        lim[x][y] = limit(8 * x + 2 * t + y);
+        lim[x][y] = TREE ? token(8 * x + 2 * t + y) : limit(8 * x + 2 * t + y);
       }
     }
-    const int min_lim = limit(0);
+    const int min_lim = TREE ? min(start, c.seq.len) : limit(0);
 
     float o[NR][MTS][4];  // dims g * VB + i and g * VB + VB/2 + i of rows 2t, 2t + 1
 #pragma unroll
@@ -573,7 +580,20 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
           for (int k = 0; k < 4; ++k)
             s[h][x][k] = (KL == 2 ? part[0][x][k] + part[KL - 1][x][k] : part[0][x][k]) * (f_row[x][k & 1] * kf);
       }
-      if (edge) {
+      if (TREE && edge) {
+        const uint32_t there = (meta.y & 1u ? 0xFFFFu : 0u) | (meta.y & 2u ? 0xFFFF0000u : 0u);
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t sees = (window(lim[x][y], tok) & there) >> g;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int k = y; k < 4; k += 2)
+                if (!(sees >> (h * 16 + (k >> 1) * 8) & 1u)) s[h][x][k] = -INFINITY;
+          }
+      } else if (edge) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -724,9 +744,16 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
           if (__any_sync(0xffffffffu, nans != 0)) {
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
-              const int li = limit(8 * x + g), tk = tok + h * 16 + 2 * t;
-              const uint32_t b0 = (tk < li ? 0x3C00u : 0u) | (tk + 1 < li ? 0x3C000000u : 0u);
-              const uint32_t b1 = (tk + 8 < li ? 0x3C00u : 0u) | (tk + 9 < li ? 0x3C000000u : 0u);
+              uint32_t b0, b1;
+              if (TREE) {
+                const uint32_t sees = window(token(8 * x + g), tok) >> (h * 16 + 2 * t);
+                b0 = (sees & 1u ? 0x3C00u : 0u) | (sees & 2u ? 0x3C000000u : 0u);
+                b1 = (sees & 0x100u ? 0x3C00u : 0u) | (sees & 0x200u ? 0x3C000000u : 0u);
+              } else {
+                const int li = limit(8 * x + g), tk = tok + h * 16 + 2 * t;
+                b0 = (tk < li ? 0x3C00u : 0u) | (tk + 1 < li ? 0x3C000000u : 0u);
+                b1 = (tk + 8 < li ? 0x3C00u : 0u) | (tk + 9 < li ? 0x3C000000u : 0u);
+              }
 #pragma unroll
               for (int i = 0; i < MTS; ++i) {
                 uint32_t a[2][2];  // [dims i or VB/2 + i][tokens 2t.. or 2t+8..]
@@ -930,11 +957,11 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
   pdl_wait_previous();  // the call ends when the kernel for many rows has ended too
 }
 
-template <int D, int NR, int WARPS, int PER_SM>
+template <int D, int NR, int WARPS, int PER_SM, bool TREE>
 tl_status launch_decode(void** args, int ctas, cudaStream_t st, bool early) {
   using Smem = DecodeSmem<D, NR, WARPS, PER_SM>;
   static_assert(sizeof(Smem) <= 232448 / PER_SM - (PER_SM - 1) * 1024, "shared memory above the limit");
-  return launch(reinterpret_cast<const void*>(&kv_decode_kernel<D, NR, WARPS, PER_SM>), ctas * PER_SM, WARPS * 32, sizeof(Smem), st, args,
+  return launch(reinterpret_cast<const void*>(&kv_decode_kernel<D, NR, WARPS, PER_SM, TREE>), ctas * PER_SM, WARPS * 32, sizeof(Smem), st, args,
                 early);
 }
 
@@ -962,35 +989,43 @@ extern "C" size_t tl_kv_attn_workspace_size(int n_tokens, int B, int H, int H_kv
   return bytes;
 }
 
-extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
-  using namespace tl;
-  if (!a) return fail(TL_ERR_INVALID, "tl_kv_attn: NULL args");
+namespace tl {
+namespace {
+
+// Both calls; tree: the masks of tl_kv_tree_attn, or NULL.
+tl_status attention(const char* who, const tl_kv_attn_args* a, const KvTree* tree, void* stream) {
+  if (!a) return fail(TL_ERR_INVALID, "%s: NULL args", who);
   if (a->n_tokens < 0 || a->B < 1 || a->B > (1 << 20) || a->max_pages < 1)
-    return fail(TL_ERR_INVALID, "tl_kv_attn: n_tokens %d, B %d, max_pages %d", a->n_tokens, a->B, a->max_pages);
-  if (tl_status s = check_kv_cache("tl_kv_attn", a->cache)) return s;
+    return fail(TL_ERR_INVALID, "%s: n_tokens %d, B %d, max_pages %d", who, a->n_tokens, a->B, a->max_pages);
+  if (tl_status s = check_kv_cache(who, a->cache)) return s;
   const tl_kv_cache& c = a->cache;
   if (a->H < 1 || a->H > 65536 || a->H % c.H_kv)
-    return fail(TL_ERR_INVALID, "tl_kv_attn: H=%d is not a multiple of H_kv=%d", a->H, c.H_kv);
-  if (a->causal != 0 && a->causal != 1) return fail(TL_ERR_INVALID, "tl_kv_attn: causal %d", a->causal);
-  if (a->max_q_len < 0) return fail(TL_ERR_INVALID, "tl_kv_attn: max_q_len %d", a->max_q_len);
+    return fail(TL_ERR_INVALID, "%s: H=%d is not a multiple of H_kv=%d", who, a->H, c.H_kv);
+  if (tree && a->causal != 0) return fail(TL_ERR_INVALID, "%s: causal goes by the tree (0)", who);
+  if (tree && (tree->words < 1 || tree->words > 256))
+    return fail(TL_ERR_UNSUPPORTED, "%s: tree_words %d (1..256)", who, tree->words);
+  if (a->causal != 0 && a->causal != 1) return fail(TL_ERR_INVALID, "%s: causal %d", who, a->causal);
+  if (a->max_q_len < 0) return fail(TL_ERR_INVALID, "%s: max_q_len %d", who, a->max_q_len);
   if (!(a->scale >= 0.0f) || std::isinf(a->scale))
-    return fail(TL_ERR_INVALID, "tl_kv_attn: scale must be positive and finite (0 = 1/sqrt(head_dim))");
+    return fail(TL_ERR_INVALID, "%s: scale must be positive and finite (0 = 1/sqrt(head_dim))", who);
   if (!a->cu_seqlens || !a->seq_lens || !a->page_table || !a->signals)
-    return fail(TL_ERR_INVALID, "tl_kv_attn: NULL pointer argument");
+    return fail(TL_ERR_INVALID, "%s: NULL pointer argument", who);
   if (a->n_tokens == 0) return TL_OK;
-  if (!a->q || !a->out || !a->workspace) return fail(TL_ERR_INVALID, "tl_kv_attn: NULL pointer argument");
+  if (!a->q || !a->out || !a->workspace) return fail(TL_ERR_INVALID, "%s: NULL pointer argument", who);
+  if (tree && (!tree->mask || (reinterpret_cast<uintptr_t>(tree->mask) & 3u)))
+    return fail(TL_ERR_INVALID, "%s: tree is NULL or not 4-byte aligned", who);
   if (!aligned16(a->q) || !aligned16(a->out) || !aligned16(a->workspace) || (reinterpret_cast<uintptr_t>(a->lse) & 3u))
-    return fail(TL_ERR_INVALID, "tl_kv_attn: pointers must be 16-byte aligned (lse 4-byte)");
+    return fail(TL_ERR_INVALID, "%s: pointers must be 16-byte aligned (lse 4-byte)", who);
   for (int64_t s : {a->q_token_stride, a->q_head_stride})
-    if (s < 0 || s % 8) return fail(TL_ERR_INVALID, "tl_kv_attn: strides must be multiples of 8 elements");
+    if (s < 0 || s % 8) return fail(TL_ERR_INVALID, "%s: strides must be multiples of 8 elements", who);
   if (int64_t(a->n_tokens) * (a->H / c.H_kv) > 0x7FFF0000ll)
-    return fail(TL_ERR_UNSUPPORTED, "tl_kv_attn: too many query rows");
+    return fail(TL_ERR_UNSUPPORTED, "%s: too many query rows", who);
   DeviceInfo di{};
   if (tl_status s = device_info(&di)) return s;
-  if (a->signals->device != di.device) return fail(TL_ERR_INVALID, "tl_kv_attn: signals belong to another device");
+  if (a->signals->device != di.device) return fail(TL_ERR_INVALID, "%s: signals belong to another device", who);
   const size_t need = tl_kv_attn_workspace_size(a->n_tokens, a->B, a->H, c.H_kv, c.head_dim, di.sm_count);
   if (a->workspace_bytes < need)
-    return fail(TL_ERR_INVALID, "tl_kv_attn: workspace of %zu bytes, need %zu", a->workspace_bytes, need);
+    return fail(TL_ERR_INVALID, "%s: workspace of %zu bytes, need %zu", who, a->workspace_bytes, need);
 
   DecodeParams p{};
   p.c = KvCacheDev{static_cast<uint8_t*>(c.k), static_cast<uint8_t*>(c.v), c.k_scale, c.v_scale, c.page_stride,
@@ -1006,6 +1041,7 @@ extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
   p.H = a->H;
   p.group = a->H / c.H_kv;
   p.causal = a->causal;
+  if (tree) p.tree = *tree;
   p.scale_log2 = (a->scale > 0.0f ? a->scale : 1.0f / std::sqrt(float(c.head_dim))) * 1.4426950408889634f;
   // Most new tokens that a sequence can have, as far as the host knows
   const int most = a->max_q_len ? std::min(a->max_q_len, a->n_tokens) : std::max(1, a->n_tokens - a->B + 1);
@@ -1029,6 +1065,7 @@ extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
     f.H = a->H;
     f.group = p.group;
     f.causal = a->causal;
+    f.tree = p.tree;
     f.min_rows = a->B == 1 ? 0 : few_rows(a->B);
     f.scale_log2 = p.scale_log2;
     if (tl_status s = launch_kv_prefill(f, c.head_dim, di.sm_count, st)) return s;
@@ -1039,11 +1076,29 @@ extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
   const bool small = int64_t(most) * p.group <= 8;
   void* args[] = {&p};
   const int per = per_sm(int64_t(a->B) * c.H_kv, small, di.sm_count);
-  auto go = [&](auto dim) {
+  auto go = [&](auto dim, auto by_tree) {
     constexpr int D = decltype(dim)::value;
-    if (!small) return per == 1 ? launch_decode<D, 2, 8, 1>(args, di.sm_count, st, many) : launch_decode<D, 2, 4, 2>(args, di.sm_count, st, many);
-    if (per == 1) return launch_decode<D, 1, 12, 1>(args, di.sm_count, st, many);
-    return per == 2 ? launch_decode<D, 1, 6, 2>(args, di.sm_count, st, many) : launch_decode<D, 1, 3, 4>(args, di.sm_count, st, many);
+    constexpr bool TREE = decltype(by_tree)::value;
+    if (!small)
+      return per == 1 ? launch_decode<D, 2, 8, 1, TREE>(args, di.sm_count, st, many)
+                      : launch_decode<D, 2, 4, 2, TREE>(args, di.sm_count, st, many);
+    if (per == 1) return launch_decode<D, 1, 12, 1, TREE>(args, di.sm_count, st, many);
+    return per == 2 ? launch_decode<D, 1, 6, 2, TREE>(args, di.sm_count, st, many)
+                    : launch_decode<D, 1, 3, 4, TREE>(args, di.sm_count, st, many);
   };
-  return c.head_dim == 128 ? go(std::integral_constant<int, 128>()) : go(std::integral_constant<int, 64>());
+  auto pick = [&](auto dim) { return tree ? go(dim, std::true_type()) : go(dim, std::false_type()); };
+  return c.head_dim == 128 ? pick(std::integral_constant<int, 128>()) : pick(std::integral_constant<int, 64>());
+}
+
+}  // namespace
+}  // namespace tl
+
+extern "C" tl_status tl_kv_attn(const tl_kv_attn_args* a, void* stream) {
+  return tl::attention("tl_kv_attn", a, nullptr, stream);
+}
+
+extern "C" tl_status tl_kv_tree_attn(const tl_kv_tree_attn_args* a, void* stream) {
+  if (!a) return tl::fail(TL_ERR_INVALID, "tl_kv_tree_attn: NULL args");
+  const tl::KvTree tree{a->tree, a->tree_words};
+  return tl::attention("tl_kv_tree_attn", &a->attn, &tree, stream);
 }

@@ -43,10 +43,14 @@
 // token of each dim is kept: rows see prefixes, so a row's result in that dim is NaN
 // exactly if the row sees that token.
 //
+// A tree's rows see what their tokens' masks say: all keys go to every row's unit, windows of 32 mask bits take the place
+// of the limit, and which rows see a NaN value is looked up in the cache once there is one (tree_nan).
+//
 // TMEM (lane = query row of the tile): S_A columns 0-63 and 64-127, S_B 128-191 and
 // 192-255 (P in the first half of each), O_A from 256, O_B from 384.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "tl_common.cuh"
 #include "tl_internal.h"
@@ -317,6 +321,36 @@ __device__ __forceinline__ void mask(uint32_t (&v)[32], int vis) {
       if (k >= vis) v[k] = __float_as_uint(-INFINITY);
   }
 }
+// Which tokens of a tile a row sees: those before its limit (int), or in a tree those of the bits.
+struct Seen {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ void mask(uint32_t (&v)[32], int vis, int half) { mask(v, vis - 32 * half); }
+__device__ __forceinline__ void mask(uint32_t (&v)[32], const Seen& w, int half) {
+  const uint32_t bits = half ? w.hi : w.lo;
+  if (bits != 0xFFFFFFFFu) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (!(bits >> k & 1u)) v[k] = __float_as_uint(-INFINITY);
+  }
+}
+// Which of dims d0 .. d0+31 are NaN in the rows of new token `token`, by a value of a token first .. last-1 that it sees.  Runs over the cache once more, for units that hold such a value.
+__device__ __noinline__ uint32_t tree_nan(const PrefillParams& p, int s, int hk, int token, int start, int first, int last, int d0) {
+  const uint32_t* m = p.tree.mask + int64_t(token) * p.tree.words;
+  uint32_t out = 0;
+  for (int tok = first; tok < last; ++tok) {
+    if (!(tree_window(m, p.tree.words, tok - start) & 1u)) continue;
+    const int no = tok / p.c.ps;
+    const int page = __ldg(p.b.table + int64_t(s) * p.b.max_pages + no);
+    if (page < 0 || page >= p.c.num_pages) continue;
+    if (p.c.vs[int64_t(page) * p.c.Hkv + hk] == 255) return 0xFFFFFFFFu;
+    const uint8_t* at = p.c.v + int64_t(page) * p.c.page_stride + int64_t(hk) * p.c.head_stride +
+                        int64_t(tok - no * p.c.ps) * p.c.token_stride + d0;
+    for (int d = 0; d < 32; ++d)
+      if ((at[d] & 0x7Fu) == 0x7Fu) out |= 1u << d;
+  }
+  return out;
+}
 __device__ __forceinline__ float max32(const uint32_t (&v)[32]) {  // in four chains
   float q[4];
 #pragma unroll
@@ -370,7 +404,8 @@ __device__ __forceinline__ float score_factor(float scale, int e) {
 // Without scale bytes (nullptr): f is the factor of all scores, e stays 0.  This is for great scores.  Elsewhere s f - m
 // is one fused operation, whose product is not rounded as the maximum m was: of scores above 2^27 the largest would come
 // out beyond what P holds, or vanish.
-__device__ __noinline__ float4 far_tile(uint32_t s_addr, int vis, const volatile uint16_t* bytes, float scale, int qe, float m,
+template <typename SEEN>
+__device__ __noinline__ float4 far_tile(uint32_t s_addr, SEEN seen, const volatile uint16_t* bytes, float scale, int qe, float m,
                                         float l, int e) {
   float most[GROUPS], f[GROUPS];
   int vb[GROUPS];
@@ -380,7 +415,7 @@ __device__ __noinline__ float4 far_tile(uint32_t s_addr, int vis, const volatile
     uint32_t v[32];
     tmem_ld_32cols(s_addr + uint32_t(h * 32), v);
     tmem_ld_wait();
-    mask(v, vis - 32 * h);
+    mask(v, seen, h);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const uint32_t b = bytes ? bytes[2 * h + q] : 127u | 127u << 8;
@@ -409,7 +444,7 @@ __device__ __noinline__ float4 far_tile(uint32_t s_addr, int vis, const volatile
     uint32_t v[32], w[16];
     tmem_ld_32cols(s_addr + uint32_t(h * 32), v);
     tmem_ld_wait();
-    mask(v, vis - 32 * h);
+    mask(v, seen, h);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       // weight times scale from one exponent: of a small weight and a large scale each alone may leave fp32
@@ -468,7 +503,7 @@ __device__ __noinline__ float2 join_parts(const float* rows_at, int c0, int c1, 
   return make_float2(top, sum);
 }
 
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_constant__ PrefillParams p) {
   using L = Layout<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -605,7 +640,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     for (int i = 0; ok; ++i) {
       const int rows = seq_rows(p, g.seq);
       const int len = g.seq.len;
-      const int min_lim = row_limit(p, g.seq, g.qb * UNIT);
+      const int min_lim = TREE ? len - g.seq.q : row_limit(p, g.seq, g.qb * UNIT);
       const int32_t* table = b.table + int64_t(g.s) * b.max_pages;
       // the largest scales of the segment's pages
       const int tok_end = min(len, g.t1 * KV);
@@ -865,6 +900,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const int r = g.qb * UNIT + X * ROWS + row;
       const int rows = seq_rows(p, g.seq);
       const int lim = row_limit(p, g.seq, min(r, rows - 1));
+      const int token = TREE ? g.seq.row0 + min(r, rows - 1) / p.group : 0;
       float m = -INFINITY, l = 0.0f, f = 0.0f;
       int e = kFar;  // O is in units of 2^e where scales are far apart
       for (int j = g.t0; j < g.t1; ++j, ++sc) {
@@ -881,6 +917,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         const uint32_t s_addr = s_base + (sc & 1) * 64;
         const int vis = lim - j * KV;
+        std::conditional_t<TREE, Seen, int> seen;
+        if constexpr (TREE) {
+          seen = Seen{0xFFFFFFFFu, 0xFFFFFFFFu};
+          const int rel = j * KV - (g.seq.len - g.seq.q);  // the tile's first token among the new ones
+          if (rel > -KV) {
+            const uint32_t* m = p.tree.mask + int64_t(token) * p.tree.words;
+            seen.lo = tree_window(m, p.tree.words, rel) & low_bits(vis);
+            seen.hi = tree_window(m, p.tree.words, rel + 32) & low_bits(vis - 32);
+          }
+        } else {
+          seen = vis;
+        }
         // P first with the maximum as it is; the sum tells whether that was enough (each weight is at most the sum, and up to
         // 2^15 is fine).  Only if it was not is the tile's maximum taken, for the rows concerned, and P once more: on a
         // segment's first tile, and seldom after it.
@@ -893,8 +941,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           tmem_ld_32cols(s_addr, va);
           tmem_ld_32cols(s_addr + 32u, vb);
           tmem_ld_wait();
-          mask(va, vis);
-          mask(vb, vis - 32);
+          mask(va, seen, 0);
+          mask(vb, seen, 1);
           if (again) {
             const float mnew = __fmul_rn(fmaxf(max32(va), max32(vb)), f);
             resc = bad && mnew > m;
@@ -925,8 +973,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         const bool far = e != kFar;
         if (far || (again && __any_sync(0xffffffffu, fabsf(m) >= kGreat && m != -INFINITY))) {
-          const float4 r = far ? far_tile(s_addr, vis, sd.far[sc & 7], p.scale_log2, sd.q_exp[i & 1][X * ROWS + row], m, l, e)
-                               : far_tile(s_addr, vis, nullptr, f, 0, m, l, 0);
+          const float4 r = far ? far_tile(s_addr, seen, sd.far[sc & 7], p.scale_log2, sd.q_exp[i & 1][X * ROWS + row], m, l, e)
+                               : far_tile(s_addr, seen, nullptr, f, 0, m, l, 0);
           m = r.x;
           l = r.y;
           sum = 0.0f;
@@ -988,7 +1036,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         float x[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(o[k]) * inv * pe;
-        if (least_nan < lim) {
+        if (TREE && least_nan < lim) {
+          // (new tokens, and those that share 16 with them)
+          const int start = g.seq.len - g.seq.q;
+          const uint32_t nan = tree_nan(p, g.s, g.hk, token, start, max(g.t0 * KV, max(start, 0) & ~15), min(g.t1 * KV, g.seq.len), c * 32);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (nan >> k & 1u) x[k] = __uint_as_float(0x7FFFFFFFu);
+        } else if (least_nan < lim) {
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (sd.nan_at[i & 3][c * 32 + k] < lim) x[k] = __uint_as_float(0x7FFFFFFFu);
@@ -1060,10 +1115,12 @@ tl_status launch_kv_prefill(PrefillParams& p, int D, int ctas, cudaStream_t st) 
   const uint32_t halves = uint32_t(p.c.ps) / 16;
   p.page_magic = halves == 1 ? 0u : uint32_t((uint64_t(1) << 32) / halves) + 1;
   void* args[] = {&p};
-  return D == 128 ? launch(reinterpret_cast<const void*>(&kv_prefill_kernel<128>), ctas, THREADS, smem_bytes<128>(), st,
-                           args, false)
-                  : launch(reinterpret_cast<const void*>(&kv_prefill_kernel<64>), ctas, THREADS, smem_bytes<64>(), st,
-                           args, false);
+  auto go = [&](const void* kernel, uint32_t smem) { return launch(kernel, ctas, THREADS, smem, st, args, false); };
+  if (p.tree.mask)
+    return D == 128 ? go(reinterpret_cast<const void*>(&kv_prefill_kernel<128, true>), smem_bytes<128>())
+                    : go(reinterpret_cast<const void*>(&kv_prefill_kernel<64, true>), smem_bytes<64>());
+  return D == 128 ? go(reinterpret_cast<const void*>(&kv_prefill_kernel<128, false>), smem_bytes<128>())
+                  : go(reinterpret_cast<const void*>(&kv_prefill_kernel<64, false>), smem_bytes<64>());
 }
 
 }  // namespace tl

@@ -19,6 +19,7 @@ struct PrefillParams {
   int32_t H, group, causal;
   int32_t min_rows;    // sequences of more query rows per kv head than this are this kernel's
   float scale_log2;
+  KvTree tree;         // tl_kv_tree_attn (mask not NULL; causal is 0 then)
   uint32_t page_magic; // groups of 16 tokens to pages: the upper half of a product with it (set by launch_kv_prefill)
 };
 
