@@ -775,6 +775,129 @@ typedef struct tl_kv_tree_attn_args {
 
 tl_status tl_kv_tree_attn(const tl_kv_tree_attn_args* args, void* stream);
 
+/* ---------------------------------------------------------------- pages of the cache: shared, copied, compacted, taken, freed
+ * Which pages are whose: page tables [B, max_pages] with lengths as above (a sequence
+ * holds the first ceil(len / page_size) entries of its row), and refs[page], the number
+ * of sequences that hold a page; 0 is a free one.  tl_kv_fork and tl_kv_resize change
+ * tables and counts, once for all layers that share them; tl_kv_copy_pages and
+ * tl_kv_compact move codes and scales, in all layers' caches (of equal layout) in one
+ * launch for each 64.  New counts go to refs_out, which may be refs itself or a buffer
+ * apart.  Pages taken are the lowest-numbered free ones, in the order of the rows that
+ * need them; those that a call frees are free for the next call.  All of it runs on the
+ * device: no length, count or page number is read on the host.  What is wrong in the
+ * device arrays records TL_ERR_INVALID and nothing outside the caller's buffers is
+ * touched; calls on one stream may follow one another without a wait.
+ *
+ * tl_kv_fork: row o of the new table is a copy of row parents[o] (0..B_in-1; -1: an
+ * empty sequence), so several rows may go on from one and others end.  Full pages are
+ * shared.  A part-filled last page goes to the lowest row among its parent's children if
+ * nobody but the parent holds it (refs 1); each other child gets a page of its own, and
+ * copy i of n_copies is: the first copies[2][i] slots of page copies[0][i] to page
+ * copies[1][i], in the order of the rows; tl_kv_copy_pages takes these arrays as they
+ * are.  refs_out = refs, less one for each page of each old row, plus one for each page
+ * of each new one.  Where the free pages do not suffice TL_ERR_INVALID is recorded with
+ * the number missing, n_copies is 0, refs_out = refs, and the new table and lengths are
+ * left as they were (copies is undefined).  Entries behind a row's pages are left as they
+ * were.
+ */
+typedef struct tl_kv_fork_args {
+  int32_t B_in;                /* rows of page_table, >= 1 */
+  int32_t B_out;               /* rows of page_table_out, >= 1 */
+  int32_t max_pages;           /* columns of both */
+  int32_t page_size;           /* a multiple of 16, 16..256 */
+  int32_t num_pages;           /* entries of refs, >= 1 */
+  int32_t reserved0;
+  const int32_t* page_table;   /* device int32 [B_in, max_pages] */
+  const int32_t* seq_lens;     /* device int32 [B_in] */
+  const int32_t* refs;         /* device int32 [num_pages], 16-byte aligned */
+  const int32_t* parents;      /* device int32 [B_out] */
+  int32_t* page_table_out;     /* device int32 [B_out, max_pages], written; must not overlap page_table */
+  int32_t* seq_lens_out;       /* device int32 [B_out], written; must not overlap seq_lens */
+  int32_t* refs_out;           /* device int32 [num_pages], written */
+  int32_t* copies;             /* device int32 [3, B_out], written: from, to, filled slots */
+  int32_t* n_copies;           /* device int32, written */
+  void* workspace;             /* device scratch, 16-byte aligned; calls sharing it must not run concurrently */
+  size_t workspace_bytes;      /* >= tl_kv_fork_workspace_size(B_in, B_out) */
+  tl_signals* signals;         /* receives device-side errors in its status word (any size >= 1) */
+} tl_kv_fork_args;
+
+/* Workspace bytes; 0 for invalid sizes. */
+size_t tl_kv_fork_workspace_size(int B_in, int B_out);
+tl_status tl_kv_fork(const tl_kv_fork_args* args, void* stream);
+
+/* tl_kv_resize: sequence s goes from seq_lens[s] to new_lens[s] tokens.  Longer: pages
+ * are taken for it and entered in its row.  Shorter: the pages behind its new end lose
+ * its reference (0 tokens: all of them).  A sequence that ends in a part-filled page that
+ * others hold too (after it was cut) is forked before it is appended to.  Where the free
+ * pages do not suffice TL_ERR_INVALID is recorded with the number missing, refs_out =
+ * refs, and the entries behind the sequences' pages are undefined; a wrong length records
+ * TL_ERR_INVALID with the sequence, which keeps its pages.
+ */
+typedef struct tl_kv_resize_args {
+  int32_t B;                   /* sequences, >= 1 */
+  int32_t max_pages;           /* columns of page_table */
+  int32_t page_size;           /* a multiple of 16, 16..256 */
+  int32_t num_pages;           /* entries of refs, >= 1 */
+  int32_t* page_table;         /* device int32 [B, max_pages], new entries written */
+  const int32_t* seq_lens;     /* device int32 [B] */
+  const int32_t* new_lens;     /* device int32 [B] */
+  const int32_t* refs;         /* device int32 [num_pages], 16-byte aligned */
+  int32_t* refs_out;           /* device int32 [num_pages], written */
+  void* workspace;             /* device scratch, 16-byte aligned; calls sharing it must not run concurrently */
+  size_t workspace_bytes;      /* >= tl_kv_resize_workspace_size(B) */
+  tl_signals* signals;         /* receives device-side errors in its status word (any size >= 1) */
+} tl_kv_resize_args;
+
+/* Workspace bytes; 0 for invalid sizes. */
+size_t tl_kv_resize_workspace_size(int B);
+tl_status tl_kv_resize(const tl_kv_resize_args* args, void* stream);
+
+/* tl_kv_copy_pages: for i below n (and below *count where count is given) page src[i]'s
+ * first slots[i] tokens (NULL: all) and its scales go to page dst[i], keys and values, in
+ * every head and layer.  A page must not be written twice in a call, nor be read and
+ * written, unless by a copy to itself, which does nothing.  A page outside the pool or
+ * slots outside 0..page_size record TL_ERR_INVALID with i; that copy is left out.
+ */
+typedef struct tl_kv_copy_pages_args {
+  int32_t n_layers;            /* caches, 1..4096 */
+  int32_t n;                   /* entries of src and dst, >= 0 (0: nothing to do) */
+  const tl_kv_cache* caches;   /* host array [n_layers], of equal layout */
+  const int32_t* src;          /* device int32 [n] */
+  const int32_t* dst;          /* device int32 [n] */
+  const int32_t* slots;        /* device int32 [n], or NULL */
+  const int32_t* count;        /* device int32, or NULL */
+  tl_signals* signals;         /* receives device-side errors in its status word (any size >= 1) */
+} tl_kv_copy_pages_args;
+
+tl_status tl_kv_copy_pages(const tl_kv_copy_pages_args* args, void* stream);
+
+/* tl_kv_compact: of each sequence's n_s new tokens (the batch as for tl_kv_append and
+ * tl_kv_tree_attn) those that kept names stay: new token kept[s][i], i < n_kept[s],
+ * strictly rising, becomes the sequence's token seq_lens[s] - n_s + i, in every head and
+ * layer, and seq_lens_out[s] = seq_lens[s] - n_s + n_kept[s].  A page that receives kept
+ * tokens has as its scale byte the largest of those that its tokens (older ones too) were
+ * stored under; codes of a smaller one are shifted to it, rounded once to nearest even.
+ * Slots behind a sequence's new end hold nothing.  Kept tokens that are not rising, not
+ * new, or more than the new ones or max_kept record TL_ERR_INVALID with the sequence; it
+ * stays as it is, with its length.  The pages of a sequence's new tokens are its alone.
+ */
+typedef struct tl_kv_compact_args {
+  int32_t n_layers;            /* caches, 1..4096 */
+  int32_t B;                   /* sequences, >= 1 */
+  int32_t max_pages;           /* columns of page_table */
+  int32_t max_kept;            /* columns of kept, >= 1 */
+  const tl_kv_cache* caches;   /* host array [n_layers], of equal layout */
+  const int32_t* kept;         /* device int32 [B, max_kept] */
+  const int32_t* n_kept;       /* device int32 [B] */
+  const int32_t* cu_seqlens;   /* device int32 [B + 1] */
+  const int32_t* seq_lens;     /* device int32 [B] */
+  const int32_t* page_table;   /* device int32 [B, max_pages] */
+  int32_t* seq_lens_out;       /* device int32 [B], written; must not overlap seq_lens */
+  tl_signals* signals;         /* receives device-side errors in its status word (any size >= 1) */
+} tl_kv_compact_args;
+
+tl_status tl_kv_compact(const tl_kv_compact_args* args, void* stream);
+
 /* ---------------------------------------------------------------- MoE layer for a few tokens
  * A whole mixture-of-experts layer for the tokens of a decode step: router
  * selection, gated experts, combine.  For token t:

@@ -88,3 +88,116 @@ def test_tree_attention_null_and_nothing_to_do(B):
 
 def test_tree_attention_packed_arguments_are_the_structure(B):
     check_packed(B._TREE, B.tl_kv_tree_attn_args, floats=[6])
+
+
+# ------------------------------------------------------------------ pages
+def fork_args(L, **kw):
+    a = dict(B_in=4, B_out=6, max_pages=8, page_size=32, num_pages=100, reserved0=0, page_table=4096, seq_lens=8192, refs=16384,
+             parents=4, page_table_out=32768, seq_lens_out=65536, refs_out=16384, copies=4, n_copies=4, workspace=256,
+             workspace_bytes=1 << 20, signals=64)
+    a.update(kw)
+    return L.tl_kv_fork_args(**a)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B_in=0), 1), (dict(B_out=0), 1), (dict(B_out=1 << 21), 1), (dict(max_pages=0), 1), (dict(num_pages=0), 1),
+    (dict(page_size=8), 4), (dict(page_size=40), 4), (dict(page_size=512), 4), (dict(max_pages=1 << 28), 4),
+    (dict(page_table=None), 1), (dict(seq_lens=None), 1), (dict(refs=None), 1), (dict(parents=None), 1),
+    (dict(page_table_out=None), 1), (dict(seq_lens_out=None), 1), (dict(refs_out=None), 1), (dict(copies=None), 1),
+    (dict(n_copies=None), 1), (dict(workspace=None), 1), (dict(signals=None), 1), (dict(refs=16388), 1), (dict(workspace=260), 1),
+    (dict(workspace_bytes=64), 1), (dict(page_table_out=4096 + 64), 1), (dict(page_table_out=4096 - 64), 1),
+    (dict(seq_lens_out=8192), 1), (dict(refs_out=16384 + 16), 1)])
+def test_fork_refuses(B, kw, code):
+    assert B.lib.tl_kv_fork(ctypes.byref(fork_args(B, **kw)), None) == code, kw
+    assert "tl_kv_fork" in B.tl_last_error()
+
+
+def resize_args(L, **kw):
+    a = dict(B=4, max_pages=8, page_size=32, num_pages=100, page_table=4096, seq_lens=8192, new_lens=8192, refs=16384,
+             refs_out=16384, workspace=256, workspace_bytes=1 << 20, signals=64)
+    a.update(kw)
+    return L.tl_kv_resize_args(**a)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=0), 1), (dict(max_pages=0), 1), (dict(num_pages=0), 1), (dict(page_size=8), 4), (dict(page_table=None), 1),
+    (dict(seq_lens=None), 1), (dict(new_lens=None), 1), (dict(refs=None), 1), (dict(refs_out=None), 1), (dict(workspace=None), 1),
+    (dict(signals=None), 1), (dict(refs=16388), 1), (dict(workspace=260), 1), (dict(workspace_bytes=64), 1),
+    (dict(refs_out=16384 + 396), 1)])
+def test_resize_refuses(B, kw, code):
+    assert B.lib.tl_kv_resize(ctypes.byref(resize_args(B, **kw)), None) == code, kw
+    assert "tl_kv_resize" in B.tl_last_error()
+
+
+def layers(L, n=2, **kw):
+    return (L.tl_kv_cache * n)(*[cache(L, **(kw if i == n - 1 else {})) for i in range(n)])
+
+
+def test_copy_pages_refuses(B):
+    def call(caches, code, **kw):
+        a = dict(n_layers=2, n=3, caches=ctypes.addressof(caches) if caches else None, src=4, dst=8, slots=None, count=None, signals=64)
+        a.update(kw)
+        assert B.lib.tl_kv_copy_pages(ctypes.byref(B.tl_kv_copy_pages_args(**a)), None) == code, kw
+        assert code == 0 or "tl_kv_copy_pages" in B.tl_last_error()
+    good = layers(B)
+    for kw in (dict(n=-1), dict(n_layers=0), dict(src=None), dict(dst=None), dict(signals=None)):
+        call(good, 1, **kw)
+    call(good, 4, n_layers=5000)
+    call(None, 1)
+    call(good, 0, n=0, src=None, dst=None)
+    for kw, code in CACHE_ERRORS:
+        call(layers(B, **kw), code)
+    for kw in (dict(num_pages=5), dict(page_size=32), dict(H_kv=1), dict(head_dim=64), dict(token_stride=256)):
+        call(layers(B, **kw), 1)  # not laid out as the first
+    assert B.lib.tl_kv_copy_pages(None, None) == 1
+
+
+def test_compact_refuses(B):
+    def call(caches, code, **kw):
+        a = dict(n_layers=2, B=3, max_pages=4, max_kept=5, caches=ctypes.addressof(caches) if caches else None, kept=4, n_kept=4,
+                 cu_seqlens=4, seq_lens=4096, page_table=4, seq_lens_out=8192, signals=64)
+        a.update(kw)
+        assert B.lib.tl_kv_compact(ctypes.byref(B.tl_kv_compact_args(**a)), None) == code, kw
+        assert "tl_kv_compact" in B.tl_last_error()
+    good = layers(B)
+    for kw in (dict(B=0), dict(max_pages=0), dict(max_kept=0), dict(n_layers=0), dict(kept=None), dict(n_kept=None),
+               dict(cu_seqlens=None), dict(seq_lens=None), dict(page_table=None), dict(seq_lens_out=None), dict(signals=None),
+               dict(seq_lens_out=4100)):
+        call(good, 1, **kw)
+    call(None, 1)
+    for kw, code in CACHE_ERRORS:
+        call(layers(B, **kw), code)
+    assert B.lib.tl_kv_compact(None, None) == 1
+
+
+def test_page_calls_packed_arguments_and_sizes(B):
+    for fmt, cls in ((B._FORK, B.tl_kv_fork_args), (B._RESIZE, B.tl_kv_resize_args), (B._COPY_PAGES, B.tl_kv_copy_pages_args),
+                     (B._COMPACT, B.tl_kv_compact_args)):
+        check_packed(fmt, cls)
+    assert B.tl_kv_fork_workspace_size(4, 6) >= 4 * (2 * 4 + 6) and B.tl_kv_resize_workspace_size(1000) >= 4000
+    assert not any(B.tl_kv_fork_workspace_size(*a) for a in ((0, 1), (1, 0), (-1, 4), (1 << 21, 1)))
+    assert not B.tl_kv_resize_workspace_size(0) and not B.tl_kv_resize_workspace_size(1 << 21)
+
+
+# ------------------------------------------------------------------ the oracle
+def test_oracle_fork_and_resize_by_hand():
+    import numpy as np
+    from oracle import kv_pages
+    table = np.array([[4, 2, 0], [4, 5, 1]], np.int32)
+    lens, refs = np.array([20, 40], np.int32), np.array([0, 1, 1, 0, 2, 1, 0], np.int32)
+    out, n, new, copies = kv_pages.fork(table, lens, refs, [0, 0, -1, 1], 16, np.full((4, 3), -1, np.int32))
+    assert out.tolist() == [[4, 2, -1], [4, 0, -1], [-1, -1, -1], [4, 5, 1]] and n.tolist() == [20, 20, 0, 40]
+    assert copies == [(2, 0, 4)] and new.tolist() == [1, 1, 1, 0, 3, 1, 0]
+    t, r = kv_pages.resize(table, lens, [33, 16], refs, 16)
+    assert t.tolist() == [[4, 2, 0], [4, 5, 1]] and r.tolist() == [1, 0, 1, 0, 2, 0, 0]
+
+
+def test_oracle_compact_by_hand():
+    import numpy as np
+    from oracle import kv_pages
+    codes = np.zeros((2, 1, 16, 64), np.uint8)
+    codes[0, 0, 14:16, 0], codes[1, 0, :3, 0] = [0x38, 0x40], [0x48, 0x38, 0x50]  # 1, 2; 4, 1, 8
+    scales = np.array([[127], [129]], np.uint8)
+    c, s, n = kv_pages.compact(codes, scales, [[1, 3]], [0, 4], [19], np.array([[0, 1]]))  # tokens 15..18: keep 16, 18
+    assert n.tolist() == [17] and s.ravel().tolist() == [129, 129]
+    assert c[0, 0, 14, 0] == 0x28 and c[0, 0, 15, 0] == 0x48 and c[1, 0, 0, 0] == 0x50  # 1/4 of 2^2; 4; 8

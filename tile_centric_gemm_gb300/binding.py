@@ -39,6 +39,7 @@ EXPORTED = [
     "tl_ag_attn_num_flags", "tl_ag_attn", "tl_allgather_ll_link_bytes", "tl_allgather_ll",
     "tl_test_hold_chunks",
     "tl_kv_append", "tl_kv_append_norm", "tl_kv_attn_workspace_size", "tl_kv_attn", "tl_kv_tree_attn",
+    "tl_kv_fork_workspace_size", "tl_kv_fork", "tl_kv_resize_workspace_size", "tl_kv_resize", "tl_kv_copy_pages", "tl_kv_compact",
     "tl_moe_decode_workspace_size", "tl_moe_decode",
 ]
 
@@ -185,6 +186,28 @@ class tl_kv_tree_attn_args(ctypes.Structure):
     _fields_ = [("attn", tl_kv_attn_args), ("tree", _vp), ("tree_words", ctypes.c_int32), ("reserved0", ctypes.c_int32)]
 
 
+class tl_kv_fork_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B_in", "B_out", "max_pages", "page_size", "num_pages", "reserved0")] + [
+        (n, _vp) for n in ("page_table", "seq_lens", "refs", "parents", "page_table_out", "seq_lens_out", "refs_out", "copies",
+                           "n_copies", "workspace")] + [("workspace_bytes", ctypes.c_size_t), ("signals", _vp)]
+
+
+class tl_kv_resize_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "max_pages", "page_size", "num_pages")] + [
+        (n, _vp) for n in ("page_table", "seq_lens", "new_lens", "refs", "refs_out", "workspace")] + [
+        ("workspace_bytes", ctypes.c_size_t), ("signals", _vp)]
+
+
+class tl_kv_copy_pages_args(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n", ctypes.c_int32)] + [
+        (n, _vp) for n in ("caches", "src", "dst", "slots", "count", "signals")]
+
+
+class tl_kv_compact_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_layers", "B", "max_pages", "max_kept")] + [
+        (n, _vp) for n in ("caches", "kept", "n_kept", "cu_seqlens", "seq_lens", "page_table", "seq_lens_out", "signals")]
+
+
 class tl_moe_decode_args(ctypes.Structure):
     _fields_ = [
         ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("Hd", ctypes.c_int32),
@@ -237,6 +260,14 @@ _decl("tl_ag_attn", _i, ctypes.POINTER(tl_ag_attn_args), _vp)
 _decl("tl_kv_append", _i, ctypes.POINTER(tl_kv_append_args), _vp)
 _decl("tl_kv_attn_workspace_size", _sz, _i, _i, _i, _i, _i, _i)
 _decl("tl_kv_attn", _i, ctypes.POINTER(tl_kv_attn_args), _vp)
+_decl("tl_kv_append_norm", _i, ctypes.POINTER(tl_kv_append_norm_args), _vp)
+_decl("tl_kv_tree_attn", _i, ctypes.POINTER(tl_kv_tree_attn_args), _vp)
+_decl("tl_kv_fork_workspace_size", _sz, _i, _i)
+_decl("tl_kv_fork", _i, ctypes.POINTER(tl_kv_fork_args), _vp)
+_decl("tl_kv_resize_workspace_size", _sz, _i)
+_decl("tl_kv_resize", _i, ctypes.POINTER(tl_kv_resize_args), _vp)
+_decl("tl_kv_copy_pages", _i, ctypes.POINTER(tl_kv_copy_pages_args), _vp)
+_decl("tl_kv_compact", _i, ctypes.POINTER(tl_kv_compact_args), _vp)
 _decl("tl_moe_decode_workspace_size", _sz, _i, _i, _i, _i, _i, _i)
 _decl("tl_moe_decode", _i, ctypes.POINTER(tl_moe_decode_args), _vp)
 
@@ -567,10 +598,16 @@ _APPEND = struct.Struct("@8i4P3q4i3P6q7P")
 _APPEND_NORM = struct.Struct(_APPEND.format + "3Pfi")
 _ATTN = struct.Struct("@6ifi4P3q4iP2q6PNP")
 _TREE = struct.Struct(_ATTN.format + "P2i")
+_FORK = struct.Struct("@6i10PNP")
+_RESIZE = struct.Struct("@4i6PNP")
+_COPY_PAGES = struct.Struct("@2i6P")
+_COMPACT = struct.Struct("@4i8P")
 _MOE = struct.Struct("@8i8PN")
 assert _APPEND.size == ctypes.sizeof(tl_kv_append_args) and \
     _APPEND_NORM.size == ctypes.sizeof(tl_kv_append_norm_args) and _TREE.size == ctypes.sizeof(tl_kv_tree_attn_args) and _ATTN.size == ctypes.sizeof(tl_kv_attn_args) and \
-    _MOE.size == ctypes.sizeof(tl_moe_decode_args)
+    _MOE.size == ctypes.sizeof(tl_moe_decode_args) and _FORK.size == ctypes.sizeof(tl_kv_fork_args) and \
+    _RESIZE.size == ctypes.sizeof(tl_kv_resize_args) and _COPY_PAGES.size == ctypes.sizeof(tl_kv_copy_pages_args) and \
+    _COMPACT.size == ctypes.sizeof(tl_kv_compact_args)
 
 
 def _packed(name):
@@ -582,6 +619,8 @@ def _packed(name):
 
 _kv_append, _kv_attn, _moe_decode = _packed("tl_kv_append"), _packed("tl_kv_attn"), _packed("tl_moe_decode")
 _kv_append_norm, _kv_tree_attn = _packed("tl_kv_append_norm"), _packed("tl_kv_tree_attn")
+_kv_fork, _kv_resize = _packed("tl_kv_fork"), _packed("tl_kv_resize")
+_kv_copy_pages, _kv_compact = _packed("tl_kv_copy_pages"), _packed("tl_kv_compact")
 _torch = None
 
 
@@ -758,6 +797,93 @@ def tl_kv_tree_attn(q, cache: KvCache, out, cu_seqlens, seq_lens, page_table, tr
     words = tree.shape[1]
     fields = _attn_fields(dev, q, cache, out, cu_seqlens, seq_lens, page_table, workspace, signals, 0, scale, max_q_len, lse)
     code = _kv_tree_attn(_TREE.pack(*fields, _typed(tree, "tree", _torch.int32, (q.shape[0], words), dev), words, 0), st)
+    if code:
+        _check(code)
+
+
+class KvLayers:
+    """The caches of the layers that share one page table, all laid out alike.  Holds them."""
+
+    def __init__(self, caches):
+        if not caches:
+            raise ValueError("KvLayers: one cache at least")
+        self.caches, self.device = list(caches), caches[0].device
+        if any(c.fields[4:] != caches[0].fields[4:] or c.device != self.device for c in self.caches):
+            raise ValueError("KvLayers: the caches must have the same sizes and strides, on one device")
+        self.array = (tl_kv_cache * len(self.caches))(*(tl_kv_cache(*c.fields) for c in self.caches))
+        self.address = ctypes.addressof(self.array)
+
+
+def tl_kv_fork_workspace_size(B_in, B_out):
+    return int(lib.tl_kv_fork_workspace_size(B_in, B_out))
+
+
+def tl_kv_fork(page_table, seq_lens, refs, parents, page_table_out, seq_lens_out, refs_out, copies, n_copies, workspace,
+               signals: Signals, *, page_size, stream=None):
+    """Row o of page_table_out [B_out, max_pages] goes on from row parents[o] of page_table [B_in, max_pages]: pages are
+    shared, part-filled ones listed in copies [3, B_out] and n_copies [1] for tl_kv_copy_pages; refs [pages] count the
+    holders (all int32; see tilelink.h)."""
+    st, dev = _place(stream)
+    i32 = _torch.int32
+    (B, max_pages), n, pages = page_table.shape, parents.shape[0], refs.shape[0]
+    code = _kv_fork(_FORK.pack(
+        B, n, max_pages, page_size, pages, 0, _typed(page_table, "page_table", i32, (B, max_pages), dev),
+        _typed(seq_lens, "seq_lens", i32, (B,), dev), _typed(refs, "refs", i32, (pages,), dev),
+        _typed(parents, "parents", i32, (n,), dev), _typed(page_table_out, "page_table_out", i32, (n, max_pages), dev),
+        _typed(seq_lens_out, "seq_lens_out", i32, (n,), dev), _typed(refs_out, "refs_out", i32, (pages,), dev),
+        _typed(copies, "copies", i32, (3, n), dev), _typed(n_copies, "n_copies", i32, (1,), dev), *_scratch(workspace, dev),
+        signals.handle.value), st)
+    if code:
+        _check(code)
+
+
+def tl_kv_resize_workspace_size(B):
+    return int(lib.tl_kv_resize_workspace_size(B))
+
+
+def tl_kv_resize(page_table, seq_lens, new_lens, refs, refs_out, workspace, signals: Signals, *, page_size, stream=None):
+    """Sequences go from seq_lens [B] to new_lens [B] tokens: pages are taken into page_table [B, max_pages], or given
+    back; refs [pages] count the holders (all int32; see tilelink.h)."""
+    st, dev = _place(stream)
+    i32 = _torch.int32
+    (B, max_pages), pages = page_table.shape, refs.shape[0]
+    code = _kv_resize(_RESIZE.pack(
+        B, max_pages, page_size, pages, _typed(page_table, "page_table", i32, (B, max_pages), dev),
+        _typed(seq_lens, "seq_lens", i32, (B,), dev), _typed(new_lens, "new_lens", i32, (B,), dev),
+        _typed(refs, "refs", i32, (pages,), dev), _typed(refs_out, "refs_out", i32, (pages,), dev), *_scratch(workspace, dev),
+        signals.handle.value), st)
+    if code:
+        _check(code)
+
+
+def tl_kv_copy_pages(layers: KvLayers, src, dst, signals: Signals, *, slots=None, count=None, stream=None):
+    """In every layer's cache the first slots[i] tokens (None: all) of page src[i] go to page dst[i], i below count [1]
+    (None: all of src [n]; all int32; see tilelink.h)."""
+    st, dev = _place(stream)
+    i32 = _torch.int32
+    _held(layers, dev)
+    n, = src.shape
+    code = _kv_copy_pages(_COPY_PAGES.pack(
+        len(layers.caches), n, layers.address, _typed(src, "src", i32, (n,), dev), _typed(dst, "dst", i32, (n,), dev),
+        0 if slots is None else _typed(slots, "slots", i32, (n,), dev),
+        0 if count is None else _typed(count, "count", i32, (1,), dev), signals.handle.value), st)
+    if code:
+        _check(code)
+
+
+def tl_kv_compact(layers: KvLayers, kept, n_kept, cu_seqlens, seq_lens, page_table, seq_lens_out, signals: Signals, *,
+                  stream=None):
+    """Of each sequence's new tokens those that kept [B, max_kept] names, n_kept [B] of them, move together behind the
+    earlier ones, in every layer's cache; seq_lens_out [B] are the lengths then (all int32; see tilelink.h)."""
+    st, dev = _place(stream)
+    i32 = _torch.int32
+    _held(layers, dev)
+    B, max_pages, cu, lens, table = _batch(cu_seqlens, seq_lens, page_table, i32, dev)
+    max_kept = kept.shape[1]
+    code = _kv_compact(_COMPACT.pack(
+        len(layers.caches), B, max_pages, max_kept, layers.address, _typed(kept, "kept", i32, (B, max_kept), dev),
+        _typed(n_kept, "n_kept", i32, (B,), dev), cu, lens, table, _typed(seq_lens_out, "seq_lens_out", i32, (B,), dev),
+        signals.handle.value), st)
     if code:
         _check(code)
 
