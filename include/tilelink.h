@@ -898,6 +898,55 @@ typedef struct tl_kv_compact_args {
 
 tl_status tl_kv_compact(const tl_kv_compact_args* args, void* stream);
 
+/* ---------------------------------------------------------------- beam search's selection
+ * For each of B users with K beams (rows u * K .. u * K + K - 1 of logits): the N best
+ * continuations of all its beams,
+ *   score(k, v) = scores[u, k] + logits[k][v] - lse[k],  lse[k] = log sum_v exp(logits[k][v])
+ * best first, equal ones by beam, then by logit, then by token:
+ *   parents[u, n] = u * K + k (as tl_kv_fork takes them),  tokens[u, n] = v,
+ *   scores_out[u, n] = score(k, v)
+ * Scores are compared in 64 bits (an lse is good to about 2^-20, of logits near one another far better) and
+ * returned in fp32.  Only finite scores count: tokens whose logit is -infinity, beams whose score is not
+ * finite, and beams whose lse is not (all logits -infinity, or one NaN or +infinity) offer
+ * nothing.  A beam whose done is not 0 has ended: its logits are not read, its lse is 0, and it offers one
+ * continuation, token eos at its own score.  Where fewer than N are offered the places
+ * left have parent -1, token -1 and score -infinity.
+ * done_out[u, n] = 1 where the parent had ended, the token is eos, or nothing was
+ * offered.  With history: row u * N + n of history_out = the first `length` entries of the
+ * parent's row, then the token (rows of places left over are not written, nor entries
+ * behind).
+ * One launch; deterministic.
+ */
+typedef struct tl_beam_select_args {
+  int32_t B;                   /* users, 0..16384 (0: nothing to do) */
+  int32_t K;                   /* beams of each, 1..64 */
+  int32_t N;                   /* continuations of each, 1..64 */
+  int32_t V;                   /* tokens, >= 1; K * V < 2^31 */
+  int32_t dtype;               /* of logits: 0 = fp32, 1 = bf16 */
+  int32_t eos;                 /* the token that ends a beam, or -1 */
+  int32_t history_stride;      /* entries of a history row */
+  int32_t length;              /* 0..history_stride-1 */
+  int64_t row_stride;          /* elements from row to row of logits, >= V */
+  const void* logits;          /* device, B * K rows */
+  const float* scores;         /* device float [B, K] */
+  const uint8_t* done;         /* device uint8 [B, K], or NULL: none has ended */
+  int32_t* parents;            /* device int32 [B, N], written */
+  int32_t* tokens;             /* device int32 [B, N], written */
+  float* scores_out;           /* device float [B, N], written; must not overlap scores */
+  uint8_t* done_out;           /* device uint8 [B, N], written; must not overlap done; NULL = none */
+  float* lse;                  /* device float [B, K], written; NULL = none */
+  const int32_t* history;      /* device int32 [B * K, history_stride], or NULL */
+  int32_t* history_out;        /* device int32 [B * N, history_stride], written; must not overlap history */
+  void* workspace;             /* device scratch, 16-byte aligned, zeroed before its first use; left ready for
+                                  the next call, of any sizes, by every call.  Calls sharing it must not run
+                                  concurrently. */
+  size_t workspace_bytes;      /* >= tl_beam_select_workspace_size(B, K, N, V) */
+} tl_beam_select_args;
+
+/* Workspace bytes for the sizes; 0 for invalid ones. */
+size_t tl_beam_select_workspace_size(int B, int K, int N, int V);
+tl_status tl_beam_select(const tl_beam_select_args* args, void* stream);
+
 /* ---------------------------------------------------------------- MoE layer for a few tokens
  * A whole mixture-of-experts layer for the tokens of a decode step: router
  * selection, gated experts, combine.  For token t:

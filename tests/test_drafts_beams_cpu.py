@@ -201,3 +201,50 @@ def test_oracle_compact_by_hand():
     c, s, n = kv_pages.compact(codes, scales, [[1, 3]], [0, 4], [19], np.array([[0, 1]]))  # tokens 15..18: keep 16, 18
     assert n.tolist() == [17] and s.ravel().tolist() == [129, 129]
     assert c[0, 0, 14, 0] == 0x28 and c[0, 0, 15, 0] == 0x48 and c[1, 0, 0, 0] == 0x50  # 1/4 of 2^2; 4; 8
+
+
+# ------------------------------------------------------------------ beam selection
+def beam_args(L, **kw):
+    a = dict(B=2, K=4, N=8, V=1000, dtype=0, eos=-1, history_stride=0, length=0, row_stride=1000, logits=4, scores=4096, done=None,
+             parents=4, tokens=4, scores_out=8192, done_out=None, lse=None, history=None, history_out=None, workspace=256,
+             workspace_bytes=1 << 24)
+    a.update(kw)
+    return L.tl_beam_select_args(**a)
+
+
+HIST = dict(history=1 << 20, history_out=1 << 22, history_stride=10)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=-1), 1), (dict(B=20000), 4), (dict(K=0), 1), (dict(K=65), 4), (dict(N=0), 1), (dict(N=65), 4), (dict(V=0), 1),
+    (dict(V=1 << 30, row_stride=1 << 30), 4), (dict(dtype=2), 1), (dict(row_stride=999), 1), (dict(eos=1000), 1), (dict(eos=-2), 1),
+    (dict(done=1 << 16), 1), (dict(logits=None), 1), (dict(scores=None), 1), (dict(parents=None), 1), (dict(tokens=None), 1),
+    (dict(scores_out=None), 1), (dict(workspace=None), 1), (dict(logits=6), 1), (dict(logits=5, dtype=1), 1),
+    (dict(workspace=264), 1), (dict(workspace_bytes=1000), 1), (dict(scores_out=4096), 1), (dict(scores_out=4096 - 4), 1),
+    (dict(done=1 << 16, done_out=(1 << 16) + 4, eos=1), 1), (dict(history=1 << 20), 1), (dict(HIST, length=10), 1),
+    (dict(HIST, length=-1), 1), (dict(HIST, history_out=(1 << 20) + 40), 1)])
+def test_beam_select_refuses(B, kw, code):
+    assert B.lib.tl_beam_select(ctypes.byref(beam_args(B, **kw)), None) == code, kw
+    assert "tl_beam_select" in B.tl_last_error()
+
+
+def test_beam_select_null_sizes_and_nothing_to_do(B):
+    assert B.lib.tl_beam_select(None, None) == 1
+    assert B.lib.tl_beam_select(ctypes.byref(beam_args(B, B=0, logits=None, workspace=None)), None) == 0
+    check_packed(B._BEAM, B.tl_beam_select_args)
+    size = B.tl_beam_select_workspace_size
+    assert 0 < size(1, 1, 1, 1) < size(64, 8, 16, 50001) < size(64, 8, 64, 50001)
+    assert not any(size(*a) for a in ((0, 1, 1, 1), (20000, 1, 1, 1), (1, 65, 1, 1), (1, 1, 65, 1), (1, 1, 1, 0), (1, 64, 1, 1 << 26)))
+
+
+def test_oracle_beams_by_hand():
+    import numpy as np
+    from oracle import beam
+    x = np.log(np.array([[[0.5, 0.25, 0.25], [0.1, 0.8, 0.1]], [[1.0, 1.0, 1.0], [np.nan, 1.0, 1.0]]]))
+    total, lse = beam.totals(x, np.array([[0.0, -1.0], [0.0, 5.0]]), None, -1)
+    assert np.allclose(lse[0], 0) and np.isclose(lse[1, 0], np.log(3)) and np.isnan(lse[1, 1])
+    best = beam.select(total, 4)
+    assert [b[:2] for b in best[0]] == [(0, 0), (1, 1), (0, 1), (0, 2)] and np.isclose(best[0][1][2], np.log(0.8) - 1)
+    assert [b[:2] for b in best[1]] == [(0, 0), (0, 1), (0, 2), (-1, -1)]
+    total, lse = beam.totals(x[:1], np.array([[-0.5, -1.0]]), np.array([[1, 0]]), 2)
+    assert [b[:2] for b in beam.select(total, 2)[0]] == [(0, 2), (1, 1)] and lse[0, 0] == 0

@@ -40,7 +40,7 @@ EXPORTED = [
     "tl_test_hold_chunks",
     "tl_kv_append", "tl_kv_append_norm", "tl_kv_attn_workspace_size", "tl_kv_attn", "tl_kv_tree_attn",
     "tl_kv_fork_workspace_size", "tl_kv_fork", "tl_kv_resize_workspace_size", "tl_kv_resize", "tl_kv_copy_pages", "tl_kv_compact",
-    "tl_moe_decode_workspace_size", "tl_moe_decode",
+    "tl_beam_select_workspace_size", "tl_beam_select", "tl_moe_decode_workspace_size", "tl_moe_decode",
 ]
 
 
@@ -208,6 +208,13 @@ class tl_kv_compact_args(ctypes.Structure):
         (n, _vp) for n in ("caches", "kept", "n_kept", "cu_seqlens", "seq_lens", "page_table", "seq_lens_out", "signals")]
 
 
+class tl_beam_select_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "K", "N", "V", "dtype", "eos", "history_stride", "length")] + [
+        ("row_stride", ctypes.c_int64)] + [
+        (n, _vp) for n in ("logits", "scores", "done", "parents", "tokens", "scores_out", "done_out", "lse", "history",
+                           "history_out", "workspace")] + [("workspace_bytes", ctypes.c_size_t)]
+
+
 class tl_moe_decode_args(ctypes.Structure):
     _fields_ = [
         ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("Hd", ctypes.c_int32),
@@ -268,6 +275,8 @@ _decl("tl_kv_resize_workspace_size", _sz, _i)
 _decl("tl_kv_resize", _i, ctypes.POINTER(tl_kv_resize_args), _vp)
 _decl("tl_kv_copy_pages", _i, ctypes.POINTER(tl_kv_copy_pages_args), _vp)
 _decl("tl_kv_compact", _i, ctypes.POINTER(tl_kv_compact_args), _vp)
+_decl("tl_beam_select_workspace_size", _sz, _i, _i, _i, _i)
+_decl("tl_beam_select", _i, ctypes.POINTER(tl_beam_select_args), _vp)
 _decl("tl_moe_decode_workspace_size", _sz, _i, _i, _i, _i, _i, _i)
 _decl("tl_moe_decode", _i, ctypes.POINTER(tl_moe_decode_args), _vp)
 
@@ -602,12 +611,13 @@ _FORK = struct.Struct("@6i10PNP")
 _RESIZE = struct.Struct("@4i6PNP")
 _COPY_PAGES = struct.Struct("@2i6P")
 _COMPACT = struct.Struct("@4i8P")
+_BEAM = struct.Struct("@8iq11PN")
 _MOE = struct.Struct("@8i8PN")
 assert _APPEND.size == ctypes.sizeof(tl_kv_append_args) and \
     _APPEND_NORM.size == ctypes.sizeof(tl_kv_append_norm_args) and _TREE.size == ctypes.sizeof(tl_kv_tree_attn_args) and _ATTN.size == ctypes.sizeof(tl_kv_attn_args) and \
     _MOE.size == ctypes.sizeof(tl_moe_decode_args) and _FORK.size == ctypes.sizeof(tl_kv_fork_args) and \
     _RESIZE.size == ctypes.sizeof(tl_kv_resize_args) and _COPY_PAGES.size == ctypes.sizeof(tl_kv_copy_pages_args) and \
-    _COMPACT.size == ctypes.sizeof(tl_kv_compact_args)
+    _COMPACT.size == ctypes.sizeof(tl_kv_compact_args) and _BEAM.size == ctypes.sizeof(tl_beam_select_args)
 
 
 def _packed(name):
@@ -620,7 +630,7 @@ def _packed(name):
 _kv_append, _kv_attn, _moe_decode = _packed("tl_kv_append"), _packed("tl_kv_attn"), _packed("tl_moe_decode")
 _kv_append_norm, _kv_tree_attn = _packed("tl_kv_append_norm"), _packed("tl_kv_tree_attn")
 _kv_fork, _kv_resize = _packed("tl_kv_fork"), _packed("tl_kv_resize")
-_kv_copy_pages, _kv_compact = _packed("tl_kv_copy_pages"), _packed("tl_kv_compact")
+_kv_copy_pages, _kv_compact, _beam_select = _packed("tl_kv_copy_pages"), _packed("tl_kv_compact"), _packed("tl_beam_select")
 _torch = None
 
 
@@ -884,6 +894,40 @@ def tl_kv_compact(layers: KvLayers, kept, n_kept, cu_seqlens, seq_lens, page_tab
         len(layers.caches), B, max_pages, max_kept, layers.address, _typed(kept, "kept", i32, (B, max_kept), dev),
         _typed(n_kept, "n_kept", i32, (B,), dev), cu, lens, table, _typed(seq_lens_out, "seq_lens_out", i32, (B,), dev),
         signals.handle.value), st)
+    if code:
+        _check(code)
+
+
+def tl_beam_select_workspace_size(B, K, N, V):
+    return int(lib.tl_beam_select_workspace_size(B, K, N, V))
+
+
+def tl_beam_select(logits, scores, parents, tokens, scores_out, workspace, *, done=None, done_out=None, eos=-1, lse=None,
+                   history=None, history_out=None, length=0, stream=None):
+    """The N best continuations of each user's K beams: logits [B * K, V] (float or bf16, rows any distance apart), scores
+    [B, K]; parents (rows of logits), tokens (int32) and scores_out [B, N] written (see tilelink.h)."""
+    st, dev = _place(stream)
+    i32, f32, u8 = _torch.int32, _torch.float32, _torch.uint8
+    (B, K), N, (rows, V) = scores.shape, parents.shape[1], logits.shape
+    half = logits.dtype is _torch.bfloat16
+    if rows != B * K or logits.get_device() != dev or not (half or logits.dtype is f32):
+        _mistyped(logits, "logits", "float32 or bfloat16", (B * K, V), dev)
+    stride = logits.stride(0) if rows > 1 else V
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: a row's elements must lie next to one another")
+    hist = hist_out = width = 0
+    if history is not None or history_out is not None:
+        if history is None or history_out is None:
+            raise ValueError("history and history_out go together")
+        width = history.shape[1]
+        hist = _typed(history, "history", i32, (B * K, width), dev)
+        hist_out = _typed(history_out, "history_out", i32, (B * N, width), dev)
+    code = _beam_select(_BEAM.pack(
+        B, K, N, V, half, eos, width, length, stride, logits.data_ptr(), _typed(scores, "scores", f32, (B, K), dev),
+        0 if done is None else _typed(done, "done", u8, (B, K), dev), _typed(parents, "parents", i32, (B, N), dev),
+        _typed(tokens, "tokens", i32, (B, N), dev), _typed(scores_out, "scores_out", f32, (B, N), dev),
+        0 if done_out is None else _typed(done_out, "done_out", u8, (B, N), dev),
+        0 if lse is None else _typed(lse, "lse", f32, (B, K), dev), hist, hist_out, *_scratch(workspace, dev)), st)
     if code:
         _check(code)
 
