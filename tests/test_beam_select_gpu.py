@@ -45,13 +45,16 @@ class Case:
     def check(self):
         x, scores = f64(self.logits), self.scores.astype(np.float32).astype(np.float64)
         total, lse = ora.totals(x, scores, self.done, self.eos)
-        # A logit's distance d from the maximum is rounded to 2^-24 of it, and so is its product with log2 e, itself off by
-        # as much: 3 d 2^-24 in the exponent at most.  The exponential adds 2^-22 of its result, the sum of up to 8 in a chain and
-        # two more 2^-24 each (pairs and 64 bits from there on).  lse is off by the mean of that over the softmax.
+        # A logit's distance from its thread's reference, and the reference's from the maximum, d + 2 together (d the logit's
+        # distance from the maximum; references lie up to 1 below a maximum), are rounded to 2^-24 of them, and so are their
+        # products with log2 e, itself off by as much: 3 (d + 2) 2^-24 in the exponent.  Exponentials are off by 2^-22 of
+        # their result: a logit's, the reference's, and those of references that were raised (what came before is e times
+        # less each time): 4 of them at most.  Sums: four in a chain and two more, 2^-24 each (pairs and 64 bits from there
+        # on), and as much for the products.  lse is off by the mean of that over the softmax.
         with np.errstate(all="ignore"):
             w = np.exp(x - lse[..., None])
             d = np.where(w > 0, x.max(2, keepdims=True) - x, 0.0)
-            tol = np.nan_to_num((w * d).sum(2) * 3 * 2.0 ** -24 + 2.0 ** -22 + 12 * 2.0 ** -24, nan=0.0, posinf=0.0, neginf=0.0)
+            tol = np.nan_to_num((w * (d + 2)).sum(2) * 3 * 2.0 ** -24 + 4 * 2.0 ** -22 + 12 * 2.0 ** -24, nan=0.0, posinf=0.0, neginf=0.0)
         got_lse = f64(self.lse)
         same = np.isclose(got_lse, lse, rtol=0, atol=0, equal_nan=True) & ~np.isfinite(lse)
         fine = np.isfinite(lse)
@@ -122,6 +125,11 @@ def test_many_beams_and_users(B, K, N, users):
     Case(B, normal(K, users, K, 600), some_scores(N, users, K), N).run().check()
 
 
+@pytest.mark.parametrize("half", [False, True])
+def test_many_rows_of_many_steps(B, half):
+    Case(B, normal(12, 80, 8, 9001, half=half), some_scores(12, 80, 8), 16).run().check()
+
+
 def test_a_large_vocabulary(B):
     Case(B, normal(1, 2, 5, 300007, half=True), some_scores(1, 2, 5), 10).run().check()
 
@@ -163,6 +171,28 @@ def test_more_equal_scores_than_the_list_holds(B, N):
         assert c.parents[b].tolist() == [64 * b] * N and c.tokens[b].tolist() == list(range(N))
     near = torch.ones(1, 64, 40000) + torch.arange(40000) * 2.0 ** -23  # (in steps of fp32's grain: far below 64-bit scores' upper halves)
     Case(B, near, np.full((1, 64), -3.0), N).run().check()
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_plateaus_in_long_rows(B, half):
+    """Rows of many steps to a block: more values above the bound than there is room for, and a value shared by many."""
+    users, K, V = 160, 4, 70001
+    x = torch.zeros(1, K, V)
+    x[0, 0, ::3] = 2.0                      # a third of the row is the maximum
+    x[0, 1] = torch.arange(V) % 4096 / 64   # rises again and again
+    x[0, 2, ::256] = 5.0                    # one thread's
+    x[0, 2, 1::256] = torch.arange(len(x[0, 2, 1::256])) / 128.0
+    x[0, 3, 60000:] = 1.0
+    x = x.to(torch.bfloat16) if half else x
+    c = Case(B, x.expand(users, K, V), np.tile(some_scores(11, 1, K) / 10, (users, 1)), 24)
+    c.run()
+    for out in (c.parents - torch.arange(users, device="cuda", dtype=torch.int32)[:, None] * K, c.tokens, c.out, c.lse):
+        assert (out == out[:1]).all()
+    one = Case(B, x, c.scores[:1], 24)
+    one.run().check()
+    c.logits, c.scores, c.B = c.logits[:1], c.scores[:1], 1
+    c.parents, c.tokens, c.out, c.lse, c.done_out = (t[:1] for t in (c.parents, c.tokens, c.out, c.lse, c.done_out))
+    c.check()
 
 
 @pytest.mark.parametrize("half", [False, True])
