@@ -905,8 +905,8 @@ tl_status tl_kv_compact(const tl_kv_compact_args* args, void* stream);
  * best first, equal ones by beam, then by logit, then by token:
  *   parents[u, n] = u * K + k (as tl_kv_fork takes them),  tokens[u, n] = v,
  *   scores_out[u, n] = score(k, v)
- * Scores are compared in 64 bits (an lse is good to about 2^-20, of logits near one another far better) and
- * returned in fp32.  Only finite scores count: tokens whose logit is -infinity, beams whose score is not
+ * Scores are compared in pairs of fp32 (48 bits; the sum of exponentials is good to
+ * 2^-19 at worst, where they are many to about 2^-26) and returned in fp32.  Only finite scores count: tokens whose logit is -infinity, beams whose score is not
  * finite, and beams whose lse is not (all logits -infinity, or one NaN or +infinity) offer
  * nothing.  A beam whose done is not 0 has ended: its logits are not read, its lse is 0, and it offers one
  * continuation, token eos at its own score.  Where fewer than N are offered the places

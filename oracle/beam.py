@@ -11,10 +11,11 @@ def totals(logits, scores, done, eos):
     with np.errstate(all="ignore"):
         m = x.max(2, keepdims=True)
         finite = np.isfinite(m)
-        s = np.exp(x - np.where(finite, m, 0.0)).sum(2)
-        lse = m[..., 0] + np.log(s)
+        s = np.log(np.exp(x - np.where(finite, m, 0.0)).sum(2))
+        lse = m[..., 0] + s
         lse = np.where(np.isnan(x).any(2), np.nan, np.where(np.isposinf(m[..., 0]), np.inf, lse))
-        total = scores[..., None] + (x - lse[..., None])
+        # x - lse as (x - m) - log s: m + log s has no room for log s where m is the lowest float
+        total = scores[..., None] + ((x - m) - s[..., None])
     total = np.where(np.isfinite(lse)[..., None] & np.isfinite(total), total, -np.inf)
     if done is not None:
         ended = np.asarray(done) != 0

@@ -2,23 +2,22 @@
 //
 //   score(k, v) = scores[k] + logits[k][v] - lse[k],   lse[k] = log sum_v exp(logits[k][v])
 //
-// equal scores by beam, then by logit (which 64 bits may not tell apart beside a large score), then by token.
+// equal scores by beam, then by logit (which scores may not tell apart beside a large sum), then by token.
 //
-// The logits are read once.  A row is cut into as many parts as fill the GPU with blocks; a block leaves its part's
-// maximum, its sum of exponentials and its N largest values, and the block of a user that ends
-// last joins the K rows.  (Within a row scores and logits rise together, so the N best of a
-// user are among the rows' N largest, ties included.)
+// The logits are read once, as a stream: a row is cut into as many parts as fill the GPU with
+// blocks, a thread takes 16 logits at a time, and what a block leaves is its part's sum of
+// exponentials and the maximum of each group of up to 256 logits that four neighbouring threads took.  The block of a
+// user that ends last joins the K rows: the groups' maxima are scores themselves, so any bound
+// that N of them reach is at or below the N-th best score.  A bound that few groups reach is found
+// from the threads' best ones (256 bins between the least and the largest, then bisection by the
+// block's votes), those groups are read again, and what reaches the bound goes to a list in shared
+// memory, in which each candidate counts those before it.  (With the selection in each part
+// instead, 512 beams of 50001 took 31 us: a block's list cost it as much time as its logits.)
+// Where more reach the bound than the list holds (plateaus), rows are taken apart value by value.
 //
-// The N largest of a part: any bound that N threads' own maxima reach is at or below the N-th
-// largest value, and one that at most 2 N reach leaves few values to look at.  It is found
-// by bisection, a vote of the block at each step.  Each thread has kept the maximum of each of its
-// 16 values that it took at once; the few whose maximum reaches the bound are read again, and
-// what reaches it goes to a list in shared memory, in which each value counts those before it.
-// Where the bisection ends at a value that too many share, the values above it go to the list
-// and the places left are filled with that value's lowest tokens.
-//
-// Beams are compared by 64-bit scores: the sums of exponentials are kept in pairs of fp32 and
-// 64 bits, so that what decides between two beams is not lost beside scores of -20.
+// Beams are compared by scores in pairs of fp32 (48 bits), and sums of exponentials are pairs too, so that
+// what decides between two beams is not lost beside scores of -20.  (64-bit arithmetic took 5000 of the
+// joining block's cycles: a warp's instruction holds its unit for 16.)
 //
 // Bound by memory for many beams and by latency for few.
 #include <algorithm>
@@ -31,13 +30,16 @@ namespace tl {
 namespace {
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
-constexpr int UNIT = 16;              // values that a thread takes at once
+constexpr int UNIT = 16;              // logits that a thread takes at once
 constexpr int STEP = THREADS * UNIT;  // and a block
+constexpr int GROUP = 4;              // steps of four neighbouring threads whose maximum is kept
+constexpr int LINE = THREADS / 4;     // maxima of a block's four steps
 constexpr int MOST_STEPS = 16;        // of a block, at least one
-constexpr int BLOCKS = 608;           // that fill the GPU: four to an SM
-constexpr int HITS = 1024;            // units that are looked at again, at most
-constexpr float kSlack = 1.0f;        // by how much logits may pass a thread's reference: what came before a new one is e times less
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int BLOCKS = 304;           // wanted: two to an SM at least, all at once (four fit)
+constexpr int HITS = 512;             // groups that are looked at again, at most
+constexpr int AHEAD = 8;              // groups of a thread that stay in registers
+constexpr float kFar = 32768.0f;      // references of sums are whole powers of two up to 2^kFar
+constexpr float kLog2e = 1.4426950216f, kLog2eLow = 1.9259629e-08f;
 constexpr int MAX_BEAMS = 64, MAX_N = 64, MAX_B = 16384;
 constexpr int NONE = int(0x80000000);
 
@@ -54,17 +56,12 @@ struct BeamParams {
   const int32_t* history;
   int32_t* history_out;
   uint32_t* counters;  // [B], zero between calls
-  uint8_t* parts;      // [B K splits] parts of part_bytes
-  int32_t B, K, N, V, eos, splits, part_bytes;
-  int32_t steps, list;  // of a block at most; places of the list in shared memory
+  float4* heads;       // [B K splits] of a part: reference (-infinity, infinity: of nothing but that) and sum of exp(x - reference)
+  float* maxima;       // [B K splits][lines][LINE]
+  int32_t B, K, N, V, eos, splits, lines;  // lines: of a part
+  int32_t per;         // vectors of a part
+  int32_t list;                                         // places of the list in shared memory
   int32_t history_stride, length;
-};
-
-// What a block leaves of its part of a row: this, then N values and their tokens, the largest first.
-struct PartHead {
-  float most;
-  float pad;
-  double sum;  // of exp(x - most)
 };
 
 // Floats as whole numbers in the same order (-0 is brought to 0 before).
@@ -73,27 +70,111 @@ __device__ __forceinline__ int ordered(float x) {
   return b ^ ((b >> 31) & 0x7FFFFFFF);
 }
 __device__ __forceinline__ float unordered(int o) { return __int_as_float(o ^ ((o >> 31) & 0x7FFFFFFF)); }
-__device__ __forceinline__ int64_t ordered(double x) {
-  const int64_t b = __double_as_longlong(x + 0.0);
-  return b ^ ((b >> 63) & 0x7FFFFFFFFFFFFFFFll);
+
+// ---------------------------------------------------------------- pairs: x + y, y below half a step of x
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+  const float sum = __fadd_rn(a, b), back = __fsub_rn(sum, a);
+  return make_float2(sum, __fadd_rn(__fsub_rn(a, __fsub_rn(sum, back)), __fsub_rn(b, back)));
+}
+__device__ __forceinline__ float2 normal(float hi, float lo) {  // |hi| >= |lo|, or nearly
+  const float sum = __fadd_rn(hi, lo);
+  return make_float2(sum, __fsub_rn(lo, __fsub_rn(sum, hi)));
+}
+__device__ __forceinline__ float2 operator+(float2 a, float2 b) {
+  const float2 s = two_sum(a.x, b.x);
+  return normal(s.x, s.y + (a.y + b.y));
+}
+__device__ __forceinline__ float2 operator*(float2 a, float2 b) {
+  const float p = __fmul_rn(a.x, b.x);
+  return normal(p, fmaf(a.x, b.y, fmaf(a.y, b.x, __fmaf_rn(a.x, b.x, -p))));
+}
+// exp(a - b) for a <= b, to about 2^-25: 2^n (1 + u), u the series of exp(f ln 2) - 1 for |f| <= 1/2.
+__device__ __noinline__ float2 exp_below(float2 a, float2 b) {
+  if (!(a.x - b.x > -80.0f)) return make_float2(0.0f, 0.0f);  // (infinities, too)
+  const float2 d = a + make_float2(-b.x, -b.y);
+  const float t = __fmul_rn(d.x, kLog2e);
+  const float rest = fmaf(d.x, kLog2eLow, fmaf(d.y, kLog2e, __fmaf_rn(d.x, kLog2e, -t)));
+  const float n = rintf(t), y = ((t - n) + rest) * 0.69314718056f;
+  float u = 1.0f / 362880;
+  u = fmaf(u, y, 1.0f / 40320);
+  u = fmaf(u, y, 1.0f / 5040);
+  u = fmaf(u, y, 1.0f / 720);
+  u = fmaf(u, y, 1.0f / 120);
+  u = fmaf(u, y, 1.0f / 24);
+  u = fmaf(u, y, 1.0f / 6);
+  u = fmaf(u, y, 0.5f);
+  const float2 r = two_sum(1.0f, fmaf(u * y, y, y));
+  const float scale = __int_as_float((int(n) + 127) << 23);  // n >= -116
+  return make_float2(r.x * scale, r.y * scale);
+}
+// log(s) for s > 0, finite: s = 2^e f, sqrt(1/2) <= f <= sqrt(2), and log f = 2 atanh(z), z = (f - 1) / (f + 1), by its series.
+__device__ __forceinline__ float2 log_of(float2 s) {
+  int e = int(__float_as_uint(s.x) >> 23) - 127;
+  float scale = __int_as_float((127 - e) << 23);
+  if (s.x * scale > 1.4142135f) {
+    ++e;
+    scale *= 0.5f;
+  }
+  const float f = s.x * scale, low = s.y * scale, up = f - 1.0f;
+  const float2 den = two_sum(f, 1.0f);
+  const float z = __fdividef(up, den.x);  // (what it is off by goes to z1)
+  const float z1 = __fdividef(__fmaf_rn(-z, den.x, up) + (low - z * (den.y + low)), den.x);
+  const float w = z * z;
+  float p = 2.0f / 13;
+  p = fmaf(p, w, 2.0f / 11);
+  p = fmaf(p, w, 2.0f / 9);
+  p = fmaf(p, w, 2.0f / 7);
+  p = fmaf(p, w, 2.0f / 5);
+  p = fmaf(p, w, 2.0f / 3);
+  // ln 2 in two parts, the first of 14 bits: exact times e
+  return two_sum(float(e) * 0x1.62ep-1f, 2.0f * z) + make_float2(fmaf(float(e), 3.194618e-05f, fmaf(p * w, z, 2.0f * z1)), 0.0f);
+}
+// Pairs as whole numbers in the same order.
+__device__ __forceinline__ int64_t ordered(float2 x) {
+  return int64_t(ordered(x.x + 0.0f)) << 32 | (uint32_t(ordered(x.y + 0.0f)) ^ 0x80000000u);
 }
 
+// Two at a time: (x, y) = (a, b) f + c; (x, y) += (a, b).
+__device__ __forceinline__ void fma2(float a, float b, float f, float c, float& x, float& y) {
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmov.b64 r, {%5, %5};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(f), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 2^d for whole d <= 0
+__device__ __forceinline__ float pow2_below(float d) { return d < -126.0f ? 0.0f : __int_as_float((int(d) + 127) << 23); }
+
 struct Smem {
-  float warp_f[WARPS];
   int warp_lo[WARPS], warp_hi[WARPS];
   float2 warp_sum[WARPS];
-  uint64_t warp_best[WARPS];
+  float warp_most[WARPS];
   int count, hits, last;
-  double lse[MAX_BEAMS];    // by the joining block: infinity for a row that offers nothing, -infinity for an ended beam
-  double score[MAX_BEAMS];  // its beam's
-  int64_t best_key[WARPS];
-  uint64_t best_tie[WARPS];
-  uint32_t best_token[WARPS];
-  int winner[MAX_N];  // its beam, or -1
+  int bins[THREADS];
+  float2 lse[MAX_BEAMS];   // by the joining block: infinity for a row that offers nothing, -infinity for an ended beam
+  float score[MAX_BEAMS];  // its beam's
+  float bias[MAX_BEAMS];   // score - lse in fp32, -infinity for rows that offer nothing
+  float next[MAX_BEAMS];   // row by row: the largest logit not taken yet
+  int winner[MAX_N];       // its beam, or -1
 };
 
 // A bound on the threads' keys (NONE: a thread without) that at least n of them reach; and at most 2 n of them, unless
-// exact: then fewer than n lie above it.  NONE + 1 where fewer than n threads have one.
+// exact: then fewer than n lie above it.  NONE + 1 where fewer than n threads have one.  sm.bins is 0 before.
 __device__ __forceinline__ int bound(Smem& sm, int key, int n, bool& exact) {
   exact = false;
   int lo = __reduce_min_sync(0xffffffffu, key == NONE ? 0x7FFFFFFF : key), hi = __reduce_max_sync(0xffffffffu, key);
@@ -109,9 +190,37 @@ __device__ __forceinline__ int bound(Smem& sm, int key, int n, bool& exact) {
   }
   if (have < n) return NONE + 1;
   if (have <= 2 * n) return lo;
+  // 256 bins between the least and the largest; the highest ones that hold n, found by every warp
+  const int shift = max(0, 24 - __clz(int(uint32_t(hi) - uint32_t(lo))));
+  if (key != NONE) atomicAdd(&sm.bins[(uint32_t(key) - uint32_t(lo)) >> shift], 1);
+  __syncthreads();
+  int mine[THREADS / 32], sum = 0;
+  const int top = THREADS - 1 - int(lane_id()) * (THREADS / 32);  // a lane's bins, from its highest down
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) sum += mine[i] = sm.bins[top - i];
+  int before = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, before, d);
+    if (int(lane_id()) >= d) before += x;
+  }
+  const int lane = __ffs(__ballot_sync(0xffffffffu, before >= n)) - 1;
+  before -= sum;
+  int bin = -1;
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) {
+    if (bin < 0) {
+      before += mine[i];
+      if (before >= n) bin = top - i;
+    }
+  }
+  bin = __shfl_sync(0xffffffffu, bin, lane);
+  have = __shfl_sync(0xffffffffu, before, lane);
+  lo += int(uint32_t(bin) << shift);
+  if (have <= 2 * n) return lo;
+  hi = min(hi, lo + int((1u << shift) - 1u));
   while (lo < hi) {
-    const uint32_t d = uint32_t(hi) - uint32_t(lo);
-    const int mid = lo + int((d >> 1) + (d & 1u));
+    const int mid = lo + int((uint32_t(hi) - uint32_t(lo) + 1u) >> 1);
     have = __syncthreads_count(key >= mid);
     if (have >= n) {
       lo = mid;
@@ -178,354 +287,501 @@ struct Row {
   __device__ __forceinline__ int token(int v, int c) const { return v * W - skew + c; }
   __device__ __forceinline__ uint4 load(int v, bool in) const {
     const int e = v * W - skew;
-    if (in && e >= 0 && e + W <= V) return Vec<T>::load(first + e);
+    uint4 r;
+    if (in && e >= 0 && e + W <= V) {
+      r = Vec<T>::load(first + e);
+    } else if (in && e < V) {
+      r = edge(first, e, V);
+    } else {
+#pragma unroll
+      for (int c = 0; c < W; ++c) Vec<T>::set(r, c, -INFINITY);
+    }
+    return r;
+  }
+  // Code that runs once a launch costs more to fetch than to run: what is rare is kept out of line.
+  static __device__ __noinline__ uint4 edge(const T* first, int e, int V) {
     uint4 r;
 #pragma unroll
-    for (int c = 0; c < W; ++c) Vec<T>::set(r, c, in && e + c >= 0 && e + c < V ? Vec<T>::one(first + e + c) : -INFINITY);
+    for (int c = 0; c < W; ++c) Vec<T>::set(r, c, e + c >= 0 && e + c < V ? Vec<T>::one(first + e + c) : -INFINITY);
     return r;
   }
 };
 
-// Larger values first, then lower tokens, as one number; 0 is below all.
-__device__ __forceinline__ uint64_t value_key(float x, int token) {
-  return uint64_t(uint32_t(ordered(x + 0.0f)) ^ 0x80000000u) << 32 | uint32_t(~token);
-}
-__device__ __forceinline__ float2 value_of(uint64_t key) {
-  return make_float2(unordered(int(uint32_t(key >> 32) ^ 0x80000000u)), __int_as_float(int(~uint32_t(key))));
-}
-
-// The N largest one after the other, by reading the part N times: where more reach the bound than there is room for.
+// The UNIT values of a thread at one step.
 template <typename T>
-__device__ __noinline__ void take_one_by_one(const BeamParams& p, Smem& sm, int row, int v0, int v1, float2* out) {
-  const Row<T> r(p, row);
-  constexpr int W = Row<T>::W;
-  uint64_t last = ~0ull;
-  for (int i = 0; i < p.N; ++i) {
-    uint64_t best = 0;
-    if (last) {
-      for (int v = v0 + int(threadIdx.x); v < v1; v += THREADS) {
-        float x[W];
-        Vec<T>::unpack(r.load(v, true), x);
+__device__ __forceinline__ void load_unit(const Row<T>& r, int v, int v1, uint4 (&x)[UNIT / Vec<T>::W]) {
+  constexpr int W = Vec<T>::W, VECS = UNIT / W;
+  if (v * W >= r.skew && v + (VECS - 1) * THREADS < v1 && (v + (VECS - 1) * THREADS + 1) * W - r.skew <= r.V) {
+    const T* at = r.first + (v * W - r.skew);
 #pragma unroll
-        for (int c = 0; c < W; ++c) {
-          const uint64_t key = value_key(x[c], r.token(v, c));
-          if (x[c] > -INFINITY && key < last && key > best) best = key;
-        }
-      }
-    }
+    for (int i = 0; i < VECS; ++i) x[i] = Vec<T>::load(at + i * THREADS * W);
+  } else {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) best = max(best, uint64_t(__shfl_xor_sync(0xffffffffu, best, d)));
-    __syncthreads();
-    if (lane_id() == 0) sm.warp_best[warp_id()] = best;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) best = max(best, sm.warp_best[w]);
-    if (threadIdx.x == 0) __stcg(out + i, best ? value_of(best) : make_float2(-INFINITY, 0.0f));
-    last = best;
+    for (int i = 0; i < VECS; ++i) x[i] = r.load(v + i * THREADS, v + i * THREADS < v1);
   }
 }
 
-// One block's part of a row: its sum and its N largest to `part`.
+// The block's sum again, relative to the maximum itself: for logits whose powers of two fp32 does not tell apart, and for
+// infinities (1 for each; what is NaN stays).
 template <typename T>
-__device__ __forceinline__ void take_part(const BeamParams& p, Smem& sm, uint64_t* list, int row, int split, uint8_t* part) {
+__device__ __noinline__ void far_sum(const BeamParams& p, Smem& sm, int row, int v0, int v1, float most) {
+  const Row<T> r(p, row);
+  constexpr int W = Row<T>::W;
+  float2 sum = make_float2(0.0f, 0.0f);
+  for (int v = v0 + int(threadIdx.x); v < v1; v += THREADS) {
+    float x[W];
+    Vec<T>::unpack(r.load(v, true), x);
+#pragma unroll
+    for (int c = 0; c < W; ++c) {
+      const float e = x[c] == most ? 1.0f : x[c] == x[c] ? ex2_approx((x[c] - most) * kLog2e) : x[c];
+      sum = sum + make_float2(most == -INFINITY && x[c] == x[c] ? 0.0f : e, 0.0f);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+    sum = sum + make_float2(__shfl_xor_sync(0xffffffffu, sum.x, d), __shfl_xor_sync(0xffffffffu, sum.y, d));
+  __syncthreads();
+  if (lane_id() == 0) sm.warp_sum[warp_id()] = sum;
+  __syncthreads();
+}
+
+// Which vectors a part of a row has.
+template <typename T>
+__device__ __forceinline__ int2 part_vectors(const BeamParams& p, const Row<T>& r, int split) {
+  return make_int2(split * p.per, min((p.V + r.skew + Row<T>::W - 1) / Row<T>::W, (split + 1) * p.per));
+}
+
+// One block's part of a row: its sum and its groups' maxima.
+template <typename T>
+__device__ __forceinline__ void take_part(const BeamParams& p, Smem& sm, int row, int split) {
   constexpr int W = Vec<T>::W, VECS = UNIT / W;
   const int tid = threadIdx.x, lane = int(lane_id()), warp = int(warp_id());
-  int* hit = reinterpret_cast<int*>(list + p.list);
-  float* unit_most = reinterpret_cast<float*>(hit + HITS);  // [steps][threads]
   const Row<T> r(p, row);
-  const int vecs = (p.V + r.skew + W - 1) / W, per = (vecs + p.splits - 1) / p.splits;
-  const int v0 = split * per, v1 = min(vecs, v0 + per);
-  const int steps = max(1, (v1 - v0 + THREADS * VECS - 1) / (THREADS * VECS));
-  auto vec = [&](int unit, int i) { return v0 + ((unit / THREADS) * VECS + i) * THREADS + unit % THREADS; };
-
-  // ---------------------------------------------------------------- maxima, and sums of exponentials
-  // A thread's sum is relative to its reference m, which follows its maximum at a distance.
+  const int2 v = part_vectors(p, r, split);
+  const int steps = max(0, v.y - v.x + THREADS * VECS - 1) / (THREADS * VECS);
+  float* out = p.maxima + int64_t(blockIdx.x) * p.lines * LINE + tid / 4;
+  auto put = [&](int line, float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+    if (tid % 4 == 0) __stcg(out + line * LINE, x);
+  };
+  // A thread's sum is relative to 2^c, c a whole number that follows the maximum times log2 e: one fused operation brings
+  // a logit to its exponent, and what changes reference does so exactly.
   uint4 next[VECS];
-  float most = -INFINITY, m = -INFINITY, hi = 0.0f, lo = 0.0f;
-#pragma unroll
-  for (int i = 0; i < VECS; ++i) next[i] = r.load(vec(tid, i), vec(tid, i) < v1);
+  float most = -INFINITY, group = -INFINITY, c = -kFar, hi = 0.0f, lo = 0.0f;
+  load_unit(r, v.x + tid, v.y, next);
   for (int b = 0; b < steps; ++b) {
     float x[UNIT];
 #pragma unroll
     for (int i = 0; i < VECS; ++i) Vec<T>::unpack(next[i], x + i * W);
-    if (b + 1 < steps) {
+    if (b + 1 < steps) load_unit(r, v.x + (b + 1) * THREADS * VECS + tid, v.y, next);
+    float top = max3(x[0], x[1], -INFINITY);  // (a NaN is below everything)
 #pragma unroll
-      for (int i = 0; i < VECS; ++i) next[i] = r.load(vec((b + 1) * THREADS + tid, i), vec((b + 1) * THREADS + tid, i) < v1);
-    }
-    float top = x[0];
-#pragma unroll
-    for (int i = 1; i < UNIT; ++i) top = fmaxf(top, x[i]);
-    if (!(top >= -INFINITY)) top = -INFINITY;  // nothing but NaN
-    unit_most[b * THREADS + tid] = top;
-    most = fmaxf(most, top);
-    if (top > m + kSlack) {
-      const float f = ex2_approx((m - top) * kLog2e);
+    for (int i = 2; i < UNIT; i += 2) top = max3(top, x[i], x[i + 1]);
+    group = fmaxf(group, top);
+    if (top * kLog2e > c + 1.0f) {
+      const float now = fminf(rintf(top * kLog2e), kFar), f = pow2_below(c - now);
       hi *= f;
       lo *= f;
-      m = top;
+      c = now;
     }
-    const float base = m == -INFINITY ? 0.0f : m;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < UNIT; ++i) s[i & 3] += ex2_approx((x[i] - base) * kLog2e);
-    const float add = (s[0] + s[1]) + (s[2] + s[3]), sum = __fadd_rn(hi, add), back = __fsub_rn(sum, hi);
-    lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, back)), __fsub_rn(add, back));
-    hi = sum;
+    for (int i = 0; i < UNIT; i += 2) {
+      float y0, y1;
+      fma2(x[i], x[i + 1], kLog2e, -c, y0, y1);
+      add2(s[i & 2], s[(i & 2) + 1], ex2_ftz(y0), ex2_ftz(y1));
+    }
+    const float2 sum = two_sum(hi, (s[0] + s[1]) + (s[2] + s[3]));
+    hi = sum.x;
+    lo += sum.y;
+    if (b % GROUP == GROUP - 1) {
+      put(b / GROUP, group);
+      most = fmaxf(most, group);
+      group = -INFINITY;
+    }
   }
-  most += 0.0f;
-  bool exact;
-  const int cut = bound(sm, most > -INFINITY ? ordered(most) : NONE, p.N, exact);
-  int top = NONE;
+  for (int g = steps / GROUP; g < p.lines; ++g) {  // (the last part of a row may have fewer)
+    put(g, group);
+    most = fmaxf(most, group);
+    group = -INFINITY;
+  }
+  float block_most = most;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) top = max(top, sm.warp_hi[w]);
-  const float block_most = top == NONE ? -INFINITY : unordered(top);
-  const float least = cut == NONE + 1 ? -3.402823466e38f : unordered(cut);
-  if (tid == 0) sm.count = sm.hits = 0;
+  for (int d = 16; d > 0; d >>= 1) block_most = fmaxf(block_most, __shfl_xor_sync(0xffffffffu, block_most, d));
+  // the warp's sum, relative to a power of two that no thread's is above
+  float warp_c = fminf(fmaxf(rintf(block_most * kLog2e), -kFar), kFar);
+  float2 sum = make_float2(hi, lo);
   {
-    // the block's sum, relative to its maximum
-    const float f = block_most == -INFINITY ? 1.0f : ex2_approx((m - block_most) * kLog2e);
-    hi *= f;
-    lo *= f;
+    const float f = pow2_below(c - warp_c);
+    sum = make_float2(sum.x * f, sum.y * f);
+  }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      const float h2 = __shfl_xor_sync(0xffffffffu, hi, d), l2 = __shfl_xor_sync(0xffffffffu, lo, d);
-      const float sum = __fadd_rn(hi, h2), back = __fsub_rn(sum, hi);
-      lo = (lo + l2) + __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, back)), __fsub_rn(h2, back));
-      hi = sum;
-    }
-    if (lane == 0) sm.warp_sum[warp] = make_float2(hi, lo);
+  for (int d = 16; d > 0; d >>= 1)
+    sum = sum + make_float2(__shfl_xor_sync(0xffffffffu, sum.x, d), __shfl_xor_sync(0xffffffffu, sum.y, d));
+  if (lane == 0) {
+    sm.warp_sum[warp] = sum;
+    sm.warp_most[warp] = block_most;
   }
   __syncthreads();
-
-  // ---------------------------------------------------------------- what reaches the bound
-  if (most > -INFINITY && (exact ? most > least : most >= least)) {
-    for (int b = 0; b < steps; ++b) {
-      const float u = unit_most[b * THREADS + tid];
-      if (exact ? u > least : u >= least) {
-        const int at = atomicAdd(&sm.hits, 1);
-        if (at < HITS) hit[at] = b * THREADS + tid;
-      }
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) block_most = fmaxf(block_most, sm.warp_most[w]);
+  const bool far = fabsf(block_most) > kFar / 2;  // (no logit above -infinity, too)
+  if (far) far_sum<T>(p, sm, row, v.x, v.y, block_most);
+  if (warp == 0) {
+    const float block_c = rintf(block_most * kLog2e);
+    sum = sm.warp_sum[lane % WARPS];
+    if (!far) {
+      warp_c = fminf(fmaxf(rintf(sm.warp_most[lane % WARPS] * kLog2e), -kFar), kFar);
+      const float f = pow2_below(warp_c - block_c);
+      sum = make_float2(sum.x * f, sum.y * f);
     }
-  }
-  __syncthreads();
-  const int hits = sm.hits;
-  float2* out = reinterpret_cast<float2*>(part + sizeof(PartHead));
-  bool many = hits > HITS;
-  if (!many) {
-    for (int h = tid; h < hits * VECS; h += THREADS) {
-      const int v = vec(hit[h / VECS], h % VECS);
-      float x[W];
-      Vec<T>::unpack(r.load(v, v < v1), x);
 #pragma unroll
-      for (int c = 0; c < W; ++c)
-        if (x[c] > -INFINITY && (exact ? x[c] > least : x[c] >= least)) {
-          const int at = atomicAdd(&sm.count, 1);
-          if (at < p.list) list[at] = value_key(x[c], r.token(v, c));
-        }
+    for (int d = WARPS / 2; d > 0; d >>= 1)
+      sum = sum + make_float2(__shfl_xor_sync(0xffffffffu, sum.x, d), __shfl_xor_sync(0xffffffffu, sum.y, d));
+    if (lane == 0) {
+      // 2^block_c in natural units, and log2 e's second part: 2^(x low) is 2^(most low) but for what is far below it
+      float2 ref = make_float2(block_c * 0x1.62ep-1f, fmaf(block_c, 3.194618e-05f, block_most * (kLog2eLow * 0.69314718f)));
+      ref = two_sum(ref.x, ref.y + __fmaf_rn(block_c, 0x1.62ep-1f, -ref.x));
+      if (far) ref = make_float2(block_most, 0.0f);
+      __stcg(p.heads + blockIdx.x, make_float4(ref.x, ref.y, sum.x, sum.y));
     }
-    __syncthreads();
-    many = sm.count > p.list - p.N;
-  }
-  if (many) {
-    take_one_by_one<T>(p, sm, row, v0, v1, out);
-  } else {
-    if (exact && sm.count < p.N) {
-      // that value's lowest tokens
-      int at = sm.count;
-      __syncthreads();
-      for (int b = 0; b < steps && at < p.N; ++b) {
-        if (!__syncthreads_or(unit_most[b * THREADS + tid] >= least)) continue;
-        for (int i = 0; i < VECS && at < p.N; ++i) {
-          const int v = vec(b * THREADS + tid, i);
-          float x[W];
-          Vec<T>::unpack(r.load(v, v < v1), x);
-          int mine = 0;
-#pragma unroll
-          for (int c = 0; c < W; ++c) mine += x[c] == least;
-          int before = mine;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, before, d);
-            if (lane >= d) before += y;
-          }
-          if (lane == 31) sm.warp_lo[warp] = before;
-          __syncthreads();
-          int all = 0;
-          before += at - mine;
-#pragma unroll
-          for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) before += sm.warp_lo[w];
-            all += sm.warp_lo[w];
-          }
-#pragma unroll
-          for (int c = 0; c < W; ++c)
-            if (x[c] == least) {
-              if (before < p.N) list[before] = value_key(least, r.token(v, c));
-              ++before;
-            }
-          at = min(at + all, p.N);
-          __syncthreads();
-        }
-      }
-      if (tid == 0) sm.count = at;
-      __syncthreads();
-    }
-    // ---------------------------------------------------------------- the N largest, in order: eight lanes to a value
-    const int n = sm.count;
-    for (int e0 = 0; e0 < n; e0 += THREADS / 8) {
-      const int e = e0 + tid / 8;
-      const uint64_t mine = list[min(e, n - 1)];
-      int rank = 0;
-      for (int k = tid % 8; k < n; k += 8) rank += list[k] > mine;
-      rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-      rank += __shfl_xor_sync(0xffffffffu, rank, 2);
-      rank += __shfl_xor_sync(0xffffffffu, rank, 4);
-      if (e < n && tid % 8 == 0 && rank < p.N) __stcg(out + rank, value_of(mine));
-    }
-    for (int e = n + tid; e < p.N; e += THREADS) __stcg(out + e, make_float2(-INFINITY, 0.0f));
-  }
-  bool nan = false;
-  if (block_most == INFINITY) {  // the sum came to nothing: is there a NaN too?
-    for (int v = v0 + tid; v < v1; v += THREADS) {
-      float x[W];
-      Vec<T>::unpack(r.load(v, true), x);
-#pragma unroll
-      for (int c = 0; c < W; ++c) nan |= !(x[c] == x[c]);
-    }
-    nan = __syncthreads_or(nan);
-  }
-  if (tid == 0) {
-    double sum = 0.0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) sum += double(sm.warp_sum[w].x) + double(sm.warp_sum[w].y);
-    if (block_most == INFINITY) sum = nan ? __longlong_as_double(0x7FF8000000000000ll) : 1.0;
-    __stcg(reinterpret_cast<float*>(part), block_most);
-    __stcg(reinterpret_cast<double*>(part) + 1, sum);
   }
 }
 
-// The candidates of a user: slot j is candidate j % N of part j / N, or behind the parts' slots an ended beam's only one.
-struct Candidate {
-  int64_t key;     // the score's; larger is better
-  uint64_t tie;    // beam, then logit; smaller is better
-  uint32_t token;  // smaller is better
-  bool any;
-};
+// ---------------------------------------------------------------- a user's beams together
+// A candidate's score: 0.0 where the row offers it, infinity or NaN where it does not.
+__device__ __forceinline__ float2 score_of(const Smem& sm, int k, float x) {
+  const float2 lse = sm.lse[k];
+  return make_float2(sm.score[k], 0.0f) + (make_float2(x, 0.0f) + make_float2(-lse.x, -lse.y));
+}
+__device__ __forceinline__ bool offered(const Smem& sm, int k, float x, float2 score) {
+  return x > -INFINITY && fabsf(sm.lse[k].x) < INFINITY && fabsf(score.x) < INFINITY;
+}
+// Beam, then logit: smaller is better among equal scores.
+__device__ __forceinline__ uint64_t tie_of(int k, float x) {
+  return uint64_t(uint32_t(k)) << 32 | uint32_t(~(uint32_t(ordered(x + 0.0f)) ^ 0x80000000u));
+}
 __device__ __forceinline__ bool before(int64_t key, uint64_t tie, uint32_t token, int64_t key2, uint64_t tie2, uint32_t token2) {
   return key > key2 || (key == key2 && (tie < tie2 || (tie == tie2 && token < token2)));
 }
-__device__ __forceinline__ float2 candidate_value(const BeamParams& p, int user, int j) {
-  if (j >= p.K * p.splits * p.N) return make_float2(0.0f, 0.0f);
-  const int part = j / p.N;
-  return __ldcg(reinterpret_cast<const float2*>(p.parts + (int64_t(user) * p.K * p.splits + part) * p.part_bytes + sizeof(PartHead)) +
-                (j - part * p.N));
+__device__ __forceinline__ void win(const BeamParams& p, Smem& sm, int user, int rank, float score, int k, int t) {
+  const int64_t o = int64_t(user) * p.N + rank;
+  sm.winner[rank] = k;
+  p.parents[o] = user * p.K + k;
+  p.tokens[o] = t;
+  p.scores_out[o] = score;
+  if (p.done_out) p.done_out[o] = sm.lse[k].x == -INFINITY || t == p.eos;
+  if (p.history) p.history_out[o * p.history_stride + p.length] = t;
 }
-__device__ __forceinline__ Candidate candidate(const BeamParams& p, const Smem& sm, int user, int j, float2 v) {
-  const int slots = p.K * p.splits * p.N;
-  Candidate c;
-  double s = -INFINITY;
-  if (j >= slots) {
-    const int k = j - slots;
-    c.token = uint32_t(p.eos);
-    c.tie = uint64_t(k) << 32;
-    if (sm.lse[k] == -INFINITY) s = sm.score[k];
-  } else {
-    const int k = j / (p.N * p.splits);
-    c.token = uint32_t(__float_as_int(v.y));
-    c.tie = uint64_t(k) << 32 | uint32_t(~(uint32_t(ordered(v.x)) ^ 0x80000000u));
-    if (v.x > -INFINITY && fabs(sm.lse[k]) < INFINITY) s = sm.score[k] + (double(v.x) - sm.lse[k]);
-  }
-  c.any = fabs(s) < INFINITY;  // (not for NaN either)
-  c.key = ordered(s);
-  return c;
-}
-
-// The last block of a user: its beams' sums, and the N best of their candidates.
-__device__ __noinline__ void join(const BeamParams& p, Smem& sm, uint64_t* list, int user) {
-  const int tid = threadIdx.x, lane = int(lane_id()), warp = int(warp_id());
-  // a thread's first candidates are on their way while the sums are taken together
-  constexpr int AHEAD = 4;
-  const int slots = p.K * p.splits * p.N + (p.done ? p.K : 0);
-  float2 ahead[AHEAD];
-#pragma unroll
-  for (int i = 0; i < AHEAD; ++i) ahead[i] = tid + i * THREADS < slots ? candidate_value(p, user, tid + i * THREADS) : make_float2(-INFINITY, 0.0f);
-  auto each = [&](auto f) {
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-      if (tid + i * THREADS < slots) f(candidate(p, sm, user, tid + i * THREADS, ahead[i]));
-    for (int j = tid + AHEAD * THREADS; j < slots; j += THREADS) f(candidate(p, sm, user, j, candidate_value(p, user, j)));
-  };
-  // a row's parts to 2^n lanes, several rows to a warp: 64-bit arithmetic takes as long for one lane as for 32
+// The beams' sums.
+__device__ __forceinline__ void join_sums(const BeamParams& p, Smem& sm, int user) {
+  const int lane = int(lane_id()), warp = int(warp_id());
+  // a row's parts to 2^n lanes, several rows to a warp
   int seg = 1;
   while (seg < min(p.splits, 32)) seg *= 2;
-  for (int k0 = warp * (32 / seg); k0 < p.K; k0 += WARPS * (32 / seg)) {
+  const int rows = 32 / seg;
+#pragma unroll 1
+  for (int k0 = warp * rows; k0 < p.K; k0 += WARPS * rows) {
     const int k = k0 + lane / seg;
-    const bool row = k < p.K, ended = row && p.done && p.done[user * p.K + k];
-    const uint8_t* parts = p.parts + int64_t(user * p.K + min(k, p.K - 1)) * p.splits * p.part_bytes;
-    float most = -INFINITY;
-    double sum = 0.0;
+    const bool row = k < p.K;
+    const int beam = user * p.K + min(k, p.K - 1);
+    const float4* heads = p.heads + int64_t(beam) * p.splits;
+    // three loads at once
+    float4 head = __ldcg(heads + min(lane % seg, p.splits - 1));
+    const float score = p.scores[beam];
+    const bool ended = p.done && p.done[beam];
+    float2 ref = make_float2(-INFINITY, 0.0f), sum = make_float2(0.0f, 0.0f);
+#pragma unroll 1
     for (int i0 = 0; i0 < p.splits; i0 += seg) {
       const int i = i0 + lane % seg;
-      float m = -INFINITY;
-      double s = 0.0;
-      if (i < p.splits && row && !ended) {
-        m = __ldcg(reinterpret_cast<const float*>(parts + int64_t(i) * p.part_bytes));
-        s = __ldcg(reinterpret_cast<const double*>(parts + int64_t(i) * p.part_bytes) + 1);
+      if (i0 > 0) head = __ldcg(heads + min(i, p.splits - 1));
+      float2 m = make_float2(-INFINITY, 0.0f), s = make_float2(0.0f, 0.0f);
+      if (i < p.splits && !ended) {
+        m = make_float2(head.x, head.y);
+        s = make_float2(head.z, head.w);
       }
-      float top = fmaxf(most, m);
-      for (int d = seg / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      if (m != top && m > -INFINITY) s *= exp(double(m) - double(top));
-      if (most != top && most > -INFINITY) sum *= exp(double(most) - double(top));
-      most = top;
-      for (int d = seg / 2; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      sum += s;
+      float2 top = m.x > ref.x || (m.x == ref.x && m.y > ref.y) ? m : ref;
+#pragma unroll 1
+      for (int d = seg / 2; d > 0; d >>= 1) {
+        const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, top.x, d), __shfl_xor_sync(0xffffffffu, top.y, d));
+        if (o.x > top.x || (o.x == top.x && o.y > top.y)) top = o;
+      }
+      if (m.x != top.x || m.y != top.y) s = s * exp_below(m, top);
+      if (i0 > 0 && (ref.x != top.x || ref.y != top.y)) sum = sum * exp_below(ref, top);
+      ref = top;
+#pragma unroll 1
+      for (int d = seg / 2; d > 0; d >>= 1)
+        s = s + make_float2(__shfl_xor_sync(0xffffffffu, s.x, d), __shfl_xor_sync(0xffffffffu, s.y, d));
+      sum = sum + s;
     }
     if (row && lane % seg == 0) {
-      const double lse = ended ? 0.0 : double(most) + log(sum);
+      float2 lse = make_float2(0.0f, 0.0f);
+      if (!ended) lse = sum.x > 0.0f && fabsf(ref.x) < INFINITY ? ref + log_of(sum) : make_float2(ref.x + (sum.x - sum.x), 0.0f);
+      if (p.lse) p.lse[user * p.K + k] = lse.x;
       // a row of -infinity, or with +infinity or NaN, offers nothing
-      sm.lse[k] = ended ? -INFINITY : fabs(lse) < INFINITY ? lse : INFINITY;
-      sm.score[k] = double(p.scores[user * p.K + k]);
-      if (p.lse) p.lse[user * p.K + k] = float(lse);
+      sm.lse[k] = ended ? make_float2(-INFINITY, 0.0f) : fabsf(lse.x) < INFINITY ? lse : make_float2(INFINITY, 0.0f);
+      sm.score[k] = score;
+      const float bias = score - lse.x;
+      sm.bias[k] = !ended && fabsf(lse.x) < INFINITY && fabsf(bias) < INFINITY ? bias : -INFINITY;
     }
   }
-  if (tid == 0) sm.count = 0;
+}
+
+// The groups' maxima of a user lie in lines, a part's after another's; a thread has its place of every fourth one.
+// (Counted on, not divided: code that runs once costs its fetch.)
+struct Lines {
+  int line, k, left;  // its row; lines left of the row, this one included
+  __device__ __forceinline__ Lines(const BeamParams& p) : line(int(threadIdx.x) / LINE), k(0), left(p.splits * p.lines - line) { settle(p); }
+  __device__ __forceinline__ void settle(const BeamParams& p) {
+    while (left <= 0) {
+      ++k;
+      left += p.splits * p.lines;
+    }
+  }
+  __device__ __forceinline__ void next(const BeamParams& p) {
+    line += THREADS / LINE;
+    left -= THREADS / LINE;
+    settle(p);
+  }
+};
+
+// The largest of the row's logits below `below`, over the block (all threads get it).
+template <typename T>
+__device__ __noinline__ float largest_below(const BeamParams& p, Smem& sm, int row, float below) {
+  const Row<T> r(p, row);
+  constexpr int W = Row<T>::W;
+  const int vecs = (p.V + r.skew + W - 1) / W;
+  float best = -INFINITY;
+#pragma unroll 4
+  for (int v = int(threadIdx.x); v < vecs; v += THREADS) {
+    float x[W];
+    Vec<T>::unpack(r.load(v, true), x);
+#pragma unroll
+    for (int c = 0; c < W; ++c)
+      if (x[c] < below) best = fmaxf(best, x[c]);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
   __syncthreads();
-  int best = NONE;
-  each([&](const Candidate& c) {
-    if (c.any) best = max(best, int(c.key >> 32));
-  });
+  if (lane_id() == 0) sm.warp_most[warp_id()] = best;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) best = fmaxf(best, sm.warp_most[w]);
+  return best;
+}
+
+// The best one value of a row after the other, all tokens that have it in order: for plateaus.
+template <typename T>
+__device__ __noinline__ void join_by_value(const BeamParams& p, Smem& sm, int user) {
+  constexpr int W = Row<T>::W;
+  const int tid = threadIdx.x, lane = int(lane_id()), warp = int(warp_id());
+  for (int k = 0; k < p.K; ++k) {
+    const bool row = fabsf(sm.lse[k].x) < INFINITY;
+    const float x = row ? largest_below<T>(p, sm, user * p.K + k, INFINITY) : -INFINITY;  // (such a row has no infinity)
+    if (tid == 0) sm.next[k] = sm.lse[k].x == -INFINITY ? 0.0f : x;  // (an ended beam's one candidate)
+  }
+  __syncthreads();
+  int placed = 0;
+  while (placed < p.N) {
+    // the best row, by every thread
+    int best = -1;
+    int64_t key = 0;
+    float2 score = make_float2(0.0f, 0.0f);
+    for (int k = 0; k < p.K; ++k) {
+      const bool ended = sm.lse[k].x == -INFINITY;
+      const float x = sm.next[k];
+      const float2 s = ended ? make_float2(sm.score[k], 0.0f) : score_of(sm, k, x);
+      if (!(x > -INFINITY) || !(ended ? fabsf(s.x) < INFINITY : offered(sm, k, x, s))) continue;
+      if (best < 0 || ordered(s) > key) {
+        best = k;
+        key = ordered(s);
+        score = s;
+      }
+    }
+    if (best < 0) break;
+    const float x = sm.next[best];
+    __syncthreads();
+    if (sm.lse[best].x == -INFINITY) {
+      if (tid == 0) {
+        win(p, sm, user, placed, score.x, best, p.eos);
+        sm.next[best] = -INFINITY;
+      }
+      ++placed;
+      __syncthreads();
+      continue;
+    }
+    const Row<T> r(p, user * p.K + best);
+    const int vecs = (p.V + r.skew + W - 1) / W;
+    for (int v0 = 0; v0 < vecs && placed < p.N; v0 += THREADS) {
+      const int v = v0 + tid;
+      float y[W];
+      Vec<T>::unpack(r.load(v, v < vecs), y);
+      int mine = 0;
+#pragma unroll
+      for (int c = 0; c < W; ++c) mine += y[c] == x;
+      if (!__syncthreads_or(mine)) continue;
+      int at = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, at, d);
+        if (lane >= d) at += z;
+      }
+      if (lane == 31) sm.warp_lo[warp] = at;
+      __syncthreads();
+      int all = 0;
+      at += placed - mine;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) at += sm.warp_lo[w];
+        all += sm.warp_lo[w];
+      }
+#pragma unroll
+      for (int c = 0; c < W; ++c)
+        if (y[c] == x) {
+          if (at < p.N) win(p, sm, user, at, score.x, best, r.token(v, c));
+          ++at;
+        }
+      placed = min(placed + all, p.N);
+      __syncthreads();
+    }
+    if (placed < p.N) {
+      const float y = largest_below<T>(p, sm, user * p.K + best, x);
+      if (tid == 0) sm.next[best] = y;
+      __syncthreads();
+    }
+  }
+}
+
+// A group that is looked at again.
+struct Hit {
+  int row, token, end;  // of the user; the group's first token (below 0 where the row begins in a vector); its part's end
+};
+
+// The last block of a user: its beams' sums, and the N best of their candidates.
+template <typename T>
+__device__ __noinline__ void join(const BeamParams& p, Smem& sm, int64_t* keys, int user) {
+  constexpr int W = Row<T>::W, VECS = UNIT / W;
+  const int tid = threadIdx.x;
+  uint64_t* ties = reinterpret_cast<uint64_t*>(keys + p.list);
+  uint32_t* tokens = reinterpret_cast<uint32_t*>(ties + p.list);
+  Hit* hit = reinterpret_cast<Hit*>(tokens + p.list);
+  const int lines = p.K * p.splits * p.lines;
+  const float* maxima = p.maxima + int64_t(user) * lines * LINE + tid % LINE;
+  sm.bins[tid] = 0;
+  if (tid < p.N) sm.winner[tid] = -1;
+  if (tid == 0) sm.count = sm.hits = 0;
+  float x[AHEAD];  // on their way while the sums are taken together
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+    const int line = tid / LINE + i * (THREADS / LINE);
+    x[i] = -INFINITY;
+    if (line < lines) x[i] = __ldcg(maxima + line * LINE);
+  }
+  join_sums(p, sm, user);
+  __syncthreads();
+  // The threads' best groups (and ended beams), in fp32, and a bound that N of them reach.
+  const bool ended = tid < p.K && sm.lse[tid].x == -INFINITY && fabsf(sm.score[tid]) < INFINITY;
+  float best = ended ? sm.score[tid] : -INFINITY;
+  Lines at(p);
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+    x[i] += sm.bias[min(at.k, p.K - 1)];
+    best = fmaxf(best, x[i]);
+    at.next(p);
+  }
+  {
+    Lines l = at;
+#pragma unroll 4
+    for (; l.line < lines; l.next(p)) best = fmaxf(best, __ldcg(maxima + int64_t(l.line) * LINE) + sm.bias[l.k]);
+  }
   bool exact;
-  const int cut = bound(sm, best, p.N, exact);
-  int64_t* keys = reinterpret_cast<int64_t*>(list);
-  const int places = p.list * 8 / 20;
-  uint64_t* ties = reinterpret_cast<uint64_t*>(keys + places);
-  uint32_t* tokens = reinterpret_cast<uint32_t*>(ties + places);
-  if (best != NONE && best >= cut) {
-    each([&](const Candidate& c) {
-      if (c.any && int(c.key >> 32) >= cut) {
-        const int at = atomicAdd(&sm.count, 1);
-        if (at < places) {
-          keys[at] = c.key;
-          ties[at] = c.tie;
-          tokens[at] = c.token;
+  const int cut = bound(sm, best > -INFINITY ? ordered(best + 0.0f) : NONE, p.N, exact);
+  // An fp32 score is off by 2^-24 of itself and of the bias: what lies twice that below the bound may be among the N best.
+  float large = fmaxf(fabsf(unordered(cut)), 0.0f);
+  for (int k = int(lane_id()); k < p.K; k += 32)
+    if (sm.bias[k] > -INFINITY) large = fmaxf(large, fabsf(sm.bias[k]));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) large = fmaxf(large, __shfl_xor_sync(0xffffffffu, large, d));
+  const float above = cut == NONE + 1 ? -3.402823466e38f : fmaxf(unordered(cut) - large * 0x1p-20f, -3.402823466e38f);
+  if (best >= above) {
+    if (ended && sm.score[tid] >= above) {
+      const int at = atomicAdd(&sm.count, 1);  // (64 of them: the list has more places)
+      ties[at] = uint64_t(uint32_t(tid)) << 32;
+      tokens[at] = uint32_t(p.eos);
+    }
+    auto take = [&](int line) {
+      const int at = atomicAdd(&sm.hits, 1);
+      if (at >= HITS) return;
+      const int k = line / (p.splits * p.lines), part = line / p.lines;
+      const Row<T> r(p, user * p.K + k);
+      const int2 range = part_vectors(p, r, part - k * p.splits);
+      const int v = range.x + (line - part * p.lines) * (GROUP * VECS * THREADS) + tid % LINE * 4;
+      hit[at] = Hit{k, r.token(v, 0), min(r.token(range.y, 0), p.V)};
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (x[i] >= above) take(tid / LINE + i * (THREADS / LINE));
+#pragma unroll 4
+    for (; at.line < lines; at.next(p))
+      if (__ldcg(maxima + int64_t(at.line) * LINE) + sm.bias[at.k] >= above) take(at.line);
+  }
+  __syncthreads();
+  const int hits = sm.hits;
+  // ---------------------------------------------------------------- what reaches the bound
+  if (hits <= HITS) {
+    // a group's vectors are four neighbouring ones of each step
+    constexpr int VPG = 4 * GROUP * VECS, BATCH = 4;
+    const int offset = (tid / 4 % (GROUP * VECS) * THREADS + tid % 4) * W;
+#pragma unroll 1
+    for (int h0 = tid / VPG; h0 < hits; h0 += BATCH * (THREADS / VPG)) {
+      uint4 w[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const Hit at = hit[min(h0 + i * (THREADS / VPG), hits - 1)];
+        const T* first = static_cast<const T*>(p.logits) + int64_t(user * p.K + at.row) * p.stride;
+        const int e = at.token + offset;
+        if (e >= 0 && e + W <= at.end) w[i] = Vec<T>::load(first + e);
+        else w[i] = Row<T>::edge(first, e, at.end);
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int h = h0 + i * (THREADS / VPG);
+        if (h >= hits) break;
+        float x[W];
+        Vec<T>::unpack(w[i], x);
+        float most = x[0];
+#pragma unroll
+        for (int c = 1; c < W; ++c) most = fmaxf(most, x[c]);
+        const float bias = sm.bias[hit[h].row];
+        if (!(most + bias >= above)) continue;
+        for (int c = 0; c < W; ++c) {
+          float y = x[0];
+#pragma unroll
+          for (int j = 1; j < W; ++j)
+            if (j == c) y = x[j];
+          if (!(y + bias >= above)) continue;
+          const int place = atomicAdd(&sm.count, 1);
+          if (place < p.list) {
+            ties[place] = tie_of(hit[h].row, y);
+            tokens[place] = uint32_t(hit[h].token + offset + c);
+          }
         }
       }
-    });
+    }
   }
-  for (int i = tid; i < p.N; i += THREADS) sm.winner[i] = -1;
   __syncthreads();
   const int n = sm.count;
-  auto win = [&](int rank, int64_t key, int k, int t) {
-    const double s = __longlong_as_double(key ^ ((key >> 63) & 0x7FFFFFFFFFFFFFFFll));
-    const int64_t o = int64_t(user) * p.N + rank;
-    sm.winner[rank] = k;
-    p.parents[o] = user * p.K + k;
-    p.tokens[o] = t;
-    p.scores_out[o] = float(s);
-    if (p.done_out) p.done_out[o] = sm.lse[k] == -INFINITY || t == p.eos;
-    if (p.history) p.history_out[o * p.history_stride + p.length] = t;
-  };
-  if (n <= places) {
+  if (hits <= HITS && n <= p.list) {
+    for (int e = tid; e < n; e += THREADS) {
+      const int k = int(ties[e] >> 32);
+      const float y = unordered(int(~uint32_t(ties[e]) ^ 0x80000000u));
+      const bool ended = sm.lse[k].x == -INFINITY;
+      const float2 s = ended ? make_float2(sm.score[k], 0.0f) : score_of(sm, k, y);
+      keys[e] = ended || offered(sm, k, y, s) ? ordered(s) : int64_t(0x8000000000000000ull);
+    }
+    __syncthreads();
+    // eight lanes to a candidate
     for (int e0 = 0; e0 < n; e0 += THREADS / 8) {
       const int e = e0 + tid / 8, at = min(e, n - 1);
       const int64_t key = keys[at];
@@ -536,60 +792,14 @@ __device__ __noinline__ void join(const BeamParams& p, Smem& sm, uint64_t* list,
       rank += __shfl_xor_sync(0xffffffffu, rank, 1);
       rank += __shfl_xor_sync(0xffffffffu, rank, 2);
       rank += __shfl_xor_sync(0xffffffffu, rank, 4);
-      if (e < n && tid % 8 == 0 && rank < p.N) win(rank, key, int(tie >> 32), int(t));
+      if (e < n && tid % 8 == 0 && rank < p.N && key != int64_t(0x8000000000000000ull)) win(p, sm, user, rank, unordered(int(key >> 32)), int(tie >> 32), int(t));
     }
   } else {
-    // more scores next to one another than the list holds: the best, one after the other
-    int64_t last_key = 0x7FFFFFFFFFFFFFFFll;  // (no score has it)
-    uint64_t last_tie = 0;
-    uint32_t last_token = 0;
-    constexpr uint32_t NO_TOKEN = 0xFFFFFFFFu;
-    for (int r = 0; r < p.N; ++r) {
-      int64_t key = int64_t(0x8000000000000000ull);
-      uint64_t tie = ~0ull;
-      uint32_t t = NO_TOKEN;
-      each([&](const Candidate& c) {
-        if (c.any && before(last_key, last_tie, last_token, c.key, c.tie, c.token) && before(c.key, c.tie, c.token, key, tie, t)) {
-          key = c.key;
-          tie = c.tie;
-          t = c.token;
-        }
-      });
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        const int64_t key2 = __shfl_xor_sync(0xffffffffu, key, d);
-        const uint64_t tie2 = __shfl_xor_sync(0xffffffffu, tie, d);
-        const uint32_t t2 = __shfl_xor_sync(0xffffffffu, t, d);
-        if (before(key2, tie2, t2, key, tie, t)) {
-          key = key2;
-          tie = tie2;
-          t = t2;
-        }
-      }
-      if (lane == 0) {
-        sm.best_key[warp] = key;
-        sm.best_tie[warp] = tie;
-        sm.best_token[warp] = t;
-      }
-      __syncthreads();
-      for (int w = 0; w < WARPS; ++w)
-        if (before(sm.best_key[w], sm.best_tie[w], sm.best_token[w], key, tie, t)) {
-          key = sm.best_key[w];
-          tie = sm.best_tie[w];
-          t = sm.best_token[w];
-        }
-      __syncthreads();
-      if (t == NO_TOKEN) break;
-      if (tid == 0) win(r, key, int(tie >> 32), int(t));
-      last_key = key;
-      last_tie = tie;
-      last_token = t;
-    }
+    join_by_value<T>(p, sm, user);
   }
   __syncthreads();
-  for (int i = tid; i < p.N; i += THREADS) {
-    if (sm.winner[i] >= 0) continue;
-    const int64_t o = int64_t(user) * p.N + i;
+  if (tid < p.N && sm.winner[tid] < 0) {
+    const int64_t o = int64_t(user) * p.N + tid;
     p.parents[o] = p.tokens[o] = -1;
     p.scores_out[o] = -INFINITY;
     if (p.done_out) p.done_out[o] = 1;
@@ -605,20 +815,20 @@ __device__ __noinline__ void join(const BeamParams& p, Smem& sm, uint64_t* list,
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS, 4) beam_kernel(const __grid_constant__ BeamParams p) {
-  extern __shared__ __align__(16) uint64_t list[];
+  extern __shared__ __align__(16) int64_t list[];
   __shared__ Smem sm;
   const int row = int(blockIdx.x) / p.splits, split = int(blockIdx.x) - row * p.splits, user = row / p.K;
-  if (!(p.done && p.done[row])) take_part<T>(p, sm, list, row, split, p.parts + int64_t(blockIdx.x) * p.part_bytes);
-  __threadfence();
+  if (!(p.done && p.done[row])) take_part<T>(p, sm, row, split);
   __syncthreads();
   if (threadIdx.x == 0) {
-    sm.last = atomicAdd(p.counters + user, 1u) == uint32_t(p.K * p.splits - 1);
+    // what the block has written is released, what the others have is acquired
+    uint32_t before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.counters + user) : "memory");
+    sm.last = before == uint32_t(p.K * p.splits - 1);
     if (sm.last) p.counters[user] = 0;
   }
   __syncthreads();
-  if (!sm.last) return;
-  __threadfence();
-  join(p, sm, list, user);
+  if (sm.last) join<T>(p, sm, list, user);
 }
 
 constexpr size_t kCounters = size_t(MAX_B) * 4;  // in a place that does not depend on the sizes
@@ -629,8 +839,14 @@ int split_count(int64_t rows, int V) {
   const int most = int((int64_t(V) + 7 + STEP - 1) / STEP);
   return std::max(least_splits(V), std::min(std::min(most, 32), int((BLOCKS + rows - 1) / rows)));
 }
-int part_bytes(int N) { return int(sizeof(PartHead)) + N * 8; }
-int list_places(int N) { return std::max(256, 32 * N); }
+// Vectors of a part, at least: of W elements, a row's first one up to W - 1 behind 16 bytes.
+int part_vectors(int V, int W, int splits) { return int((int64_t(V) + 2 * (W - 1)) / W + splits - 1) / splits; }
+// Lines of maxima of a part, of either type: of 4 W-element vectors to a thread for fp32, 2 for bf16.
+int line_count(int V, int splits) {
+  const int a = part_vectors(V, 4, splits), b = part_vectors(V, 8, splits);
+  return std::max(1, std::max(cdiv(a, GROUP * STEP / 4), cdiv(b, GROUP * STEP / 8)));
+}
+int64_t part_bytes(int lines) { return int64_t(sizeof(float4)) + lines * LINE * 4; }
 
 bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -643,8 +859,8 @@ bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
 extern "C" size_t tl_beam_select_workspace_size(int B, int K, int N, int V) {
   using namespace tl;
   if (B < 1 || B > MAX_B || K < 1 || K > MAX_BEAMS || N < 1 || N > MAX_N || V < 1 || int64_t(K) * V > 0x7FFFFFFF) return 0;
-  // (rows times their parts never fall as rows grow, with BLOCKS beside them)
-  return kCounters + (size_t(B) * K * least_splits(V) + BLOCKS) * part_bytes(N);
+  // parts of all rows are at most this many, of at most this size, which never fall as B or K grow
+  return kCounters + (size_t(B) * K * least_splits(V) + BLOCKS) * part_bytes(line_count(V, least_splits(V)));
 }
 
 extern "C" tl_status tl_beam_select(const tl_beam_select_args* a, void* stream) {
@@ -692,18 +908,18 @@ extern "C" tl_status tl_beam_select(const tl_beam_select_args* a, void* stream) 
   p.history_stride = a->history_stride;
   p.length = a->length;
   p.counters = static_cast<uint32_t*>(a->workspace);
-  p.parts = static_cast<uint8_t*>(a->workspace) + kCounters;
   p.B = a->B;
   p.K = a->K;
   p.N = a->N;
   p.V = a->V;
   p.eos = a->eos;
   p.splits = split_count(in, a->V);
-  p.part_bytes = part_bytes(a->N);
-  p.list = list_places(a->N);
-  p.steps = cdiv(cdiv(a->V + 7 + 7, a->dtype ? 8 : 4), p.splits);            // vectors of a part,
-  p.steps = std::max(1, cdiv(p.steps, STEP / (a->dtype ? 8 : 4)));           // and its steps
-  const size_t smem = size_t(p.list) * 8 + HITS * 4 + size_t(p.steps) * THREADS * 4;
+  p.lines = line_count(a->V, p.splits);
+  p.per = part_vectors(a->V, a->dtype ? 8 : 4, p.splits);
+  p.heads = reinterpret_cast<float4*>(static_cast<uint8_t*>(a->workspace) + kCounters);
+  p.maxima = reinterpret_cast<float*>(p.heads + in * p.splits);
+  p.list = std::max(256, 16 * a->N);
+  const size_t smem = size_t(p.list) * 20 + HITS * 12;
   const int64_t blocks = in * p.splits;
   if (blocks > 0x7FFFFFFF) return fail(TL_ERR_UNSUPPORTED, "%s: too many rows", who);
   void* args[] = {&p};
