@@ -254,3 +254,115 @@ def test_binding_refuses_wrong_trees(B):
         c.run()
     c.tree = good
     c.run().check()
+
+
+# ------------------------------------------------------------------ the kernel for many rows
+def by_many(b):
+    """The rule by which the call's kernels share the sequences, on 152 SMs: whether those of many rows go to the one for many."""
+    least = 32 if len(b.q) >= 8 else 64
+    units = tiles = few = 0
+    for q, n in zip(b.q, b.lens):
+        rows = q * (b.H // b.Hkv)
+        if rows > least:
+            u = -(-rows // 256) * b.Hkv
+            units, tiles = units + u, tiles + u * max(1, -(-n // 64))
+            few += -(-rows // 16) * b.Hkv * (-(-n // 32) + 24)
+    if not units:
+        return False
+    runs = min(152, max(units, tiles // 8))
+    join = 0 if runs == units else 8000 + 2200 * runs // units
+    return (950 * tiles + 8000 * units) // 152 + join + 20000 < 210 * few // 152 + 8000
+
+
+MANY = dict(H=32, Hkv=8, D=128, ps=64)
+
+
+@pytest.mark.parametrize("q,lens,layout", [
+    ([64] * 8, [64, 65, 127, 128, 129, 400, 500, 300], MANY),                      # two tiles of rows
+    ([64, 3, 40, 1, 0, 64, 33, 64, 64, 50], [164, 70, 300, 90, 10, 64, 200, 401, 90, 51], MANY),   # few and many, one tile and two
+    ([31, 30, 64, 20] * 3, [131, 95, 164, 200] * 3, dict(H=24, Hkv=8, D=64, ps=16)),
+    ([100] * 4, [900, 350, 100, 612], dict(H=40, Hkv=8, D=128, ps=128)),           # three units to a sequence, the last part-filled
+    ([128], [9000], MANY)])
+def test_ragged_trees_of_many_rows(B, q, lens, layout):
+    b = Batch(q, lens, seed=51, extra_columns=600, **layout)
+    assert by_many(b)
+    TreeCall(B, b).run().check()
+
+
+def test_any_masks_of_many_rows(B):
+    rng = np.random.default_rng(52)
+    b = Batch([64] * 8, [64, 100, 64, 300, 64, 65, 190, 400], seed=52, extra_columns=100, **MANY)
+    assert by_many(b)
+    sees = [rng.random((64, 64)) < 0.4 for _ in range(8)]
+    sees[0][[1, 63]] = False
+    sees[1][2] = False
+    sees[2][:] = False
+    c = TreeCall(B, b, sees=sees, words=3).run().check()
+    empty = [1, 63] + list(range(128, 192))
+    assert (c.out[empty] == 0).all() and torch.isneginf(c.lse[:, empty]).all()
+
+
+@pytest.mark.parametrize("D,group", [(128, 4), (64, 8)])
+def test_nan_in_trees_of_many_rows(B, D, group):
+    n = 64
+    def edit(c):
+        b = c.b
+        for s, i, d in ((0, 1, 3), (0, 3, 60), (1, 2, 3), (2, 0, 5), (3, 63, 50)):
+            pos = b.lens[s] - n + i
+            c.vc[b.table[s, pos // b.ps], :, pos % b.ps, d] = 127
+        pos = b.lens[1] - n + 1
+        c.kc[b.table[1, pos // b.ps], 0, pos % b.ps, 7] = 255
+        pos = b.lens[4] - n - 1
+        c.vc[b.table[4, pos // b.ps], :, pos % b.ps, 9] = 255
+        c.vs[b.table[5, (b.lens[5] - 1) // b.ps], 2] = 255  # one head's last page, which holds its last new token alone
+        for s, m in enumerate(b.lens):
+            if m % b.ps:
+                c.vc[b.table[s, m // b.ps], :, m % b.ps:] = 127
+    b = Batch([n] * 8, [n + 40, n + 21, n, n + 70, n + 2, 16 * 9 + 1, n + 200, n + 90], H=8 * group, Hkv=8, D=D, ps=16, seed=53,
+              extra_columns=100)
+    assert by_many(b)
+    c = TreeCall(B, b, edit=edit, noise=False).run()
+    assert B.tl_query_status(c.sig)[0] == 0
+    want, lse, vmax, smax = c.expected()
+    got = f64(c.out)
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.isnan(got).any() and not np.isnan(got).all()
+    check_attention(got, f64(c.lse), want, lse, vmax, smax)
+
+
+@pytest.mark.parametrize("spread", [8, 25])
+def test_scales_far_apart_in_trees_of_many_rows(B, spread):
+    def edit(c):
+        c.ks[:] = c.b.rng.integers(110 - spread // 2, 110 + spread // 2, c.ks.shape)
+        c.vs[:] = c.b.rng.integers(120 - spread, 120 + spread, c.vs.shape)
+    b = Batch([64, 30] * 4, [300, 140, 64, 95] * 2, seed=54, extra_columns=100, **MANY)
+    assert by_many(b)
+    c = TreeCall(B, b, edit=edit).run()
+    assert B.tl_query_status(c.sig)[0] == 0
+    check_attention(f64(c.out), f64(c.lse), *c.expected())
+
+
+def test_great_scores_in_trees_of_many_rows(B):
+    b = Batch([64] * 8, [300] * 8, seed=55, extra_columns=100, **MANY)
+    assert by_many(b)
+    TreeCall(B, b, q_scale=200.0).run().check()
+
+
+def test_trees_of_many_rows_again_and_captured(B):
+    b = Batch([64, 40, 64, 64, 7, 64, 64, 33, 64], [500, 70, 1300, 131, 90, 64, 300, 200, 400], seed=56, extra_columns=50, **MANY)
+    assert by_many(b)
+    c = TreeCall(B, b).run().check()
+    first = c.out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run()
+    for _ in range(3):
+        c.out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c.out, first)
+    b2 = Batch([2, 64], [60, 80], seed=57, **LAYOUTS[0])
+    d = TreeCall(B, b2)
+    d.ws = c.ws if c.ws.numel() >= d.ws.numel() else d.ws
+    d.run().check()
+    c.run()
+    assert torch.equal(c.out, first)

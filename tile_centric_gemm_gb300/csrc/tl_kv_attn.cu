@@ -93,6 +93,7 @@ struct DecodeParams {
   int32_t max_rows;    // sequences of more query rows per kv head are left to the kernel for many
   float scale_log2;
   KvTree tree;         // tl_kv_tree_attn
+  int32_t many_ctas;   // of the other kernel, where a tree's sequences may be its
 };
 
 template <int D, int NR, int WARPS, int PER_SM>
@@ -106,6 +107,7 @@ struct DecodeSmem {
   uint2 meta[WARPS][STAGES];  // scale bytes (k, v of the first half, k, v of the second); which halves' pages are good
   int32_t spare[WARPS];
   int64_t warp_sum[WARPS];
+  int64_t rule[3][WARPS];
   int32_t warp_items[WARPS];
   int64_t begin_off;
   int32_t begin_seq, last;
@@ -120,14 +122,10 @@ struct Segment {
   int64_t left;                       // of the run from there on
 };
 
-// a / b, in 32 bits where that is enough (a 64-bit division takes about 500 cycles)
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return ((a | b) >> 32) ? a / b : int64_t(uint32_t(a) / uint32_t(b));
-}
 template <int TILE>
-__device__ __forceinline__ int seq_tiles(const DecodeParams& p, const KvSeq& q) {
+__device__ __forceinline__ int seq_tiles(const DecodeParams& p, const KvSeq& q, int max_rows) {
   const uint32_t rows = uint32_t(q.q) * uint32_t(p.group);  // in 31 bits (checked by the host)
-  return rows > uint32_t(p.max_rows) ? 0 : int((rows + TILE - 1) / TILE);
+  return rows > uint32_t(max_rows) ? 0 : int((rows + TILE - 1) / TILE);
 }
 __device__ __forceinline__ int seq_chunks(const KvSeq& q) { return max(1, (q.len + CHUNK - 1) / CHUNK); }
 
@@ -138,11 +136,11 @@ __device__ __forceinline__ void seg_cut(Segment& g, int o) {
   g.ce = o + g.used - LEAD;  // not above cb: nothing but places that stand for a tile's cost
 }
 template <int TILE>
-__device__ __forceinline__ void seg_open(const DecodeParams& p, Segment& g, int s, int64_t off, int64_t left) {
+__device__ __forceinline__ void seg_open(const DecodeParams& p, Segment& g, int s, int64_t off, int64_t left, int max_rows) {
   g.seq = kv_seq(p.b, p.c.ps, s);
   g.s = s;
   g.nch = seq_chunks(g.seq);
-  g.tiles = seq_tiles<TILE>(p, g.seq);
+  g.tiles = seq_tiles<TILE>(p, g.seq, max_rows);
   const int sub = int(quotient(off, g.nch + LEAD));
   g.hk = sub / max(g.tiles, 1);
   g.rt = sub - g.hk * g.tiles;
@@ -150,7 +148,7 @@ __device__ __forceinline__ void seg_open(const DecodeParams& p, Segment& g, int 
   seg_cut(g, int(off - int64_t(sub) * (g.nch + LEAD)));
 }
 template <int TILE>
-__device__ __forceinline__ bool seg_next(const DecodeParams& p, Segment& g) {
+__device__ __forceinline__ bool seg_next(const DecodeParams& p, Segment& g, int max_rows) {
   g.left -= g.used;
   if (g.left <= LEAD) return false;
   if (++g.rt == g.tiles) {
@@ -162,9 +160,9 @@ __device__ __forceinline__ bool seg_next(const DecodeParams& p, Segment& g) {
     return true;
   }
   int s = g.s + 1;
-  while (s < p.b.B && seq_tiles<TILE>(p, kv_seq(p.b, p.c.ps, s)) == 0) ++s;
+  while (s < p.b.B && seq_tiles<TILE>(p, kv_seq(p.b, p.c.ps, s), max_rows) == 0) ++s;
   if (s >= p.b.B) return false;
-  seg_open<TILE>(p, g, s, 0, g.left);
+  seg_open<TILE>(p, g, s, 0, g.left, max_rows);
   return true;
 }
 
@@ -262,11 +260,36 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
   // ---------------------------------------------------------------- this CTA's run of chunks
   const int per = (b.B + THREADS - 1) / THREADS;
   const int first = min(b.B, tid * per), end = min(b.B, first + per);
+  int max_rows = p.max_rows;
+  if (TREE && p.many_ctas > 0) {
+    // which kernel takes the sequences of many rows: the other one decides the same
+    int64_t v[3] = {0, 0, 0};  // units, tiles, and what they cost here
+    for (int s = first; s < end; ++s) {
+      const KvSeq q = kv_seq(b, p.c.ps, s);
+      const int64_t rows = int64_t(q.q) * p.group, units = rows > p.max_rows ? (rows + 255) / 256 * p.c.Hkv : 0;
+      v[0] += units;
+      v[1] += units * max(1, (q.len + 63) / 64);
+      v[2] += few_cost(p.c.Hkv, p.group, p.max_rows, q);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+      if (lane == 0) sm.rule[i][warp] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      v[i] = 0;
+      for (int w = 0; w < WARPS; ++w) v[i] += sm.rule[i][w];
+    }
+    if (!tree_by_many(p.many_ctas, v[0], v[1], v[2])) max_rows = 0x7FFFFFFF;
+  }
   int64_t mine = 0;
   uint32_t items = 0;
   for (int s = first; s < end; ++s) {
     const KvSeq q = kv_seq(b, p.c.ps, s);
-    const int tiles = seq_tiles<TILE>(p, q) * p.c.Hkv;
+    const int tiles = seq_tiles<TILE>(p, q, max_rows) * p.c.Hkv;
     items += uint32_t(tiles);
     mine += int64_t(tiles) * (seq_chunks(q) + LEAD);
   }
@@ -309,7 +332,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
     for (int s = lane; s < b.B; s += 32) {
       const KvSeq q = kv_seq(b, p.c.ps, s);
       const int L = least + warp * TRY;
-      pieces += uint32_t(seq_tiles<TILE>(p, q) * p.c.Hkv) * uint32_t((seq_chunks(q) + L - 1) / L);
+      pieces += uint32_t(seq_tiles<TILE>(p, q, max_rows) * p.c.Hkv) * uint32_t((seq_chunks(q) + L - 1) / L);
     }
     pieces = __reduce_add_sync(0xffffffffu, pieces);
     if (lane == 0) sm.pieces[warp] = int(pieces);
@@ -328,7 +351,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
         int cnt = 0;
         if (s < b.B) {
           const KvSeq q = kv_seq(b, p.c.ps, s);
-          cnt = seq_tiles<TILE>(p, q) * p.c.Hkv * ((seq_chunks(q) + L - 1) / L);
+          cnt = seq_tiles<TILE>(p, q, max_rows) * p.c.Hkv * ((seq_chunks(q) + L - 1) / L);
         }
         int sum = cnt;
 #pragma unroll
@@ -340,7 +363,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
         if (hit) {
           const int src = __ffs(hit) - 1;
           at -= __shfl_sync(0xffffffffu, sum - cnt, src);
-          seg_open<TILE>(p, c, s0 + src, 0, 1);
+          seg_open<TILE>(p, c, s0 + src, 0, 1, max_rows);
           break;
         }
         at -= __shfl_sync(0xffffffffu, sum, 31);
@@ -368,7 +391,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
       int64_t at = before;
       for (int s = first; s < end; ++s) {
         const KvSeq q = kv_seq(b, p.c.ps, s);
-        const int64_t size = int64_t(seq_tiles<TILE>(p, q)) * p.c.Hkv * (seq_chunks(q) + LEAD);
+        const int64_t size = int64_t(seq_tiles<TILE>(p, q, max_rows)) * p.c.Hkv * (seq_chunks(q) + LEAD);
         if (run0 < at + size) {
           sm.begin_seq = s;
           sm.begin_off = run0 - at;
@@ -378,7 +401,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
       }
     }
     __syncthreads();
-    seg_open<TILE>(p, c, sm.begin_seq, sm.begin_off, run1 - run0);
+    seg_open<TILE>(p, c, sm.begin_seq, sm.begin_off, run1 - run0, max_rows);
     if (c.ce <= c.cb) {
       pdl_wait_previous();
       return;
@@ -398,7 +421,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
   uint32_t scale_bytes[2][2] = {{0, 0}, {0, 0}};
   auto settle = [&]() {  // on to a segment that has a chunk for this warp
     while (f_ok && fc >= f.ce) {
-      f_ok = seg_next<TILE>(p, f);
+      f_ok = seg_next<TILE>(p, f, max_rows);
       fc = f.cb + warp;
       f_new = true;
     }
@@ -949,7 +972,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) kv_decode_kernel(const __g
         p.lse[int64_t(h) * b.n_tokens + tok] = L == 0.0f ? -INFINITY : (M1 - kShift + log2f(L)) * 0.69314718055994531f;
     }
     at += c.used;
-    if (!seg_next<TILE>(p, c)) break;
+    if (!seg_next<TILE>(p, c, max_rows)) break;
     load_q(c);
     __syncthreads();  // the merge buffers are free again
   }
@@ -1046,12 +1069,21 @@ tl_status attention(const char* who, const tl_kv_attn_args* a, const KvTree* tre
   // Most new tokens that a sequence can have, as far as the host knows
   const int most = a->max_q_len ? std::min(a->max_q_len, a->n_tokens) : std::max(1, a->n_tokens - a->B + 1);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool many = int64_t(most) * p.group > few_rows(a->B);
+  bool many = int64_t(most) * p.group > few_rows(a->B);
+  if (many && tree) {
+    // ... unless it would not take them however long they are: then it is not launched (as far as the page table can say; to
+    // find it has nothing to do takes it 5 us)
+    const int64_t rows = int64_t(most) * p.group, units = (rows + 255) / 256 * a->B * c.H_kv;
+    const int64_t len = std::min(int64_t(a->max_pages) * c.page_size, int64_t(0x7FFFFF00));
+    if (units < (1 << 20))
+      many = tree_by_many(di.sm_count, units, units * ((len + 63) / 64),
+                          few_cost(c.H_kv, p.group, 0, KvSeq{0, most, int(len)}) * a->B);
+  }
   p.max_rows = 0x7FFFFFFF;
   if (many) {
-    // A sequence of many rows goes to the tensor-core kernel, one of few to this file's; where there is one
-    // sequence only, the first takes it whatever it is.
     PrefillParams f{};
+    // A sequence of many rows goes to the tensor-core kernel, one of few to this file's; where there is one
+    // sequence only, the first takes it whatever it is.  (Trees' go by what each would take: tree_by_many.)
     f.c = p.c;
     f.b = p.b;
     f.q = p.q;
@@ -1066,11 +1098,12 @@ tl_status attention(const char* who, const tl_kv_attn_args* a, const KvTree* tre
     f.group = p.group;
     f.causal = a->causal;
     f.tree = p.tree;
-    f.min_rows = a->B == 1 ? 0 : few_rows(a->B);
+    f.min_rows = a->B == 1 && !tree ? 0 : few_rows(a->B);
     f.scale_log2 = p.scale_log2;
     if (tl_status s = launch_kv_prefill(f, c.head_dim, di.sm_count, st)) return s;
-    if (a->B == 1) return TL_OK;
+    if (a->B == 1 && !tree) return TL_OK;
     p.max_rows = few_rows(a->B);
+    if (tree) p.many_ctas = di.sm_count;
   }
   // Tiles of 8 query rows where a sequence's rows of one kv head fit in one, of 16 otherwise
   const bool small = int64_t(most) * p.group <= 8;

@@ -103,7 +103,7 @@ struct Side {
   union {
     int32_t nan_at[4][128];  // least token whose value is NaN in the dim, among those not all rows see
     struct {                 // before the segments: sums of the work list
-      int64_t warp_sum[16];
+      int64_t warp_sum[16], warp_few[16];
       uint32_t warp_units[16];
     };
   };
@@ -112,6 +112,7 @@ struct Side {
   int32_t begin[4];           // sequence, kv head, row block, tile
   int32_t tiles[4];           // of the segments in work
   int32_t last[2];
+  uint8_t single[4];          // whether the segment has rows in its first tile only
 };
 
 template <int D>
@@ -503,6 +504,36 @@ __device__ __noinline__ float2 join_parts(const float* rows_at, int c0, int c1, 
   return make_float2(top, sum);
 }
 
+// Where a row's 16-byte unit c8 lies.
+template <int D>
+__device__ __forceinline__ uint32_t query_place(uint32_t q, int r, int c8) {
+  return q + uint32_t((r >> 7) * Layout<D>::Q_TILE + (c8 >> 3) * BOX + (r & 127) * 128 + (((c8 & 7) ^ (r & 7)) << 4));
+}
+// Queries: a row to D/8 lanes, copied to its place in bf16, all rows at once, and brought to fp16 there by the lanes that
+// copied it.  (Through registers, row after row, this took 25000 cycles a segment.)  Rows that are none are zeros; of a
+// second tile without any nothing is written.
+template <int D>
+__device__ __noinline__ void copy_queries(const PrefillParams& p, uint32_t q, int row0, int hk, int first, int rows) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, STRIDE = CONV * RPW;  // lanes of a row; rows of a warp, of all
+  const int lane = int(lane_id()), c8 = lane % LPR, r0 = int(warp_id()) * RPW + lane / LPR;
+  const int step_tk = STRIDE / p.group, step_hd = STRIDE - step_tk * p.group;  // from a lane's query row to its next
+  const int64_t q_step = step_tk * p.q_ts + step_hd * p.q_hs, q_wrap = p.q_ts - p.group * p.q_hs;
+  const int tk0 = (first + r0) / p.group, last = rows - first <= ROWS ? ROWS : UNIT;
+  int hd = first + r0 - tk0 * p.group;
+  const uint16_t* from = p.q + int64_t(row0 + tk0) * p.q_ts + int64_t(hk * p.group + hd) * p.q_hs + c8 * 8;
+#pragma unroll 2
+  for (int r = r0; r < last; r += STRIDE) {
+    const bool in = first + r < rows;
+    cp_async16z(query_place<D>(q, r, c8), in ? from : p.q, in);
+    hd += step_hd;
+    from += q_step;
+    if (hd >= p.group) {
+      hd -= p.group;
+      from += q_wrap;
+    }
+  }
+}
+
 template <int D, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_constant__ PrefillParams p) {
   using L = Layout<D>;
@@ -530,6 +561,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     const KvSeq q = kv_seq(b, p.c.ps, s);
     mine += p.c.Hkv * seq_tiles(p, q);
     units += uint32_t(p.c.Hkv) * uint32_t((seq_rows(p, q) + UNIT - 1) / UNIT);
+  }
+  if (TREE) {
+    int64_t few = 0;
+    for (int s = first; s < end; ++s) few += few_cost(p.c.Hkv, p.group, p.min_rows, kv_seq(b, p.c.ps, s));
+    for (int d = 16; d > 0; d >>= 1) few += __shfl_xor_sync(0xffffffffu, few, d);
+    if (lane == 0) sd.warp_few[warp] = few;
   }
   units = __reduce_add_sync(0xffffffffu, units);
   if (lane == 0) sd.warp_units[warp] = units;
@@ -574,10 +611,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     all_units += sd.warp_units[w];
   }
   before -= mine;
+  if (TREE) {
+    int64_t few = 0;
+    for (int w = 0; w < THREADS / 32; ++w) few += sd.warp_few[w];
+    if (!tree_by_many(p.ctas, all_units, total, few)) return;
+  }
   // a CTA for each unit as far as they go, and where units are split MIN_TILES to a CTA at least
   const int64_t n = min(int64_t(gridDim.x), max(all_units, total / MIN_TILES));
   const int64_t cta = blockIdx.x;
-  const int64_t run0 = cta < n ? cta * total / n : 0, run1 = cta < n ? (cta + 1) * total / n : 0;
+  const int64_t run0 = cta < n ? quotient(cta * total, n) : 0, run1 = cta < n ? quotient((cta + 1) * total, n) : 0;
   if (run0 >= run1) return;
   if (mine > 0 && before <= run0 && run0 < before + mine) {
     int64_t at = before;
@@ -586,7 +628,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const int64_t one = seq_tiles(p, q), size = one * p.c.Hkv;
       if (run0 < at + size) {
         int64_t off = run0 - at;
-        const int hk = int(off / one);
+        const int hk = int(quotient(off, one));
         off -= hk * one;
         int qb = 0;
         const int rows = seq_rows(p, q);
@@ -632,9 +674,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     const int r8 = lane >> 2, u4 = lane & 3;
     // where a lane's 16 dims of token r8 go: 16-byte units 2 u4 and 2 u4 + 1 of the row, swizzled by the row
     const uint32_t lane_lo = uint32_t(r8 * 128 + (((2 * u4) ^ r8) << 4)), lane_hi = uint32_t(r8 * 128 + (((2 * u4 + 1) ^ r8) << 4));
-    // from a lane's query row to its next
-    const int step_tk = CONV * 256 / D / p.group, step_hd = CONV * 256 / D - step_tk * p.group;
-    const int64_t q_step = step_tk * p.q_ts + step_hd * p.q_hs, q_wrap = p.q_ts - p.group * p.q_hs;
     int before_seg = 0;              // tiles of earlier segments
     bool ok = true;
     for (int i = 0; ok; ++i) {
@@ -642,6 +681,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const int len = g.seq.len;
       const int min_lim = TREE ? len - g.seq.q : row_limit(p, g.seq, g.qb * UNIT);
       const int32_t* table = b.table + int64_t(g.s) * b.max_pages;
+      if (i == 0 && __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, 1u, abort, b.status, tmo, 11)))
+        copy_queries<D>(p, smem + L::Q, g.seq.row0, g.hk, g.qb * UNIT, rows);  // (nothing to wait for)
       // the largest scales of the segment's pages
       const int tok_end = min(len, g.t1 * KV);
       int km = -127, vm = -127, kl = 127, vl = 127;
@@ -683,6 +724,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       if (km - kl > kNearK || vm - vl > kNearV) km = kFar;
       if (tid == 0) {
         sd.tiles[i & 3] = g.left > g.t1 - g.t0 ? g.t1 - g.t0 : g.t0 - g.t1;  // the run's last one: negative
+        sd.single[i & 3] = rows - g.qb * UNIT <= ROWS;
         sd.kv_exp[i & 3][0] = int16_t(km);
         sd.kv_exp[i & 3][1] = int16_t(vm);
       }
@@ -729,40 +771,25 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       load(p.c.v, cv, warp);
       load_scales();
       page = look_up(warp + CONV);
-      // Queries: a row to D/8 lanes, copied to its place in bf16, all rows at once, and brought to fp16 there by the lanes
-      // that copied it.  (Through registers, row after row, this took 25000 cycles a segment.)
-      constexpr int LPR = D / 8, RPW = 32 / LPR, STRIDE = CONV * RPW;  // lanes of a row; rows of a warp, of all
-      const int c8 = lane % LPR, r0 = warp * RPW + lane / LPR;
-      auto place = [&](int r) {
-        return smem + L::Q + uint32_t((r >> 7) * L::Q_TILE + (c8 >> 3) * BOX + (r & 127) * 128 + (((c8 & 7) ^ (r & 7)) << 4));
-      };
-      const int tk0 = (g.qb * UNIT + r0) / p.group;
-      int hd = g.qb * UNIT + r0 - tk0 * p.group;
-      const uint16_t* from = p.q + int64_t(g.seq.row0 + tk0) * p.q_ts + int64_t(g.hk * p.group + hd) * p.q_hs + c8 * 8;
-      ok = mbar_wait(&bars->q_empty, uint32_t(i & 1) ^ 1u, abort, b.status, tmo, 11);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-#pragma unroll 2
-      for (int r = r0; r < UNIT; r += STRIDE) {
-        const bool in = g.qb * UNIT + r < rows;
-        cp_async16z(place(r), in ? from : p.q, in);
-        hd += step_hd;
-        from += q_step;
-        if (hd >= p.group) {
-          hd -= p.group;
-          from += q_wrap;
+      if (i > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->q_empty, uint32_t(i & 1) ^ 1u, abort, b.status, tmo, 11))) {
+          ok = false;
+          break;
         }
+        copy_queries<D>(p, smem + L::Q, g.seq.row0, g.hk, g.qb * UNIT, rows);
       }
+      // ... and bring them to fp16
+      constexpr int LPR = D / 8, RPW = 32 / LPR, STRIDE = CONV * RPW;  // lanes of a row; rows of a warp, of all
+      const int c8 = lane % LPR, unit_rows = min(UNIT, rows - g.qb * UNIT);
       asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
-      for (int r1 = r0; r1 < UNIT; r1 += 4 * STRIDE) {  // four rows side by side: each is a chain of shuffles
+      for (int rw = warp * RPW; rw < unit_rows; rw += 4 * STRIDE) {  // four rows side by side: each is a chain of shuffles
+        const int r1 = rw + lane / LPR;
         uint32_t u[4][4];
         float amax[4];
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
-          ld_shared_v4(place(min(r1 + a * STRIDE, UNIT - 1)), u[a][0], u[a][1], u[a][2], u[a][3]);
+          ld_shared_v4(query_place<D>(smem + L::Q, min(r1 + a * STRIDE, unit_rows - 1), c8), u[a][0], u[a][1], u[a][2], u[a][3]);
           amax[a] = 0.0f;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -781,8 +808,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             u[a][k] = pack_f16x2(__uint_as_float(u[a][k] << 16) * down, __uint_as_float(u[a][k] & 0xFFFF0000u) * down);
-          if (r < UNIT) {
-            st_shared_v4(place(r), u[a][0], u[a][1], u[a][2], u[a][3]);
+          if (r < unit_rows) {
+            st_shared_v4(query_place<D>(smem + L::Q, r, c8), u[a][0], u[a][1], u[a][2], u[a][3]);
             if (c8 == 0) sd.q_exp[i & 1][r] = int8_t(e);
           }
         }
@@ -842,12 +869,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       uint32_t kph = 0, vph = 0;
       uint32_t scount = 0, pcount = 0;  // tiles whose S, whose O += P V has been issued
       bool ok = true;
+      bool none = false;  // no rows: nothing to issue, the others' buffers are released all the same
       auto scores = [&](bool last) {
-        issue_qk<D>(q0, k0 + ks * TSTEP, s_tmem + (scount & 1) * 64, leader);
-        commit(&bars->s_full[X][scount & 1], leader);
+        if (!none) {
+          issue_qk<D>(q0, k0 + ks * TSTEP, s_tmem + (scount & 1) * 64, leader);
+          commit(&bars->s_full[X][scount & 1], leader);
+          ++scount;
+        }
         commit(&bars->k_empty[ks], leader);
         if (last) commit(&bars->q_empty, leader);
-        ++scount;
         if (++ks == KST) {
           ks = 0;
           kph ^= 1u;
@@ -858,20 +888,23 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         if (!ok) break;
         const int said = int(__reduce_max_sync(0xffffffffu, uint32_t(*reinterpret_cast<volatile int32_t*>(&sd.tiles[i & 3]))));
         const int tiles = said < 0 ? -said : said;
+        none = X == 1 && __reduce_max_sync(0xffffffffu, uint32_t(*reinterpret_cast<volatile uint8_t*>(&sd.single[i & 3]))) != 0u;
         for (int j = 0; j < min(tiles, 2) && ok; ++j) {  // two tiles' scores ahead
           if (!(ok = wait(&bars->k_full[ks], kph, 22))) break;
           tc_fence_after();
           scores(j + 1 == tiles);
         }
         for (int j = 0; j < tiles && ok; ++j) {
-          ok = wait(&bars->v_full[vs], vph, 23) && wait(&bars->p_full[X][pcount & 1], (pcount >> 1) & 1u, 24);
-          if (ok && j == 0) ok = wait(&bars->o_empty[X], uint32_t(i & 1) ^ 1u, 25);
+          ok = wait(&bars->v_full[vs], vph, 23) && (none || wait(&bars->p_full[X][pcount & 1], (pcount >> 1) & 1u, 24));
+          if (ok && j == 0 && !none) ok = wait(&bars->o_empty[X], uint32_t(i & 1) ^ 1u, 25);
           if (!ok) break;
           tc_fence_after();
-          issue_pv<D>(s_tmem + (pcount & 1) * 64, v0 + vs * TSTEP, o_tmem, j > 0, leader);
-          commit(&bars->o_done[X][pcount & 1], leader);
+          if (!none) {
+            issue_pv<D>(s_tmem + (pcount & 1) * 64, v0 + vs * TSTEP, o_tmem, j > 0, leader);
+            commit(&bars->o_done[X][pcount & 1], leader);
+            ++pcount;
+          }
           commit(&bars->v_empty[vs], leader);
-          ++pcount;
           if (++vs == VST) {
             vs = 0;
             vph ^= 1u;
@@ -899,6 +932,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     for (int i = 0;; ++i) {
       const int r = g.qb * UNIT + X * ROWS + row;
       const int rows = seq_rows(p, g.seq);
+      if (X == 1 && rows - g.qb * UNIT <= ROWS) {  // (no products are issued for it)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->o_empty[X]);
+        done += g.t1 - g.t0;
+        if (!seg_next(p, g)) break;
+        continue;
+      }
       const int lim = row_limit(p, g.seq, min(r, rows - 1));
       const int token = TREE ? g.seq.row0 + min(r, rows - 1) / p.group : 0;
       float m = -INFINITY, l = 0.0f, f = 0.0f;
@@ -973,7 +1013,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         const bool far = e != kFar;
         if (far || (again && __any_sync(0xffffffffu, fabsf(m) >= kGreat && m != -INFINITY))) {
-          const float4 r = far ? far_tile(s_addr, seen, sd.far[sc & 7], p.scale_log2, sd.q_exp[i & 1][X * ROWS + row], m, l, e)
+          const float4 r = far ? far_tile(s_addr, seen, sd.far[(done + j - g.t0) & 7], p.scale_log2, sd.q_exp[i & 1][X * ROWS + row], m, l, e)
                                : far_tile(s_addr, seen, nullptr, f, 0, m, l, 0);
           m = r.x;
           l = r.y;
@@ -1069,7 +1109,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           __stcg(mine_row + (D + 2) * ROWS, float(unit));
         }
         const int64_t t0 = sd.run0 + done - g.t0;
-        const int64_t c0 = ((t0 + 1) * sd.ctas - 1) / sd.total, c1 = ((t0 + g.nkv) * sd.ctas - 1) / sd.total;
+        const int64_t c0 = quotient((t0 + 1) * sd.ctas - 1, sd.total), c1 = quotient((t0 + g.nkv) * sd.ctas - 1, sd.total);
         __threadfence();
         ok = meet(&bars->soft[X], meets++ & 1, abort, b.status, tmo, 34);
         if (!ok) break;
@@ -1113,6 +1153,7 @@ size_t prefill_partial_bytes(int ctas, int D) { return size_t(ctas) * 2 * UNIT *
 tl_status launch_kv_prefill(PrefillParams& p, int D, int ctas, cudaStream_t st) {
   // floor(g / h) = floor(g m / 2^32), m = floor(2^32 / h) + 1, as long as g < 2^32 / h: g < 2^27, h <= 16
   const uint32_t halves = uint32_t(p.c.ps) / 16;
+  p.ctas = ctas;
   p.page_magic = halves == 1 ? 0u : uint32_t((uint64_t(1) << 32) / halves) + 1;
   void* args[] = {&p};
   auto go = [&](const void* kernel, uint32_t smem) { return launch(kernel, ctas, THREADS, smem, st, args, false); };
