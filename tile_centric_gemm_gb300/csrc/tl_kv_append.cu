@@ -209,6 +209,17 @@ __device__ __forceinline__ void square_sum(const float (&x)[8], float scale, uin
 }
 // EXACT: to about 2^-45 by a step of Newton's iteration from the reciprocal root, its residual taken exactly:
 // r (1 + d / 2 + 3 d^2 / 8), d = 1 - a r^2.
+struct Eight {
+  float x[8];
+};
+// The sum of a row's squares times 2^-160.  (What is rare is kept out of line: the blocks' three paths share the
+// instruction cache.)
+template <int D, bool EXACT>
+__device__ __noinline__ float2 small_square_sum(Eight x, uint32_t mask) {
+  float s, e;
+  square_sum<D, EXACT>(x.x, 0x1p-80f, mask, s, e);
+  return make_float2(s, e);
+}
 template <int D, bool EXACT>
 __device__ __forceinline__ Norm row_norm(const float (&x)[8], float eps) {
   constexpr uint32_t UNITS = D / 8;
@@ -218,7 +229,9 @@ __device__ __forceinline__ Norm row_norm(const float (&x)[8], float eps) {
   square_sum<D, EXACT>(x, 1.0f, mask, s, e);
   if (!(s < INFINITY)) {  // the same for all lanes of the row
     n.scale = 0x1p-80f;
-    square_sum<D, EXACT>(x, n.scale, mask, s, e);
+    const float2 small = small_square_sum<D, EXACT>(Eight{{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}}, mask);
+    s = small.x;
+    e = small.y;
     if (!(s < INFINITY)) {
       n.hi = s == INFINITY ? 0.0f : s;
       return n;
@@ -278,6 +291,67 @@ __device__ __forceinline__ void turn_normed(const AppendParams& p, const Turn& w
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = normed_dot2<EXACT>(n, a[i], w.c[i], w.first ? -b[i] : b[i], w.s[i]);
   }
+}
+
+// What a normed and rotated element is off by in fp32, relative to the sum of its two products' magnitudes: the row's factor
+// by 2^-20.7 (12 roundings of a sum of squares, halved by the root, and the root's own 2^-22), the products and their sum by
+// 2^-23, the last product by 2^-24.
+constexpr float kNormErr = 0x1p-19f;
+// Dims 8u .. 8u+7 of a row of keys, in fp32, and what each may be off by.
+template <int D>
+__device__ __forceinline__ void fast_key8(const AppendParams& p, const uint16_t* row, int u, int pos, float (&y)[8], float (&off)[8]) {
+  Turn w;
+  turn_at(p, u, pos, w);
+  float x[8], t[8], a[8], b[8];
+  load8(row + 8 * u, x);
+  load8(row + max(w.partner, 0), t);
+  const Norm n = row_norm<D, false>(x, p.eps);
+  load8(p.k_w + 8 * u, a);
+  load8(p.k_w + max(w.partner, 0), b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] *= x[i] * n.scale;
+    b[i] *= t[i] * n.scale;
+  }
+  const float err = n.hi * kNormErr;
+  auto one = [&](int i, float q, float c, float r, float s) {
+    const float m = q * c, o = r * s;
+    y[i] = (m + o) * n.hi;
+    off[i] = (fabsf(m) + fabsf(o)) * err;
+  };
+  if (w.partner < 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) one(i, a[i], 1.0f, 0.0f, 0.0f);
+  } else if (p.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      one(2 * i, a[2 * i], w.c[i], -a[2 * i + 1], w.s[i]);
+      one(2 * i + 1, a[2 * i + 1], w.c[i], a[2 * i], w.s[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) one(i, a[i], w.c[i], w.first ? -b[i] : b[i], w.s[i]);
+  }
+}
+// The same exactly, rounded to odd.
+template <int D>
+__device__ __noinline__ Eight exact_key8(const AppendParams& p, const uint16_t* row, int u, int pos) {
+  Turn w;
+  turn_at(p, u, pos, w);
+  float x[8], t[8];
+  load8(row + 8 * u, x);
+  load8(row + max(w.partner, 0), t);
+  Eight y;
+  turn_normed<true>(p, w, row_norm<D, true>(x, p.eps), x, t, *reinterpret_cast<const uint4*>(p.k_w + 8 * u),
+                    *reinterpret_cast<const uint4*>(p.k_w + max(w.partner, 0)), y.x);
+  return y;
+}
+
+// Keys that are not normed, out of line.
+__device__ __noinline__ Eight rotated_key8(const AppendParams& p, const uint16_t* row, int u, int pos) {
+  Eight y;
+  rotated8<true>(p, row, u, pos, y.x);
+  return y;
 }
 
 // How many of the f(s) given by the functor are at or below x, over the block; and in the upper bits whether any
@@ -386,11 +460,11 @@ __device__ __forceinline__ int table_row(const AppendParams& p, int t, int pos, 
 
 // TEAM threads to one (page, head, keys or values); KEEP passes' rows stay in registers.
 template <int D, int TEAM, int KEEP, bool NORM>
-__global__ void __launch_bounds__(APP_THREADS, NORM ? 5 : 8) kv_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(APP_THREADS, NORM ? 6 : 8) kv_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int UNITS = D / 8;             // threads to a row
   constexpr int STEP = TEAM / UNITS;       // rows of one pass
   __shared__ uint32_t counts[4];
-  __shared__ uint32_t team_max[4];
+  __shared__ uint32_t team_max[4], team_low[4];
   const int tid = threadIdx.x;
   const KvBatch& b = p.b;
   const int ps = p.c.ps;
@@ -413,7 +487,7 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 5 : 8) kv_append_kernel(co
     uint16_t* dst = p.q_out + int64_t(t) * p.H * D;
     // a thread has the same dims of every fourth (eighth) head or so: the tables once, four heads' loads at a time
     const int u = tid % UNITS;
-    constexpr int STRIDE = APP_THREADS / UNITS, BATCH = 4;
+    constexpr int STRIDE = APP_THREADS / UNITS, BATCH = NORM ? 2 : 4;
     Turn w;
     turn_at(p, u, pos, w);
     const bool norm = NORM && p.q_w;
@@ -489,16 +563,9 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 5 : 8) kv_append_kernel(co
     if (values) {
       load8(row + 8 * u, out);
     } else if (NORM) {
-      Turn w;
-      turn_at(p, u, table_row(p, src0 + r, lo + r, s), w);
-      float x[8], t[8];
-      load8(row + 8 * u, x);
-      load8(row + max(w.partner, 0), t);
-      if (p.k_w)
-        turn_normed<true>(p, w, row_norm<D, true>(x, p.eps), x, t, *reinterpret_cast<const uint4*>(p.k_w + 8 * u),
-                          *reinterpret_cast<const uint4*>(p.k_w + max(w.partner, 0)), out);
-      else
-        turn<true>(p, w, x, t, out);
+      const Eight y = rotated_key8(p, row, u, table_row(p, src0 + r, lo + r, s));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) out[i] = y.x[i];
     } else {
       rotated8<true>(p, row, u, lo + r, out);
     }
@@ -510,6 +577,78 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 5 : 8) kv_append_kernel(co
       if (a < 0x7F800000u) amax = max(amax, a);
     }
   };
+  auto reduce = [&]() {
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    if (TEAM > 32) {
+      if (lane_id() == 0) team_max[warp_id()] = amax;
+      __syncthreads();
+      amax = max(max(team_max[0], team_max[1]), max(team_max[2], team_max[3]));
+    } else {
+      __syncwarp();  // the scale is read by the whole team before one of it writes it
+    }
+  };
+  if (NORM && !values && p.k_w) {
+    // ---------------------------------------------------------------- normed keys
+    // A code is that of the exact value; fp32 tells it wherever what it is off by does not reach across a border between
+    // two codes.  The exact value is computed where it does (one element of some 10000), and for the block's
+    // maximum where its byte hangs on that, or where it is so large that fp32 might not hold it.
+    constexpr uint32_t ROW = (UNITS == 32 ? 0u : 1u << UNITS) - 1u;
+    const uint32_t row_lanes = ROW << (lane_id() & ~uint32_t(UNITS - 1));
+    auto row_at = [&](int r) { return src + int64_t(src0 + r) * src_ts; };
+    auto pos_of = [&](int r) { return table_row(p, src0 + r, lo + r, s); };
+    uint32_t low = 0;
+    for (int r = r0; r < rows; r += STEP) {
+      float x[8], off[8];
+      fast_key8<D>(p, row_at(r), u, pos_of(r), x, off);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        amax = max(amax, __float_as_uint(fabsf(x[i]) + off[i]) & 0x7FFFFFFFu);  // (NaN and infinity are above all)
+        low = max(low, __float_as_uint(fmaxf(fabsf(x[i]) - off[i], 0.0f)));
+      }
+    }
+    low = __reduce_max_sync(0xffffffffu, low);
+    if (TEAM > 32 && lane_id() == 0) team_low[warp_id()] = low;
+    reduce();
+    if (TEAM > 32) low = max(max(team_low[0], team_low[1]), max(team_low[2], team_low[3]));
+    if (amax >= 0x7E800000u || scale_need(amax) != scale_need(low)) {
+      if (TEAM > 32) __syncthreads();
+      amax = 0;
+      for (int r = r0; r < rows; r += STEP) {
+        const Eight x = exact_key8<D>(p, row_at(r), u, pos_of(r));
+        take_max(x.x);
+      }
+      reduce();
+    }
+    const int byte = max(old, scale_need(amax));
+    const float inv = byte == 255 ? __uint_as_float(0x00200000u) : pow2f(127 - byte);
+    if (slot0 > 0 && byte > old) {
+      const float f = pow2f(max(old - byte, -127));
+      for (int i = member; i < slot0 * (D / 16); i += TEAM) {
+        uint4* at = reinterpret_cast<uint4*>(codes + int64_t(i / (D / 16)) * p.c.token_stride + (i % (D / 16)) * 16);
+        *at = recode16(*at, f);
+      }
+    }
+    if (member == 0) *scale_at = uint8_t(byte);
+    for (int r = r0; r < rows; r += STEP) {
+      float x[8], off[8];
+      fast_key8<D>(p, row_at(r), u, pos_of(r), x, off);
+      uint32_t below[4], above[4], differ = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        below[i] = f32x2_to_e4m3x2((x[2 * i] - off[2 * i]) * inv, (x[2 * i + 1] - off[2 * i + 1]) * inv);
+        above[i] = f32x2_to_e4m3x2((x[2 * i] + off[2 * i]) * inv, (x[2 * i + 1] + off[2 * i + 1]) * inv);
+        differ |= below[i] ^ above[i];
+      }
+      if (__any_sync(row_lanes, differ != 0)) {
+        const Eight e = exact_key8<D>(p, row_at(r), u, pos_of(r));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) below[i] = f32x2_to_e4m3x2(e.x[2 * i] * inv, e.x[2 * i + 1] * inv);
+      }
+      *reinterpret_cast<uint2*>(codes + int64_t(slot0 + r) * p.c.token_stride + 8 * u) =
+          make_uint2(below[0] | below[1] << 16, below[2] | below[3] << 16);
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < KEEP; ++j) {
     const int r = r0 + j * STEP;
@@ -523,14 +662,7 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 5 : 8) kv_append_kernel(co
     row8(r, x);
     take_max(x);
   }
-  amax = __reduce_max_sync(0xffffffffu, amax);
-  if (TEAM > 32) {
-    if (lane_id() == 0) team_max[warp_id()] = amax;
-    __syncthreads();
-    amax = max(max(team_max[0], team_max[1]), max(team_max[2], team_max[3]));
-  } else {
-    __syncwarp();  // the scale is read by the whole team before one of it writes it
-  }
+  reduce();
   const int byte = max(old, scale_need(amax));
   const float inv = byte == 255 ? __uint_as_float(0x00200000u) : pow2f(127 - byte);  // 255: NaN it was and stays
   if (slot0 > 0 && byte > old) {
