@@ -1,6 +1,6 @@
-"""One decoder layer serving a ragged batch: prompts in chunks, then a token at a time.
+"""One decoder layer serving a ragged batch: prompts in chunks, then a token or a tree of drafts at a time.
 
-    python examples/serve_layer.py [--steps 32] [--check]
+    python examples/serve_layer.py [--steps 32] [--drafts 0] [--check]
 
 The layer's calls, all on one stream and all on the caller's buffers:
 
@@ -11,12 +11,23 @@ The layer's calls, all on one stream and all on the caller's buffers:
     logits = x Wr                     tl_gemm          (fp32 out)
     x += experts of the top k         tl_moe_decode    (up to 64 tokens a call)
 
-Pages are dealt out by the host as sequences grow.  --check runs the same layer in plain
+Pages are dealt out by the host as sequences grow.  With --drafts N the layer norms its
+queries and keys, pages are dealt out on the device, and each step tries a tree of N
+drafted tokens for each sequence, of which a path is kept:
+
+    pages for the drafts              tl_kv_resize
+    norm, rotate by depth, append     tl_kv_append_norm
+    each draft sees its path          tl_kv_tree_attn
+    the kept path moves together      tl_kv_compact
+    pages behind it are freed         tl_kv_resize
+
+--check runs the same layer in plain
 fp32 torch over an unquantised cache and prints how far the results are apart: the cache's
 8 bits (a relative step of 2^-4 in each key and value) are what separates them.
 """
 import argparse
 import os
+import random
 import sys
 
 import torch
@@ -50,24 +61,33 @@ class Layer:
         self.free = list(range(pages))[::-1]
         self.lens = [0] * max_seqs
 
-    def __call__(self, x, new):
-        """x [n, hidden] bf16: the new tokens of all sequences, new[s] of sequence s.  Returns x after the layer."""
-        n, H, Hkv, D = x.shape[0], self.H, self.H_kv, self.D
+    def room(self, new):
+        """Pages for new[s] more tokens of sequence s; the batch's boundaries, lengths and page table on the device."""
         for s, k in enumerate(new):
             for p in range(-(-self.lens[s] // self.page), -(-(self.lens[s] + k) // self.page)):
                 self.table[s, p] = self.free.pop()
             self.lens[s] += k
         cu = torch.tensor([0] + new, dtype=torch.int32).cumsum(0, dtype=torch.int32).cuda()
-        lens, table = torch.tensor(self.lens[:len(new)], dtype=torch.int32).cuda(), self.table[:len(new)].cuda()
+        return cu, torch.tensor(self.lens[:len(new)], dtype=torch.int32).cuda(), self.table[:len(new)].cuda()
+
+    def append(self, q, k, v, q_out, batch, most, positions):
+        B.tl_kv_append(self.cache, k, v, *batch, self.signals, q=q, q_out=q_out, cos=self.cos, sin=self.sin, max_q_len=most)
+
+    def attention(self, q, o, batch, most, tree):
+        B.tl_kv_attn(q, self.cache, o, *batch, self.ws_attn, self.signals, max_q_len=most)
+
+    def __call__(self, x, new, positions=None, tree=None):
+        """x [n, hidden] bf16: the new tokens of all sequences, new[s] of sequence s.  Returns x after the layer."""
+        n, H, Hkv, D = x.shape[0], self.H, self.H_kv, self.D
+        batch = self.room(new)
         new_bf16 = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")
         qkv = new_bf16(n, (H + 2 * Hkv) * D)
         B.tl_gemm(x, self.w_qkv, qkv, self.signals)
         heads = qkv.view(n, H + 2 * Hkv, D)
         q, o = new_bf16(n, H, D), new_bf16(n, H, D)
         most = max(new)
-        B.tl_kv_append(self.cache, heads[:, H:H + Hkv], heads[:, H + Hkv:], cu, lens, table, self.signals, q=heads[:, :H],
-                       q_out=q, cos=self.cos, sin=self.sin, max_q_len=most)
-        B.tl_kv_attn(q, self.cache, o, cu, lens, table, self.ws_attn, self.signals, max_q_len=most)
+        self.append(heads[:, :H], heads[:, H:H + Hkv], heads[:, H + Hkv:], q, batch, most, positions)
+        self.attention(q, o, batch, most, tree)
         y = new_bf16(n, self.hidden)
         B.tl_gemm(o.view(n, H * D), self.w_o, y, self.signals)
         x = x + y
@@ -86,6 +106,61 @@ class Layer:
             raise RuntimeError(f"{B.STATUS_NAMES.get(code, code)} at {where}")
 
 
+class DraftLayer(Layer):
+    """The layer with normed queries and keys, for trees of drafts; lengths and pages are the device's."""
+    eps = 1e-6
+
+    def __init__(self, seqs, **kw):
+        super().__init__(**kw)
+        g = torch.Generator(device="cuda").manual_seed(2)
+        self.q_norm, self.k_norm = ((0.5 + torch.rand(self.D, generator=g, device="cuda")).to(torch.bfloat16) for _ in range(2))
+        self.layers = B.KvLayers([self.cache])
+        self.refs = torch.zeros(len(self.free), dtype=torch.int32, device="cuda")
+        self.pages = self.table[:seqs].cuda()
+        self.d_lens = torch.zeros(seqs, dtype=torch.int32, device="cuda")
+        self.ws_pages = torch.zeros(B.tl_kv_resize_workspace_size(seqs), dtype=torch.uint8, device="cuda")
+
+    def resize(self, lens):
+        B.tl_kv_resize(self.pages, self.d_lens, lens, self.refs, self.refs, self.ws_pages, self.signals, page_size=self.page)
+        self.d_lens = lens
+
+    def room(self, new):
+        more = torch.tensor(new, dtype=torch.int32).cuda()
+        self.resize(self.d_lens + more)
+        self.cu = torch.nn.functional.pad(more.cumsum(0, dtype=torch.int32), (1, 0))
+        return self.cu, self.d_lens, self.pages
+
+    def append(self, q, k, v, q_out, batch, most, positions):
+        B.tl_kv_append_norm(self.cache, k, v, *batch, self.signals, q=q, q_out=q_out, q_weight=self.q_norm, k_weight=self.k_norm,
+                            eps=self.eps, cos=self.cos, sin=self.sin, positions=positions, max_q_len=most)
+
+    def attention(self, q, o, batch, most, tree):
+        if tree is None:
+            super().attention(q, o, batch, most, tree)
+        else:
+            B.tl_kv_tree_attn(q, self.cache, o, *batch, tree, self.ws_attn, self.signals, max_q_len=most)
+
+    def keep(self, kept, n_kept):
+        """Of each sequence's last drafts those that kept names: int32 [sequences, most] and [sequences], on the device."""
+        lens = torch.empty_like(self.d_lens)
+        B.tl_kv_compact(self.layers, kept, n_kept, self.cu, self.d_lens, self.pages, lens, self.signals)
+        self.resize(lens)
+
+
+def draft_tree(n, rng):
+    """n drafts behind parents of lower number (-1: behind the last token): their masks as words, depths, and a path."""
+    words, depth, paths = [], [], []
+    for i in range(n):
+        p = rng.randrange(-1, i)
+        paths.append((paths[p] if p >= 0 else []) + [i])
+        depth.append(len(paths[i]) - 1)
+        row = [0] * -(-n // 32)
+        for j in paths[i]:
+            row[j // 32] |= 1 << j % 32
+        words.append([w - (1 << 32) if w >> 31 else w for w in row])
+    return words, depth, rng.choice(paths)
+
+
 class Plain:
     """The same layer in fp32 torch, keys and values kept as they are."""
 
@@ -99,6 +174,9 @@ class Plain:
     def __call__(self, x, new):
         l, x = self.l, x.float()
         qkv = (x @ l.w_qkv.float()).view(-1, l.H + 2 * l.H_kv, l.D)
+        if isinstance(l, DraftLayer):
+            norm = lambda t, w: t * (t.square().mean(-1, keepdim=True) + l.eps).rsqrt() * w.float()
+            qkv = torch.cat([norm(qkv[:, :l.H], l.q_norm), norm(qkv[:, l.H:l.H + l.H_kv], l.k_norm), qkv[:, l.H + l.H_kv:]], 1)
         out, at = [], 0
         for s, n in enumerate(new):
             q, k, v = qkv[at:at + n, :l.H], qkv[at:at + n, l.H:l.H + l.H_kv], qkv[at:at + n, l.H + l.H_kv:]
@@ -125,16 +203,32 @@ class Plain:
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=32)
+    ap.add_argument("--drafts", type=int, default=0, help="drafted tokens of a sequence in each step (0: none)")
     ap.add_argument("--check", action="store_true")
     a = ap.parse_args(argv)
-    layer = Layer()
+    layer = DraftLayer(4) if a.drafts else Layer()
     plain = Plain(layer) if a.check else None
     g = torch.Generator(device="cuda").manual_seed(1)
-    batches = [[100, 3, 257, 0], [60, 90, 1, 130]] + [[1, 1, 1, 1]] * a.steps  # two rounds of chunks, then tokens
+    rng = random.Random(1)
+    batches = [[100, 3, 257, 0], [60, 90, 1, 130]] + [[a.drafts or 1] * 4] * a.steps  # two rounds of chunks, then steps
+    lens = [0] * 4
     worst = 0.0
-    for new in batches:
+    for step, new in enumerate(batches):
         x = torch.randn(sum(new), layer.hidden, generator=g, device="cuda").to(torch.bfloat16)
-        y = layer(x, new)
+        if a.drafts and step >= 2:
+            trees = [draft_tree(a.drafts, rng) for _ in new]
+            positions = torch.tensor([n + d for n, (_, depth, _) in zip(lens, trees) for d in depth], dtype=torch.int32)
+            masks = torch.tensor([w for words, _, _ in trees for w in words], dtype=torch.int32)
+            y = layer(x, new, positions.cuda(), masks.cuda())
+            paths = [path for _, _, path in trees]
+            new = [len(p) for p in paths]
+            layer.keep(torch.tensor([p + [0] * (a.drafts - len(p)) for p in paths], dtype=torch.int32).cuda(),
+                       torch.tensor(new, dtype=torch.int32).cuda())
+            rows = torch.tensor([s * a.drafts + i for s, p in enumerate(paths) for i in p]).cuda()
+            x, y = x[rows], y[rows]  # what goes on
+        else:
+            y = layer(x, new)
+        lens = [n + k for n, k in zip(lens, new)]
         if plain:
             want, logits = plain(x, new)
             # where two experts' logits are closer than the cache's steps move them, another may be chosen: left out
@@ -143,7 +237,7 @@ def main(argv=None):
             if clear.any():
                 worst = max(worst, float(((y.float() - want)[clear].norm(dim=1) / want[clear].norm(dim=1)).max()))
     layer.status()
-    print(f"{len(batches)} calls, lengths {layer.lens[:4]}" + (f", worst relative distance {worst:.4f}" if plain else ""))
+    print(f"{len(batches)} calls, lengths {lens}" + (f", worst relative distance {worst:.4f}" if plain else ""))
     return worst
 
 

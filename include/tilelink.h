@@ -689,7 +689,8 @@ tl_status tl_kv_append(const tl_kv_append_args* args, void* stream);
  * at positions[t] for new token t where positions are given: tokens of a drafted tree
  * rotate by their depth, not by their slot.  All else is as for tl_kv_append: the slots,
  * the scales, and each key's code, which is the exact normed and rotated value (to
- * 2^-40 of it) rounded once.  Queries are computed in fp32 and rounded once to bf16.
+ * 2^-40 of it, or to 2^-127 where that is more: weights below 2^-80) rounded once.
+ * Queries are computed in fp32 and rounded once to bf16.
  * A row with an infinite element has 0 in its finite ones and NaN in the others; one
  * with a NaN is NaN.  A position outside 0..max_pos-1 records TL_ERR_INVALID with the
  * sequence number, and that token is undefined.
@@ -906,11 +907,12 @@ tl_status tl_kv_compact(const tl_kv_compact_args* args, void* stream);
  *   parents[u, n] = u * K + k (as tl_kv_fork takes them),  tokens[u, n] = v,
  *   scores_out[u, n] = score(k, v)
  * Scores are compared in pairs of fp32 (48 bits; the sum of exponentials is good to
- * 2^-19 at worst, where they are many to about 2^-26) and returned in fp32.  Only finite scores count: tokens whose logit is -infinity, beams whose score is not
- * finite, and beams whose lse is not (all logits -infinity, or one NaN or +infinity) offer
- * nothing.  A beam whose done is not 0 has ended: its logits are not read, its lse is 0, and it offers one
- * continuation, token eos at its own score.  Where fewer than N are offered the places
- * left have parent -1, token -1 and score -infinity.
+ * 2^-19 at worst, where they are many to about 2^-26) and returned in fp32.  Only finite
+ * scores count: tokens whose logit is -infinity, beams whose score is not finite, and
+ * beams whose lse is not (all logits -infinity, or one NaN or +infinity) offer nothing.
+ * A beam whose done is not 0 has ended: its logits are not read, its lse is 0, and it
+ * offers one continuation, token eos at its own score.  Where fewer than N are offered
+ * the places left have parent -1, token -1 and score -infinity.
  * done_out[u, n] = 1 where the parent had ended, the token is eos, or nothing was
  * offered.  With history: row u * N + n of history_out = the first `length` entries of the
  * parent's row, then the token (rows of places left over are not written, nor entries

@@ -15,11 +15,15 @@
 // instead, 512 beams of 50001 took 31 us: a block's list cost it as much time as its logits.)
 // Where more reach the bound than the list holds (plateaus), rows are taken apart value by value.
 //
-// Beams are compared by scores in pairs of fp32 (48 bits), and sums of exponentials are pairs too, so that
-// what decides between two beams is not lost beside scores of -20.  (64-bit arithmetic took 5000 of the
-// joining block's cycles: a warp's instruction holds its unit for 16.)
+// Beams are compared by scores in pairs of fp32 (48 bits), and a row's sum of exponentials is joined in pairs
+// too, so that what decides between two beams is not lost beside scores of -20.  (64-bit arithmetic took 5000
+// of the joining block's cycles: a warp's instruction holds its unit for 16.)
 //
-// Bound by memory for many beams and by latency for few.
+// Bound by memory for many beams and by latency for few.  512 beams of 50001 in fp32, a sixth of them ended, 16
+// continuations to each 8: 25.3 us in a graph for 86 MB; the stream alone takes 16.9 (5.1 TB/s, 75 % of a copy's rate),
+// the users' joins 8.4 behind it, one block to each.  (Smaller parts, so that users end one after the other
+// and joins run beside the stream: 27.8 us with 2 of them to a row, 31.9 with 3.)  4 beams of 32000 in bf16: 9.9 us, 6.8 of
+// them the join: a dozen barriers and two trips to L2 and memory.
 #include <algorithm>
 #include <cmath>
 
