@@ -110,6 +110,29 @@ def test_rows_of_any_magnitude(B, scale):
     c.check()
 
 
+@pytest.mark.parametrize("weight", [2.0 ** -70, 2.0 ** 62, 2.0 ** -30])
+def test_weights_of_any_magnitude(B, weight):
+    """Scale bytes next to both ends."""
+    b = Batch([40, 3], [40, 20], seed=13, H=4, Hkv=2, D=128, ps=16)
+    w = (b.bf16(128).float() * weight).to(torch.bfloat16)
+    c = Case(B, b, rot=128, weights=(w, w))
+    c.call()
+    c.check()
+
+
+@pytest.mark.parametrize("rot,interleaved", [(128, False), (96, True), (48, False)])
+def test_many_heads_and_rows_to_a_page(B, rot, interleaved):
+    """More heads than a block takes at a time, and more rows of a page than its threads hold."""
+    def edit(rows):
+        rows[100, -3:, 5] = float("inf")
+        rows[300, -2:, 77] = float("nan")
+        rows[400, -1:, 8:16] = -float("inf")
+    b = Batch([512, 1, 90], [700, 130, 90], seed=14, H=40, Hkv=8, D=128, ps=256)
+    c = Case(B, b, rot=rot, interleaved=interleaved, edit=edit)
+    c.call()
+    c.check()
+
+
 def test_rows_of_zeros_infinities_and_nan(B):
     def edit(rows):
         rows[2] = 0.0

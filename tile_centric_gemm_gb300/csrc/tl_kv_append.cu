@@ -34,16 +34,17 @@
 // written, issue slots 65 % busy.
 //
 // tl_kv_append_norm is the same kernel with norms, x w / sqrt(mean x^2 + eps), and positions
-// of its own.  The exact normed value costs two to three times the instructions (a sum of squares in
+// of its own.  The exact normed value costs ten times the instructions (a sum of squares in
 // pairs, a Newton step for the root, products in pairs), and a code needs it only next to
 // a border, so keys are computed in fp32 with a bound on what they are off by; where both
-// ends of the bound have one code that is the code, else (one element of some 10000) the row
-// is computed exactly, out of line.  8192 tokens as above: 76 us (96 all exact), of which keys and
-// values take 47 and queries 20 at the memory's rate; 32 trees of up to 60 drafts behind 2000:
-// 22 us (31).  A page's block is a chain of two passes over its rows, 14 us for 64 rows even
-// when it is alone, and six blocks of 128 threads (72 registers) share an SM.  Rows kept
-// in shared memory, tables or values fetched ahead, queries' blocks of several tokens and
-// their blocks between those of the keys were measured: 75 to 90 us.
+// ends of the bound have one code that is the code, else (one element of some 20000) the row
+// is computed exactly, out of line.  Queries and keys have both elements of a rotated pair in one thread
+// (77 -> 64 us for 8192 tokens as above), values stay in registers between maximum and write (61 -> 59), and so 8192
+// tokens take 55 us (96 all exact), 3.4 TB/s, the queries 33 of them alone, keys 31 and values 10; 32 trees of
+// up to 60 drafts behind 2000: 20 us.  Bound by the issue of instructions and the chains of a
+// block of queries (position, tables) and of keys (two passes over the rows, the exact rows); six
+// blocks of 128 threads (80 registers) share an SM (5: 56 us, 7: 64).  Rows kept in shared memory, tables fetched ahead,
+// blocks of several tokens' queries or between those of the keys were slower.
 #include <algorithm>
 #include <type_traits>
 
@@ -190,24 +191,30 @@ __device__ __forceinline__ void two_sum(float a, float b, float& sum, float& err
   const float back = __fsub_rn(sum, a);
   err = __fadd_rn(__fsub_rn(a, __fsub_rn(sum, back)), __fsub_rn(b, back));
 }
-// The sum of squares over the D dims of a row that UNITS neighbouring lanes hold: squares of bf16 are exact in fp32, sums
-// are pairs.  Below 2^-63 squares lose bits, which eps (1e-12 at least) makes up for.
-template <int D, bool EXACT>
-__device__ __forceinline__ void square_sum(const float (&x)[8], float scale, uint32_t mask, float& s, float& e) {
+// The sum of squares over the D dims of a row that neighbouring lanes hold, N of them each: squares of bf16 are exact in
+// fp32, sums are pairs.  Below 2^-63 squares lose bits, which eps (1e-12 at least) makes up for.
+template <int D, int N, bool EXACT>
+__device__ __forceinline__ void square_sum(const float (&x)[N], float scale, uint32_t mask, float& s, float& e) {
   s = e = 0.0f;
+  if (EXACT) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = x[i] * scale;
-    if (EXACT) {
+    for (int i = 0; i < N; ++i) {
+      const float v = x[i] * scale;
       float d;
       two_sum(s, __fmul_rn(v, v), s, d);
       e += d;
-    } else {
-      s = fmaf(v, v, s);
     }
+  } else {
+    float q[N / 8];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float v = x[i] * scale;
+      q[i / 8] = fmaf(v, v, i % 8 ? q[i / 8] : 0.0f);
+    }
+    s = q[0] + (N > 8 ? q[N / 8 - 1] : 0.0f);
   }
 #pragma unroll
-  for (int d = 1; d < D / 8; d <<= 1) {
+  for (int d = 1; d < D / N; d <<= 1) {
     const float s2 = __shfl_xor_sync(mask, s, d);
     if (EXACT) {
       const float e2 = __shfl_xor_sync(mask, e, d);
@@ -219,29 +226,39 @@ __device__ __forceinline__ void square_sum(const float (&x)[8], float scale, uin
     }
   }
 }
-// EXACT: to about 2^-45 by a step of Newton's iteration from the reciprocal root, its residual taken exactly:
-// r (1 + d / 2 + 3 d^2 / 8), d = 1 - a r^2.
-struct Eight {
-  float x[8];
+template <int N>
+struct Some {
+  float x[N];
 };
+using Eight = Some<8>;
 // The sum of a row's squares times 2^-160.  (What is rare is kept out of line: the blocks' three paths share the
 // instruction cache.)
-template <int D, bool EXACT>
-__device__ __noinline__ float2 small_square_sum(Eight x, uint32_t mask) {
+template <int D, int N, bool EXACT>
+__device__ __noinline__ float2 small_square_sum(Some<N> x, uint32_t mask) {
   float s, e;
-  square_sum<D, EXACT>(x.x, 0x1p-80f, mask, s, e);
+  square_sum<D, N, EXACT>(x.x, 0x1p-80f, mask, s, e);
   return make_float2(s, e);
 }
-template <int D, bool EXACT>
-__device__ __forceinline__ Norm row_norm(const float (&x)[8], float eps) {
-  constexpr uint32_t UNITS = D / 8;
-  const uint32_t mask = ((1u << UNITS) - 1u) << (lane_id() & ~(UNITS - 1u));
+// The lanes that hold a row, N dims each.
+template <int D, int N>
+__device__ __forceinline__ uint32_t row_lanes() {
+  constexpr uint32_t LANES = D / N;
+  return ((1u << LANES) - 1u) << (lane_id() & ~(LANES - 1u));
+}
+// EXACT: to about 2^-45 by a step of Newton's iteration from the reciprocal root, its residual taken exactly:
+// r (1 + d / 2 + 3 d^2 / 8), d = 1 - a r^2.
+template <int D, bool EXACT, int N>
+__device__ __forceinline__ Norm row_norm(const float (&x)[N], float eps) {
+  const uint32_t mask = row_lanes<D, N>();
   Norm n{0.0f, 0.0f, 1.0f};
   float s, e;
-  square_sum<D, EXACT>(x, 1.0f, mask, s, e);
+  square_sum<D, N, EXACT>(x, 1.0f, mask, s, e);
   if (!(s < INFINITY)) {  // the same for all lanes of the row
     n.scale = 0x1p-80f;
-    const float2 small = small_square_sum<D, EXACT>(Eight{{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}}, mask);
+    Some<N> all;
+#pragma unroll
+    for (int i = 0; i < N; ++i) all.x[i] = x[i];
+    const float2 small = small_square_sum<D, N, EXACT>(all, mask);
     s = small.x;
     e = small.y;
     if (!(s < INFINITY)) {
@@ -306,57 +323,199 @@ __device__ __forceinline__ void turn_normed(const AppendParams& p, const Turn& w
 }
 
 // What a normed and rotated element is off by in fp32, relative to the sum of its two products' magnitudes: the row's factor
-// by 2^-20.7 (12 roundings of a sum of squares, halved by the root, and the root's own 2^-22), the products and their sum by
-// 2^-23, the last product by 2^-24.
-constexpr float kNormErr = 0x1p-19f;
-// Dims 8u .. 8u+7 of a row of keys, in fp32, and what each may be off by.
-template <int D>
-__device__ __forceinline__ void fast_key8(const AppendParams& p, const uint16_t* row, int u, int pos, float (&y)[8], float (&off)[8]) {
-  Turn w;
-  turn_at(p, u, pos, w);
-  float x[8], t[8], a[8], b[8];
-  load8(row + 8 * u, x);
-  load8(row + max(w.partner, 0), t);
-  const Norm n = row_norm<D, false>(x, p.eps);
-  load8(p.k_w + 8 * u, a);
-  load8(p.k_w + max(w.partner, 0), b);
+// by 10 steps of 2^-24 (12 roundings of a mean of squares, halved by the root, and the root's own 4), the products and their
+// sum by one each, the product with the factor and the bound's end by one each: 14, and 16 leave room for what these do to
+// one another.
+constexpr float kNormErr = 0x1p-20f;
+// A thread's 16 dims of a row of keys: two units of 8 whose dims are each other's partners, so that a row and the tables
+// are read once, and every product of an element and its weight serves two outputs.
+struct Pair {
+  int first, second;  // units
+  int table;          // first of 8 entries of a table's row; below 0: not rotated
+};
+__device__ __forceinline__ Pair pair_of(const AppendParams& p, int m) {
+  const int turned = p.rot >> 4;
+  if (m >= turned) return {2 * m, 2 * m + 1, -1};
+  return p.interleaved ? Pair{2 * m, 2 * m + 1, 8 * m} : Pair{m, m + turned, 8 * m};
+}
+__device__ __forceinline__ void unpack_pair(uint4 a, uint4 b, float (&x)[16]) {
+  float u[8], v[8];
+  unpack8(a, u);
+  unpack8(b, v);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    a[i] *= x[i] * n.scale;
-    b[i] *= t[i] * n.scale;
+    x[i] = u[i];
+    x[8 + i] = v[i];
   }
-  const float err = n.hi * kNormErr;
-  auto one = [&](int i, float q, float c, float r, float s) {
-    const float m = q * c, o = r * s;
-    y[i] = (m + o) * n.hi;
-    off[i] = (fabsf(m) + fabsf(o)) * err;
-  };
-  if (w.partner < 0) {
+}
+struct PairRow {
+  uint4 a, b;
+};
+__device__ __forceinline__ PairRow raw_pair(const uint16_t* row, const Pair& m) {
+  return {*reinterpret_cast<const uint4*>(row + 8 * m.first), *reinterpret_cast<const uint4*>(row + 8 * m.second)};
+}
+__device__ __forceinline__ void load_pair(const uint16_t* row, const Pair& m, float (&x)[16]) {
+  const PairRow r = raw_pair(row, m);
+  unpack_pair(r.a, r.b, x);
+}
+__device__ __forceinline__ void load_tables(const AppendParams& p, const Pair& m, int pos, float (&c)[8], float (&s)[8]) {
+  if (m.table < 0) return;
+  const int64_t at = int64_t(pos) * (p.rot >> 1) + m.table;
+  load4(p.cos + at, c);
+  load4(p.cos + at + 4, c + 4);
+  load4(p.sin + at, s);
+  load4(p.sin + at + 4, s + 4);
+}
+// Sixteen elements in fp32 but for the row's factor, and their products' magnitudes added up, in pairs of neighbours:
+// use(factor, i, y of 2 i, of 2 i + 1, z of both).
+template <int D, class Use>
+__device__ __forceinline__ void fast_key16(const AppendParams& p, const PairRow& row, const Pair& m, int pos, Use use) {
+  float c[8], s[8], x[16], w[16];
+  load_tables(p, m, pos, c, s);
+  unpack_pair(row.a, row.b, x);
+  const Norm n = row_norm<D, false>(x, p.eps);
+  if (n.scale != 1.0f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) one(i, a[i], 1.0f, 0.0f, 0.0f);
+    for (int i = 0; i < 16; ++i) x[i] *= n.scale;
+  }
+  load_pair(p.k_w, m, w);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] *= w[i];
+  auto turn = [&](int a, int b, int j, float& ya, float& yb, float& za, float& zb) {
+    const float ac = x[a] * c[j], bs = x[b] * s[j], bc = x[b] * c[j], as = x[a] * s[j];
+    ya = ac - bs;
+    za = fabsf(ac) + fabsf(bs);
+    yb = bc + as;
+    zb = fabsf(bc) + fabsf(as);
+  };
+  if (m.table < 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) use(n.hi, i, x[2 * i], x[2 * i + 1], fabsf(x[2 * i]), fabsf(x[2 * i + 1]));
   } else if (p.interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      one(2 * i, a[2 * i], w.c[i], -a[2 * i + 1], w.s[i]);
-      one(2 * i + 1, a[2 * i + 1], w.c[i], a[2 * i], w.s[i]);
+    for (int j = 0; j < 8; ++j) {
+      float y0, y1, z0, z1;
+      turn(2 * j, 2 * j + 1, j, y0, y1, z0, z1);
+      use(n.hi, j, y0, y1, z0, z1);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) one(i, a[i], w.c[i], w.first ? -b[i] : b[i], w.s[i]);
+    for (int j = 0; j < 4; ++j) {
+      float a0, a1, b0, b1, za0, za1, zb0, zb1;
+      turn(2 * j, 8 + 2 * j, 2 * j, a0, b0, za0, zb0);
+      turn(2 * j + 1, 9 + 2 * j, 2 * j + 1, a1, b1, za1, zb1);
+      use(n.hi, j, a0, a1, za0, za1);
+      use(n.hi, 4 + j, b0, b1, zb0, zb1);
+    }
   }
 }
 // The same exactly, rounded to odd.
 template <int D>
-__device__ __noinline__ Eight exact_key8(const AppendParams& p, const uint16_t* row, int u, int pos) {
+__device__ __noinline__ Some<16> exact_key16(const AppendParams& p, const uint16_t* row, Pair m, int pos) {
+  float x[16], a[8], b[8];
+  load_pair(row, m, x);
+  const Norm n = row_norm<D, true>(x, p.eps);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = x[i];
+    b[i] = x[8 + i];
+  }
+  const uint4 wa = *reinterpret_cast<const uint4*>(p.k_w + 8 * m.first), wb = *reinterpret_cast<const uint4*>(p.k_w + 8 * m.second);
+  const bool own = m.table < 0 || p.interleaved;  // no partners among the other unit
+  Some<16> out;
+  float y[8];
   Turn w;
-  turn_at(p, u, pos, w);
-  float x[8], t[8];
-  load8(row + 8 * u, x);
-  load8(row + max(w.partner, 0), t);
-  Eight y;
-  turn_normed<true>(p, w, row_norm<D, true>(x, p.eps), x, t, *reinterpret_cast<const uint4*>(p.k_w + 8 * u),
-                    *reinterpret_cast<const uint4*>(p.k_w + max(w.partner, 0)), y.x);
-  return y;
+  turn_at(p, m.first, pos, w);
+  turn_normed<true>(p, w, n, a, own ? a : b, wa, own ? wa : wb, y);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) out.x[i] = y[i];
+  turn_at(p, m.second, pos, w);
+  turn_normed<true>(p, w, n, b, own ? b : a, wb, own ? wb : wa, y);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) out.x[8 + i] = y[i];
+  return out;
+}
+
+// A token's queries by the block: a thread has the same dims of every 16th (32nd) head, the tables and weights once, two
+// heads' loads at a time, the first ones before the block knows the token's position (8192 tokens: 64 -> 61 us).
+struct Nothing {
+  __device__ __forceinline__ Nothing(const AppendParams&, int) {}
+};
+template <int D>
+struct Queries {
+  static constexpr int PAIRS = D / 16, STRIDE = APP_THREADS / PAIRS, BATCH = 2;
+  Pair m;
+  const uint16_t* row;
+  int h0;
+  uint4 xa[BATCH], xb[BATCH];
+
+  __device__ __forceinline__ Queries(const AppendParams& p, int t) : m(pair_of(p, int(threadIdx.x) % PAIRS)),
+        row(p.q + int64_t(t) * p.q_ts), h0(int(threadIdx.x) / PAIRS) {
+    load(p);
+  }
+  __device__ __forceinline__ void load(const AppendParams& p) {
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const uint16_t* head = row + min(h0 + k * STRIDE, p.H - 1) * p.q_hs;
+      xa[k] = *reinterpret_cast<const uint4*>(head + 8 * m.first);
+      xb[k] = *reinterpret_cast<const uint4*>(head + 8 * m.second);
+    }
+  }
+  __device__ __forceinline__ void store(const AppendParams& p, uint16_t* dst, int pos);
+};
+template <int D>
+__device__ __forceinline__ void Queries<D>::store(const AppendParams& p, uint16_t* dst, int pos) {
+  float c[8], s[8];
+  load_tables(p, m, pos, c, s);
+  const bool norm = p.q_w;
+  uint4 wa = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), wb = wa;  // ones
+  if (norm) {
+    wa = *reinterpret_cast<const uint4*>(p.q_w + 8 * m.first);
+    wb = *reinterpret_cast<const uint4*>(p.q_w + 8 * m.second);
+  }
+  while (h0 < p.H) {
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int h = h0 + k * STRIDE;
+      if (h >= p.H) break;
+      float x[16], w[16];
+      unpack_pair(xa[k], xb[k], x);
+      float f = 1.0f;
+      if (norm) {
+        const Norm n = row_norm<D, false>(x, p.eps);
+        f = n.hi;
+        if (n.scale != 1.0f) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] *= n.scale;
+        }
+      }
+      unpack_pair(wa, wb, w);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= w[i];
+      auto turn = [&](int a, int b, int j) {
+        const float ya = fmaf(x[a], c[j], -x[b] * s[j]), yb = fmaf(x[b], c[j], x[a] * s[j]);
+        x[a] = ya;
+        x[b] = yb;
+      };
+      if (m.table >= 0) {
+        if (p.interleaved) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) turn(2 * j, 2 * j + 1, j);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) turn(j, 8 + j, j);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= f;
+      uint16_t* to = dst + h * D;
+      st_global_v4(to + 8 * m.first, pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+      st_global_v4(to + 8 * m.second, pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]),
+                   pack_bf16x2(x[14], x[15]));
+    }
+    h0 += STRIDE * BATCH;
+    if (h0 < p.H) load(p);
+  }
 }
 
 // Keys that are not normed, out of line.
@@ -484,6 +643,7 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 6 : 8) kv_append_kernel(co
   if (int(blockIdx.x) >= p.kv_blocks) {
     // ---------------------------------------------------------------- one token's queries
     const int t = int(blockIdx.x) - p.kv_blocks;
+    std::conditional_t<NORM, Queries<D>, Nothing> queries(p, t);
     const uint32_t n = count_below(b, t, counts, [](int, int c0) { return c0; });
     const int s = n < kOutOfOrder ? int(n) - 1 : find_among_wrong<false>(b, ps, t).x;
     if (s < 0) return;
@@ -497,17 +657,15 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 6 : 8) kv_append_kernel(co
     }
     const uint16_t* row = p.q + int64_t(t) * p.q_ts;
     uint16_t* dst = p.q_out + int64_t(t) * p.H * D;
+    if constexpr (NORM) {
+      queries.store(p, dst, pos);
+      return;
+    }
     // a thread has the same dims of every fourth (eighth) head or so: the tables once, four heads' loads at a time
     const int u = tid % UNITS;
-    constexpr int STRIDE = APP_THREADS / UNITS, BATCH = NORM ? 2 : 4;
+    constexpr int STRIDE = APP_THREADS / UNITS, BATCH = 4;
     Turn w;
     turn_at(p, u, pos, w);
-    const bool norm = NORM && p.q_w;
-    uint4 wx = make_uint4(0, 0, 0, 0), wt = wx;
-    if (norm) {
-      wx = *reinterpret_cast<const uint4*>(p.q_w + 8 * u);
-      wt = *reinterpret_cast<const uint4*>(p.q_w + max(w.partner, 0));
-    }
     for (int h0 = tid / UNITS; h0 < p.H; h0 += STRIDE * BATCH) {
       uint4 x[BATCH], t4[BATCH];
 #pragma unroll
@@ -523,8 +681,7 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 6 : 8) kv_append_kernel(co
         float a[8], b8[8], y[8];
         unpack8(x[k], a);
         unpack8(t4[k], b8);
-        if (norm) turn_normed<false>(p, w, row_norm<D, false>(a, p.eps), a, b8, wx, wt, y);
-        else turn<false>(p, w, a, b8, y);
+        turn<false>(p, w, a, b8, y);
         st_global_v4(dst + h * D + 8 * u, pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                      pack_bf16x2(y[6], y[7]));
       }
@@ -582,9 +739,9 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 6 : 8) kv_append_kernel(co
       rotated8<true>(p, row, u, lo + r, out);
     }
   };
-  auto take_max = [&](const float(&x)[8]) {
+  auto take_max = [&](const auto& x) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < int(sizeof(x) / sizeof(float)); ++i) {
       const uint32_t a = __float_as_uint(x[i]) & 0x7FFFFFFFu;
       if (a < 0x7F800000u) amax = max(amax, a);
     }
@@ -599,40 +756,8 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 6 : 8) kv_append_kernel(co
       __syncwarp();  // the scale is read by the whole team before one of it writes it
     }
   };
-  if (NORM && !values && p.k_w) {
-    // ---------------------------------------------------------------- normed keys
-    // A code is that of the exact value; fp32 tells it wherever what it is off by does not reach across a border between
-    // two codes.  The exact value is computed where it does (one element of some 10000), and for the block's
-    // maximum where its byte hangs on that, or where it is so large that fp32 might not hold it.
-    constexpr uint32_t ROW = (UNITS == 32 ? 0u : 1u << UNITS) - 1u;
-    const uint32_t row_lanes = ROW << (lane_id() & ~uint32_t(UNITS - 1));
-    auto row_at = [&](int r) { return src + int64_t(src0 + r) * src_ts; };
-    auto pos_of = [&](int r) { return table_row(p, src0 + r, lo + r, s); };
-    uint32_t low = 0;
-    for (int r = r0; r < rows; r += STEP) {
-      float x[8], off[8];
-      fast_key8<D>(p, row_at(r), u, pos_of(r), x, off);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        amax = max(amax, __float_as_uint(fabsf(x[i]) + off[i]) & 0x7FFFFFFFu);  // (NaN and infinity are above all)
-        low = max(low, __float_as_uint(fmaxf(fabsf(x[i]) - off[i], 0.0f)));
-      }
-    }
-    low = __reduce_max_sync(0xffffffffu, low);
-    if (TEAM > 32 && lane_id() == 0) team_low[warp_id()] = low;
-    reduce();
-    if (TEAM > 32) low = max(max(team_low[0], team_low[1]), max(team_low[2], team_low[3]));
-    if (amax >= 0x7E800000u || scale_need(amax) != scale_need(low)) {
-      if (TEAM > 32) __syncthreads();
-      amax = 0;
-      for (int r = r0; r < rows; r += STEP) {
-        const Eight x = exact_key8<D>(p, row_at(r), u, pos_of(r));
-        take_max(x.x);
-      }
-      reduce();
-    }
-    const int byte = max(old, scale_need(amax));
-    const float inv = byte == 255 ? __uint_as_float(0x00200000u) : pow2f(127 - byte);
+  // The older rows to the new scale, and the scale.
+  auto settle = [&](int byte) {
     if (slot0 > 0 && byte > old) {
       const float f = pow2f(max(old - byte, -127));
       for (int i = member; i < slot0 * (D / 16); i += TEAM) {
@@ -641,23 +766,111 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 6 : 8) kv_append_kernel(co
       }
     }
     if (member == 0) *scale_at = uint8_t(byte);
-    for (int r = r0; r < rows; r += STEP) {
-      float x[8], off[8];
-      fast_key8<D>(p, row_at(r), u, pos_of(r), x, off);
-      uint32_t below[4], above[4], differ = 0;
+  };
+  if (NORM && values) {
+    // ---------------------------------------------------------------- values
+    // A thread's first rows stay in registers, all on their way at once.
+    constexpr int HOLD = 8;
+    const uint16_t* from = src + int64_t(src0 + r0) * src_ts + 8 * u;
+    auto load = [&](int k) { return *reinterpret_cast<const uint4*>(from + int64_t(k) * STEP * src_ts); };
+    auto here = [&](int k) { return r0 + k * STEP < rows; };
+    uint4 v[HOLD];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        below[i] = f32x2_to_e4m3x2((x[2 * i] - off[2 * i]) * inv, (x[2 * i + 1] - off[2 * i + 1]) * inv);
-        above[i] = f32x2_to_e4m3x2((x[2 * i] + off[2 * i]) * inv, (x[2 * i + 1] + off[2 * i + 1]) * inv);
-        differ |= below[i] ^ above[i];
-      }
-      if (__any_sync(row_lanes, differ != 0)) {
-        const Eight e = exact_key8<D>(p, row_at(r), u, pos_of(r));
+    for (int k = 0; k < HOLD; ++k) v[k] = here(k) ? load(k) : make_uint4(0, 0, 0, 0);
+    uint32_t most = 0;  // of the halves, without their signs
+    auto look = [&](const uint4& x) {
+      most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+    };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) below[i] = f32x2_to_e4m3x2(e.x[2 * i] * inv, e.x[2 * i + 1] * inv);
+    for (int k = 0; k < HOLD; ++k) look(v[k]);
+    for (int k = HOLD; here(k); ++k) look(load(k));
+    amax = max(most << 16, most & 0xFFFF0000u);
+    if (amax >= 0x7F800000u) {  // (infinities and NaN do not count)
+      amax = 0;
+      for (int k = 0; here(k); ++k) {
+        float x[8];
+        unpack8(load(k), x);
+        take_max(x);
       }
-      *reinterpret_cast<uint2*>(codes + int64_t(slot0 + r) * p.c.token_stride + 8 * u) =
-          make_uint2(below[0] | below[1] << 16, below[2] | below[3] << 16);
+    }
+    reduce();
+    const int byte = max(old, scale_need(amax));
+    const float inv = byte == 255 ? __uint_as_float(0x00200000u) : pow2f(127 - byte);
+    settle(byte);
+    uint8_t* to = codes + int64_t(slot0 + r0) * p.c.token_stride + 8 * u;
+    auto write = [&](int k, const uint4& w) {
+      float x[8];
+      unpack8(w, x);
+      *reinterpret_cast<uint2*>(to + int64_t(k) * STEP * p.c.token_stride) =
+          make_uint2(f32x2_to_e4m3x2(x[0] * inv, x[1] * inv) | (f32x2_to_e4m3x2(x[2] * inv, x[3] * inv) << 16),
+                     f32x2_to_e4m3x2(x[4] * inv, x[5] * inv) | (f32x2_to_e4m3x2(x[6] * inv, x[7] * inv) << 16));
+    };
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k)
+      if (here(k)) write(k, v[k]);
+    for (int k = HOLD; here(k); ++k) write(k, load(k));
+    return;
+  }
+  if (NORM && !values && p.k_w) {
+    // ---------------------------------------------------------------- normed keys
+    // A code is that of the exact value; fp32 tells it wherever what it is off by does not reach across a border between
+    // two codes.  The exact value is computed where it does (one element of some 10000), and for the block's
+    // maximum where its byte hangs on that, or where it is so large that fp32 might not hold it.
+    constexpr int PAIRS = D / 16, ROWS = TEAM / PAIRS;  // threads of a row; rows of a pass
+    const Pair m = pair_of(p, member % PAIRS);
+    auto row_at = [&](int r) { return src + int64_t(src0 + r) * src_ts; };
+    auto pos_of = [&](int r) { return table_row(p, src0 + r, lo + r, s); };
+    uint32_t low = 0;
+    PairRow next = raw_pair(row_at(min(member / PAIRS, rows - 1)), m);
+    for (int r = member / PAIRS; r < rows; r += ROWS) {
+      const PairRow row = next;
+      next = raw_pair(row_at(r + ROWS < rows ? r + ROWS : member / PAIRS), m);  // (at last the first again)
+      float h, most = 0.0f;
+      uint32_t sum = 0;  // (as whole numbers NaN and infinity are above all)
+      fast_key16<D>(p, row, m, pos_of(r), [&](float f, int, float y0, float y1, float z0, float z1) {
+        h = f;
+        most = fmaxf(most, fmaxf(fabsf(y0), fabsf(y1)));
+        sum = max(sum, max(__float_as_uint(z0), __float_as_uint(z1)));
+      });
+      const float off = __uint_as_float(sum) * kNormErr;
+      amax = max(amax, __float_as_uint((most + off) * h) & 0x7FFFFFFFu);
+      low = max(low, __float_as_uint(fmaxf((most - off) * h, 0.0f)));
+    }
+    low = __reduce_max_sync(0xffffffffu, low);
+    if (TEAM > 32 && lane_id() == 0) team_low[warp_id()] = low;
+    reduce();
+    if (TEAM > 32) low = max(max(team_low[0], team_low[1]), max(team_low[2], team_low[3]));
+    if (amax >= 0x7E800000u || scale_need(amax) != scale_need(low)) {
+      if (TEAM > 32) __syncthreads();
+      amax = 0;
+      for (int r = member / PAIRS; r < rows; r += ROWS) {
+        const Some<16> x = exact_key16<D>(p, row_at(r), m, pos_of(r));
+        take_max(x.x);
+      }
+      reduce();
+    }
+    const int byte = max(old, scale_need(amax));
+    const float inv = byte == 255 ? __uint_as_float(0x00200000u) : pow2f(127 - byte);
+    settle(byte);
+    // (Scales so small or large that a row's factor times one might leave fp32: exactly.)
+    const bool fast = byte >= 40 && byte <= 180;
+    for (int r = member / PAIRS; r < rows; r += ROWS) {
+      const PairRow row = next;
+      next = raw_pair(row_at(min(r + ROWS, rows - 1)), m);
+      uint32_t code[8], differ = fast ? 0u : 1u;
+      fast_key16<D>(p, row, m, pos_of(r), [&](float f, int i, float y0, float y1, float z0, float z1) {
+        const float h = f * inv, err = h * kNormErr, a = y0 * h, b = y1 * h;
+        code[i] = f32x2_to_e4m3x2(fmaf(z0, -err, a), fmaf(z1, -err, b));
+        differ |= code[i] ^ f32x2_to_e4m3x2(fmaf(z0, err, a), fmaf(z1, err, b));
+      });
+      if (__any_sync(row_lanes<D, 16>(), differ != 0)) {
+        const Some<16> e = exact_key16<D>(p, row_at(r), m, pos_of(r));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) code[i] = f32x2_to_e4m3x2(e.x[2 * i] * inv, e.x[2 * i + 1] * inv);
+      }
+      uint8_t* at = codes + int64_t(slot0 + r) * p.c.token_stride;
+      *reinterpret_cast<uint2*>(at + 8 * m.first) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+      *reinterpret_cast<uint2*>(at + 8 * m.second) = make_uint2(code[4] | code[5] << 16, code[6] | code[7] << 16);
     }
     return;
   }
