@@ -25,7 +25,8 @@ i32 = lambda x: torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()
 class Decoder:
     """Some sequences' pages and some layers' caches, on the device and for the oracle."""
 
-    def __init__(self, B, rows, *, layers=2, H=8, Hkv=2, D=64, ps=16, pages=200, columns=24, most=40, seed=0):
+    def __init__(self, B, rows, *, layers=2, H=8, Hkv=2, D=64, ps=16, pages=200, columns=24, most=40, seed=0, pad=0):
+        self.pad = pad  # rows behind the last sequence's in every batch
         self.B, self.rng, self.rows, self.n_layers, self.H, self.Hkv, self.D, self.ps = B, np.random.default_rng(seed), rows, layers, H, Hkv, D, ps
         self.codes = np.zeros((layers, 2, pages, Hkv, ps, D), np.uint8)
         self.scales = np.zeros(self.codes.shape[:4], np.uint8)
@@ -40,7 +41,7 @@ class Decoder:
         self.bf, self.sig = bf, B.Signals(1)
         byte = lambda n: torch.zeros(n, dtype=torch.uint8, device="cuda")
         self.ws_pages = byte(max(B.tl_kv_resize_workspace_size(rows), B.tl_kv_fork_workspace_size(rows, rows)))
-        self.ws_attn = byte(B.tl_kv_attn_workspace_size(rows * most, rows, H, Hkv, D))
+        self.ws_attn = byte(B.tl_kv_attn_workspace_size(rows * most + pad, rows, H, Hkv, D))
 
     def resize(self, new):
         """To these lengths: an array, or a device tensor with the array."""
@@ -56,17 +57,20 @@ class Decoder:
         n, H, Hkv = int(cu[-1]), self.H, self.Hkv
         pos = np.concatenate([np.arange(l - m, l) for l, m in zip(self.lens, q)]) if positions is None else positions
         d_cu = i32(cu)
-        q_out = torch.empty(n, H, self.D, dtype=torch.bfloat16, device="cuda")
+        q_out = torch.full((n + self.pad, H, self.D), 7.0, dtype=torch.bfloat16, device="cuda")
+        if positions is not None:
+            positions = np.concatenate([positions, np.full(self.pad, -5)])
         for l, cache in enumerate(self.layers.caches):
-            x = self.bf(n, H + 2 * Hkv, self.D)
+            x = self.bf(n + self.pad, H + 2 * Hkv, self.D)
             dx = x.cuda()
             self.B.tl_kv_append_norm(cache, dx[:, H:H + Hkv], dx[:, H + Hkv:], d_cu, self.d_lens, self.d_table, self.sig, q=dx[:, :H],
                                      q_out=q_out, q_weight=self.wq.cuda(), k_weight=self.wk.cuda(), eps=EPS, cos=self.d_cos,
                                      sin=self.d_sin, positions=None if positions is None else i32(positions), max_q_len=int(max(q)))
-            k = ora.normed(f64(x)[:, H:H + Hkv], f64(self.wk), EPS)
-            k = np.stack([ora.rotate(k[t], p, self.cos, self.sin, False) for t, p in enumerate(pos)])
-            for i, rows in enumerate((k, f64(x)[:, H + Hkv:])):
+            k = ora.normed(f64(x)[:n, H:H + Hkv], f64(self.wk), EPS)
+            k = np.stack([ora.rotate(k[t], p, self.cos, self.sin, False) for t, p in enumerate(pos[:n])])
+            for i, rows in enumerate((k, f64(x)[:n, H + Hkv:])):
                 self.codes[l, i], self.scales[l, i] = ora.append(self.codes[l, i], self.scales[l, i], rows, cu, self.lens, self.table)
+        assert (q_out[n:] == 7).all()
         return q_out, cu, d_cu
 
     def check_cache(self):
@@ -89,8 +93,9 @@ class Decoder:
 
     def attend(self, q_out, cu, d_cu, tree=None, sees=None):
         """Attention over the last layer's cache, against the oracle."""
-        n, q = q_out.shape[0], f64(q_out)
-        out, lse = torch.empty_like(q_out), torch.empty(self.H, n, device="cuda")
+        n = int(cu[-1])
+        q = f64(q_out)[:n]
+        out, lse = torch.full_like(q_out, 9.0), torch.full((self.H, n + self.pad), 9.0, device="cuda")
         if tree is None:
             self.B.tl_kv_attn(q_out, self.layers.caches[-1], out, d_cu, self.d_lens, self.d_table, self.ws_attn, self.sig, lse=lse)
         else:
@@ -108,13 +113,15 @@ class Decoder:
             kk, vv = (np.abs(x).repeat(self.H // self.Hkv, 1) for x in (k, v))
             vmax[rows] = vv.max((0, 2))[None, :, None]
             smax[rows] = self.D ** -0.5 * np.einsum("thd,jhd->thj", np.abs(q[rows]), kk).max(2)[:, :, None]
-        check_attention(f64(out), f64(lse), want, wl, vmax, smax)
+        assert (out[n:] == 9).all() and (lse[:, n:] == 9).all()
+        check_attention(f64(out)[:n], f64(lse)[:, :n], want, wl, vmax, smax)
 
 
-def test_drafted_trees(B):
+@pytest.mark.parametrize("pad", [0, 13])
+def test_drafted_trees(B, pad):
     """Room for the drafts, the drafts appended by depth, seen along their paths, an accepted path kept, the rest given back."""
     rows = 4
-    d = Decoder(B, rows, seed=1)
+    d = Decoder(B, rows, seed=1, pad=pad)
     d.resize([20, 33, 5, 47])
     q = d.append([20, 33, 5, 47])
     d.attend(*q)
@@ -135,7 +142,7 @@ def test_drafted_trees(B):
         d.resize(start + n)
         positions = np.concatenate([start[s] + depth[s] for s in range(rows)]).astype(np.int32)
         q_out, cu, d_cu = d.append(n, positions)
-        bits = np.zeros((sum(n), 32), bool)
+        bits = np.zeros((sum(n) + pad, 32), bool)
         for s in range(rows):
             bits[cu[s]:cu[s + 1], :n[s]] = sees[s]
         tree = torch.from_numpy(np.packbits(bits, axis=1, bitorder="little").view(np.int32).copy()).cuda()
@@ -157,11 +164,12 @@ def test_drafted_trees(B):
         d.check_cache()
 
 
-def test_beams(B):
+@pytest.mark.parametrize("pad", [0, 5])
+def test_beams(B, pad):
     """Beams chosen, their pages shared and copied, a token appended to each, attention; some beams end on the way."""
     users, K, V, T = 3, 4, 600, 9
     rows = users * K
-    d = Decoder(B, rows, seed=2)
+    d = Decoder(B, rows, seed=2, pad=pad)
     lens = np.repeat([18, 32, 7], K)
     first = np.where(np.arange(rows) % K == 0, lens, 0)  # one beam of each user to begin with
     d.resize(first)
