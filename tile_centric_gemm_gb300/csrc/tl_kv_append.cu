@@ -37,7 +37,7 @@
 // of its own.  The exact normed value costs ten times the instructions (a sum of squares in
 // pairs, a Newton step for the root, products in pairs), and a code needs it only next to
 // a border, so keys are computed in fp32 with a bound on what they are off by; where both
-// ends of the bound have one code that is the code, else (one element of some 20000) the row
+// ends of the bound have one code that is the code, else (one element of some 30000) the row
 // is computed exactly, out of line.  Queries and keys have both elements of a rotated pair in one thread
 // (77 -> 64 us for 8192 tokens as above), values stay in registers between maximum and write (61 -> 59), and so 8192
 // tokens take 55 us (96 all exact), 3.4 TB/s, the queries 33 of them alone, keys 31 and values 10; 32 trees of
@@ -205,13 +205,14 @@ __device__ __forceinline__ void square_sum(const float (&x)[N], float scale, uin
       e += d;
     }
   } else {
-    float q[N / 8];
+    float q[N / 4];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float v = x[i] * scale;
-      q[i / 8] = fmaf(v, v, i % 8 ? q[i / 8] : 0.0f);
+      q[i / 4] = fmaf(v, v, i % 4 ? q[i / 4] : 0.0f);
     }
-    s = q[0] + (N > 8 ? q[N / 8 - 1] : 0.0f);
+    s = q[0] + q[1];
+    if (N == 16) s += q[N / 4 - 2] + q[N / 4 - 1];
   }
 #pragma unroll
   for (int d = 1; d < D / N; d <<= 1) {
@@ -268,7 +269,8 @@ __device__ __forceinline__ Norm row_norm(const float (&x)[N], float eps) {
     eps = 0.0f;
   }
   if (!EXACT) {
-    n.hi = rsqrtf(fmaf(s, 1.0f / D, eps));
+    const float a = fmaf(s, 1.0f / D, eps), r = rsqrtf(a);
+    n.hi = fmaf(r * 0.5f, fmaf(a * r, -r, 1.0f), r);
     return n;
   }
   float h, l;
@@ -322,11 +324,11 @@ __device__ __forceinline__ void turn_normed(const AppendParams& p, const Turn& w
   }
 }
 
-// What a normed and rotated element is off by in fp32, relative to the sum of its two products' magnitudes: the row's factor
-// by 10 steps of 2^-24 (12 roundings of a mean of squares, halved by the root, and the root's own 4), the products and their
-// sum by one each, the product with the factor and the bound's end by one each: 14, and 16 leave room for what these do to
-// one another.
-constexpr float kNormErr = 0x1p-20f;
+// What a normed and rotated element is off by in fp32, relative to the sum of its two products' magnitudes, in steps of 2^-24:
+// the row's factor by 6 (a mean of squares by 9 roundings, halved by the root, and one and a half of the corrected root),
+// the products, their sum, the product with the factor and the bound's end by one each: 10, and 11 leave room for what these
+// do to one another.
+constexpr float kNormErr = 0x1.6p-21f;
 // A thread's 16 dims of a row of keys: two units of 8 whose dims are each other's partners, so that a row and the tables
 // are read once, and every product of an element and its weight serves two outputs.
 struct Pair {
