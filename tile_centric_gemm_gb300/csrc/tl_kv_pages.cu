@@ -14,9 +14,9 @@
 //
 // All four are bound by latency: what they move is little.  GPU time in a graph, heads of 128, 8 kv
 // heads: four beams of 1000 tokens forked and three part-filled pages copied in 16 layers
-// (5 MB) 9 us; 512 beams of 900, 4 layers (54 MB) 22 us; 26 drafts compacted behind 4099 in 16 layers 6.6 us;
-// 64 trees of up to 60 in 8 layers (13 MB) 12 us.  A call from Python takes 15 to 20 us of the host, launches of
-// 64 layers' addresses (2 KB of parameters) among them.
+// (5 MB) 8.3 us; 512 beams of 900, 4 layers (54 MB) 20.7 us, the copies 10 of them (5.3 TB/s); 26 drafts compacted
+// behind 4099 in 16 layers 6.3 us; 64 trees of up to 60 in 8 layers (13 MB) 12.4 us.  A call from Python takes 5 to 9 us
+// of the host, 2 to 3 of them the launch.
 #include <algorithm>
 
 #include "tl_internal.h"
@@ -297,26 +297,35 @@ __global__ void __launch_bounds__(COPY_THREADS) copy_pages_kernel(const __grid_c
   uint8_t* scales = values ? l.vs : l.ks;
   for (int h = tid; h < heads; h += COPY_THREADS)
     scales[int64_t(dst) * p.Hkv + h0 + h] = scales[int64_t(src) * p.Hkv + h0 + h];
-  constexpr int UNITS = D / 16, BATCH = 8;
-  const int units = heads * slots * UNITS;
-  const uint8_t* from = pool + int64_t(src) * p.page_stride + h0 * p.head_stride;
-  uint8_t* to = pool + int64_t(dst) * p.page_stride + h0 * p.head_stride;
-  auto at = [&](int i) {
-    const int row = i / UNITS, h = row / slots;
-    return h * p.head_stride + int64_t(row - h * slots) * p.token_stride + (i % UNITS) * 16;
+  if (slots == 0) return;
+  constexpr int UNITS = D / 16, BATCH = 8, STEP = COPY_THREADS / UNITS;  // rows of a pass
+  const uint8_t* from = pool + int64_t(src) * p.page_stride + h0 * p.head_stride + tid % UNITS * 16;
+  uint8_t* to = pool + int64_t(dst) * p.page_stride + h0 * p.head_stride + tid % UNITS * 16;
+  // a thread's rows, counted on through the heads (by divisions the copies of 512 beams, 54 MB, took 12.4 us and not 10.3)
+  int h = 0, row = tid / UNITS;
+  auto settle = [&]() {
+    while (row >= slots) {
+      row -= slots;
+      ++h;
+    }
   };
-  for (int i0 = tid; i0 < units; i0 += COPY_THREADS * BATCH) {
+  settle();
+  while (h < heads) {
     uint4 w[BATCH];
+    int64_t at[BATCH];
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
-      const int i = i0 + k * COPY_THREADS;
-      if (i < units) w[k] = __ldg(reinterpret_cast<const uint4*>(from + at(i)));
+      at[k] = -1;
+      if (h < heads) {
+        at[k] = h * p.head_stride + row * p.token_stride;
+        w[k] = __ldg(reinterpret_cast<const uint4*>(from + at[k]));
+        row += STEP;
+        settle();
+      }
     }
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const int i = i0 + k * COPY_THREADS;
-      if (i < units) *reinterpret_cast<uint4*>(to + at(i)) = w[k];
-    }
+    for (int k = 0; k < BATCH; ++k)
+      if (at[k] >= 0) *reinterpret_cast<uint4*>(to + at[k]) = w[k];
   }
 }
 
