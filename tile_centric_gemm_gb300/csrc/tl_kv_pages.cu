@@ -15,7 +15,7 @@
 // All four are bound by latency: what they move is little.  GPU time in a graph, heads of 128, 8 kv
 // heads: four beams of 1000 tokens forked and three part-filled pages copied in 16 layers
 // (5 MB) 8.3 us; 512 beams of 900, 4 layers (54 MB) 20.7 us, the copies 10 of them (5.3 TB/s); 26 drafts compacted
-// behind 4099 in 16 layers 6.3 us; 64 trees of up to 60 in 8 layers (13 MB) 12.4 us.  A call from Python takes 5 to 9 us
+// behind 4099 in 16 layers 6.5 us; 64 trees of up to 60 in 8 layers (13 MB) 10.5 us.  A call from Python takes 5 to 9 us
 // of the host, 2 to 3 of them the launch.
 #include <algorithm>
 
@@ -353,13 +353,14 @@ __device__ __forceinline__ uint4 recoded(uint4 w, float f) {
 // The factor that brings codes of scale byte `from` to byte `to` >= from.  (255 is NaN and stays: the codes do not matter.)
 __device__ __forceinline__ float recode_factor(int from, int to) { return to == 255 ? 1.0f : pow2f(max(from - to, -127)); }
 
-// A warp to a sequence's keys or values of one head and layer.  Token kept[i] goes to place i; places rise with i and lie
-// at or below the tokens, so in ascending order, each batch read before it is written, nothing is lost.
+// A warp to a sequence's keys and values of one head and layer (one search for both: 64 trees of up to 60 in 8 layers 12.4 -> 10.5 us).
+// Token kept[i] goes to place i; places rise with i and lie at or below the tokens, so in ascending order, each batch
+// read before it is written, nothing is lost.
 template <int D>
 __global__ void __launch_bounds__(COPY_THREADS) compact_kernel(const __grid_constant__ CompactParams p) {
-  constexpr int UNITS = D / 16, RPP = 32 / UNITS, BATCH = 4;  // rows of a pass; passes on their way at once
+  constexpr int UNITS = D / 16, RPP = 32 / UNITS, BATCH = 2;  // rows of a pass; passes on their way at once
   const int s = blockIdx.x, lane = int(lane_id());
-  const int team = int(blockIdx.y) * (COPY_THREADS / 32) + int(warp_id());
+  const int head = int(blockIdx.y) * (COPY_THREADS / 32) + int(warp_id());
   const KvSeq seq = kv_seq(p.b, p.ps, s);
   const int start = seq.len - seq.q, n = p.n_kept[s];
   const int32_t* kept = p.kept + int64_t(s) * p.max_kept;
@@ -368,15 +369,14 @@ __global__ void __launch_bounds__(COPY_THREADS) compact_kernel(const __grid_cons
     for (int i = lane; i < n; i += 32) bad |= kept[i] >= seq.q || kept[i] <= (i ? kept[i - 1] : -1);
     bad = __any_sync(0xffffffffu, bad);
   }
-  if (team == 0 && blockIdx.z == 0 && lane == 0) {
+  if (head == 0 && blockIdx.z == 0 && lane == 0) {
     if (bad) record_error(p.b.status, kKvInvalid, uint32_t(s), uint32_t(n), uint32_t(seq.q));
     if (p.lens_out) p.lens_out[s] = bad ? seq.len : start + n;
   }
-  if (bad || n == 0 || team >= 2 * p.Hkv) return;
-  const int head = team >> 1;
+  if (bad || n == 0 || head >= p.Hkv) return;
   const Layer& l = p.layers[blockIdx.z];
-  uint8_t* codes = (team & 1 ? l.v : l.k) + head * p.head_stride;
-  uint8_t* scales = (team & 1 ? l.vs : l.ks) + head;
+  uint8_t* const codes[2] = {l.k + head * p.head_stride, l.v + head * p.head_stride};
+  uint8_t* const scales[2] = {l.ks + head, l.vs + head};
   const int32_t* table = p.b.table + int64_t(s) * p.b.max_pages;
   auto page_at = [&](int no) {
     const int page = table[no];
@@ -390,31 +390,39 @@ __global__ void __launch_bounds__(COPY_THREADS) compact_kernel(const __grid_cons
     const int i1 = min(n, base + p.ps - start);  // those that go to this page
     const int page = page_at(no);
     if (page < 0) return;
-    const int old = scales[int64_t(page) * p.Hkv];
-    // a lane's token: where it lies in the pool and its scale
+    // a lane's token: where it lies in the pool and its scales
     int64_t of = -1;
-    int sc = 0;
+    int sc[2], old[2], most[2];
     auto look_up = [&](int i) {
       of = -1;
-      sc = 0;
+      sc[0] = sc[1] = 0;
       if (i < i1) {
         const int pos = start + kept[i], from = page_at(pos / p.ps);
         if (from >= 0) {
           of = int64_t(from) * p.page_stride + int64_t(pos % p.ps) * p.token_stride;
-          sc = scales[int64_t(from) * p.Hkv];
+          sc[0] = scales[0][int64_t(from) * p.Hkv];
+          sc[1] = scales[1][int64_t(from) * p.Hkv];
         }
       }
     };
-    int most = start + i0 > base ? old : 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      old[x] = scales[x][int64_t(page) * p.Hkv];
+      most[x] = start + i0 > base ? old[x] : 0;
+    }
     for (int c = i0; c < i1; c += 32) {
       look_up(c + lane);
-      most = max(most, int(__reduce_max_sync(0xffffffffu, uint32_t(sc))));
+#pragma unroll
+      for (int x = 0; x < 2; ++x) most[x] = max(most[x], int(__reduce_max_sync(0xffffffffu, uint32_t(sc[x]))));
     }
-    uint8_t* to = codes + int64_t(page) * p.page_stride;
-    if (most > old && most != 255) {
-      const float f = recode_factor(old, most);
+    const int64_t page_at0 = int64_t(page) * p.page_stride;
+#pragma unroll 1
+    for (int x = 0; x < 2; ++x) {
+      const int now = x ? most[1] : most[0], was = x ? old[1] : old[0];
+      if (now <= was || now == 255) continue;
+      const float f = recode_factor(was, now);
       for (int r = row; r < start + i0 - base; r += RPP) {
-        uint4* at = reinterpret_cast<uint4*>(to + r * p.token_stride + unit);
+        uint4* at = reinterpret_cast<uint4*>((x ? codes[1] : codes[0]) + page_at0 + r * p.token_stride + unit);
         *at = recoded(*at, f);
       }
     }
@@ -423,29 +431,38 @@ __global__ void __launch_bounds__(COPY_THREADS) compact_kernel(const __grid_cons
       if (again) look_up(c + lane);
       // (a page's own scale byte is written once all is read: it is what its tokens are in until then)
       for (int k0 = 0; k0 < min(32, i1 - c); k0 += RPP * BATCH) {
-        uint4 w[BATCH];
-        bool move[BATCH];
+        uint4 w[BATCH][2];
+        bool move[BATCH][2];
+        int b[BATCH][2];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
           const int i = k0 + k * RPP + row;
           const int64_t from = __shfl_sync(0xffffffffu, of, i & 31);
-          const int b = __shfl_sync(0xffffffffu, sc, i & 31);
-          move[k] = i < 32 && c + i < i1 && from >= 0 &&
-                    (b != most || from != int64_t(page) * p.page_stride + (start + c + i - base) * p.token_stride);
-          if (move[k]) {
-            w[k] = *reinterpret_cast<const uint4*>(codes + from + unit);
-            if (b != most) w[k] = recoded(w[k], recode_factor(b, most));
+          const bool here = i < 32 && c + i < i1 && from >= 0, moves = from != page_at0 + (start + c + i - base) * p.token_stride;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            b[k][x] = __shfl_sync(0xffffffffu, sc[x], i & 31);
+            move[k][x] = here && (moves || b[k][x] != most[x]);
+            if (move[k][x]) w[k][x] = *reinterpret_cast<const uint4*>(codes[x] + from + unit);
           }
         }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (move[k][x] && b[k][x] != most[x]) w[k][x] = recoded(w[k][x], recode_factor(b[k][x], most[x]));
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < BATCH; ++k)
-          if (move[k]) *reinterpret_cast<uint4*>(to + (start + c + k0 + k * RPP + row - base) * p.token_stride + unit) = w[k];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (move[k][x])
+              *reinterpret_cast<uint4*>(codes[x] + page_at0 + (start + c + k0 + k * RPP + row - base) * p.token_stride + unit) = w[k][x];
         __syncwarp();
       }
     }
     __syncwarp();
-    if (lane == 0) scales[int64_t(page) * p.Hkv] = uint8_t(most);
+    if (lane < 2) (lane ? scales[1] : scales[0])[int64_t(page) * p.Hkv] = uint8_t(lane ? most[1] : most[0]);
     __syncwarp();
     i0 = i1;
   }
@@ -664,7 +681,7 @@ extern "C" tl_status tl_kv_compact(const tl_kv_compact_args* a, void* stream) {
   p.n_kept = a->n_kept;
   p.lens_out = a->seq_lens_out;
   return by_layers(p, a->caches, a->n_layers, [&](int layers) {
-    const dim3 grid(unsigned(a->B), unsigned(cdiv(2 * c.H_kv, COPY_THREADS / 32)), unsigned(layers));
+    const dim3 grid(unsigned(a->B), unsigned(cdiv(c.H_kv, COPY_THREADS / 32)), unsigned(layers));
     if (c.head_dim == 128) compact_kernel<128><<<grid, COPY_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
     else compact_kernel<64><<<grid, COPY_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
     p.lens_out = nullptr;
