@@ -867,7 +867,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       uint32_t kph = 0, vph = 0;
       uint32_t scount = 0, pcount = 0;  // tiles whose S, whose O += P V has been issued
       bool ok = true;
-      bool none = false;  // no rows: nothing to issue, the others' buffers are released all the same
+      // No rows: nothing to issue, the others' buffers are released all the same.  But not before this tile's softmax has left
+      // the segments that had rows: the converters write a segment's place among four (nan_at, kv_exp) again once the queries
+      // of the second segment after it are released, and it has to be read by then.
+      bool none = false;
+      uint32_t with = 0;  // segments with rows so far
       auto scores = [&](bool last) {
         if (!none) {
           issue_qk<D>(q0, k0 + ks * TSTEP, s_tmem + (scount & 1) * 64, leader);
@@ -887,6 +891,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         const int said = int(__reduce_max_sync(0xffffffffu, uint32_t(*reinterpret_cast<volatile int32_t*>(&sd.tiles[i & 3]))));
         const int tiles = said < 0 ? -said : said;
         none = X == 1 && __reduce_max_sync(0xffffffffu, uint32_t(*reinterpret_cast<volatile uint8_t*>(&sd.single[i & 3]))) != 0u;
+        if (none && !(ok = wait(&bars->o_empty[X], (with & 1u) ^ 1u, 25))) break;
         for (int j = 0; j < min(tiles, 2) && ok; ++j) {  // two tiles' scores ahead
           if (!(ok = wait(&bars->k_full[ks], kph, 22))) break;
           tc_fence_after();
@@ -894,7 +899,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         for (int j = 0; j < tiles && ok; ++j) {
           ok = wait(&bars->v_full[vs], vph, 23) && (none || wait(&bars->p_full[X][pcount & 1], (pcount >> 1) & 1u, 24));
-          if (ok && j == 0 && !none) ok = wait(&bars->o_empty[X], uint32_t(i & 1) ^ 1u, 25);
+          if (ok && j == 0 && !none) ok = wait(&bars->o_empty[X], (with++ & 1u) ^ 1u, 25);
           if (!ok) break;
           tc_fence_after();
           if (!none) {
@@ -931,8 +936,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const int r = g.qb * UNIT + X * ROWS + row;
       const int rows = seq_rows(p, g.seq);
       if (X == 1 && rows - g.qb * UNIT <= ROWS) {  // (no products are issued for it)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->o_empty[X]);
         done += g.t1 - g.t0;
         if (!seg_next(p, g)) break;
         continue;
