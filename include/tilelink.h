@@ -831,8 +831,8 @@ tl_status tl_kv_fork(const tl_kv_fork_args* args, void* stream);
  * its reference (0 tokens: all of them).  A sequence that ends in a part-filled page that
  * others hold too (after it was cut) is forked before it is appended to.  Where the free
  * pages do not suffice TL_ERR_INVALID is recorded with the number missing, refs_out =
- * refs, and the entries behind the sequences' pages are undefined; a wrong length records
- * TL_ERR_INVALID with the sequence, which keeps its pages.
+ * refs, and the entries behind the sequences' pages are undefined; a wrong length, old or
+ * new, records TL_ERR_INVALID with the sequence, whose row and pages stay as they are.
  */
 typedef struct tl_kv_resize_args {
   int32_t B;                   /* sequences, >= 1 */

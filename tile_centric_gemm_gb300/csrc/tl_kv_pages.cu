@@ -88,6 +88,12 @@ __device__ __forceinline__ int safe_len(const TableParams& p, int len, int s) {
   record_error(p.status, kKvInvalid, uint32_t(s), uint32_t(len), uint32_t(p.max_pages));
   return len < 0 ? 0 : int(room);
 }
+// Whether sequence s may have the length; which pages it holds is not known if not.
+__device__ __forceinline__ bool is_len(const TableParams& p, int len, int s) {
+  if (len >= 0 && len <= int64_t(p.max_pages) * p.ps) return true;
+  record_error(p.status, kKvInvalid, uint32_t(s), uint32_t(len), uint32_t(p.max_pages));
+  return false;
+}
 __device__ __forceinline__ int pages_of(const TableParams& p, int len) { return (len + p.ps - 1) / p.ps; }
 __device__ __forceinline__ bool is_page(const TableParams& p, int page) { return page >= 0 && page < p.pages; }
 
@@ -112,14 +118,11 @@ __device__ __forceinline__ int fork_need(const TableParams& p, int o, int& src, 
   }
   return p.first[b] != o || p.refs[src] != 1;
 }
-// RESIZE: pages before and after.
+// RESIZE: pages before and after; none of either where a length is wrong.
 __device__ __forceinline__ int2 resize_pages(const TableParams& p, int s) {
-  const int before = pages_of(p, safe_len(p, p.lens[s], s)), len = p.to[s];
-  if (len < 0 || len > int64_t(p.max_pages) * p.ps) {
-    record_error(p.status, kKvInvalid, uint32_t(s), uint32_t(len), uint32_t(p.max_pages));
-    return make_int2(before, before);
-  }
-  return make_int2(before, pages_of(p, len));
+  const int before = p.lens[s], after = p.to[s];
+  if (!is_len(p, before, s) || !is_len(p, after, s)) return make_int2(0, 0);
+  return make_int2(pages_of(p, before), pages_of(p, after));
 }
 
 // What the plan means for one row, by THREADS threads: of a fork a new row (below B_out) or what an old one held.
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) plan_kernel(const __grid_cons
           if (p.base[mid] <= rank) lo = mid;
           else hi = mid - 1;
         }
-        p.table_out[int64_t(lo) * p.max_pages + pages_of(p, safe_len(p, p.lens[lo], lo)) + rank - p.base[lo]] = page;
+        p.table_out[int64_t(lo) * p.max_pages + pages_of(p, p.lens[lo]) + rank - p.base[lo]] = page;
       }
       ++rank;
     }
