@@ -799,7 +799,9 @@ tl_status tl_kv_tree_attn(const tl_kv_tree_attn_args* args, void* stream);
  * of each new one.  Where the free pages do not suffice TL_ERR_INVALID is recorded with
  * the number missing, n_copies is 0, refs_out = refs, and the new table and lengths are
  * left as they were (copies is undefined).  Entries behind a row's pages are left as they
- * were.
+ * were.  A wrong parent records TL_ERR_INVALID with the new row, which is empty; a wrong
+ * length records it with the old row, whose pages keep their counts and whose children
+ * are empty.
  */
 typedef struct tl_kv_fork_args {
   int32_t B_in;                /* rows of page_table, >= 1 */

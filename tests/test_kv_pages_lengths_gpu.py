@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_kv_pages_gpu import Tables, i32
+from tests.test_kv_pages_gpu import Tables, fork, i32
 from oracle import kv_pages
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +47,24 @@ def test_resize_of_a_wrong_current_length(B, rows, in_place, length, new):
     to[wrong] = lens[wrong]  # the others' changes alone
     table, want = kv_pages.resize(t.table, t.lens, to, t.refs, 16)
     assert np.array_equal(out.cpu().numpy(), want) and np.array_equal(d.cpu().numpy(), table)
+
+
+@pytest.mark.parametrize("rows", [5, 700])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("length", [-1, 10 ** 7, "one above"])
+@pytest.mark.parametrize("children", [0, 1, 3])
+def test_fork_of_a_wrong_length(B, rows, in_place, length, children):
+    lens = [40 + s % 37 for s in range(rows)]
+    wrong = rows // 2
+    t = stale(lens, wrong, spare=rows + 30)
+    true = t.lens.copy()
+    t.lens[wrong] = t.table.shape[1] * 16 + 1 if length == "one above" else length
+    parents = np.random.default_rng(12).integers(-1, rows, rows)
+    parents[parents == wrong] = -1
+    parents[1:1 + children] = wrong
+    got, status, before = fork(B, t, parents, in_place=in_place)
+    assert status == (B.TL_ERR_INVALID, wrong)
+    true[wrong] = 0  # it gives nothing on and nothing back
+    table, out, refs, copies = kv_pages.fork(t.table, true, t.refs, parents, t.ps, before)
+    assert np.array_equal(got[0], table) and np.array_equal(got[1], out) and np.array_equal(got[2], refs)
+    assert got[4][0] == len(copies) and [tuple(c) for c in got[3].T[:len(copies)]] == copies

@@ -81,13 +81,6 @@ __device__ __forceinline__ T block_scan(T v, T* warp_sums, T& all) {
 }
 static_assert(PLAN_THREADS == 32 * 32, "a warp sums the warps");
 
-// A length that the table's row can hold.
-__device__ __forceinline__ int safe_len(const TableParams& p, int len, int s) {
-  const int64_t room = int64_t(p.max_pages) * p.ps;
-  if (len >= 0 && len <= room) return len;
-  record_error(p.status, kKvInvalid, uint32_t(s), uint32_t(len), uint32_t(p.max_pages));
-  return len < 0 ? 0 : int(room);
-}
 // Whether sequence s may have the length; which pages it holds is not known if not.
 __device__ __forceinline__ bool is_len(const TableParams& p, int len, int s) {
   if (len >= 0 && len <= int64_t(p.max_pages) * p.ps) return true;
@@ -108,7 +101,8 @@ __device__ __forceinline__ int parent_of(const TableParams& p, int o) {
 __device__ __forceinline__ int fork_need(const TableParams& p, int o, int& src, int& slots) {
   const int b = parent_of(p, o);
   if (b < 0) return 0;
-  const int len = safe_len(p, p.lens[b], b);
+  const int len = p.lens[b];
+  if (!is_len(p, len, b)) return 0;
   slots = len % p.ps;
   if (slots == 0) return 0;
   src = p.table[int64_t(b) * p.max_pages + len / p.ps];
@@ -139,11 +133,11 @@ __device__ __forceinline__ void change_row(const TableParams& p, int row_no, int
     }
   } else if (row_no < p.B_out) {
     const int o = row_no, b = p.to[o];
-    if (b < 0 || b >= p.B_in) {
+    if (b < 0 || b >= p.B_in || !is_len(p, p.lens[b], b)) {
       if (tid == 0) p.lens_out[o] = 0;
       return;
     }
-    const int len = safe_len(p, p.lens[b], b), n = pages_of(p, len), at = p.base[o];
+    const int len = p.lens[b], n = pages_of(p, len), at = p.base[o];
     const int32_t* from = p.table + int64_t(b) * p.max_pages;
     int32_t* row = p.table_out + int64_t(o) * p.max_pages;
     for (int i = tid; i < n; i += THREADS) row[i] = at >= 0 && i == n - 1 ? p.copies[p.B_out + at] : from[i];
@@ -153,7 +147,9 @@ __device__ __forceinline__ void change_row(const TableParams& p, int row_no, int
     }
   } else {
     const int b = row_no - p.B_out;
-    const int len = safe_len(p, p.lens[b], b), full = len / p.ps, children = p.count[b];
+    const int len = p.lens[b];
+    if (!is_len(p, len, b)) return;
+    const int full = len / p.ps, children = p.count[b];
     const int32_t* row = p.table + int64_t(b) * p.max_pages;
     if (children != 1) {
       for (int i = tid; i < full; i += THREADS) {
@@ -195,7 +191,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) plan_kernel(const __grid_cons
     }
     __syncthreads();
   }
-  int64_t total = 0;  // (of wrong lengths it may be anything; only if the pool has as many does it matter)
+  int64_t total = 0;
   for (int r0 = 0; r0 < p.B_out; r0 += PLAN_THREADS) {
     const int r = r0 + tid;
     int need = 0, src = 0, slots = 0;
