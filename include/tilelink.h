@@ -925,7 +925,7 @@ typedef struct tl_beam_select_args {
   int32_t B;                   /* users, 0..16384 (0: nothing to do) */
   int32_t K;                   /* beams of each, 1..64 */
   int32_t N;                   /* continuations of each, 1..64 */
-  int32_t V;                   /* tokens, >= 1; K * V < 2^31 */
+  int32_t V;                   /* tokens, >= 1; K * V <= 2^30 */
   int32_t dtype;               /* of logits: 0 = fp32, 1 = bf16 */
   int32_t eos;                 /* the token that ends a beam, or -1 */
   int32_t history_stride;      /* entries of a history row */

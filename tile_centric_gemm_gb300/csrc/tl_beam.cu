@@ -45,6 +45,7 @@ constexpr int AHEAD = 8;              // groups of a thread that stay in registe
 constexpr float kFar = 32768.0f;      // references of sums are whole powers of two up to 2^kFar
 constexpr float kLog2e = 1.4426950216f, kLog2eLow = 1.9259629e-08f;
 constexpr int MAX_BEAMS = 64, MAX_N = 64, MAX_B = 16384;
+constexpr int64_t MAX_LOGITS = int64_t(1) << 30;  // of a user: places in a row, a step or two behind its end too, stay within 32 bits
 constexpr int NONE = int(0x80000000);
 
 struct BeamParams {
@@ -862,7 +863,7 @@ bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
 
 extern "C" size_t tl_beam_select_workspace_size(int B, int K, int N, int V) {
   using namespace tl;
-  if (B < 1 || B > MAX_B || K < 1 || K > MAX_BEAMS || N < 1 || N > MAX_N || V < 1 || int64_t(K) * V > 0x7FFFFFFF) return 0;
+  if (B < 1 || B > MAX_B || K < 1 || K > MAX_BEAMS || N < 1 || N > MAX_N || V < 1 || int64_t(K) * V > MAX_LOGITS) return 0;
   // parts of all rows are at most this many, of at most this size, which never fall as B or K grow
   return kCounters + (size_t(B) * K * least_splits(V) + BLOCKS) * part_bytes(line_count(V, least_splits(V)));
 }
@@ -873,8 +874,9 @@ extern "C" tl_status tl_beam_select(const tl_beam_select_args* a, void* stream) 
   if (!a) return fail(TL_ERR_INVALID, "%s: NULL args", who);
   if (a->B < 0 || a->K < 1 || a->N < 1 || a->V < 1)
     return fail(TL_ERR_INVALID, "%s: B %d, K %d, N %d, V %d", who, a->B, a->K, a->N, a->V);
-  if (a->B > MAX_B || a->K > MAX_BEAMS || a->N > MAX_N || int64_t(a->K) * a->V > 0x7FFFFFFF)
-    return fail(TL_ERR_UNSUPPORTED, "%s: B %d (at most 16384), K %d, N %d (64 each), K * V below 2^31", who, a->B, a->K, a->N);
+  if (a->B > MAX_B || a->K > MAX_BEAMS || a->N > MAX_N || int64_t(a->K) * a->V > MAX_LOGITS)
+    return fail(TL_ERR_UNSUPPORTED, "%s: B %d (at most 16384), K %d, N %d (64 each), K * V = %lld (2^30)", who, a->B, a->K, a->N,
+                static_cast<long long>(a->K) * a->V);
   if (a->dtype != 0 && a->dtype != 1) return fail(TL_ERR_INVALID, "%s: dtype %d", who, a->dtype);
   if (a->row_stride < a->V) return fail(TL_ERR_INVALID, "%s: row_stride below V", who);
   if (a->eos < -1 || a->eos >= a->V || (a->done && a->eos < 0))
