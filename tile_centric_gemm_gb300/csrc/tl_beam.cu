@@ -6,7 +6,7 @@
 //
 // The logits are read once, as a stream: a row is cut into as many parts as fill the GPU with
 // blocks, a thread takes 16 logits at a time, and what a block leaves is its part's sum of
-// exponentials and the maximum of each group of up to 256 logits that four neighbouring threads took.  The block of a
+// exponentials and the maximum of each group of up to 256 logits that 16 neighbouring threads took in a step.  The block of a
 // user that ends last joins the K rows: the groups' maxima are scores themselves, so any bound
 // that N of them reach is at or below the N-th best score.  A bound that few groups reach is found
 // from the threads' best ones (256 bins between the least and the largest, then bisection by the
@@ -16,14 +16,17 @@
 // Where more reach the bound than the list holds (plateaus), rows are taken apart value by value.
 //
 // Beams are compared by scores in pairs of fp32 (48 bits), and a row's sum of exponentials is joined in pairs
-// too, so that what decides between two beams is not lost beside scores of -20.  (64-bit arithmetic took 5000
+// too, so that joining and comparing add nothing to what the exponentials themselves are off by (2^-22 each, which is
+// what lse is good to where a few logits make up the sum).  (64-bit arithmetic took 5000
 // of the joining block's cycles: a warp's instruction holds its unit for 16.)
 //
 // Bound by memory for many beams and by latency for few.  512 beams of 50001 in fp32, a sixth of them ended, 16
-// continuations to each 8: 25.3 us in a graph for 86 MB; the stream alone takes 16.9 (5.1 TB/s, 75 % of a copy's rate),
-// the users' joins 8.4 behind it, one block to each.  (Smaller parts, so that users end one after the other
-// and joins run beside the stream: 27.8 us with 2 of them to a row, 31.9 with 3.)  4 beams of 32000 in bf16: 9.9 us, 6.8 of
-// them the join: a dozen barriers and two trips to L2 and memory.
+// continuations to each 8: 26.8 us in a graph for 86 MB; the stream alone takes 18.2 (4.7 TB/s, 70 % of a copy's rate),
+// with three blocks on some SMs and four on others, the users' joins 8.6 behind it, one block to each.  (Smaller parts, so
+// that users end one after the other and joins run beside the stream, took 2.5 us more with 2 of them to a row, 6.6 with 3.)
+// 4 beams of 32000 in bf16: 9.5 us, 6.3 of them the join, a chain of some 12,000 cycles: the sums 3,500 to 4,000 (with the
+// first loads), the threads' best groups 2,000, the bound 1,300, the list of groups 2,300, reading them again 2,100, the
+// ranks 1,900.
 #include <algorithm>
 #include <cmath>
 
@@ -36,8 +39,8 @@ namespace {
 constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int UNIT = 16;              // logits that a thread takes at once
 constexpr int STEP = THREADS * UNIT;  // and a block
-constexpr int GROUP = 4;              // steps of four neighbouring threads whose maximum is kept
-constexpr int LINE = THREADS / 4;     // maxima of a block's four steps
+constexpr int GROUP = 16;             // neighbouring threads whose maximum of a step is kept
+constexpr int LINE = THREADS / GROUP; // maxima of a block's step
 constexpr int MOST_STEPS = 16;        // of a block, at least one
 constexpr int BLOCKS = 304;           // wanted: two to an SM at least, all at once (four fit)
 constexpr int HITS = 512;             // groups that are looked at again, at most
@@ -63,8 +66,8 @@ struct BeamParams {
   uint32_t* counters;  // [B], zero between calls
   float4* heads;       // [B K splits] of a part: reference (-infinity, infinity: of nothing but that) and sum of exp(x - reference)
   float* maxima;       // [B K splits][lines][LINE]
-  int32_t B, K, N, V, eos, splits, lines;  // lines: of a part
-  int32_t per;         // vectors of a part
+  int32_t B, K, N, V, eos, splits, lines;  // lines: of a part, its steps
+  int32_t per;         // elements of a part
   int32_t list;                                         // places of the list in shared memory
   int32_t history_stride, length;
 };
@@ -243,6 +246,13 @@ struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int W = 4;
+  static constexpr uint32_t NONE_RAW = 0xFF800000u;  // -infinity
+  static __device__ __forceinline__ uint32_t raw(const float* p) {
+    uint32_t r;
+    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
+    return r;
+  }
+  static __device__ __forceinline__ float value(uint32_t r) { return __uint_as_float(r); }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
   static __device__ __forceinline__ uint4 load(const float* p) {
     uint4 v;
@@ -260,6 +270,9 @@ struct Vec<float> {
 template <>
 struct Vec<uint16_t> {
   static constexpr int W = 8;
+  static constexpr uint32_t NONE_RAW = 0xFF80u;
+  static __device__ __forceinline__ uint32_t raw(const uint16_t* p) { return __ldg(p); }
+  static __device__ __forceinline__ float value(uint32_t r) { return __uint_as_float(r << 16); }
   static __device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
   static __device__ __forceinline__ uint4 load(const uint16_t* p) { return Vec<float>::load(reinterpret_cast<const float*>(p)); }
   static __device__ __forceinline__ void unpack(uint4 v, float* x) {
@@ -312,35 +325,37 @@ struct Row {
   }
 };
 
-// The UNIT values of a thread at one step.
+// Which elements of a row a part has.
+__device__ __forceinline__ int2 part_range(const BeamParams& p, int split) {
+  return make_int2(min(p.V, split * p.per), min(p.V, (split + 1) * p.per));
+}
+// The UNIT values of a thread at one step: a warp's are 32 UNIT neighbours from `at` on, a lane's every 32nd.  Which thread has
+// which goes by the token alone, not by where the row begins in memory, so that rows of the same logits have the same sum, and
+// equal beams stay in order.  (Loads of 16 bytes whose elements go by alignment took 512 beams of 50001 in 25 us and not 27,
+// one user's 4 of 128256 in 15.3 and not 9.6; by the token in three narrower pieces the former took 38.)
 template <typename T>
-__device__ __forceinline__ void load_unit(const Row<T>& r, int v, int v1, uint4 (&x)[UNIT / Vec<T>::W]) {
-  constexpr int W = Vec<T>::W, VECS = UNIT / W;
-  if (v * W >= r.skew && v + (VECS - 1) * THREADS < v1 && (v + (VECS - 1) * THREADS + 1) * W - r.skew <= r.V) {
-    const T* at = r.first + (v * W - r.skew);
+__device__ __forceinline__ void load_unit(const T* first, int at, int end, uint32_t (&x)[UNIT]) {
+  const T* from = first + at + int(lane_id());
+  if (at + 32 * UNIT <= end) {
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) x[i] = Vec<T>::load(at + i * THREADS * W);
+    for (int i = 0; i < UNIT; ++i) x[i] = Vec<T>::raw(from + 32 * i);
   } else {
+    const int left = end - at - int(lane_id());
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) x[i] = r.load(v + i * THREADS, v + i * THREADS < v1);
+    for (int i = 0; i < UNIT; ++i) x[i] = 32 * i < left ? Vec<T>::raw(from + 32 * i) : Vec<T>::NONE_RAW;
   }
 }
 
 // The block's sum again, relative to the maximum itself: for logits whose powers of two fp32 does not tell apart, and for
 // infinities (1 for each; what is NaN stays).
 template <typename T>
-__device__ __noinline__ void far_sum(const BeamParams& p, Smem& sm, int row, int v0, int v1, float most) {
-  const Row<T> r(p, row);
-  constexpr int W = Row<T>::W;
+__device__ __noinline__ void far_sum(Smem& sm, const T* first, int begin, int end, float most) {
   float2 sum = make_float2(0.0f, 0.0f);
-  for (int v = v0 + int(threadIdx.x); v < v1; v += THREADS) {
-    float x[W];
-    Vec<T>::unpack(r.load(v, true), x);
-#pragma unroll
-    for (int c = 0; c < W; ++c) {
-      const float e = x[c] == most ? 1.0f : x[c] == x[c] ? ex2_approx((x[c] - most) * kLog2e) : x[c];
-      sum = sum + make_float2(most == -INFINITY && x[c] == x[c] ? 0.0f : e, 0.0f);
-    }
+#pragma unroll 4
+  for (int t = begin + int(threadIdx.x); t < end; t += THREADS) {
+    const float x = Vec<T>::value(Vec<T>::raw(first + t));
+    const float e = x == most ? 1.0f : x == x ? ex2_approx((x - most) * kLog2e) : x;
+    sum = sum + make_float2(most == -INFINITY && x == x ? 0.0f : e, 0.0f);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1)
@@ -350,40 +365,32 @@ __device__ __noinline__ void far_sum(const BeamParams& p, Smem& sm, int row, int
   __syncthreads();
 }
 
-// Which vectors a part of a row has.
-template <typename T>
-__device__ __forceinline__ int2 part_vectors(const BeamParams& p, const Row<T>& r, int split) {
-  return make_int2(split * p.per, min((p.V + r.skew + Row<T>::W - 1) / Row<T>::W, (split + 1) * p.per));
-}
-
 // One block's part of a row: its sum and its groups' maxima.
 template <typename T>
 __device__ __forceinline__ void take_part(const BeamParams& p, Smem& sm, int row, int split) {
-  constexpr int W = Vec<T>::W, VECS = UNIT / W;
   const int tid = threadIdx.x, lane = int(lane_id()), warp = int(warp_id());
-  const Row<T> r(p, row);
-  const int2 v = part_vectors(p, r, split);
-  const int steps = max(0, v.y - v.x + THREADS * VECS - 1) / (THREADS * VECS);
-  float* out = p.maxima + int64_t(blockIdx.x) * p.lines * LINE + tid / 4;
+  const T* first = static_cast<const T*>(p.logits) + int64_t(row) * p.stride;
+  const int2 range = part_range(p, split);
+  const int steps = (range.y - range.x + STEP - 1) / STEP, begin = range.x + warp * (32 * UNIT);
+  float* out = p.maxima + int64_t(blockIdx.x) * p.lines * LINE + tid / GROUP;
   auto put = [&](int line, float x) {
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-    if (tid % 4 == 0) __stcg(out + line * LINE, x);
+#pragma unroll
+    for (int d = 1; d < GROUP; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+    if (tid % GROUP == 0) __stcg(out + line * LINE, x);
   };
   // A thread's sum is relative to 2^c, c a whole number that follows the maximum times log2 e: one fused operation brings
   // a logit to its exponent, and what changes reference does so exactly.
-  uint4 next[VECS];
-  float most = -INFINITY, group = -INFINITY, c = -kFar, hi = 0.0f, lo = 0.0f;
-  load_unit(r, v.x + tid, v.y, next);
+  uint32_t next[UNIT];
+  float most = -INFINITY, c = -kFar, hi = 0.0f, lo = 0.0f;
+  load_unit(first, begin, range.y, next);
   for (int b = 0; b < steps; ++b) {
     float x[UNIT];
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) Vec<T>::unpack(next[i], x + i * W);
-    if (b + 1 < steps) load_unit(r, v.x + (b + 1) * THREADS * VECS + tid, v.y, next);
+    for (int i = 0; i < UNIT; ++i) x[i] = Vec<T>::value(next[i]);
+    if (b + 1 < steps) load_unit(first, begin + (b + 1) * STEP, range.y, next);
     float top = max3(x[0], x[1], -INFINITY);  // (a NaN is below everything)
 #pragma unroll
     for (int i = 2; i < UNIT; i += 2) top = max3(top, x[i], x[i + 1]);
-    group = fmaxf(group, top);
     if (top * kLog2e > c + 1.0f) {
       const float now = fminf(rintf(top * kLog2e), kFar), f = pow2_below(c - now);
       hi *= f;
@@ -400,17 +407,10 @@ __device__ __forceinline__ void take_part(const BeamParams& p, Smem& sm, int row
     const float2 sum = two_sum(hi, (s[0] + s[1]) + (s[2] + s[3]));
     hi = sum.x;
     lo += sum.y;
-    if (b % GROUP == GROUP - 1) {
-      put(b / GROUP, group);
-      most = fmaxf(most, group);
-      group = -INFINITY;
-    }
+    put(b, top);
+    most = fmaxf(most, top);
   }
-  for (int g = steps / GROUP; g < p.lines; ++g) {  // (the last part of a row may have fewer)
-    put(g, group);
-    most = fmaxf(most, group);
-    group = -INFINITY;
-  }
+  for (int b = steps; b < p.lines; ++b) put(b, -INFINITY);  // (the last part of a row may have fewer)
   float block_most = most;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) block_most = fmaxf(block_most, __shfl_xor_sync(0xffffffffu, block_most, d));
@@ -432,7 +432,7 @@ __device__ __forceinline__ void take_part(const BeamParams& p, Smem& sm, int row
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) block_most = fmaxf(block_most, sm.warp_most[w]);
   const bool far = fabsf(block_most) > kFar / 2;  // (no logit above -infinity, too)
-  if (far) far_sum<T>(p, sm, row, v.x, v.y, block_most);
+  if (far) far_sum<T>(sm, first, range.x, range.y, block_most);
   if (warp == 0) {
     const float block_c = rintf(block_most * kLog2e);
     sum = sm.warp_sum[lane % WARPS];
@@ -660,13 +660,12 @@ __device__ __noinline__ void join_by_value(const BeamParams& p, Smem& sm, int us
 
 // A group that is looked at again.
 struct Hit {
-  int row, token, end;  // of the user; the group's first token (below 0 where the row begins in a vector); its part's end
+  int row, token, end;  // of the user; the group's first token; its part's end
 };
 
 // The last block of a user: its beams' sums, and the N best of their candidates.
 template <typename T>
 __device__ __noinline__ void join(const BeamParams& p, Smem& sm, int64_t* keys, int user) {
-  constexpr int W = Row<T>::W, VECS = UNIT / W;
   const int tid = threadIdx.x;
   uint64_t* ties = reinterpret_cast<uint64_t*>(keys + p.list);
   uint32_t* tokens = reinterpret_cast<uint32_t*>(ties + p.list);
@@ -719,10 +718,9 @@ __device__ __noinline__ void join(const BeamParams& p, Smem& sm, int64_t* keys, 
       const int at = atomicAdd(&sm.hits, 1);
       if (at >= HITS) return;
       const int k = line / (p.splits * p.lines), part = line / p.lines;
-      const Row<T> r(p, user * p.K + k);
-      const int2 range = part_vectors(p, r, part - k * p.splits);
-      const int v = range.x + (line - part * p.lines) * (GROUP * VECS * THREADS) + tid % LINE * 4;
-      hit[at] = Hit{k, r.token(v, 0), min(r.token(range.y, 0), p.V)};
+      const int2 range = part_range(p, part - k * p.splits);
+      const int q = tid % LINE;
+      hit[at] = Hit{k, range.x + (line - part * p.lines) * STEP + q / (32 / GROUP) * (32 * UNIT) + q % (32 / GROUP) * GROUP, range.y};
     };
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
@@ -735,41 +733,33 @@ __device__ __noinline__ void join(const BeamParams& p, Smem& sm, int64_t* keys, 
   const int hits = sm.hits;
   // ---------------------------------------------------------------- what reaches the bound
   if (hits <= HITS) {
-    // a group's vectors are four neighbouring ones of each step
-    constexpr int VPG = 4 * GROUP * VECS, BATCH = 4;
-    const int offset = (tid / 4 % (GROUP * VECS) * THREADS + tid % 4) * W;
+    // a group's elements are GROUP neighbours of every 32 of its warp's; a thread takes EACH of them, 32 APART places apart
+    constexpr int EACH = 4, APART = UNIT / EACH, PER_HIT = GROUP * APART, BATCH = 4;
+    const int offset = tid / GROUP % APART * 32 + tid % GROUP;
 #pragma unroll 1
-    for (int h0 = tid / VPG; h0 < hits; h0 += BATCH * (THREADS / VPG)) {
-      uint4 w[BATCH];
+    for (int h0 = tid / PER_HIT; h0 < hits; h0 += BATCH * (THREADS / PER_HIT)) {
+      uint32_t w[BATCH][EACH];
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        const Hit at = hit[min(h0 + i * (THREADS / VPG), hits - 1)];
-        const T* first = static_cast<const T*>(p.logits) + int64_t(user * p.K + at.row) * p.stride;
-        const int e = at.token + offset;
-        if (e >= 0 && e + W <= at.end) w[i] = Vec<T>::load(first + e);
-        else w[i] = Row<T>::edge(first, e, at.end);
+        const Hit at = hit[min(h0 + i * (THREADS / PER_HIT), hits - 1)];
+        const T* from = static_cast<const T*>(p.logits) + int64_t(user * p.K + at.row) * p.stride + at.token + offset;
+#pragma unroll
+        for (int j = 0; j < EACH; ++j)
+          w[i][j] = at.token + offset + j * (32 * APART) < at.end ? Vec<T>::raw(from + j * (32 * APART)) : Vec<T>::NONE_RAW;
       }
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        const int h = h0 + i * (THREADS / VPG);
+        const int h = h0 + i * (THREADS / PER_HIT);
         if (h >= hits) break;
-        float x[W];
-        Vec<T>::unpack(w[i], x);
-        float most = x[0];
-#pragma unroll
-        for (int c = 1; c < W; ++c) most = fmaxf(most, x[c]);
         const float bias = sm.bias[hit[h].row];
-        if (!(most + bias >= above)) continue;
-        for (int c = 0; c < W; ++c) {
-          float y = x[0];
 #pragma unroll
-          for (int j = 1; j < W; ++j)
-            if (j == c) y = x[j];
+        for (int j = 0; j < EACH; ++j) {
+          const float y = Vec<T>::value(w[i][j]);
           if (!(y + bias >= above)) continue;
           const int place = atomicAdd(&sm.count, 1);
           if (place < p.list) {
             ties[place] = tie_of(hit[h].row, y);
-            tokens[place] = uint32_t(hit[h].token + offset + c);
+            tokens[place] = uint32_t(hit[h].token + offset + j * (32 * APART));
           }
         }
       }
@@ -837,20 +827,14 @@ __global__ void __launch_bounds__(THREADS, 4) beam_kernel(const __grid_constant_
 }
 
 constexpr size_t kCounters = size_t(MAX_B) * 4;  // in a place that does not depend on the sizes
-// Parts of a row: as many as fill the GPU, of 4096 elements at least and 65536 at most.  (7: elements that a row may begin
-// behind 16 bytes.)
-int least_splits(int V) { return int((int64_t(V) + 7 + MOST_STEPS * STEP - 1) / (MOST_STEPS * STEP)); }
+// Parts of a row: as many as fill the GPU, of 4096 elements at least and 65536 at most.
+int least_splits(int V) { return cdiv(V, MOST_STEPS * STEP); }
 int split_count(int64_t rows, int V) {
-  const int most = int((int64_t(V) + 7 + STEP - 1) / STEP);
-  return std::max(least_splits(V), std::min(std::min(most, 32), int((BLOCKS + rows - 1) / rows)));
+  return std::max(least_splits(V), std::min(std::min(cdiv(V, STEP), 32), int((BLOCKS + rows - 1) / rows)));
 }
-// Vectors of a part, at least: of W elements, a row's first one up to W - 1 behind 16 bytes.
-int part_vectors(int V, int W, int splits) { return int((int64_t(V) + 2 * (W - 1)) / W + splits - 1) / splits; }
-// Lines of maxima of a part, of either type: of 4 W-element vectors to a thread for fp32, 2 for bf16.
-int line_count(int V, int splits) {
-  const int a = part_vectors(V, 4, splits), b = part_vectors(V, 8, splits);
-  return std::max(1, std::max(cdiv(a, GROUP * STEP / 4), cdiv(b, GROUP * STEP / 8)));
-}
+// Elements of a part, a multiple of a warp's 32; and its lines of maxima.
+int part_elements(int V, int splits) { return cdiv(cdiv(V, splits), 32) * 32; }
+int line_count(int V, int splits) { return cdiv(part_elements(V, splits), STEP); }
 int64_t part_bytes(int lines) { return int64_t(sizeof(float4)) + lines * LINE * 4; }
 
 bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
@@ -921,7 +905,7 @@ extern "C" tl_status tl_beam_select(const tl_beam_select_args* a, void* stream) 
   p.eos = a->eos;
   p.splits = split_count(in, a->V);
   p.lines = line_count(a->V, p.splits);
-  p.per = part_vectors(a->V, a->dtype ? 8 : 4, p.splits);
+  p.per = part_elements(a->V, p.splits);
   p.heads = reinterpret_cast<float4*>(static_cast<uint8_t*>(a->workspace) + kCounters);
   p.maxima = reinterpret_cast<float*>(p.heads + in * p.splits);
   p.list = std::max(256, 16 * a->N);
