@@ -889,7 +889,7 @@ typedef struct tl_kv_compact_args {
   int32_t B;                   /* sequences, >= 1 */
   int32_t max_pages;           /* columns of page_table */
   int32_t max_kept;            /* columns of kept, >= 1 */
-  const tl_kv_cache* caches;   /* host array [n_layers], of equal layout */
+  const tl_kv_cache* caches;   /* host array [n_layers], of equal layout, each once */
   const int32_t* kept;         /* device int32 [B, max_kept] */
   const int32_t* n_kept;       /* device int32 [B] */
   const int32_t* cu_seqlens;   /* device int32 [B + 1] */

@@ -18,6 +18,7 @@
 // behind 4099 in 16 layers 6.5 us; 64 trees of up to 60 in 8 layers (13 MB) 10.5 us.  A call from Python takes 5 to 9 us
 // of the host, 2 to 3 of them the launch.
 #include <algorithm>
+#include <functional>
 
 #include "tl_internal.h"
 #include "tl_kv.cuh"
@@ -487,6 +488,17 @@ tl_status check_layers(const char* who, const tl_kv_cache* caches, int n) {
   return TL_OK;
 }
 
+// Whether two of the caches are one: it would be written twice at once.
+bool a_cache_twice(const tl_kv_cache* caches, int n) {
+  const void* all[4096];
+  for (const auto side : {&tl_kv_cache::k, &tl_kv_cache::v}) {
+    for (int i = 0; i < n; ++i) all[i] = caches[i].*side;
+    std::sort(all, all + n, std::less<const void*>());
+    if (std::adjacent_find(all, all + n) != all + n) return true;
+  }
+  return false;
+}
+
 // Runs launch(params, first layer) for each LAYERS of them.
 template <class P, class F>
 tl_status by_layers(P& p, const tl_kv_cache* caches, int n, F launch) {
@@ -663,6 +675,7 @@ extern "C" tl_status tl_kv_compact(const tl_kv_compact_args* a, void* stream) {
     return fail(TL_ERR_INVALID, "%s: NULL pointer argument", who);
   if (meet(a->seq_lens, a->B * 4ll, a->seq_lens_out, a->B * 4ll))
     return fail(TL_ERR_INVALID, "%s: seq_lens_out overlaps seq_lens", who);
+  if (a_cache_twice(a->caches, a->n_layers)) return fail(TL_ERR_INVALID, "%s: a cache is given twice", who);
   DeviceInfo di{};
   if (tl_status s = device_info(&di)) return s;
   if (a->signals->device != di.device) return fail(TL_ERR_INVALID, "%s: signals belong to another device", who);
