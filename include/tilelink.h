@@ -913,7 +913,8 @@ tl_status tl_kv_compact(const tl_kv_compact_args* args, void* stream);
  * 2^-26) and returned in fp32.  Where rows begin in memory does not enter: beams of the
  * same logits have the same lse.  Only finite
  * scores count: tokens whose logit is -infinity, beams whose score is not finite, and
- * beams whose lse is not (all logits -infinity, or one NaN or +infinity) offer nothing.
+ * beams whose lse is not (all logits -infinity, or one NaN or +infinity), or whose score
+ * less lse is not in fp32, offer nothing.
  * A beam whose done is not 0 has ended: its logits are not read, its lse is 0, and it
  * offers one continuation, token eos at its own score.  Where fewer than N are offered
  * the places left have parent -1, token -1 and score -infinity.

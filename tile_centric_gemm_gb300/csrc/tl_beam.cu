@@ -524,11 +524,12 @@ __device__ __forceinline__ void join_sums(const BeamParams& p, Smem& sm, int use
       float2 lse = make_float2(0.0f, 0.0f);
       if (!ended) lse = sum.x > 0.0f && fabsf(ref.x) < INFINITY ? ref + log_of(sum) : make_float2(ref.x + (sum.x - sum.x), 0.0f);
       if (p.lse) p.lse[user * p.K + k] = lse.x;
-      // a row of -infinity, or with +infinity or NaN, offers nothing
-      sm.lse[k] = ended ? make_float2(-INFINITY, 0.0f) : fabsf(lse.x) < INFINITY ? lse : make_float2(INFINITY, 0.0f);
-      sm.score[k] = score;
+      // a row of -infinity, or with +infinity or NaN, offers nothing; nor does one whose score less lse leaves fp32
       const float bias = score - lse.x;
-      sm.bias[k] = !ended && fabsf(lse.x) < INFINITY && fabsf(bias) < INFINITY ? bias : -INFINITY;
+      const bool offers = !ended && fabsf(lse.x) < INFINITY && fabsf(bias) < INFINITY;
+      sm.lse[k] = ended ? make_float2(-INFINITY, 0.0f) : offers ? lse : make_float2(INFINITY, 0.0f);
+      sm.score[k] = score;
+      sm.bias[k] = offers ? bias : -INFINITY;
     }
   }
 }
