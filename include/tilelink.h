@@ -880,6 +880,9 @@ tl_status tl_kv_copy_pages(const tl_kv_copy_pages_args* args, void* stream);
  * layer, and seq_lens_out[s] = seq_lens[s] - n_s + n_kept[s].  A page that receives kept
  * tokens has as its scale byte the largest of those that its tokens (older ones too) were
  * stored under; codes of a smaller one are shifted to it, rounded once to nearest even.
+ * (So a draft that was larger than its page's scale, and made the append shift the page's
+ * older codes, leaves them as they are then, kept or not: a cache that drafts went through
+ * is not bit for bit the one that plain decoding leaves.)
  * Slots behind a sequence's new end hold nothing.  Kept tokens that are not rising, not
  * new, or more than the new ones or max_kept record TL_ERR_INVALID with the sequence; it
  * stays as it is, with its length.  The pages of a sequence's new tokens are its alone.

@@ -37,7 +37,7 @@
 // of its own.  The exact normed value costs ten times the instructions (a sum of squares in
 // pairs, a Newton step for the root, products in pairs), and a code needs it only next to
 // a border, so keys are computed in fp32 with a bound on what they are off by; where both
-// ends of the bound have one code that is the code, else (one element of some 30000) the row
+// ends of the bound have one code that is the code, else (one element of some 20000) the row
 // is computed exactly, out of line.  Queries and keys have both elements of a rotated pair in one thread
 // (77 -> 64 us for 8192 tokens as above), values stay in registers between maximum and write (61 -> 59), and so 8192
 // tokens take 55 us (96 all exact), 3.4 TB/s, the queries 33 of them alone, keys 31 and values 10; 32 trees of
@@ -816,7 +816,7 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 6 : 8) kv_append_kernel(co
   if (NORM && !values && p.k_w) {
     // ---------------------------------------------------------------- normed keys
     // A code is that of the exact value; fp32 tells it wherever what it is off by does not reach across a border between
-    // two codes.  The exact value is computed where it does (one element of some 10000), and for the block's
+    // two codes.  The exact value is computed where it does (one element of some 20000), and for the block's
     // maximum where its byte hangs on that, or where it is so large that fp32 might not hold it.
     constexpr int PAIRS = D / 16, ROWS = TEAM / PAIRS;  // threads of a row; rows of a pass
     const Pair m = pair_of(p, member % PAIRS);
@@ -1020,7 +1020,9 @@ tl_status append(const char* who, const tl_kv_append_args* a, const tl_kv_append
   }
   const int per_seq = a->max_q_len ? std::min(a->max_q_len, a->n_tokens) : cdiv(a->n_tokens, a->B);
   // A whole block to a page's keys or values of one head where a page gets 32 rows, else a warp: 8192 tokens of 8 kv heads
-  // of 128 into pages of 16, 32, 64 and 256 take 58, 54, 52 and 82 us with blocks, 54, 54, 75 and 211 us with warps.
+  // of 128 into pages of 16, 32, 64 and 256 take 58, 54, 52 and 82 us with blocks, 54, 54, 75 and 211 us with warps.  With
+  // norms 76, 63 and 55 us, and 57, 59 and 66 (16, 32, 64); few sequences gain from blocks earlier there, as a key's row has
+  // half the lanes and two passes: one tree of 26 takes 10.5 and 17.6 us, 32 trees of 16 10.4 and 15.1, 96 of 16 19.1 and 17.9.
   const bool wide = std::min(per_seq, c.page_size) >= 32;
   const int64_t items = int64_t(a->n_tokens) / c.page_size + 2 * int64_t(a->B);
   p.groups = wide ? 2 * c.H_kv : cdiv(2 * c.H_kv, APP_THREADS / 32);

@@ -15,8 +15,9 @@ __host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 // on the device, so both kernels decide, from the same whole numbers.  In ns, as measured: the kernel for few rows takes
 // 8 us and 0.21 us of a CTA for each 32 tokens of 16 rows (and as if each tile had 24 times 32 more); the one for many
 // 20 us, 0.95 us for each 64 tokens of a unit of 256 rows and 8 us for the unit, and where units are cut 8 us and 2.2 us for
-// each part to join them.  One tree of 26 over 4099 takes 25 us by few and 46 us by many, one of 64 over 16000 100 and
-// 71 us, eight of 64 over 500 62 and 25 us, 32 of 12 over 300 29 and 47 us (4 query heads to each of 8 kv heads).
+// each part to join them (all of it with 4 query heads to each of 8 kv heads of 128; heads of 64 go by the same figures,
+// though half as much is read and computed for them).  One tree of 26 over 4099 takes 25 us by few and 46 us by many, one
+// of 64 over 16000 100 and 71 us, eight of 64 over 500 62 and 25 us, 32 of 12 over 300 29 and 47 us.
 constexpr int kFewLead = 24, kManyTiles = 8;
 __host__ __device__ __forceinline__ int64_t few_cost(int Hkv, int group, int min_rows, const KvSeq& q) {  // in 32 tokens of 16 rows
   const int64_t rows = int64_t(q.q) * group;
