@@ -80,10 +80,6 @@ __device__ __forceinline__ int ordered(float x) {
 __device__ __forceinline__ float unordered(int o) { return __int_as_float(o ^ ((o >> 31) & 0x7FFFFFFF)); }
 
 // ---------------------------------------------------------------- pairs: x + y, y below half a step of x
-__device__ __forceinline__ float2 two_sum(float a, float b) {
-  const float sum = __fadd_rn(a, b), back = __fsub_rn(sum, a);
-  return make_float2(sum, __fadd_rn(__fsub_rn(a, __fsub_rn(sum, back)), __fsub_rn(b, back)));
-}
 __device__ __forceinline__ float2 normal(float hi, float lo) {  // |hi| >= |lo|, or nearly
   const float sum = __fadd_rn(hi, lo);
   return make_float2(sum, __fsub_rn(lo, __fsub_rn(sum, hi)));
@@ -838,11 +834,6 @@ int part_elements(int V, int splits) { return cdiv(cdiv(V, splits), 32) * 32; }
 int line_count(int V, int splits) { return cdiv(part_elements(V, splits), STEP); }
 int64_t part_bytes(int lines) { return int64_t(sizeof(float4)) + lines * LINE * 4; }
 
-bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + uintptr_t(nb) && y < x + uintptr_t(na);
-}
-
 }  // namespace
 }  // namespace tl
 
@@ -874,14 +865,14 @@ extern "C" tl_status tl_beam_select(const tl_beam_select_args* a, void* stream) 
   const size_t need = tl_beam_select_workspace_size(a->B, a->K, a->N, a->V);
   if (a->workspace_bytes < need) return fail(TL_ERR_INVALID, "%s: workspace of %zu bytes, need %zu", who, a->workspace_bytes, need);
   const int64_t in = int64_t(a->B) * a->K, out = int64_t(a->B) * a->N;
-  if (meet(a->scores, in * 4, a->scores_out, out * 4) || (a->done && a->done_out && meet(a->done, in, a->done_out, out)))
+  if (ranges_meet(a->scores, in * 4, a->scores_out, out * 4) || (a->done && a->done_out && ranges_meet(a->done, in, a->done_out, out)))
     return fail(TL_ERR_INVALID, "%s: scores_out or done_out overlaps what it is made from", who);
   if ((a->history != nullptr) != (a->history_out != nullptr))
     return fail(TL_ERR_INVALID, "%s: history and history_out go together", who);
   if (a->history) {
     if (a->length < 0 || a->length >= a->history_stride)
       return fail(TL_ERR_INVALID, "%s: length %d, history rows of %d", who, a->length, a->history_stride);
-    if (meet(a->history, in * a->history_stride * 4, a->history_out, out * a->history_stride * 4))
+    if (ranges_meet(a->history, in * a->history_stride * 4, a->history_out, out * a->history_stride * 4))
       return fail(TL_ERR_INVALID, "%s: history_out overlaps history", who);
   }
   BeamParams p{};

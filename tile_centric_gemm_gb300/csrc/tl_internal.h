@@ -80,5 +80,10 @@ tl_status test_hold(const char* who, uint64_t timeout_ns, int32_t* first, int32_
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline int cdiv(int a, int b) { return (a + b - 1) / b; }
+// Whether the na bytes at a and the nb bytes at b have one in common.
+inline bool ranges_meet(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + uintptr_t(nb) && y < x + uintptr_t(na);
+}
 
 }  // namespace tl

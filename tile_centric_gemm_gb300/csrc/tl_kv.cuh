@@ -110,4 +110,15 @@ __device__ __forceinline__ float pow2f(int e) {
   return e <= -127 ? __uint_as_float(0x00400000u) : __uint_as_float(uint32_t(e + 127) << 23);
 }
 
+// Sixteen codes times f (a power of two <= 1), rounded to nearest even.
+__device__ __forceinline__ uint4 recode16(uint4 w, float f) {
+  uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2(u[i])), b = f16x2_to_f32x2(e4m3x2_to_f16x2_hi(u[i]));
+    u[i] = f32x2_to_e4m3x2(a.x * f, a.y * f) | (f32x2_to_e4m3x2(b.x * f, b.y * f) << 16);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
 }  // namespace tl

@@ -186,42 +186,37 @@ __device__ __forceinline__ void rotated8(const AppendParams& p, const uint16_t* 
 struct Norm {
   float hi, lo, scale;
 };
-__device__ __forceinline__ void two_sum(float a, float b, float& sum, float& err) {
-  sum = __fadd_rn(a, b);
-  const float back = __fsub_rn(sum, a);
-  err = __fadd_rn(__fsub_rn(a, __fsub_rn(sum, back)), __fsub_rn(b, back));
-}
-// The sum of squares over the D dims of a row that neighbouring lanes hold, N of them each: squares of bf16 are exact in
+// The sum of squares over the D dims of a row that neighbouring lanes hold, 16 of them each: squares of bf16 are exact in
 // fp32, sums are pairs.  Below 2^-63 squares lose bits, which eps (1e-12 at least) makes up for.
-template <int D, int N, bool EXACT>
-__device__ __forceinline__ void square_sum(const float (&x)[N], float scale, uint32_t mask, float& s, float& e) {
+template <int D, bool EXACT>
+__device__ __forceinline__ void square_sum(const float (&x)[16], float scale, uint32_t mask, float& s, float& e) {
   s = e = 0.0f;
   if (EXACT) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < 16; ++i) {
       const float v = x[i] * scale;
-      float d;
-      two_sum(s, __fmul_rn(v, v), s, d);
-      e += d;
+      const float2 t = two_sum(s, __fmul_rn(v, v));
+      s = t.x;
+      e += t.y;
     }
   } else {
-    float q[N / 4];
+    float q[4];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < 16; ++i) {
       const float v = x[i] * scale;
       q[i / 4] = fmaf(v, v, i % 4 ? q[i / 4] : 0.0f);
     }
     s = q[0] + q[1];
-    if (N == 16) s += q[N / 4 - 2] + q[N / 4 - 1];
+    s += q[2] + q[3];
   }
 #pragma unroll
-  for (int d = 1; d < D / N; d <<= 1) {
+  for (int d = 1; d < D / 16; d <<= 1) {
     const float s2 = __shfl_xor_sync(mask, s, d);
     if (EXACT) {
       const float e2 = __shfl_xor_sync(mask, e, d);
-      float f;
-      two_sum(s, s2, s, f);
-      e = (e + e2) + f;
+      const float2 t = two_sum(s, s2);
+      s = t.x;
+      e = (e + e2) + t.y;
     } else {
       s += s2;
     }
@@ -234,32 +229,32 @@ struct Some {
 using Eight = Some<8>;
 // The sum of a row's squares times 2^-160.  (What is rare is kept out of line: the blocks' three paths share the
 // instruction cache.)
-template <int D, int N, bool EXACT>
-__device__ __noinline__ float2 small_square_sum(Some<N> x, uint32_t mask) {
+template <int D, bool EXACT>
+__device__ __noinline__ float2 small_square_sum(Some<16> x, uint32_t mask) {
   float s, e;
-  square_sum<D, N, EXACT>(x.x, 0x1p-80f, mask, s, e);
+  square_sum<D, EXACT>(x.x, 0x1p-80f, mask, s, e);
   return make_float2(s, e);
 }
-// The lanes that hold a row, N dims each.
-template <int D, int N>
+// The lanes that hold a row.
+template <int D>
 __device__ __forceinline__ uint32_t row_lanes() {
-  constexpr uint32_t LANES = D / N;
+  constexpr uint32_t LANES = D / 16;
   return ((1u << LANES) - 1u) << (lane_id() & ~(LANES - 1u));
 }
 // EXACT: to about 2^-45 by a step of Newton's iteration from the reciprocal root, its residual taken exactly:
 // r (1 + d / 2 + 3 d^2 / 8), d = 1 - a r^2.
-template <int D, bool EXACT, int N>
-__device__ __forceinline__ Norm row_norm(const float (&x)[N], float eps) {
-  const uint32_t mask = row_lanes<D, N>();
+template <int D, bool EXACT>
+__device__ __forceinline__ Norm row_norm(const float (&x)[16], float eps) {
+  const uint32_t mask = row_lanes<D>();
   Norm n{0.0f, 0.0f, 1.0f};
   float s, e;
-  square_sum<D, N, EXACT>(x, 1.0f, mask, s, e);
+  square_sum<D, EXACT>(x, 1.0f, mask, s, e);
   if (!(s < INFINITY)) {  // the same for all lanes of the row
     n.scale = 0x1p-80f;
-    Some<N> all;
+    Some<16> all;
 #pragma unroll
-    for (int i = 0; i < N; ++i) all.x[i] = x[i];
-    const float2 small = small_square_sum<D, N, EXACT>(all, mask);
+    for (int i = 0; i < 16; ++i) all.x[i] = x[i];
+    const float2 small = small_square_sum<D, EXACT>(all, mask);
     s = small.x;
     e = small.y;
     if (!(s < INFINITY)) {
@@ -273,10 +268,9 @@ __device__ __forceinline__ Norm row_norm(const float (&x)[N], float eps) {
     n.hi = fmaf(r * 0.5f, fmaf(a * r, -r, 1.0f), r);
     return n;
   }
-  float h, l;
-  two_sum(s * (1.0f / D), eps, h, l);
-  l = fmaf(e, 1.0f / D, l);
-  const float a = __fadd_rn(h, l), b = __fsub_rn(l, __fsub_rn(a, h));  // mean + eps = a + b
+  const float2 t = two_sum(s * (1.0f / D), eps);
+  const float l = fmaf(e, 1.0f / D, t.y);
+  const float a = __fadd_rn(t.x, l), b = __fsub_rn(l, __fsub_rn(a, t.x));  // mean + eps = a + b
   const float r = rsqrtf(a);
   const float p = __fmul_rn(r, r), pe = __fmaf_rn(r, r, -p);
   const float u = __fmul_rn(a, p), ue = __fmaf_rn(a, p, -u);
@@ -286,10 +280,8 @@ __device__ __forceinline__ Norm row_norm(const float (&x)[N], float eps) {
   n.lo = __fsub_rn(step, __fsub_rn(n.hi, r));
   return n;
 }
-// (x c + t s) times the row's factor; x and t with their weights, exact in fp32.  EXACT: rounded to odd.
-template <bool EXACT>
+// (x c + t s) times the row's factor, rounded to odd; x and t with their weights, exact in fp32.
 __device__ __forceinline__ float normed_dot2(const Norm& n, float x, float c, float t, float s) {
-  if (!EXACT) return fmaf(x, c, t * s) * n.hi;
   float hi, rest;
   if (!dot2_pair(x, c, t, s, hi, rest)) return hi * n.hi;
   const float y = __fmul_rn(hi, n.hi);
@@ -298,7 +290,6 @@ __device__ __forceinline__ float normed_dot2(const Norm& n, float x, float c, fl
   return to_odd(z, __fsub_rn(e, __fsub_rn(z, y)));
 }
 // Dims 8u .. 8u+7 of a row, normed by n with the weights wx (its partner's: wt) and rotated.
-template <bool EXACT>
 __device__ __forceinline__ void turn_normed(const AppendParams& p, const Turn& w, const Norm& n, const float (&x)[8],
                                             const float (&t)[8], uint4 wx, uint4 wt, float (&y)[8]) {
   float a[8], b[8];
@@ -311,16 +302,16 @@ __device__ __forceinline__ void turn_normed(const AppendParams& p, const Turn& w
   }
   if (w.partner < 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = normed_dot2<EXACT>(n, a[i], 1.0f, 0.0f, 0.0f);
+    for (int i = 0; i < 8; ++i) y[i] = normed_dot2(n, a[i], 1.0f, 0.0f, 0.0f);
   } else if (p.interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      y[2 * i] = normed_dot2<EXACT>(n, a[2 * i], w.c[i], -a[2 * i + 1], w.s[i]);
-      y[2 * i + 1] = normed_dot2<EXACT>(n, a[2 * i + 1], w.c[i], a[2 * i], w.s[i]);
+      y[2 * i] = normed_dot2(n, a[2 * i], w.c[i], -a[2 * i + 1], w.s[i]);
+      y[2 * i + 1] = normed_dot2(n, a[2 * i + 1], w.c[i], a[2 * i], w.s[i]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = normed_dot2<EXACT>(n, a[i], w.c[i], w.first ? -b[i] : b[i], w.s[i]);
+    for (int i = 0; i < 8; ++i) y[i] = normed_dot2(n, a[i], w.c[i], w.first ? -b[i] : b[i], w.s[i]);
   }
 }
 
@@ -428,11 +419,11 @@ __device__ __noinline__ Some<16> exact_key16(const AppendParams& p, const uint16
   float y[8];
   Turn w;
   turn_at(p, m.first, pos, w);
-  turn_normed<true>(p, w, n, a, own ? a : b, wa, own ? wa : wb, y);
+  turn_normed(p, w, n, a, own ? a : b, wa, own ? wa : wb, y);
 #pragma unroll
   for (int i = 0; i < 8; ++i) out.x[i] = y[i];
   turn_at(p, m.second, pos, w);
-  turn_normed<true>(p, w, n, b, own ? b : a, wb, own ? wb : wa, y);
+  turn_normed(p, w, n, b, own ? b : a, wb, own ? wb : wa, y);
 #pragma unroll
   for (int i = 0; i < 8; ++i) out.x[8 + i] = y[i];
   return out;
@@ -609,17 +600,6 @@ __device__ __noinline__ int2 find_among_wrong(const KvBatch& b, int ps, int t) {
 // The least scale byte whose 448 * 2^(byte-127) holds the magnitude with these bits.
 __device__ __forceinline__ int scale_need(uint32_t amax_bits) {
   return max(0, int(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0));
-}
-
-// Sixteen codes times f (a power of two <= 1), rounded to nearest even.
-__device__ __forceinline__ uint4 recode16(uint4 w, float f) {
-  uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2(u[i])), b = f16x2_to_f32x2(e4m3x2_to_f16x2_hi(u[i]));
-    u[i] = f32x2_to_e4m3x2(a.x * f, a.y * f) | (f32x2_to_e4m3x2(b.x * f, b.y * f) << 16);
-  }
-  return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 // Where the tables are read for the token at `pos`, new token `t` of the batch.
@@ -865,7 +845,7 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 6 : 8) kv_append_kernel(co
         code[i] = f32x2_to_e4m3x2(fmaf(z0, -err, a), fmaf(z1, -err, b));
         differ |= code[i] ^ f32x2_to_e4m3x2(fmaf(z0, err, a), fmaf(z1, err, b));
       });
-      if (__any_sync(row_lanes<D, 16>(), differ != 0)) {
+      if (__any_sync(row_lanes<D>(), differ != 0)) {
         const Some<16> e = exact_key16<D>(p, row_at(r), m, pos_of(r));
 #pragma unroll
         for (int i = 0; i < 8; ++i) code[i] = f32x2_to_e4m3x2(e.x[2 * i] * inv, e.x[2 * i + 1] * inv);
@@ -892,14 +872,7 @@ __global__ void __launch_bounds__(APP_THREADS, NORM ? 6 : 8) kv_append_kernel(co
   reduce();
   const int byte = max(old, scale_need(amax));
   const float inv = byte == 255 ? __uint_as_float(0x00200000u) : pow2f(127 - byte);  // 255: NaN it was and stays
-  if (slot0 > 0 && byte > old) {
-    const float f = pow2f(max(old - byte, -127));
-    for (int i = member; i < slot0 * (D / 16); i += TEAM) {
-      uint4* at = reinterpret_cast<uint4*>(codes + int64_t(i / (D / 16)) * p.c.token_stride + (i % (D / 16)) * 16);
-      *at = recode16(*at, f);
-    }
-  }
-  if (member == 0) *scale_at = uint8_t(byte);
+  settle(byte);
   auto write8 = [&](int r, const float(&x)[8]) {
     uint2 w;
     w.x = f32x2_to_e4m3x2(x[0] * inv, x[1] * inv) | (f32x2_to_e4m3x2(x[2] * inv, x[3] * inv) << 16);

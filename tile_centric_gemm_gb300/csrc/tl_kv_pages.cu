@@ -340,16 +340,6 @@ struct CompactParams {
   Layer layers[LAYERS];
 };
 
-// Sixteen codes times f, a power of two <= 1, each rounded once to nearest even.
-__device__ __forceinline__ uint4 recoded(uint4 w, float f) {
-  uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2(u[i])), b = f16x2_to_f32x2(e4m3x2_to_f16x2_hi(u[i]));
-    u[i] = f32x2_to_e4m3x2(a.x * f, a.y * f) | (f32x2_to_e4m3x2(b.x * f, b.y * f) << 16);
-  }
-  return make_uint4(u[0], u[1], u[2], u[3]);
-}
 // The factor that brings codes of scale byte `from` to byte `to` >= from.  (255 is NaN and stays: the codes do not matter.)
 __device__ __forceinline__ float recode_factor(int from, int to) { return to == 255 ? 1.0f : pow2f(max(from - to, -127)); }
 
@@ -423,7 +413,7 @@ __global__ void __launch_bounds__(COPY_THREADS) compact_kernel(const __grid_cons
       const float f = recode_factor(was, now);
       for (int r = row; r < start + i0 - base; r += RPP) {
         uint4* at = reinterpret_cast<uint4*>((x ? codes[1] : codes[0]) + page_at0 + r * p.token_stride + unit);
-        *at = recoded(*at, f);
+        *at = recode16(*at, f);
       }
     }
     const bool again = i1 - i0 > 32;
@@ -450,7 +440,7 @@ __global__ void __launch_bounds__(COPY_THREADS) compact_kernel(const __grid_cons
         for (int k = 0; k < BATCH; ++k)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            if (move[k][x] && b[k][x] != most[x]) w[k][x] = recoded(w[k][x], recode_factor(b[k][x], most[x]));
+            if (move[k][x] && b[k][x] != most[x]) w[k][x] = recode16(w[k][x], recode_factor(b[k][x], most[x]));
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < BATCH; ++k)
@@ -469,11 +459,6 @@ __global__ void __launch_bounds__(COPY_THREADS) compact_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------- checks
-bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + uintptr_t(nb) && y < x + uintptr_t(na);
-}
-
 tl_status check_layers(const char* who, const tl_kv_cache* caches, int n) {
   if (!caches || n < 1) return fail(TL_ERR_INVALID, "%s: no caches", who);
   if (n > 4096) return fail(TL_ERR_UNSUPPORTED, "%s: %d layers (at most 4096)", who, n);
@@ -563,9 +548,9 @@ extern "C" tl_status tl_kv_fork(const tl_kv_fork_args* a, void* stream) {
     return fail(TL_ERR_INVALID, "%s: workspace of %zu bytes, need %zu", who, a->workspace_bytes,
                 tl_kv_fork_workspace_size(a->B_in, a->B_out));
   const int64_t in = int64_t(a->B_in) * a->max_pages * 4, out = int64_t(a->B_out) * a->max_pages * 4;
-  if (meet(a->page_table, in, a->page_table_out, out) || meet(a->seq_lens, a->B_in * 4ll, a->seq_lens_out, a->B_out * 4ll))
+  if (ranges_meet(a->page_table, in, a->page_table_out, out) || ranges_meet(a->seq_lens, a->B_in * 4ll, a->seq_lens_out, a->B_out * 4ll))
     return fail(TL_ERR_INVALID, "%s: the new table and lengths overlap the old ones", who);
-  if (a->refs != a->refs_out && meet(a->refs, a->num_pages * 4ll, a->refs_out, a->num_pages * 4ll))
+  if (a->refs != a->refs_out && ranges_meet(a->refs, a->num_pages * 4ll, a->refs_out, a->num_pages * 4ll))
     return fail(TL_ERR_INVALID, "%s: refs_out overlaps refs", who);
   DeviceInfo di{};
   if (tl_status s = device_info(&di)) return s;
@@ -609,7 +594,7 @@ extern "C" tl_status tl_kv_resize(const tl_kv_resize_args* a, void* stream) {
     return fail(TL_ERR_INVALID, "%s: refs and workspace must be 16-byte aligned", who);
   if (a->workspace_bytes < tl_kv_resize_workspace_size(a->B))
     return fail(TL_ERR_INVALID, "%s: workspace of %zu bytes, need %zu", who, a->workspace_bytes, tl_kv_resize_workspace_size(a->B));
-  if (a->refs != a->refs_out && meet(a->refs, a->num_pages * 4ll, a->refs_out, a->num_pages * 4ll))
+  if (a->refs != a->refs_out && ranges_meet(a->refs, a->num_pages * 4ll, a->refs_out, a->num_pages * 4ll))
     return fail(TL_ERR_INVALID, "%s: refs_out overlaps refs", who);
   DeviceInfo di{};
   if (tl_status s = device_info(&di)) return s;
@@ -673,7 +658,7 @@ extern "C" tl_status tl_kv_compact(const tl_kv_compact_args* a, void* stream) {
     return fail(TL_ERR_INVALID, "%s: B %d, max_pages %d, max_kept %d", who, a->B, a->max_pages, a->max_kept);
   if (!a->kept || !a->n_kept || !a->cu_seqlens || !a->seq_lens || !a->page_table || !a->seq_lens_out || !a->signals)
     return fail(TL_ERR_INVALID, "%s: NULL pointer argument", who);
-  if (meet(a->seq_lens, a->B * 4ll, a->seq_lens_out, a->B * 4ll))
+  if (ranges_meet(a->seq_lens, a->B * 4ll, a->seq_lens_out, a->B * 4ll))
     return fail(TL_ERR_INVALID, "%s: seq_lens_out overlaps seq_lens", who);
   if (a_cache_twice(a->caches, a->n_layers)) return fail(TL_ERR_INVALID, "%s: a cache is given twice", who);
   DeviceInfo di{};

@@ -19,6 +19,12 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
+// a + b exactly: the nearest float and the rest.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+  const float sum = __fadd_rn(a, b), back = __fsub_rn(sum, a);
+  return make_float2(sum, __fadd_rn(__fsub_rn(a, __fsub_rn(sum, back)), __fsub_rn(b, back)));
+}
+
 __device__ __forceinline__ uint32_t warp_id() { return threadIdx.x >> 5; }
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31u; }
 
