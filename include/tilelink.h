@@ -914,10 +914,10 @@ tl_status tl_kv_compact(const tl_kv_compact_args* args, void* stream);
  * Scores are compared in pairs of fp32 (48 bits; the sum of exponentials is good to
  * 2^-19 at worst, where a few logits make it up to about 2^-22, where many do to about
  * 2^-26) and returned in fp32.  Where rows begin in memory does not enter: beams of the
- * same logits have the same lse.  Only finite
- * scores count: tokens whose logit is -infinity, beams whose score is not finite, and
- * beams whose lse is not (all logits -infinity, or one NaN or +infinity), or whose score
- * less lse is not in fp32, offer nothing.
+ * same logits have the same lse.  Only finite scores count: tokens whose logit is
+ * -infinity, beams whose score is not finite, and beams whose lse is not (all logits
+ * -infinity, or one NaN or +infinity), or whose score less lse is not in fp32, offer
+ * nothing.
  * A beam whose done is not 0 has ended: its logits are not read, its lse is 0, and it
  * offers one continuation, token eos at its own score.  Where fewer than N are offered
  * the places left have parent -1, token -1 and score -infinity.

@@ -14,8 +14,8 @@
 //
 // All four are bound by latency: what they move is little.  GPU time in a graph, heads of 128, 8 kv
 // heads: four beams of 1000 tokens forked and three part-filled pages copied in 16 layers
-// (5 MB) 8.3 us; 512 beams of 900, 4 layers (54 MB) 20.7 us, the copies 10 of them (5.3 TB/s); 26 drafts compacted
-// behind 4099 in 16 layers 6.5 us; 64 trees of up to 60 in 8 layers (13 MB) 10.5 us.  A call from Python takes 5 to 9 us
+// (5 MB) 8.3 us; 512 beams of 900, 4 layers (54 MB) 18.7 us, the copies 10 of them (5.3 TB/s); 26 drafts compacted
+// behind 4099 in 16 layers 6.2 us; 64 trees of up to 60 in 8 layers (13 MB) 10.2 us.  A call from Python takes 5 to 9 us
 // of the host, 2 to 3 of them the launch.
 #include <algorithm>
 #include <functional>

@@ -45,7 +45,7 @@
 //
 // A tree's rows see what their tokens' masks say: all keys go to every row's unit, windows of 32 mask bits take the place
 // of the limit, and which rows see a NaN value is looked up in the cache once there is one (tree_nan).  16 trees of 64 over
-// 6001 at most (32 heads, 8 kv heads of 128) take 99 us, 590 TFLOP/s: 128 units on 152 SMs, so that each run opens one or two
+// 6001 at most (32 heads, 8 kv heads of 128) take 97 us, 600 TFLOP/s: 128 units on 152 SMs, so that each run opens one or two
 // and joins with its neighbours.
 //
 // TMEM (lane = query row of the tile): S_A columns 0-63 and 64-127, S_B 128-191 and
